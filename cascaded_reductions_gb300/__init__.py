@@ -17,6 +17,7 @@ instead, e.g. the bounds-checked debug variant that
 ``cascaded_reductions_gb300._build.build_checked()`` makes.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -27,7 +28,7 @@ LIB_PATH = os.environ.get("RF_LIBRARY") or os.path.join(_HERE, "librf.so")
 
 (RF_OK, RF_ERR_INVALID_ARG, RF_ERR_UNSUPPORTED, RF_ERR_MISALIGNED, RF_ERR_CUDA, RF_ERR_TIMEOUT,
  RF_ERR_BOUNDS) = range(7)
-RF_F32, RF_BF16 = 0, 1
+RF_F32, RF_BF16, RF_F16 = 0, 1, 2
 RF_FUSE_NONE, RF_FUSE_THREAD, RF_FUSE_WARP, RF_FUSE_BLOCK = range(4)
 
 _P = ctypes.c_void_p
@@ -59,6 +60,13 @@ _SIGNATURES = {
     "rf_bounds_checked": (_I, []),
     "rf_selftest_bounds": (_I, [_P]),
     "rf_stream_read": (_I, [_P, ctypes.c_size_t, _P, _P]),
+    "rf_decode_segments": (_I, [_I, _I]),
+    "rf_attn_decode_window": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P,
+                                   _P, _P, _P, _I, _P, _P]),
+    "rf_attn_decode_weights": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P,
+                                    _P, _P, _I, _P, _P, _P, _P]),
+    "rf_cache_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
+                            _P]),
 }
 
 
@@ -117,6 +125,39 @@ def _dtype_code(dt):
     if dt == torch.bfloat16:
         return RF_BF16
     raise ValueError(f"unsupported dtype {dt}")
+
+
+# The calls over a cache of grouped heads run on the device that holds their
+# tensors, whichever is current: their arguments share one device, and the
+# stream (by default that device's current one) belongs to it.
+
+_CACHE_DTYPES = {torch.float32: RF_F32, torch.bfloat16: RF_BF16, torch.float16: RF_F16}
+
+
+def _cache_dtype(dt, name):
+    if dt not in _CACHE_DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {dt}")
+    return _CACHE_DTYPES[dt]
+
+
+def _one_device(*tensors):
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one call works on one device")
+    return dev
+
+
+def _call_on(dev, stream, where, fn, *args):
+    """fn(*args, stream) with ``dev`` current; raises RFError on a bad status."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+    ptr = ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, ptr), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, ptr), where)
 
 
 def version():
@@ -357,6 +398,100 @@ def rf_incremental_quant_fp8_gemm(x, wq, sw, y, sx_final=None, stream=None):
            "rf_incremental_quant_fp8_gemm")
 
 
+def rf_decode_segments(groups, keys):
+    """A number of segments that fills the current device: ``groups`` =
+    B * Hkv * ceil(G / 16) rows of CTAs over up to ``keys`` visible keys each."""
+    return _lib.rf_decode_segments(int(groups), int(keys))
+
+
+def _need_cache(q, k, v, lens):
+    """Checks q [B, H, D], k/v [B, Hkv, cap, D] and lens [B]; returns the sizes."""
+    if q.dim() != 3 or k.dim() != 4:
+        raise ValueError("q must be [B, H, D] and k [B, Hkv, cap, D]")
+    B, H, D = q.shape
+    Hkv, cap = k.shape[1], k.shape[2]
+    _need(q, q.dtype, "q")
+    _need(k, q.dtype, "k", (B, Hkv, cap, D))
+    _need(v, q.dtype, "v", (B, Hkv, cap, D))
+    if lens is not None:
+        _need(lens, torch.int32, "lens", (B,))
+    return B, H, Hkv, cap, D
+
+
+def _need_scratch(B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters, out, lse):
+    _need(seg_m, torch.float32, "seg_m", (B * H, S))
+    _need(seg_l, torch.float32, "seg_l", (B * H, S))
+    _need(seg_acc, torch.float32, "seg_acc", (B * H, S, D))
+    _need(counters, torch.int32, "counters")
+    if counters.numel() < B * Hkv * (-(-(H // max(Hkv, 1)) // 16)):
+        raise ValueError("counters must hold B * Hkv * ceil(H / Hkv / 16) elements")
+    _need(out, out.dtype, "out", (B, H, D))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (B, H))
+
+
+def rf_attn_decode_window(q, k, v, lens, window, sinks, S, scale, seg_m, seg_l, seg_acc, counters,
+                          out, lse=None, stream=None):
+    """q [B, H, D], k/v [B, Hkv, cap, D] (bf16 or fp16, D = 128), lens int32 [B] or None ->
+    out [B, H, D] (q's type or fp32), lse [B, H].  Scratch: seg_m/seg_l [B*H, S],
+    seg_acc [B*H, S, D] fp32, counters int32 [B * Hkv * ceil(H / Hkv / 16)], zero at first."""
+    B, H, Hkv, cap, D = _need_cache(q, k, v, lens)
+    _need_scratch(B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters, out, lse)
+    dev = _one_device(q, k, v, lens, seg_m, seg_l, seg_acc, counters, out, lse)
+    _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, _ptr(q), _ptr(k),
+             _ptr(v), _ptr(lens), B, H, Hkv, cap, D, int(window), int(sinks), int(S), float(scale),
+             _cache_dtype(q.dtype, "q"), _ptr(seg_m), _ptr(seg_l), _ptr(seg_acc), _ptr(counters),
+             _ptr(out), _cache_dtype(out.dtype, "out"), _ptr(lse))
+
+
+def rf_attn_decode_weights(q, k, v, lens, S, scale, seg_m, seg_l, seg_acc, counters, scores, out,
+                           lse, weight, weight_out, stream=None):
+    """Decode as rf_attn_decode_window without a window; weight_out [B, Hkv, cap] = weight (or 0
+    for None; may be weight_out itself) + the softmax weights summed over each group's heads.
+    scores [B, H, cap] fp32 scratch."""
+    B, H, Hkv, cap, D = _need_cache(q, k, v, lens)
+    _need_scratch(B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters, out, lse)
+    _need(scores, torch.float32, "scores", (B, H, cap))
+    _need(weight_out, torch.float32, "weight_out", (B, Hkv, cap))
+    if weight is not None:
+        _need(weight, torch.float32, "weight", (B, Hkv, cap))
+    dev = _one_device(q, k, v, lens, seg_m, seg_l, seg_acc, counters, scores, out, lse, weight,
+                      weight_out)
+    _call_on(dev, stream, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, _ptr(q), _ptr(k),
+             _ptr(v), _ptr(lens), B, H, Hkv, cap, D, int(S), float(scale),
+             _cache_dtype(q.dtype, "q"), _ptr(seg_m), _ptr(seg_l), _ptr(seg_acc), _ptr(counters),
+             _ptr(scores), _ptr(out), _cache_dtype(out.dtype, "out"), _ptr(lse), _ptr(weight),
+             _ptr(weight_out))
+
+
+def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight_out, lens_out,
+                   kept, stream=None):
+    """k/v [B, Hkv, cap, D] (fp32, bf16 or fp16; v None for a cache of one tensor), weight
+    [B, Hkv, cap] fp32, lens int32 [B] or None -> k_out/v_out [B, Hkv, cap_out, D], weight_out
+    [B, Hkv, cap_out], lens_out int32 [B], kept int32 [B, Hkv, keep]."""
+    if k.dim() != 4 or k_out.dim() != 4:
+        raise ValueError("k and k_out must be [B, Hkv, rows, D]")
+    B, Hkv, cap, D = k.shape
+    cap_out = k_out.shape[2]
+    _need(k, k.dtype, "k")
+    _need(k_out, k.dtype, "k_out", (B, Hkv, cap_out, D))
+    if v is not None:
+        _need(v, k.dtype, "v", (B, Hkv, cap, D))
+    if v_out is not None:
+        _need(v_out, k.dtype, "v_out", (B, Hkv, cap_out, D))
+    _need(weight, torch.float32, "weight", (B, Hkv, cap))
+    _need(weight_out, torch.float32, "weight_out", (B, Hkv, cap_out))
+    if lens is not None:
+        _need(lens, torch.int32, "lens", (B,))
+    _need(lens_out, torch.int32, "lens_out", (B,))
+    _need(kept, torch.int32, "kept", (B, Hkv, keep))
+    dev = _one_device(k, v, weight, lens, k_out, v_out, weight_out, lens_out, kept)
+    _call_on(dev, stream, "rf_cache_evict", _lib.rf_cache_evict, _ptr(k), _ptr(v), _ptr(weight),
+             _ptr(lens), B, Hkv, cap, D, _cache_dtype(k.dtype, "k"), int(keep), int(sinks),
+             int(recent), cap_out, _ptr(k_out), _ptr(v_out), _ptr(weight_out), _ptr(lens_out),
+             _ptr(kept))
+
+
 def rf_stream_read(x, out_xor, stream=None):
     """XOR every 32-bit word of the CUDA tensor ``x`` into ``out_xor`` (one
     int32 element, device memory) with one streaming read of ``x``."""
@@ -459,3 +594,106 @@ def attn_prefill(q, k, v, causal=True, scale=None, stream=None):
     lse = torch.empty(B, H, N, device=q.device, dtype=torch.float32)
     rf_attn_prefill(q, k, v, causal, scale, out, lse, stream)
     return out, lse
+
+
+class DecodeWorkspace:
+    """Scratch of one decode call over a cache of grouped heads (decode_workspace makes it):
+    segment states, zeroed counters and, where asked for, a score per head and key.  A serving
+    loop keeps one per call that may be in flight at a time."""
+
+    def __init__(self, B, H, Hkv, D, S, prefix_S, cap, weights, device):
+        f32 = dict(device=device, dtype=torch.float32)
+        self.S, self.prefix_S = S, prefix_S
+        self.seg_m = torch.empty(B * H, S + prefix_S, **f32)
+        self.seg_l = torch.empty(B * H, S + prefix_S, **f32)
+        self.seg_acc = torch.empty(B * H, S + prefix_S, D, **f32)
+        self.counters = torch.zeros(B * Hkv * (-(-(H // Hkv) // 16)), device=device,
+                                    dtype=torch.int32)
+        self.scores = torch.empty(B, H, cap, **f32) if weights else None
+
+
+def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights=False, S=None,
+                     device=None):
+    """Scratch for attn_decode_window (window, sinks as in the call) or attn_decode_weights
+    (weights=True), with the number of segments that fills the device."""
+    if H < 1 or Hkv < 1 or H % Hkv:
+        raise ValueError("H must be a positive multiple of Hkv")
+    if prefix:
+        raise ValueError("prefix is not supported yet")
+    dev = torch.device("cuda" if device is None else device)
+    with torch.cuda.device(dev):
+        if S is None:
+            keys = min(cap, window + sinks) if window else cap
+            S = rf_decode_segments(B * Hkv * (-(-(H // Hkv) // 16)), keys)
+        return DecodeWorkspace(B, H, Hkv, D, S, 0, cap, weights, torch.device("cuda", torch.cuda.current_device()))
+
+
+def _on_stream(stream):
+    """Allocations inside belong to ``stream`` (None: the current one), so that their memory is
+    not handed out again while the stream still uses it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=None,
+                       out_dtype=None, stream=None):
+    """Single-token decode over the visible keys of a ragged batch of caches.
+
+    q [B, H, D], k/v [B, Hkv, cap, D] (bf16 or fp16), lens int32 [B] (None: all cap rows in use).
+    Key j is visible if it is one of the last ``window`` (0: all) or of the first ``sinks``.
+    Returns out [B, H, D] and lse [B, H]; ``work`` from decode_workspace saves its allocation."""
+    B, H, D = q.shape
+    with _on_stream(stream):
+        if work is None:
+            work = decode_workspace(B, H, k.shape[1], k.shape[2], D, window=window, sinks=sinks,
+                                    device=q.device)
+        out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
+        lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
+        rf_attn_decode_window(q, k, v, lens, window, sinks, work.S,
+                              D ** -0.5 if scale is None else scale, work.seg_m, work.seg_l,
+                              work.seg_acc, work.counters, out, lse, stream)
+    return out, lse
+
+
+def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, weight_out=None,
+                        out_dtype=None, stream=None):
+    """Single-token decode that also totals each key's attention weight.
+
+    Returns out [B, H, D], lse [B, H] and weight_out [B, Hkv, cap] = weight (None: 0) plus the
+    softmax weights of this token, summed over each key head's query heads; ``weight_out`` may be
+    ``weight`` itself."""
+    B, H, D = q.shape
+    with _on_stream(stream):
+        if work is None:
+            work = decode_workspace(B, H, k.shape[1], k.shape[2], D, weights=True, device=q.device)
+        if work.scores is None:
+            raise ValueError("work must come from decode_workspace(..., weights=True)")
+        out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
+        lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
+        if weight_out is None:
+            weight_out = torch.empty(B, k.shape[1], k.shape[2], device=q.device,
+                                     dtype=torch.float32)
+        rf_attn_decode_weights(q, k, v, lens, work.S, D ** -0.5 if scale is None else scale,
+                               work.seg_m, work.seg_l, work.seg_acc, work.counters, work.scores,
+                               out, lse, weight, weight_out, stream)
+    return out, lse, weight_out
+
+
+def cache_evict(k, v, weight, lens, keep, sinks=0, recent=0, cap_out=None, out=None, stream=None):
+    """Keep ``keep`` rows per sequence and key head: the first ``sinks``, the last ``recent`` and
+    the rows of largest weight between them, in their old order.
+
+    k/v [B, Hkv, cap, D] (v may be None), weight [B, Hkv, cap], lens int32 [B] or None.  Returns
+    k_out, v_out, weight_out (``out`` if given, else new zeroed tensors of cap_out = keep rows by
+    default), lens_out [B] and kept [B, Hkv, keep] (source rows, -1 behind a short sequence)."""
+    B, Hkv, cap, D = k.shape
+    dev = k.device
+    with _on_stream(stream):
+        if out is None:
+            rows = keep if cap_out is None else cap_out
+            out = (torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
+                   None if v is None else torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
+                   torch.zeros(B, Hkv, rows, device=dev, dtype=torch.float32))
+        lens_out = torch.empty(B, device=dev, dtype=torch.int32)
+        kept = torch.empty(B, Hkv, keep, device=dev, dtype=torch.int32)
+        rf_cache_evict(k, v, weight, lens, keep, sinks, recent, *out, lens_out, kept, stream)
+    return (*out, lens_out, kept)

@@ -3,11 +3,38 @@
 
 #include <math.h>
 
-#include "common.cuh"
+#include "cache_common.cuh"
+#include "tc_common.cuh"
 
 namespace {
 
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+
+// The checks that the calls over a cache of grouped heads share.  Sizes first
+// (RF_ERR_INVALID_ARG), then what is outside the supported set.
+rf_status check_cache_shape(int B, int H, int Hkv, int cap, int D, float scale, int dtype) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || cap <= 0 || D <= 0) return RF_ERR_INVALID_ARG;
+  if (H % Hkv != 0 || !isfinite(scale)) return RF_ERR_INVALID_ARG;
+  if (dtype != RF_F32 && dtype != RF_BF16 && dtype != RF_F16) return RF_ERR_INVALID_ARG;
+  if (D != 128 || dtype == RF_F32 || cap > (1 << 30)) return RF_ERR_UNSUPPORTED;
+  return RF_OK;
+}
+
+rf_status check_segments(int B, int H, int Hkv, int S, int dtype, int out_dtype) {
+  if (S < 1) return RF_ERR_INVALID_ARG;
+  if (out_dtype != RF_F32 && out_dtype != dtype) return RF_ERR_INVALID_ARG;
+  if (S > 4096) return RF_ERR_UNSUPPORTED;
+  const long long tiles = ((long long)H / Hkv + 15) / 16;
+  const long long groups = (long long)B * Hkv;             // below 2^62
+  if (groups > 0x7fffffffLL / tiles || groups * tiles > 0x7fffffffLL / S) return RF_ERR_UNSUPPORTED;
+  return RF_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 
 }  // namespace
 
@@ -229,6 +256,114 @@ rf_status rf_incremental_quant_fp8_gemm(const void* x, int M, int K, const uint8
       rf::launch_fp8_incremental_cluster(x, wq, sw, M, N, K, y, sx_final, as_stream(stream));
   if (s != RF_ERR_UNSUPPORTED) return s;
   return rf::launch_fp8_incremental(x, wq, sw, M, N, K, y, sx_final, as_stream(stream));
+}
+
+int rf_decode_segments(int groups, int keys) {
+  const int sms = rf::tc::sm_count();
+  if (sms <= 0) return 0;
+  if (groups < 1) groups = 1;
+  if (keys < 1) keys = 1;
+  return rf::decode_segments(groups, keys, sms);
+}
+
+rf_status rf_attn_decode_window(const void* q, const void* k, const void* v, const int32_t* lens,
+                                int B, int H, int Hkv, int cap, int D, int window, int sinks,
+                                int S, float scale, int dtype, float* seg_m, float* seg_l,
+                                float* seg_acc, int* counters, void* out, int out_dtype,
+                                float* lse, void* stream) {
+  if (!q || !k || !v || !seg_m || !seg_l || !seg_acc || !counters || !out)
+    return RF_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return RF_ERR_INVALID_ARG;
+  rf_status s = check_cache_shape(B, H, Hkv, cap, D, scale, dtype);
+  if (s != RF_OK) return s;
+  s = check_segments(B, H, Hkv, S, dtype, out_dtype);
+  if (s != RF_OK) return s;
+  if (!rf::aligned16(q) || !rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(out) ||
+      !rf::aligned16(seg_acc))
+    return RF_ERR_MISALIGNED;
+  rf::CacheDecode a = {};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k = static_cast<const uint8_t*>(k);
+  a.v = static_cast<const uint8_t*>(v);
+  a.lens = lens;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.cap = cap;
+  a.window = window, a.sinks = sinks;
+  a.S = a.S_total = S;
+  a.scale_log2 = scale * rf::kLog2e;
+  a.seg_m = seg_m, a.seg_l = seg_l, a.seg_acc = seg_acc;
+  a.counters = counters;
+  a.out = out, a.out_dtype = out_dtype, a.lse = lse;
+  return rf::launch_cache_decode(a, dtype, as_stream(stream));
+}
+
+rf_status rf_attn_decode_weights(const void* q, const void* k, const void* v, const int32_t* lens,
+                                 int B, int H, int Hkv, int cap, int D, int S, float scale,
+                                 int dtype, float* seg_m, float* seg_l, float* seg_acc,
+                                 int* counters, float* scores, void* out, int out_dtype,
+                                 float* lse, const float* weight, float* weight_out,
+                                 void* stream) {
+  if (!q || !k || !v || !seg_m || !seg_l || !seg_acc || !counters || !scores || !out ||
+      !weight_out)
+    return RF_ERR_INVALID_ARG;
+  rf_status s = check_cache_shape(B, H, Hkv, cap, D, scale, dtype);
+  if (s != RF_OK) return s;
+  s = check_segments(B, H, Hkv, S, dtype, out_dtype);
+  if (s != RF_OK) return s;
+  const size_t bytes = (size_t)B * Hkv * cap * sizeof(float);
+  if (weight != weight_out && overlap(weight, bytes, weight_out, bytes)) return RF_ERR_INVALID_ARG;
+  if ((long long)B * Hkv * ((cap + 255) / 256) > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(q) || !rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(out) ||
+      !rf::aligned16(seg_acc))
+    return RF_ERR_MISALIGNED;
+  rf::CacheDecode a = {};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k = static_cast<const uint8_t*>(k);
+  a.v = static_cast<const uint8_t*>(v);
+  a.lens = lens;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.cap = cap;
+  a.S = a.S_total = S;
+  a.scale_log2 = scale * rf::kLog2e;
+  a.seg_m = seg_m, a.seg_l = seg_l, a.seg_acc = seg_acc;
+  a.counters = counters;
+  a.out = out, a.out_dtype = out_dtype, a.lse = lse;
+  a.scores = scores;
+  s = rf::launch_cache_decode(a, dtype, as_stream(stream));
+  if (s != RF_OK) return s;
+  return rf::launch_add_weights(a, weight, weight_out, as_stream(stream));
+}
+
+rf_status rf_cache_evict(const void* k, const void* v, const float* weight, const int32_t* lens,
+                         int B, int Hkv, int cap, int D, int dtype, int keep, int sinks,
+                         int recent, int cap_out, void* k_out, void* v_out, float* weight_out,
+                         int32_t* lens_out, int32_t* kept, void* stream) {
+  if (!k || !weight || !k_out || !weight_out || !lens_out || !kept || (v == nullptr) != (v_out == nullptr))
+    return RF_ERR_INVALID_ARG;
+  if (B <= 0 || Hkv <= 0 || cap <= 0 || D <= 0 || keep < 1 || keep > cap_out || sinks < 0 ||
+      recent < 0 || (long long)sinks + recent > keep)
+    return RF_ERR_INVALID_ARG;
+  if (dtype != RF_F32 && dtype != RF_BF16 && dtype != RF_F16) return RF_ERR_INVALID_ARG;
+  const long long row_bytes = (long long)D * (dtype == RF_F32 ? 4 : 2);
+  if (row_bytes % 16 != 0 || row_bytes > 65536 || cap > (1 << 30) || cap_out > (1 << 30) ||
+      (long long)B * Hkv > 0x7fffffffLL)
+    return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(k_out) || !rf::aligned16(v_out))
+    return RF_ERR_MISALIGNED;
+  const size_t groups = (size_t)B * Hkv;
+  const struct { const void* p; size_t n; } in[] = {
+      {k, groups * cap * row_bytes}, {v, groups * cap * row_bytes}, {weight, groups * cap * 4},
+      {lens, (size_t)B * 4}};
+  const struct { const void* p; size_t n; } out[] = {
+      {k_out, groups * cap_out * row_bytes}, {v_out, groups * cap_out * row_bytes},
+      {weight_out, groups * cap_out * 4}, {lens_out, (size_t)B * 4}, {kept, groups * keep * 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (const auto& x : in)
+      if (overlap(out[i].p, out[i].n, x.p, x.n)) return RF_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return RF_ERR_INVALID_ARG;
+  }
+  return rf::launch_cache_evict(k, v, weight, lens, B, Hkv, cap, (int)row_bytes, keep, sinks,
+                                recent, cap_out, k_out, v_out, weight_out, lens_out, kept,
+                                as_stream(stream));
 }
 
 rf_status rf_device_error(int* status, void* stream) {

@@ -48,7 +48,7 @@ int sm_count() {
 namespace {
 // Filled during static initialisation of the library (one entry per status
 // word); zero-initialised storage, so registration order does not matter.
-constexpr int kMaxStatusWords = 32;
+constexpr int kMaxStatusWords = 64;
 status_take_fn g_status_words[kMaxStatusWords];
 std::atomic<int> g_n_status_words{0};
 }  // namespace

@@ -54,7 +54,8 @@ typedef enum {
                                range and its access was skipped (see below)   */
 } rf_status;
 
-typedef enum { RF_F32 = 0, RF_BF16 = 1 } rf_dtype;
+/* RF_F16 (IEEE half) is accepted by the calls whose comment names it. */
+typedef enum { RF_F32 = 0, RF_BF16 = 1, RF_F16 = 2 } rf_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* rf_status_string(int status);
@@ -311,6 +312,105 @@ rf_status rf_attn_decode_noalloc(const void* q, const void* k, const void* v,
 rf_status rf_incremental_quant_fp8_gemm(const void* x, int M, int K, const uint8_t* wq,
                                         const float* sw, int N, void* y, float* sx_final,
                                         void* stream);
+
+/*
+ * Attention over a serving cache of grouped heads
+ * -----------------------------------------------
+ * The calls below compute the same softmax cascade (scores, running max,
+ * exp-sum, weighted sum: transcript cues 9, 15-19, 21, 31) in the shapes a
+ * serving loop has; the pages name none of these forms.  Common to them:
+ *   - H query heads share Hkv key/value heads: H % Hkv == 0, and query head h
+ *     reads key head h / G, G = H / Hkv (G = 1: a key head for every query
+ *     head; Hkv = 1: one for all);
+ *   - dtype RF_BF16 or RF_F16 for q, k and v; head dim D = 128;
+ *   - `cap` is the number of rows allocated per sequence and key head, and
+ *     lens [B] (int32, DEVICE memory, may be NULL: every sequence holds cap
+ *     keys) the number of rows in use; the query stands at the last of them.
+ *     Values outside 0..cap are taken as the nearer bound.  Rows behind the
+ *     end are never read, so they may hold anything, NaN included;
+ *   - `window` > 0 leaves key j visible to the query at position p if
+ *     p - window < j <= p or j < sinks; window = 0: every j <= p;
+ *   - out is RF_F32 or of q's type (out_dtype), rounded once; lse fp32 in
+ *     natural-log units, may be NULL where not stated otherwise.  A row without
+ *     a visible key gets out = 0 and lse = -inf;
+ *   - seg_m, seg_l [B*H, S], seg_acc [B*H, S, D] fp32: scratch of one call in
+ *     flight (unlike rf_attn_decode_split's, their contents are not an
+ *     output).  counters: int32 [B * Hkv * ceil(G / 16)], all 0 before the
+ *     first call; a call that completes leaves them 0.  Calls (or graph
+ *     replays) that may overlap on the GPU need scratch and counters of their
+ *     own.  Segments only divide the work: results do not depend on which CTA
+ *     finishes first, and S is at most 4096 (rf_decode_segments proposes one).
+ * Errors common to them: RF_ERR_INVALID_ARG for null pointers (but those that
+ * may be NULL), sizes <= 0, H % Hkv != 0, window or sinks < 0, S < 1, a
+ * non-finite scale or a bad dtype; RF_ERR_UNSUPPORTED for D != 128, RF_F32
+ * inputs, S > 4096, cap > 2^30, or a launch of 2^31 CTAs or more;
+ * RF_ERR_MISALIGNED unless q, k, v, out and seg_acc are 16-byte aligned.
+ */
+
+/*
+ * rf_decode_segments -- a number of segments that fills the current device
+ * when `groups` rows of CTAs (B * Hkv * ceil(G / 16)) each read up to `keys`
+ * visible keys: at least 1, at most 4096; 0 if the device cannot be queried.
+ */
+int rf_decode_segments(int groups, int keys);
+
+/*
+ * rf_attn_decode_window -- one token per sequence over the visible keys of a
+ * ragged batch of caches, in one launch.
+ *   q [B, H, D];  k, v [B, Hkv, cap, D];  out [B, H, D];  lse [B, H]
+ */
+rf_status rf_attn_decode_window(const void* q, const void* k, const void* v, const int32_t* lens,
+                                int B, int H, int Hkv, int cap, int D, int window, int sinks,
+                                int S, float scale, int dtype, float* seg_m, float* seg_l,
+                                float* seg_acc, int* counters, void* out, int out_dtype,
+                                float* lse, void* stream);
+
+/*
+ * rf_attn_decode_weights -- rf_attn_decode_window without a window, which also
+ * adds to each key the weight it received: for key head k
+ *   weight_out[b, k, j] = weight[b, k, j] + sum_{h of the group} exp(s_hj - lse_h),  j < lens[b].
+ * Behind the end weight_out is a copy of weight.
+ *   weight      [B, Hkv, cap] fp32, may be NULL (zeros) or equal to weight_out
+ *               (in place; no other overlap)
+ *   scores      [B, H, cap] fp32 scratch
+ *   weight_out  [B, Hkv, cap] fp32 out
+ * Two launches (the weights need the finished normaliser of their row).
+ */
+rf_status rf_attn_decode_weights(const void* q, const void* k, const void* v, const int32_t* lens,
+                                 int B, int H, int Hkv, int cap, int D, int S, float scale,
+                                 int dtype, float* seg_m, float* seg_l, float* seg_acc,
+                                 int* counters, float* scores, void* out, int out_dtype,
+                                 float* lse, const float* weight, float* weight_out,
+                                 void* stream);
+
+/*
+ * rf_cache_evict -- keep `keep` rows of every (sequence, key head) of a cache:
+ * the first `sinks`, the last `recent` and, of those between, the ones of
+ * largest weight (equal weights: lower index first; NaN ranks below every
+ * number).  Kept rows move to another cache in their old order; a sequence
+ * of at most `keep` rows is copied whole.  Destination rows behind a short
+ * sequence are left as they were.
+ *   k, v        [B, Hkv, cap, D] of dtype (RF_F32, RF_BF16 or RF_F16); v and
+ *               v_out may both be NULL (a cache of one tensor, as MLA's)
+ *   weight      [B, Hkv, cap] fp32
+ *   lens        [B] int32 or NULL, as above
+ *   keep        1 <= keep <= cap_out; sinks + recent <= keep
+ *   k_out, v_out [B, Hkv, cap_out, D], weight_out [B, Hkv, cap_out] fp32 out
+ *   lens_out    [B] int32 out: min(lens[b], keep)
+ *   kept        [B, Hkv, keep] int32 out: source row of each kept row, -1
+ *               behind a short sequence
+ * No output may overlap an input.  D * element size a multiple of 16.
+ * Errors: RF_ERR_INVALID_ARG for null pointers, sizes <= 0, sinks or recent
+ * < 0, sinks + recent > keep, keep > cap_out, v without v_out or the reverse,
+ * a bad dtype or overlapping buffers; RF_ERR_UNSUPPORTED for rows that are
+ * not a multiple of 16 bytes or larger than 65536, cap > 2^30 or a launch of
+ * 2^31 CTAs or more;
+ * RF_ERR_MISALIGNED unless k, v, k_out and v_out are 16-byte aligned.
+ */
+rf_status rf_cache_evict(const void* k, const void* v, const float* weight, const int32_t* lens,
+                         int B, int Hkv, int cap, int D, int dtype, int keep, int sinks,
+                         int recent, int cap_out, void* k_out, void* v_out, float* weight_out,
+                         int32_t* lens_out, int32_t* kept, void* stream);
 
 /* Phase 1 of rf_absmax_quant_fp8_gemm alone (same arguments and rules;
  * any K % 8 == 0 is supported). */

@@ -24,6 +24,9 @@ float64 (numpy), exactly as the pages state the stages:
   (transcript cue 47).
 * multi-latent attention decode -- the attention cascade with every query
   head reading one shared latent cache (transcript cues 41 and 55).
+* attention over a serving cache of grouped heads (windows, sinks, a shared
+  prefix, weights per key) and eviction from it -- the same softmax over the
+  visible keys, one sequence at a time; the pages name none of these forms.
 
 Every floating-point step is float64 unless the step itself is a rounding to a
 narrower format the method fixes (fp32 scale and fp32 quotient before the e4m3
@@ -36,4 +39,4 @@ scaled-dot-product attention, torch's own float8/bfloat16 casts), the e4m3
 definition checked exhaustively, and brute force on tiny inputs.
 """
 
-from . import attention, routing, fp8, bf16, rowcascades, mla  # noqa: F401
+from . import attention, routing, fp8, bf16, rowcascades, mla, cache  # noqa: F401
