@@ -65,6 +65,11 @@ _SIGNATURES = {
                                    _P, _P, _P, _I, _P, _P]),
     "rf_attn_decode_weights": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P,
                                     _P, _P, _I, _P, _P, _P, _P]),
+    "rf_attn_prefill_window": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P,
+                                    _P]),
+    "rf_prefix_segments": (_I, [_I, _I, _I, _I]),
+    "rf_attn_decode_shared": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                   _P, _P, _P, _P, _P, _I, _P, _P]),
     "rf_cache_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                             _P]),
 }
@@ -464,6 +469,48 @@ def rf_attn_decode_weights(q, k, v, lens, S, scale, seg_m, seg_l, seg_acc, count
              _ptr(weight_out))
 
 
+def rf_attn_prefill_window(q, k, v, window, sinks, scale, out, lse=None, stream=None):
+    """q/out [B, H, N, D], the last N of L positions; k/v [B, Hkv, L, D] (bf16 or fp16, D = 128);
+    lse [B, H, N] fp32 (optional)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, H, N, D] and k [B, Hkv, L, D]")
+    B, H, N, D = q.shape
+    Hkv, L = k.shape[1], k.shape[2]
+    _need(q, q.dtype, "q")
+    _need(k, q.dtype, "k", (B, Hkv, L, D))
+    _need(v, q.dtype, "v", (B, Hkv, L, D))
+    _need(out, q.dtype, "out", (B, H, N, D))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (B, H, N))
+    dev = _one_device(q, k, v, out, lse)
+    _call_on(dev, stream, "rf_attn_prefill_window", _lib.rf_attn_prefill_window, _ptr(q), _ptr(k),
+             _ptr(v), B, H, Hkv, N, L, D, int(window), int(sinks), float(scale),
+             _cache_dtype(q.dtype, "q"), _ptr(out), _ptr(lse))
+
+
+def rf_prefix_segments(B, H, Hkv, prefix):
+    """Segments that rf_attn_decode_shared uses for the prefix on the current device (0: none)."""
+    return _lib.rf_prefix_segments(int(B), int(H), int(Hkv), int(prefix))
+
+
+def rf_attn_decode_shared(q, kp, vp, k, v, lens, Sp, S, scale, seg_m, seg_l, seg_acc, counters,
+                          out, lse=None, stream=None):
+    """q [B, H, D]; kp/vp [Hkv, prefix, D] shared by the batch; k/v [B, Hkv, cap, D] with lens [B]
+    own keys -> out [B, H, D], lse [B, H].  Scratch as rf_attn_decode_window with Sp + S segments."""
+    B, H, Hkv, cap, D = _need_cache(q, k, v, lens)
+    if kp.dim() != 3:
+        raise ValueError("kp must be [Hkv, prefix, D]")
+    prefix = kp.shape[1]
+    _need(kp, q.dtype, "kp", (Hkv, prefix, D))
+    _need(vp, q.dtype, "vp", (Hkv, prefix, D))
+    _need_scratch(B, H, Hkv, D, Sp + S, seg_m, seg_l, seg_acc, counters, out, lse)
+    dev = _one_device(q, kp, vp, k, v, lens, seg_m, seg_l, seg_acc, counters, out, lse)
+    _call_on(dev, stream, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, _ptr(q), _ptr(kp),
+             _ptr(vp), prefix, _ptr(k), _ptr(v), _ptr(lens), B, H, Hkv, cap, D, int(Sp), int(S),
+             float(scale), _cache_dtype(q.dtype, "q"), _ptr(seg_m), _ptr(seg_l), _ptr(seg_acc),
+             _ptr(counters), _ptr(out), _cache_dtype(out.dtype, "out"), _ptr(lse))
+
+
 def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight_out, lens_out,
                    kept, stream=None):
     """k/v [B, Hkv, cap, D] (fp32, bf16 or fp16; v None for a cache of one tensor), weight
@@ -614,18 +661,18 @@ class DecodeWorkspace:
 
 def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights=False, S=None,
                      device=None):
-    """Scratch for attn_decode_window (window, sinks as in the call) or attn_decode_weights
-    (weights=True), with the number of segments that fills the device."""
+    """Scratch for attn_decode_window (window, sinks as in the call), attn_decode_shared (the
+    prefix's length) or attn_decode_weights (weights=True), with the number of segments that
+    fills the device."""
     if H < 1 or Hkv < 1 or H % Hkv:
         raise ValueError("H must be a positive multiple of Hkv")
-    if prefix:
-        raise ValueError("prefix is not supported yet")
-    dev = torch.device("cuda" if device is None else device)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(torch.device("cuda" if device is None else device)):
+        dev = torch.device("cuda", torch.cuda.current_device())
         if S is None:
             keys = min(cap, window + sinks) if window else cap
             S = rf_decode_segments(B * Hkv * (-(-(H // Hkv) // 16)), keys)
-        return DecodeWorkspace(B, H, Hkv, D, S, 0, cap, weights, torch.device("cuda", torch.cuda.current_device()))
+        prefix_S = rf_prefix_segments(B, H, Hkv, prefix) if prefix else 0
+        return DecodeWorkspace(B, H, Hkv, D, S, prefix_S, cap, weights, dev)
 
 
 def _on_stream(stream):
@@ -649,6 +696,38 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
         out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
         lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
         rf_attn_decode_window(q, k, v, lens, window, sinks, work.S,
+                              D ** -0.5 if scale is None else scale, work.seg_m, work.seg_l,
+                              work.seg_acc, work.counters, out, lse, stream)
+    return out, lse
+
+
+def attn_prefill_window(q, k, v, window=0, sinks=0, scale=None, stream=None):
+    """Attention of the last N of L positions over their visible keys: one of the ``window`` keys
+    up to the position itself (0: all) or one of the first ``sinks``.
+
+    q [B, H, N, D], k/v [B, Hkv, L, D] (bf16 or fp16).  Returns out [B, H, N, D] and lse [B, H, N]."""
+    with _on_stream(stream):
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:-1], device=q.device, dtype=torch.float32)
+        rf_attn_prefill_window(q, k, v, window, sinks, q.shape[-1] ** -0.5 if scale is None else scale,
+                               out, lse, stream)
+    return out, lse
+
+
+def attn_decode_shared(q, kp, vp, k, v, lens=None, scale=None, work=None, out_dtype=None,
+                       stream=None):
+    """Single-token decode for a batch whose sequences share their first keys.
+
+    q [B, H, D]; kp/vp [Hkv, prefix, D]; k/v [B, Hkv, cap, D] with lens [B] own keys behind the
+    prefix (None: cap; 0 allowed).  Returns out [B, H, D] and lse [B, H]."""
+    B, H, D = q.shape
+    with _on_stream(stream):
+        if work is None:
+            work = decode_workspace(B, H, k.shape[1], k.shape[2], D, prefix=kp.shape[1],
+                                    device=q.device)
+        out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
+        lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
+        rf_attn_decode_shared(q, kp, vp, k, v, lens, work.prefix_S, work.S,
                               D ** -0.5 if scale is None else scale, work.seg_m, work.seg_l,
                               work.seg_acc, work.counters, out, lse, stream)
     return out, lse

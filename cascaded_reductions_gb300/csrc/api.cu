@@ -332,6 +332,62 @@ rf_status rf_attn_decode_weights(const void* q, const void* k, const void* v, co
   return rf::launch_add_weights(a, weight, weight_out, as_stream(stream));
 }
 
+rf_status rf_attn_prefill_window(const void* q, const void* k, const void* v, int B, int H,
+                                 int Hkv, int N, int L, int D, int window, int sinks, float scale,
+                                 int dtype, void* out, float* lse, void* stream) {
+  if (!q || !k || !v || !out) return RF_ERR_INVALID_ARG;
+  if (N <= 0 || N > L || window < 0 || sinks < 0) return RF_ERR_INVALID_ARG;
+  const rf_status s = check_cache_shape(B, H, Hkv, L, D, scale, dtype);
+  if (s != RF_OK) return s;
+  if (!(scale > 0.f)) return RF_ERR_UNSUPPORTED;
+  const long long heads = (long long)B * H;
+  if (heads > 0x7fffffffLL || heads * N > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(q) || !rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(out))
+    return RF_ERR_MISALIGNED;
+  return rf::launch_prefill_window(q, k, v, B, H, Hkv, N, L, window, sinks, scale, dtype, out, lse,
+                                   as_stream(stream));
+}
+
+int rf_prefix_segments(int B, int H, int Hkv, int prefix) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128 || prefix <= 0 ||
+      (long long)B * Hkv > 0x7fffffffLL)
+    return 0;
+  return rf::prefix_segments(B, H, Hkv, prefix);
+}
+
+rf_status rf_attn_decode_shared(const void* q, const void* kp, const void* vp, int prefix,
+                                const void* k, const void* v, const int32_t* lens, int B, int H,
+                                int Hkv, int cap, int D, int Sp, int S, float scale, int dtype,
+                                float* seg_m, float* seg_l, float* seg_acc, int* counters,
+                                void* out, int out_dtype, float* lse, void* stream) {
+  if (!q || !kp || !vp || !k || !v || !seg_m || !seg_l || !seg_acc || !counters || !out)
+    return RF_ERR_INVALID_ARG;
+  if (prefix <= 0 || Sp < 2) return RF_ERR_INVALID_ARG;
+  rf_status s = check_cache_shape(B, H, Hkv, cap, D, scale, dtype);
+  if (s != RF_OK) return s;
+  s = check_segments(B, H, Hkv, S, dtype, out_dtype);
+  if (s != RF_OK) return s;
+  if (!(scale > 0.f) || Sp > 4096 || H / Hkv > 128 || prefix > (1 << 30)) return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(q) || !rf::aligned16(kp) || !rf::aligned16(vp) || !rf::aligned16(k) ||
+      !rf::aligned16(v) || !rf::aligned16(out) || !rf::aligned16(seg_acc))
+    return RF_ERR_MISALIGNED;
+  s = rf::launch_prefix_states(q, kp, vp, prefix, B, H, Hkv, Sp, Sp + S, scale, dtype, seg_m, seg_l,
+                               seg_acc, as_stream(stream));
+  if (s != RF_OK) return s;
+  rf::CacheDecode a = {};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k = static_cast<const uint8_t*>(k);
+  a.v = static_cast<const uint8_t*>(v);
+  a.lens = lens;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.cap = cap;
+  a.S = S, a.S_total = Sp + S, a.seg0 = Sp;
+  a.scale_log2 = scale * rf::kLog2e;
+  a.seg_m = seg_m, a.seg_l = seg_l, a.seg_acc = seg_acc;
+  a.counters = counters;
+  a.out = out, a.out_dtype = out_dtype, a.lse = lse;
+  return rf::launch_cache_decode(a, dtype, as_stream(stream));
+}
+
 rf_status rf_cache_evict(const void* k, const void* v, const float* weight, const int32_t* lens,
                          int B, int Hkv, int cap, int D, int dtype, int keep, int sinks,
                          int recent, int cap_out, void* k_out, void* v_out, float* weight_out,

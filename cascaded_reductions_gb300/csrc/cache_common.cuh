@@ -57,6 +57,18 @@ rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st);
 // weight may be null (zeros) or equal to total (in place)
 rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* total,
                              cudaStream_t st);
+// window 0: none.  scale > 0.
+rf_status launch_prefill_window(const void* q, const void* k, const void* v, int B, int H, int Hkv,
+                                int N, int L, int window, int sinks, float scale, int dtype,
+                                void* out, float* lse, cudaStream_t st);
+// State slots that the prefix kernel would use per row on the current device
+// (at least 2), 0 if it cannot run there.  B, H / Hkv <= 128 as checked.
+int prefix_segments(int B, int H, int Hkv, int prefix);
+// States of every row over the shared prefix, in slots 0 .. Sp - 1 of S_total
+// (unused ones marked empty).  Sp >= 2, scale > 0.
+rf_status launch_prefix_states(const void* q, const void* kp, const void* vp, int prefix, int B,
+                               int H, int Hkv, int Sp, int S_total, float scale, int dtype,
+                               float* seg_m, float* seg_l, float* seg_acc, cudaStream_t st);
 rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
                              const int32_t* lens, int B, int Hkv, int cap, int row_bytes, int keep,
                              int sinks, int recent, int cap_out, void* k_out, void* v_out,

@@ -1,0 +1,288 @@
+// Prefill of the last N of L positions with a sliding window and a few first
+// tokens that stay visible, grouped heads, on CTA pairs (the kernel is in
+// attn_pair.cuh).
+//
+// Mathematics: the causal prefill's cascade over the visible keys only,
+//   visible(p) = { j <= p : j > p - window or j < sinks }.
+//
+// What bounds it: the tensor pipe, 4 D flops per pair of row and key.  An item
+// is 256 adjacent rows; it visits the 256-key blocks that cover the keys any
+// of its rows sees, counted from the lowest of them (so a window of W keys
+// takes ceil((W + 255) / 256) blocks and never one more for alignment), last
+// block first, and then the blocks of the sinks below that cover.  Only the
+// blocks at the two edges are masked, and only by the warps that an edge
+// crosses.
+//
+// A row that sees nothing of a block must not be disturbed by it: its
+// reference starts at a finite value below every score, so such a block gives
+// weights of exactly 0.  The products still multiply those zeros with V, and
+// 0 * NaN is NaN: a value row that is not finite would reach rows that do not
+// see it.  A row whose output is NaN is therefore computed again after the
+// last item, from its visible keys alone.
+
+#include <cuda_fp16.h>
+
+#include "attn_pair.cuh"
+
+namespace rf {
+namespace {
+
+using pair::BM;
+using pair::BN;
+using pair::HALF_BYTES;
+using pair::HD;
+
+template <bool F16_>
+struct WindowPrefill {
+  static constexpr bool F16 = F16_;
+  static constexpr float M_START = -1e30f;
+  struct Item {
+    int bh, kvh;     // query head of the batch, key head of the batch
+    int row0;        // first of 256 query rows
+    int lo;          // first key of the window blocks
+    int nb;          // window blocks; block j < nb starts at lo + 256 (nb - 1 - j)
+    int limit;       // sinks below lo; block j >= nb starts at 256 (j - nb)
+    int n;
+  };
+  struct Pending {
+    int bh, row;
+    bool in;
+  };
+
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  float* lse;
+  int N, L, G, window, sinks;      // window and sinks at most L
+  int heads;                       // B * H
+  int pairs;                       // items per head
+  float scale_log2;
+
+  // items head-major (query heads of a key head together), last rows first, in
+  // snake order as the causal prefill's
+  __device__ __forceinline__ bool item(int t, int cluster, int nclusters, Item& it) const {
+    const long long turn =
+        (long long)t * nclusters + ((t & 1) ? nclusters - 1 - cluster : cluster);
+    if (turn >= (long long)heads * pairs) return false;
+    const int i = (int)turn;                            // below B * H * N < 2^31
+    it.bh = i / pairs;
+    it.kvh = it.bh / G;
+    it.row0 = (pairs - 1 - i % pairs) * 2 * BM;
+    const int p0 = L - N + it.row0;                     // position of the first row
+    const int hi = min(p0 + 2 * BM, L) - 1;             // last key of the last row
+    it.lo = max(0, p0 - window + 1);
+    it.nb = (hi - it.lo + BN) / BN;
+    it.limit = min(sinks, it.lo);
+    it.n = it.nb + (it.limit + BN - 1) / BN;
+    return true;
+  }
+  __device__ __forceinline__ int key0(const Item& it, int j) const {
+    return j < it.nb ? it.lo + (it.nb - 1 - j) * BN : (j - it.nb) * BN;
+  }
+  __device__ __forceinline__ uint32_t q_bytes() const { return pair::TILE_BYTES; }
+  __device__ __forceinline__ void load_q(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
+                                         const Item& it, int rank) const {
+    const int row = it.row0 + rank * BM;
+    tc::tma_load_3d_pair(dst, map, bar, 0, row, it.bh);
+    tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, row, it.bh);
+  }
+  __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
+                                         const Item& it, int j, int rank) const {
+    const int key = key0(it, j) + rank * (BN / 2);
+    tc::tma_load_3d_pair(dst, map, bar, 0, key, it.kvh);
+    tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, key, it.kvh);
+  }
+  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
+                                         const Item& it, int j, int rank) const {
+    tc::tma_load_3d_pair(dst, map, bar, rank * 64, key0(it, j), it.kvh);
+  }
+  __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
+                                       float (&s)[128]) const {
+    const int base = key0(it, j) + kh * 128;
+    if (j < it.nb) {
+      const int p = L - N + it.row0 + rank * BM + r;    // this row's position
+      const int first = p - (r & 31), last = first + 31;   // the warp's positions
+      const int hi = p - base;                          // s[c] visible up to c = hi
+      if (first - base < 127) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > hi) s[c] = -INFINITY;
+      }
+      if (last - window + 1 > base) {
+        const int lo = p - window + 1 - base, cs = sinks - base;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < lo && c >= cs) s[c] = -INFINITY;
+      }
+    } else {
+      const int lim = it.limit - base;
+      if (lim < 128) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= lim) s[c] = -INFINITY;
+      }
+    }
+  }
+  __device__ __forceinline__ Pending pending(const Item& it, int rank, int r) const {
+    const int row = it.row0 + rank * BM + r;
+    return {it.bh, row, row < N};
+  }
+  __device__ __forceinline__ bool store(const Pending& pend, int kh, const uint32_t (&v)[64],
+                                        float m, float lt) const {
+    const size_t row = (size_t)pend.bh * N + pend.row;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+    const float inv = 1.f / lt;
+    float probe = 0.f;                                  // NaN if any of the row's is not finite
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      uint32_t pkd[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float x0 = __uint_as_float(v[32 * hh + 2 * c]) * inv;
+        const float x1 = __uint_as_float(v[32 * hh + 2 * c + 1]) * inv;
+        probe = fmaf(x0, 0.f, probe);
+        probe = fmaf(x1, 0.f, probe);
+        pkd[c] = pair::pack_16x2<F16>(x0, x1);
+      }
+      const int col = kh * 64 + hh * 32;
+      if (pend.in && RF_SPAN_OK(row * HD + col, 32, (size_t)heads * N * HD))
+        pair::st_row32(out + row * HD + col, pkd, wide);
+    }
+    if (lse != nullptr && kh == 0 && pend.in && RF_IDX_OK(row, (size_t)heads * N))
+      lse[row] = (m + log2f(lt)) * kLn2;
+    return pend.in && !(probe == 0.f);
+  }
+
+  static __device__ __forceinline__ float widen(uint32_t w, int hi) {
+    if constexpr (F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      return hi ? f.y : f.x;
+    }
+    return hi ? bf16_hi(w) : bf16_lo(w);
+  }
+  static __device__ __forceinline__ void widen4(const uint2& u, float (&f)[4]) {
+    f[0] = widen(u.x, 0);
+    f[1] = widen(u.x, 1);
+    f[2] = widen(u.y, 0);
+    f[3] = widen(u.y, 1);
+  }
+  // elements [i, i + 4) of a tensor of n elements
+  static __device__ __forceinline__ uint2 load4(const uint16_t* t, size_t i, size_t n) {
+    (void)n;                                            // read by the checked build only
+    return RF_SPAN_OK(i, 4, n) ? __ldg(reinterpret_cast<const uint2*>(t + i)) : make_uint2(0, 0);
+  }
+  // NaN among the 32-bit word's two values
+  static __device__ __forceinline__ bool has_nan(uint32_t w) {
+    const uint32_t inf = F16 ? 0x7c00u : 0x7f80u;
+    return (w & 0x7fffu) > inf || ((w >> 16) & 0x7fffu) > inf;
+  }
+
+  // One output row's columns 64 kh .. + 63, from its visible keys alone: the
+  // warp's lanes hold four columns each, one key at a time.
+  __device__ void redo(int bh, int row, int kh, int lane) const {
+    const int p = L - N + row;
+    const size_t kv0 = (size_t)(bh / G) * L;
+    const size_t q_n = (size_t)heads * N * HD, kv_n = (size_t)(heads / G) * L * HD;
+    float qf[4];
+    widen4(load4(q, ((size_t)bh * N + row) * HD + lane * 4, q_n), qf);
+    const int lo = max(0, p - window + 1), ns = min(sinks, lo);
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int t = 0; t < ns + p - lo + 1; ++t) {
+      const int key = t < ns ? t : t - ns + lo;
+      const size_t at = (kv0 + key) * HD + lane * 4;
+      float kf[4], vf[4];
+      widen4(load4(k, at, kv_n), kf);
+      widen4(load4(v, at, kv_n), vf);
+      float d = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d = fmaf(qf[e], kf[e], d);
+      const float s = group_sum<32>(d) * scale_log2;
+      const float mn = fmaxf(m, s), ref = ref_of(mn);
+      const float corr = exp2f(m - ref), w = exp2f(s - ref);
+      m = mn;
+      l = fmaf(l, corr, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], corr, w * vf[e]);
+    }
+    const size_t o = ((size_t)bh * N + row) * HD + lane * 4;
+    if ((lane >> 4) == kh && RF_SPAN_OK(o, 4, q_n)) {
+      uint2 w;
+      w.x = pair::pack_16x2<F16>(acc[0] / l, acc[1] / l);
+      w.y = pair::pack_16x2<F16>(acc[2] / l, acc[3] / l);
+      *reinterpret_cast<uint2*>(out + o) = w;
+    }
+    if (lse != nullptr && kh == 0 && lane == 0 && RF_IDX_OK((size_t)bh * N + row, (size_t)heads * N))
+      lse[(size_t)bh * N + row] = (m + log2f(l)) * kLn2;
+  }
+
+  // Rows of this thread whose stored columns hold a NaN are computed again.
+  __device__ __noinline__ void repair(int cluster, int nclusters, int rank, int r, int kh) const {
+    Item it;
+    for (int t = 0; item(t, cluster, nclusters, it); ++t) {
+      const int row = it.row0 + rank * BM + r;
+      bool nan = false;
+      if (row < N) {
+        const size_t o = ((size_t)it.bh * N + row) * HD + kh * 64;
+        for (int c = 0; c < 8; ++c) {
+          if (!RF_SPAN_OK(o + c * 8, 8, (size_t)heads * N * HD)) continue;
+          const uint4 u = *(reinterpret_cast<const uint4*>(out + o) + c);
+          nan |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
+        }
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, nan);
+      while (todo) {
+        const int lane0 = __ffs(todo) - 1;
+        todo &= todo - 1;
+        redo(it.bh, __shfl_sync(0xffffffffu, row, lane0), kh, r & 31);
+      }
+    }
+  }
+  __device__ __forceinline__ void after(bool any, int cluster, int nclusters, int rank, int r,
+                                        int kh) const {
+    if (__any_sync(0xffffffffu, any)) repair(cluster, nclusters, rank, r, kh);
+  }
+};
+
+template <bool F16>
+rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, int Hkv, int N, int L,
+                   int window, int sinks, float scale, void* out, float* lse, cudaStream_t st) {
+  using P = WindowPrefill<F16>;
+  const int pairs = pair::resident_pairs<P>();
+  if (pairs <= 0) return RF_ERR_UNSUPPORTED;
+  CUtensorMap tq, tk, tv;
+  const uint64_t qh = (uint64_t)B * H, kh = (uint64_t)B * Hkv;
+  if (!tc::make_tmap_3d_16(&tq, F16, q, HD, N, qh, 64, BM, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_tmap_3d_16(&tk, F16, k, HD, L, kh, 64, BN / 2, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_tmap_3d_16(&tv, F16, v, HD, L, kh, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B))
+    return RF_ERR_CUDA;
+  P p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.N = N, p.L = L, p.G = H / Hkv;
+  p.window = window == 0 || window > L ? L : window;
+  p.sinks = sinks > L ? L : sinks;
+  p.heads = B * H;
+  p.pairs = (N + 2 * BM - 1) / (2 * BM);
+  p.scale_log2 = scale * kLog2e;
+  const long long items = (long long)p.heads * p.pairs;
+  return pair::launch_pair(tq, tk, tv, p, (int)(pairs < items ? pairs : items), st);
+}
+
+}  // namespace
+
+rf_status launch_prefill_window(const void* q, const void* k, const void* v, int B, int H, int Hkv,
+                                int N, int L, int window, int sinks, float scale, int dtype,
+                                void* out, float* lse, cudaStream_t st) {
+  return dtype == RF_F16
+             ? launch_t<true>(q, k, v, B, H, Hkv, N, L, window, sinks, scale, out, lse, st)
+             : launch_t<false>(q, k, v, B, H, Hkv, N, L, window, sinks, scale, out, lse, st);
+}
+
+RF_TIMEOUT_WORD_OF_THIS_FILE
+
+RF_BOUNDS_WORD_OF_THIS_FILE
+
+}  // namespace rf

@@ -369,6 +369,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// the same for a 3-D tile; z is the outermost coordinate
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                 int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // D (TMEM of both CTAs) [+]= A (shared memory of both CTAs) * B (both), e4m3.
 // M = 256: CTA r supplies rows [128 r, 128 r + 128) of A and holds those rows
 // of D; B's N columns are split the same way between the two CTAs.
@@ -474,6 +484,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
 bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
                   uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                   uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
+// the same for a dense 3-D tensor [outer][mid][inner] of 16-bit elements; reads
+// past an extent give zeros, so a box never leaves its row of `outer`
+bool make_tmap_3d_16(CUtensorMap* map, bool f16, const void* base, uint64_t inner, uint64_t mid,
+                     uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
+                     CUtensorMapSwizzle swizzle);
 
 int sm_count();
 

@@ -366,6 +366,53 @@ rf_status rf_attn_decode_window(const void* q, const void* k, const void* v, con
                                 float* lse, void* stream);
 
 /*
+ * rf_attn_prefill_window -- attention of N query rows at the positions
+ * L - N .. L - 1 of a sequence over its L keys, with the window and sinks of
+ * the conventions above (window = 0: causal).  N = L is a whole prompt, N < L
+ * one chunk of it behind what the cache holds already.  All sequences of a
+ * batch have the same N and L; a prompt padded at its end is right as it is
+ * (no row sees a key behind it).
+ *   q [B, H, N, D];  k, v [B, Hkv, L, D];  out [B, H, N, D] of q's type;
+ *   lse [B, H, N] fp32 or NULL
+ * A key or value row that is not finite reaches only the rows that see it.
+ * Errors: as the conventions above (no lens, S, scratch or counters), plus
+ * RF_ERR_INVALID_ARG for N > L and RF_ERR_UNSUPPORTED for scale <= 0,
+ * B*H*N >= 2^31, or a device that cannot hold a cluster of two CTAs with about
+ * 200 KiB of shared memory each.
+ */
+rf_status rf_attn_prefill_window(const void* q, const void* k, const void* v, int B, int H,
+                                 int Hkv, int N, int L, int D, int window, int sinks, float scale,
+                                 int dtype, void* out, float* lse, void* stream);
+
+/*
+ * rf_prefix_segments -- the number of segments that rf_attn_decode_shared uses
+ * for the prefix on the current device: at least 2; 0 if the device cannot run
+ * it or the sizes are not valid.
+ */
+int rf_prefix_segments(int B, int H, int Hkv, int prefix);
+
+/*
+ * rf_attn_decode_shared -- one token per sequence for a batch whose sequences
+ * share their first `prefix` keys: softmax attention over the prefix and the
+ * sequence's own keys together.  The prefix is read once for the whole batch
+ * (on the tensor cores, B * G rows against each key), the own keys as by
+ * rf_attn_decode_window, and the states are merged.  Two launches.
+ *   q [B, H, D];  kp, vp [Hkv, prefix, D], prefix >= 1;  k, v [B, Hkv, cap, D]
+ *   with lens [B] own keys each (0 allowed; the query stands behind all of them)
+ *   Sp   segments of the prefix, >= 2;  S  segments of the own keys, >= 1
+ *   seg_m, seg_l [B*H, Sp + S], seg_acc [B*H, Sp + S, D], counters: as above
+ * Errors: as above, plus RF_ERR_INVALID_ARG for prefix <= 0 or Sp < 2,
+ * RF_ERR_UNSUPPORTED for Sp > 4096, H / Hkv > 128, prefix > 2^30, scale <= 0 or
+ * a device as for rf_attn_prefill_window; RF_ERR_MISALIGNED unless kp and vp
+ * are 16-byte aligned.
+ */
+rf_status rf_attn_decode_shared(const void* q, const void* kp, const void* vp, int prefix,
+                                const void* k, const void* v, const int32_t* lens, int B, int H,
+                                int Hkv, int cap, int D, int Sp, int S, float scale, int dtype,
+                                float* seg_m, float* seg_l, float* seg_acc, int* counters,
+                                void* out, int out_dtype, float* lse, void* stream);
+
+/*
  * rf_attn_decode_weights -- rf_attn_decode_window without a window, which also
  * adds to each key the weight it received: for key head k
  *   weight_out[b, k, j] = weight[b, k, j] + sum_{h of the group} exp(s_hj - lse_h),  j < lens[b].

@@ -107,3 +107,66 @@ def test_evict_refusals(lib):
 
 def test_segment_proposal_is_positive_or_zero_without_a_device(lib):
     assert 0 <= lib.rf_decode_segments(64, 4096) <= 64
+
+
+def prefill_args(**o):
+    return [o.get("q", FAKE), o.get("k", FAKE), o.get("v", FAKE), o.get("B", 2), o.get("H", 8),
+            o.get("Hkv", 2), o.get("N", 10), o.get("cap", 100), o.get("D", 128), o.get("window", 0),
+            o.get("sinks", 0), F(o.get("scale", 0.1)), o.get("dtype", 1), o.get("out", FAKE), NULL, NULL]
+
+
+def test_prefill_refusals(lib):
+    f = lib.rf_attn_prefill_window
+    for name in ("q", "k", "v", "out"):
+        assert f(*prefill_args(**{name: NULL})) == 1, name
+        assert f(*prefill_args(**{name: ODD})) == 3, name
+    for name in ("B", "H", "Hkv", "N", "cap", "D"):
+        assert f(*prefill_args(**{name: 0})) == 1, name
+    assert f(*prefill_args(N=101)) == 1             # more rows than positions
+    assert f(*prefill_args(H=7)) == 1
+    assert f(*prefill_args(window=-1)) == 1
+    assert f(*prefill_args(sinks=-1)) == 1
+    assert f(*prefill_args(scale=float("nan"))) == 1
+    assert f(*prefill_args(dtype=3)) == 1
+    assert f(*prefill_args(dtype=0)) == 2           # fp32
+    assert f(*prefill_args(D=64)) == 2
+    assert f(*prefill_args(scale=0.0)) == 2
+    assert f(*prefill_args(scale=-0.1)) == 2
+    assert f(*prefill_args(B=1 << 20, H=1 << 10, Hkv=1 << 10, N=4, cap=4)) == 2
+    assert f(*prefill_args(cap=(1 << 30) + 1)) == 2
+
+
+def shared_args(**o):
+    return [o.get("q", FAKE), o.get("kp", FAKE), o.get("vp", FAKE), o.get("prefix", 1000), o.get("k", FAKE),
+            o.get("v", FAKE), NULL, o.get("B", 2), o.get("H", 8), o.get("Hkv", 2), o.get("cap", 100),
+            o.get("D", 128), o.get("Sp", 4), o.get("S", 4), F(o.get("scale", 0.1)), o.get("dtype", 1),
+            o.get("seg_m", FAKE), o.get("seg_l", FAKE), o.get("seg_acc", FAKE), o.get("counters", FAKE),
+            o.get("out", FAKE), o.get("out_dtype", 1), NULL, NULL]
+
+
+def test_shared_refusals(lib):
+    f = lib.rf_attn_decode_shared
+    for name in ("q", "kp", "vp", "k", "v", "seg_m", "seg_l", "seg_acc", "counters", "out"):
+        assert f(*shared_args(**{name: NULL})) == 1, name
+    for name in ("B", "H", "Hkv", "cap", "D", "prefix"):
+        assert f(*shared_args(**{name: 0})) == 1, name
+    assert f(*shared_args(Sp=1)) == 1
+    assert f(*shared_args(S=0)) == 1
+    assert f(*shared_args(H=7)) == 1
+    assert f(*shared_args(out_dtype=2)) == 1
+    assert f(*shared_args(scale=float("inf"))) == 1
+    assert f(*shared_args(Sp=4097)) == 2
+    assert f(*shared_args(S=4097)) == 2
+    assert f(*shared_args(scale=0.0)) == 2
+    assert f(*shared_args(scale=-1.0)) == 2
+    assert f(*shared_args(H=129, Hkv=1)) == 2       # more query heads than a tile has rows
+    assert f(*shared_args(prefix=(1 << 30) + 1)) == 2
+    assert f(*shared_args(dtype=0, out_dtype=0)) == 2
+    assert f(*shared_args(D=64)) == 2
+    for name in ("q", "kp", "vp", "k", "v", "out", "seg_acc"):
+        assert f(*shared_args(**{name: ODD})) == 3, name
+
+
+def test_prefix_segments_refuses_bad_sizes(lib):
+    for a in ((0, 8, 2, 10), (2, 7, 2, 10), (2, 8, 2, 0), (2, 129, 1, 10), (-1, 8, 2, 10)):
+        assert lib.rf_prefix_segments(*a) == 0
