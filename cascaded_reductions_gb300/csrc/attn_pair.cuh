@@ -62,6 +62,7 @@
 //                              where the first block always holds a visible
 //                              key, else a finite value below every score, for
 //                              which a block without visible keys gives p = 0
+//   DEPENDENTS                 the next kernel may start beside this one's end
 //   Item, Pending              a work item; what its output still needs
 //   item(t, c, nc, it)         cluster c's t-th item of nc clusters; it.n key
 //                              blocks, at least one; false past the last
@@ -207,6 +208,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int rank = (int)tc::cluster_ctarank();        // 0 or 1
   const int cluster = (int)(blockIdx.x >> 1), nclusters = (int)(gridDim.x >> 1);
 
+  if constexpr (P::DEPENDENTS) allow_dependents();
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sh->q_full[b], 1);

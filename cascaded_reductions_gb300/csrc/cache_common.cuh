@@ -12,26 +12,60 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Keys of a segment when n keys are split into S: whole 16-key tiles, and at
-// least 64 keys (one tile for each of a CTA's four warps), so that short
-// sequences leave segments empty instead of warps idle.
-__host__ __device__ __forceinline__ int segment_keys(int n, int S) {
-  const int c = ((n + S - 1) / S + 15) & ~15;
-  return c < 64 ? 64 : c;
+constexpr int kDecodeTile = 16;        // keys of one tile of the decode kernels
+
+// Programmatic dependent launch: a kernel launched with launch_after begins when
+// every CTA of the kernel before it on the stream has called
+// allow_dependents() or ended, and may use that kernel's results (and those of
+// everything before it) after wait_prerequisite().
+__device__ __forceinline__ void allow_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_prerequisite() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+inline rf_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                              cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return RF_ERR_CUDA;
+  }
+  return launch_status();
 }
 
-// Segments for `groups` rows of CTAs of up to `keys` visible keys each: two
-// resident CTAs on every SM, in segments of no more than 512 keys where there
-// are more CTAs than that anyway (so that the last ones to run are short), and
-// no segment below 64 keys.
+// Keys of a piece of a row at least: one step of the CTA's four warps in a small
+// call, enough to pay for a CTA's start and end in a large one.
+constexpr int kFewKeys = 4 * kDecodeTile, kManyKeys = 768;
+
+// Whether a call of `groups` row groups of up to `keys` visible keys is small:
+// at most four steps of 64 keys for each of two CTAs per SM.
+inline bool decode_is_few(long long groups, int keys, int sms) {
+  return groups * ((keys + kFewKeys - 1) / kFewKeys) <= 8ll * sms;
+}
+
+// Pieces per row for such a call: a small one is divided until two CTAs per SM
+// have work, a large one into the smallest pieces that are worth a CTA.
 inline int decode_segments(int groups, int keys, int sms) {
-  const long long fill = (2ll * sms + groups - 1) / groups;
-  const long long fine = groups >= sms / 4 ? (keys + 511) / 512 : 1;
-  long long s = fill > fine ? fill : fine;
-  const long long most = (keys + 63) / 64;
-  if (s > most) s = most;
-  if (s > 4096) s = 4096;
-  return (int)(s < 1 ? 1 : s);
+  long long s;
+  if (decode_is_few(groups, keys, sms)) {
+    s = (2ll * sms + groups - 1) / groups;
+    const int steps = (keys + kFewKeys - 1) / kFewKeys;
+    if (s > steps) s = steps;
+  } else {
+    s = (keys + kManyKeys - 1) / kManyKeys;
+  }
+  return (int)(s > 4096 ? 4096 : s);
 }
 
 // One call's arguments.  Segment states are scratch between kernels: seg_m
@@ -42,17 +76,18 @@ struct CacheDecode {
   const int32_t* lens;           // [B] or null (every sequence holds cap keys)
   int B, H, Hkv, cap;
   int window, sinks;             // window 0: every key is visible
-  int S, S_total, seg0;          // this kernel's segments seg0 .. seg0 + S - 1 of S_total
+  int S, S_total, seg0;          // this kernel's slots seg0 .. seg0 + S - 1 of S_total
   float scale_log2;
   float *seg_m, *seg_l, *seg_acc;   // [B * H, S_total (, 128)]
-  int* counters;                 // [B * Hkv * mtiles], zero before and after
+  int* counters;                 // [B * Hkv * mtiles], zero before and after the call
   void* out;                     // [B, H, 128]
   int out_dtype;
   float* lse;                    // [B, H] or null
   float* scores;                 // [B, H, cap] log2-unit scores, or null
-  int G, mtiles;                 // set by the launcher
+  int G, mtiles, piece_keys;     // set by the launcher
 };
 
+// With seg0 > 0 the kernel before it on the stream writes the first seg0 slots.
 rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st);
 // weight may be null (zeros) or equal to total (in place)
 rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* total,

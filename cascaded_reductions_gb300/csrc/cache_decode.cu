@@ -1,12 +1,12 @@
 // Single-token decode over a cache of grouped heads: H query heads share Hkv
 // key/value heads (head h reads key head h / G, G = H / Hkv), every sequence
 // has its own length, and a mask may leave only the last `window` keys and the
-// first `sinks` visible.  The same kernel, with its segments numbered after
-// those of the prefix kernel, is the suffix half of the shared-prefix decode,
-// and with its scores kept it feeds the running total of each key's weight.
+// first `sinks` visible.  The same kernels, with their states numbered after
+// those of the prefix kernel, are the suffix half of the shared-prefix decode,
+// and with their scores kept they feed the running total of each key's weight.
 //
 // Mathematics: per row the cascade of the split-KV decode (running m, l, acc,
-// rescale by exp2(m_old - m_new), segment states merged by the same rescale).
+// rescale by exp2(m_old - m_new), states merged by the same rescale).
 //
 // What bounds it: HBM.  A key of a key head costs 512 bytes (K and V) and
 // 4 G D = 512 G flops; on the FP32 pipes G = 4 heads would already need as
@@ -15,37 +15,49 @@
 // idle, which costs nothing here: 16 keys need 48 instructions while their
 // 8 KiB take an SM about 350 cycles).
 //
-// Split: one CTA per (sequence, key head, 16-row tile of query heads,
-// segment); its four warps take turns over tiles of 16 keys, each warp with a
-// ring of its own (3 stages of 8 KiB, filled by 16-byte asynchronous copies,
-// so no block-wide barrier is needed until the end).  Only visible keys are
-// read: positions are numbered over the visible keys and mapped to cache rows.
-// Rows past a segment's end are zero-filled, never read.
+// Only visible keys are read: positions are numbered over the visible keys and
+// mapped to cache rows, in tiles of 16 per warp; a warp fills a ring of its own
+// (3 stages of 8 KiB) by 16-byte asynchronous copies.  Rows past a group's end
+// are zero-filled, never read.
 //
 // P in two terms: the weights enter the second product as hi + lo, two 16-bit
 // terms, so that they carry 16 (bf16) or 22 (fp16) bits and the output is
 // rounded once; the 16 extra matrix instructions per tile are free here.
 //
-// The CTA that completes a row group's count merges its segments in segment
-// order (bitwise reproducible) and sets the count back to 0.
+// Split: a row group (sequence, key head, 16-row tile of query heads) is divided
+// into pieces by its own length, one CTA of four warps each; a step of the CTA
+// is 64 keys, a tile per warp.  Warps merge through shared memory, pieces
+// through state slots in memory: in small calls by the last CTA of the group to
+// arrive (no second launch), in large ones by merge_kernel, because the fence
+// and the count cost a CTA that streams about 2 us (@@).
+// Both merge in order: the same lengths give the same bits.
+//
+// Also built and measured for large calls (64 sequences, 8 key heads, 4100
+// visible keys each, 1.07 GB; pure streaming by the same copies 153 us): equal
+// contiguous shares of all tiles per warp, 173 us, or per CTA, 166 us (SMs
+// stream at rates up to 10 % apart, which equal shares wait for), and per-warp
+// shares with smaller units taken later from a queue, 188 us (a warp holds an
+// eighth of an SM's bandwidth, so even a unit of six tiles takes 10 us).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "cache_common.cuh"
+#include "tc_common.cuh"
 
 namespace rf {
 namespace {
 
 constexpr int HD = 128;                 // head dimension
 constexpr int ROW_BYTES = HD * 2;
-constexpr int TK = 16;                  // keys per warp tile
+constexpr int TK = kDecodeTile;         // keys per warp tile
+static_assert(TK == 16, "two n8 tiles of scores, one k16 step of weights");
 constexpr int WARPS = 4;
 constexpr int STAGES = 3;
 constexpr int STAGE_BYTES = 2 * TK * ROW_BYTES;   // K tile, V tile
-constexpr int MROWS = 16;               // query heads per CTA
-constexpr size_t SMEM_BYTES = (size_t)WARPS * STAGES * STAGE_BYTES;
-static_assert(STAGE_BYTES >= MROWS * HD * 4, "a warp's state reuses its first stage");
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int MROWS = 16;               // query heads per row group
+constexpr size_t SMEM_BYTES = (size_t)WARPS * RING_BYTES;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -102,311 +114,448 @@ __device__ __forceinline__ void split16(float p0, float p1, uint32_t& hi, uint32
   }
 }
 
-__device__ __forceinline__ void store_out(void* out, size_t i, float x, int dtype) {
+// elements i and i + 1 (i even) of the output
+__device__ __forceinline__ void store_out2(void* out, size_t i, float x, float y, int dtype) {
   if (dtype == RF_F32)
-    static_cast<float*>(out)[i] = x;
-  else if (dtype == RF_F16)
-    static_cast<__half*>(out)[i] = __float2half_rn(x);
+    *reinterpret_cast<float2*>(static_cast<float*>(out) + i) = make_float2(x, y);
   else
-    static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + i) =
+        dtype == RF_F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
 }
 
 // acc / l, and 0 where the row has no weight at all (no visible key); a NaN
 // sum stays NaN
 __device__ __forceinline__ float normalised(float acc, float l) { return l == 0.f ? 0.f : acc / l; }
 
-template <bool F16, bool SCORES>
-__global__ void __launch_bounds__(WARPS * 32)
-cache_decode_kernel(const CacheDecode a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sm_m[WARPS][MROWS], sm_l[WARPS][MROWS];
-  __shared__ int last;
+// A row group's keys: the visible ones of its sequence.
+struct Group {
+  int n, lo, ns;         // visible keys; key t is cache row t (t < ns) or t - ns + lo
+  size_t kv0;            // first cache row of its key head
+};
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mt = blockIdx.x % a.mtiles;
-  const int seg = (int)(blockIdx.x / a.mtiles) % a.S;
-  const int group = (int)(blockIdx.x / a.mtiles) / a.S;            // b * Hkv + key head
-  const int b = group / a.Hkv, hk = group - b * a.Hkv;
-  const int rows = min(MROWS, a.G - mt * MROWS);
-  const size_t row0 = (size_t)b * a.H + (size_t)hk * a.G + mt * MROWS;   // first query row
-
-  // visible keys: t < ns are the sinks, the rest the last keys of the sequence
+__device__ __forceinline__ int visible_keys(const CacheDecode& a, int b, int& lo, int& ns) {
   int len = a.cap;
-  if (a.lens != nullptr && RF_IDX_OK(b, a.B)) len = min(max(a.lens[b], 0), a.cap);
-  const int lo = a.window > 0 ? max(0, len - a.window) : 0;
-  const int ns = min(a.sinks, lo);
-  const int n = ns + len - lo;
-  const int chunk = segment_keys(n, a.S);
-  const int t_begin = min(n, seg * chunk), t_end = min(n, t_begin + chunk);
-  const int tiles = (t_end - t_begin + TK - 1) / TK;
+  if (a.lens != nullptr && RF_IDX_OK(b, a.B)) len = min(max(__ldg(a.lens + b), 0), a.cap);
+  lo = a.window > 0 ? max(0, len - a.window) : 0;
+  ns = min(a.sinks, lo);
+  return ns + len - lo;
+}
 
-  // Q fragments: rows lane / 4 and + 8, columns 16 kk + 2 (lane % 4) (+ 8)
+// tiles of n keys; at least one, so that a group without keys has an owner
+__device__ __forceinline__ int tiles_of(int n) { return n > TK ? (n + TK - 1) / TK : 1; }
+
+// group g = (b Hkv + key head) mtiles + tile of query heads
+__device__ __forceinline__ Group group_of(const CacheDecode& a, int g) {
+  Group r;
+  const int head = g / a.mtiles;
+  r.n = visible_keys(a, head / a.Hkv, r.lo, r.ns);
+  r.kv0 = (size_t)head * a.cap;
+  return r;
+}
+
+struct Rows {
+  size_t row0;           // first query row
+  int n;                 // 1 .. 16
+};
+__device__ __forceinline__ Rows rows_of(const CacheDecode& a, int g) {
+  const int head = g / a.mtiles, mt = g - head * a.mtiles;
+  const int b = head / a.Hkv, hk = head - b * a.Hkv;
+  return {(size_t)b * a.H + (size_t)hk * a.G + mt * MROWS, min(MROWS, a.G - mt * MROWS)};
+}
+
+// The warp's copies of keys t0 .. t0 + 15 of a group into one stage: K rows,
+// then V rows, 16-byte chunks permuted by row % 8 so that ldmatrix meets all
+// banks; two rows per instruction.
+__device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, int t0, uint32_t stage,
+                                          int lane) {
+#pragma unroll
+  for (int u = 0; u < TK / 2; ++u) {
+    const int r = 2 * u + (lane >> 4), c = lane & 15;
+    const int t = t0 + r;
+    const int key = t < q.ns ? t : t - q.ns + q.lo;
+    const bool in = t < q.n && RF_IDX_OK(q.kv0 + key, (size_t)a.B * a.Hkv * a.cap);
+    const size_t off = (q.kv0 + (in ? key : 0)) * ROW_BYTES + c * 16;
+    const uint32_t dst = stage + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
+    cp_async16(dst, a.k + off, in ? 16u : 0u);
+    cp_async16(dst + TK * ROW_BYTES, a.v + off, in ? 16u : 0u);
+  }
+}
+
+// One warp's running state of a row group: rows lane / 4 (index 0) and + 8
+// (index 1); acc[d] holds columns 8 d + 2 (lane % 4) and + 1 of both.
+template <bool F16, bool SCORES>
+struct State {
   uint32_t qf[HD / 16][4];
-  {
+  float acc[HD / 8][4];
+  float m0, m1, l0, l1;
+
+  __device__ __forceinline__ void start(const CacheDecode& a, const Rows& w, int lane) {
+    // Q fragments: columns 16 kk + 2 (lane % 4) (+ 8) of the two rows
     const int r = lane >> 2;
-    const bool in0 = r < rows, in1 = r + 8 < rows;
-    const uint8_t* q0 = a.q + (row0 + r) * ROW_BYTES + (lane & 3) * 4;
+    const bool in0 = r < w.n && RF_IDX_OK(w.row0 + r, (size_t)a.B * a.H);
+    const bool in1 = r + 8 < w.n && RF_IDX_OK(w.row0 + r + 8, (size_t)a.B * a.H);
+    const uint8_t* q0 = a.q + (w.row0 + r) * ROW_BYTES + (lane & 3) * 4;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
-      const bool ok0 = in0 && RF_SPAN_OK((row0 + r) * ROW_BYTES + kk * 32, 32, (size_t)a.B * a.H * ROW_BYTES);
-      const bool ok1 = in1 && RF_SPAN_OK((row0 + r + 8) * ROW_BYTES + kk * 32, 32, (size_t)a.B * a.H * ROW_BYTES);
-      qf[kk][0] = ok0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32) : 0u;
-      qf[kk][1] = ok1 ? *reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32) : 0u;
-      qf[kk][2] = ok0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16) : 0u;
-      qf[kk][3] = ok1 ? *reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32 + 16) : 0u;
+      qf[kk][0] = in0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 32)) : 0u;
+      qf[kk][1] = in1 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32)) : 0u;
+      qf[kk][2] = in0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16)) : 0u;
+      qf[kk][3] = in1 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32 + 16)) : 0u;
     }
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
   }
 
-  uint8_t* ring = smem + warp * STAGES * STAGE_BYTES;
-  const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  const size_t kv0 = (size_t)group * a.cap;                        // first cache row of the group
-
-  // tile i of this warp: keys t_begin + (i WARPS + warp) TK ..
-  auto issue = [&](int i) {
-    const int t0 = t_begin + (i * WARPS + warp) * TK;
-    if (t0 < t_end) {
-      const uint32_t st = ring32 + (uint32_t)(i % STAGES) * STAGE_BYTES;
-#pragma unroll
-      for (int u = 0; u < TK / 2; ++u) {
-        const int r = 2 * u + (lane >> 4), c = lane & 15;
-        const int t = t0 + r;
-        const int key = t < ns ? t : t - ns + lo;
-        const bool in = t < t_end && RF_IDX_OK(kv0 + key, (size_t)a.B * a.Hkv * a.cap);
-        const size_t off = (kv0 + (in ? key : 0)) * ROW_BYTES + c * 16;
-        const uint32_t dst = st + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
-        cp_async16(dst, a.k + off, in ? 16u : 0u);
-        cp_async16(dst + TK * ROW_BYTES, a.v + off, in ? 16u : 0u);
-      }
-    }
-    cp_async_commit();
-  };
-
-  float acc[HD / 8][4];
-#pragma unroll
-  for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-#pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) issue(i);
-  for (int i = 0; i * WARPS + warp < tiles; ++i) {
-    cp_async_wait<STAGES - 2>();
-    __syncwarp();                       // every lane's copies of tile i landed, tile i - 1 is read
-    issue(i + STAGES - 1);
-    const uint32_t st = ring32 + (uint32_t)(i % STAGES) * STAGE_BYTES;
-    const int t0 = t_begin + (i * WARPS + warp) * TK;
-
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    {
-      const int r = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk) {
-        const int c = 2 * kk + ((lane >> 3) & 1);
-        uint32_t kb[4];
-        ldmatrix_x4(st + r * ROW_BYTES + ((c ^ (r & 7)) << 4), kb);
-        mma16816<F16>(s[0], qf[kk], kb[0], kb[1]);
-        mma16816<F16>(s[1], qf[kk], kb[2], kb[3]);
-      }
-    }
-    float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = t0 + nt * 8 + 2 * (lane & 3) + e;
-        const bool in = t < t_end;
-        s[nt][e] = in ? s[nt][e] * a.scale_log2 : -INFINITY;
-        s[nt][2 + e] = in ? s[nt][2 + e] * a.scale_log2 : -INFINITY;
-        mx0 = fmaxf(mx0, s[nt][e]);
-        mx1 = fmaxf(mx1, s[nt][2 + e]);
-        if constexpr (SCORES) {
-          const int r = lane >> 2;
-          if (in && r < rows && RF_IDX_OK((row0 + r) * a.cap + t, (size_t)a.B * a.H * a.cap))
-            a.scores[(row0 + r) * a.cap + t] = s[nt][e];
-          if (in && r + 8 < rows && RF_IDX_OK((row0 + r + 8) * a.cap + t, (size_t)a.B * a.H * a.cap))
-            a.scores[(row0 + r + 8) * a.cap + t] = s[nt][2 + e];
-        }
-      }
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    const bool grew = mx0 > m0 || mx1 > m1;
-    if (__any_sync(0xffffffffu, grew)) {
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      const float c0 = exp2f(m0 - ref_of(n0)), c1 = exp2f(m1 - ref_of(n1));
-      m0 = n0;
-      m1 = n1;
-      l0 *= c0;
-      l1 *= c1;
-#pragma unroll
-      for (int d = 0; d < HD / 8; ++d) {
-        acc[d][0] *= c0;
-        acc[d][1] *= c0;
-        acc[d][2] *= c1;
-        acc[d][3] *= c1;
-      }
-    }
-    const float f0 = ref_of(m0), f1 = ref_of(m1);
-    uint32_t hi[4], lw[4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const float p00 = exp2f(s[nt][0] - f0), p01 = exp2f(s[nt][1] - f0);
-      const float p10 = exp2f(s[nt][2] - f1), p11 = exp2f(s[nt][3] - f1);
-      l0 += p00 + p01;
-      l1 += p10 + p11;
-      split16<F16>(p00, p01, hi[2 * nt], lw[2 * nt]);
-      split16<F16>(p10, p11, hi[2 * nt + 1], lw[2 * nt + 1]);
-    }
-    {
-      const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
-#pragma unroll
-      for (int d = 0; d < HD / 16; ++d) {
-        const int c = 2 * d + (lane >> 4);
-        uint32_t vb[4];
-        ldmatrix_x4_trans(st + TK * ROW_BYTES + r * ROW_BYTES + ((c ^ (r & 7)) << 4), vb);
-        mma16816<F16>(acc[2 * d], hi, vb[0], vb[1]);
-        mma16816<F16>(acc[2 * d + 1], hi, vb[2], vb[3]);
-        mma16816<F16>(acc[2 * d], lw, vb[0], vb[1]);
-        mma16816<F16>(acc[2 * d + 1], lw, vb[2], vb[3]);
-      }
-    }
-  }
-  cp_async_wait<0>();
-  __syncwarp();
-
-  // warp states into shared memory (the warp's own first stage)
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  // folds in keys t0 .. min(t0 + 15, n - 1), whose copies are in `st`
+  __device__ __forceinline__ void tile(const CacheDecode& a, const Rows& w, uint32_t st, int t0, int n,
+                                       int lane) {
+  float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   {
-    const int r = lane >> 2;
-    float* st = reinterpret_cast<float*>(ring);
+    const int r = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const int c = 2 * kk + ((lane >> 3) & 1);
+      uint32_t kb[4];
+      ldmatrix_x4(st + r * ROW_BYTES + ((c ^ (r & 7)) << 4), kb);
+      mma16816<F16>(s[0], qf[kk], kb[0], kb[1]);
+      mma16816<F16>(s[1], qf[kk], kb[2], kb[3]);
+    }
+  }
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = t0 + nt * 8 + 2 * (lane & 3) + e;
+      const bool in = t < n;
+      s[nt][e] = in ? s[nt][e] * a.scale_log2 : -INFINITY;
+      s[nt][2 + e] = in ? s[nt][2 + e] * a.scale_log2 : -INFINITY;
+      mx0 = fmaxf(mx0, s[nt][e]);
+      mx1 = fmaxf(mx1, s[nt][2 + e]);
+      if constexpr (SCORES) {
+        const int r = lane >> 2;
+        if (in && r < w.n && RF_IDX_OK((w.row0 + r) * a.cap + t, (size_t)a.B * a.H * a.cap))
+          a.scores[(w.row0 + r) * a.cap + t] = s[nt][e];
+        if (in && r + 8 < w.n && RF_IDX_OK((w.row0 + r + 8) * a.cap + t, (size_t)a.B * a.H * a.cap))
+          a.scores[(w.row0 + r + 8) * a.cap + t] = s[nt][2 + e];
+      }
+    }
+  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+  const bool grew = mx0 > m0 || mx1 > m1;
+  if (__any_sync(0xffffffffu, grew)) {
+    const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+    const float c0 = exp2f(m0 - ref_of(n0)), c1 = exp2f(m1 - ref_of(n1));
+    m0 = n0;
+    m1 = n1;
+    l0 *= c0;
+    l1 *= c1;
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d) {
-      const int col = d * 8 + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(st + r * HD + col) = make_float2(acc[d][0], acc[d][1]);
-      *reinterpret_cast<float2*>(st + (r + 8) * HD + col) = make_float2(acc[d][2], acc[d][3]);
-    }
-    if ((lane & 3) == 0) {
-      sm_m[warp][r] = m0;
-      sm_m[warp][r + 8] = m1;
-      sm_l[warp][r] = l0;
-      sm_l[warp][r + 8] = l1;
+      acc[d][0] *= c0;
+      acc[d][1] *= c0;
+      acc[d][2] *= c1;
+      acc[d][3] *= c1;
     }
   }
-  __syncthreads();
-  const bool direct = a.S_total == 1;             // the only segment: the output itself
+  const float f0 = ref_of(m0), f1 = ref_of(m1);
+  uint32_t hi[4], lw[4];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    const float p00 = exp2f(s[nt][0] - f0), p01 = exp2f(s[nt][1] - f0);
+    const float p10 = exp2f(s[nt][2] - f1), p11 = exp2f(s[nt][3] - f1);
+    l0 += p00 + p01;
+    l1 += p10 + p11;
+    split16<F16>(p00, p01, hi[2 * nt], lw[2 * nt]);
+    split16<F16>(p10, p11, hi[2 * nt + 1], lw[2 * nt + 1]);
+  }
+  {
+    const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) {
+      const int c = 2 * d + (lane >> 4);
+      uint32_t vb[4];
+      ldmatrix_x4_trans(st + TK * ROW_BYTES + r * ROW_BYTES + ((c ^ (r & 7)) << 4), vb);
+      mma16816<F16>(acc[2 * d], hi, vb[0], vb[1]);
+      mma16816<F16>(acc[2 * d + 1], hi, vb[2], vb[3]);
+      mma16816<F16>(acc[2 * d], lw, vb[0], vb[1]);
+      mma16816<F16>(acc[2 * d + 1], lw, vb[2], vb[3]);
+    }
+  }
+  }
+
+  // the row sums over the four lanes that share a row; once, before the state is used
+  __device__ __forceinline__ void close() {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  }
+
+  // the warp's rows into out and lse (`direct`: this was the whole group) or
+  // into state slot `slot` of each row
+  __device__ __forceinline__ void write(const CacheDecode& a, const Rows& w, bool direct, int slot,
+                                        int lane) const {
+    const size_t states = (size_t)a.B * a.H * a.S_total;
+    (void)states;                                 // read by the checked build only
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = (lane >> 2) + 8 * half;
+      const size_t row = w.row0 + r;
+      if (r >= w.n || !RF_IDX_OK(row, (size_t)a.B * a.H)) continue;
+      const float m = half ? m1 : m0, l = half ? l1 : l0;
+      if (direct) {
+#pragma unroll
+        for (int d = 0; d < HD / 8; ++d)
+          store_out2(a.out, row * HD + d * 8 + 2 * (lane & 3), normalised(acc[d][2 * half], l),
+                     normalised(acc[d][2 * half + 1], l), a.out_dtype);
+        if ((lane & 3) == 0) {
+          const float lse2 = m + log2f(l);
+          if (a.lse != nullptr) a.lse[row] = lse2 * kLn2;
+          if (SCORES && RF_IDX_OK(row * a.S_total, states)) a.seg_m[row * a.S_total] = lse2;
+        }
+      } else {
+        const size_t s = row * a.S_total + slot;
+        if (!RF_IDX_OK(s, states)) continue;
+#pragma unroll
+        for (int d = 0; d < HD / 8; ++d)
+          *reinterpret_cast<float2*>(a.seg_acc + s * HD + d * 8 + 2 * (lane & 3)) =
+              make_float2(acc[d][2 * half], acc[d][2 * half + 1]);
+        if ((lane & 3) == 0) {
+          a.seg_m[s] = m;
+          a.seg_l[s] = l;
+        }
+      }
+    }
+  }
+};
+
+// Merges a group's rows, their states in order: the prefix's slots
+// 0 .. seg0 - 1 and this kernel's seg0 .. seg0 + pieces - 1.  One warp, four
+// columns per lane; RB rows and 32 / RB states are in flight at a time.
+template <int RB, bool SCORES>
+__device__ void merge_rows(const CacheDecode& a, size_t row0, int rows, int pieces, int lane) {
   const size_t states = (size_t)a.B * a.H * a.S_total;
   (void)states;                                   // read by the checked build only
-  for (int r = 0; r < rows; ++r) {
-    const int d = threadIdx.x;                    // WARPS * 32 == HD
-    float M = -INFINITY;
+  constexpr int SB = 32 / RB;                     // states in flight: 32 loads per lane
+  const int n = a.seg0 + pieces;
+  for (int r0 = 0; r0 < rows; r0 += RB) {
+    const int nr = min(RB, rows - r0);
+    float M[RB], L[RB];
+    float4 A[RB];
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm_m[w][r]);
-    const float ref = ref_of(M);
-    float A = 0.f, L = 0.f;
+    for (int r = 0; r < RB; ++r) {
+      M[r] = -INFINITY;
+      L[r] = 0.f;
+      A[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int s = lane; s < n; s += 32)
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = exp2f(sm_m[w][r] - ref);
-      A = fmaf(f, reinterpret_cast<const float*>(smem + (size_t)w * STAGES * STAGE_BYTES)[r * HD + d], A);
-      L = fmaf(f, sm_l[w][r], L);
-    }
-    const size_t row = row0 + r;
-    const size_t slot = row * a.S_total + a.seg0 + seg;
-    if (direct) {
-      if (RF_IDX_OK(row * HD + d, (size_t)a.B * a.H * HD))
-        store_out(a.out, row * HD + d, normalised(A, L), a.out_dtype);
-      if (d == 0) {
-        const float lse2 = M + log2f(L);
-        if (a.lse != nullptr && RF_IDX_OK(row, (size_t)a.B * a.H)) a.lse[row] = lse2 * kLn2;
-        if (SCORES && RF_IDX_OK(slot, states)) a.seg_m[slot] = lse2;
+      for (int r = 0; r < RB; ++r) {
+        const size_t at = (row0 + r0 + r) * a.S_total + s;
+        if (r < nr && RF_IDX_OK(at, states)) M[r] = fmaxf(M[r], __ldcg(a.seg_m + at));
       }
-    } else {
-      // a segment without keys leaves its accumulator unwritten: nobody reads it
-      if (t_begin < t_end && RF_IDX_OK(slot * HD + d, states * HD)) a.seg_acc[slot * HD + d] = A;
-      if (d == 0 && RF_IDX_OK(slot, states)) {
-        a.seg_m[slot] = M;
-        a.seg_l[slot] = L;
-      }
-    }
-  }
-  if (direct) return;
-
-  // the last segment to arrive merges the rows
-  __threadfence();
-  __syncthreads();
-  const int counter = group * a.mtiles + mt;
-  if (threadIdx.x == 0) {
-    const int seen = RF_IDX_OK(counter, (size_t)a.B * a.Hkv * a.mtiles)
-                         ? atomicAdd(a.counters + counter, 1) : -1;
-    last = seen == a.S - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  for (int r = warp; r < rows; r += WARPS) {
-    const size_t row = row0 + r;
-    const float* sm = a.seg_m + row * a.S_total;
-    const float* sl = a.seg_l + row * a.S_total;
-    const float4* sa = reinterpret_cast<const float4*>(a.seg_acc + row * a.S_total * HD) + lane;
-    float M = -INFINITY;
-    for (int s = lane; s < a.S_total; s += 32)
-      if (RF_IDX_OK(row * a.S_total + s, states)) M = fmaxf(M, __ldcg(sm + s));
-    M = group_max<32>(M);
-    const float ref = ref_of(M);
-    float L = 0.f;
-    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < a.S_total; s0 += 32) {
-      // lane j holds segment s0 + j's weight; -1 marks one without keys
-      float f = -1.f;
-      const int s = s0 + lane;
-      if (s < a.S_total && RF_IDX_OK(row * a.S_total + s, states)) {
-        const float ms = __ldcg(sm + s);
-        if (ms != -INFINITY) {
-          f = exp2f(ms - ref);
-          L = fmaf(f, __ldcg(sl + s), L);
-        } else {
-          L += __ldcg(sl + s);                    // 0, or NaN where every score was NaN
+#pragma unroll
+    for (int r = 0; r < RB; ++r) M[r] = group_max<32>(M[r]);
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      // lane j holds state s0 + j's weight; -1 marks one without keys
+      float f[RB];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        f[r] = -1.f;
+        const size_t at = (row0 + r0 + r) * a.S_total + s0 + lane;
+        if (r < nr && s0 + lane < n && RF_IDX_OK(at, states)) {
+          const float ms = __ldcg(a.seg_m + at), ls = __ldcg(a.seg_l + at);
+          if (ms != -INFINITY) {
+            f[r] = exp2f(ms - ref_of(M[r]));
+            L[r] = fmaf(f[r], ls, L[r]);
+          } else {
+            L[r] += ls;                           // 0, or NaN where every score was NaN
+          }
         }
       }
-      const int cnt = min(32, a.S_total - s0);
-#pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
-        const float fj = __shfl_sync(0xffffffffu, f, j);
-        if (fj != -1.f && RF_SPAN_OK(((row * a.S_total + s0 + j) * HD + lane * 4), 4, states * HD)) {
-          const float4 x = __ldcg(sa + (size_t)(s0 + j) * (HD / 4));
-          A.x = fmaf(fj, x.x, A.x);
-          A.y = fmaf(fj, x.y, A.y);
-          A.z = fmaf(fj, x.z, A.z);
-          A.w = fmaf(fj, x.w, A.w);
-        }
+      const int cnt = min(32, n - s0);
+      for (int j0 = 0; j0 < cnt; j0 += SB) {
+        float4 v[RB][SB];
+        float fj[RB][SB];
+#pragma unroll
+        for (int j = 0; j < SB; ++j)
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            fj[r][j] = __shfl_sync(0xffffffffu, f[r], (j0 + j) & 31);
+            if (j0 + j >= cnt) fj[r][j] = -1.f;
+            const size_t at = (row0 + r0 + r) * a.S_total + s0 + j0 + j;
+            v[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (fj[r][j] != -1.f && RF_SPAN_OK(at * HD + lane * 4, 4, states * HD))
+              v[r][j] = __ldcg(reinterpret_cast<const float4*>(a.seg_acc + at * HD) + lane);
+          }
+#pragma unroll
+        for (int j = 0; j < SB; ++j)
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            if (fj[r][j] == -1.f) continue;
+            A[r].x = fmaf(fj[r][j], v[r][j].x, A[r].x);
+            A[r].y = fmaf(fj[r][j], v[r][j].y, A[r].y);
+            A[r].z = fmaf(fj[r][j], v[r][j].z, A[r].z);
+            A[r].w = fmaf(fj[r][j], v[r][j].w, A[r].w);
+          }
       }
     }
-    L = group_sum<32>(L);
-    if (RF_SPAN_OK(row * HD + lane * 4, 4, (size_t)a.B * a.H * HD)) {
+    __syncwarp();                                 // every lane has read the rows' seg_m
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      L[r] = group_sum<32>(L[r]);
+      const size_t row = row0 + r0 + r;
+      if (r >= nr || !RF_IDX_OK(row, (size_t)a.B * a.H)) continue;
       const size_t o = row * HD + lane * 4;
-      store_out(a.out, o, normalised(A.x, L), a.out_dtype);
-      store_out(a.out, o + 1, normalised(A.y, L), a.out_dtype);
-      store_out(a.out, o + 2, normalised(A.z, L), a.out_dtype);
-      store_out(a.out, o + 3, normalised(A.w, L), a.out_dtype);
-    }
-    __syncwarp();                                 // every lane has read the states
-    if (lane == 0) {
-      const float lse2 = M + log2f(L);
-      if (a.lse != nullptr && RF_IDX_OK(row, (size_t)a.B * a.H)) a.lse[row] = lse2 * kLn2;
-      if (SCORES && RF_IDX_OK(row * a.S_total, states)) a.seg_m[row * a.S_total] = lse2;
+      store_out2(a.out, o, normalised(A[r].x, L[r]), normalised(A[r].y, L[r]), a.out_dtype);
+      store_out2(a.out, o + 2, normalised(A[r].z, L[r]), normalised(A[r].w, L[r]), a.out_dtype);
+      if (lane == 0) {
+        const float lse2 = M[r] + log2f(L[r]);
+        if (a.lse != nullptr) a.lse[row] = lse2 * kLn2;
+        if (SCORES && RF_IDX_OK(row * a.S_total, states)) a.seg_m[row * a.S_total] = lse2;
+      }
     }
   }
-  if (threadIdx.x == 0 && RF_IDX_OK(counter, (size_t)a.B * a.Hkv * a.mtiles)) a.counters[counter] = 0;
+}
+
+// Pieces of a group of n keys: none below piece_keys, at most S.
+__device__ __forceinline__ int pieces_of(const CacheDecode& a, int n) {
+  return max(1, min(a.S, (n + a.piece_keys - 1) / a.piece_keys));
+}
+
+constexpr size_t MERGE_BYTES = (size_t)2 * MROWS * HD * 4;
+static_assert(MERGE_BYTES <= SMEM_BYTES, "two warps' accumulators reuse the rings");
+
+// One CTA per (group, piece); pieces that a group does not have return at once.
+template <bool F16, bool SCORES, bool FUSED>
+__global__ void __launch_bounds__(WARPS * 32, 2)
+cache_decode_kernel(const CacheDecode a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float4 sm_ml[2][8];
+  __shared__ int last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = (int)(blockIdx.x / a.S), piece = (int)(blockIdx.x - (unsigned)g * a.S);
+  allow_dependents();
+  const Group q = group_of(a, g);
+  const int pieces = pieces_of(a, q.n);
+  if (piece >= pieces) {
+    wait_prerequisite();                // done means the prefix is done too
+    return;
+  }
+  const Rows w = rows_of(a, g);
+  const int steps = (tiles_of(q.n) + WARPS - 1) / WARPS;
+  const int k0 = (int)((long long)steps * piece / pieces);
+  const int k1 = (int)((long long)steps * (piece + 1) / pieces);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * RING_BYTES;
+
+  int in = 0;                           // the stage that the next copies go to
+  auto issue = [&](int k) {
+    const int t0 = (k * WARPS + warp) * TK;
+    if (k < k1 && t0 < q.n) copy_tile(a, q, t0, ring + (uint32_t)in * STAGE_BYTES, lane);
+    cp_async_commit();
+    in = in + 1 == STAGES ? 0 : in + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) issue(k0 + i);
+  State<F16, SCORES> st;
+  st.start(a, w, lane);
+  int slot = 0;
+  for (int k = k0; k < k1; ++k) {
+    cp_async_wait<STAGES - 2>();
+    __syncwarp();                       // every lane's copies of this step landed, the last is read
+    issue(k + STAGES - 1);
+    const int t0 = (k * WARPS + warp) * TK;
+    if (t0 < q.n) st.tile(a, w, ring + (uint32_t)slot * STAGE_BYTES, t0, q.n, lane);
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+  }
+  cp_async_wait<0>();
+  st.close();
+  __syncthreads();                      // the rings are free
+
+  // warps 2, 3 into 0, 1, then 1 into 0, fragment by fragment (every warp
+  // holds the same elements in the same lanes)
+  float4* mbuf = reinterpret_cast<float4*>(smem);
+  auto give = [&](int i) {
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d)
+      mbuf[(i * (HD / 8) + d) * 32 + lane] =
+          make_float4(st.acc[d][0], st.acc[d][1], st.acc[d][2], st.acc[d][3]);
+    if ((lane & 3) == 0) sm_ml[i][lane >> 2] = make_float4(st.m0, st.m1, st.l0, st.l1);
+  };
+  auto take = [&](int i) {
+    const float4 o = sm_ml[i][lane >> 2];
+    const float n0 = fmaxf(st.m0, o.x), n1 = fmaxf(st.m1, o.y);
+    const float c0 = exp2f(st.m0 - ref_of(n0)), c1 = exp2f(st.m1 - ref_of(n1));
+    const float f0 = exp2f(o.x - ref_of(n0)), f1 = exp2f(o.y - ref_of(n1));
+    st.m0 = n0;
+    st.m1 = n1;
+    st.l0 = fmaf(o.z, f0, st.l0 * c0);
+    st.l1 = fmaf(o.w, f1, st.l1 * c1);
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d) {
+      const float4 v = mbuf[(i * (HD / 8) + d) * 32 + lane];
+      st.acc[d][0] = fmaf(v.x, f0, st.acc[d][0] * c0);
+      st.acc[d][1] = fmaf(v.y, f0, st.acc[d][1] * c0);
+      st.acc[d][2] = fmaf(v.z, f1, st.acc[d][2] * c1);
+      st.acc[d][3] = fmaf(v.w, f1, st.acc[d][3] * c1);
+    }
+  };
+  if (warp >= 2) give(warp - 2);
+  __syncthreads();
+  if (warp < 2) take(warp);
+  __syncthreads();
+  if (warp == 1) give(0);
+  __syncthreads();
+  const bool direct = pieces == 1 && a.seg0 == 0;   // the output itself
+  if (warp == 0) {
+    take(0);
+    st.write(a, w, direct, a.seg0 + piece, lane);
+  }
+  wait_prerequisite();                  // the prefix's states, where there are some
+  if constexpr (FUSED) {
+    if (direct) return;
+    // the last piece to arrive merges the group's rows, a row per warp at a time
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int seen = 0;
+      if (pieces > 1)
+        seen = RF_IDX_OK(g, (size_t)a.B * a.Hkv * a.mtiles) ? atomicAdd(a.counters + g, 1) : -1;
+      last = seen == pieces - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    for (int r = warp; r < w.n; r += WARPS) merge_rows<1, SCORES>(a, w.row0 + r, 1, pieces, lane);
+    if (threadIdx.x == 0 && pieces > 1 && RF_IDX_OK(g, (size_t)a.B * a.Hkv * a.mtiles))
+      a.counters[g] = 0;
+  }
+}
+
+// One warp per group: merges the rows of divided groups.
+template <bool SCORES>
+__global__ void __launch_bounds__(WARPS * 32)
+merge_kernel(const CacheDecode a) {
+  const int g = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  allow_dependents();
+  const int pieces = g < a.B * a.Hkv * a.mtiles ? pieces_of(a, group_of(a, g).n) : 1;
+  wait_prerequisite();
+  if (g >= a.B * a.Hkv * a.mtiles) return;
+  if (pieces == 1 && a.seg0 == 0) return;        // written by its CTA
+  const Rows w = rows_of(a, g);
+  merge_rows<4, SCORES>(a, w.row0, w.n, pieces, lane);
 }
 
 // total[j] = weight[j] + sum over the group's heads of exp2(score - lse2):
 // the weights of the row's softmax, each below 1, summed in fp32 head by head
 // in order.  One thread per key; reads 4 (G + 1) bytes and writes 4 per key.
 __global__ void __launch_bounds__(256)
-add_weights_kernel(const float* __restrict__ scores, const float* __restrict__ seg_m,
-                   const int32_t* __restrict__ lens, const float* weight, float* total, int B,
+add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __restrict__ lens, const float* weight, float* total, int B,
                    int Hkv, int G, int cap, int S, int blocks) {
   const int group = blockIdx.x / blocks;
   const int j = (blockIdx.x - group * blocks) * 256 + threadIdx.x;
@@ -414,6 +563,7 @@ add_weights_kernel(const float* __restrict__ scores, const float* __restrict__ s
   const size_t row0 = (size_t)group * G;                          // b * H + key head * G
   int len = cap;
   if (lens != nullptr && RF_IDX_OK(b, B)) len = min(max(lens[b], 0), cap);
+  wait_prerequisite();
   if (j >= cap) return;
   const size_t i = (size_t)group * cap + j;
   if (!RF_IDX_OK(i, (size_t)B * Hkv * cap)) return;
@@ -422,7 +572,7 @@ add_weights_kernel(const float* __restrict__ scores, const float* __restrict__ s
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
       if (!RF_IDX_OK((row0 + g) * cap + j, (size_t)B * Hkv * G * cap)) continue;
-      const float z = __ldg(seg_m + (row0 + g) * S);
+      const float z = __ldcg(seg_m + (row0 + g) * S);
       const float x = __ldcs(scores + (row0 + g) * cap + j);
       w += z == -INFINITY ? 0.f : exp2f(x - z);   // a row without weight adds none
     }
@@ -433,11 +583,21 @@ add_weights_kernel(const float* __restrict__ scores, const float* __restrict__ s
 }
 
 template <bool F16, bool SCORES>
-rf_status launch_t(const CacheDecode& a, unsigned grid, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  if (smem_attr(cache_decode_kernel<F16, SCORES>, SMEM_BYTES, done) != RF_OK) return RF_ERR_CUDA;
-  cache_decode_kernel<F16, SCORES><<<grid, WARPS * 32, SMEM_BYTES, st>>>(a);
-  return launch_status();
+rf_status launch_t(const CacheDecode& a, bool few, cudaStream_t st) {
+  static std::atomic<uint64_t> done_few{0}, done_many{0};
+  const unsigned groups = (unsigned)(a.B * a.Hkv * a.mtiles);
+  auto* kernel = few ? cache_decode_kernel<F16, SCORES, true> : cache_decode_kernel<F16, SCORES, false>;
+  if (smem_attr(kernel, SMEM_BYTES, few ? done_few : done_many) != RF_OK) return RF_ERR_CUDA;
+  rf_status s;
+  if (a.seg0 > 0) {
+    // beside the end of the prefix kernel
+    s = launch_after(kernel, groups * a.S, WARPS * 32, SMEM_BYTES, st, a);
+  } else {
+    kernel<<<groups * a.S, WARPS * 32, SMEM_BYTES, st>>>(a);
+    s = launch_status();
+  }
+  if (s != RF_OK || few || (a.S == 1 && a.seg0 == 0)) return s;
+  return launch_after(merge_kernel<SCORES>, (groups + WARPS - 1) / WARPS, WARPS * 32, 0, st, a);
 }
 
 }  // namespace
@@ -445,10 +605,17 @@ rf_status launch_t(const CacheDecode& a, unsigned grid, cudaStream_t st) {
 rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st) {
   a.G = a.H / a.Hkv;
   a.mtiles = (a.G + MROWS - 1) / MROWS;
-  const unsigned grid = (unsigned)((long long)a.B * a.Hkv * a.mtiles * a.S);
+  const int sms = tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  const int keys = a.window > 0 && a.window < a.cap - a.sinks ? a.window + a.sinks : a.cap;
+  const bool few = decode_is_few((long long)a.B * a.Hkv * a.mtiles, keys, sms);
+  a.piece_keys = few ? kFewKeys : kManyKeys;
+  // no more pieces than the longest possible row has
+  const int most = (keys + a.piece_keys - 1) / a.piece_keys;
+  if (a.S > most) a.S = most;
   if (dtype == RF_F16)
-    return a.scores ? launch_t<true, true>(a, grid, st) : launch_t<true, false>(a, grid, st);
-  return a.scores ? launch_t<false, true>(a, grid, st) : launch_t<false, false>(a, grid, st);
+    return a.scores ? launch_t<true, true>(a, few, st) : launch_t<true, false>(a, few, st);
+  return a.scores ? launch_t<false, true>(a, few, st) : launch_t<false, false>(a, few, st);
 }
 
 rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* total,
@@ -456,9 +623,8 @@ rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* t
   const int blocks = (a.cap + 255) / 256;
   const long long grid = (long long)a.B * a.Hkv * blocks;
   if (grid > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
-  add_weights_kernel<<<(unsigned)grid, 256, 0, st>>>(a.scores, a.seg_m, a.lens, weight, total, a.B,
-                                                     a.Hkv, a.H / a.Hkv, a.cap, a.S_total, blocks);
-  return launch_status();
+  return launch_after(add_weights_kernel, (unsigned)grid, 256, 0, st, a.scores, a.seg_m, a.lens, weight,
+                      total, a.B, a.Hkv, a.H / a.Hkv, a.cap, a.S_total, blocks);
 }
 
 RF_BOUNDS_WORD_OF_THIS_FILE

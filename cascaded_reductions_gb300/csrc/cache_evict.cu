@@ -49,6 +49,7 @@ evict_select_kernel(const Evict a) {
   __shared__ uint32_t sh_prefix, sh_need;
   __shared__ int above[SEL_WARPS], equal[SEL_WARPS];
 
+  allow_dependents();
   const int group = blockIdx.x;
   const int b = group / a.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -183,7 +184,7 @@ constexpr int COPY_UNROLL = 8;
 // COPY_THREADS * COPY_UNROLL consecutive units of one (sequence, key head).
 __global__ void __launch_bounds__(COPY_THREADS)
 evict_copy_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                  const float* __restrict__ weight, const int32_t* __restrict__ kept, int groups,
+                  const float* __restrict__ weight, const int32_t* kept, int groups,
                   int cap, uint32_t chunks, int keep, int cap_out, int blocks, uint4* __restrict__ k_out,
                   uint4* __restrict__ v_out, float* __restrict__ weight_out) {
   const int part = blockIdx.x % 2;                 // 0: K and the weights, 1: V
@@ -191,6 +192,7 @@ evict_copy_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
   const int group = (int)(blockIdx.x / 2) / blocks;
   const uint4* src = part ? v : k;
   uint4* dst = part ? v_out : k_out;
+  wait_prerequisite();                             // the kept rows' indices
   if (src == nullptr) return;
   const uint32_t u0 = (uint32_t)block * (COPY_THREADS * COPY_UNROLL) + threadIdx.x;
   const uint32_t units = (uint32_t)keep * (uint32_t)chunks;      // below 2^31
@@ -205,7 +207,7 @@ evict_copy_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
     row[e] = -1;
     if (u < units) {
       const uint32_t i = u / chunks;
-      if (RF_IDX_OK((size_t)group * keep + i, slots)) row[e] = idx[i];
+      if (RF_IDX_OK((size_t)group * keep + i, slots)) row[e] = __ldcg(idx + i);
     }
   }
 #pragma unroll
@@ -247,11 +249,10 @@ rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
       Evict{weight, lens, B, Hkv, cap, keep, sinks, recent, lens_out, kept});
   const rf_status s = launch_status();
   if (s != RF_OK) return s;
-  evict_copy_kernel<<<(unsigned)(blocks * 2 * B * Hkv), COPY_THREADS, 0, st>>>(
-      static_cast<const uint4*>(k), static_cast<const uint4*>(v), weight, kept, B * Hkv, cap,
-      (uint32_t)chunks, keep, cap_out, (int)blocks, static_cast<uint4*>(k_out), static_cast<uint4*>(v_out),
-      weight_out);
-  return launch_status();
+  return launch_after(evict_copy_kernel, (unsigned)(blocks * 2 * B * Hkv), COPY_THREADS, 0, st,
+                      static_cast<const uint4*>(k), static_cast<const uint4*>(v), weight, kept,
+                      B * Hkv, cap, (uint32_t)chunks, keep, cap_out, (int)blocks,
+                      static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), weight_out);
 }
 
 RF_BOUNDS_WORD_OF_THIS_FILE

@@ -35,6 +35,7 @@ using pair::HD;
 template <bool F16_>
 struct WindowPrefill {
   static constexpr bool F16 = F16_;
+  static constexpr bool DEPENDENTS = false;
   static constexpr float M_START = -1e30f;
   struct Item {
     int bh, kvh;     // query head of the batch, key head of the batch

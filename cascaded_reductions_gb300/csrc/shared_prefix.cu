@@ -48,6 +48,7 @@ struct Split {
 template <bool F16_>
 struct PrefixStates {
   static constexpr bool F16 = F16_;
+  static constexpr bool DEPENDENTS = true;
   static constexpr float M_START = -1e30f;
   struct Item {
     int hk, seq0;            // key head; first sequence of the pair of tiles

@@ -338,8 +338,9 @@ rf_status rf_incremental_quant_fp8_gemm(const void* x, int M, int K, const uint8
  *     output).  counters: int32 [B * Hkv * ceil(G / 16)], all 0 before the
  *     first call; a call that completes leaves them 0.  Calls (or graph
  *     replays) that may overlap on the GPU need scratch and counters of their
- *     own.  Segments only divide the work: results do not depend on which CTA
- *     finishes first, and S is at most 4096 (rf_decode_segments proposes one).
+ *     own.  S is the most pieces that a row's keys may be divided into, at most
+ *     4096 (rf_decode_segments proposes one; 1 leaves every row whole): results
+ *     do not depend on which CTA finishes first.
  * Errors common to them: RF_ERR_INVALID_ARG for null pointers (but those that
  * may be NULL), sizes <= 0, H % Hkv != 0, window or sinks < 0, S < 1, a
  * non-finite scale or a bad dtype; RF_ERR_UNSUPPORTED for D != 128, RF_F32
@@ -348,9 +349,10 @@ rf_status rf_incremental_quant_fp8_gemm(const void* x, int M, int K, const uint8
  */
 
 /*
- * rf_decode_segments -- a number of segments that fills the current device
- * when `groups` rows of CTAs (B * Hkv * ceil(G / 16)) each read up to `keys`
- * visible keys: at least 1, at most 4096; 0 if the device cannot be queried.
+ * rf_decode_segments -- a number S of pieces per row for `groups` row groups
+ * (B * Hkv * ceil(G / 16)) of up to `keys` visible keys each that lets the
+ * current device be filled: at least 1, at most 4096; 0 if the device cannot
+ * be queried.
  */
 int rf_decode_segments(int groups, int keys);
 
@@ -385,8 +387,8 @@ rf_status rf_attn_prefill_window(const void* q, const void* k, const void* v, in
                                  int dtype, void* out, float* lse, void* stream);
 
 /*
- * rf_prefix_segments -- the number of segments that rf_attn_decode_shared uses
- * for the prefix on the current device: at least 2; 0 if the device cannot run
+ * rf_prefix_segments -- the number of pieces that rf_attn_decode_shared makes of
+ * the prefix on the current device: at least 2; 0 if the device cannot run
  * it or the sizes are not valid.
  */
 int rf_prefix_segments(int B, int H, int Hkv, int prefix);
@@ -399,7 +401,7 @@ int rf_prefix_segments(int B, int H, int Hkv, int prefix);
  * rf_attn_decode_window, and the states are merged.  Two launches.
  *   q [B, H, D];  kp, vp [Hkv, prefix, D], prefix >= 1;  k, v [B, Hkv, cap, D]
  *   with lens [B] own keys each (0 allowed; the query stands behind all of them)
- *   Sp   segments of the prefix, >= 2;  S  segments of the own keys, >= 1
+ *   Sp   most pieces of the prefix, >= 2;  S  most pieces of the own keys, >= 1
  *   seg_m, seg_l [B*H, Sp + S], seg_acc [B*H, Sp + S, D], counters: as above
  * Errors: as above, plus RF_ERR_INVALID_ARG for prefix <= 0 or Sp < 2,
  * RF_ERR_UNSUPPORTED for Sp > 4096, H / Hkv > 128, prefix > 2^30, scale <= 0 or

@@ -70,6 +70,34 @@ def test_segment_counts(rf, S):
     assert torch.all(work.counters == 0)
 
 
+@pytest.mark.parametrize("S", [None, 1, 2, 3, 9, 60, 4096])
+@pytest.mark.parametrize("lens", [[2100, 0, 1, 17, 1600, 2099], [2100] * 6, [0, 0, 0, 0, 0, 1500]])
+def test_large_calls(rf, lens, S):
+    # enough tiles (48 groups of up to 132) for the warps to share them across groups
+    q, k, v, n = make(3, 6, 16, 8, 2100, lens, 0, 0, torch.bfloat16)
+    work = rf.decode_workspace(6, 16, 8, 2100, S=S)
+    for _ in range(2):
+        out, lse = rf.attn_decode_window(q, k, v, n, scale=SCALE, work=work)
+    check_decode(out, lse, q, k, v, lens, SCALE)
+    assert torch.all(work.counters == 0)
+
+
+def test_large_batch_of_short_sequences(rf):
+    # more sequences than a block has threads, most of a tile or less
+    lens = [(5 * b) % 37 for b in range(700)]
+    lens[333] = 300
+    q, k, v, n = make(4, 700, 8, 4, 300, lens, 0, 0, torch.float16)
+    out, lse = rf.attn_decode_window(q, k, v, n, scale=SCALE)
+    check_decode(out, lse, q, k, v, lens, SCALE)
+
+
+def test_large_windowed_call_with_many_query_heads(rf):
+    lens = [3000, 1, 700, 2999, 64]
+    q, k, v, n = make(5, 5, 40, 2, 3000, lens, 2500, 33, torch.bfloat16)
+    out, lse = rf.attn_decode_window(q, k, v, n, window=2500, sinks=33, scale=SCALE)
+    check_decode(out, lse, q, k, v, lens, SCALE, 2500, 33)
+
+
 def test_fp32_output_whole_cache_and_peaked_scores(rf):
     # no lengths: every sequence holds cap keys; large queries move the maximum often
     q, k, v, _ = make(5, 2, 4, 1, 777, [777, 777], 0, 0, torch.float16, gain=8.0)
