@@ -68,10 +68,21 @@
 //                              blocks, at least one; false past the last
 //   q_bytes()                  bytes of one CTA's Q tile that load_q copies
 //   load_q / load_k / load_v   the TMA copies of one CTA, into its halves
-//   mask(it, j, rank, row, kh, s)  scores of 128 keys of block j set to -inf
+//   keys(it, j)                256, or 64 for a block whose other keys no row
+//                              sees: its products stop there
+//   PARTIAL, words(it, j, rank, row, kh)  with PARTIAL, which of the warp's 128
+//                              keys (128 kh ..) of block j its rows may see: 4
+//                              (32-key words, all), 2 (only the first two; the
+//                              block is a narrow one) or 0; 4 for block 0
+//   mask<NW>(it, j, rank, row, kh, s)  sets hidden scores of the first 32 NW of
+//                              them to -inf
 //   pending(it, rank, row)     and  store(pend, kh, v, m, l): an output row's
 //                              64 columns 64 kh .. from O, m (log2 units), l;
-//                              true asks for
+//                              true asks for after(true, ...)
+//   STAGED                     instead of store():  pack(pend, kh, v, m, l, w)
+//                              gives the columns in 16 bits, and
+//                              send(map, box, pend, quarter, kh) starts the
+//                              copy of a warp's 32 x 64 box from shared memory
 //   after(any, c, nc, rank, row, kh)  once everything of the thread is stored
 #pragma once
 
@@ -85,6 +96,7 @@ namespace pair {
 
 constexpr int BM = 128;                      // query rows per CTA (256 per pair)
 constexpr int BN = 256;                      // keys per block
+constexpr int NARROW = 64;                   // keys of a narrow block
 constexpr int HD = 128;                      // head dim
 constexpr int STAGES = 2;
 constexpr int TILE_BYTES = 32768;            // Q tile, K half or V half
@@ -98,7 +110,8 @@ constexpr float RESCALE_THRESHOLD = 8.0f;    // log2 units
 
 struct Shared {
   uint64_t q_full[2];           // CTA 0: both Q tiles of a buffer
-  uint64_t q_empty[2];          // each CTA: the item's S MMAs are done with the buffer
+  uint64_t q_empty[2];          // each CTA: the item's S MMAs are done with the buffer (and, with
+                                // STAGED, its eight softmax warps' output stores have read it)
   uint64_t k_full[STAGES];      // CTA 0: both K halves of a stage
   uint64_t v_full[STAGES];      // CTA 0: both V halves of a stage
   uint64_t k_empty[STAGES];     // each CTA: S of that block done
@@ -151,6 +164,12 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // one 32-byte global store (sm_100+); `dst` 32-byte aligned
 __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
@@ -170,6 +189,11 @@ __device__ __forceinline__ void st_row32(void* dst, const uint32_t (&w)[16], boo
       d4[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   }
 }
+
+template <int N>
+struct Words {
+  static constexpr int value = N;
+};
 
 // arrival on a barrier of CTA 0 without release semantics (see the file
 // comment for why none is needed)
@@ -194,7 +218,8 @@ __device__ __forceinline__ uint32_t pack_16x2(float lo, float hi) {
 template <class P>
 __global__ void __launch_bounds__(THREADS, 1)
 attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ P p) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                 const __grid_constant__ P p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -212,7 +237,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sh->q_full[b], 1);
-      tc::mbar_init(&sh->q_empty[b], 1);
+      tc::mbar_init(&sh->q_empty[b], P::STAGED ? 1 + SM_WARPS : 1);
     }
     for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(&sh->k_full[s], 1);
@@ -269,6 +294,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // ------------------------------------------------------ MMA ----
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc_s = idesc_16<P::F16>(2 * BM, BN, false);
+      constexpr uint32_t idesc_s_narrow = idesc_16<P::F16>(2 * BM, NARROW, false);
       constexpr uint32_t idesc_pv = idesc_16<P::F16>(2 * BM, HD, true);
       // first K-step descriptors; a K-step adds its byte offset >> 4
       const uint64_t q_desc0 = tc::sdesc_sw128(tc::smem_u32(sQ), 16, 1024);
@@ -284,16 +310,17 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // S(g) = Q K^T from Q buffer qb: eight K-steps of 16 head-dimension
       // columns; the second 64 columns sit in the second swizzled box.  The
       // item's last S also releases its Q buffer.
-      auto issue_s = [&](uint32_t g, int qb, bool last_of_item) -> bool {
+      auto issue_s = [&](uint32_t g, int qb, bool narrow, bool last_of_item) -> bool {
         const int s = (int)(g & 1u);
         if (!tc::mbar_wait(&sh->k_full[s], (g >> 1) & 1u, abort)) return false;
         tc::fence_after_sync();
         const uint64_t kd = s ? k_desc1 : k_desc0;
         const uint64_t qd = qb ? q_desc1 : q_desc0;
+        const uint32_t idesc = narrow ? idesc_s_narrow : idesc_s;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4);
-          tc::mma_pair_f16_ss(tmem + S_COL, qd + off, kd + off, idesc_s, kk != 0);
+          tc::mma_pair_f16_ss(tmem + S_COL, qd + off, kd + off, idesc, kk != 0);
         }
         tc::commit_pair_both(&sh->s_full);
         tc::commit_pair_both(&sh->k_empty[s]);
@@ -301,16 +328,18 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         return true;
       };
       // O [+]= P V(g): sixteen K-steps of 16 keys (8 TMEM columns of P, 2 KiB of V)
-      auto issue_pv = [&](uint32_t g, bool accumulate) -> bool {
+      auto issue_pv = [&](uint32_t g, bool narrow, bool accumulate) -> bool {
         const int s = (int)(g & 1u);
         if (!tc::mbar_wait(&sh->v_full[s], (g >> 1) & 1u, abort)) return false;
         tc::fence_after_sync();
         const uint64_t vd = s ? v_desc1 : v_desc0;
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          if (kk >= NARROW / 16 && narrow) break;
           tc::mma_pair_f16_ts(tmem + O_COL, tmem + P_COL + (uint32_t)(kk * 8),
                               vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
                               (accumulate || kk > 0) ? 1u : 0u);
+        }
         tc::commit_pair_both(&sh->pv_done);
         tc::commit_pair_both(&sh->v_empty[s]);
         return true;
@@ -319,7 +348,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // the next) as soon as S(g) has been read, then P V(g) once P(g) is in
       typename P::Item it, next;
       bool ok = p.item(0, cluster, nclusters, it);
-      if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, it.n == 1);
+      if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0) < BN, it.n == 1);
       uint32_t g = 0;
       for (int t = 0; ok; ++t) {
         const bool has_next = p.item(t + 1, cluster, nclusters, next);
@@ -328,11 +357,11 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
             if (!(ok = tc::mbar_wait(&sh->s_free, g & 1u, abort))) break;
             if (j + 1 < it.n) {
-              ok = issue_s(g + 1, t & 1, j + 2 == it.n);
+              ok = issue_s(g + 1, t & 1, p.keys(it, j + 1) < BN, j + 2 == it.n);
             } else {
               const int qb = (t + 1) & 1;
               ok = tc::mbar_wait(&sh->q_full[qb], ((uint32_t)(t + 1) >> 1) & 1u, abort) &&
-                   issue_s(g + 1, qb, next.n == 1);
+                   issue_s(g + 1, qb, p.keys(next, 0) < BN, next.n == 1);
             }
             if (!ok) break;
           }
@@ -340,7 +369,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // the item's first P V overwrites O: the last item's O has been read
           if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort)))
             break;
-          ok = issue_pv(g, j > 0);
+          ok = issue_pv(g, p.keys(it, j) < BN, j > 0);
         }
         if (!has_next) break;
         it = next;
@@ -362,7 +391,9 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool pend = false;                              // an item's output is still to be written
     float pend_m = 0.f, pend_l = 0.f;
     typename P::Pending pending = {};
-    bool repair = false;                            // what store() found, for after()
+    bool repair = false;                            // what store() or pack() found, for after()
+    bool staged = false;                            // an output store may still read its Q buffer
+    int pend_qb = 0, staged_qb = 0;
     // O columns 64 kh .. + 63 of this thread's row
     auto load_o = [&](uint32_t (&v)[64]) {
       uint32_t (&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
@@ -371,44 +402,80 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       tc::tmem_ld_32x32b_x32(lanes + O_COL + (uint32_t)(kh * 64 + 32), v1);
       tc::tmem_ld_wait();
     };
-    auto finish = [&](const uint32_t (&v)[64]) -> bool {
-      sh->part_l[kh][r] = pend_l;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sh->red_bar[quarter]);
-      if (!tc::mbar_wait(&sh->red_bar[quarter], x & 1u, abort)) return false;
-      ++x;
+    // both halves of the row sums are in part_l: they were written before the
+    // exchange of the next item's first maxima
+    auto finish = [&](const uint32_t (&v)[64]) {
       const float lt = sh->part_l[0][r] + sh->part_l[1][r];
-      repair |= p.store(pending, kh, v, pend_m, lt);
-      return true;
+      if constexpr (P::STAGED) {
+        // the warp's 32 rows x 64 columns, swizzled as the map's box, over the
+        // item's own Q tile, whose products are long done
+        uint32_t w[32];
+        repair |= p.pack(pending, kh, v, pend_m, lt, w);
+        uint8_t* box = sQ + pend_qb * TILE_BYTES + kh * HALF_BYTES + quarter * 4096;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        tc::fence_proxy_async_cta();
+        __syncwarp();
+        if (lane == 0) {
+          p.send(&tmO, box, pending, quarter, kh);
+          tc::bulk_commit();
+        }
+        staged = true;
+        staged_qb = pend_qb;
+      } else {
+        repair |= p.store(pending, kh, v, pend_m, lt);
+      }
+    };
+    // the Q buffer that the last output went through may be filled again
+    auto release = [&] {
+      if constexpr (P::STAGED) {
+        if (!staged) return;
+        if (lane == 0) {
+          tc::bulk_wait_read();
+          tc::mbar_arrive(&sh->q_empty[staged_qb]);
+        }
+        staged = false;
+      }
     };
     typename P::Item it;
     for (int t = 0; ok; ++t) {
       if (!p.item(t, cluster, nclusters, it)) break;
       float m_ref = P::M_START, l = 0.f;
-      for (int j = 0; j < it.n; ++j, ++g) {
-        if (!(ok = tc::mbar_wait(&sh->s_full, g & 1u, abort))) break;
+      // One block, of which this warp's rows see keys in the first NW 32-key
+      // words of its 128 only; false if a wait gave up.  With NW < 4 it is not
+      // the item's first block.
+      auto block = [&](auto words, int j) -> bool {
+        constexpr int NW = decltype(words)::value;
+        release();
+        if (!tc::mbar_wait(&sh->s_full, g & 1u, abort)) return false;
         tc::fence_after_sync();
-        float s[128];                               // s[c] = key 128 kh + c of block j
-        {
+        float s[NW > 0 ? 32 * NW : 1];              // s[c] = key 128 kh + c of block j
+        if constexpr (NW > 0) {
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t (&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q4]);
-            tc::tmem_ld_32x32b_x32(lanes + S_COL + (uint32_t)(kh * 128 + 32 * q4), v);
+          for (int q = 0; q < NW; ++q) {
+            uint32_t (&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]);
+            tc::tmem_ld_32x32b_x32(lanes + S_COL + (uint32_t)(kh * 128 + 32 * q), v);
           }
           tc::tmem_ld_wait();
         }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive_cluster_relaxed(s_free0);
-        p.mask(it, j, rank, r, kh, s);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (NW > 0) {
+          p.template mask<NW>(it, j, rank, r, kh, s);
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], s[c], s[c + 1]);
+          for (int c = 0; c < 32 * NW; c += 2)
+            mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], s[c], s[c + 1]);
+        }
         float* red = &sh->red[x & 1u][0][0];
         red[kh * BM + r] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (NW == 4 && j == 0 && pend) sh->part_l[kh][r] = pend_l;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh->red_bar[quarter]);
-        if (!(ok = tc::mbar_wait(&sh->red_bar[quarter], x & 1u, abort))) break;
+        if (!tc::mbar_wait(&sh->red_bar[quarter], x & 1u, abort)) return false;
         ++x;
         const float pm = fmaxf(red[r], red[BM + r]);
         const float mt = pm * scale_log2;
@@ -417,12 +484,12 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const float alpha = ex2(m_ref - m_new);
         l *= alpha;
         m_ref = m_new;
-        uint32_t w[64];
-        {
+        uint32_t w[NW > 0 ? 16 * NW : 1];
+        if constexpr (NW > 0) {
           const uint64_t nm2 = pack_f32x2(-m_new, -m_new);
           uint64_t sum2 = 0ull;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < 16 * NW; ++c) {
             float a0, a1;
             unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), sl2, nm2), a0, a1);
             const float p0 = ex2(a0), p1 = ex2(a1);
@@ -434,7 +501,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           l += s0 + s1;
         }
         if (j > 0) {
-          if (!(ok = tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort))) break;
+          if (!tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort)) return false;
           tc::fence_after_sync();
           if (__any_sync(0xffffffffu, move)) {
 #pragma unroll 1
@@ -449,16 +516,24 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
           }
         }
-        const bool have_o = j == 0 && pend;
+        const bool have_o = NW == 4 && j == 0 && pend;
         if (have_o) {
-          if (!(ok = tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort))) break;
+          if (!tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort)) return false;
           tc::fence_after_sync();
         }
-        {
-          uint32_t (&w0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&w[0]);
-          uint32_t (&w1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&w[32]);
-          tc::tmem_st_32x32b_x32(lanes + P_COL + (uint32_t)(kh * 64), w0);
-          tc::tmem_st_32x32b_x32(lanes + P_COL + (uint32_t)(kh * 64 + 32), w1);
+        // P: the words in hand; a full block's products read the others as zeros
+        if constexpr (NW >= 2) {
+#pragma unroll
+          for (int h = 0; h < NW / 2; ++h) {
+            uint32_t (&wh)[32] = *reinterpret_cast<uint32_t(*)[32]>(&w[32 * h]);
+            tc::tmem_st_32x32b_x32(lanes + P_COL + (uint32_t)(kh * 64 + 32 * h), wh);
+          }
+        } else if (p.keys(it, j) == BN) {
+          uint32_t z[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) z[c] = 0u;
+          tc::tmem_st_32x32b_x32(lanes + P_COL + (uint32_t)(kh * 64), z);
+          tc::tmem_st_32x32b_x32(lanes + P_COL + (uint32_t)(kh * 64 + 32), z);
         }
         tc::tmem_st_wait();
         if (have_o) {
@@ -470,12 +545,23 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             arrive_cluster_relaxed(o_free0);
             arrive_cluster_relaxed(p_ready0);
           }
-          if (!(ok = finish(ov))) break;
+          finish(ov);
           pend = false;
+          // the next item's first S needs its Q tile before this warp comes here again
+          if (it.n == 1) release();
         } else {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) arrive_cluster_relaxed(p_ready0);
+        }
+        return true;
+      };
+      for (int j = 0; ok && j < it.n; ++j, ++g) {
+        if constexpr (P::PARTIAL) {
+          const int words = p.words(it, j, rank, r, kh);
+          ok = words == 4 ? block(Words<4>{}, j) : words == 2 ? block(Words<2>{}, j) : block(Words<0>{}, j);
+        } else {
+          ok = block(Words<4>{}, j);
         }
       }
       if (!ok) break;
@@ -483,9 +569,15 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       pend_m = m_ref;
       pend_l = l;
       pending = p.pending(it, rank, r);
+      pend_qb = t & 1;
     }
     if (ok && pend) {
-      if (tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort)) {
+      sh->part_l[kh][r] = pend_l;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh->red_bar[quarter]);
+      ok = tc::mbar_wait(&sh->red_bar[quarter], x & 1u, abort) &&
+           tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort);
+      if (ok) {
         tc::fence_after_sync();
         uint32_t ov[64];
         load_o(ov);
@@ -495,6 +587,9 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         finish(ov);
       }
     }
+    // no output is read from shared memory after the CTA is gone
+    if (P::STAGED && lane == 0) tc::bulk_wait();
+    __syncwarp();
     if (ok) p.after(repair, cluster, nclusters, rank, r, kh);
   }
 
@@ -551,11 +646,11 @@ int resident_pairs() {
 }
 
 template <class P>
-rf_status launch_pair(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const P& p,
-                      int clusters, cudaStream_t st) {
+rf_status launch_pair(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                      const CUtensorMap& o, const P& p, int clusters, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pair_config(attr, 2u * (unsigned)clusters, st);
-  if (cudaLaunchKernelEx(&cfg, attn_pair_kernel<P>, q, k, v, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, attn_pair_kernel<P>, q, k, v, o, p) != cudaSuccess) {
     cudaGetLastError();
     return RF_ERR_CUDA;
   }

@@ -21,7 +21,7 @@ using pair::HD;
 
 struct CausalPrefill {
   static constexpr bool F16 = false;
-  static constexpr bool DEPENDENTS = false;
+  static constexpr bool DEPENDENTS = false, PARTIAL = false, STAGED = false;
   static constexpr float M_START = -INFINITY;
   // A work item: 256 query rows (two 128-row tiles) of one head.
   struct Item {
@@ -70,8 +70,10 @@ struct CausalPrefill {
                                          const Item& it, int j, int rank) const {
     tc::tma_load_2d_pair(dst, map, bar, rank * 64, it.key0 + j * BN);
   }
+  __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
+  template <int NW>
   __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
-                                       float (&s)[128]) const {
+                                       float (&s)[32 * NW]) const {
     const int NKB = (N + BN - 1) / BN;
     if (causal && j == it.n - 1) {
       const int lim = BM * rank + r - kh * 128;
@@ -137,7 +139,7 @@ rf_status launch_prefill(const void* q, const void* k, const void* v, int B, int
   if (items > INT32_MAX) return RF_ERR_UNSUPPORTED;
   const int clusters = (int)(pairs < items ? pairs : items);
   const CausalPrefill p{static_cast<__nv_bfloat16*>(out), lse, N, causal, (int)items, scale * kLog2e};
-  return pair::launch_pair(tq, tk, tv, p, clusters, st);
+  return pair::launch_pair(tq, tk, tv, tq, p, clusters, st);
 }
 
 RF_TIMEOUT_WORD_OF_THIS_FILE

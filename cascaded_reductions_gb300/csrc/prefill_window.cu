@@ -35,7 +35,7 @@ using pair::HD;
 template <bool F16_>
 struct WindowPrefill {
   static constexpr bool F16 = F16_;
-  static constexpr bool DEPENDENTS = false;
+  static constexpr bool DEPENDENTS = false, PARTIAL = true, STAGED = true;
   static constexpr float M_START = -1e30f;
   struct Item {
     int bh, kvh;     // query head of the batch, key head of the batch
@@ -88,7 +88,7 @@ struct WindowPrefill {
   }
   __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
                                          const Item& it, int j, int rank) const {
-    const int key = key0(it, j) + rank * (BN / 2);
+    const int key = key0(it, j) + rank * (keys(it, j) / 2);
     tc::tma_load_3d_pair(dst, map, bar, 0, key, it.kvh);
     tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, key, it.kvh);
   }
@@ -96,30 +96,46 @@ struct WindowPrefill {
                                          const Item& it, int j, int rank) const {
     tc::tma_load_3d_pair(dst, map, bar, rank * 64, key0(it, j), it.kvh);
   }
-  __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
-                                       float (&s)[128]) const {
+  // the sinks' block below the window's is usually a few keys
+  __device__ __forceinline__ int keys(const Item& it, int j) const {
+    return j >= it.nb && it.limit <= pair::NARROW ? pair::NARROW : BN;
+  }
+  // bits below n of a word
+  static __device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  }
+  // A warp whose rows see none of its keys of a block (half of those at the two
+  // edges) skips its scores; of a narrow block there are 64 keys.
+  __device__ __forceinline__ int words(const Item& it, int j, int rank, int r, int kh) const {
+    if (j >= it.nb) return keys(it, j) == BN ? 4 : kh == 0 ? 2 : 0;
     const int base = key0(it, j) + kh * 128;
+    const int first = L - N + it.row0 + rank * BM + (r & ~31), last = first + 31;
+    const bool some = last >= base && (first - window + 1 < base + 128 || sinks > base);
+    return some || j == 0 ? 4 : 0;
+  }
+  // A word of visible keys per row and 32 of them; an edge crosses a warp's 32
+  // rows within one or two words.
+  template <int NW>
+  __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
+                                       float (&s)[32 * NW]) const {
+    const int base = key0(it, j) + kh * 128;
+    const int p = L - N + it.row0 + rank * BM + r;      // this row's position
+    const int first = p - (r & 31), last = first + 31;   // the warp's positions
+    // keys [lo, hi] and below cs, counted from base
+    int hi = p - base, lo = p - window + 1 - base, cs = sinks - base;
     if (j < it.nb) {
-      const int p = L - N + it.row0 + rank * BM + r;    // this row's position
-      const int first = p - (r & 31), last = first + 31;   // the warp's positions
-      const int hi = p - base;                          // s[c] visible up to c = hi
-      if (first - base < 127) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > hi) s[c] = -INFINITY;
-      }
-      if (last - window + 1 > base) {
-        const int lo = p - window + 1 - base, cs = sinks - base;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < lo && c >= cs) s[c] = -INFINITY;
-      }
+      if (first - base >= 127 && last - window + 1 <= base) return;
     } else {
-      const int lim = it.limit - base;
-      if (lim < 128) {
+      hi = 127, lo = 128, cs = it.limit - base;
+      if (cs >= 128) return;
+    }
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= lim) s[c] = -INFINITY;
+    for (int q = 0; q < NW; ++q) {
+      const uint32_t vis = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));
+      if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!(vis & (1u << c))) s[32 * q + c] = -INFINITY;
       }
     }
   }
@@ -127,30 +143,33 @@ struct WindowPrefill {
     const int row = it.row0 + rank * BM + r;
     return {it.bh, row, row < N};
   }
-  __device__ __forceinline__ bool store(const Pending& pend, int kh, const uint32_t (&v)[64],
-                                        float m, float lt) const {
-    const size_t row = (size_t)pend.bh * N + pend.row;
-    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+  __device__ __forceinline__ bool pack(const Pending& pend, int kh, const uint32_t (&v)[64], float m,
+                                       float lt, uint32_t (&w)[32]) const {
     const float inv = 1.f / lt;
-    float probe = 0.f;                                  // NaN if any of the row's is not finite
+    const uint64_t inv2 = pair::pack_f32x2(inv, inv);
+    uint64_t probe = 0ull;                              // NaN if a value is not finite
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      uint32_t pkd[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float x0 = __uint_as_float(v[32 * hh + 2 * c]) * inv;
-        const float x1 = __uint_as_float(v[32 * hh + 2 * c + 1]) * inv;
-        probe = fmaf(x0, 0.f, probe);
-        probe = fmaf(x1, 0.f, probe);
-        pkd[c] = pair::pack_16x2<F16>(x0, x1);
-      }
-      const int col = kh * 64 + hh * 32;
-      if (pend.in && RF_SPAN_OK(row * HD + col, 32, (size_t)heads * N * HD))
-        pair::st_row32(out + row * HD + col, pkd, wide);
+    for (int c = 0; c < 32; ++c) {
+      const uint64_t x = pair::mul_f32x2(
+          pair::pack_f32x2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), inv2);
+      probe = pair::fma_f32x2(x, 0ull, probe);
+      float x0, x1;
+      pair::unpack_f32x2(x, x0, x1);
+      w[c] = pair::pack_16x2<F16>(x0, x1);
     }
+    const size_t row = (size_t)pend.bh * N + pend.row;
     if (lse != nullptr && kh == 0 && pend.in && RF_IDX_OK(row, (size_t)heads * N))
       lse[row] = (m + log2f(lt)) * kLn2;
-    return pend.in && !(probe == 0.f);
+    float p0, p1;
+    pair::unpack_f32x2(probe, p0, p1);
+    return pend.in && !(p0 == 0.f && p1 == 0.f);
+  }
+  // rows past N lie past the map's extent and are not written
+  __device__ __forceinline__ void send(const CUtensorMap* map, const uint8_t* box, const Pending& pend,
+                                       int quarter, int kh) const {
+    const int row = pend.row & ~31;
+    (void)quarter;
+    if (row < N) tc::tma_store_3d(map, box, kh * 64, row, pend.bh);
   }
 
   static __device__ __forceinline__ float widen(uint32_t w, int hi) {
@@ -250,11 +269,12 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   using P = WindowPrefill<F16>;
   const int pairs = pair::resident_pairs<P>();
   if (pairs <= 0) return RF_ERR_UNSUPPORTED;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   const uint64_t qh = (uint64_t)B * H, kh = (uint64_t)B * Hkv;
   if (!tc::make_tmap_3d_16(&tq, F16, q, HD, N, qh, 64, BM, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tk, F16, k, HD, L, kh, 64, BN / 2, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tc::make_tmap_3d_16(&tv, F16, v, HD, L, kh, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B))
+      !tc::make_tmap_3d_16(&tv, F16, v, HD, L, kh, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_tmap_3d_16(&to, F16, out, HD, N, qh, 64, 32, 1, CU_TENSOR_MAP_SWIZZLE_128B))
     return RF_ERR_CUDA;
   P p = {};
   p.q = static_cast<const uint16_t*>(q);
@@ -269,7 +289,7 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   p.pairs = (N + 2 * BM - 1) / (2 * BM);
   p.scale_log2 = scale * kLog2e;
   const long long items = (long long)p.heads * p.pairs;
-  return pair::launch_pair(tq, tk, tv, p, (int)(pairs < items ? pairs : items), st);
+  return pair::launch_pair(tq, tk, tv, to, p, (int)(pairs < items ? pairs : items), st);
 }
 
 }  // namespace

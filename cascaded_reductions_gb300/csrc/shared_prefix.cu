@@ -39,16 +39,12 @@ struct Split {
   __host__ __device__ int owner(long long x) const {
     return (int)(((x + 1) * clusters + total - 1) / total) - 1;
   }
-  // states of one row of tile i
-  __host__ __device__ int slots(int i) const {
-    return owner((long long)(i + 1) * blocks - 1) - owner((long long)i * blocks) + 1;
-  }
 };
 
 template <bool F16_>
 struct PrefixStates {
   static constexpr bool F16 = F16_;
-  static constexpr bool DEPENDENTS = true;
+  static constexpr bool DEPENDENTS = true, PARTIAL = false, STAGED = false;
   static constexpr float M_START = -1e30f;
   struct Item {
     int hk, seq0;            // key head; first sequence of the pair of tiles
@@ -100,8 +96,10 @@ struct PrefixStates {
                                          const Item& it, int j, int rank) const {
     tc::tma_load_3d_pair(dst, map, bar, rank * 64, (it.block0 + j) * BN, it.hk);
   }
+  __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
+  template <int NW>
   __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
-                                       float (&s)[128]) const {
+                                       float (&s)[32 * NW]) const {
     (void)rank;
     (void)r;
     const int lim = P - (it.block0 + j) * BN - kh * 128;
@@ -182,7 +180,7 @@ rf_status launch_t(const void* q, const void* kp, const void* vp, int prefix, in
       !tc::make_tmap_3d_16(&tk, F16, kp, HD, prefix, Hkv, 64, BN / 2, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tv, F16, vp, HD, prefix, Hkv, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B))
     return RF_ERR_CUDA;
-  return pair::launch_pair(tq, tk, tv, p, p.split.clusters, st);
+  return pair::launch_pair(tq, tk, tv, tq, p, p.split.clusters, st);
 }
 
 }  // namespace
