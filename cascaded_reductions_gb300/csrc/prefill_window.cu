@@ -6,12 +6,13 @@
 //   visible(p) = { j <= p : j > p - window or j < sinks }.
 //
 // What bounds it: the tensor pipe, 4 D flops per pair of row and key.  An item
-// is 256 adjacent rows; it visits the 256-key blocks that cover the keys any
-// of its rows sees, counted from the lowest of them (so a window of W keys
-// takes ceil((W + 255) / 256) blocks and never one more for alignment), last
-// block first, and then the blocks of the sinks below that cover.  Only the
-// blocks at the two edges are masked, and only by the warps that an edge
-// crosses.
+// is 256 query rows on one key head: up to 8 of the query heads that share it,
+// and 256 / heads adjacent positions (256 rows of one head would need the keys
+// of 256 positions; 64 positions of four heads need 192 fewer).  It visits the
+// 256-key blocks that cover the keys any of its rows sees, last block first, a
+// remainder of up to 64 keys as a narrow block, and then the sinks below that
+// cover, narrow too where 64 keys are enough.  Only the blocks at the two edges
+// are masked, only by the warps that an edge crosses, a 32-key word at a time.
 //
 // A row that sees nothing of a block must not be disturbed by it: its
 // reference starts at a finite value below every score, so such a block gives
@@ -38,11 +39,13 @@ struct WindowPrefill {
   static constexpr bool DEPENDENTS = false, PARTIAL = true, STAGED = true;
   static constexpr float M_START = -1e30f;
   struct Item {
-    int bh, kvh;     // query head of the batch, key head of the batch
-    int row0;        // first of 256 query rows
-    int lo;          // first key of the window blocks
-    int nb;          // window blocks; block j < nb starts at lo + 256 (nb - 1 - j)
-    int limit;       // sinks below lo; block j >= nb starts at 256 (j - nb)
+    int bh, kvh;     // first query head and key head, of the batch
+    int row0;        // first position's row
+    int lo;          // first key that a row sees beside the sinks
+    int rem;         // keys of the narrow window block at lo, or 0
+    int nb;          // full window blocks; block j < nb starts at lo + rem + 256 (nb - 1 - j)
+    int nw;          // window blocks; block nb, if it is one, is the narrow one
+    int limit;       // sinks below lo; block j >= nw starts at 256 (j - nw)
     int n;
   };
   struct Pending {
@@ -55,7 +58,8 @@ struct WindowPrefill {
   float* lse;
   int N, L, G, window, sinks;      // window and sinks at most L
   int heads;                       // B * H
-  int pairs;                       // items per head
+  int packed, positions;           // query heads per item, 256 / packed positions
+  int pairs;                       // items per `packed` heads
   float scale_log2;
 
   // items head-major (query heads of a key head together), last rows first, in
@@ -63,28 +67,40 @@ struct WindowPrefill {
   __device__ __forceinline__ bool item(int t, int cluster, int nclusters, Item& it) const {
     const long long turn =
         (long long)t * nclusters + ((t & 1) ? nclusters - 1 - cluster : cluster);
-    if (turn >= (long long)heads * pairs) return false;
+    if (turn >= (long long)(heads / packed) * pairs) return false;
     const int i = (int)turn;                            // below B * H * N < 2^31
-    it.bh = i / pairs;
+    it.bh = i / pairs * packed;
     it.kvh = it.bh / G;
-    it.row0 = (pairs - 1 - i % pairs) * 2 * BM;
-    const int p0 = L - N + it.row0;                     // position of the first row
-    const int hi = min(p0 + 2 * BM, L) - 1;             // last key of the last row
+    it.row0 = (pairs - 1 - i % pairs) * positions;
+    const int p0 = L - N + it.row0;                     // the first position
+    const int hi = min(p0 + positions, L) - 1;          // last key of the last one
     it.lo = max(0, p0 - window + 1);
-    it.nb = (hi - it.lo + BN) / BN;
+    const int span = hi - it.lo + 1;
+    it.nb = span / BN;
+    it.rem = span - it.nb * BN;
+    if (it.rem > pair::NARROW || it.nb == 0) {
+      ++it.nb;
+      it.rem = 0;
+    }
+    it.nw = it.nb + (it.rem > 0);
     it.limit = min(sinks, it.lo);
-    it.n = it.nb + (it.limit + BN - 1) / BN;
+    it.n = it.nw + (it.limit + BN - 1) / BN;
     return true;
   }
   __device__ __forceinline__ int key0(const Item& it, int j) const {
-    return j < it.nb ? it.lo + (it.nb - 1 - j) * BN : (j - it.nb) * BN;
+    return j < it.nb ? it.lo + it.rem + (it.nb - 1 - j) * BN : j < it.nw ? it.lo : (j - it.nw) * BN;
+  }
+  // row r of CTA `rank`: head bh + head_of, position row0 + row_of
+  __device__ __forceinline__ int head_of(int rank, int r) const { return (rank * BM + r) / positions; }
+  __device__ __forceinline__ int row_of(int rank, int r) const {
+    return (rank * BM + r) & (positions - 1);
   }
   __device__ __forceinline__ uint32_t q_bytes() const { return pair::TILE_BYTES; }
   __device__ __forceinline__ void load_q(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
                                          const Item& it, int rank) const {
-    const int row = it.row0 + rank * BM;
-    tc::tma_load_3d_pair(dst, map, bar, 0, row, it.bh);
-    tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, row, it.bh);
+    const int row = it.row0 + row_of(rank, 0), head = it.bh + head_of(rank, 0);
+    tc::tma_load_3d_pair(dst, map, bar, 0, row, head);
+    tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, row, head);
   }
   __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
                                          const Item& it, int j, int rank) const {
@@ -96,9 +112,8 @@ struct WindowPrefill {
                                          const Item& it, int j, int rank) const {
     tc::tma_load_3d_pair(dst, map, bar, rank * 64, key0(it, j), it.kvh);
   }
-  // the sinks' block below the window's is usually a few keys
   __device__ __forceinline__ int keys(const Item& it, int j) const {
-    return j >= it.nb && it.limit <= pair::NARROW ? pair::NARROW : BN;
+    return j >= it.nb && (j < it.nw || it.limit <= pair::NARROW) ? pair::NARROW : BN;
   }
   // bits below n of a word
   static __device__ __forceinline__ uint32_t below(int n) {
@@ -109,7 +124,7 @@ struct WindowPrefill {
   __device__ __forceinline__ int words(const Item& it, int j, int rank, int r, int kh) const {
     if (j >= it.nb) return keys(it, j) == BN ? 4 : kh == 0 ? 2 : 0;
     const int base = key0(it, j) + kh * 128;
-    const int first = L - N + it.row0 + rank * BM + (r & ~31), last = first + 31;
+    const int first = L - N + it.row0 + row_of(rank, r & ~31), last = first + 31;
     const bool some = last >= base && (first - window + 1 < base + 128 || sinks > base);
     return some || j == 0 ? 4 : 0;
   }
@@ -119,12 +134,14 @@ struct WindowPrefill {
   __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
                                        float (&s)[32 * NW]) const {
     const int base = key0(it, j) + kh * 128;
-    const int p = L - N + it.row0 + rank * BM + r;      // this row's position
+    const int p = L - N + it.row0 + row_of(rank, r);    // this row's position
     const int first = p - (r & 31), last = first + 31;   // the warp's positions
     // keys [lo, hi] and below cs, counted from base
     int hi = p - base, lo = p - window + 1 - base, cs = sinks - base;
     if (j < it.nb) {
       if (first - base >= 127 && last - window + 1 <= base) return;
+    } else if (j < it.nw) {
+      hi = min(hi, it.rem - 1);                         // the rest is the next block's
     } else {
       hi = 127, lo = 128, cs = it.limit - base;
       if (cs >= 128) return;
@@ -140,8 +157,8 @@ struct WindowPrefill {
     }
   }
   __device__ __forceinline__ Pending pending(const Item& it, int rank, int r) const {
-    const int row = it.row0 + rank * BM + r;
-    return {it.bh, row, row < N};
+    const int row = it.row0 + row_of(rank, r);
+    return {it.bh + head_of(rank, r), row, row < N};
   }
   __device__ __forceinline__ bool pack(const Pending& pend, int kh, const uint32_t (&v)[64], float m,
                                        float lt, uint32_t (&w)[32]) const {
@@ -239,10 +256,10 @@ struct WindowPrefill {
   __device__ __noinline__ void repair(int cluster, int nclusters, int rank, int r, int kh) const {
     Item it;
     for (int t = 0; item(t, cluster, nclusters, it); ++t) {
-      const int row = it.row0 + rank * BM + r;
+      const int row = it.row0 + row_of(rank, r), head = it.bh + head_of(rank, r);
       bool nan = false;
       if (row < N) {
-        const size_t o = ((size_t)it.bh * N + row) * HD + kh * 64;
+        const size_t o = ((size_t)head * N + row) * HD + kh * 64;
         for (int c = 0; c < 8; ++c) {
           if (!RF_SPAN_OK(o + c * 8, 8, (size_t)heads * N * HD)) continue;
           const uint4 u = *(reinterpret_cast<const uint4*>(out + o) + c);
@@ -253,7 +270,7 @@ struct WindowPrefill {
       while (todo) {
         const int lane0 = __ffs(todo) - 1;
         todo &= todo - 1;
-        redo(it.bh, __shfl_sync(0xffffffffu, row, lane0), kh, r & 31);
+        redo(head, __shfl_sync(0xffffffffu, row, lane0), kh, r & 31);
       }
     }
   }
@@ -271,7 +288,10 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   if (pairs <= 0) return RF_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv, to;
   const uint64_t qh = (uint64_t)B * H, kh = (uint64_t)B * Hkv;
-  if (!tc::make_tmap_3d_16(&tq, F16, q, HD, N, qh, 64, BM, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const int G = H / Hkv;
+  const int packed = G % 8 == 0 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
+  const int positions = 2 * BM / packed, box = positions < BM ? positions : BM;
+  if (!tc::make_tmap_3d_16(&tq, F16, q, HD, N, qh, 64, box, BM / box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tk, F16, k, HD, L, kh, 64, BN / 2, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tv, F16, v, HD, L, kh, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&to, F16, out, HD, N, qh, 64, 32, 1, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -282,13 +302,14 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   p.v = static_cast<const uint16_t*>(v);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.N = N, p.L = L, p.G = H / Hkv;
+  p.N = N, p.L = L, p.G = G;
   p.window = window == 0 || window > L ? L : window;
   p.sinks = sinks > L ? L : sinks;
   p.heads = B * H;
-  p.pairs = (N + 2 * BM - 1) / (2 * BM);
+  p.packed = packed, p.positions = positions;
+  p.pairs = (N + positions - 1) / positions;
   p.scale_log2 = scale * kLog2e;
-  const long long items = (long long)p.heads * p.pairs;
+  const long long items = (long long)(p.heads / packed) * p.pairs;
   return pair::launch_pair(tq, tk, tv, to, p, (int)(pairs < items ? pairs : items), st);
 }
 

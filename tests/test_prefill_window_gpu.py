@@ -83,7 +83,7 @@ def test_chunks_behind_a_cache(rf, N, L, window, sinks):
     check(out, lse, q, k, v, window, sinks, rows=sorted({*range(0, N, 5), N - 1}))
 
 
-@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2), (7, 1), (6, 3)])
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2), (7, 1), (6, 3), (8, 1), (12, 1), (32, 2)])
 def test_head_groups(rf, H, Hkv):
     q, k, v = make(H, 2, H, Hkv, 200, 333, torch.float16)
     out, lse = run(rf, q, k, v, 90, 3)
@@ -182,3 +182,13 @@ def test_prompt_then_tokens(rf):
     n = torch.tensor([600], dtype=torch.int32, device="cuda")
     out, l1 = rf.attn_decode_window(q[:, :, 599].contiguous(), k, v, n, window=window, sinks=sinks, scale=SCALE)
     check(out[:, :, None], l1[:, :, None], q[:, :, 599:600], k[:, :, :600], v[:, :, :600], window, sinks)
+
+
+@pytest.mark.parametrize("N,L,window,sinks", [(1, 1, 0, 0), (5, 400, 300, 2), (33, 33, 7, 1), (70, 391, 256, 64),
+                                              (200, 900, 512, 70), (65, 2000, 1984, 65)])
+def test_query_heads_of_a_group_share_blocks(rf, N, L, window, sinks):
+    # 8, 4 and 2 query heads to an item: covers that end in a narrow block and that do not
+    for H, Hkv in ((8, 1), (8, 2), (4, 2)):
+        q, k, v = make(N + H, 1, H, Hkv, N, L, torch.bfloat16)
+        out, lse = run(rf, q, k, v, window, sinks)
+        check(out, lse, q, k, v, window, sinks, rows=sorted({*range(0, N, 13), N - 1}))
