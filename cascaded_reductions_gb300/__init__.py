@@ -20,6 +20,7 @@ instead, e.g. the bounds-checked debug variant that
 import contextlib
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -145,24 +146,47 @@ def _cache_dtype(dt, name):
     return _CACHE_DTYPES[dt]
 
 
-def _one_device(*tensors):
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one call works on one device")
+# the current stream's handle and the current device, without making objects of
+# them: a decode step is a handful of microseconds
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
     return dev
 
 
+def _on(dev, t, dtype, shape, name):
+    """``t`` as it has to be: on device ``dev`` (an index), of a type and shape, contiguous."""
+    if (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return
+    _need(t, dtype, name, shape)
+    raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}: one call works on one device")
+
+
 def _call_on(dev, stream, where, fn, *args):
-    """fn(*args, stream) with ``dev`` current; raises RFError on a bad status."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-    ptr = ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, ptr), where)
+    """fn(*args, stream) with device ``dev`` (an index) current; raises RFError on a bad status."""
+    if stream is None:
+        ptr = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+    else:
+        ptr = stream.cuda_stream
+    if _current_device() == dev:
+        status = fn(*args, ptr)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, ptr), where)
+            status = fn(*args, ptr)
+    if status != RF_OK:
+        raise RFError(status, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def version():
@@ -410,29 +434,28 @@ def rf_decode_segments(groups, keys):
 
 
 def _need_cache(q, k, v, lens):
-    """Checks q [B, H, D], k/v [B, Hkv, cap, D] and lens [B]; returns the sizes."""
+    """Checks q [B, H, D], k/v [B, Hkv, cap, D] and lens [B]; returns the sizes and the device."""
     if q.dim() != 3 or k.dim() != 4:
         raise ValueError("q must be [B, H, D] and k [B, Hkv, cap, D]")
+    dev = _device_of(q, "q")
     B, H, D = q.shape
-    Hkv, cap = k.shape[1], k.shape[2]
-    _need(q, q.dtype, "q")
-    _need(k, q.dtype, "k", (B, Hkv, cap, D))
-    _need(v, q.dtype, "v", (B, Hkv, cap, D))
+    _, Hkv, cap, _ = k.shape
+    dt = q.dtype
+    _on(dev, q, dt, q.shape, "q")
+    _on(dev, k, dt, (B, Hkv, cap, D), "k")
+    _on(dev, v, dt, k.shape, "v")
     if lens is not None:
-        _need(lens, torch.int32, "lens", (B,))
-    return B, H, Hkv, cap, D
+        _on(dev, lens, torch.int32, (B,), "lens")
+    return B, H, Hkv, cap, D, dev
 
 
-def _need_scratch(B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters, out, lse):
-    _need(seg_m, torch.float32, "seg_m", (B * H, S))
-    _need(seg_l, torch.float32, "seg_l", (B * H, S))
-    _need(seg_acc, torch.float32, "seg_acc", (B * H, S, D))
-    _need(counters, torch.int32, "counters")
+def _need_scratch(dev, B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters):
+    _on(dev, seg_m, torch.float32, (B * H, S), "seg_m")
+    _on(dev, seg_l, torch.float32, (B * H, S), "seg_l")
+    _on(dev, seg_acc, torch.float32, (B * H, S, D), "seg_acc")
+    _on(dev, counters, torch.int32, counters.shape, "counters")
     if counters.numel() < B * Hkv * (-(-(H // max(Hkv, 1)) // 16)):
         raise ValueError("counters must hold B * Hkv * ceil(H / Hkv / 16) elements")
-    _need(out, out.dtype, "out", (B, H, D))
-    if lse is not None:
-        _need(lse, torch.float32, "lse", (B, H))
 
 
 def rf_attn_decode_window(q, k, v, lens, window, sinks, S, scale, seg_m, seg_l, seg_acc, counters,
@@ -440,13 +463,15 @@ def rf_attn_decode_window(q, k, v, lens, window, sinks, S, scale, seg_m, seg_l, 
     """q [B, H, D], k/v [B, Hkv, cap, D] (bf16 or fp16, D = 128), lens int32 [B] or None ->
     out [B, H, D] (q's type or fp32), lse [B, H].  Scratch: seg_m/seg_l [B*H, S],
     seg_acc [B*H, S, D] fp32, counters int32 [B * Hkv * ceil(H / Hkv / 16)], zero at first."""
-    B, H, Hkv, cap, D = _need_cache(q, k, v, lens)
-    _need_scratch(B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters, out, lse)
-    dev = _one_device(q, k, v, lens, seg_m, seg_l, seg_acc, counters, out, lse)
-    _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, _ptr(q), _ptr(k),
-             _ptr(v), _ptr(lens), B, H, Hkv, cap, D, int(window), int(sinks), int(S), float(scale),
-             _cache_dtype(q.dtype, "q"), _ptr(seg_m), _ptr(seg_l), _ptr(seg_acc), _ptr(counters),
-             _ptr(out), _cache_dtype(out.dtype, "out"), _ptr(lse))
+    B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
+    _need_scratch(dev, B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters)
+    _on(dev, out, out.dtype, (B, H, D), "out")
+    if lse is not None:
+        _on(dev, lse, torch.float32, (B, H), "lse")
+    _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, S, scale,
+             _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
+             counters.data_ptr(), out.data_ptr(), _cache_dtype(out.dtype, "out"), _addr(lse))
 
 
 def rf_attn_decode_weights(q, k, v, lens, S, scale, seg_m, seg_l, seg_acc, counters, scores, out,
@@ -454,19 +479,20 @@ def rf_attn_decode_weights(q, k, v, lens, S, scale, seg_m, seg_l, seg_acc, count
     """Decode as rf_attn_decode_window without a window; weight_out [B, Hkv, cap] = weight (or 0
     for None; may be weight_out itself) + the softmax weights summed over each group's heads.
     scores [B, H, cap] fp32 scratch."""
-    B, H, Hkv, cap, D = _need_cache(q, k, v, lens)
-    _need_scratch(B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters, out, lse)
-    _need(scores, torch.float32, "scores", (B, H, cap))
-    _need(weight_out, torch.float32, "weight_out", (B, Hkv, cap))
+    B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
+    _need_scratch(dev, B, H, Hkv, D, S, seg_m, seg_l, seg_acc, counters)
+    _on(dev, out, out.dtype, (B, H, D), "out")
+    if lse is not None:
+        _on(dev, lse, torch.float32, (B, H), "lse")
+    _on(dev, scores, torch.float32, (B, H, cap), "scores")
+    _on(dev, weight_out, torch.float32, (B, Hkv, cap), "weight_out")
     if weight is not None:
-        _need(weight, torch.float32, "weight", (B, Hkv, cap))
-    dev = _one_device(q, k, v, lens, seg_m, seg_l, seg_acc, counters, scores, out, lse, weight,
-                      weight_out)
-    _call_on(dev, stream, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, _ptr(q), _ptr(k),
-             _ptr(v), _ptr(lens), B, H, Hkv, cap, D, int(S), float(scale),
-             _cache_dtype(q.dtype, "q"), _ptr(seg_m), _ptr(seg_l), _ptr(seg_acc), _ptr(counters),
-             _ptr(scores), _ptr(out), _cache_dtype(out.dtype, "out"), _ptr(lse), _ptr(weight),
-             _ptr(weight_out))
+        _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
+    _call_on(dev, stream, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, S, scale,
+             _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
+             counters.data_ptr(), scores.data_ptr(), out.data_ptr(),
+             _cache_dtype(out.dtype, "out"), _addr(lse), _addr(weight), weight_out.data_ptr())
 
 
 def rf_attn_prefill_window(q, k, v, window, sinks, scale, out, lse=None, stream=None):
@@ -474,41 +500,45 @@ def rf_attn_prefill_window(q, k, v, window, sinks, scale, out, lse=None, stream=
     lse [B, H, N] fp32 (optional)."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, H, N, D] and k [B, Hkv, L, D]")
+    dev = _device_of(q, "q")
     B, H, N, D = q.shape
-    Hkv, L = k.shape[1], k.shape[2]
-    _need(q, q.dtype, "q")
-    _need(k, q.dtype, "k", (B, Hkv, L, D))
-    _need(v, q.dtype, "v", (B, Hkv, L, D))
-    _need(out, q.dtype, "out", (B, H, N, D))
+    _, Hkv, L, _ = k.shape
+    dt = q.dtype
+    _on(dev, q, dt, q.shape, "q")
+    _on(dev, k, dt, (B, Hkv, L, D), "k")
+    _on(dev, v, dt, k.shape, "v")
+    _on(dev, out, dt, q.shape, "out")
     if lse is not None:
-        _need(lse, torch.float32, "lse", (B, H, N))
-    dev = _one_device(q, k, v, out, lse)
-    _call_on(dev, stream, "rf_attn_prefill_window", _lib.rf_attn_prefill_window, _ptr(q), _ptr(k),
-             _ptr(v), B, H, Hkv, N, L, D, int(window), int(sinks), float(scale),
-             _cache_dtype(q.dtype, "q"), _ptr(out), _ptr(lse))
+        _on(dev, lse, torch.float32, (B, H, N), "lse")
+    _call_on(dev, stream, "rf_attn_prefill_window", _lib.rf_attn_prefill_window, q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), B, H, Hkv, N, L, D, window, sinks, scale,
+             _cache_dtype(dt, "q"), out.data_ptr(), _addr(lse))
 
 
 def rf_prefix_segments(B, H, Hkv, prefix):
-    """Segments that rf_attn_decode_shared uses for the prefix on the current device (0: none)."""
+    """Pieces that rf_attn_decode_shared makes of the prefix on the current device (0: none)."""
     return _lib.rf_prefix_segments(int(B), int(H), int(Hkv), int(prefix))
 
 
 def rf_attn_decode_shared(q, kp, vp, k, v, lens, Sp, S, scale, seg_m, seg_l, seg_acc, counters,
                           out, lse=None, stream=None):
     """q [B, H, D]; kp/vp [Hkv, prefix, D] shared by the batch; k/v [B, Hkv, cap, D] with lens [B]
-    own keys -> out [B, H, D], lse [B, H].  Scratch as rf_attn_decode_window with Sp + S segments."""
-    B, H, Hkv, cap, D = _need_cache(q, k, v, lens)
+    own keys -> out [B, H, D], lse [B, H].  Scratch as rf_attn_decode_window with Sp + S pieces."""
+    B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if kp.dim() != 3:
         raise ValueError("kp must be [Hkv, prefix, D]")
     prefix = kp.shape[1]
-    _need(kp, q.dtype, "kp", (Hkv, prefix, D))
-    _need(vp, q.dtype, "vp", (Hkv, prefix, D))
-    _need_scratch(B, H, Hkv, D, Sp + S, seg_m, seg_l, seg_acc, counters, out, lse)
-    dev = _one_device(q, kp, vp, k, v, lens, seg_m, seg_l, seg_acc, counters, out, lse)
-    _call_on(dev, stream, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, _ptr(q), _ptr(kp),
-             _ptr(vp), prefix, _ptr(k), _ptr(v), _ptr(lens), B, H, Hkv, cap, D, int(Sp), int(S),
-             float(scale), _cache_dtype(q.dtype, "q"), _ptr(seg_m), _ptr(seg_l), _ptr(seg_acc),
-             _ptr(counters), _ptr(out), _cache_dtype(out.dtype, "out"), _ptr(lse))
+    _on(dev, kp, q.dtype, (Hkv, prefix, D), "kp")
+    _on(dev, vp, q.dtype, kp.shape, "vp")
+    _need_scratch(dev, B, H, Hkv, D, Sp + S, seg_m, seg_l, seg_acc, counters)
+    _on(dev, out, out.dtype, (B, H, D), "out")
+    if lse is not None:
+        _on(dev, lse, torch.float32, (B, H), "lse")
+    _call_on(dev, stream, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
+             kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B, H,
+             Hkv, cap, D, Sp, S, scale, _cache_dtype(q.dtype, "q"), seg_m.data_ptr(),
+             seg_l.data_ptr(), seg_acc.data_ptr(), counters.data_ptr(), out.data_ptr(),
+             _cache_dtype(out.dtype, "out"), _addr(lse))
 
 
 def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight_out, lens_out,
@@ -518,25 +548,26 @@ def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight
     [B, Hkv, cap_out], lens_out int32 [B], kept int32 [B, Hkv, keep]."""
     if k.dim() != 4 or k_out.dim() != 4:
         raise ValueError("k and k_out must be [B, Hkv, rows, D]")
+    dev = _device_of(k, "k")
     B, Hkv, cap, D = k.shape
     cap_out = k_out.shape[2]
-    _need(k, k.dtype, "k")
-    _need(k_out, k.dtype, "k_out", (B, Hkv, cap_out, D))
+    dt = k.dtype
+    _on(dev, k, dt, k.shape, "k")
+    _on(dev, k_out, dt, (B, Hkv, cap_out, D), "k_out")
     if v is not None:
-        _need(v, k.dtype, "v", (B, Hkv, cap, D))
+        _on(dev, v, dt, k.shape, "v")
     if v_out is not None:
-        _need(v_out, k.dtype, "v_out", (B, Hkv, cap_out, D))
-    _need(weight, torch.float32, "weight", (B, Hkv, cap))
-    _need(weight_out, torch.float32, "weight_out", (B, Hkv, cap_out))
+        _on(dev, v_out, dt, k_out.shape, "v_out")
+    _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
+    _on(dev, weight_out, torch.float32, (B, Hkv, cap_out), "weight_out")
     if lens is not None:
-        _need(lens, torch.int32, "lens", (B,))
-    _need(lens_out, torch.int32, "lens_out", (B,))
-    _need(kept, torch.int32, "kept", (B, Hkv, keep))
-    dev = _one_device(k, v, weight, lens, k_out, v_out, weight_out, lens_out, kept)
-    _call_on(dev, stream, "rf_cache_evict", _lib.rf_cache_evict, _ptr(k), _ptr(v), _ptr(weight),
-             _ptr(lens), B, Hkv, cap, D, _cache_dtype(k.dtype, "k"), int(keep), int(sinks),
-             int(recent), cap_out, _ptr(k_out), _ptr(v_out), _ptr(weight_out), _ptr(lens_out),
-             _ptr(kept))
+        _on(dev, lens, torch.int32, (B,), "lens")
+    _on(dev, lens_out, torch.int32, (B,), "lens_out")
+    _on(dev, kept, torch.int32, (B, Hkv, keep), "kept")
+    _call_on(dev, stream, "rf_cache_evict", _lib.rf_cache_evict, k.data_ptr(), _addr(v),
+             weight.data_ptr(), _addr(lens), B, Hkv, cap, D, _cache_dtype(dt, "k"), keep, sinks,
+             recent, cap_out, k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
+             lens_out.data_ptr(), kept.data_ptr())
 
 
 def rf_stream_read(x, out_xor, stream=None):
@@ -643,27 +674,33 @@ def attn_prefill(q, k, v, causal=True, scale=None, stream=None):
     return out, lse
 
 
-class DecodeWorkspace:
+class DecodeWorkspace(typing.NamedTuple):
     """Scratch of one decode call over a cache of grouped heads (decode_workspace makes it):
-    segment states, zeroed counters and, where asked for, a score per head and key.  A serving
-    loop keeps one per call that may be in flight at a time."""
+    states of up to ``prefix_S`` + ``S`` pieces per row, zeroed counters and, where asked for, a
+    score per head and key.  A serving loop keeps one per call that may be in flight at a time."""
+    S: int
+    prefix_S: int
+    seg_m: torch.Tensor
+    seg_l: torch.Tensor
+    seg_acc: torch.Tensor
+    counters: torch.Tensor
+    scores: torch.Tensor
+    sizes: tuple        # (device index, B, H, Hkv, D), and cap with scores
+    addresses: tuple    # of seg_m, seg_l, seg_acc, counters
 
-    def __init__(self, B, H, Hkv, D, S, prefix_S, cap, weights, device):
-        f32 = dict(device=device, dtype=torch.float32)
-        self.S, self.prefix_S = S, prefix_S
-        self.seg_m = torch.empty(B * H, S + prefix_S, **f32)
-        self.seg_l = torch.empty(B * H, S + prefix_S, **f32)
-        self.seg_acc = torch.empty(B * H, S + prefix_S, D, **f32)
-        self.counters = torch.zeros(B * Hkv * (-(-(H // Hkv) // 16)), device=device,
-                                    dtype=torch.int32)
-        self.scores = torch.empty(B, H, cap, **f32) if weights else None
+    def scratch(self, *sizes):
+        """The scratch addresses, for a call of these sizes."""
+        if sizes != self.sizes[:len(sizes)]:
+            raise ValueError(f"work was made for (device, B, H, Hkv, D, cap) = {self.sizes}, "
+                             f"the call has {sizes}")
+        return self.addresses
 
 
 def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights=False, S=None,
                      device=None):
     """Scratch for attn_decode_window (window, sinks as in the call), attn_decode_shared (the
-    prefix's length) or attn_decode_weights (weights=True), with the number of segments that
-    fills the device."""
+    prefix's length) or attn_decode_weights (weights=True).  S pieces per row (None: as many as
+    fill the device)."""
     if H < 1 or Hkv < 1 or H % Hkv:
         raise ValueError("H must be a positive multiple of Hkv")
     with torch.cuda.device(torch.device("cuda" if device is None else device)):
@@ -672,13 +709,28 @@ def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights
             keys = min(cap, window + sinks) if window else cap
             S = rf_decode_segments(B * Hkv * (-(-(H // Hkv) // 16)), keys)
         prefix_S = rf_prefix_segments(B, H, Hkv, prefix) if prefix else 0
-        return DecodeWorkspace(B, H, Hkv, D, S, prefix_S, cap, weights, dev)
+        f32 = dict(device=dev, dtype=torch.float32)
+        seg_m, seg_l = (torch.empty(B * H, prefix_S + S, **f32) for _ in range(2))
+        seg_acc = torch.empty(B * H, prefix_S + S, D, **f32)
+        counters = torch.zeros(B * Hkv * (-(-(H // Hkv) // 16)), device=dev, dtype=torch.int32)
+        scores = torch.empty(B, H, cap, **f32) if weights else None
+        return DecodeWorkspace(S, prefix_S, seg_m, seg_l, seg_acc, counters, scores,
+                               (dev.index, B, H, Hkv, D, cap if weights else None),
+                               tuple(t.data_ptr() for t in (seg_m, seg_l, seg_acc, counters)))
+
+
+_NO_STREAM = contextlib.nullcontext()
 
 
 def _on_stream(stream):
     """Allocations inside belong to ``stream`` (None: the current one), so that their memory is
     not handed out again while the stream still uses it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
+
+
+def _outputs(q, out_dtype):
+    out = torch.empty_like(q) if out_dtype is None else torch.empty_like(q, dtype=out_dtype)
+    return out, torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
 
 
 def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=None,
@@ -688,16 +740,16 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
     q [B, H, D], k/v [B, Hkv, cap, D] (bf16 or fp16), lens int32 [B] (None: all cap rows in use).
     Key j is visible if it is one of the last ``window`` (0: all) or of the first ``sinks``.
     Returns out [B, H, D] and lse [B, H]; ``work`` from decode_workspace saves its allocation."""
-    B, H, D = q.shape
+    B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     with _on_stream(stream):
         if work is None:
-            work = decode_workspace(B, H, k.shape[1], k.shape[2], D, window=window, sinks=sinks,
-                                    device=q.device)
-        out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
-        lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
-        rf_attn_decode_window(q, k, v, lens, window, sinks, work.S,
-                              D ** -0.5 if scale is None else scale, work.seg_m, work.seg_l,
-                              work.seg_acc, work.counters, out, lse, stream)
+            work = decode_workspace(B, H, Hkv, cap, D, window=window, sinks=sinks, device=q.device)
+        m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
+        out, lse = _outputs(q, out_dtype)
+        _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
+                 k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, work.S,
+                 D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
+                 counters, out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
 
@@ -707,8 +759,7 @@ def attn_prefill_window(q, k, v, window=0, sinks=0, scale=None, stream=None):
 
     q [B, H, N, D], k/v [B, Hkv, L, D] (bf16 or fp16).  Returns out [B, H, N, D] and lse [B, H, N]."""
     with _on_stream(stream):
-        out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:-1], device=q.device, dtype=torch.float32)
+        out, lse = _outputs(q, None)
         rf_attn_prefill_window(q, k, v, window, sinks, q.shape[-1] ** -0.5 if scale is None else scale,
                                out, lse, stream)
     return out, lse
@@ -720,16 +771,22 @@ def attn_decode_shared(q, kp, vp, k, v, lens=None, scale=None, work=None, out_dt
 
     q [B, H, D]; kp/vp [Hkv, prefix, D]; k/v [B, Hkv, cap, D] with lens [B] own keys behind the
     prefix (None: cap; 0 allowed).  Returns out [B, H, D] and lse [B, H]."""
-    B, H, D = q.shape
+    B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
+    if kp.dim() != 3:
+        raise ValueError("kp must be [Hkv, prefix, D]")
+    prefix = kp.shape[1]
+    _on(dev, kp, q.dtype, (Hkv, prefix, D), "kp")
+    _on(dev, vp, q.dtype, kp.shape, "vp")
     with _on_stream(stream):
         if work is None:
-            work = decode_workspace(B, H, k.shape[1], k.shape[2], D, prefix=kp.shape[1],
-                                    device=q.device)
-        out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
-        lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
-        rf_attn_decode_shared(q, kp, vp, k, v, lens, work.prefix_S, work.S,
-                              D ** -0.5 if scale is None else scale, work.seg_m, work.seg_l,
-                              work.seg_acc, work.counters, out, lse, stream)
+            work = decode_workspace(B, H, Hkv, cap, D, prefix=prefix, device=q.device)
+        m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
+        out, lse = _outputs(q, out_dtype)
+        _call_on(dev, stream, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
+                 kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B,
+                 H, Hkv, cap, D, work.prefix_S, work.S, D ** -0.5 if scale is None else scale,
+                 _cache_dtype(q.dtype, "q"), m, l, acc, counters, out.data_ptr(),
+                 _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
 
@@ -740,20 +797,24 @@ def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, 
     Returns out [B, H, D], lse [B, H] and weight_out [B, Hkv, cap] = weight (None: 0) plus the
     softmax weights of this token, summed over each key head's query heads; ``weight_out`` may be
     ``weight`` itself."""
-    B, H, D = q.shape
+    B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
+    if weight is not None:
+        _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
     with _on_stream(stream):
         if work is None:
-            work = decode_workspace(B, H, k.shape[1], k.shape[2], D, weights=True, device=q.device)
-        if work.scores is None:
-            raise ValueError("work must come from decode_workspace(..., weights=True)")
-        out = torch.empty(B, H, D, device=q.device, dtype=out_dtype or q.dtype)
-        lse = torch.empty(B, H, device=q.device, dtype=torch.float32)
+            work = decode_workspace(B, H, Hkv, cap, D, weights=True, device=q.device)
+        m, l, acc, counters = work.scratch(dev, B, H, Hkv, D, cap)
+        out, lse = _outputs(q, out_dtype)
         if weight_out is None:
-            weight_out = torch.empty(B, k.shape[1], k.shape[2], device=q.device,
-                                     dtype=torch.float32)
-        rf_attn_decode_weights(q, k, v, lens, work.S, D ** -0.5 if scale is None else scale,
-                               work.seg_m, work.seg_l, work.seg_acc, work.counters, work.scores,
-                               out, lse, weight, weight_out, stream)
+            weight_out = torch.empty((B, Hkv, cap), device=q.device, dtype=torch.float32)
+        else:
+            _on(dev, weight_out, torch.float32, (B, Hkv, cap), "weight_out")
+        _call_on(dev, stream, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
+                 k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, work.S,
+                 D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
+                 counters, work.scores.data_ptr(), out.data_ptr(),
+                 _cache_dtype(out.dtype, "out"), lse.data_ptr(), _addr(weight),
+                 weight_out.data_ptr())
     return out, lse, weight_out
 
 

@@ -170,3 +170,18 @@ def test_shared_refusals(lib):
 def test_prefix_segments_refuses_bad_sizes(lib):
     for a in ((0, 8, 2, 10), (2, 7, 2, 10), (2, 8, 2, 0), (2, 129, 1, 10), (-1, 8, 2, 10)):
         assert lib.rf_prefix_segments(*a) == 0
+
+
+# ------------------------------------------------ refusals of the Python layer --
+
+def test_python_layer_refuses_cpu_tensors_and_bad_shapes():
+    import torch
+    import cascaded_reductions_gb300 as rf
+    q, k = torch.zeros(2, 8, 128, dtype=torch.bfloat16), torch.zeros(2, 2, 10, 128, dtype=torch.bfloat16)
+    w = torch.zeros(2, 2, 10)
+    for call in (lambda: rf.attn_decode_window(q, k, k), lambda: rf.attn_decode_weights(q, k, k),
+                 lambda: rf.attn_decode_shared(q, k[0], k[0], k, k),
+                 lambda: rf.attn_prefill_window(k, k, k), lambda: rf.cache_evict(k, k, w, None, 5),
+                 lambda: rf.attn_decode_window(q[0], k, k), lambda: rf.decode_workspace(2, 7, 2, 10)):
+        with pytest.raises(ValueError):
+            call()

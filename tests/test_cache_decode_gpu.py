@@ -224,3 +224,24 @@ def test_on_another_stream(rf):
     out, lse = rf.attn_decode_window(q, k, v, n, scale=SCALE, stream=st)
     st.synchronize()
     check_decode(out, lse, q, k, v, lens, SCALE)
+
+
+def test_python_layer_refusals(rf):
+    q, k, v, n = make(60, 2, 8, 2, 50, [50, 3], 0, 0, torch.bfloat16)
+    work = rf.decode_workspace(2, 8, 2, 50)
+    for bad in (lambda: rf.attn_decode_window(q, k.transpose(1, 2), v, n),          # not contiguous
+                lambda: rf.attn_decode_window(q, k.half(), v, n),                   # another type
+                lambda: rf.attn_decode_window(q, k, v[:, :, :40].contiguous(), n),  # another shape
+                lambda: rf.attn_decode_window(q, k, v, n.long()),
+                lambda: rf.attn_decode_window(q, k, v, n.cpu()),
+                lambda: rf.attn_decode_window(q[:1].contiguous(), k[:1].contiguous(),
+                                              v[:1].contiguous(), n[:1].contiguous(), work=work),
+                lambda: rf.attn_decode_weights(q, k, v, n, work=work)):             # no scores in it
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: rf.attn_decode_window(q, k, v, n, window=-1),
+                lambda: rf.attn_decode_window(q, k, v, n, out_dtype=torch.float16),
+                lambda: rf.attn_decode_window(q[..., :64].contiguous(), k[..., :64].contiguous(),
+                                              v[..., :64].contiguous(), n)):
+        with pytest.raises(rf.RFError):
+            bad()

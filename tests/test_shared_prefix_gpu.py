@@ -58,16 +58,17 @@ def test_batches_and_head_groups(rf, B, H, Hkv):
 def test_segment_counts(rf, Sp, S):
     lens = [300, 0, 77]
     args = make(Sp, 3, 8, 2, 5000, 300, lens, torch.bfloat16)
-    work = rf.decode_workspace(3, 8, 2, 300, S=S)
-    work.prefix_S = Sp
-    f32 = dict(device="cuda", dtype=torch.float32)
+    q, kp, vp, k, v, n = args
     # whatever the scratch held before must not show
-    work.seg_m = torch.full((24, Sp + S), float("nan"), **f32)
-    work.seg_l = torch.full((24, Sp + S), float("nan"), **f32)
-    work.seg_acc = torch.full((24, Sp + S, 128), float("nan"), **f32)
+    f32 = dict(device="cuda", dtype=torch.float32)
+    m, l = (torch.full((24, Sp + S), float("nan"), **f32) for _ in range(2))
+    acc = torch.full((24, Sp + S, 128), float("nan"), **f32)
+    counters = torch.zeros(6, device="cuda", dtype=torch.int32)
     for _ in range(2):
-        check(rf, args, lens, work)
-    assert torch.all(work.counters == 0)
+        out, lse = torch.empty_like(q), torch.empty(3, 8, **f32)
+        rf.rf_attn_decode_shared(q, kp, vp, k, v, n, Sp, S, SCALE, m, l, acc, counters, out, lse)
+        check_decode(out, lse, q, k, v, lens, SCALE, kp=kp, vp=vp, p_step=2.0 ** -8)
+    assert torch.all(counters == 0)
 
 
 def test_long_prefix_and_fp32_output(rf):
