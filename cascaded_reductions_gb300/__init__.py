@@ -17,7 +17,6 @@ instead, e.g. the bounds-checked debug variant that
 ``cascaded_reductions_gb300._build.build_checked()`` makes.
 """
 
-import contextlib
 import ctypes
 import os
 import typing
@@ -719,13 +718,13 @@ def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights
                                tuple(t.data_ptr() for t in (seg_m, seg_l, seg_acc, counters)))
 
 
-_NO_STREAM = contextlib.nullcontext()
-
-
-def _on_stream(stream):
-    """Allocations inside belong to ``stream`` (None: the current one), so that their memory is
-    not handed out again while the stream still uses it."""
-    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
+def _within(stream, t, call, *args, **kwargs):
+    """call(*args, **kwargs) with ``stream`` current, so that what it allocates belongs to that
+    stream and is not handed out again while the stream still uses it."""
+    if stream.device != t.device:
+        raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
 
 
 def _outputs(q, out_dtype):
@@ -740,16 +739,18 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
     q [B, H, D], k/v [B, Hkv, cap, D] (bf16 or fp16), lens int32 [B] (None: all cap rows in use).
     Key j is visible if it is one of the last ``window`` (0: all) or of the first ``sinks``.
     Returns out [B, H, D] and lse [B, H]; ``work`` from decode_workspace saves its allocation."""
+    if stream is not None:
+        return _within(stream, q, attn_decode_window, q, k, v, lens, window, sinks, scale, work,
+                       out_dtype)
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
-    with _on_stream(stream):
-        if work is None:
-            work = decode_workspace(B, H, Hkv, cap, D, window=window, sinks=sinks, device=q.device)
-        m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
-        out, lse = _outputs(q, out_dtype)
-        _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
-                 k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, work.S,
-                 D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
-                 counters, out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
+    if work is None:
+        work = decode_workspace(B, H, Hkv, cap, D, window=window, sinks=sinks, device=q.device)
+    m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
+    out, lse = _outputs(q, out_dtype)
+    _call_on(dev, None, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, work.S,
+             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
+             counters, out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
 
@@ -758,10 +759,11 @@ def attn_prefill_window(q, k, v, window=0, sinks=0, scale=None, stream=None):
     up to the position itself (0: all) or one of the first ``sinks``.
 
     q [B, H, N, D], k/v [B, Hkv, L, D] (bf16 or fp16).  Returns out [B, H, N, D] and lse [B, H, N]."""
-    with _on_stream(stream):
-        out, lse = _outputs(q, None)
-        rf_attn_prefill_window(q, k, v, window, sinks, q.shape[-1] ** -0.5 if scale is None else scale,
-                               out, lse, stream)
+    if stream is not None:
+        return _within(stream, q, attn_prefill_window, q, k, v, window, sinks, scale)
+    out, lse = _outputs(q, None)
+    rf_attn_prefill_window(q, k, v, window, sinks, q.shape[-1] ** -0.5 if scale is None else scale,
+                           out, lse)
     return out, lse
 
 
@@ -771,22 +773,23 @@ def attn_decode_shared(q, kp, vp, k, v, lens=None, scale=None, work=None, out_dt
 
     q [B, H, D]; kp/vp [Hkv, prefix, D]; k/v [B, Hkv, cap, D] with lens [B] own keys behind the
     prefix (None: cap; 0 allowed).  Returns out [B, H, D] and lse [B, H]."""
+    if stream is not None:
+        return _within(stream, q, attn_decode_shared, q, kp, vp, k, v, lens, scale, work, out_dtype)
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if kp.dim() != 3:
         raise ValueError("kp must be [Hkv, prefix, D]")
     prefix = kp.shape[1]
     _on(dev, kp, q.dtype, (Hkv, prefix, D), "kp")
     _on(dev, vp, q.dtype, kp.shape, "vp")
-    with _on_stream(stream):
-        if work is None:
-            work = decode_workspace(B, H, Hkv, cap, D, prefix=prefix, device=q.device)
-        m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
-        out, lse = _outputs(q, out_dtype)
-        _call_on(dev, stream, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
-                 kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B,
-                 H, Hkv, cap, D, work.prefix_S, work.S, D ** -0.5 if scale is None else scale,
-                 _cache_dtype(q.dtype, "q"), m, l, acc, counters, out.data_ptr(),
-                 _cache_dtype(out.dtype, "out"), lse.data_ptr())
+    if work is None:
+        work = decode_workspace(B, H, Hkv, cap, D, prefix=prefix, device=q.device)
+    m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
+    out, lse = _outputs(q, out_dtype)
+    _call_on(dev, None, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
+             kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B,
+             H, Hkv, cap, D, work.prefix_S, work.S, D ** -0.5 if scale is None else scale,
+             _cache_dtype(q.dtype, "q"), m, l, acc, counters, out.data_ptr(),
+             _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
 
@@ -797,24 +800,26 @@ def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, 
     Returns out [B, H, D], lse [B, H] and weight_out [B, Hkv, cap] = weight (None: 0) plus the
     softmax weights of this token, summed over each key head's query heads; ``weight_out`` may be
     ``weight`` itself."""
+    if stream is not None:
+        return _within(stream, q, attn_decode_weights, q, k, v, lens, weight, scale, work, weight_out,
+                       out_dtype)
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if weight is not None:
         _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
-    with _on_stream(stream):
-        if work is None:
-            work = decode_workspace(B, H, Hkv, cap, D, weights=True, device=q.device)
-        m, l, acc, counters = work.scratch(dev, B, H, Hkv, D, cap)
-        out, lse = _outputs(q, out_dtype)
-        if weight_out is None:
-            weight_out = torch.empty((B, Hkv, cap), device=q.device, dtype=torch.float32)
-        else:
-            _on(dev, weight_out, torch.float32, (B, Hkv, cap), "weight_out")
-        _call_on(dev, stream, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
-                 k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, work.S,
-                 D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
-                 counters, work.scores.data_ptr(), out.data_ptr(),
-                 _cache_dtype(out.dtype, "out"), lse.data_ptr(), _addr(weight),
-                 weight_out.data_ptr())
+    if work is None:
+        work = decode_workspace(B, H, Hkv, cap, D, weights=True, device=q.device)
+    m, l, acc, counters = work.scratch(dev, B, H, Hkv, D, cap)
+    out, lse = _outputs(q, out_dtype)
+    if weight_out is None:
+        weight_out = torch.empty((B, Hkv, cap), device=q.device, dtype=torch.float32)
+    else:
+        _on(dev, weight_out, torch.float32, (B, Hkv, cap), "weight_out")
+    _call_on(dev, None, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, work.S,
+             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
+             counters, work.scores.data_ptr(), out.data_ptr(),
+             _cache_dtype(out.dtype, "out"), lse.data_ptr(), _addr(weight),
+             weight_out.data_ptr())
     return out, lse, weight_out
 
 
@@ -825,15 +830,16 @@ def cache_evict(k, v, weight, lens, keep, sinks=0, recent=0, cap_out=None, out=N
     k/v [B, Hkv, cap, D] (v may be None), weight [B, Hkv, cap], lens int32 [B] or None.  Returns
     k_out, v_out, weight_out (``out`` if given, else new zeroed tensors of cap_out = keep rows by
     default), lens_out [B] and kept [B, Hkv, keep] (source rows, -1 behind a short sequence)."""
+    if stream is not None:
+        return _within(stream, k, cache_evict, k, v, weight, lens, keep, sinks, recent, cap_out, out)
     B, Hkv, cap, D = k.shape
     dev = k.device
-    with _on_stream(stream):
-        if out is None:
-            rows = keep if cap_out is None else cap_out
-            out = (torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
-                   None if v is None else torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
-                   torch.zeros(B, Hkv, rows, device=dev, dtype=torch.float32))
-        lens_out = torch.empty(B, device=dev, dtype=torch.int32)
-        kept = torch.empty(B, Hkv, keep, device=dev, dtype=torch.int32)
-        rf_cache_evict(k, v, weight, lens, keep, sinks, recent, *out, lens_out, kept, stream)
+    if out is None:
+        rows = keep if cap_out is None else cap_out
+        out = (torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
+               None if v is None else torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
+               torch.zeros(B, Hkv, rows, device=dev, dtype=torch.float32))
+    lens_out = torch.empty(B, device=dev, dtype=torch.int32)
+    kept = torch.empty(B, Hkv, keep, device=dev, dtype=torch.int32)
+    rf_cache_evict(k, v, weight, lens, keep, sinks, recent, *out, lens_out, kept)
     return (*out, lens_out, kept)

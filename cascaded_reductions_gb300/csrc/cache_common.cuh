@@ -48,10 +48,10 @@ inline rf_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned
 // call, enough to pay for a CTA's start and end in a large one.
 constexpr int kFewKeys = 4 * kDecodeTile, kManyKeys = 768;
 
-// Whether a call of `groups` row groups of up to `keys` visible keys is small:
-// at most four steps of 64 keys for each of two CTAs per SM.
+// Whether a call of `groups` row groups of up to `keys` visible keys is small: its
+// pieces fit two CTAs on every SM, at most four steps of 64 keys each.
 inline bool decode_is_few(long long groups, int keys, int sms) {
-  return groups * ((keys + kFewKeys - 1) / kFewKeys) <= 8ll * sms;
+  return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= 8ll * sms;
 }
 
 // Pieces per row for such a call: a small one is divided until two CTAs per SM

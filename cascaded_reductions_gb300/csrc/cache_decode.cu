@@ -59,9 +59,20 @@ constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int MROWS = 16;               // query heads per row group
 constexpr size_t SMEM_BYTES = (size_t)WARPS * RING_BYTES;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+// 16 bytes (or, for bytes = 0, zeros) with an L2 eviction policy
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes,
+                                           uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(bytes), "l"(policy)
                : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy(bool evict_first) {
+  uint64_t p;
+  if (evict_first)
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -167,7 +178,7 @@ __device__ __forceinline__ Rows rows_of(const CacheDecode& a, int g) {
 // then V rows, 16-byte chunks permuted by row % 8 so that ldmatrix meets all
 // banks; two rows per instruction.
 __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, int t0, uint32_t stage,
-                                          int lane) {
+                                          uint64_t policy, int lane) {
 #pragma unroll
   for (int u = 0; u < TK / 2; ++u) {
     const int r = 2 * u + (lane >> 4), c = lane & 15;
@@ -176,8 +187,8 @@ __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, 
     const bool in = t < q.n && RF_IDX_OK(q.kv0 + key, (size_t)a.B * a.Hkv * a.cap);
     const size_t off = (q.kv0 + (in ? key : 0)) * ROW_BYTES + c * 16;
     const uint32_t dst = stage + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
-    cp_async16(dst, a.k + off, in ? 16u : 0u);
-    cp_async16(dst + TK * ROW_BYTES, a.v + off, in ? 16u : 0u);
+    cp_async16(dst, a.k + off, in ? 16u : 0u, policy);
+    cp_async16(dst + TK * ROW_BYTES, a.v + off, in ? 16u : 0u, policy);
   }
 }
 
@@ -234,14 +245,28 @@ struct State {
       s[nt][2 + e] = in ? s[nt][2 + e] * a.scale_log2 : -INFINITY;
       mx0 = fmaxf(mx0, s[nt][e]);
       mx1 = fmaxf(mx1, s[nt][2 + e]);
-      if constexpr (SCORES) {
-        const int r = lane >> 2;
-        if (in && r < w.n && RF_IDX_OK((w.row0 + r) * a.cap + t, (size_t)a.B * a.H * a.cap))
-          a.scores[(w.row0 + r) * a.cap + t] = s[nt][e];
-        if (in && r + 8 < w.n && RF_IDX_OK((w.row0 + r + 8) * a.cap + t, (size_t)a.B * a.H * a.cap))
-          a.scores[(w.row0 + r + 8) * a.cap + t] = s[nt][2 + e];
+    }
+  if constexpr (SCORES) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int t = t0 + nt * 8 + 2 * (lane & 3);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = (lane >> 2) + 8 * half;
+        if (r >= w.n || t >= n) continue;
+        float* at = a.scores + (w.row0 + r) * a.cap + t;
+        const size_t i = (w.row0 + r) * a.cap + t, all = (size_t)a.B * a.H * a.cap;
+        (void)i, (void)all;                       // read by the checked build only
+        if (t + 1 < n && a.cap % 2 == 0) {        // t is even, and so the pair is aligned
+          if (RF_SPAN_OK(i, 2, all))
+            *reinterpret_cast<float2*>(at) = make_float2(s[nt][2 * half], s[nt][2 * half + 1]);
+        } else {
+          if (RF_IDX_OK(i, all)) at[0] = s[nt][2 * half];
+          if (t + 1 < n && RF_IDX_OK(i + 1, all)) at[1] = s[nt][2 * half + 1];
+        }
       }
     }
+  }
   mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
   mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
   mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
@@ -453,10 +478,13 @@ cache_decode_kernel(const CacheDecode a) {
   const int k1 = (int)((long long)steps * (piece + 1) / pieces);
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * RING_BYTES;
 
+  // a large call's cache passes through L2 once; what it leaves there for the
+  // next kernel (states, scores) stays
+  const uint64_t policy = l2_policy(!FUSED);
   int in = 0;                           // the stage that the next copies go to
   auto issue = [&](int k) {
     const int t0 = (k * WARPS + warp) * TK;
-    if (k < k1 && t0 < q.n) copy_tile(a, q, t0, ring + (uint32_t)in * STAGE_BYTES, lane);
+    if (k < k1 && t0 < q.n) copy_tile(a, q, t0, ring + (uint32_t)in * STAGE_BYTES, policy, lane);
     cp_async_commit();
     in = in + 1 == STAGES ? 0 : in + 1;
   };
@@ -537,28 +565,44 @@ cache_decode_kernel(const CacheDecode a) {
   }
 }
 
-// One warp per group: merges the rows of divided groups.
-template <bool SCORES>
+// Merges the rows of divided groups: with few states per row a warp per group,
+// four rows at a time (4096 rows of 7 states: 94 us of a whole shared-prefix
+// step, 99 us with a warp per row), with many a warp per row (1024 rows of 22:
+// 225 us of a weight-totalling step, 232 us with a warp per group).
+template <bool SCORES, bool BY_ROW>
 __global__ void __launch_bounds__(WARPS * 32)
 merge_kernel(const CacheDecode a) {
-  const int g = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const bool in = unit < (BY_ROW ? (long long)a.B * a.H : (long long)a.B * a.Hkv * a.mtiles);
   allow_dependents();
-  const int pieces = g < a.B * a.Hkv * a.mtiles ? pieces_of(a, group_of(a, g).n) : 1;
+  Rows w = {0, 0};
+  int pieces = 1;
+  if (in) {
+    int g = (int)unit;
+    if (BY_ROW) {
+      const int b = (int)(unit / a.H), h = (int)(unit - (long long)b * a.H);
+      g = (b * a.Hkv + h / a.G) * a.mtiles;
+    }
+    pieces = pieces_of(a, group_of(a, g).n);
+    w = BY_ROW ? Rows{(size_t)unit, 1} : rows_of(a, g);
+  }
   wait_prerequisite();
-  if (g >= a.B * a.Hkv * a.mtiles) return;
-  if (pieces == 1 && a.seg0 == 0) return;        // written by its CTA
-  const Rows w = rows_of(a, g);
-  merge_rows<4, SCORES>(a, w.row0, w.n, pieces, lane);
+  if (!in || (pieces == 1 && a.seg0 == 0)) return;   // written by its CTA
+  merge_rows<BY_ROW ? 1 : 4, SCORES>(a, w.row0, w.n, pieces, lane);
 }
 
 // total[j] = weight[j] + sum over the group's heads of exp2(score - lse2):
 // the weights of the row's softmax, each below 1, summed in fp32 head by head
-// in order.  One thread per key; reads 4 (G + 1) bytes and writes 4 per key.
+// in order.  KEYS adjacent keys per thread (4: 16-byte accesses, for rows that
+// stay aligned); reads 4 (G + 1) bytes and writes 4 per key.
+template <int KEYS>
 __global__ void __launch_bounds__(256)
-add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __restrict__ lens, const float* weight, float* total, int B,
-                   int Hkv, int G, int cap, int S, int blocks) {
+add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __restrict__ lens,
+                   const float* weight, float* total, int B, int Hkv, int G, int cap, int S,
+                   int blocks) {
   const int group = blockIdx.x / blocks;
-  const int j = (blockIdx.x - group * blocks) * 256 + threadIdx.x;
+  const int j = ((blockIdx.x - group * blocks) * 256 + threadIdx.x) * KEYS;
   const int b = group / Hkv;
   const size_t row0 = (size_t)group * G;                          // b * H + key head * G
   int len = cap;
@@ -566,20 +610,36 @@ add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __res
   wait_prerequisite();
   if (j >= cap) return;
   const size_t i = (size_t)group * cap + j;
-  if (!RF_IDX_OK(i, (size_t)B * Hkv * cap)) return;
-  float w = weight != nullptr ? weight[i] : 0.f;
+  if (!RF_SPAN_OK(i, KEYS, (size_t)B * Hkv * cap)) return;
+  if (j >= len && weight == total) return;        // behind the end: left as it was
+  float w[KEYS] = {};
+  if (weight != nullptr) {
+    if constexpr (KEYS == 4)
+      *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(weight + i);
+    else
+      w[0] = weight[i];
+  }
   if (j < len) {
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
-      if (!RF_IDX_OK((row0 + g) * cap + j, (size_t)B * Hkv * G * cap)) continue;
+      const size_t at = (row0 + g) * cap + j;
+      if (!RF_SPAN_OK(at, KEYS, (size_t)B * Hkv * G * cap)) continue;
       const float z = __ldcg(seg_m + (row0 + g) * S);
-      const float x = __ldcs(scores + (row0 + g) * cap + j);
-      w += z == -INFINITY ? 0.f : exp2f(x - z);   // a row without weight adds none
+      if (z == -INFINITY) continue;               // a row without weight adds none
+      float x[KEYS];
+      if constexpr (KEYS == 4)
+        *reinterpret_cast<float4*>(x) = __ldcs(reinterpret_cast<const float4*>(scores + at));
+      else
+        x[0] = __ldcs(scores + at);
+#pragma unroll
+      for (int e = 0; e < KEYS; ++e)
+        if (j + e < len) w[e] += exp2f(x[e] - z);
     }
-  } else if (weight == total) {
-    return;                                       // behind the end: left as it was
   }
-  total[i] = w;
+  if constexpr (KEYS == 4)
+    *reinterpret_cast<float4*>(total + i) = *reinterpret_cast<const float4*>(w);
+  else
+    total[i] = w[0];
 }
 
 template <bool F16, bool SCORES>
@@ -597,7 +657,10 @@ rf_status launch_t(const CacheDecode& a, bool few, cudaStream_t st) {
     s = launch_status();
   }
   if (s != RF_OK || few || (a.S == 1 && a.seg0 == 0)) return s;
-  return launch_after(merge_kernel<SCORES>, (groups + WARPS - 1) / WARPS, WARPS * 32, 0, st, a);
+  if (a.seg0 + a.S <= 8)
+    return launch_after(merge_kernel<SCORES, false>, (groups + WARPS - 1) / WARPS, WARPS * 32, 0, st, a);
+  const unsigned rows = (unsigned)(((long long)a.B * a.H + WARPS - 1) / WARPS);
+  return launch_after(merge_kernel<SCORES, true>, rows, WARPS * 32, 0, st, a);
 }
 
 }  // namespace
@@ -620,11 +683,17 @@ rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st) {
 
 rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* total,
                              cudaStream_t st) {
-  const int blocks = (a.cap + 255) / 256;
+  // four keys per thread only where that leaves threads enough: 16384 keys took
+  // 5.8 us so, and 3.6 us with one
+  const bool wide = (long long)a.B * a.Hkv * a.cap >= (1 << 19) && a.cap % 4 == 0 && aligned16(a.scores) &&
+                    aligned16(weight) && aligned16(total);
+  const int keys = wide ? 1024 : 256;             // of a CTA
+  const int blocks = (a.cap + keys - 1) / keys;
   const long long grid = (long long)a.B * a.Hkv * blocks;
   if (grid > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
-  return launch_after(add_weights_kernel, (unsigned)grid, 256, 0, st, a.scores, a.seg_m, a.lens, weight,
-                      total, a.B, a.Hkv, a.H / a.Hkv, a.cap, a.S_total, blocks);
+  return launch_after(wide ? add_weights_kernel<4> : add_weights_kernel<1>, (unsigned)grid, 256, 0, st,
+                      a.scores, a.seg_m, a.lens, weight, total, a.B, a.Hkv, a.H / a.Hkv, a.cap,
+                      a.S_total, blocks);
 }
 
 RF_BOUNDS_WORD_OF_THIS_FILE

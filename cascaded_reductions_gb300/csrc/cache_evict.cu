@@ -8,15 +8,17 @@
 //
 // evict_select_kernel, one CTA per (sequence, key head): weights become
 // 32-bit keys whose unsigned order is the weights' order (NaN lowest, -0 as
-// +0), the need-th largest is found digit by digit (four histograms of 8
-// bits), and the compaction needs two sweeps with warp votes: the number kept
+// +0).  The need-th largest is found digit by digit, 11, 11 and 10 bits: one
+// histogram over all keys, then two over the few that share its threshold's
+// first digit, which are gathered for it (all keys again if there are more
+// than 4096).  The compaction needs two sweeps with warp votes: the number kept
 // before a row is  above_before + min(equal_before, equal_needed),  so ties go
 // to the lowest index without a second selection.  Weights are read from
 // memory once and kept in shared memory (up to 48 Ki of them; longer rows are
-// read again from L2).
+// read again from L2).  Four 8-bit histograms over all keys, one add per
+// distinct digit of a warp, took 44 us for 256 rows of 16384, this takes 26 us.
 //
-// evict_copy_kernel, bound by HBM (each kept row is read and written once):
-// 16-byte streaming copies, eight in flight per lane.
+// evict_copy_kernel, bound by HBM: each kept row is read and written once.
 
 #include "cache_common.cuh"
 
@@ -26,6 +28,8 @@ namespace {
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_KEYS = 48 * 1024;              // keys that fit in shared memory
+constexpr int SEL_BINS = 2048;
+constexpr int SEL_LIST = 4096;                   // keys gathered for the second and third digit
 
 // unsigned order = weight order; NaN ranks below every number
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -45,8 +49,8 @@ struct Evict {
 __global__ void __launch_bounds__(SEL_THREADS)
 evict_select_kernel(const Evict a) {
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sh_prefix, sh_need;
+  __shared__ uint32_t hist[SEL_BINS], list[SEL_LIST], warp_sum[SEL_WARPS];
+  __shared__ uint32_t sh_digit, sh_need, sh_count, sh_listed;
   __shared__ int above[SEL_WARPS], equal[SEL_WARPS];
 
   allow_dependents();
@@ -81,59 +85,75 @@ evict_select_kernel(const Evict a) {
     return RF_IDX_OK(w0 + i, weights) ? order_key(a.weight[w0 + i]) : 0u;
   };
   auto key = [&](int i) -> uint32_t { return in_smem ? keys[i] : load(i); };
-  if (in_smem)
-    for (int i = tid; i < n; i += SEL_THREADS) keys[i] = load(i);
 
-  // the need-th largest key, eight bits at a time from the top
-  uint32_t prefix = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int i0 = 0; i0 < n; i0 += SEL_THREADS) {
-        const int i = i0 + tid;
-        bool in = i < n;
-        uint32_t k = 0;
-        if (in) k = key(i);
-        if (shift < 24) in = in && (k >> (shift + 8)) == (prefix >> (shift + 8));
-        const uint32_t digit = in ? (k >> shift) & 255u : 256u;
-        // one add per distinct digit of the warp: weights share exponents
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(peers));
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane l holds bins 8 l .. 8 l + 7; find the bin where the count from
-        // the top reaches need
-        uint32_t mine = 0;
-        for (int e = 0; e < 8; ++e) mine += hist[8 * lane + e];
-        uint32_t from_top = mine;                // sum over lanes >= this one
+  // Adds up hist[] and finds the digit at which the count from the top reaches
+  // `need`: what is still needed of that digit's keys, and how many there are.
+  auto pick_digit = [&]() {
+    __syncthreads();
+    // thread t holds the bins 2047 - 2 t and 2046 - 2 t
+    const uint32_t hi = hist[SEL_BINS - 1 - 2 * tid], lo = hist[SEL_BINS - 2 - 2 * tid];
+    uint32_t upto = hi + lo;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_down_sync(0xffffffffu, from_top, o);
-          if (lane + o < 32) from_top += x;
-        }
-        uint32_t before = from_top - mine;
-        if (before < (uint32_t)need && from_top >= (uint32_t)need) {
-          for (int e = 7; e >= 0; --e) {
-            const uint32_t h = hist[8 * lane + e];
-            if (before + h >= (uint32_t)need) {
-              sh_prefix = prefix | ((uint32_t)(8 * lane + e) << shift);
-              sh_need = (uint32_t)need - before;
-              break;
-            }
-            before += h;
-          }
-        }
-      }
-      __syncthreads();
-      prefix = sh_prefix;
-      need = (int)sh_need;
-      __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
     }
-  } else {
-    prefix = 0xffffffffu;                        // no weight's key: none is kept
-    need = 0;
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    uint32_t before = lane < warp ? warp_sum[lane] : 0u;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    upto += before;
+    before = upto - hi - lo;
+    const uint32_t want = (uint32_t)need;
+    if (before < want && upto >= want) {
+      const bool first_bin = before + hi >= want;
+      sh_digit = (uint32_t)(SEL_BINS - 1 - 2 * tid) - (first_bin ? 0u : 1u);
+      sh_need = want - before - (first_bin ? 0u : hi);
+      sh_count = first_bin ? hi : lo;
+    }
+    __syncthreads();
+    need = (int)sh_need;
+  };
+  auto clear = [&]() {
+    hist[tid] = 0;
+    hist[tid + SEL_THREADS] = 0;
+    __syncthreads();
+  };
+  static_assert(SEL_BINS == 2 * SEL_THREADS, "two bins per thread");
+
+  uint32_t prefix = 0xffffffffu;                 // no weight's key: none is kept
+  if (need > 0) {
+    if (tid == 0) sh_listed = 0;
+    clear();
+    for (int i = tid; i < n; i += SEL_THREADS) {
+      const uint32_t k = load(i);
+      if (in_smem) keys[i] = k;
+      atomicAdd(&hist[k >> 21], 1u);
+    }
+    pick_digit();
+    prefix = sh_digit << 21;
+    const bool listed = sh_count <= SEL_LIST;
+    if (listed) {
+      for (int i = tid; i < n; i += SEL_THREADS) {
+        const uint32_t k = key(i);
+        if (k >> 21 == prefix >> 21) list[atomicAdd(&sh_listed, 1u)] = k;
+      }
+    }
+    const int m = listed ? (int)sh_count : n;
+    for (int shift = 10; shift >= 0; shift -= 10) {
+      const int bits = shift == 10 ? 11 : 10;    // 20 .. 10, then 9 .. 0
+      clear();
+      for (int i = tid; i < m; i += SEL_THREADS) {
+        const uint32_t k = listed ? list[i] : key(i);
+        if (k >> (shift + bits) == prefix >> (shift + bits))
+          atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      pick_digit();
+      prefix |= sh_digit << shift;
+    }
+  } else if (in_smem) {
+    for (int i = tid; i < n; i += SEL_THREADS) keys[i] = load(i);
   }
   __syncthreads();
 
@@ -177,57 +197,59 @@ evict_select_kernel(const Evict a) {
     if (RF_IDX_OK(slot0 + tail + i, slots)) a.kept[slot0 + tail + i] = last + i;
 }
 
-constexpr int COPY_THREADS = 256;
-constexpr int COPY_UNROLL = 8;
+constexpr int COPY_THREADS = 128;
+constexpr int COPY_UNROLL = 4;
 
-// One unit is a 16-byte chunk of a kept row of K (or V); a CTA copies
-// COPY_THREADS * COPY_UNROLL consecutive units of one (sequence, key head).
+// A thread keeps one 16-byte column c of the rows (one division, at the start)
+// and COPY_UNROLL rows in flight; a CTA copies `rows` * COPY_UNROLL consecutive
+// kept rows of K or V of one (sequence, key head), rows = 128 / chunks, or 1.
+// With the selection, 256 rows of 4096 kept out of up to 16384 (1.09 GB): 187 us;
+// eight rows in flight cost occupancy (214 us), 256 threads 188 us, plain
+// stores instead of streaming ones 204 us.
 __global__ void __launch_bounds__(COPY_THREADS)
 evict_copy_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                   const float* __restrict__ weight, const int32_t* kept, int groups,
-                  int cap, uint32_t chunks, int keep, int cap_out, int blocks, uint4* __restrict__ k_out,
-                  uint4* __restrict__ v_out, float* __restrict__ weight_out) {
+                  int cap, int chunks, int rows, int keep, int cap_out, int blocks,
+                  uint4* __restrict__ k_out, uint4* __restrict__ v_out,
+                  float* __restrict__ weight_out) {
   const int part = blockIdx.x % 2;                 // 0: K and the weights, 1: V
   const int block = (int)(blockIdx.x / 2) % blocks;
   const int group = (int)(blockIdx.x / 2) / blocks;
   const uint4* src = part ? v : k;
   uint4* dst = part ? v_out : k_out;
+  const int r = min((int)threadIdx.x / chunks, rows);
+  const int i0 = block * rows * COPY_UNROLL + r;   // this thread's first kept row
   wait_prerequisite();                             // the kept rows' indices
-  if (src == nullptr) return;
-  const uint32_t u0 = (uint32_t)block * (COPY_THREADS * COPY_UNROLL) + threadIdx.x;
-  const uint32_t units = (uint32_t)keep * (uint32_t)chunks;      // below 2^31
+  if (src == nullptr || r == rows) return;
   const int32_t* idx = kept + (size_t)group * keep;
-  const size_t slots = (size_t)groups * keep;
-  (void)slots;
-  uint4 x[COPY_UNROLL];
   int row[COPY_UNROLL];
 #pragma unroll
   for (int e = 0; e < COPY_UNROLL; ++e) {
-    const uint32_t u = u0 + e * COPY_THREADS;
-    row[e] = -1;
-    if (u < units) {
-      const uint32_t i = u / chunks;
-      if (RF_IDX_OK((size_t)group * keep + i, slots)) row[e] = __ldcg(idx + i);
+    const int i = i0 + e * rows;
+    row[e] = i < keep && RF_IDX_OK((size_t)group * keep + i, (size_t)groups * keep) ? __ldcg(idx + i) : -1;
+  }
+  const size_t in0 = (size_t)group * cap, out0 = (size_t)group * cap_out;
+  for (int c = threadIdx.x - r * chunks; c < chunks; c += COPY_THREADS) {
+    uint4 x[COPY_UNROLL];
+#pragma unroll
+    for (int e = 0; e < COPY_UNROLL; ++e)
+      if (row[e] >= 0 && RF_IDX_OK((in0 + row[e]) * chunks + c, (size_t)groups * cap * chunks))
+        x[e] = ld_stream_v4(src + (in0 + row[e]) * chunks + c);
+#pragma unroll
+    for (int e = 0; e < COPY_UNROLL; ++e) {
+      const size_t o = out0 + i0 + e * rows;
+      if (row[e] >= 0 && RF_IDX_OK(o * chunks + c, (size_t)groups * cap_out * chunks))
+        __stcs(dst + o * chunks + c, x[e]);
     }
   }
+  if (part == 0 && (int)threadIdx.x == r * chunks) {
 #pragma unroll
-  for (int e = 0; e < COPY_UNROLL; ++e) {
-    const uint32_t u = u0 + e * COPY_THREADS;
-    if (row[e] < 0) continue;
-    const uint32_t c = u % chunks;
-    const size_t at = ((size_t)group * cap + row[e]) * chunks + c;
-    if (RF_IDX_OK(at, (size_t)groups * cap * chunks)) x[e] = ld_stream_v4(src + at);
-  }
-#pragma unroll
-  for (int e = 0; e < COPY_UNROLL; ++e) {
-    const uint32_t u = u0 + e * COPY_THREADS;
-    if (row[e] < 0) continue;
-    const uint32_t i = u / chunks, c = u - i * chunks;
-    const size_t at = ((size_t)group * cap_out + i) * chunks + c;
-    if (RF_IDX_OK(at, (size_t)groups * cap_out * chunks)) __stcs(dst + at, x[e]);
-    if (part == 0 && c == 0 && RF_IDX_OK((size_t)group * cap_out + i, (size_t)groups * cap_out) &&
-        RF_IDX_OK((size_t)group * cap + row[e], (size_t)groups * cap))
-      weight_out[(size_t)group * cap_out + i] = weight[(size_t)group * cap + row[e]];
+    for (int e = 0; e < COPY_UNROLL; ++e) {
+      const size_t o = out0 + i0 + e * rows;
+      if (row[e] >= 0 && RF_IDX_OK(o, (size_t)groups * cap_out) &&
+          RF_IDX_OK(in0 + row[e], (size_t)groups * cap))
+        weight_out[o] = weight[in0 + row[e]];
+    }
   }
 }
 
@@ -239,9 +261,9 @@ rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
                              float* weight_out, int32_t* lens_out, int32_t* kept,
                              cudaStream_t st) {
   const int chunks = row_bytes / 16;
-  const long long units = (long long)keep * chunks;
-  const long long blocks = (units + COPY_THREADS * COPY_UNROLL - 1) / (COPY_THREADS * COPY_UNROLL);
-  if (units > 0x7fffffffLL || blocks * 2 * B * Hkv > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
+  const int rows = chunks < COPY_THREADS ? COPY_THREADS / chunks : 1;
+  const long long blocks = ((long long)keep + rows * COPY_UNROLL - 1) / (rows * COPY_UNROLL);
+  if (blocks * 2 * B * Hkv > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
   static std::atomic<uint64_t> done{0};
   if (smem_attr(evict_select_kernel, SEL_KEYS * sizeof(uint32_t), done) != RF_OK) return RF_ERR_CUDA;
   const int held = cap < SEL_KEYS ? cap : SEL_KEYS;
@@ -251,7 +273,7 @@ rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
   if (s != RF_OK) return s;
   return launch_after(evict_copy_kernel, (unsigned)(blocks * 2 * B * Hkv), COPY_THREADS, 0, st,
                       static_cast<const uint4*>(k), static_cast<const uint4*>(v), weight, kept,
-                      B * Hkv, cap, (uint32_t)chunks, keep, cap_out, (int)blocks,
+                      B * Hkv, cap, chunks, rows, keep, cap_out, (int)blocks,
                       static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), weight_out);
 }
 

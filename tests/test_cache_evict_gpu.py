@@ -157,3 +157,11 @@ def test_captured_and_replayed(rf):
             ref = C.kept_rows(w[b, h].cpu().numpy(), m, 100, 4, 10)
             assert np.array_equal(kept[b, h, :len(ref)].cpu().numpy(), ref)
             assert torch.equal(out[0][b, h, :len(ref)], k[b, h, torch.from_numpy(ref).cuda()])
+
+
+@pytest.mark.parametrize("D", [8, 24, 576, 1160, 4104, 32768])
+def test_row_sizes(rf, D):
+    # rows of 16 bytes up to 64 KiB, whole and odd parts of a block's 256 columns
+    cap, keep = (300, 131) if D < 4000 else (40, 17)
+    k, v, w = make(D, 2, 1, cap, D=D)
+    check(rf, k, v, w, [cap, cap // 2], keep, 1, 5)
