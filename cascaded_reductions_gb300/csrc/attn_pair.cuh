@@ -34,11 +34,13 @@
 //   warps 0-7   softmax of this CTA's 128 rows: warp w reads TMEM lanes
 //               32 (w % 4) .. + 31 (thread = row) and keys 128 (w / 4) .. + 127
 //               of the block into registers; the two warps of a row exchange
-//               their partial maxima through shared memory.
+//               their partial maxima through shared memory;
+//   warps 12-15 output of an item's rows: O from TMEM once its last P V is done,
+//               while the softmax warps are in the next item's first block.
 // Two softmax warps per SM sub-partition (not four) leave the MMA-issuing
 // thread, which shares a sub-partition with two of them, enough issue slots
-// for the 64-cycle P V MMAs; with ten warps a thread may hold 168 registers,
-// enough for its 128 scores.
+// for the 64-cycle P V MMAs.  Their threads hold 128 scores each, so the
+// registers are divided unevenly between the warpgroups.
 // Rescaling is lazy: the reference max m_ref of a row moves (and O and l are
 // multiplied by exp2(m_ref_old - m_ref_new)) only when the block max exceeds
 // it by more than 8, so p <= 2^8.
@@ -51,8 +53,6 @@
 // after a wait are MMAs, whose operands were completed by the TMA
 // transaction count or by the softmax warps' tcgen05.wait (an acquire at
 // cluster scope idles the tensor pipe about 160 cycles per wait).
-// An item's epilogue is deferred into the first block of the next item (see
-// the softmax role).
 // Every barrier wait is bounded (see tc_common.cuh); the two CTAs meet at a
 // cluster barrier before either exits.
 //
@@ -68,22 +68,24 @@
 //                              blocks, at least one; false past the last
 //   q_bytes()                  bytes of one CTA's Q tile that load_q copies
 //   load_q / load_k / load_v   the TMA copies of one CTA, into its halves
-//   keys(it, j)                256, or 64 for a block whose other keys no row
-//                              sees: its products stop there
+//   keys(it, j)                256, or 128 or 64 where no row sees the block's
+//                              other keys: its products stop there
+//   v_bytes(it, j)             bytes that load_v copies (with one map or both)
 //   PARTIAL, words(it, j, rank, row, kh)  with PARTIAL, which of the warp's 128
 //                              keys (128 kh ..) of block j its rows may see: 4
-//                              (32-key words, all), 2 (only the first two; the
-//                              block is a narrow one) or 0; 4 for block 0
+//                              (32-key words, all), 2 (the first two; keys is
+//                              64) or 0; 4 for block 0
 //   mask<NW>(it, j, rank, row, kh, s)  sets hidden scores of the first 32 NW of
 //                              them to -inf
-//   pending(it, rank, row)     and  store(pend, kh, v, m, l): an output row's
-//                              64 columns 64 kh .. from O, m (log2 units), l;
-//                              true asks for after(true, ...)
-//   STAGED                     instead of store():  pack(pend, kh, v, m, l, w)
-//                              gives the columns in 16 bits, and
-//                              send(map, box, pend, quarter, kh) starts the
-//                              copy of a warp's 32 x 64 box from shared memory
-//   after(any, c, nc, rank, row, kh)  once everything of the thread is stored
+//   pending(it, rank, row)     what an output row needs beside its values, and
+//   store(pend, col, v, m, l)  its columns col .. + 31 from O, with the row's
+//                              reference m (log2 units) and sum l
+//   STAGED                     instead of store():  pack(pend, col, v, m, l, w)
+//                              gives the columns in 16 bits (true: call
+//                              after(true, ...)), and  send(map, box, pend)
+//                              starts the copies of a warp's two 32 x 64 boxes,
+//                              HALF_BYTES apart in shared memory
+//   after(any, c, nc, rank, row)  once everything of the row's items is stored
 #pragma once
 
 #include <cuda_bf16.h>
@@ -96,14 +98,19 @@ namespace pair {
 
 constexpr int BM = 128;                      // query rows per CTA (256 per pair)
 constexpr int BN = 256;                      // keys per block
-constexpr int NARROW = 64;                   // keys of a narrow block
+constexpr int NARROW = 64, MIXED = 128;      // keys of a narrow block, and of two in one
 constexpr int HD = 128;                      // head dim
 constexpr int STAGES = 2;
 constexpr int TILE_BYTES = 32768;            // Q tile, K half or V half
 constexpr int HALF_BYTES = 16384;            // one 64-column swizzled box of a 128-row tile
 constexpr int SM_WARPS = 8;                // softmax warps: two per TMEM lane quarter
 constexpr int TMA_WARP = 8, MMA_WARP = 9;
-constexpr int THREADS = 10 * 32;
+constexpr int OUT_WARP = 12, OUT_WARPS = 4;  // output warps, one per TMEM lane quarter
+constexpr int THREADS = 16 * 32;             // four warpgroups (10 and 11 only fill theirs)
+// Registers per thread: at launch, then softmax warps and the others.
+constexpr int REGS = 128, REGS_SOFTMAX = 176, REGS_OTHER = 80;
+static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHER == THREADS * REGS,
+              "the shares of the four warpgroups add up to what the CTA is launched with");
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t S_COL = 0, P_COL = 256, O_COL = 384;
 constexpr float RESCALE_THRESHOLD = 8.0f;    // log2 units
@@ -111,7 +118,7 @@ constexpr float RESCALE_THRESHOLD = 8.0f;    // log2 units
 struct Shared {
   uint64_t q_full[2];           // CTA 0: both Q tiles of a buffer
   uint64_t q_empty[2];          // each CTA: the item's S MMAs are done with the buffer (and, with
-                                // STAGED, its eight softmax warps' output stores have read it)
+                                // STAGED, the output warps' copies have read it)
   uint64_t k_full[STAGES];      // CTA 0: both K halves of a stage
   uint64_t v_full[STAGES];      // CTA 0: both V halves of a stage
   uint64_t k_empty[STAGES];     // each CTA: S of that block done
@@ -120,10 +127,13 @@ struct Shared {
   uint64_t pv_done;             // each CTA: P V(g) complete
   uint64_t s_free;              // CTA 0: both CTAs' softmax warps have read S(g) (32 warps)
   uint64_t p_ready;             // CTA 0: both CTAs' P(g) and O rescale written (32 warps)
-  uint64_t o_free;              // CTA 0: both CTAs' epilogues have read O (32 warps)
-  uint64_t red_bar[4];          // each CTA, per lane quarter: its four warps' maxima / sums
+  uint64_t o_full;              // each CTA: the item's last P V complete
+  uint64_t o_free;              // CTA 0: both CTAs' output warps have read O (8 warps)
+  uint64_t l_ready[2];          // each CTA: an item's row sums and references are in part_l, row_m
+  uint64_t red_bar[4];          // each CTA, per lane quarter: its two warps' maxima
   float red[2][2][BM];          // [exchange & 1][key half][row]: partial row maxima
-  float part_l[2][BM];          // [key half][row]: partial row sums of an item
+  float part_l[2][2][BM];       // [item & 1][key half][row]: partial row sums of an item
+  float row_m[2][BM];           // [item & 1][row]: its reference maxima
   uint32_t tmem_base;
   int abort;
 };
@@ -218,8 +228,8 @@ __device__ __forceinline__ uint32_t pack_16x2(float lo, float hi) {
 template <class P>
 __global__ void __launch_bounds__(THREADS, 1)
 attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                 const __grid_constant__ P p) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ P p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -237,7 +247,8 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sh->q_full[b], 1);
-      tc::mbar_init(&sh->q_empty[b], P::STAGED ? 1 + SM_WARPS : 1);
+      tc::mbar_init(&sh->q_empty[b], P::STAGED ? 1 + OUT_WARPS : 1);
+      tc::mbar_init(&sh->l_ready[b], SM_WARPS);
     }
     for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(&sh->k_full[s], 1);
@@ -249,7 +260,8 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc::mbar_init(&sh->pv_done, 1);
     tc::mbar_init(&sh->s_free, 2 * SM_WARPS);
     tc::mbar_init(&sh->p_ready, 2 * SM_WARPS);
-    tc::mbar_init(&sh->o_free, 2 * SM_WARPS);
+    tc::mbar_init(&sh->o_full, 1);
+    tc::mbar_init(&sh->o_free, 2 * OUT_WARPS);
     for (int q = 0; q < 4; ++q) tc::mbar_init(&sh->red_bar[q], 2);
     sh->abort = 0;
     tc::fence_barrier_init();
@@ -263,119 +275,9 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort = &sh->abort;
 
-  if (warp == TMA_WARP) {
-    // ------------------------------------------------------ TMA ----
-    if (lane == 0) {
-      tc::prefetch_tmap(&tmQ);
-      tc::prefetch_tmap(&tmK);
-      tc::prefetch_tmap(&tmV);
-      uint32_t g = 0;                                 // key blocks loaded so far
-      bool ok = true;
-      typename P::Item it;
-      for (int t = 0; ok; ++t) {
-        if (!p.item(t, cluster, nclusters, it)) break;
-        const int qb = t & 1;
-        if (!(ok = tc::mbar_wait(&sh->q_empty[qb], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort))) break;
-        if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full[qb], 2 * p.q_bytes());
-        p.load_q(sQ + qb * TILE_BYTES, &tmQ, tc::mapa(tc::smem_u32(&sh->q_full[qb]), 0), it, rank);
-        for (int j = 0; j < it.n; ++j, ++g) {
-          const int s = (int)(g & 1u);
-          const uint32_t ph = (g >> 1) & 1u;
-          if (!(ok = tc::mbar_wait(&sh->k_empty[s], ph ^ 1u, abort))) break;
-          if (rank == 0) tc::mbar_arrive_expect_tx(&sh->k_full[s], 2 * TILE_BYTES);
-          p.load_k(sK + s * TILE_BYTES, &tmK, tc::mapa(tc::smem_u32(&sh->k_full[s]), 0), it, j, rank);
-          if (!(ok = tc::mbar_wait(&sh->v_empty[s], ph ^ 1u, abort))) break;
-          if (rank == 0) tc::mbar_arrive_expect_tx(&sh->v_full[s], 2 * TILE_BYTES);
-          p.load_v(sV + s * TILE_BYTES, &tmV, tc::mapa(tc::smem_u32(&sh->v_full[s]), 0), it, j, rank);
-        }
-      }
-    }
-  } else if (warp == MMA_WARP) {
-    // ------------------------------------------------------ MMA ----
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc_s = idesc_16<P::F16>(2 * BM, BN, false);
-      constexpr uint32_t idesc_s_narrow = idesc_16<P::F16>(2 * BM, NARROW, false);
-      constexpr uint32_t idesc_pv = idesc_16<P::F16>(2 * BM, HD, true);
-      // first K-step descriptors; a K-step adds its byte offset >> 4
-      const uint64_t q_desc0 = tc::sdesc_sw128(tc::smem_u32(sQ), 16, 1024);
-      const uint64_t q_desc1 = tc::sdesc_sw128(tc::smem_u32(sQ + TILE_BYTES), 16, 1024);
-      static_assert(STAGES == 2, "one descriptor per stage, picked by g & 1");
-      const uint64_t k_desc0 = tc::sdesc_sw128(tc::smem_u32(sK), 16, 1024);
-      const uint64_t k_desc1 = tc::sdesc_sw128(tc::smem_u32(sK + TILE_BYTES), 16, 1024);
-      // V halves are MN-major: 128-byte rows of 64 head-dimension columns,
-      // 8-key groups 1 KiB apart (one swizzle atom wide, so the leading
-      // offset is not used)
-      const uint64_t v_desc0 = tc::sdesc_sw128(tc::smem_u32(sV), TILE_BYTES, 1024);
-      const uint64_t v_desc1 = tc::sdesc_sw128(tc::smem_u32(sV + TILE_BYTES), TILE_BYTES, 1024);
-      // S(g) = Q K^T from Q buffer qb: eight K-steps of 16 head-dimension
-      // columns; the second 64 columns sit in the second swizzled box.  The
-      // item's last S also releases its Q buffer.
-      auto issue_s = [&](uint32_t g, int qb, bool narrow, bool last_of_item) -> bool {
-        const int s = (int)(g & 1u);
-        if (!tc::mbar_wait(&sh->k_full[s], (g >> 1) & 1u, abort)) return false;
-        tc::fence_after_sync();
-        const uint64_t kd = s ? k_desc1 : k_desc0;
-        const uint64_t qd = qb ? q_desc1 : q_desc0;
-        const uint32_t idesc = narrow ? idesc_s_narrow : idesc_s;
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint64_t off = (uint64_t)(((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4);
-          tc::mma_pair_f16_ss(tmem + S_COL, qd + off, kd + off, idesc, kk != 0);
-        }
-        tc::commit_pair_both(&sh->s_full);
-        tc::commit_pair_both(&sh->k_empty[s]);
-        if (last_of_item) tc::commit_pair_both(&sh->q_empty[qb]);
-        return true;
-      };
-      // O [+]= P V(g): sixteen K-steps of 16 keys (8 TMEM columns of P, 2 KiB of V)
-      auto issue_pv = [&](uint32_t g, bool narrow, bool accumulate) -> bool {
-        const int s = (int)(g & 1u);
-        if (!tc::mbar_wait(&sh->v_full[s], (g >> 1) & 1u, abort)) return false;
-        tc::fence_after_sync();
-        const uint64_t vd = s ? v_desc1 : v_desc0;
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk) {
-          if (kk >= NARROW / 16 && narrow) break;
-          tc::mma_pair_f16_ts(tmem + O_COL, tmem + P_COL + (uint32_t)(kk * 8),
-                              vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                              (accumulate || kk > 0) ? 1u : 0u);
-        }
-        tc::commit_pair_both(&sh->pv_done);
-        tc::commit_pair_both(&sh->v_empty[s]);
-        return true;
-      };
-      // the first item's first S; then per block g: S(g + 1) (of this item or
-      // the next) as soon as S(g) has been read, then P V(g) once P(g) is in
-      typename P::Item it, next;
-      bool ok = p.item(0, cluster, nclusters, it);
-      if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0) < BN, it.n == 1);
-      uint32_t g = 0;
-      for (int t = 0; ok; ++t) {
-        const bool has_next = p.item(t + 1, cluster, nclusters, next);
-        for (int j = 0; ok && j < it.n; ++j, ++g) {
-          if (j + 1 < it.n || has_next) {
-            // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
-            if (!(ok = tc::mbar_wait(&sh->s_free, g & 1u, abort))) break;
-            if (j + 1 < it.n) {
-              ok = issue_s(g + 1, t & 1, p.keys(it, j + 1) < BN, j + 2 == it.n);
-            } else {
-              const int qb = (t + 1) & 1;
-              ok = tc::mbar_wait(&sh->q_full[qb], ((uint32_t)(t + 1) >> 1) & 1u, abort) &&
-                   issue_s(g + 1, qb, p.keys(next, 0) < BN, next.n == 1);
-            }
-            if (!ok) break;
-          }
-          if (!(ok = tc::mbar_wait(&sh->p_ready, g & 1u, abort))) break;
-          // the item's first P V overwrites O: the last item's O has been read
-          if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort)))
-            break;
-          ok = issue_pv(g, p.keys(it, j) < BN, j > 0);
-        }
-        if (!has_next) break;
-        it = next;
-      }
-    }
-  } else {
+  // Each warpgroup takes its share of the registers, all its warps alike.
+  if (warp < SM_WARPS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     // --------------------------------------------------- softmax ----
     const int quarter = warp & 3;                   // TMEM lanes 32 quarter .. + 31
     const int kh = warp >> 2;                       // keys 128 kh .. + 127 of each block
@@ -383,62 +285,10 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_free0 = tc::mapa(tc::smem_u32(&sh->s_free), 0);
     const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&sh->p_ready), 0);
-    const uint32_t o_free0 = tc::mapa(tc::smem_u32(&sh->o_free), 0);
     const float scale_log2 = p.scale_log2;
     const uint64_t sl2 = pack_f32x2(scale_log2, scale_log2);
     uint32_t g = 0, x = 0;                          // blocks and red_bar exchanges so far
     bool ok = true;
-    bool pend = false;                              // an item's output is still to be written
-    float pend_m = 0.f, pend_l = 0.f;
-    typename P::Pending pending = {};
-    bool repair = false;                            // what store() or pack() found, for after()
-    bool staged = false;                            // an output store may still read its Q buffer
-    int pend_qb = 0, staged_qb = 0;
-    // O columns 64 kh .. + 63 of this thread's row
-    auto load_o = [&](uint32_t (&v)[64]) {
-      uint32_t (&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
-      uint32_t (&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
-      tc::tmem_ld_32x32b_x32(lanes + O_COL + (uint32_t)(kh * 64), v0);
-      tc::tmem_ld_32x32b_x32(lanes + O_COL + (uint32_t)(kh * 64 + 32), v1);
-      tc::tmem_ld_wait();
-    };
-    // both halves of the row sums are in part_l: they were written before the
-    // exchange of the next item's first maxima
-    auto finish = [&](const uint32_t (&v)[64]) {
-      const float lt = sh->part_l[0][r] + sh->part_l[1][r];
-      if constexpr (P::STAGED) {
-        // the warp's 32 rows x 64 columns, swizzled as the map's box, over the
-        // item's own Q tile, whose products are long done
-        uint32_t w[32];
-        repair |= p.pack(pending, kh, v, pend_m, lt, w);
-        uint8_t* box = sQ + pend_qb * TILE_BYTES + kh * HALF_BYTES + quarter * 4096;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        tc::fence_proxy_async_cta();
-        __syncwarp();
-        if (lane == 0) {
-          p.send(&tmO, box, pending, quarter, kh);
-          tc::bulk_commit();
-        }
-        staged = true;
-        staged_qb = pend_qb;
-      } else {
-        repair |= p.store(pending, kh, v, pend_m, lt);
-      }
-    };
-    // the Q buffer that the last output went through may be filled again
-    auto release = [&] {
-      if constexpr (P::STAGED) {
-        if (!staged) return;
-        if (lane == 0) {
-          tc::bulk_wait_read();
-          tc::mbar_arrive(&sh->q_empty[staged_qb]);
-        }
-        staged = false;
-      }
-    };
     typename P::Item it;
     for (int t = 0; ok; ++t) {
       if (!p.item(t, cluster, nclusters, it)) break;
@@ -448,7 +298,6 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // the item's first block.
       auto block = [&](auto words, int j) -> bool {
         constexpr int NW = decltype(words)::value;
-        release();
         if (!tc::mbar_wait(&sh->s_full, g & 1u, abort)) return false;
         tc::fence_after_sync();
         float s[NW > 0 ? 32 * NW : 1];              // s[c] = key 128 kh + c of block j
@@ -472,7 +321,6 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         float* red = &sh->red[x & 1u][0][0];
         red[kh * BM + r] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (NW == 4 && j == 0 && pend) sh->part_l[kh][r] = pend_l;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh->red_bar[quarter]);
         if (!tc::mbar_wait(&sh->red_bar[quarter], x & 1u, abort)) return false;
@@ -500,10 +348,11 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           unpack_f32x2(sum2, s0, s1);
           l += s0 + s1;
         }
-        if (j > 0) {
+        // the last block's P V is done: P may be overwritten, and O rescaled
+        if (g > 0) {
           if (!tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort)) return false;
           tc::fence_after_sync();
-          if (__any_sync(0xffffffffu, move)) {
+          if (j > 0 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
             for (int hh = 0; hh < 2; ++hh) {
               const uint32_t oc = lanes + O_COL + (uint32_t)(kh * 64 + hh * 32);
@@ -515,11 +364,6 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               tc::tmem_st_32x32b_x32(oc, v);
             }
           }
-        }
-        const bool have_o = NW == 4 && j == 0 && pend;
-        if (have_o) {
-          if (!tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort)) return false;
-          tc::fence_after_sync();
         }
         // P: the words in hand; a full block's products read the others as zeros
         if constexpr (NW >= 2) {
@@ -536,24 +380,9 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           tc::tmem_st_32x32b_x32(lanes + P_COL + (uint32_t)(kh * 64 + 32), z);
         }
         tc::tmem_st_wait();
-        if (have_o) {
-          uint32_t ov[64];
-          load_o(ov);
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            arrive_cluster_relaxed(o_free0);
-            arrive_cluster_relaxed(p_ready0);
-          }
-          finish(ov);
-          pend = false;
-          // the next item's first S needs its Q tile before this warp comes here again
-          if (it.n == 1) release();
-        } else {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive_cluster_relaxed(p_ready0);
-        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_cluster_relaxed(p_ready0);
         return true;
       };
       for (int j = 0; ok && j < it.n; ++j, ++g) {
@@ -565,32 +394,191 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       if (!ok) break;
-      pend = true;
-      pend_m = m_ref;
-      pend_l = l;
-      pending = p.pending(it, rank, r);
-      pend_qb = t & 1;
-    }
-    if (ok && pend) {
-      sh->part_l[kh][r] = pend_l;
+      // The output warps have read what was here two items ago: this block waited
+      // for a P V that was issued after they had read that item's O.
+      sh->part_l[t & 1][kh][r] = l;
+      if (kh == 0) sh->row_m[t & 1][r] = m_ref;
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sh->red_bar[quarter]);
-      ok = tc::mbar_wait(&sh->red_bar[quarter], x & 1u, abort) &&
-           tc::mbar_wait(&sh->pv_done, (g - 1) & 1u, abort);
-      if (ok) {
-        tc::fence_after_sync();
-        uint32_t ov[64];
-        load_o(ov);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) arrive_cluster_relaxed(o_free0);
-        finish(ov);
-      }
+      if (lane == 0) tc::mbar_arrive(&sh->l_ready[t & 1]);
     }
-    // no output is read from shared memory after the CTA is gone
-    if (P::STAGED && lane == 0) tc::bulk_wait();
-    __syncwarp();
-    if (ok) p.after(repair, cluster, nclusters, rank, r, kh);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    if (warp == TMA_WARP) {
+      // ------------------------------------------------------ TMA ----
+      if (lane == 0) {
+        tc::prefetch_tmap(&tmQ);
+        tc::prefetch_tmap(&tmK);
+        tc::prefetch_tmap(&tmV);
+        uint32_t g = 0;                                 // key blocks loaded so far
+        bool ok = true;
+        typename P::Item it;
+        for (int t = 0; ok; ++t) {
+          if (!p.item(t, cluster, nclusters, it)) break;
+          const int qb = t & 1;
+          if (!(ok = tc::mbar_wait(&sh->q_empty[qb], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort))) break;
+          if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full[qb], 2 * p.q_bytes());
+          p.load_q(sQ + qb * TILE_BYTES, &tmQ, tc::mapa(tc::smem_u32(&sh->q_full[qb]), 0), it, rank);
+          for (int j = 0; j < it.n; ++j, ++g) {
+            const int s = (int)(g & 1u);
+            const uint32_t ph = (g >> 1) & 1u;
+            if (!(ok = tc::mbar_wait(&sh->k_empty[s], ph ^ 1u, abort))) break;
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sh->k_full[s], 2 * TILE_BYTES);
+            p.load_k(sK + s * TILE_BYTES, &tmK, tc::mapa(tc::smem_u32(&sh->k_full[s]), 0), it, j, rank);
+            if (!(ok = tc::mbar_wait(&sh->v_empty[s], ph ^ 1u, abort))) break;
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sh->v_full[s], 2 * p.v_bytes(it, j));
+            p.load_v(sV + s * TILE_BYTES, &tmV, &tmW, tc::mapa(tc::smem_u32(&sh->v_full[s]), 0), it, j,
+                   rank);
+          }
+        }
+      }
+    } else if (warp == MMA_WARP) {
+      // ------------------------------------------------------ MMA ----
+      if (lane == 0 && rank == 0) {
+        constexpr uint32_t idesc_s = idesc_16<P::F16>(2 * BM, BN, false);
+        constexpr uint32_t idesc_s_narrow = idesc_16<P::F16>(2 * BM, NARROW, false);
+        constexpr uint32_t idesc_s_mixed = idesc_16<P::F16>(2 * BM, MIXED, false);
+        constexpr uint32_t idesc_pv = idesc_16<P::F16>(2 * BM, HD, true);
+        // first K-step descriptors; a K-step adds its byte offset >> 4
+        const uint64_t q_desc0 = tc::sdesc_sw128(tc::smem_u32(sQ), 16, 1024);
+        const uint64_t q_desc1 = tc::sdesc_sw128(tc::smem_u32(sQ + TILE_BYTES), 16, 1024);
+        static_assert(STAGES == 2, "one descriptor per stage, picked by g & 1");
+        const uint64_t k_desc0 = tc::sdesc_sw128(tc::smem_u32(sK), 16, 1024);
+        const uint64_t k_desc1 = tc::sdesc_sw128(tc::smem_u32(sK + TILE_BYTES), 16, 1024);
+        // V halves are MN-major: 128-byte rows of 64 head-dimension columns,
+        // 8-key groups 1 KiB apart (one swizzle atom wide, so the leading
+        // offset is not used)
+        const uint64_t v_desc0 = tc::sdesc_sw128(tc::smem_u32(sV), TILE_BYTES, 1024);
+        const uint64_t v_desc1 = tc::sdesc_sw128(tc::smem_u32(sV + TILE_BYTES), TILE_BYTES, 1024);
+        // S(g) = Q K^T from Q buffer qb: eight K-steps of 16 head-dimension
+        // columns; the second 64 columns sit in the second swizzled box.  The
+        // item's last S also releases its Q buffer.
+        auto issue_s = [&](uint32_t g, int qb, int keys, bool last_of_item) -> bool {
+          const int s = (int)(g & 1u);
+          if (!tc::mbar_wait(&sh->k_full[s], (g >> 1) & 1u, abort)) return false;
+          tc::fence_after_sync();
+          const uint64_t kd = s ? k_desc1 : k_desc0;
+          const uint64_t qd = qb ? q_desc1 : q_desc0;
+          const uint32_t idesc = keys == BN ? idesc_s : keys == MIXED ? idesc_s_mixed : idesc_s_narrow;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4);
+            tc::mma_pair_f16_ss(tmem + S_COL, qd + off, kd + off, idesc, kk != 0);
+          }
+          tc::commit_pair_both(&sh->s_full);
+          tc::commit_pair_both(&sh->k_empty[s]);
+          if (last_of_item) tc::commit_pair_both(&sh->q_empty[qb]);
+          return true;
+        };
+        // O [+]= P V(g): sixteen K-steps of 16 keys (8 TMEM columns of P, 2 KiB of V)
+        auto issue_pv = [&](uint32_t g, int keys, bool accumulate, bool last_of_item) -> bool {
+          const int s = (int)(g & 1u);
+          if (!tc::mbar_wait(&sh->v_full[s], (g >> 1) & 1u, abort)) return false;
+          tc::fence_after_sync();
+          const uint64_t vd = s ? v_desc1 : v_desc0;
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk) {
+            if ((kk == NARROW / 16 || kk == MIXED / 16) && kk * 16 >= keys) break;
+            tc::mma_pair_f16_ts(tmem + O_COL, tmem + P_COL + (uint32_t)(kk * 8),
+                                vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                                (accumulate || kk > 0) ? 1u : 0u);
+          }
+          tc::commit_pair_both(&sh->pv_done);
+          tc::commit_pair_both(&sh->v_empty[s]);
+          if (last_of_item) tc::commit_pair_both(&sh->o_full);
+          return true;
+        };
+        // the first item's first S; then per block g: S(g + 1) (of this item or
+        // the next) as soon as S(g) has been read, then P V(g) once P(g) is in
+        typename P::Item it, next;
+        bool ok = p.item(0, cluster, nclusters, it);
+        if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0), it.n == 1);
+        uint32_t g = 0;
+        for (int t = 0; ok; ++t) {
+          const bool has_next = p.item(t + 1, cluster, nclusters, next);
+          for (int j = 0; ok && j < it.n; ++j, ++g) {
+            if (j + 1 < it.n || has_next) {
+              // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
+              if (!(ok = tc::mbar_wait(&sh->s_free, g & 1u, abort))) break;
+              if (j + 1 < it.n) {
+                ok = issue_s(g + 1, t & 1, p.keys(it, j + 1), j + 2 == it.n);
+              } else {
+                const int qb = (t + 1) & 1;
+                ok = tc::mbar_wait(&sh->q_full[qb], ((uint32_t)(t + 1) >> 1) & 1u, abort) &&
+                     issue_s(g + 1, qb, p.keys(next, 0), next.n == 1);
+              }
+              if (!ok) break;
+            }
+            if (!(ok = tc::mbar_wait(&sh->p_ready, g & 1u, abort))) break;
+            // the item's first P V overwrites O: the last item's O has been read
+            if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort)))
+              break;
+            ok = issue_pv(g, p.keys(it, j), j > 0, j + 1 == it.n);
+          }
+          if (!has_next) break;
+          it = next;
+        }
+      }
+    } else if (warp >= OUT_WARP) {
+      // ---------------------------------------------------- output ----
+      const int quarter = warp - OUT_WARP;            // TMEM lanes 32 quarter .. + 31
+      const int r = quarter * 32 + lane;              // this thread's row of the tile
+      const uint32_t o_cols = tmem + ((uint32_t)(quarter * 32) << 16) + O_COL;
+      const uint32_t o_free0 = tc::mapa(tc::smem_u32(&sh->o_free), 0);
+      bool ok = true, repair = false;
+      typename P::Item it;
+      for (int t = 0; ok; ++t) {
+        if (!p.item(t, cluster, nclusters, it)) break;
+        const int b = t & 1;
+        // a whole item may pass meanwhile: 20 us more for each of its blocks (one takes 2)
+        const unsigned long long limit = tc::kWaitLimitNs + (unsigned long long)it.n * 20000ull;
+        ok = tc::mbar_wait(&sh->l_ready[b], (uint32_t)(t >> 1) & 1u, abort, limit) &&
+             tc::mbar_wait(&sh->o_full, (uint32_t)t & 1u, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const float lt = sh->part_l[b][0][r] + sh->part_l[b][1][r], m = sh->row_m[b][r];
+        const typename P::Pending pending = p.pending(it, rank, r);
+        // with STAGED, the warp's 32 rows x 64 columns twice, swizzled as the
+        // map's box, over the item's own Q tile, whose products are long done
+        uint8_t* box = sQ + b * TILE_BYTES + quarter * 4096;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t v[32];
+          tc::tmem_ld_32x32b_x32(o_cols + (uint32_t)(32 * c), v);
+          tc::tmem_ld_wait();
+          if (c == HD / 32 - 1) {                     // all of O is in registers or out
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_cluster_relaxed(o_free0);
+          }
+          if constexpr (P::STAGED) {
+            uint32_t w[16];
+            repair |= p.pack(pending, 32 * c, v, m, lt, w);
+            uint8_t* row = box + (c >> 1) * HALF_BYTES + lane * 128;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          } else {
+            p.store(pending, 32 * c, v, m, lt);
+          }
+        }
+        if constexpr (P::STAGED) {
+          tc::fence_proxy_async_cta();
+          __syncwarp();
+          if (lane == 0) {
+            p.send(&tmO, box, pending);
+            tc::bulk_commit();
+            tc::bulk_wait_read();                     // the Q buffer may be filled again
+            tc::mbar_arrive(&sh->q_empty[b]);
+          }
+          __syncwarp();
+        }
+      }
+      // no output is read from shared memory after the CTA is gone
+      if (P::STAGED && lane == 0) tc::bulk_wait();
+      __syncwarp();
+      if (ok) p.after(repair, cluster, nclusters, rank, r);
+    }
   }
 
   tc::fence_before_sync();
@@ -634,7 +622,11 @@ int resident_pairs() {
   const uint64_t bit = 1ull << dev;
   if (known.load(std::memory_order_acquire) & bit) return count[dev].load();
   int n = 0;
-  if (smem_attr(attn_pair_kernel<P>, SMEM_BYTES, attr_done) == RF_OK) {
+  // launched with fewer registers than the warpgroups' shares add up to, the
+  // softmax warps would wait for them for ever
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, attn_pair_kernel<P>) == cudaSuccess && fa.numRegs == REGS &&
+      smem_attr(attn_pair_kernel<P>, SMEM_BYTES, attr_done) == RF_OK) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pair_config(attr, 2u, 0);
     if (cudaOccupancyMaxActiveClusters(&n, attn_pair_kernel<P>, &cfg) != cudaSuccess) n = 0;
@@ -647,10 +639,11 @@ int resident_pairs() {
 
 template <class P>
 rf_status launch_pair(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                      const CUtensorMap& o, const P& p, int clusters, cudaStream_t st) {
+                      const CUtensorMap& w, const CUtensorMap& o, const P& p, int clusters,
+                      cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pair_config(attr, 2u * (unsigned)clusters, st);
-  if (cudaLaunchKernelEx(&cfg, attn_pair_kernel<P>, q, k, v, o, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, attn_pair_kernel<P>, q, k, v, w, o, p) != cudaSuccess) {
     cudaGetLastError();
     return RF_ERR_CUDA;
   }

@@ -66,8 +66,9 @@ struct CausalPrefill {
     tc::tma_load_2d_pair(dst, map, bar, 0, row);
     tc::tma_load_2d_pair(dst + HALF_BYTES, map, bar, 64, row);
   }
-  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
-                                         const Item& it, int j, int rank) const {
+  __device__ __forceinline__ uint32_t v_bytes(const Item&, int) const { return pair::TILE_BYTES; }
+  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, const CUtensorMap*,
+                                         uint32_t bar, const Item& it, int j, int rank) const {
     tc::tma_load_2d_pair(dst, map, bar, rank * 64, it.key0 + j * BN);
   }
   __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
@@ -91,28 +92,22 @@ struct CausalPrefill {
     const int m_tile = 2 * it.pair + rank;
     return {it.key0 + m_tile * BM + r, m_tile * BM + r < N};
   }
-  __device__ __forceinline__ bool store(const Pending& pend, int kh, const uint32_t (&v)[64],
+  __device__ __forceinline__ void store(const Pending& pend, int col, const uint32_t (&v)[32],
                                         float m, float lt) const {
     const long long heads = (long long)num_items / ((((N + BM - 1) / BM) + 1) / 2);
     (void)heads;                                    // read by the checked build only
     const bool out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     const float inv = 1.f / lt;
+    uint32_t pkd[16];
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      uint32_t pkd[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        pkd[c] = pack_bf16x2(__uint_as_float(v[32 * hh + 2 * c]) * inv,
-                             __uint_as_float(v[32 * hh + 2 * c + 1]) * inv);
-      const int col = kh * 64 + hh * 32;
-      if (pend.in && RF_SPAN_OK((size_t)pend.row * HD + col, 32, heads * N * HD))
-        pair::st_row32(out + (size_t)pend.row * HD + col, pkd, out32);
-    }
-    if (lse != nullptr && kh == 0 && pend.in && RF_IDX_OK(pend.row, heads * N))
+    for (int c = 0; c < 16; ++c)
+      pkd[c] = pack_bf16x2(__uint_as_float(v[2 * c]) * inv, __uint_as_float(v[2 * c + 1]) * inv);
+    if (pend.in && RF_SPAN_OK((size_t)pend.row * HD + col, 32, heads * N * HD))
+      pair::st_row32(out + (size_t)pend.row * HD + col, pkd, out32);
+    if (lse != nullptr && col == 0 && pend.in && RF_IDX_OK(pend.row, heads * N))
       lse[pend.row] = (m + log2f(lt)) * kLn2;
-    return false;
   }
-  __device__ __forceinline__ void after(bool, int, int, int, int, int) const {}
+  __device__ __forceinline__ void after(bool, int, int, int, int) const {}
 };
 
 }  // namespace
@@ -139,7 +134,7 @@ rf_status launch_prefill(const void* q, const void* k, const void* v, int B, int
   if (items > INT32_MAX) return RF_ERR_UNSUPPORTED;
   const int clusters = (int)(pairs < items ? pairs : items);
   const CausalPrefill p{static_cast<__nv_bfloat16*>(out), lse, N, causal, (int)items, scale * kLog2e};
-  return pair::launch_pair(tq, tk, tv, tq, p, clusters, st);
+  return pair::launch_pair(tq, tk, tv, tv, tq, p, clusters, st);
 }
 
 RF_TIMEOUT_WORD_OF_THIS_FILE

@@ -11,8 +11,10 @@
 // of 256 positions; 64 positions of four heads need 192 fewer).  It visits the
 // 256-key blocks that cover the keys any of its rows sees, last block first, a
 // remainder of up to 64 keys as a narrow block, and then the sinks below that
-// cover, narrow too where 64 keys are enough.  Only the blocks at the two edges
-// are masked, only by the warps that an edge crosses, a 32-key word at a time.
+// cover, narrow too where 64 keys are enough; a remainder and up to 64 sinks
+// share one block (a block costs its chain of waits whatever its width).  Only
+// the blocks at the two edges are masked, only by the warps that an edge crosses,
+// a 32-key word at a time.
 //
 // A row that sees nothing of a block must not be disturbed by it: its
 // reference starts at a finite value below every score, so such a block gives
@@ -46,6 +48,7 @@ struct WindowPrefill {
     int nb;          // full window blocks; block j < nb starts at lo + rem + 256 (nb - 1 - j)
     int nw;          // window blocks; block nb, if it is one, is the narrow one
     int limit;       // sinks below lo; block j >= nw starts at 256 (j - nw)
+    bool mixed;      // block nb holds the remainder in keys 0-63 and the sinks in 64-127
     int n;
   };
   struct Pending {
@@ -84,7 +87,8 @@ struct WindowPrefill {
     }
     it.nw = it.nb + (it.rem > 0);
     it.limit = min(sinks, it.lo);
-    it.n = it.nw + (it.limit + BN - 1) / BN;
+    it.mixed = it.rem > 0 && it.limit > 0 && it.limit <= pair::NARROW;
+    it.n = it.mixed ? it.nw : it.nw + (it.limit + BN - 1) / BN;
     return true;
   }
   __device__ __forceinline__ int key0(const Item& it, int j) const {
@@ -104,16 +108,28 @@ struct WindowPrefill {
   }
   __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
                                          const Item& it, int j, int rank) const {
-    const int key = key0(it, j) + rank * (keys(it, j) / 2);
+    // of a mixed block the second CTA's half are the sinks
+    const int key = it.mixed && j == it.nb ? (rank == 0 ? it.lo : 0) : key0(it, j) + rank * (keys(it, j) / 2);
     tc::tma_load_3d_pair(dst, map, bar, 0, key, it.kvh);
     tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, key, it.kvh);
   }
-  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
-                                         const Item& it, int j, int rank) const {
-    tc::tma_load_3d_pair(dst, map, bar, rank * 64, key0(it, j), it.kvh);
+  __device__ __forceinline__ uint32_t v_bytes(const Item& it, int j) const {
+    return it.mixed && j == it.nb ? 2 * pair::NARROW * 128 : pair::TILE_BYTES;
+  }
+  // `narrow`: the map whose boxes are 64 keys high
+  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, const CUtensorMap* narrow,
+                                         uint32_t bar, const Item& it, int j, int rank) const {
+    if (it.mixed && j == it.nb) {
+      tc::tma_load_3d_pair(dst, narrow, bar, rank * 64, it.lo, it.kvh);
+      tc::tma_load_3d_pair(dst + pair::NARROW * 128, narrow, bar, rank * 64, 0, it.kvh);
+    } else {
+      tc::tma_load_3d_pair(dst, map, bar, rank * 64, key0(it, j), it.kvh);
+    }
   }
   __device__ __forceinline__ int keys(const Item& it, int j) const {
-    return j >= it.nb && (j < it.nw || it.limit <= pair::NARROW) ? pair::NARROW : BN;
+    return j < it.nb ? BN
+           : it.mixed ? pair::MIXED
+           : j < it.nw || it.limit <= pair::NARROW ? pair::NARROW : BN;
   }
   // bits below n of a word
   static __device__ __forceinline__ uint32_t below(int n) {
@@ -122,7 +138,7 @@ struct WindowPrefill {
   // A warp whose rows see none of its keys of a block (half of those at the two
   // edges) skips its scores; of a narrow block there are 64 keys.
   __device__ __forceinline__ int words(const Item& it, int j, int rank, int r, int kh) const {
-    if (j >= it.nb) return keys(it, j) == BN ? 4 : kh == 0 ? 2 : 0;
+    if (j >= it.nb) return keys(it, j) == BN ? 4 : kh == 1 ? 0 : it.mixed ? 4 : 2;
     const int base = key0(it, j) + kh * 128;
     const int first = L - N + it.row0 + row_of(rank, r & ~31), last = first + 31;
     const bool some = last >= base && (first - window + 1 < base + 128 || sinks > base);
@@ -142,12 +158,23 @@ struct WindowPrefill {
       if (first - base >= 127 && last - window + 1 <= base) return;
     } else if (j < it.nw) {
       hi = min(hi, it.rem - 1);                         // the rest is the next block's
+      if (NW == 4 && it.mixed) {                        // (and kh is 0)
+        mask_words<0, 2>(hi, lo, cs, s);
+        mask_words<2, 4>(pair::NARROW + it.limit - 1, 0, 0, s);
+        return;
+      }
     } else {
       hi = 127, lo = 128, cs = it.limit - base;
       if (cs >= 128) return;
     }
+    mask_words<0, NW>(hi, lo, cs, s);
+  }
+  // words Q0 .. Q1 - 1 of s: visible are keys [lo, hi], and of those up to hi the
+  // ones below cs
+  template <int Q0, int Q1, int C>
+  static __device__ __forceinline__ void mask_words(int hi, int lo, int cs, float (&s)[C]) {
 #pragma unroll
-    for (int q = 0; q < NW; ++q) {
+    for (int q = Q0; q < Q1; ++q) {
       const uint32_t vis = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));
       if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
 #pragma unroll
@@ -160,13 +187,13 @@ struct WindowPrefill {
     const int row = it.row0 + row_of(rank, r);
     return {it.bh + head_of(rank, r), row, row < N};
   }
-  __device__ __forceinline__ bool pack(const Pending& pend, int kh, const uint32_t (&v)[64], float m,
-                                       float lt, uint32_t (&w)[32]) const {
+  __device__ __forceinline__ bool pack(const Pending& pend, int col, const uint32_t (&v)[32], float m,
+                                       float lt, uint32_t (&w)[16]) const {
     const float inv = 1.f / lt;
     const uint64_t inv2 = pair::pack_f32x2(inv, inv);
     uint64_t probe = 0ull;                              // NaN if a value is not finite
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 16; ++c) {
       const uint64_t x = pair::mul_f32x2(
           pair::pack_f32x2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), inv2);
       probe = pair::fma_f32x2(x, 0ull, probe);
@@ -175,18 +202,19 @@ struct WindowPrefill {
       w[c] = pair::pack_16x2<F16>(x0, x1);
     }
     const size_t row = (size_t)pend.bh * N + pend.row;
-    if (lse != nullptr && kh == 0 && pend.in && RF_IDX_OK(row, (size_t)heads * N))
+    if (lse != nullptr && col == 0 && pend.in && RF_IDX_OK(row, (size_t)heads * N))
       lse[row] = (m + log2f(lt)) * kLn2;
     float p0, p1;
     pair::unpack_f32x2(probe, p0, p1);
     return pend.in && !(p0 == 0.f && p1 == 0.f);
   }
-  // rows past N lie past the map's extent and are not written
-  __device__ __forceinline__ void send(const CUtensorMap* map, const uint8_t* box, const Pending& pend,
-                                       int quarter, int kh) const {
-    const int row = pend.row & ~31;
-    (void)quarter;
-    if (row < N) tc::tma_store_3d(map, box, kh * 64, row, pend.bh);
+  // called by the warp's first lane, whose row is the boxes' first; rows past N
+  // lie past the map's extent and are not written
+  __device__ __forceinline__ void send(const CUtensorMap* map, const uint8_t* box,
+                                       const Pending& pend) const {
+    if (!pend.in) return;
+    tc::tma_store_3d(map, box, 0, pend.row, pend.bh);
+    tc::tma_store_3d(map, box + HALF_BYTES, 64, pend.row, pend.bh);
   }
 
   static __device__ __forceinline__ float widen(uint32_t w, int hi) {
@@ -213,9 +241,9 @@ struct WindowPrefill {
     return (w & 0x7fffu) > inf || ((w >> 16) & 0x7fffu) > inf;
   }
 
-  // One output row's columns 64 kh .. + 63, from its visible keys alone: the
-  // warp's lanes hold four columns each, one key at a time.
-  __device__ void redo(int bh, int row, int kh, int lane) const {
+  // One output row, from its visible keys alone: the warp's lanes hold four
+  // columns each, one key at a time.
+  __device__ __forceinline__ void redo(int bh, int row, int lane) const {
     const int p = L - N + row;
     const size_t kv0 = (size_t)(bh / G) * L;
     const size_t q_n = (size_t)heads * N * HD, kv_n = (size_t)(heads / G) * L * HD;
@@ -242,25 +270,25 @@ struct WindowPrefill {
       for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], corr, w * vf[e]);
     }
     const size_t o = ((size_t)bh * N + row) * HD + lane * 4;
-    if ((lane >> 4) == kh && RF_SPAN_OK(o, 4, q_n)) {
+    if (RF_SPAN_OK(o, 4, q_n)) {
       uint2 w;
       w.x = pair::pack_16x2<F16>(acc[0] / l, acc[1] / l);
       w.y = pair::pack_16x2<F16>(acc[2] / l, acc[3] / l);
       *reinterpret_cast<uint2*>(out + o) = w;
     }
-    if (lse != nullptr && kh == 0 && lane == 0 && RF_IDX_OK((size_t)bh * N + row, (size_t)heads * N))
+    if (lse != nullptr && lane == 0 && RF_IDX_OK((size_t)bh * N + row, (size_t)heads * N))
       lse[(size_t)bh * N + row] = (m + log2f(l)) * kLn2;
   }
 
-  // Rows of this thread whose stored columns hold a NaN are computed again.
-  __device__ __noinline__ void repair(int cluster, int nclusters, int rank, int r, int kh) const {
+  // Rows of this thread whose stored values hold a NaN are computed again.
+  __device__ __forceinline__ void repair(int cluster, int nclusters, int rank, int r) const {
     Item it;
     for (int t = 0; item(t, cluster, nclusters, it); ++t) {
       const int row = it.row0 + row_of(rank, r), head = it.bh + head_of(rank, r);
       bool nan = false;
       if (row < N) {
-        const size_t o = ((size_t)head * N + row) * HD + kh * 64;
-        for (int c = 0; c < 8; ++c) {
+        const size_t o = ((size_t)head * N + row) * HD;
+        for (int c = 0; c < 16; ++c) {
           if (!RF_SPAN_OK(o + c * 8, 8, (size_t)heads * N * HD)) continue;
           const uint4 u = *(reinterpret_cast<const uint4*>(out + o) + c);
           nan |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
@@ -270,13 +298,12 @@ struct WindowPrefill {
       while (todo) {
         const int lane0 = __ffs(todo) - 1;
         todo &= todo - 1;
-        redo(head, __shfl_sync(0xffffffffu, row, lane0), kh, r & 31);
+        redo(head, __shfl_sync(0xffffffffu, row, lane0), r & 31);
       }
     }
   }
-  __device__ __forceinline__ void after(bool any, int cluster, int nclusters, int rank, int r,
-                                        int kh) const {
-    if (__any_sync(0xffffffffu, any)) repair(cluster, nclusters, rank, r, kh);
+  __device__ __forceinline__ void after(bool any, int cluster, int nclusters, int rank, int r) const {
+    if (__any_sync(0xffffffffu, any)) repair(cluster, nclusters, rank, r);
   }
 };
 
@@ -286,7 +313,7 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   using P = WindowPrefill<F16>;
   const int pairs = pair::resident_pairs<P>();
   if (pairs <= 0) return RF_ERR_UNSUPPORTED;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv, tw, to;
   const uint64_t qh = (uint64_t)B * H, kh = (uint64_t)B * Hkv;
   const int G = H / Hkv;
   const int packed = G % 8 == 0 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
@@ -294,6 +321,7 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   if (!tc::make_tmap_3d_16(&tq, F16, q, HD, N, qh, 64, box, BM / box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tk, F16, k, HD, L, kh, 64, BN / 2, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tv, F16, v, HD, L, kh, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_tmap_3d_16(&tw, F16, v, HD, L, kh, 64, pair::NARROW, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&to, F16, out, HD, N, qh, 64, 32, 1, CU_TENSOR_MAP_SWIZZLE_128B))
     return RF_ERR_CUDA;
   P p = {};
@@ -310,7 +338,7 @@ rf_status launch_t(const void* q, const void* k, const void* v, int B, int H, in
   p.pairs = (N + positions - 1) / positions;
   p.scale_log2 = scale * kLog2e;
   const long long items = (long long)(p.heads / packed) * p.pairs;
-  return pair::launch_pair(tq, tk, tv, to, p, (int)(pairs < items ? pairs : items), st);
+  return pair::launch_pair(tq, tk, tv, tw, to, p, (int)(pairs < items ? pairs : items), st);
 }
 
 }  // namespace

@@ -52,7 +52,9 @@ struct PrefixStates {
     int slot, end;           // state slot; 1: the item's last block is here
   };
   struct Pending {
-    int seq0, hk, slot, end;
+    size_t row;              // b * H + query head
+    int slot, end;
+    bool in;
   };
 
   float *seg_m, *seg_l, *seg_acc;
@@ -92,8 +94,9 @@ struct PrefixStates {
     tc::tma_load_3d_pair(dst, map, bar, 0, key, it.hk);
     tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, key, it.hk);
   }
-  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
-                                         const Item& it, int j, int rank) const {
+  __device__ __forceinline__ uint32_t v_bytes(const Item&, int) const { return pair::TILE_BYTES; }
+  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, const CUtensorMap*,
+                                         uint32_t bar, const Item& it, int j, int rank) const {
     tc::tma_load_3d_pair(dst, map, bar, rank * 64, (it.block0 + j) * BN, it.hk);
   }
   __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
@@ -110,38 +113,34 @@ struct PrefixStates {
     }
   }
   __device__ __forceinline__ Pending pending(const Item& it, int rank, int r) const {
-    (void)r;
-    return {it.seq0 + rank * nb, it.hk, it.slot, it.end};
-  }
-  __device__ __forceinline__ bool store(const Pending& pend, int kh, const uint32_t (&v)[64],
-                                        float m, float lt) const {
     // row r of the tile: sequence r / G, query head r % G of the group
-    const int r = (int)(threadIdx.x & 127);
-    const int b = pend.seq0 + r / G, g = r - (r / G) * G;
-    if (r >= nb * G || b >= B) return false;
-    const size_t row = (size_t)b * H + (size_t)pend.hk * G + g;
-    const size_t slot = row * S_total + pend.slot;
+    const int b = it.seq0 + rank * nb + r / G, g = r - (r / G) * G;
+    return {(size_t)b * H + (size_t)it.hk * G + g, it.slot, it.end, r < nb * G && b < B};
+  }
+  __device__ __forceinline__ void store(const Pending& pend, int col, const uint32_t (&v)[32],
+                                        float m, float lt) const {
+    if (!pend.in) return;
+    const size_t slot = pend.row * S_total + pend.slot;
     const size_t states = (size_t)B * H * S_total;
     (void)states;                                 // read by the checked build only
-    if (RF_SPAN_OK(slot * HD + kh * 64, 64, states * HD)) {
-      uint4* dst = reinterpret_cast<uint4*>(seg_acc + slot * HD + kh * 64);
+    if (RF_SPAN_OK(slot * HD + col, 32, states * HD)) {
+      uint4* dst = reinterpret_cast<uint4*>(seg_acc + slot * HD + col);
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
+      for (int c = 0; c < 8; ++c)
         dst[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     }
-    if (kh == 0 && RF_IDX_OK(slot, states)) {
+    if (col == 0 && RF_IDX_OK(slot, states)) {
       seg_m[slot] = m;
       seg_l[slot] = lt;
       if (pend.end)
         for (int s = pend.slot + 1; s < prefix_slots; ++s)
-          if (RF_IDX_OK(row * S_total + s, states)) {
-            seg_m[row * S_total + s] = -INFINITY;
-            seg_l[row * S_total + s] = 0.f;
+          if (RF_IDX_OK(pend.row * S_total + s, states)) {
+            seg_m[pend.row * S_total + s] = -INFINITY;
+            seg_l[pend.row * S_total + s] = 0.f;
           }
     }
-    return false;
   }
-  __device__ __forceinline__ void after(bool, int, int, int, int, int) const {}
+  __device__ __forceinline__ void after(bool, int, int, int, int) const {}
 };
 
 // The split for B sequences of G heads on Hkv key heads, at most `slots` states
@@ -180,7 +179,7 @@ rf_status launch_t(const void* q, const void* kp, const void* vp, int prefix, in
       !tc::make_tmap_3d_16(&tk, F16, kp, HD, prefix, Hkv, 64, BN / 2, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_tmap_3d_16(&tv, F16, vp, HD, prefix, Hkv, 64, BN, 1, CU_TENSOR_MAP_SWIZZLE_128B))
     return RF_ERR_CUDA;
-  return pair::launch_pair(tq, tk, tv, tq, p, p.split.clusters, st);
+  return pair::launch_pair(tq, tk, tv, tv, tq, p, p.split.clusters, st);
 }
 
 }  // namespace

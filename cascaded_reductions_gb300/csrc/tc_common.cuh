@@ -65,16 +65,17 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
 
 // Wait until the barrier phase with the given parity has completed.  Returns
 // false, without waiting further, once `abort` is set by any thread of the
-// CTA, or after kWaitLimitNs; in the latter case it sets `abort` and records
-// RF_ERR_TIMEOUT so that every other wait of the CTA gives up too.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// CTA, or after `limit` nanoseconds; in the latter case it sets `abort` and
+// records RF_ERR_TIMEOUT so that every other wait of the CTA gives up too.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          unsigned long long limit = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 31u) == 0) {
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (globaltimer_ns() - t0 > limit) {
         *abort = 1;
         atomicExch(&g_timeout_status, (int)RF_ERR_TIMEOUT);
         return false;
