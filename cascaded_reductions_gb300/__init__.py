@@ -140,9 +140,10 @@ _CACHE_DTYPES = {torch.float32: RF_F32, torch.bfloat16: RF_BF16, torch.float16: 
 
 
 def _cache_dtype(dt, name):
-    if dt not in _CACHE_DTYPES:
+    code = _CACHE_DTYPES.get(dt)
+    if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {dt}")
-    return _CACHE_DTYPES[dt]
+    return code
 
 
 # the current stream's handle and the current device, without making objects of
@@ -161,7 +162,7 @@ def _device_of(t, name):
 
 def _on(dev, t, dtype, shape, name):
     """``t`` as it has to be: on device ``dev`` (an index), of a type and shape, contiguous."""
-    if (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return
     _need(t, dtype, name, shape)
     raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}: one call works on one device")
@@ -540,14 +541,9 @@ def rf_attn_decode_shared(q, kp, vp, k, v, lens, Sp, S, scale, seg_m, seg_l, seg
              _cache_dtype(out.dtype, "out"), _addr(lse))
 
 
-def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight_out, lens_out,
-                   kept, stream=None):
-    """k/v [B, Hkv, cap, D] (fp32, bf16 or fp16; v None for a cache of one tensor), weight
-    [B, Hkv, cap] fp32, lens int32 [B] or None -> k_out/v_out [B, Hkv, cap_out, D], weight_out
-    [B, Hkv, cap_out], lens_out int32 [B], kept int32 [B, Hkv, keep]."""
+def _need_evict(dev, k, v, weight, lens, k_out, v_out, weight_out):
     if k.dim() != 4 or k_out.dim() != 4:
         raise ValueError("k and k_out must be [B, Hkv, rows, D]")
-    dev = _device_of(k, "k")
     B, Hkv, cap, D = k.shape
     cap_out = k_out.shape[2]
     dt = k.dtype
@@ -561,11 +557,21 @@ def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight
     _on(dev, weight_out, torch.float32, (B, Hkv, cap_out), "weight_out")
     if lens is not None:
         _on(dev, lens, torch.int32, (B,), "lens")
+
+
+def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight_out, lens_out,
+                   kept, stream=None):
+    """k/v [B, Hkv, cap, D] (fp32, bf16 or fp16; v None for a cache of one tensor), weight
+    [B, Hkv, cap] fp32, lens int32 [B] or None -> k_out/v_out [B, Hkv, cap_out, D], weight_out
+    [B, Hkv, cap_out], lens_out int32 [B], kept int32 [B, Hkv, keep]."""
+    dev = _device_of(k, "k")
+    _need_evict(dev, k, v, weight, lens, k_out, v_out, weight_out)
+    B, Hkv, cap, D = k.shape
     _on(dev, lens_out, torch.int32, (B,), "lens_out")
     _on(dev, kept, torch.int32, (B, Hkv, keep), "kept")
     _call_on(dev, stream, "rf_cache_evict", _lib.rf_cache_evict, k.data_ptr(), _addr(v),
-             weight.data_ptr(), _addr(lens), B, Hkv, cap, D, _cache_dtype(dt, "k"), keep, sinks,
-             recent, cap_out, k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
+             weight.data_ptr(), _addr(lens), B, Hkv, cap, D, _cache_dtype(k.dtype, "k"), keep,
+             sinks, recent, k_out.shape[2], k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
              lens_out.data_ptr(), kept.data_ptr())
 
 
@@ -684,15 +690,13 @@ class DecodeWorkspace(typing.NamedTuple):
     seg_acc: torch.Tensor
     counters: torch.Tensor
     scores: torch.Tensor
-    sizes: tuple        # (device index, B, H, Hkv, D), and cap with scores
+    sizes: tuple        # (device index, B, H, Hkv, D)
     addresses: tuple    # of seg_m, seg_l, seg_acc, counters
 
-    def scratch(self, *sizes):
-        """The scratch addresses, for a call of these sizes."""
-        if sizes != self.sizes[:len(sizes)]:
-            raise ValueError(f"work was made for (device, B, H, Hkv, D, cap) = {self.sizes}, "
+    def check(self, *sizes):
+        if sizes != self.sizes:
+            raise ValueError(f"work was made for (device, B, H, Hkv, D) = {self.sizes}, "
                              f"the call has {sizes}")
-        return self.addresses
 
 
 def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights=False, S=None,
@@ -714,7 +718,7 @@ def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights
         counters = torch.zeros(B * Hkv * (-(-(H // Hkv) // 16)), device=dev, dtype=torch.int32)
         scores = torch.empty(B, H, cap, **f32) if weights else None
         return DecodeWorkspace(S, prefix_S, seg_m, seg_l, seg_acc, counters, scores,
-                               (dev.index, B, H, Hkv, D, cap if weights else None),
+                               (dev.index, B, H, Hkv, D),
                                tuple(t.data_ptr() for t in (seg_m, seg_l, seg_acc, counters)))
 
 
@@ -745,12 +749,12 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if work is None:
         work = decode_workspace(B, H, Hkv, cap, D, window=window, sinks=sinks, device=q.device)
-    m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
+    work.check(dev, B, H, Hkv, D)
     out, lse = _outputs(q, out_dtype)
     _call_on(dev, None, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
              k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, work.S,
-             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
-             counters, out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
+             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
+             out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
 
@@ -783,12 +787,12 @@ def attn_decode_shared(q, kp, vp, k, v, lens=None, scale=None, work=None, out_dt
     _on(dev, vp, q.dtype, kp.shape, "vp")
     if work is None:
         work = decode_workspace(B, H, Hkv, cap, D, prefix=prefix, device=q.device)
-    m, l, acc, counters = work.scratch(dev, B, H, Hkv, D)
+    work.check(dev, B, H, Hkv, D)
     out, lse = _outputs(q, out_dtype)
     _call_on(dev, None, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
              kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B,
              H, Hkv, cap, D, work.prefix_S, work.S, D ** -0.5 if scale is None else scale,
-             _cache_dtype(q.dtype, "q"), m, l, acc, counters, out.data_ptr(),
+             _cache_dtype(q.dtype, "q"), *work.addresses, out.data_ptr(),
              _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
@@ -808,7 +812,9 @@ def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, 
         _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
     if work is None:
         work = decode_workspace(B, H, Hkv, cap, D, weights=True, device=q.device)
-    m, l, acc, counters = work.scratch(dev, B, H, Hkv, D, cap)
+    work.check(dev, B, H, Hkv, D)
+    if work.scores is None or work.scores.shape[2] != cap:
+        raise ValueError("work must come from decode_workspace(..., cap, weights=True)")
     out, lse = _outputs(q, out_dtype)
     if weight_out is None:
         weight_out = torch.empty((B, Hkv, cap), device=q.device, dtype=torch.float32)
@@ -816,10 +822,9 @@ def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, 
         _on(dev, weight_out, torch.float32, (B, Hkv, cap), "weight_out")
     _call_on(dev, None, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
              k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, work.S,
-             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), m, l, acc,
-             counters, work.scores.data_ptr(), out.data_ptr(),
-             _cache_dtype(out.dtype, "out"), lse.data_ptr(), _addr(weight),
-             weight_out.data_ptr())
+             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
+             work.scores.data_ptr(), out.data_ptr(), _cache_dtype(out.dtype, "out"),
+             lse.data_ptr(), _addr(weight), weight_out.data_ptr())
     return out, lse, weight_out
 
 
@@ -832,14 +837,22 @@ def cache_evict(k, v, weight, lens, keep, sinks=0, recent=0, cap_out=None, out=N
     default), lens_out [B] and kept [B, Hkv, keep] (source rows, -1 behind a short sequence)."""
     if stream is not None:
         return _within(stream, k, cache_evict, k, v, weight, lens, keep, sinks, recent, cap_out, out)
+    if k.dim() != 4:
+        raise ValueError("k must be [B, Hkv, rows, D]")
+    dev = _device_of(k, "k")
     B, Hkv, cap, D = k.shape
-    dev = k.device
     if out is None:
         rows = keep if cap_out is None else cap_out
-        out = (torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
-               None if v is None else torch.zeros(B, Hkv, rows, D, device=dev, dtype=k.dtype),
-               torch.zeros(B, Hkv, rows, device=dev, dtype=torch.float32))
-    lens_out = torch.empty(B, device=dev, dtype=torch.int32)
-    kept = torch.empty(B, Hkv, keep, device=dev, dtype=torch.int32)
-    rf_cache_evict(k, v, weight, lens, keep, sinks, recent, *out, lens_out, kept)
-    return (*out, lens_out, kept)
+        new = dict(device=k.device, dtype=k.dtype)
+        out = (torch.zeros(B, Hkv, rows, D, **new),
+               None if v is None else torch.zeros(B, Hkv, rows, D, **new),
+               torch.zeros(B, Hkv, rows, device=k.device))
+    k_out, v_out, weight_out = out
+    _need_evict(dev, k, v, weight, lens, k_out, v_out, weight_out)
+    new = dict(device=k.device, dtype=torch.int32)
+    lens_out, kept = torch.empty(B, **new), torch.empty((B, Hkv, keep), **new)
+    _call_on(dev, None, "rf_cache_evict", _lib.rf_cache_evict, k.data_ptr(), _addr(v),
+             weight.data_ptr(), _addr(lens), B, Hkv, cap, D, _cache_dtype(k.dtype, "k"), keep,
+             sinks, recent, k_out.shape[2], k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
+             lens_out.data_ptr(), kept.data_ptr())
+    return k_out, v_out, weight_out, lens_out, kept

@@ -46,6 +46,7 @@ struct Evict {
   int32_t* kept;
 };
 
+template <bool IN_SMEM>            // whether every row's keys fit in shared memory
 __global__ void __launch_bounds__(SEL_THREADS)
 evict_select_kernel(const Evict a) {
   extern __shared__ uint32_t keys[];
@@ -78,13 +79,12 @@ evict_select_kernel(const Evict a) {
   int need = a.keep - first - (len - last);
   const int n = last - first;
   const size_t w0 = (size_t)group * a.cap + first;
-  const bool in_smem = n <= SEL_KEYS;
   const size_t weights = (size_t)a.B * a.Hkv * a.cap;
   (void)weights;
   auto load = [&](int i) -> uint32_t {
     return RF_IDX_OK(w0 + i, weights) ? order_key(a.weight[w0 + i]) : 0u;
   };
-  auto key = [&](int i) -> uint32_t { return in_smem ? keys[i] : load(i); };
+  auto key = [&](int i) -> uint32_t { return IN_SMEM ? keys[i] : load(i); };
 
   // Adds up hist[] and finds the digit at which the count from the top reaches
   // `need`: what is still needed of that digit's keys, and how many there are.
@@ -128,7 +128,7 @@ evict_select_kernel(const Evict a) {
     clear();
     for (int i = tid; i < n; i += SEL_THREADS) {
       const uint32_t k = load(i);
-      if (in_smem) keys[i] = k;
+      if (IN_SMEM) keys[i] = k;
       atomicAdd(&hist[k >> 21], 1u);
     }
     pick_digit();
@@ -152,7 +152,7 @@ evict_select_kernel(const Evict a) {
       pick_digit();
       prefix |= sh_digit << shift;
     }
-  } else if (in_smem) {
+  } else if (IN_SMEM) {
     for (int i = tid; i < n; i += SEL_THREADS) keys[i] = load(i);
   }
   __syncthreads();
@@ -161,12 +161,14 @@ evict_select_kernel(const Evict a) {
   const int per = ((n + SEL_WARPS - 1) / SEL_WARPS + 31) & ~31;
   const int i_begin = min(n, warp * per), i_end = min(n, i_begin + per);
   int ca = 0, ce = 0;
-  for (int i0 = i_begin; i0 < i_end; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < i_end ? key(i) : 0u;
-    ca += __popc(__ballot_sync(0xffffffffu, i < i_end && k > prefix));
-    ce += __popc(__ballot_sync(0xffffffffu, i < i_end && k == prefix));
+#pragma unroll 4
+  for (int i = i_begin + lane; i < i_end; i += 32) {
+    const uint32_t k = key(i);
+    ca += k > prefix;
+    ce += k == prefix;
   }
+  ca = __reduce_add_sync(0xffffffffu, ca);
+  ce = __reduce_add_sync(0xffffffffu, ce);
   if (lane == 0) {
     above[warp] = ca;
     equal[warp] = ce;
@@ -265,10 +267,15 @@ rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
   const long long blocks = ((long long)keep + rows * COPY_UNROLL - 1) / (rows * COPY_UNROLL);
   if (blocks * 2 * B * Hkv > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
   static std::atomic<uint64_t> done{0};
-  if (smem_attr(evict_select_kernel, SEL_KEYS * sizeof(uint32_t), done) != RF_OK) return RF_ERR_CUDA;
-  const int held = cap < SEL_KEYS ? cap : SEL_KEYS;
-  evict_select_kernel<<<(unsigned)(B * Hkv), SEL_THREADS, (size_t)held * sizeof(uint32_t), st>>>(
-      Evict{weight, lens, B, Hkv, cap, keep, sinks, recent, lens_out, kept});
+  const Evict e{weight, lens, B, Hkv, cap, keep, sinks, recent, lens_out, kept};
+  if (cap <= SEL_KEYS) {
+    if (smem_attr(evict_select_kernel<true>, SEL_KEYS * sizeof(uint32_t), done) != RF_OK)
+      return RF_ERR_CUDA;
+    evict_select_kernel<true>
+        <<<(unsigned)(B * Hkv), SEL_THREADS, (size_t)cap * sizeof(uint32_t), st>>>(e);
+  } else {
+    evict_select_kernel<false><<<(unsigned)(B * Hkv), SEL_THREADS, 0, st>>>(e);
+  }
   const rf_status s = launch_status();
   if (s != RF_OK) return s;
   return launch_after(evict_copy_kernel, (unsigned)(blocks * 2 * B * Hkv), COPY_THREADS, 0, st,
