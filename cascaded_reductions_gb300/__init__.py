@@ -8,7 +8,10 @@ current stream.  A status other than RF_OK raises :class:`RFError`.
 
 The convenience wrappers (``attn_decode``, ``softmax_topk``,
 ``absmax_quant_fp8_gemm``, ``attn_prefill``) only allocate the output tensors
-with torch and call the entry points.
+with torch and call the entry points; so do ``attn_prefill_window``,
+``attn_decode_window``, ``attn_decode_shared``, ``attn_decode_weights`` and
+``cache_evict``, which work over a serving cache of grouped heads, with scratch
+from ``decode_workspace`` where a loop keeps it.
 
 There is no fallback: importing this package fails if librf.so has not been
 built (``cascaded_reductions_gb300._build.build()``).  The environment
@@ -183,6 +186,11 @@ def _call_on(dev, stream, where, fn, *args):
             status = fn(*args, ptr)
     if status != RF_OK:
         raise RFError(status, where)
+
+
+def _i32(n):
+    """A count for a C int: one too large for it is as good as the largest."""
+    return n if -1 <= n <= 0x7fffffff else (0x7fffffff if n > 0 else -1)
 
 
 def _addr(t):
@@ -469,8 +477,8 @@ def rf_attn_decode_window(q, k, v, lens, window, sinks, S, scale, seg_m, seg_l, 
     if lse is not None:
         _on(dev, lse, torch.float32, (B, H), "lse")
     _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, S, scale,
-             _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
+             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, _i32(window),
+             _i32(sinks), S, scale, _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
              counters.data_ptr(), out.data_ptr(), _cache_dtype(out.dtype, "out"), _addr(lse))
 
 
@@ -511,7 +519,7 @@ def rf_attn_prefill_window(q, k, v, window, sinks, scale, out, lse=None, stream=
     if lse is not None:
         _on(dev, lse, torch.float32, (B, H, N), "lse")
     _call_on(dev, stream, "rf_attn_prefill_window", _lib.rf_attn_prefill_window, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), B, H, Hkv, N, L, D, window, sinks, scale,
+             k.data_ptr(), v.data_ptr(), B, H, Hkv, N, L, D, _i32(window), _i32(sinks), scale,
              _cache_dtype(dt, "q"), out.data_ptr(), _addr(lse))
 
 
@@ -752,8 +760,8 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
     work.check(dev, B, H, Hkv, D)
     out, lse = _outputs(q, out_dtype)
     _call_on(dev, None, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, window, sinks, work.S,
-             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
+             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, _i32(window),
+             _i32(sinks), work.S, D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
              out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 

@@ -18,9 +18,9 @@
 // has read S(j) into registers, and runs on the tensor pipe while the
 // softmax of block j is still exponentiating: the pipe order is
 // S(0) S(1) PV(0) S(2) PV(1) ...  The kernel is persistent (one cluster per
-// pair of SMs), and the numbering of blocks runs on across items, so the
-// first S of the next item is computed while the softmax warps write the
-// current item's output.
+// pair of SMs), and the numbering of blocks runs on across items: the next
+// item's first S is computed during the current item's last softmax, and its
+// first softmax while the output warps still write the current item's rows.
 //
 // TMEM (512 columns, allocated for the pair): S 0-255, P 256-383 (bf16 pairs,
 // key pair (2c, 2c + 1) in column c), O 384-511.
@@ -40,7 +40,10 @@
 // Two softmax warps per SM sub-partition (not four) leave the MMA-issuing
 // thread, which shares a sub-partition with two of them, enough issue slots
 // for the 64-cycle P V MMAs.  Their threads hold 128 scores each, so the
-// registers are divided unevenly between the warpgroups.
+// registers are divided unevenly between the warpgroups.  Output by the softmax
+// warps themselves took 1300 to 1900 cycles of an item's first block (code that
+// runs once per item comes cold from the instruction cache): 569 us instead of
+// 536 for 4 x 32 heads of 8192 with a window of 1024.
 // Rescaling is lazy: the reference max m_ref of a row moves (and O and l are
 // multiplied by exp2(m_ref_old - m_ref_new)) only when the block max exceeds
 // it by more than 8, so p <= 2^8.

@@ -28,16 +28,19 @@
 // into pieces by its own length, one CTA of four warps each; a step of the CTA
 // is 64 keys, a tile per warp.  Warps merge through shared memory, pieces
 // through state slots in memory: in small calls by the last CTA of the group to
-// arrive (no second launch), in large ones by merge_kernel, because the fence
-// and the count cost a CTA that streams about 2 us (@@).
+// arrive (no second launch), in large ones by merge_kernel, launched to begin
+// beside the last CTAs, because the fence and the count hold up the end of a
+// CTA (a shared-prefix step of 128 sequences: 115 us with them, 103 us without).
 // Both merge in order: the same lengths give the same bits.
 //
-// Also built and measured for large calls (64 sequences, 8 key heads, 4100
-// visible keys each, 1.07 GB; pure streaming by the same copies 153 us): equal
-// contiguous shares of all tiles per warp, 173 us, or per CTA, 166 us (SMs
-// stream at rates up to 10 % apart, which equal shares wait for), and per-warp
-// shares with smaller units taken later from a queue, 188 us (a warp holds an
-// eighth of an SM's bandwidth, so even a unit of six tiles takes 10 us).
+// Measured (64 sequences, 8 key heads, 4100 visible keys each, 1.07 GB): 158 us,
+// 6.8 TB/s, the card's copy rate, with pieces of 768 keys or more; 170 us with
+// 512, where a CTA's start and end weigh more.  Pure streaming by the same
+// copies takes 153 us.  Also built: equal contiguous shares of all tiles per
+// warp, 173 us, or per CTA, 166 us (SMs stream at rates up to 10 % apart, which
+// equal shares wait for), and per-warp shares with smaller units taken later
+// from a queue, 188 us (a warp holds an eighth of an SM's bandwidth, so even a
+// unit of six tiles takes 10 us).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

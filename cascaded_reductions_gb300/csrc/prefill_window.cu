@@ -303,7 +303,10 @@ struct WindowPrefill {
     }
   }
   __device__ __forceinline__ void after(bool any, int cluster, int nclusters, int rank, int r) const {
-    if (__any_sync(0xffffffffu, any)) repair(cluster, nclusters, rank, r);
+    if (!__any_sync(0xffffffffu, any)) return;
+    // the outputs were written by bulk copies; they are read as memory now
+    asm volatile("fence.proxy.async;" ::: "memory");
+    repair(cluster, nclusters, rank, r);
   }
 };
 
