@@ -74,12 +74,10 @@
 //   keys(it, j)                256, or 128 or 64 where no row sees the block's
 //                              other keys: its products stop there
 //   v_bytes(it, j)             bytes that load_v copies (with one map or both)
-//   PARTIAL, words(it, j, rank, row, kh)  with PARTIAL, which of the warp's 128
-//                              keys (128 kh ..) of block j its rows may see: 4
-//                              (32-key words, all), 2 (the first two; keys is
-//                              64) or 0; 4 for block 0
-//   mask<NW>(it, j, rank, row, kh, s)  sets hidden scores of the first 32 NW of
-//                              them to -inf
+//   PARTIAL, sees(it, j, rank, row, kh)  with PARTIAL, whether the warp's rows
+//                              see any of its 128 keys (128 kh ..) of block j;
+//                              true for block 0
+//   mask(it, j, rank, row, kh, s)  sets their hidden scores to -inf
 //   pending(it, rank, row)     what an output row needs beside its values, and
 //   store(pend, col, v, m, l)  its columns col .. + 31 from O, with the row's
 //                              reference m (log2 units) and sum l
@@ -296,9 +294,8 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int t = 0; ok; ++t) {
       if (!p.item(t, cluster, nclusters, it)) break;
       float m_ref = P::M_START, l = 0.f;
-      // One block, of which this warp's rows see keys in the first NW 32-key
-      // words of its 128 only; false if a wait gave up.  With NW < 4 it is not
-      // the item's first block.
+      // One block, of which this warp's rows see some of its 128 keys (NW = 4
+      // 32-key words) or none (NW = 0); false if a wait gave up.
       auto block = [&](auto words, int j) -> bool {
         constexpr int NW = decltype(words)::value;
         if (!tc::mbar_wait(&sh->s_full, g & 1u, abort)) return false;
@@ -317,7 +314,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (lane == 0) arrive_cluster_relaxed(s_free0);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if constexpr (NW > 0) {
-          p.template mask<NW>(it, j, rank, r, kh, s);
+          p.mask(it, j, rank, r, kh, s);
 #pragma unroll
           for (int c = 0; c < 32 * NW; c += 2)
             mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], s[c], s[c + 1]);
@@ -390,8 +387,8 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       };
       for (int j = 0; ok && j < it.n; ++j, ++g) {
         if constexpr (P::PARTIAL) {
-          const int words = p.words(it, j, rank, r, kh);
-          ok = words == 4 ? block(Words<4>{}, j) : words == 2 ? block(Words<2>{}, j) : block(Words<0>{}, j);
+          const bool some = p.sees(it, j, rank, r, kh);
+          ok = some ? block(Words<4>{}, j) : block(Words<0>{}, j);
         } else {
           ok = block(Words<4>{}, j);
         }

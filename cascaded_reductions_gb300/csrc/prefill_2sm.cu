@@ -72,9 +72,8 @@ struct CausalPrefill {
     tc::tma_load_2d_pair(dst, map, bar, rank * 64, it.key0 + j * BN);
   }
   __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
-  template <int NW>
   __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
-                                       float (&s)[32 * NW]) const {
+                                       float (&s)[128]) const {
     const int NKB = (N + BN - 1) / BN;
     if (causal && j == it.n - 1) {
       const int lim = BM * rank + r - kh * 128;

@@ -136,19 +136,17 @@ struct WindowPrefill {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   }
   // A warp whose rows see none of its keys of a block (half of those at the two
-  // edges) skips its scores; of a narrow block there are 64 keys.
-  __device__ __forceinline__ int words(const Item& it, int j, int rank, int r, int kh) const {
-    if (j >= it.nb) return keys(it, j) == BN ? 4 : kh == 1 ? 0 : it.mixed ? 4 : 2;
+  // edges) skips its scores.
+  __device__ __forceinline__ bool sees(const Item& it, int j, int rank, int r, int kh) const {
+    if (j >= it.nb) return kh == 0 || keys(it, j) == BN;
     const int base = key0(it, j) + kh * 128;
     const int first = L - N + it.row0 + row_of(rank, r & ~31), last = first + 31;
-    const bool some = last >= base && (first - window + 1 < base + 128 || sinks > base);
-    return some || j == 0 ? 4 : 0;
+    return j == 0 || (last >= base && (first - window + 1 < base + 128 || sinks > base));
   }
   // A word of visible keys per row and 32 of them; an edge crosses a warp's 32
   // rows within one or two words.
-  template <int NW>
   __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
-                                       float (&s)[32 * NW]) const {
+                                       float (&s)[128]) const {
     const int base = key0(it, j) + kh * 128;
     const int p = L - N + it.row0 + row_of(rank, r);    // this row's position
     const int first = p - (r & 31), last = first + 31;   // the warp's positions
@@ -158,7 +156,7 @@ struct WindowPrefill {
       if (first - base >= 127 && last - window + 1 <= base) return;
     } else if (j < it.nw) {
       hi = min(hi, it.rem - 1);                         // the rest is the next block's
-      if (NW == 4 && it.mixed) {                        // (and kh is 0)
+      if (it.mixed) {                                   // (and kh is 0)
         mask_words<0, 2>(hi, lo, cs, s);
         mask_words<2, 4>(pair::NARROW + it.limit - 1, 0, 0, s);
         return;
@@ -167,12 +165,12 @@ struct WindowPrefill {
       hi = 127, lo = 128, cs = it.limit - base;
       if (cs >= 128) return;
     }
-    mask_words<0, NW>(hi, lo, cs, s);
+    mask_words<0, 4>(hi, lo, cs, s);
   }
   // words Q0 .. Q1 - 1 of s: visible are keys [lo, hi], and of those up to hi the
   // ones below cs
-  template <int Q0, int Q1, int C>
-  static __device__ __forceinline__ void mask_words(int hi, int lo, int cs, float (&s)[C]) {
+  template <int Q0, int Q1>
+  static __device__ __forceinline__ void mask_words(int hi, int lo, int cs, float (&s)[128]) {
 #pragma unroll
     for (int q = Q0; q < Q1; ++q) {
       const uint32_t vis = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));

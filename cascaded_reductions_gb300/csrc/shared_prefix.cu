@@ -100,9 +100,8 @@ struct PrefixStates {
     tc::tma_load_3d_pair(dst, map, bar, rank * 64, (it.block0 + j) * BN, it.hk);
   }
   __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
-  template <int NW>
   __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh,
-                                       float (&s)[32 * NW]) const {
+                                       float (&s)[128]) const {
     (void)rank;
     (void)r;
     const int lim = P - (it.block0 + j) * BN - kh * 128;
