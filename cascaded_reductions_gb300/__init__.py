@@ -95,6 +95,33 @@ def load_library(path=LIB_PATH):
 _lib = load_library()
 
 
+def _load_calls():
+    """The extension built from csrc/calls.cpp, or None: the wrappers below then marshal the
+    same calls in Python."""
+    from . import _build
+    path, _ = _build.calls_path()
+    if path is None or not os.path.exists(path):
+        return None
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("_rf_calls", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_rf_calls", loader))
+    loader.exec_module(module)
+    return module
+
+
+_calls = _load_calls()
+
+
+def _entry(name):
+    return ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
+
+
+(_DECODE_WINDOW, _PREFILL_WINDOW, _DECODE_SHARED, _DECODE_WEIGHTS, _CACHE_EVICT) = map(
+    _entry, ("rf_attn_decode_window", "rf_attn_prefill_window", "rf_attn_decode_shared",
+             "rf_attn_decode_weights", "rf_cache_evict"))
+
+
 class RFError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -739,6 +766,13 @@ def _within(stream, t, call, *args, **kwargs):
         return call(*args, **kwargs)
 
 
+def _done(r, where):
+    """The outputs of a quick call, whose result is a status where it was refused."""
+    if type(r) is not tuple:
+        raise RFError(r, where)
+    return r
+
+
 def _outputs(q, out_dtype):
     out = torch.empty_like(q) if out_dtype is None else torch.empty_like(q, dtype=out_dtype)
     return out, torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
@@ -754,6 +788,11 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
     if stream is not None:
         return _within(stream, q, attn_decode_window, q, k, v, lens, window, sinks, scale, work,
                        out_dtype)
+    if _calls is not None and work is not None and out_dtype is None:
+        r = _calls.decode_window(_DECODE_WINDOW, q, k, v, lens, window, sinks, scale, work.S, work.sizes,
+                                 work.addresses)
+        if r is not None:
+            return _done(r, "rf_attn_decode_window")
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if work is None:
         work = decode_workspace(B, H, Hkv, cap, D, window=window, sinks=sinks, device=q.device)
@@ -773,6 +812,10 @@ def attn_prefill_window(q, k, v, window=0, sinks=0, scale=None, stream=None):
     q [B, H, N, D], k/v [B, Hkv, L, D] (bf16 or fp16).  Returns out [B, H, N, D] and lse [B, H, N]."""
     if stream is not None:
         return _within(stream, q, attn_prefill_window, q, k, v, window, sinks, scale)
+    if _calls is not None:
+        r = _calls.prefill_window(_PREFILL_WINDOW, q, k, v, window, sinks, scale)
+        if r is not None:
+            return _done(r, "rf_attn_prefill_window")
     out, lse = _outputs(q, None)
     rf_attn_prefill_window(q, k, v, window, sinks, q.shape[-1] ** -0.5 if scale is None else scale,
                            out, lse)
@@ -787,6 +830,11 @@ def attn_decode_shared(q, kp, vp, k, v, lens=None, scale=None, work=None, out_dt
     prefix (None: cap; 0 allowed).  Returns out [B, H, D] and lse [B, H]."""
     if stream is not None:
         return _within(stream, q, attn_decode_shared, q, kp, vp, k, v, lens, scale, work, out_dtype)
+    if _calls is not None and work is not None and out_dtype is None:
+        r = _calls.decode_shared(_DECODE_SHARED, q, kp, vp, k, v, lens, scale, work.prefix_S, work.S,
+                                 work.sizes, work.addresses)
+        if r is not None:
+            return _done(r, "rf_attn_decode_shared")
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if kp.dim() != 3:
         raise ValueError("kp must be [Hkv, prefix, D]")
@@ -815,6 +863,11 @@ def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, 
     if stream is not None:
         return _within(stream, q, attn_decode_weights, q, k, v, lens, weight, scale, work, weight_out,
                        out_dtype)
+    if _calls is not None and work is not None and out_dtype is None and weight_out is None:
+        r = _calls.decode_weights(_DECODE_WEIGHTS, q, k, v, lens, weight, scale, work.S, work.sizes,
+                                  work.addresses, work.scores)
+        if r is not None:
+            return _done(r, "rf_attn_decode_weights")
     B, H, Hkv, cap, D, dev = _need_cache(q, k, v, lens)
     if weight is not None:
         _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
@@ -845,6 +898,10 @@ def cache_evict(k, v, weight, lens, keep, sinks=0, recent=0, cap_out=None, out=N
     default), lens_out [B] and kept [B, Hkv, keep] (source rows, -1 behind a short sequence)."""
     if stream is not None:
         return _within(stream, k, cache_evict, k, v, weight, lens, keep, sinks, recent, cap_out, out)
+    if _calls is not None and out is not None:
+        r = _calls.cache_evict(_CACHE_EVICT, k, v, weight, lens, keep, sinks, recent, *out)
+        if r is not None:
+            return (*out, *_done(r, "rf_cache_evict"))
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, rows, D]")
     dev = _device_of(k, "k")

@@ -2,14 +2,20 @@
 
 Each ``csrc/*.cu`` file compiles to an object in parallel; the objects link
 into ``cascaded_reductions_gb300/librf.so``.  A rebuild happens only when a
-source or header is newer than the library.
+source or header is newer than the library.  ``csrc/calls.cpp``, the quick way
+from Python into some of its calls, is compiled against the installed torch
+beside it.
 """
 
 import concurrent.futures
 import glob
+import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +27,47 @@ LIB = os.path.join(HERE, "librf.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills", "-I", INCLUDE, "-I", CSRC] + ARCH
+
+
+def calls_path():
+    """Where the Python calls' extension for the installed torch lies (its file name carries the
+    interpreter's tag and a hash of torch's version), and torch's folder; (None, None) without
+    torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None, None
+    torch = list(spec.submodule_search_locations)[0]
+    with open(os.path.join(torch, "version.py"), "rb") as f:
+        tag = hashlib.sha256(f.read()).hexdigest()[:12]
+    return os.path.join(HERE, f"_rf_calls_{sys.implementation.cache_tag}_{tag}.so"), torch
+
+
+def build_calls(force=False):
+    """Compile csrc/calls.cpp with the host compiler against the installed torch.  The package
+    does without it (the same calls, marshalled in Python), so a failure is told and not raised."""
+    path, torch = calls_path()
+    src = os.path.join(CSRC, "calls.cpp")
+    if path is None or (not force and not _stale(path, [src] + _headers())):
+        return path
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [INCLUDE, os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", src, "-o", path + ".tmp"]
+    cmd += [f"-I{i}" for i in inc]
+    cmd += ["-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        err = r.stderr if r.returncode else ""
+    except OSError as e:
+        err = str(e)
+    if err:
+        print(f"calls.cpp not built, the Python calls marshal in Python: {err[-2000:]}")
+        if os.path.exists(path):
+            os.remove(path)     # of an older rf.h
+        return None
+    os.replace(path + ".tmp", path)
+    return path
 
 
 def _nvcc():
@@ -68,16 +115,21 @@ def build(force=False, verbose=False, extra_flags=(), lib=None, objdir=None):
     srcs = _sources()
     hdrs = _headers()
     if not force and not _stale(lib, srcs + hdrs):
+        if lib == LIB:
+            build_calls()
         return lib
     nvcc = _nvcc()
     os.makedirs(objdir, exist_ok=True)
     objs = [os.path.join(objdir, os.path.basename(s)[:-3] + ".o") for s in srcs]
     jobs = []
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+        calls = ex.submit(build_calls, force) if lib == LIB else None
         for s, o in zip(srcs, objs):
             if force or _stale(o, [s] + hdrs):
                 jobs.append(ex.submit(_compile, nvcc, s, o, list(extra_flags)))
         logs = [j.result() for j in jobs]
+        if calls is not None:
+            calls.result()
     if verbose:
         for lg in logs:
             if lg:

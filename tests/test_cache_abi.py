@@ -185,3 +185,29 @@ def test_python_layer_refuses_cpu_tensors_and_bad_shapes():
                  lambda: rf.attn_decode_window(q[0], k, k), lambda: rf.decode_workspace(2, 7, 2, 10)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_quick_calls_leave_what_they_cannot_take_to_python():
+    import torch
+
+    from conftest import load_builder
+    load_builder().build()
+    import cascaded_reductions_gb300 as rf
+    if rf._calls is None:
+        pytest.skip("the extension is not built here")
+    q, k = torch.zeros(2, 8, 128), torch.zeros(2, 2, 100, 128)
+    w, sizes = torch.zeros(2, 2, 100), (0, 2, 8, 2, 128)
+    fn, work = rf._DECODE_WINDOW, (1, 1, 1, 1)
+    good = (fn, q, k, k, None, 0, 0, None, 1, sizes, work)
+    assert rf._calls.decode_window(*good) is None                      # tensors on the CPU
+    for i in range(len(good)):
+        for bad in (None, "x", 1.5, (), [1], object()):
+            assert rf._calls.decode_window(*good[:i], bad, *good[i + 1:]) is None
+    assert rf._calls.decode_window(*good[:-1]) is None
+    assert rf._calls.decode_window() is None
+    assert rf._calls.decode_shared(fn, q, k[0], k[0], k, k, None, None, 0, 1, sizes, work) is None
+    assert rf._calls.decode_weights(fn, q, k, k, None, w, None, 1, sizes, work, w) is None
+    assert rf._calls.prefill_window(fn, q[None], k, k, 0, 0, None) is None
+    assert rf._calls.cache_evict(fn, k, k, w, None, 10, 0, 0, k, k, w) is None
+    with pytest.raises(ValueError):
+        rf.attn_prefill_window(k, k, k)
