@@ -26,7 +26,9 @@
 //
 // Split: a row group (sequence, key head, 16-row tile of query heads) is divided
 // into pieces by its own length, one CTA of four warps each; a step of the CTA
-// is 64 keys, a tile per warp.  Warps merge through shared memory, pieces
+// is 64 keys, a tile per warp.  Warps merge through shared memory, a row per warp
+// and four columns per lane (1216 rows of 128 keys: 21.9 us; 26.6 us when one warp
+// took over the others' fragments, idle rows and all), pieces
 // through state slots in memory: in small calls by the last CTA of the group to
 // arrive (no second launch), in large ones by merge_kernel, launched to begin
 // beside the last CTAs, because the fence and the count hold up the end of a
@@ -61,6 +63,10 @@ constexpr int STAGE_BYTES = 2 * TK * ROW_BYTES;   // K tile, V tile
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int MROWS = 16;               // query heads per row group
 constexpr size_t SMEM_BYTES = (size_t)WARPS * RING_BYTES;
+// floats per row of the merge buffer: 8 more than a row has, so that the eight
+// rows of a fragment's store lie 8 banks apart
+constexpr int MERGE_PITCH = HD + 8;
+static_assert((size_t)WARPS * MROWS * MERGE_PITCH * 4 <= SMEM_BYTES, "the warps' accumulators reuse the rings");
 
 // 16 bytes (or, for bytes = 0, zeros) with an L2 eviction policy
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes,
@@ -324,43 +330,64 @@ struct State {
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
   }
 
-  // the warp's rows into out and lse (`direct`: this was the whole group) or
-  // into state slot `slot` of each row
-  __device__ __forceinline__ void write(const CacheDecode& a, const Rows& w, bool direct, int slot,
-                                        int lane) const {
-    const size_t states = (size_t)a.B * a.H * a.S_total;
-    (void)states;                                 // read by the checked build only
+  // the warp's rows into its part of the merge buffer
+  __device__ __forceinline__ void give(float* acc_buf, float2* ml_buf, const Rows& w, int lane) const {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = (lane >> 2) + 8 * half;
-      const size_t row = w.row0 + r;
-      if (r >= w.n || !RF_IDX_OK(row, (size_t)a.B * a.H)) continue;
-      const float m = half ? m1 : m0, l = half ? l1 : l0;
-      if (direct) {
+      if (r >= w.n) continue;
 #pragma unroll
-        for (int d = 0; d < HD / 8; ++d)
-          store_out2(a.out, row * HD + d * 8 + 2 * (lane & 3), normalised(acc[d][2 * half], l),
-                     normalised(acc[d][2 * half + 1], l), a.out_dtype);
-        if ((lane & 3) == 0) {
-          const float lse2 = m + log2f(l);
-          if (a.lse != nullptr) a.lse[row] = lse2 * kLn2;
-          if (SCORES && RF_IDX_OK(row * a.S_total, states)) a.seg_m[row * a.S_total] = lse2;
-        }
-      } else {
-        const size_t s = row * a.S_total + slot;
-        if (!RF_IDX_OK(s, states)) continue;
-#pragma unroll
-        for (int d = 0; d < HD / 8; ++d)
-          *reinterpret_cast<float2*>(a.seg_acc + s * HD + d * 8 + 2 * (lane & 3)) =
-              make_float2(acc[d][2 * half], acc[d][2 * half + 1]);
-        if ((lane & 3) == 0) {
-          a.seg_m[s] = m;
-          a.seg_l[s] = l;
-        }
-      }
+      for (int d = 0; d < HD / 8; ++d)
+        *reinterpret_cast<float2*>(acc_buf + r * MERGE_PITCH + d * 8 + 2 * (lane & 3)) =
+            make_float2(acc[d][2 * half], acc[d][2 * half + 1]);
+      if ((lane & 3) == 0) ml_buf[r] = half ? make_float2(m1, l1) : make_float2(m0, l0);
     }
   }
 };
+
+// Row r of the CTA's warps merged by one warp, four columns per lane, into out
+// and lse (`direct`: this was the whole group) or into the row's state `slot`.
+template <bool SCORES>
+__device__ __forceinline__ void merge_warps(const CacheDecode& a, const float* acc_buf,
+                                            const float2 (*ml_buf)[MROWS], size_t row, int r,
+                                            bool direct, int slot, int lane) {
+  if (!RF_IDX_OK(row, (size_t)a.B * a.H)) return;
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) M = fmaxf(M, ml_buf[i][r].x);
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    const float2 ml = ml_buf[i][r];
+    const float f = exp2f(ml.x - ref_of(M));
+    const float4 v = *reinterpret_cast<const float4*>(acc_buf + (i * MROWS + r) * MERGE_PITCH + lane * 4);
+    L = fmaf(f, ml.y, L);
+    A.x = fmaf(f, v.x, A.x);
+    A.y = fmaf(f, v.y, A.y);
+    A.z = fmaf(f, v.z, A.z);
+    A.w = fmaf(f, v.w, A.w);
+  }
+  const size_t states = (size_t)a.B * a.H * a.S_total;
+  (void)states;                                   // read by the checked build only
+  if (direct) {
+    const size_t o = row * HD + lane * 4;
+    store_out2(a.out, o, normalised(A.x, L), normalised(A.y, L), a.out_dtype);
+    store_out2(a.out, o + 2, normalised(A.z, L), normalised(A.w, L), a.out_dtype);
+    if (lane == 0) {
+      const float lse2 = M + log2f(L);
+      if (a.lse != nullptr) a.lse[row] = lse2 * kLn2;
+      if (SCORES && RF_IDX_OK(row * a.S_total, states)) a.seg_m[row * a.S_total] = lse2;
+    }
+  } else {
+    const size_t s = row * a.S_total + slot;
+    if (!RF_IDX_OK(s, states)) return;
+    *(reinterpret_cast<float4*>(a.seg_acc + s * HD) + lane) = A;
+    if (lane == 0) {
+      a.seg_m[s] = M;
+      a.seg_l[s] = L;
+    }
+  }
+}
 
 // Merges a group's rows, their states in order: the prefix's slots
 // 0 .. seg0 - 1 and this kernel's seg0 .. seg0 + pieces - 1.  One warp, four
@@ -456,23 +483,24 @@ __device__ __forceinline__ int pieces_of(const CacheDecode& a, int n) {
   return max(1, min(a.S, (n + a.piece_keys - 1) / a.piece_keys));
 }
 
-constexpr size_t MERGE_BYTES = (size_t)2 * MROWS * HD * 4;
-static_assert(MERGE_BYTES <= SMEM_BYTES, "two warps' accumulators reuse the rings");
-
 // One CTA per (group, piece); pieces that a group does not have return at once.
 template <bool F16, bool SCORES, bool FUSED>
 __global__ void __launch_bounds__(WARPS * 32, 2)
 cache_decode_kernel(const CacheDecode a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float4 sm_ml[2][8];
+  __shared__ float2 sm_ml[WARPS][MROWS];
   __shared__ int last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = (int)(blockIdx.x / a.S), piece = (int)(blockIdx.x - (unsigned)g * a.S);
   allow_dependents();
   const Group q = group_of(a, g);
   const int pieces = pieces_of(a, q.n);
+  // Done means that the prefix is done too.  Where a kernel of its own merges, one
+  // CTA's wait says so for all, and the others leave their SM to the rows that
+  // follow, so that SMs without a prefix cluster work on own keys all along.
+  const bool waits = FUSED || blockIdx.x == 0;
   if (piece >= pieces) {
-    wait_prerequisite();                // done means the prefix is done too
+    if (waits) wait_prerequisite();
     return;
   }
   const Rows w = rows_of(a, g);
@@ -508,46 +536,13 @@ cache_decode_kernel(const CacheDecode a) {
   st.close();
   __syncthreads();                      // the rings are free
 
-  // warps 2, 3 into 0, 1, then 1 into 0, fragment by fragment (every warp
-  // holds the same elements in the same lanes)
-  float4* mbuf = reinterpret_cast<float4*>(smem);
-  auto give = [&](int i) {
-#pragma unroll
-    for (int d = 0; d < HD / 8; ++d)
-      mbuf[(i * (HD / 8) + d) * 32 + lane] =
-          make_float4(st.acc[d][0], st.acc[d][1], st.acc[d][2], st.acc[d][3]);
-    if ((lane & 3) == 0) sm_ml[i][lane >> 2] = make_float4(st.m0, st.m1, st.l0, st.l1);
-  };
-  auto take = [&](int i) {
-    const float4 o = sm_ml[i][lane >> 2];
-    const float n0 = fmaxf(st.m0, o.x), n1 = fmaxf(st.m1, o.y);
-    const float c0 = exp2f(st.m0 - ref_of(n0)), c1 = exp2f(st.m1 - ref_of(n1));
-    const float f0 = exp2f(o.x - ref_of(n0)), f1 = exp2f(o.y - ref_of(n1));
-    st.m0 = n0;
-    st.m1 = n1;
-    st.l0 = fmaf(o.z, f0, st.l0 * c0);
-    st.l1 = fmaf(o.w, f1, st.l1 * c1);
-#pragma unroll
-    for (int d = 0; d < HD / 8; ++d) {
-      const float4 v = mbuf[(i * (HD / 8) + d) * 32 + lane];
-      st.acc[d][0] = fmaf(v.x, f0, st.acc[d][0] * c0);
-      st.acc[d][1] = fmaf(v.y, f0, st.acc[d][1] * c0);
-      st.acc[d][2] = fmaf(v.z, f1, st.acc[d][2] * c1);
-      st.acc[d][3] = fmaf(v.w, f1, st.acc[d][3] * c1);
-    }
-  };
-  if (warp >= 2) give(warp - 2);
-  __syncthreads();
-  if (warp < 2) take(warp);
-  __syncthreads();
-  if (warp == 1) give(0);
+  float* acc_buf = reinterpret_cast<float*>(smem);
+  st.give(acc_buf + warp * MROWS * MERGE_PITCH, sm_ml[warp], w, lane);
   __syncthreads();
   const bool direct = pieces == 1 && a.seg0 == 0;   // the output itself
-  if (warp == 0) {
-    take(0);
-    st.write(a, w, direct, a.seg0 + piece, lane);
-  }
-  wait_prerequisite();                  // the prefix's states, where there are some
+  for (int r = warp; r < w.n; r += WARPS)
+    merge_warps<SCORES>(a, acc_buf, sm_ml, w.row0 + r, r, direct, a.seg0 + piece, lane);
+  if (waits) wait_prerequisite();       // the prefix's states, where there are some
   if constexpr (FUSED) {
     if (direct) return;
     // the last piece to arrive merges the group's rows, a row per warp at a time
