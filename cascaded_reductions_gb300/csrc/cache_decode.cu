@@ -408,55 +408,63 @@ __device__ void merge_rows(const CacheDecode& a, size_t row0, int rows, int piec
       L[r] = 0.f;
       A[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int s = lane; s < n; s += 32)
-#pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        const size_t at = (row0 + r0 + r) * a.S_total + s;
-        if (r < nr && RF_IDX_OK(at, states)) M[r] = fmaxf(M[r], __ldcg(a.seg_m + at));
-      }
-#pragma unroll
-    for (int r = 0; r < RB; ++r) M[r] = group_max<32>(M[r]);
     for (int s0 = 0; s0 < n; s0 += 32) {
-      // lane j holds state s0 + j's weight; -1 marks one without keys
-      float f[RB];
+      const int cnt = min(32, n - s0);
+      // lane j holds state s0 + j's maximum and sum, then its weight; -1 marks one
+      // without keys.  The accumulators are asked for before the weights are known:
+      // one wait for memory instead of three (1 sequence of 1028 visible keys:
+      // 6.8 -> 5.7 us).
+      float ms[RB], ls[RB], f[RB];
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        f[r] = -1.f;
+        ms[r] = -INFINITY;
+        ls[r] = 0.f;
         const size_t at = (row0 + r0 + r) * a.S_total + s0 + lane;
-        if (r < nr && s0 + lane < n && RF_IDX_OK(at, states)) {
-          const float ms = __ldcg(a.seg_m + at), ls = __ldcg(a.seg_l + at);
-          if (ms != -INFINITY) {
-            f[r] = exp2f(ms - ref_of(M[r]));
-            L[r] = fmaf(f[r], ls, L[r]);
-          } else {
-            L[r] += ls;                           // 0, or NaN where every score was NaN
-          }
+        if (r < nr && lane < cnt && RF_IDX_OK(at, states)) {
+          ms[r] = __ldcg(a.seg_m + at);
+          ls[r] = __ldcg(a.seg_l + at);
         }
       }
-      const int cnt = min(32, n - s0);
       for (int j0 = 0; j0 < cnt; j0 += SB) {
         float4 v[RB][SB];
-        float fj[RB][SB];
 #pragma unroll
         for (int j = 0; j < SB; ++j)
 #pragma unroll
           for (int r = 0; r < RB; ++r) {
-            fj[r][j] = __shfl_sync(0xffffffffu, f[r], (j0 + j) & 31);
-            if (j0 + j >= cnt) fj[r][j] = -1.f;
             const size_t at = (row0 + r0 + r) * a.S_total + s0 + j0 + j;
             v[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (fj[r][j] != -1.f && RF_SPAN_OK(at * HD + lane * 4, 4, states * HD))
+            if (r < nr && j0 + j < cnt && RF_SPAN_OK(at * HD + lane * 4, 4, states * HD))
               v[r][j] = __ldcg(reinterpret_cast<const float4*>(a.seg_acc + at * HD) + lane);
           }
+        if (j0 == 0) {
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            const float top = fmaxf(M[r], group_max<32>(ms[r])), c = exp2f(M[r] - ref_of(top));
+            M[r] = top;
+            L[r] *= c;
+            A[r].x *= c;
+            A[r].y *= c;
+            A[r].z *= c;
+            A[r].w *= c;
+            f[r] = -1.f;
+            if (ms[r] != -INFINITY) {
+              f[r] = exp2f(ms[r] - ref_of(top));
+              L[r] = fmaf(f[r], ls[r], L[r]);
+            } else {
+              L[r] += ls[r];                      // 0, or NaN where every score was NaN
+            }
+          }
+        }
 #pragma unroll
         for (int j = 0; j < SB; ++j)
 #pragma unroll
           for (int r = 0; r < RB; ++r) {
-            if (fj[r][j] == -1.f) continue;
-            A[r].x = fmaf(fj[r][j], v[r][j].x, A[r].x);
-            A[r].y = fmaf(fj[r][j], v[r][j].y, A[r].y);
-            A[r].z = fmaf(fj[r][j], v[r][j].z, A[r].z);
-            A[r].w = fmaf(fj[r][j], v[r][j].w, A[r].w);
+            const float fj = __shfl_sync(0xffffffffu, f[r], (j0 + j) & 31);
+            if (j0 + j >= cnt || fj == -1.f) continue;
+            A[r].x = fmaf(fj, v[r][j].x, A[r].x);
+            A[r].y = fmaf(fj, v[r][j].y, A[r].y);
+            A[r].z = fmaf(fj, v[r][j].z, A[r].z);
+            A[r].w = fmaf(fj, v[r][j].w, A[r].w);
           }
       }
     }
@@ -545,18 +553,20 @@ cache_decode_kernel(const CacheDecode a) {
   if (waits) wait_prerequisite();       // the prefix's states, where there are some
   if constexpr (FUSED) {
     if (direct) return;
-    // the last piece to arrive merges the group's rows, a row per warp at a time
-    __threadfence();
+    // the last piece to arrive merges the group's rows, a row per warp at a time;
+    // thread 0's fences stand for the CTA, which its barriers join
     __syncthreads();
     if (threadIdx.x == 0) {
       int seen = 0;
-      if (pieces > 1)
+      if (pieces > 1) {
+        __threadfence();
         seen = RF_IDX_OK(g, (size_t)a.B * a.Hkv * a.mtiles) ? atomicAdd(a.counters + g, 1) : -1;
+        __threadfence();
+      }
       last = seen == pieces - 1;
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
     for (int r = warp; r < w.n; r += WARPS) merge_rows<1, SCORES>(a, w.row0 + r, 1, pieces, lane);
     if (threadIdx.x == 0 && pieces > 1 && RF_IDX_OK(g, (size_t)a.B * a.Hkv * a.mtiles))
       a.counters[g] = 0;
