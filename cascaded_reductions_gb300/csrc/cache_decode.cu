@@ -568,7 +568,17 @@ cache_decode_kernel(const CacheDecode a) {
     }
     __syncthreads();
     if (!last) return;
-    for (int r = warp; r < w.n; r += WARPS) merge_rows<1, SCORES>(a, w.row0 + r, 1, pieces, lane);
+    // a warp's rows all at once (33 sequences of 111 visible keys, 16 heads per
+    // group: 7.9 us, row by row 9.2)
+    const int share = (w.n + WARPS - 1) / WARPS, r = warp * share, nr = min(share, w.n - r);
+    if (nr > 0) {
+      if (share == 1)
+        merge_rows<1, SCORES>(a, w.row0 + r, nr, pieces, lane);
+      else if (share == 2)
+        merge_rows<2, SCORES>(a, w.row0 + r, nr, pieces, lane);
+      else
+        merge_rows<4, SCORES>(a, w.row0 + r, nr, pieces, lane);
+    }
     if (threadIdx.x == 0 && pieces > 1 && RF_IDX_OK(g, (size_t)a.B * a.Hkv * a.mtiles))
       a.counters[g] = 0;
   }
@@ -603,9 +613,9 @@ merge_kernel(const CacheDecode a) {
 
 // total[j] = weight[j] + sum over the group's heads of exp2(score - lse2):
 // the weights of the row's softmax, each below 1, summed in fp32 head by head
-// in order.  KEYS adjacent keys per thread (4: 16-byte accesses, for rows that
-// stay aligned); reads 4 (G + 1) bytes and writes 4 per key.
-template <int KEYS>
+// in order, HEADS of them in flight at a time.  KEYS adjacent keys per thread (4:
+// 16-byte accesses, for rows that stay aligned); reads 4 (G + 1) bytes and writes 4 per key.
+template <int KEYS, int HEADS>
 __global__ void __launch_bounds__(256)
 add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __restrict__ lens,
                    const float* weight, float* total, int B, int Hkv, int G, int cap, int S,
@@ -630,20 +640,26 @@ add_weights_kernel(const float* scores, const float* seg_m, const int32_t* __res
       w[0] = weight[i];
   }
   if (j < len) {
-#pragma unroll 4
-    for (int g = 0; g < G; ++g) {
-      const size_t at = (row0 + g) * cap + j;
-      if (!RF_SPAN_OK(at, KEYS, (size_t)B * Hkv * G * cap)) continue;
-      const float z = __ldcg(seg_m + (row0 + g) * S);
-      if (z == -INFINITY) continue;               // a row without weight adds none
-      float x[KEYS];
-      if constexpr (KEYS == 4)
-        *reinterpret_cast<float4*>(x) = __ldcs(reinterpret_cast<const float4*>(scores + at));
-      else
-        x[0] = __ldcs(scores + at);
+    for (int g0 = 0; g0 < G; g0 += HEADS) {
+      float z[HEADS], x[HEADS][KEYS];
 #pragma unroll
-      for (int e = 0; e < KEYS; ++e)
-        if (j + e < len) w[e] += exp2f(x[e] - z);
+      for (int u = 0; u < HEADS; ++u) {
+        const size_t at = (row0 + g0 + u) * cap + j;
+        z[u] = -INFINITY;                         // a row without weight adds none
+        if (g0 + u >= G || !RF_SPAN_OK(at, KEYS, (size_t)B * Hkv * G * cap)) continue;
+        z[u] = __ldcg(seg_m + (row0 + g0 + u) * S);
+        if constexpr (KEYS == 4)
+          *reinterpret_cast<float4*>(x[u]) = __ldcs(reinterpret_cast<const float4*>(scores + at));
+        else
+          x[u][0] = __ldcs(scores + at);
+      }
+#pragma unroll
+      for (int u = 0; u < HEADS; ++u) {
+        if (z[u] == -INFINITY) continue;
+#pragma unroll
+        for (int e = 0; e < KEYS; ++e)
+          if (j + e < len) w[e] += exp2f(x[u][e] - z[u]);
+      }
     }
   }
   if constexpr (KEYS == 4)
@@ -694,8 +710,14 @@ rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* t
   const int blocks = (a.cap + keys - 1) / keys;
   const long long grid = (long long)a.B * a.Hkv * blocks;
   if (grid > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
-  return launch_after(wide ? add_weights_kernel<4> : add_weights_kernel<1>, (unsigned)grid, 256, 0, st,
-                      a.scores, a.seg_m, a.lens, weight, total, a.B, a.Hkv, a.H / a.Hkv, a.cap,
+  // eight heads in flight where there are more than four (2 x 16 heads of 595 keys:
+  // 11.3 us with the decode, 12.1 with four; 4 heads: 8.4 us with four, 8.8 with eight)
+  const int G = a.H / a.Hkv;
+  return launch_after(wide    ? add_weights_kernel<4, 4>
+                      : G > 4 ? add_weights_kernel<1, 8>
+                              : add_weights_kernel<1, 4>,
+                      (unsigned)grid, 256, 0, st,
+                      a.scores, a.seg_m, a.lens, weight, total, a.B, a.Hkv, G, a.cap,
                       a.S_total, blocks);
 }
 
