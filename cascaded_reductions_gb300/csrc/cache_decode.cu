@@ -693,7 +693,7 @@ rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st) {
   const bool few = decode_is_few((long long)a.B * a.Hkv * a.mtiles, keys, sms);
   a.piece_keys = few ? kFewKeys : kManyKeys;
   // no more pieces than the longest possible row has
-  const int most = (keys + a.piece_keys - 1) / a.piece_keys;
+  const int most = few ? (keys + kFewKeys - 1) / kFewKeys : decode_many_pieces(keys);
   if (a.S > most) a.S = most;
   if (dtype == RF_F16)
     return a.scores ? launch_t<true, true>(a, few, st) : launch_t<true, false>(a, few, st);
