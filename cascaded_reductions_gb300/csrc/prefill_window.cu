@@ -240,7 +240,9 @@ struct WindowPrefill {
   }
 
   // One output row, from its visible keys alone: the warp's lanes hold four
-  // columns each, one key at a time.
+  // columns each, one key at a time, until every column is NaN (a NaN query, key or
+  // value row that the row sees; the lse in place then stands, no masked score
+  // entered it).
   __device__ __forceinline__ void redo(int bh, int row, int lane) const {
     const int p = L - N + row;
     const size_t kv0 = (size_t)(bh / G) * L;
@@ -249,8 +251,9 @@ struct WindowPrefill {
     widen4(load4(q, ((size_t)bh * N + row) * HD + lane * 4, q_n), qf);
     const int lo = max(0, p - window + 1), ns = min(sinks, lo);
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    bool gone = false;
 #pragma unroll 2
-    for (int t = 0; t < ns + p - lo + 1; ++t) {
+    for (int t = 0; !gone && t < ns + p - lo + 1; ++t) {
       const int key = t < ns ? t : t - ns + lo;
       const size_t at = (kv0 + key) * HD + lane * 4;
       float kf[4], vf[4];
@@ -266,6 +269,8 @@ struct WindowPrefill {
       l = fmaf(l, corr, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], corr, w * vf[e]);
+      gone = __all_sync(0xffffffffu, acc[0] != acc[0] && acc[1] != acc[1] && acc[2] != acc[2] &&
+                                         acc[3] != acc[3]);
     }
     const size_t o = ((size_t)bh * N + row) * HD + lane * 4;
     if (RF_SPAN_OK(o, 4, q_n)) {
@@ -274,7 +279,7 @@ struct WindowPrefill {
       w.y = pair::pack_16x2<F16>(acc[2] / l, acc[3] / l);
       *reinterpret_cast<uint2*>(out + o) = w;
     }
-    if (lse != nullptr && lane == 0 && RF_IDX_OK((size_t)bh * N + row, (size_t)heads * N))
+    if (lse != nullptr && lane == 0 && !gone && RF_IDX_OK((size_t)bh * N + row, (size_t)heads * N))
       lse[(size_t)bh * N + row] = (m + log2f(l)) * kLn2;
   }
 

@@ -120,6 +120,20 @@ def test_a_bad_row_reaches_only_the_rows_that_see_it(rf, bad, dtype):
     assert torch.equal(torch.isnan(lse[0, 0]).nonzero().flatten().cpu(), torch.arange(120, 220))
 
 
+@pytest.mark.parametrize("window,sinks", [(64, 4), (0, 0)])
+def test_a_bad_first_key_and_bad_queries(rf, window, sinks):
+    q, k, v = make(8, 2, 8, 2, 1100, 1100, torch.bfloat16)
+    v[:, 0, 0] = float("nan")            # seen by every row of heads 0..3
+    v[:, 1, 1, 3] = float("nan")         # one column alone, by all rows but the first
+    q[:, 4:, 1000:] = float("nan")
+    out, lse = run(rf, q, k, v, window, sinks)
+    assert out[:, :4].isnan().all() and lse[:, :4].isfinite().all()
+    assert out[:, 4:, 1000:].isnan().all() and lse[:, 4:, 1000:].isnan().all()
+    assert lse[:, 4:, :1000].isfinite().all() and out[:, 4:, 0].isfinite().all()
+    nan = out[:, 4:, 1:1000].isnan()
+    assert nan[..., 3].all() and not nan[..., :3].any() and not nan[..., 4:].any()
+
+
 def test_padding_may_hold_anything(rf):
     # a prompt of 300 in a buffer of 512: its rows never see what lies behind
     q, k, v = make(6, 1, 2, 1, 512, 512, torch.bfloat16)
