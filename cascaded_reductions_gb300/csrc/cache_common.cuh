@@ -74,7 +74,7 @@ inline int decode_many_pieces(int keys) {
 inline int decode_segments(int groups, int keys, int sms) {
   long long s;
   if (decode_is_few(groups, keys, sms)) {
-    s = (2ll * sms + groups - 1) / groups;
+    s = 2ll * sms / groups;
     const int steps = (keys + kFewKeys - 1) / kFewKeys;
     if (s > steps) s = steps;
   } else {
