@@ -56,9 +56,11 @@ inline rf_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned
 constexpr int kFewKeys = 4 * kDecodeTile, kManyKeys = 768;
 
 // Whether a call of `groups` row groups of up to `keys` visible keys is small: its
-// pieces fit two CTAs on every SM, at most four steps of 64 keys each.
+// pieces fit two CTAs on every SM, at most sixteen steps of 64 keys each (with a
+// limit of four, 64 rows of 2048 keys took 17.4 us instead of 15.6, 8 rows of 32768
+// 33.3 instead of 26.6; with 64, 192 ragged rows of 3000 39.8 instead of 36.0).
 inline bool decode_is_few(long long groups, int keys, int sms) {
-  return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= 8ll * sms;
+  return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= 32ll * sms;
 }
 
 // Pieces of the longest row of a large call.  Rows of up to two pieces stay whole, to
@@ -69,8 +71,9 @@ inline int decode_many_pieces(int keys) {
   return keys <= 2 * kManyKeys ? 1 : (keys + kManyKeys - 1) / kManyKeys;
 }
 
-// Pieces per row for such a call: a small one is divided until two CTAs per SM
-// have work, a large one into the smallest pieces that are worth a CTA.
+// Pieces per row for such a call: a small one is divided as far as one wave of two
+// CTAs per SM goes (a second one costs 3 us, a longer piece 0.6 us per step), a large
+// one into the smallest pieces that are worth a CTA.
 inline int decode_segments(int groups, int keys, int sms) {
   long long s;
   if (decode_is_few(groups, keys, sms)) {
