@@ -69,6 +69,24 @@ def test_ties_go_to_the_lower_index(rf, levels):
     check(rf, k, v, w, [999, 500, 301], 300, 4, 64)
 
 
+@pytest.mark.parametrize("levels", [None, 7])
+@pytest.mark.parametrize("close", [1, 3, 4, 127, 128, 129, 131])
+def test_weights_close_to_the_threshold(rf, close, levels):
+    # `close` weights share their leading bits with the threshold; 100 are far above
+    k, v, w = make(10, 4, 1, 500)
+    g = torch.Generator().manual_seed(close)
+    near = 1 + torch.rand(4, close, generator=g) * 0.24
+    if levels is not None:
+        near = 1 + (near * 100).floor() % levels / 32
+    w[:] = 0.01
+    for b in range(4):
+        at = torch.randperm(500, generator=g)
+        w[b, 0, at[:close].cuda()] = near[b].cuda()
+        w[b, 0, at[close:close + 100].cuda()] = 8.0
+    for need in sorted({1, (close + 1) // 2, close}):
+        check(rf, k, v, w, [500] * 4, 100 + need, 0, 0)
+
+
 def test_ragged_and_short_sequences(rf):
     lens = [0, 1, 99, 100, 101, 640]
     k, v, w = make(4, len(lens), 2, 640)
