@@ -371,16 +371,30 @@ rf_status rf_attn_decode_shared(const void* q, const void* kp, const void* vp, i
   if (!rf::aligned16(q) || !rf::aligned16(kp) || !rf::aligned16(vp) || !rf::aligned16(k) ||
       !rf::aligned16(v) || !rf::aligned16(out) || !rf::aligned16(seg_acc))
     return RF_ERR_MISALIGNED;
-  s = rf::launch_prefix_states(q, kp, vp, prefix, B, H, Hkv, Sp, Sp + S, scale, dtype, seg_m, seg_l,
-                               seg_acc, as_stream(stream));
-  if (s != RF_OK) return s;
+  const int sms = rf::tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  const bool few = rf::decode_prefix_is_few((long long)B * Hkv * ((H / Hkv + 15) / 16), prefix, cap, sms);
+  if (!few) {
+    s = rf::launch_prefix_states(q, kp, vp, prefix, B, H, Hkv, Sp, Sp + S, scale, dtype, seg_m,
+                                 seg_l, seg_acc, as_stream(stream));
+    if (s != RF_OK) return s;
+  }
   rf::CacheDecode a = {};
   a.q = static_cast<const uint8_t*>(q);
   a.k = static_cast<const uint8_t*>(k);
   a.v = static_cast<const uint8_t*>(v);
   a.lens = lens;
   a.B = B, a.H = H, a.Hkv = Hkv, a.cap = cap;
-  a.S = S, a.S_total = Sp + S, a.seg0 = Sp;
+  a.S_total = Sp + S;
+  if (few) {
+    a.kp = static_cast<const uint8_t*>(kp);
+    a.vp = static_cast<const uint8_t*>(vp);
+    a.prefix = prefix;
+    a.S = rf::decode_segments((int)((long long)B * Hkv * ((H / Hkv + 15) / 16)), prefix + cap, sms);
+    if (a.S > a.S_total) a.S = a.S_total;
+  } else {
+    a.S = S, a.seg0 = Sp;
+  }
   a.scale_log2 = scale * rf::kLog2e;
   a.seg_m = seg_m, a.seg_l = seg_l, a.seg_acc = seg_acc;
   a.counters = counters;

@@ -86,6 +86,16 @@ inline int decode_segments(int groups, int keys, int sms) {
   return (int)(s > 4096 ? 4096 : s);
 }
 
+// Whether a shared prefix is read once per sequence, as keys before its own, instead
+// of by the prefix kernel: a small call, in which that takes less than the second
+// launch (4 sequences behind 1000 keys 7.4 us, 9.3 with it; 38 behind 300 keys 9.4 and
+// 13.9; at 16 steps per SM, 30 sequences behind 500 keys, 12.9 and 10.8).
+constexpr int kSharedSteps = 14;
+inline bool decode_prefix_is_few(long long groups, long long prefix, int cap, int sms) {
+  const long long keys = prefix + cap;
+  return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= (long long)kSharedSteps * sms;
+}
+
 // One call's arguments.  Segment states are scratch between kernels: seg_m
 // holds log2 units, and a segment without keys has m = -inf, l = 0 and an
 // accumulator that is neither written nor read.
@@ -94,6 +104,8 @@ struct CacheDecode {
   const int32_t* lens;           // [B] or null (every sequence holds cap keys)
   int B, H, Hkv, cap;
   int window, sinks;             // window 0: every key is visible
+  const uint8_t *kp, *vp;        // [Hkv, prefix, 128]: keys before every sequence's own, where
+  int prefix;                    // decode_prefix_is_few (no window, no scores); else 0
   int S, S_total, seg0;          // this kernel's slots seg0 .. seg0 + S - 1 of S_total
   float scale_log2;
   float *seg_m, *seg_l, *seg_acc;   // [B * H, S_total (, 128)]

@@ -2,7 +2,8 @@
 // key/value heads (head h reads key head h / G, G = H / Hkv), every sequence
 // has its own length, and a mask may leave only the last `window` keys and the
 // first `sinks` visible.  The same kernels, with their states numbered after
-// those of the prefix kernel, are the suffix half of the shared-prefix decode,
+// those of the prefix kernel, are the suffix half of the shared-prefix decode (and
+// all of it in a small call, with the prefix as every sequence's first keys),
 // and with their scores kept they feed the running total of each key's weight.
 //
 // Mathematics: per row the cascade of the split-KV decode (running m, l, acc,
@@ -151,13 +152,14 @@ __device__ __forceinline__ float normalised(float acc, float l) { return l == 0.
 struct Group {
   int n, lo, ns;         // visible keys; key t is cache row t (t < ns) or t - ns + lo
   size_t kv0;            // first cache row of its key head
+  size_t prefix0;        // with a prefix, key t < ns is its row prefix0 + t instead
 };
 
 __device__ __forceinline__ int visible_keys(const CacheDecode& a, int b, int& lo, int& ns) {
   int len = a.cap;
   if (a.lens != nullptr && RF_IDX_OK(b, a.B)) len = min(max(a.lens[b], 0), a.cap);
   lo = a.window > 0 ? max(0, len - a.window) : 0;
-  ns = min(a.sinks, lo);
+  ns = a.prefix > 0 ? a.prefix : min(a.sinks, lo);
   return ns + len - lo;
 }
 
@@ -170,6 +172,7 @@ __device__ __forceinline__ Group group_of(const CacheDecode& a, int g) {
   const int head = g / a.mtiles;
   r.n = visible_keys(a, head / a.Hkv, r.lo, r.ns);
   r.kv0 = (size_t)head * a.cap;
+  r.prefix0 = (size_t)(head % a.Hkv) * a.prefix;
   return r;
 }
 
@@ -186,6 +189,7 @@ __device__ __forceinline__ Rows rows_of(const CacheDecode& a, int g) {
 // The warp's copies of keys t0 .. t0 + 15 of a group into one stage: K rows,
 // then V rows, 16-byte chunks permuted by row % 8 so that ldmatrix meets all
 // banks; two rows per instruction.
+template <bool PREFIX>
 __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, int t0, uint32_t stage,
                                           uint64_t policy, int lane) {
 #pragma unroll
@@ -193,11 +197,14 @@ __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, 
     const int r = 2 * u + (lane >> 4), c = lane & 15;
     const int t = t0 + r;
     const int key = t < q.ns ? t : t - q.ns + q.lo;
-    const bool in = t < q.n && RF_IDX_OK(q.kv0 + key, (size_t)a.B * a.Hkv * a.cap);
-    const size_t off = (q.kv0 + (in ? key : 0)) * ROW_BYTES + c * 16;
+    const bool shared = PREFIX && t < q.ns;
+    const size_t row = (shared ? q.prefix0 : q.kv0) + key;
+    (void)row;                                    // read by the checked build only
+    const bool in = t < q.n && RF_IDX_OK(row, (size_t)a.Hkv * (shared ? (size_t)a.prefix : (size_t)a.B * a.cap));
+    const size_t off = ((shared ? q.prefix0 : q.kv0) + (in ? key : 0)) * ROW_BYTES + c * 16;
     const uint32_t dst = stage + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
-    cp_async16(dst, a.k + off, in ? 16u : 0u, policy);
-    cp_async16(dst + TK * ROW_BYTES, a.v + off, in ? 16u : 0u, policy);
+    cp_async16(dst, (shared ? a.kp : a.k) + off, in ? 16u : 0u, policy);
+    cp_async16(dst + TK * ROW_BYTES, (shared ? a.vp : a.v) + off, in ? 16u : 0u, policy);
   }
 }
 
@@ -492,7 +499,8 @@ __device__ __forceinline__ int pieces_of(const CacheDecode& a, int n) {
 }
 
 // One CTA per (group, piece); pieces that a group does not have return at once.
-template <bool F16, bool SCORES, bool FUSED>
+// PREFIX: keys of a shared prefix come before every sequence's own.
+template <bool F16, bool SCORES, bool FUSED, bool PREFIX>
 __global__ void __launch_bounds__(WARPS * 32, 2)
 cache_decode_kernel(const CacheDecode a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -524,7 +532,7 @@ cache_decode_kernel(const CacheDecode a) {
   int in = 0;                           // the stage that the next copies go to
   auto issue = [&](int k) {
     const int t0 = (k * WARPS + warp) * TK;
-    if (k < k1 && t0 < q.n) copy_tile(a, q, t0, ring + (uint32_t)in * STAGE_BYTES, policy, lane);
+    if (k < k1 && t0 < q.n) copy_tile<PREFIX>(a, q, t0, ring + (uint32_t)in * STAGE_BYTES, policy, lane);
     cp_async_commit();
     in = in + 1 == STAGES ? 0 : in + 1;
   };
@@ -672,8 +680,17 @@ template <bool F16, bool SCORES>
 rf_status launch_t(const CacheDecode& a, bool few, cudaStream_t st) {
   static std::atomic<uint64_t> done_few{0}, done_many{0};
   const unsigned groups = (unsigned)(a.B * a.Hkv * a.mtiles);
-  auto* kernel = few ? cache_decode_kernel<F16, SCORES, true> : cache_decode_kernel<F16, SCORES, false>;
-  if (smem_attr(kernel, SMEM_BYTES, few ? done_few : done_many) != RF_OK) return RF_ERR_CUDA;
+  auto* kernel = few ? cache_decode_kernel<F16, SCORES, true, false>
+                     : cache_decode_kernel<F16, SCORES, false, false>;
+  std::atomic<uint64_t>* done = few ? &done_few : &done_many;
+  if constexpr (!SCORES) {
+    static std::atomic<uint64_t> done_prefix{0};
+    if (a.prefix > 0) {                 // always a small call
+      kernel = cache_decode_kernel<F16, false, true, true>;
+      done = &done_prefix;
+    }
+  }
+  if (smem_attr(kernel, SMEM_BYTES, *done) != RF_OK) return RF_ERR_CUDA;
   const rf_status s = launch_after(kernel, groups * a.S, WARPS * 32, SMEM_BYTES, st, a);
   if (s != RF_OK || few || (a.S == 1 && a.seg0 == 0)) return s;
   if (a.seg0 + a.S <= 8)
@@ -689,7 +706,7 @@ rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st) {
   a.mtiles = (a.G + MROWS - 1) / MROWS;
   const int sms = tc::sm_count();
   if (sms <= 0) return RF_ERR_CUDA;
-  const int keys = a.window > 0 && a.window < a.cap - a.sinks ? a.window + a.sinks : a.cap;
+  const int keys = a.window > 0 && a.window < a.cap - a.sinks ? a.window + a.sinks : a.prefix + a.cap;
   const bool few = decode_is_few((long long)a.B * a.Hkv * a.mtiles, keys, sms);
   a.piece_keys = few ? kFewKeys : kManyKeys;
   // no more pieces than the longest possible row has

@@ -2,6 +2,7 @@
 // with the same keys: every query row of a key head (B sequences x G heads)
 // meets the one prefix, so each of its keys is read once for up to 256 rows
 // instead of once per sequence (the kernel, on CTA pairs, is in attn_pair.cuh).
+// Small calls do without it (decode_prefix_is_few).
 //
 // Mathematics: segment states (m, l, acc) of the split-KV decode, one per row
 // and piece of the prefix; the decode over the sequences' own keys merges them
@@ -200,7 +201,12 @@ int prefix_segments(int B, int H, int Hkv, int prefix) {
   if (pairs <= 0) return 0;
   const Split s = make_split(B, H, Hkv, prefix, 1 << 20, pairs);
   const int n = (s.clusters + s.tiles - 1) / s.tiles + 1;
-  return n < 2 ? 2 : n;
+  // or the decode kernel's pieces, where the call may be small enough for it
+  const long long groups = (long long)B * Hkv * ((H / Hkv + 15) / 16);
+  const int sms = tc::sm_count();
+  const int few = sms > 0 && decode_prefix_is_few(groups, prefix, 1, sms)
+                      ? decode_segments((int)groups, prefix, sms) : 0;
+  return n > few ? (n < 2 ? 2 : n) : (few < 2 ? 2 : few);
 }
 
 rf_status launch_prefix_states(const void* q, const void* kp, const void* vp, int prefix, int B,

@@ -387,7 +387,7 @@ rf_status rf_attn_prefill_window(const void* q, const void* k, const void* v, in
                                  int dtype, void* out, float* lse, void* stream);
 
 /*
- * rf_prefix_segments -- the number of pieces that rf_attn_decode_shared makes of
+ * rf_prefix_segments -- the most pieces that rf_attn_decode_shared makes of
  * the prefix on the current device: at least 2; 0 if the device cannot run
  * it or the sizes are not valid.
  */
@@ -398,7 +398,9 @@ int rf_prefix_segments(int B, int H, int Hkv, int prefix);
  * share their first `prefix` keys: softmax attention over the prefix and the
  * sequence's own keys together.  The prefix is read once for the whole batch
  * (on the tensor cores, B * G rows against each key), the own keys as by
- * rf_attn_decode_window, and the states are merged.  Two launches.
+ * rf_attn_decode_window, and the states are merged.  Two launches or three; a
+ * small call reads the prefix as the first keys of every sequence, in one
+ * launch and at most Sp + S pieces.
  *   q [B, H, D];  kp, vp [Hkv, prefix, D], prefix >= 1;  k, v [B, Hkv, cap, D]
  *   with lens [B] own keys each (0 allowed; the query stands behind all of them)
  *   Sp   most pieces of the prefix, >= 2;  S  most pieces of the own keys, >= 1
@@ -423,7 +425,7 @@ rf_status rf_attn_decode_shared(const void* q, const void* kp, const void* vp, i
  *               (in place; no other overlap)
  *   scores      [B, H, cap] fp32 scratch
  *   weight_out  [B, Hkv, cap] fp32 out
- * Two launches (the weights need the finished normaliser of their row).
+ * Two launches or three (the weights need the finished normaliser of their row).
  */
 rf_status rf_attn_decode_weights(const void* q, const void* k, const void* v, const int32_t* lens,
                                  int B, int H, int Hkv, int cap, int D, int S, float scale,

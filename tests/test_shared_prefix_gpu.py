@@ -118,3 +118,64 @@ def test_captured_and_replayed(rf):
         g.replay()
         torch.cuda.synchronize()
         check_decode(out, lse, q, k, v, lens, SCALE, kp=kp, vp=vp, p_step=2.0 ** -8)
+
+
+# Above, most calls are small enough to read the prefix once per sequence.  Below, more row
+# groups than that allows: the prefix kernel, then the merge.
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("prefix", [1, 2, 127, 128, 129, 255, 256, 257, 513, 1000])
+def test_many_sequences_prefix_lengths(rf, prefix, dtype):
+    lens = [(5 * b) % 9 for b in range(40)]
+    check(rf, make(prefix, 40, 16, 8, prefix, 8, lens, DT[dtype]), lens)
+
+
+@pytest.mark.parametrize("B,H,Hkv", [(310, 1, 1), (160, 16, 2), (110, 21, 3), (40, 128, 8), (26, 160, 4),
+                                     (20, 256, 2), (313, 3, 1)])
+def test_many_sequences_head_groups(rf, B, H, Hkv):
+    lens = [(7 * b) % 21 for b in range(B)]
+    check(rf, make(B, B, H, Hkv, 300, 20, lens, torch.bfloat16), lens)
+
+
+@pytest.mark.parametrize("Sp,S", [(2, 1), (3, 2), (40, 1)])
+def test_many_sequences_segment_counts(rf, Sp, S):
+    lens = [(37 * b) % 90 for b in range(40)]
+    args = make(Sp, 40, 16, 8, 2000, 90, lens, torch.bfloat16)
+    q, kp, vp, k, v, n = args
+    f32 = dict(device="cuda", dtype=torch.float32)
+    m, l = (torch.full((640, Sp + S), float("nan"), **f32) for _ in range(2))
+    acc = torch.full((640, Sp + S, 128), float("nan"), **f32)
+    counters = torch.zeros(320, device="cuda", dtype=torch.int32)
+    for _ in range(2):
+        out, lse = torch.empty_like(q), torch.empty(40, 16, **f32)
+        rf.rf_attn_decode_shared(q, kp, vp, k, v, n, Sp, S, SCALE, m, l, acc, counters, out, lse)
+        check_decode(out, lse, q, k, v, lens, SCALE, kp=kp, vp=vp, p_step=2.0 ** -8)
+    assert torch.all(counters == 0)
+
+
+@pytest.mark.parametrize("B", [6, 40])
+def test_nan_in_the_prefix_and_behind_it(rf, B):
+    # a NaN value row of the prefix reaches its key head's rows alone, one behind a sequence none
+    lens = [3] * B
+    q, kp, vp, k, v, n = make(10, B, 16, 8, 100, 8, lens, torch.bfloat16)
+    vp[2, 99] = float("nan")
+    out, lse = rf.attn_decode_shared(q, kp, vp, k, v, n, scale=SCALE)
+    bad = out.isnan().all(-1)
+    assert torch.equal(bad, torch.arange(16, device="cuda").expand(B, 16) // 2 == 2)
+    assert torch.equal(out.isnan().any(-1), bad) and lse.isfinite().all()
+
+
+def test_many_sequences_captured_and_replayed(rf):
+    lens = [b % 30 for b in range(40)]
+    args = make(11, 40, 16, 8, 500, 30, lens, torch.bfloat16)
+    q, kp, vp, k, v, n = args
+    work = rf.decode_workspace(40, 16, 8, 30, prefix=500)
+    check(rf, args, lens, work)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = rf.attn_decode_shared(q, kp, vp, k, v, n, scale=SCALE, work=work)
+    for seed, lens in ((12, [30] * 40), (13, [0] * 40)):
+        for dst, src in zip(args, make(seed, 40, 16, 8, 500, 30, lens, torch.bfloat16)):
+            dst.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        check_decode(out, lse, q, k, v, lens, SCALE, kp=kp, vp=vp, p_step=2.0 ** -8)
