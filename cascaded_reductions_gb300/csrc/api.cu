@@ -344,6 +344,22 @@ rf_status rf_attn_prefill_window(const void* q, const void* k, const void* v, in
   if (heads > 0x7fffffffLL || heads * N > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
   if (!rf::aligned16(q) || !rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(out))
     return RF_ERR_MISALIGNED;
+  const int sms = rf::tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  const long long keys = window > 0 && (long long)window + sinks < L ? (long long)window + sinks : L;
+  const long long rows = (long long)B * Hkv * N;              // below 2^31
+  if (rf::prefill_is_few(rows * ((H / Hkv + 15) / 16), keys, sms)) {
+    rf::CacheDecode a = {};
+    a.q = static_cast<const uint8_t*>(q);
+    a.k = static_cast<const uint8_t*>(k);
+    a.v = static_cast<const uint8_t*>(v);
+    a.B = B, a.H = H, a.Hkv = Hkv, a.cap = L;
+    a.window = window, a.sinks = sinks;
+    a.positions = N;
+    a.scale_log2 = scale * rf::kLog2e;
+    a.out = out, a.out_dtype = dtype, a.lse = lse;
+    return rf::launch_prefill_rows(a, dtype, as_stream(stream));
+  }
   return rf::launch_prefill_window(q, k, v, B, H, Hkv, N, L, window, sinks, scale, dtype, out, lse,
                                    as_stream(stream));
 }

@@ -91,9 +91,21 @@ inline int decode_segments(int groups, int keys, int sms) {
 // launch (4 sequences behind 1000 keys 7.4 us, 9.3 with it; 38 behind 300 keys 9.4 and
 // 13.9; at 16 steps per SM, 30 sequences behind 500 keys, 12.9 and 10.8).
 constexpr int kSharedSteps = 14;
+static_assert(kSharedSteps <= 32, "such a call is small");
 inline bool decode_prefix_is_few(long long groups, long long prefix, int cap, int sms) {
   const long long keys = prefix + cap;
   return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= (long long)kSharedSteps * sms;
+}
+
+// Whether a windowed prefill is so small that a CTA per position and row group is
+// faster than the pair kernel's 256 rows at a time (26 rows of 20 heads, 27 keys: 3.2
+// us, 7.3 with the pair kernel; 32 rows of 32 heads, 132 keys: 5.4 and 8.4; 4 rows of
+// 32 heads, 1004 keys: 11.8 and 13.2; 256 rows of 16 heads, at 6.7 steps per SM: 8.6
+// and 7.6).
+constexpr int kRowsSteps = 6, kRowsKeys = 1024;
+inline bool prefill_is_few(long long groups, long long keys, int sms) {
+  return groups <= 2ll * sms && keys <= kRowsKeys &&
+         groups * ((keys + kFewKeys - 1) / kFewKeys) <= (long long)kRowsSteps * sms;
 }
 
 // One call's arguments.  Segment states are scratch between kernels: seg_m
@@ -107,6 +119,7 @@ struct CacheDecode {
   const uint8_t *kp, *vp;        // [Hkv, prefix, 128]: keys before every sequence's own, where
   int prefix;                    // decode_prefix_is_few (no window, no scores); else 0
   int S, S_total, seg0;          // this kernel's slots seg0 .. seg0 + S - 1 of S_total
+  int positions;                 // launch_prefill_rows: rows per head, q and out [B, H, positions, 128]
   float scale_log2;
   float *seg_m, *seg_l, *seg_acc;   // [B * H, S_total (, 128)]
   int* counters;                 // [B * Hkv * mtiles], zero before and after the call
@@ -119,6 +132,9 @@ struct CacheDecode {
 
 // With seg0 > 0 the kernel before it on the stream writes the first seg0 slots.
 rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st);
+// Attention of each of the last `positions` of cap positions, one CTA per position
+// and row group: window and sinks as in prefill, no scratch.
+rf_status launch_prefill_rows(CacheDecode a, int dtype, cudaStream_t st);
 // weight may be null (zeros) or equal to total (in place)
 rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* total,
                              cudaStream_t st);

@@ -4,7 +4,8 @@
 // first `sinks` visible.  The same kernels, with their states numbered after
 // those of the prefix kernel, are the suffix half of the shared-prefix decode (and
 // all of it in a small call, with the prefix as every sequence's first keys),
-// and with their scores kept they feed the running total of each key's weight.
+// with their scores kept they feed the running total of each key's weight, and
+// with a group per position they are the windowed prefill of a few rows.
 //
 // Mathematics: per row the cascade of the split-KV decode (running m, l, acc,
 // rescale by exp2(m_old - m_new), states merged by the same rescale).
@@ -166,10 +167,21 @@ __device__ __forceinline__ int visible_keys(const CacheDecode& a, int b, int& lo
 // tiles of n keys; at least one, so that a group without keys has an owner
 __device__ __forceinline__ int tiles_of(int n) { return n > TK ? (n + TK - 1) / TK : 1; }
 
-// group g = (b Hkv + key head) mtiles + tile of query heads
+// group g = (b Hkv + key head) mtiles + tile of query heads; with POSITIONS, b is
+// (sequence, position) and the position sees what lies before it
+template <bool POSITIONS = false>
 __device__ __forceinline__ Group group_of(const CacheDecode& a, int g) {
   Group r;
   const int head = g / a.mtiles;
+  if constexpr (POSITIONS) {
+    const int bp = head / a.Hkv, b = bp / a.positions, len = a.cap - a.positions + (bp - b * a.positions) + 1;
+    r.lo = a.window > 0 ? max(0, len - a.window) : 0;
+    r.ns = min(a.sinks, r.lo);
+    r.n = r.ns + len - r.lo;
+    r.kv0 = ((size_t)b * a.Hkv + (head - bp * a.Hkv)) * a.cap;
+    r.prefix0 = 0;
+    return r;
+  }
   r.n = visible_keys(a, head / a.Hkv, r.lo, r.ns);
   r.kv0 = (size_t)head * a.cap;
   r.prefix0 = (size_t)(head % a.Hkv) * a.prefix;
@@ -177,13 +189,23 @@ __device__ __forceinline__ Group group_of(const CacheDecode& a, int g) {
 }
 
 struct Rows {
-  size_t row0;           // first query row
+  size_t row0, step;     // first query row, distance of one head's to the next
   int n;                 // 1 .. 16
 };
+template <bool POSITIONS = false>
 __device__ __forceinline__ Rows rows_of(const CacheDecode& a, int g) {
   const int head = g / a.mtiles, mt = g - head * a.mtiles;
   const int b = head / a.Hkv, hk = head - b * a.Hkv;
-  return {(size_t)b * a.H + (size_t)hk * a.G + mt * MROWS, min(MROWS, a.G - mt * MROWS)};
+  const int first = hk * a.G + mt * MROWS, n = min(MROWS, a.G - mt * MROWS);
+  if constexpr (POSITIONS) {
+    const int seq = b / a.positions;
+    return {((size_t)seq * a.H + first) * a.positions + (b - seq * a.positions), (size_t)a.positions, n};
+  }
+  return {(size_t)b * a.H + first, 1, n};
+}
+// query rows of the call (for the checked build)
+[[maybe_unused]] __device__ __forceinline__ size_t rows_in(const CacheDecode& a) {
+  return (size_t)a.B * a.H * (a.positions > 0 ? a.positions : 1);
 }
 
 // The warp's copies of keys t0 .. t0 + 15 of a group into one stage: K rows,
@@ -210,7 +232,7 @@ __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, 
 
 // One warp's running state of a row group: rows lane / 4 (index 0) and + 8
 // (index 1); acc[d] holds columns 8 d + 2 (lane % 4) and + 1 of both.
-template <bool F16, bool SCORES>
+template <bool F16, bool SCORES, bool POSITIONS>
 struct State {
   uint32_t qf[HD / 16][4];
   float acc[HD / 8][4];
@@ -219,15 +241,17 @@ struct State {
   __device__ __forceinline__ void start(const CacheDecode& a, const Rows& w, int lane) {
     // Q fragments: columns 16 kk + 2 (lane % 4) (+ 8) of the two rows
     const int r = lane >> 2;
-    const bool in0 = r < w.n && RF_IDX_OK(w.row0 + r, (size_t)a.B * a.H);
-    const bool in1 = r + 8 < w.n && RF_IDX_OK(w.row0 + r + 8, (size_t)a.B * a.H);
-    const uint8_t* q0 = a.q + (w.row0 + r) * ROW_BYTES + (lane & 3) * 4;
+    const size_t step = POSITIONS ? w.step : 1;
+    const bool in0 = r < w.n && RF_IDX_OK(w.row0 + r * step, rows_in(a));
+    const bool in1 = r + 8 < w.n && RF_IDX_OK(w.row0 + (r + 8) * step, rows_in(a));
+    const uint8_t* q0 = a.q + (w.row0 + r * step) * ROW_BYTES + (lane & 3) * 4;
+    const uint8_t* q1 = q0 + 8 * step * ROW_BYTES;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
       qf[kk][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32) : 0u;
-      qf[kk][1] = in1 ? *reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32) : 0u;
+      qf[kk][1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + kk * 32) : 0u;
       qf[kk][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16) : 0u;
-      qf[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q0 + 8 * ROW_BYTES + kk * 32 + 16) : 0u;
+      qf[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + kk * 32 + 16) : 0u;
     }
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
@@ -358,7 +382,7 @@ template <bool SCORES>
 __device__ __forceinline__ void merge_warps(const CacheDecode& a, const float* acc_buf,
                                             const float2 (*ml_buf)[MROWS], size_t row, int r,
                                             bool direct, int slot, int lane) {
-  if (!RF_IDX_OK(row, (size_t)a.B * a.H)) return;
+  if (!RF_IDX_OK(row, rows_in(a))) return;
   float M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) M = fmaxf(M, ml_buf[i][r].x);
@@ -499,8 +523,9 @@ __device__ __forceinline__ int pieces_of(const CacheDecode& a, int n) {
 }
 
 // One CTA per (group, piece); pieces that a group does not have return at once.
-// PREFIX: keys of a shared prefix come before every sequence's own.
-template <bool F16, bool SCORES, bool FUSED, bool PREFIX>
+// PREFIX: keys of a shared prefix come before every sequence's own.  POSITIONS: a
+// group for each of a prompt's last positions, whole (S = 1).
+template <bool F16, bool SCORES, bool FUSED, bool PREFIX, bool POSITIONS>
 __global__ void __launch_bounds__(WARPS * 32, 2)
 cache_decode_kernel(const CacheDecode a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -510,7 +535,7 @@ cache_decode_kernel(const CacheDecode a) {
   const int g = (int)(blockIdx.x / a.S), piece = (int)(blockIdx.x - (unsigned)g * a.S);
   if (a.seg0 == 0) wait_prerequisite();   // the prefix kernel has done so for its successor
   allow_dependents();
-  const Group q = group_of(a, g);
+  const Group q = group_of<POSITIONS>(a, g);
   const int pieces = pieces_of(a, q.n);
   // Done means that the prefix is done too.  Where a kernel of its own merges, one
   // CTA's wait says so for all, and the others leave their SM to the rows that
@@ -520,7 +545,7 @@ cache_decode_kernel(const CacheDecode a) {
     if (waits) wait_prerequisite();
     return;
   }
-  const Rows w = rows_of(a, g);
+  const Rows w = rows_of<POSITIONS>(a, g);
   const int steps = (tiles_of(q.n) + WARPS - 1) / WARPS;
   const int k0 = (int)((long long)steps * piece / pieces);
   const int k1 = (int)((long long)steps * (piece + 1) / pieces);
@@ -538,7 +563,7 @@ cache_decode_kernel(const CacheDecode a) {
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue(k0 + i);
-  State<F16, SCORES> st;
+  State<F16, SCORES, POSITIONS> st;
   st.start(a, w, lane);
   int slot = 0;
   for (int k = k0; k < k1; ++k) {
@@ -558,7 +583,9 @@ cache_decode_kernel(const CacheDecode a) {
   __syncthreads();
   const bool direct = pieces == 1 && a.seg0 == 0;   // the output itself
   for (int r = warp; r < w.n; r += WARPS)
-    merge_warps<SCORES>(a, acc_buf, sm_ml, w.row0 + r, r, direct, a.seg0 + piece, lane);
+    merge_warps<SCORES>(a, acc_buf, sm_ml, w.row0 + r * (POSITIONS ? w.step : 1), r, direct,
+                        a.seg0 + piece, lane);
+  if constexpr (POSITIONS) return;
   if (waits) wait_prerequisite();       // the prefix's states, where there are some
   if constexpr (FUSED) {
     if (direct) return;
@@ -603,7 +630,7 @@ merge_kernel(const CacheDecode a) {
   const int lane = threadIdx.x & 31;
   const bool in = unit < (BY_ROW ? (long long)a.B * a.H : (long long)a.B * a.Hkv * a.mtiles);
   allow_dependents();
-  Rows w = {0, 0};
+  Rows w = {0, 1, 0};
   int pieces = 1;
   if (in) {
     int g = (int)unit;
@@ -612,7 +639,7 @@ merge_kernel(const CacheDecode a) {
       g = (b * a.Hkv + h / a.G) * a.mtiles;
     }
     pieces = pieces_of(a, group_of(a, g).n);
-    w = BY_ROW ? Rows{(size_t)unit, 1} : rows_of(a, g);
+    w = BY_ROW ? Rows{(size_t)unit, 1, 1} : rows_of(a, g);
   }
   wait_prerequisite();
   if (!in || (pieces == 1 && a.seg0 == 0)) return;   // written by its CTA
@@ -680,13 +707,13 @@ template <bool F16, bool SCORES>
 rf_status launch_t(const CacheDecode& a, bool few, cudaStream_t st) {
   static std::atomic<uint64_t> done_few{0}, done_many{0};
   const unsigned groups = (unsigned)(a.B * a.Hkv * a.mtiles);
-  auto* kernel = few ? cache_decode_kernel<F16, SCORES, true, false>
-                     : cache_decode_kernel<F16, SCORES, false, false>;
+  auto* kernel = few ? cache_decode_kernel<F16, SCORES, true, false, false>
+                     : cache_decode_kernel<F16, SCORES, false, false, false>;
   std::atomic<uint64_t>* done = few ? &done_few : &done_many;
   if constexpr (!SCORES) {
     static std::atomic<uint64_t> done_prefix{0};
     if (a.prefix > 0) {                 // always a small call
-      kernel = cache_decode_kernel<F16, false, true, true>;
+      kernel = cache_decode_kernel<F16, false, true, true, false>;
       done = &done_prefix;
     }
   }
@@ -715,6 +742,19 @@ rf_status launch_cache_decode(CacheDecode a, int dtype, cudaStream_t st) {
   if (dtype == RF_F16)
     return a.scores ? launch_t<true, true>(a, few, st) : launch_t<true, false>(a, few, st);
   return a.scores ? launch_t<false, true>(a, few, st) : launch_t<false, false>(a, few, st);
+}
+
+rf_status launch_prefill_rows(CacheDecode a, int dtype, cudaStream_t st) {
+  static std::atomic<uint64_t> done[2];
+  a.G = a.H / a.Hkv;
+  a.mtiles = (a.G + MROWS - 1) / MROWS;
+  a.S = a.S_total = 1;
+  a.piece_keys = 1 << 30;
+  auto* kernel = dtype == RF_F16 ? cache_decode_kernel<true, false, true, false, true>
+                                 : cache_decode_kernel<false, false, true, false, true>;
+  if (smem_attr(kernel, SMEM_BYTES, done[dtype == RF_F16]) != RF_OK) return RF_ERR_CUDA;
+  const unsigned groups = (unsigned)(a.B * a.positions * a.Hkv * a.mtiles);
+  return launch_after(kernel, groups, WARPS * 32, SMEM_BYTES, st, a);
 }
 
 rf_status launch_add_weights(const CacheDecode& a, const float* weight, float* total,

@@ -1,6 +1,7 @@
 // Prefill of the last N of L positions with a sliding window and a few first
 // tokens that stay visible, grouped heads, on CTA pairs (the kernel is in
-// attn_pair.cuh).
+// attn_pair.cuh).  A few rows of few heads go to the decode kernel instead
+// (prefill_is_few).
 //
 // Mathematics: the causal prefill's cascade over the visible keys only,
 //   visible(p) = { j <= p : j > p - window or j < sinks }.

@@ -377,6 +377,8 @@ rf_status rf_attn_decode_window(const void* q, const void* k, const void* v, con
  *   q [B, H, N, D];  k, v [B, Hkv, L, D];  out [B, H, N, D] of q's type;
  *   lse [B, H, N] fp32 or NULL
  * A key or value row that is not finite reaches only the rows that see it.
+ * A few rows of few heads are computed row by row as by rf_attn_decode_window
+ * (weights not rounded to 16 bits), so a row's last bits may depend on N.
  * Errors: as the conventions above (no lens, S, scratch or counters), plus
  * RF_ERR_INVALID_ARG for N > L and RF_ERR_UNSUPPORTED for scale <= 0,
  * B*H*N >= 2^31, or a device that cannot hold a cluster of two CTAs with about

@@ -206,3 +206,38 @@ def test_query_heads_of_a_group_share_blocks(rf, N, L, window, sinks):
         q, k, v = make(N + H, 1, H, Hkv, N, L, torch.bfloat16)
         out, lse = run(rf, q, k, v, window, sinks)
         check(out, lse, q, k, v, window, sinks, rows=sorted({*range(0, N, 13), N - 1}))
+
+
+# few rows of few heads: a CTA per position and group of query heads
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (8, 2), (16, 1), (17, 1), (40, 1), (128, 4)])
+@pytest.mark.parametrize("N,L,window,sinks", [(1, 1, 0, 0), (1, 300, 1, 0), (2, 2, 1, 1), (5, 250, 0, 4),
+                                              (7, 5000, 200, 56), (33, 33, 20, 2), (9, 64, 64, 64),
+                                              (2, 2000, 900, 64)])
+def test_few_rows(rf, H, Hkv, N, L, window, sinks):
+    q, k, v = make(N + H, 2, H, Hkv, N, L, torch.bfloat16 if H % 2 else torch.float16)
+    out, lse = run(rf, q, k, v, window, sinks)
+    check(out, lse, q, k, v, window, sinks)
+
+
+# as few rows of more heads (over 304 groups): the pair kernel
+@pytest.mark.parametrize("B,H,Hkv", [(20, 32, 16), (160, 6, 2), (40, 64, 8)])
+@pytest.mark.parametrize("N,L,window,sinks", [(1, 1, 0, 0), (1, 300, 1, 0), (2, 2, 1, 1), (5, 250, 0, 4),
+                                              (3, 700, 200, 56), (3, 64, 64, 64)])
+def test_few_rows_of_many_heads(rf, B, H, Hkv, N, L, window, sinks):
+    q, k, v = make(N + H, B, H, Hkv, N, L, torch.bfloat16)
+    out, lse = run(rf, q, k, v, window, sinks)
+    pick = slice(0, None, 13)
+    check(out[pick], lse[pick], q[pick], k[pick], v[pick], window, sinks)
+
+
+def test_few_rows_see_nothing_else(rf):
+    q, k, v = make(12, 1, 8, 2, 6, 400, torch.bfloat16)
+    out, lse = run(rf, q, k, v, 50, 3)
+    far = torch.ones(400, dtype=torch.bool)
+    far[:3], far[345:] = False, False                    # rows 394..399 see 0..2 and 345..399
+    k[:, :, far], v[:, :, far] = float("nan"), float("inf")
+    again, lse2 = run(rf, q, k, v, 50, 3)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    v[:, :, 399] = float("nan")                          # the last position's own
+    last, _ = run(rf, q, k, v, 50, 3)
+    assert last[:, :, 5].isnan().all() and torch.equal(last[:, :, :5], out[:, :, :5])
