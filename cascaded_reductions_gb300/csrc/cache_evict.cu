@@ -16,7 +16,8 @@
 // compaction needs two sweeps with warp votes: the number kept before a row is
 // above_before + min(equal_before, equal_needed),  so ties go to the lowest index
 // without a second selection.  Weights are read from memory once and kept in
-// shared memory (up to 48 Ki of them; longer rows are read again from L2).  Four 8-bit histograms over all keys, one add per
+// shared memory (up to 48 Ki of them; longer rows are read again from L2).  Four
+// 8-bit histograms over all keys, one add per
 // distinct digit of a warp, took 44 us for 256 rows of 16384, this takes 26 us.
 //
 // evict_copy_kernel, bound by HBM: each kept row is read and written once.
