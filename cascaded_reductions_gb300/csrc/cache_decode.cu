@@ -25,6 +25,8 @@
 // P in two terms: the weights enter the second product as hi + lo, two 16-bit
 // terms, so that they carry 16 (bf16) or 22 (fp16) bits and the output is
 // rounded once; the 16 extra matrix instructions per tile are free here.
+// An infinite value times lo = 0, or times a lo below 0, makes its column NaN, so a
+// piece's columns that are NaN are computed again with whole weights (redo_columns).
 //
 // Split: a row group (sequence, key head, 16-row tile of query heads) is divided
 // into pieces by its own length, one CTA of four warps each; a step of the CTA
@@ -376,12 +378,82 @@ struct State {
   }
 };
 
+__device__ __forceinline__ bool any_nan(const float4& x) {
+  return x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w;
+}
+
+// Columns 4 lane .. + 3 of a 16-bit row, widened
+template <bool F16>
+__device__ __forceinline__ float4 load_row4(const uint8_t* row, int lane) {
+  const uint2 u = *reinterpret_cast<const uint2*>(row + lane * 8);
+  if constexpr (F16) {
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+  } else {
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  }
+}
+
+// A row's accumulator A over keys t0 .. t1 - 1, weights relative to `ref`, with the
+// columns that are NaN computed again key by key: a visible value of +-inf gives that
+// infinity.  Ends once they are all NaN again (a NaN value, or both infinities), which
+// they stay.  A call, so that the code of it lies out of the kernels' way: in line it
+// cost the single-token decode 0.2 of 5.6 us, although it does not run.
+struct Redo {
+  const uint8_t *q, *k, *v, *kp, *vp;    // the row; the group's keys and, before them, the prefix's
+  int ns, lo;                            // as in Group
+  int prefix, rows;                      // of kp and of k
+  int t0, t1;
+  float ref, scale_log2;
+};
+template <bool F16, bool PREFIX>
+__device__ __noinline__ float4 redo_columns(const Redo d, float4 A, int lane) {
+  constexpr int U = 4;                            // keys in flight
+  const float4 x = load_row4<F16>(d.q, lane);
+  float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t = d.t0; t < d.t1; t += U) {
+    float s[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool shared = PREFIX && t + u < d.ns;
+      const int key = t + u < d.ns ? t + u : t + u - d.ns + d.lo;
+      float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = k;
+      if (t + u < d.t1 && RF_IDX_OK(key, shared ? d.prefix : d.rows)) {
+        k = load_row4<F16>((shared ? d.kp : d.k) + (size_t)key * ROW_BYTES, lane);
+        v[u] = load_row4<F16>((shared ? d.vp : d.v) + (size_t)key * ROW_BYTES, lane);
+      }
+      s[u] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, x.w * k.w)));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = group_sum<32>(s[u]) * d.scale_log2;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t + u >= d.t1) break;
+      const float w = exp2f(s[u] - d.ref);
+      R.x = fmaf(w, v[u].x, R.x);
+      R.y = fmaf(w, v[u].y, R.y);
+      R.z = fmaf(w, v[u].z, R.z);
+      R.w = fmaf(w, v[u].w, R.w);
+    }
+    const bool again = (A.x != A.x && R.x == R.x) || (A.y != A.y && R.y == R.y) ||
+                       (A.z != A.z && R.z == R.z) || (A.w != A.w && R.w == R.w);
+    if (!__any_sync(0xffffffffu, again)) break;
+  }
+  return make_float4(A.x != A.x ? R.x : A.x, A.y != A.y ? R.y : A.y, A.z != A.z ? R.z : A.z,
+                     A.w != A.w ? R.w : A.w);
+}
+
 // Row r of the CTA's warps merged by one warp, four columns per lane, into out
 // and lse (`direct`: this was the whole group) or into the row's state `slot`.
-template <bool SCORES>
+// The CTA's keys are t0 .. t1 - 1 of group q.
+template <bool F16, bool SCORES, bool PREFIX>
 __device__ __forceinline__ void merge_warps(const CacheDecode& a, const float* acc_buf,
                                             const float2 (*ml_buf)[MROWS], size_t row, int r,
-                                            bool direct, int slot, int lane) {
+                                            bool direct, int slot, const Group& q, int t0, int t1,
+                                            int lane) {
   if (!RF_IDX_OK(row, rows_in(a))) return;
   float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -397,6 +469,12 @@ __device__ __forceinline__ void merge_warps(const CacheDecode& a, const float* a
     A.y = fmaf(f, v.y, A.y);
     A.z = fmaf(f, v.z, A.z);
     A.w = fmaf(f, v.w, A.w);
+  }
+  if (__any_sync(0xffffffffu, L > 0.f && any_nan(A))) {
+    const size_t own = q.kv0 * ROW_BYTES, pre = PREFIX ? q.prefix0 * ROW_BYTES : 0;
+    A = redo_columns<F16, PREFIX>({a.q + row * ROW_BYTES, a.k + own, a.v + own, a.kp + pre, a.vp + pre, q.ns, q.lo,
+                                   a.prefix, a.cap, t0, t1, ref_of(M), a.scale_log2},
+                                  A, lane);
   }
   const size_t states = (size_t)a.B * a.H * a.S_total;
   (void)states;                                   // read by the checked build only
@@ -582,9 +660,10 @@ cache_decode_kernel(const CacheDecode a) {
   st.give(acc_buf + warp * MROWS * MERGE_PITCH, sm_ml[warp], w, lane);
   __syncthreads();
   const bool direct = pieces == 1 && a.seg0 == 0;   // the output itself
+  const int key0 = k0 * WARPS * TK, key1 = min(q.n, k1 * WARPS * TK);
   for (int r = warp; r < w.n; r += WARPS)
-    merge_warps<SCORES>(a, acc_buf, sm_ml, w.row0 + r * (POSITIONS ? w.step : 1), r, direct,
-                        a.seg0 + piece, lane);
+    merge_warps<F16, SCORES, PREFIX>(a, acc_buf, sm_ml, w.row0 + r * (POSITIONS ? w.step : 1), r, direct,
+                                     a.seg0 + piece, q, key0, key1, lane);
   if constexpr (POSITIONS) return;
   if (waits) wait_prerequisite();       // the prefix's states, where there are some
   if constexpr (FUSED) {
