@@ -46,7 +46,11 @@
 // 536 for 4 x 32 heads of 8192 with a window of 1024.
 // Rescaling is lazy: the reference max m_ref of a row moves (and O and l are
 // multiplied by exp2(m_ref_old - m_ref_new)) only when the block max exceeds
-// it by more than 8, so p <= 2^8.
+// it by more than 8, so p <= 2^8.  An fp16 p has 11 bits down to 2^-14 and ends at
+// 2^-24, so it is taken 2^7 times as large (at most 2^15, of 65504): weights down
+// to 2^-21 of exp2(m_ref) keep their bits and only those below 2^-32 vanish from the
+// product (which l, summed unrounded, counts).  Without the factor 32768 keys
+// at 2^-26 of a first key's weight were lost altogether.
 //
 // The softmax warps tell CTA 0's MMA thread that S was read, that P was
 // written and that O was read with relaxed arrivals: each follows the
@@ -116,6 +120,7 @@ static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHER == THREADS * REGS,
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t S_COL = 0, P_COL = 256, O_COL = 384;
 constexpr float RESCALE_THRESHOLD = 8.0f;    // log2 units
+constexpr float P_SHIFT = 7.0f;              // log2 of the factor that an fp16 p is taken with
 
 struct Shared {
   uint64_t q_full[2];           // CTA 0: both Q tiles of a buffer
@@ -338,7 +343,8 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         m_ref = m_new;
         uint32_t w[NW > 0 ? 16 * NW : 1];
         if constexpr (NW > 0) {
-          const uint64_t nm2 = pack_f32x2(-m_new, -m_new);
+          const float nm = P::F16 ? P_SHIFT - m_new : -m_new;
+          const uint64_t nm2 = pack_f32x2(nm, nm);
           uint64_t sum2 = 0ull;
 #pragma unroll
           for (int c = 0; c < 16 * NW; ++c) {
@@ -401,7 +407,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // The output warps have read what was here two items ago: this block waited
       // for a P V that was issued after they had read that item's O.
       sh->part_l[t & 1][kh][r] = l;
-      if (kh == 0) sh->row_m[t & 1][r] = m_ref;
+      if (kh == 0) sh->row_m[t & 1][r] = P::F16 ? m_ref - P_SHIFT : m_ref;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh->l_ready[t & 1]);
     }

@@ -24,7 +24,9 @@
 //
 // P in two terms: the weights enter the second product as hi + lo, two 16-bit
 // terms, so that they carry 16 (bf16) or 22 (fp16) bits and the output is
-// rounded once; the 16 extra matrix instructions per tile are free here.
+// rounded once; the 16 extra matrix instructions per tile are free here.  fp16
+// ends at 2^-24, so its weights are taken 2^15 times as large (at most 2^15, of
+// 65504): 22 bits down to 2^-18 of the warp's largest, and no more than 2^-40 of it lost.
 // An infinite value times lo = 0, or times a lo below 0, makes its column NaN, so a
 // piece's columns that are NaN are computed again with whole weights (redo_columns).
 //
@@ -236,6 +238,8 @@ __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, 
 // (index 1); acc[d] holds columns 8 d + 2 (lane % 4) and + 1 of both.
 template <bool F16, bool SCORES, bool POSITIONS>
 struct State {
+  // weights are exp2(score - (m - SHIFT)); the state given away has m - SHIFT for its m
+  static constexpr float SHIFT = F16 ? 15.f : 0.f;
   uint32_t qf[HD / 16][4];
   float acc[HD / 8][4];
   float m0, m1, l0, l1;
@@ -316,7 +320,9 @@ struct State {
   const bool grew = mx0 > m0 || mx1 > m1;
   if (__any_sync(0xffffffffu, grew)) {
     const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-    const float c0 = exp2f(m0 - ref_of(n0)), c1 = exp2f(m1 - ref_of(n1));
+    // differences of the rounded references themselves
+    const float c0 = exp2f((m0 - SHIFT) - (ref_of(n0) - SHIFT));
+    const float c1 = exp2f((m1 - SHIFT) - (ref_of(n1) - SHIFT));
     m0 = n0;
     m1 = n1;
     l0 *= c0;
@@ -329,7 +335,7 @@ struct State {
       acc[d][3] *= c1;
     }
   }
-  const float f0 = ref_of(m0), f1 = ref_of(m1);
+  const float f0 = ref_of(m0) - SHIFT, f1 = ref_of(m1) - SHIFT;
   uint32_t hi[4], lw[4];
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {
@@ -373,7 +379,7 @@ struct State {
       for (int d = 0; d < HD / 8; ++d)
         *reinterpret_cast<float2*>(acc_buf + r * MERGE_PITCH + d * 8 + 2 * (lane & 3)) =
             make_float2(acc[d][2 * half], acc[d][2 * half + 1]);
-      if ((lane & 3) == 0) ml_buf[r] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+      if ((lane & 3) == 0) ml_buf[r] = half ? make_float2(m1 - SHIFT, l1) : make_float2(m0 - SHIFT, l0);
     }
   }
 };
