@@ -274,6 +274,11 @@ struct WindowPrefill {
                                          acc[3] != acc[3]);
     }
     const size_t o = ((size_t)bh * N + row) * HD + lane * 4;
+    if (l == 0.f) {                                     // every visible score is -inf
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = 0.f;
+      l = 1.f;
+    }
     if (RF_SPAN_OK(o, 4, q_n)) {
       uint2 w;
       w.x = pair::pack_16x2<F16>(acc[0] / l, acc[1] / l);

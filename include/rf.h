@@ -332,7 +332,8 @@ rf_status rf_incremental_quant_fp8_gemm(const void* x, int M, int K, const uint8
  *     p - window < j <= p or j < sinks; window = 0: every j <= p;
  *   - out is RF_F32 or of q's type (out_dtype), rounded once; lse fp32 in
  *     natural-log units, may be NULL where not stated otherwise.  A row without
- *     a visible key gets out = 0 and lse = -inf;
+ *     a visible key, or whose visible scores are all -inf, gets out = 0 and
+ *     lse = -inf;
  *   - an infinite value in a visible row makes its column of the output that
  *     infinity, and NaN where both signs meet or the weight underflows to 0;
  *   - seg_m, seg_l [B*H, S], seg_acc [B*H, S, D] fp32: scratch of one call in
