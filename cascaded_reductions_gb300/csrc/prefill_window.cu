@@ -21,8 +21,10 @@
 // reference starts at a finite value below every score, so such a block gives
 // weights of exactly 0.  The products still multiply those zeros with V, and
 // 0 * NaN is NaN: a value row that is not finite would reach rows that do not
-// see it.  A row whose output is NaN is therefore computed again after the
-// last item, from its visible keys alone.
+// see it.  A row with NaN in its output is therefore looked at again after the
+// last item: columns that are NaN by right (a value that the warp's 32 rows all see,
+// found in one pass over their keys) stay, the others are computed from the
+// row's visible keys alone.
 
 #include <cuda_fp16.h>
 
@@ -216,99 +218,161 @@ struct WindowPrefill {
     tc::tma_store_3d(map, box + HALF_BYTES, 64, pend.row, pend.bh);
   }
 
-  static __device__ __forceinline__ float widen(uint32_t w, int hi) {
-    if constexpr (F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-      return hi ? f.y : f.x;
-    }
-    return hi ? bf16_hi(w) : bf16_lo(w);
+  static __device__ __forceinline__ float2 widen2(uint32_t w) {
+    if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(bf16_lo(w), bf16_hi(w));
   }
   static __device__ __forceinline__ void widen4(const uint2& u, float (&f)[4]) {
-    f[0] = widen(u.x, 0);
-    f[1] = widen(u.x, 1);
-    f[2] = widen(u.y, 0);
-    f[3] = widen(u.y, 1);
+    const float2 a = widen2(u.x), b = widen2(u.y);
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
   }
   // elements [i, i + 4) of a tensor of n elements
   static __device__ __forceinline__ uint2 load4(const uint16_t* t, size_t i, size_t n) {
     (void)n;                                            // read by the checked build only
     return RF_SPAN_OK(i, 4, n) ? *reinterpret_cast<const uint2*>(t + i) : make_uint2(0, 0);
   }
-  // NaN among the 32-bit word's two values
-  static __device__ __forceinline__ bool has_nan(uint32_t w) {
+  // bits 0 and 1: whether the 32-bit word's two values are NaN
+  static __device__ __forceinline__ uint32_t nan_bits(uint32_t w) {
     const uint32_t inf = F16 ? 0x7c00u : 0x7f80u;
-    return (w & 0x7fffu) > inf || ((w >> 16) & 0x7fffu) > inf;
+    return ((w & 0x7fffu) > inf) | (((w >> 16) & 0x7fffu) > inf) << 1;
+  }
+  static __device__ __forceinline__ uint32_t nan_bits(const uint2& u) {
+    return nan_bits(u.x) | nan_bits(u.y) << 2;
+  }
+  size_t __device__ __forceinline__ q_elems() const { return (size_t)heads * N * HD; }
+  size_t __device__ __forceinline__ kv_elems() const { return (size_t)(heads / G) * L * HD; }
+
+  // Of this lane's four columns (bits), those that are NaN by right in all of rows
+  // first .. last: one of the values that all of them see is NaN, or one of the keys.
+  // `want`: the columns to look at.
+  __device__ __forceinline__ uint32_t nan_for_all(int bh, int first, int last, uint32_t want, int lane) const {
+    constexpr int U = 8;                                // keys in flight
+    const int p0 = L - N + first, lo = max(0, L - N + last - window + 1);
+    const int ns = min(min(sinks, lo), p0 + 1), n = ns + max(0, p0 - lo + 1);
+    const size_t kv0 = (size_t)(bh / G) * L;
+    uint32_t got = 0;
+    for (int t0 = 0; t0 < n; t0 += U) {
+      uint2 kk[U], vv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = min(t0 + u, n - 1), key = t < ns ? t : t - ns + lo;
+        kk[u] = load4(k, (kv0 + key) * HD + lane * 4, kv_elems());
+        vv[u] = load4(v, (kv0 + key) * HD + lane * 4, kv_elems());
+      }
+      uint32_t bad_key = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        bad_key |= nan_bits(kk[u]);
+        got |= nan_bits(vv[u]);
+      }
+      if (__any_sync(0xffffffffu, bad_key != 0)) return 15u;
+      if (!__any_sync(0xffffffffu, (want & ~got) != 0)) break;
+    }
+    return got;
   }
 
-  // One output row, from its visible keys alone: the warp's lanes hold four
-  // columns each, one key at a time, until every column is NaN (a NaN query, key or
-  // value row that the row sees; the lse in place then stands, no masked score
-  // entered it).
-  __device__ __forceinline__ void redo(int bh, int row, int lane) const {
+  // The NaN columns of one output row, but for those that are NaN by `right`, once
+  // more from the keys that the row sees; four columns per lane.  Ends once they are
+  // all NaN again.  The lse in place stands (no masked score entered it), unless
+  // the weights all vanished against the reference that the row started from.
+  // A row costs about 0.2 us per key.  The form of the loops here was chosen by the time
+  // of calls that never reach them, whose code lies beside it: other widths and
+  // orders cost the long windowed prefill 501 to 538 us instead of 499.
+  __device__ __forceinline__ void redo(int bh, int row, uint32_t right, int lane) const {
+    const size_t q0 = ((size_t)bh * N + row) * HD, o = q0 + lane * 4;
+    uint2 word = RF_SPAN_OK(o, 4, q_elems()) ? *reinterpret_cast<const uint2*>(out + o) : make_uint2(0, 0);
+    const uint32_t todo = nan_bits(word) & ~right;
+    if (!__any_sync(0xffffffffu, todo != 0)) return;
     const int p = L - N + row;
+    const int lo = max(0, p - window + 1), ns = min(sinks, lo), n = ns + p - lo + 1;
     const size_t kv0 = (size_t)(bh / G) * L;
-    const size_t q_n = (size_t)heads * N * HD, kv_n = (size_t)(heads / G) * L * HD;
     float qf[4];
-    widen4(load4(q, ((size_t)bh * N + row) * HD + lane * 4, q_n), qf);
-    const int lo = max(0, p - window + 1), ns = min(sinks, lo);
+    widen4(load4(q, q0 + lane * 4, q_elems()), qf);
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     bool gone = false;
-#pragma unroll 2
-    for (int t = 0; !gone && t < ns + p - lo + 1; ++t) {
-      const int key = t < ns ? t : t - ns + lo;
-      const size_t at = (kv0 + key) * HD + lane * 4;
-      float kf[4], vf[4];
-      widen4(load4(k, at, kv_n), kf);
-      widen4(load4(v, at, kv_n), vf);
-      float d = 0.f;
+    constexpr int U = 4;                                // keys in flight
+#pragma unroll 1
+    for (int t0 = 0; !gone && t0 < n; t0 += U) {
+      uint2 kk[U], vv[U];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d = fmaf(qf[e], kf[e], d);
-      const float s = group_sum<32>(d) * scale_log2;
-      const float mn = fmaxf(m, s), ref = ref_of(mn);
-      const float corr = exp2f(m - ref), w = exp2f(s - ref);
+      for (int u = 0; u < U; ++u) {
+        const int t = min(t0 + u, n - 1), key = t < ns ? t : t - ns + lo;
+        kk[u] = load4(k, (kv0 + key) * HD + lane * 4, kv_elems());
+        vv[u] = load4(v, (kv0 + key) * HD + lane * 4, kv_elems());
+      }
+      float s[U], mn = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float kf[4];
+        widen4(kk[u], kf);
+        s[u] = fmaf(qf[0], kf[0], fmaf(qf[1], kf[1], fmaf(qf[2], kf[2], qf[3] * kf[3])));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u] = t0 + u < n ? group_sum<32>(s[u]) * scale_log2 : -INFINITY;
+        mn = fmaxf(mn, s[u]);
+      }
+      const float ref = ref_of(mn), corr = exp2f(m - ref);
       m = mn;
-      l = fmaf(l, corr, w);
+      l *= corr;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], corr, w * vf[e]);
-      gone = __all_sync(0xffffffffu, acc[0] != acc[0] && acc[1] != acc[1] && acc[2] != acc[2] &&
-                                         acc[3] != acc[3]);
-    }
-    const size_t o = ((size_t)bh * N + row) * HD + lane * 4;
-    if (l == 0.f) {                                     // every visible score is -inf
+      for (int e = 0; e < 4; ++e) acc[e] *= corr;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = 0.f;
-      l = 1.f;
+      for (int u = 0; u < U; ++u) {
+        if (t0 + u >= n) break;
+        float vf[4];
+        widen4(vv[u], vf);
+        const float w = exp2f(s[u] - ref);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, vf[e], acc[e]);
+      }
+      uint32_t now = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) now |= (uint32_t)(acc[e] != acc[e]) << e;
+      gone = !__any_sync(0xffffffffu, (todo & ~now) != 0);
     }
-    if (RF_SPAN_OK(o, 4, q_n)) {
-      uint2 w;
-      w.x = pair::pack_16x2<F16>(acc[0] / l, acc[1] / l);
-      w.y = pair::pack_16x2<F16>(acc[2] / l, acc[3] / l);
-      *reinterpret_cast<uint2*>(out + o) = w;
-    }
-    if (lse != nullptr && lane == 0 && !gone && RF_IDX_OK((size_t)bh * N + row, (size_t)heads * N))
-      lse[(size_t)bh * N + row] = (m + log2f(l)) * kLn2;
+    if (gone) return;
+    float y[4];                                         // l = 0: every visible score is -inf
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = l == 0.f ? 0.f : acc[e] / l;
+    const uint32_t y01 = pair::pack_16x2<F16>(y[0], y[1]), y23 = pair::pack_16x2<F16>(y[2], y[3]);
+    const uint32_t m01 = (todo & 1u ? 0xffffu : 0u) | (todo & 2u ? 0xffff0000u : 0u);
+    const uint32_t m23 = (todo & 4u ? 0xffffu : 0u) | (todo & 8u ? 0xffff0000u : 0u);
+    word.x = (word.x & ~m01) | (y01 & m01);
+    word.y = (word.y & ~m23) | (y23 & m23);
+    if (RF_SPAN_OK(o, 4, q_elems())) *reinterpret_cast<uint2*>(out + o) = word;
+    const size_t i = (size_t)bh * N + row;
+    if (lse != nullptr && lane == 0 && RF_IDX_OK(i, (size_t)heads * N) && lse[i] == -INFINITY)
+      lse[i] = (m + log2f(l)) * kLn2;
   }
 
-  // Rows of this thread whose stored values hold a NaN are computed again.
+  // Rows of this thread whose stored values hold a NaN are looked at again, a
+  // warp's 32 adjacent positions of a head together.
   __device__ __forceinline__ void repair(int cluster, int nclusters, int rank, int r) const {
     Item it;
+    const int lane = r & 31;
     for (int t = 0; item(t, cluster, nclusters, it); ++t) {
       const int row = it.row0 + row_of(rank, r), head = it.bh + head_of(rank, r);
       bool nan = false;
       if (row < N) {
         const size_t o = ((size_t)head * N + row) * HD;
         for (int c = 0; c < 16; ++c) {
-          if (!RF_SPAN_OK(o + c * 8, 8, (size_t)heads * N * HD)) continue;
+          if (!RF_SPAN_OK(o + c * 8, 8, q_elems())) continue;
           const uint4 u = *(reinterpret_cast<const uint4*>(out + o) + c);
-          nan |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
+          nan |= (nan_bits(u.x) | nan_bits(u.y) | nan_bits(u.z) | nan_bits(u.w)) != 0;
         }
       }
-      uint32_t todo = __ballot_sync(0xffffffffu, nan);
-      while (todo) {
-        const int lane0 = __ffs(todo) - 1;
-        todo &= todo - 1;
-        redo(head, __shfl_sync(0xffffffffu, row, lane0), r & 31);
+      const uint32_t rows = __ballot_sync(0xffffffffu, nan);
+      if (rows == 0) continue;
+      const int row0 = row - lane, last = min(row0 + 31, N - 1);
+      uint32_t want = 0;                                // of this lane's columns, in any of the rows
+      for (uint32_t left = rows; left; left &= left - 1) {
+        const size_t o = ((size_t)head * N + row0 + __ffs(left) - 1) * HD + lane * 4;
+        if (RF_SPAN_OK(o, 4, q_elems())) want |= nan_bits(*reinterpret_cast<const uint2*>(out + o));
       }
+      const uint32_t right = nan_for_all(head, row0, last, want, lane);
+      for (uint32_t left = rows; left; left &= left - 1) redo(head, row0 + __ffs(left) - 1, right, lane);
     }
   }
   __device__ __forceinline__ void after(bool any, int cluster, int nclusters, int rank, int r) const {
