@@ -366,7 +366,7 @@ rf_status rf_attn_prefill_window(const void* q, const void* k, const void* v, in
 
 int rf_prefix_segments(int B, int H, int Hkv, int prefix) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128 || prefix <= 0 ||
-      (long long)B * Hkv > 0x7fffffffLL)
+      prefix > (1 << 30) || (long long)B * Hkv > 0x7fffffffLL)
     return 0;
   return rf::prefix_segments(B, H, Hkv, prefix);
 }

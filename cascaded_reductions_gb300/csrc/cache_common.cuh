@@ -55,12 +55,15 @@ inline rf_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned
 // call, enough to pay for a CTA's start and end in a large one.
 constexpr int kFewKeys = 4 * kDecodeTile, kManyKeys = 768;
 
+// Counts reach the largest int, where a + b - 1 would not fit one.
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
 // Whether a call of `groups` row groups of up to `keys` visible keys is small: its
 // pieces fit two CTAs on every SM, at most sixteen steps of 64 keys each (with a
 // limit of four, 64 rows of 2048 keys took 17.4 us instead of 15.6, 8 rows of 32768
 // 33.3 instead of 26.6; with 64, 192 ragged rows of 3000 39.8 instead of 36.0).
 inline bool decode_is_few(long long groups, int keys, int sms) {
-  return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= 32ll * sms;
+  return groups <= 2ll * sms && groups * ceil_div(keys, kFewKeys) <= 32ll * sms;
 }
 
 // Pieces of the longest row of a large call.  Rows of up to two pieces stay whole, to
@@ -68,7 +71,7 @@ inline bool decode_is_few(long long groups, int keys, int sms) {
 // 1024 rows of 1024 keys 56.5 and 60.2 us; one row of 1536 among 255 of 192 keys takes
 // 17.8 and 14.2 us.
 inline int decode_many_pieces(int keys) {
-  return keys <= 2 * kManyKeys ? 1 : (keys + kManyKeys - 1) / kManyKeys;
+  return keys <= 2 * kManyKeys ? 1 : (int)ceil_div(keys, kManyKeys);
 }
 
 // Pieces per row for such a call: a small one is divided as far as one wave of two
@@ -78,7 +81,7 @@ inline int decode_segments(int groups, int keys, int sms) {
   long long s;
   if (decode_is_few(groups, keys, sms)) {
     s = 2ll * sms / groups;
-    const int steps = (keys + kFewKeys - 1) / kFewKeys;
+    const long long steps = ceil_div(keys, kFewKeys);
     if (s > steps) s = steps;
   } else {
     s = decode_many_pieces(keys);
@@ -94,7 +97,7 @@ constexpr int kSharedSteps = 14;
 static_assert(kSharedSteps <= 32, "such a call is small");
 inline bool decode_prefix_is_few(long long groups, long long prefix, int cap, int sms) {
   const long long keys = prefix + cap;
-  return groups <= 2ll * sms && groups * ((keys + kFewKeys - 1) / kFewKeys) <= (long long)kSharedSteps * sms;
+  return groups <= 2ll * sms && groups * ceil_div(keys, kFewKeys) <= (long long)kSharedSteps * sms;
 }
 
 // Whether a windowed prefill is so small that a CTA per position and row group is
@@ -105,7 +108,7 @@ inline bool decode_prefix_is_few(long long groups, long long prefix, int cap, in
 constexpr int kRowsSteps = 6, kRowsKeys = 1024;
 inline bool prefill_is_few(long long groups, long long keys, int sms) {
   return groups <= 2ll * sms && keys <= kRowsKeys &&
-         groups * ((keys + kFewKeys - 1) / kFewKeys) <= (long long)kRowsSteps * sms;
+         groups * ceil_div(keys, kFewKeys) <= (long long)kRowsSteps * sms;
 }
 
 // One call's arguments.  Segment states are scratch between kernels: seg_m

@@ -157,8 +157,8 @@ struct PrefixStates {
 Split make_split(int B, int H, int Hkv, int prefix, int slots, int pairs) {
   const int G = H / Hkv, nb = 128 / G;
   Split s = {};
-  s.blocks = (prefix + BN - 1) / BN;
-  s.tiles = Hkv * ((B + 2 * nb - 1) / (2 * nb));
+  s.blocks = (int)ceil_div(prefix, BN);
+  s.tiles = Hkv * (int)ceil_div(B, 2 * nb);
   s.total = (long long)s.tiles * s.blocks;
   long long c = pairs < s.total ? pairs : s.total;
   // an item is touched by at most ceil(clusters / tiles) + 1 clusters
@@ -181,7 +181,7 @@ rf_status launch_t(const void* q, const void* kp, const void* vp, int prefix, in
   p.seg_m = seg_m, p.seg_l = seg_l, p.seg_acc = seg_acc;
   p.B = B, p.H = H, p.G = H / Hkv, p.P = prefix;
   p.nb = 128 / p.G;
-  p.tiles_per_head = (B + 2 * p.nb - 1) / (2 * p.nb);
+  p.tiles_per_head = (int)ceil_div(B, 2 * p.nb);
   p.S_total = S_total;
   p.prefix_slots = Sp;
   p.split = make_split(B, H, Hkv, prefix, Sp, pairs);
