@@ -220,6 +220,11 @@ def _i32(n):
     return n if -1 <= n <= 0x7fffffff else (0x7fffffff if n > 0 else -1)
 
 
+def _c_ints(*counts):
+    """Counts for C ints (ctypes would cut off their high bits)."""
+    return tuple(map(_i32, counts))
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -465,7 +470,7 @@ def rf_incremental_quant_fp8_gemm(x, wq, sw, y, sx_final=None, stream=None):
 def rf_decode_segments(groups, keys):
     """A number of segments that fills the current device: ``groups`` =
     B * Hkv * ceil(G / 16) rows of CTAs over up to ``keys`` visible keys each."""
-    return _lib.rf_decode_segments(int(groups), int(keys))
+    return _lib.rf_decode_segments(*_c_ints(int(groups), int(keys)))
 
 
 def _need_cache(q, k, v, lens):
@@ -504,8 +509,8 @@ def rf_attn_decode_window(q, k, v, lens, window, sinks, S, scale, seg_m, seg_l, 
     if lse is not None:
         _on(dev, lse, torch.float32, (B, H), "lse")
     _call_on(dev, stream, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, _i32(window),
-             _i32(sinks), S, scale, _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
+             k.data_ptr(), v.data_ptr(), _addr(lens), *_c_ints(B, H, Hkv, cap, D, window, sinks, S), scale,
+             _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
              counters.data_ptr(), out.data_ptr(), _cache_dtype(out.dtype, "out"), _addr(lse))
 
 
@@ -524,7 +529,7 @@ def rf_attn_decode_weights(q, k, v, lens, S, scale, seg_m, seg_l, seg_acc, count
     if weight is not None:
         _on(dev, weight, torch.float32, (B, Hkv, cap), "weight")
     _call_on(dev, stream, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, S, scale,
+             k.data_ptr(), v.data_ptr(), _addr(lens), *_c_ints(B, H, Hkv, cap, D, S), scale,
              _cache_dtype(q.dtype, "q"), seg_m.data_ptr(), seg_l.data_ptr(), seg_acc.data_ptr(),
              counters.data_ptr(), scores.data_ptr(), out.data_ptr(),
              _cache_dtype(out.dtype, "out"), _addr(lse), _addr(weight), weight_out.data_ptr())
@@ -546,13 +551,13 @@ def rf_attn_prefill_window(q, k, v, window, sinks, scale, out, lse=None, stream=
     if lse is not None:
         _on(dev, lse, torch.float32, (B, H, N), "lse")
     _call_on(dev, stream, "rf_attn_prefill_window", _lib.rf_attn_prefill_window, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), B, H, Hkv, N, L, D, _i32(window), _i32(sinks), scale,
+             k.data_ptr(), v.data_ptr(), *_c_ints(B, H, Hkv, N, L, D, window, sinks), scale,
              _cache_dtype(dt, "q"), out.data_ptr(), _addr(lse))
 
 
 def rf_prefix_segments(B, H, Hkv, prefix):
     """Pieces that rf_attn_decode_shared makes of the prefix on the current device (0: none)."""
-    return _lib.rf_prefix_segments(int(B), int(H), int(Hkv), int(prefix))
+    return _lib.rf_prefix_segments(*_c_ints(int(B), int(H), int(Hkv), int(prefix)))
 
 
 def rf_attn_decode_shared(q, kp, vp, k, v, lens, Sp, S, scale, seg_m, seg_l, seg_acc, counters,
@@ -570,8 +575,8 @@ def rf_attn_decode_shared(q, kp, vp, k, v, lens, Sp, S, scale, seg_m, seg_l, seg
     if lse is not None:
         _on(dev, lse, torch.float32, (B, H), "lse")
     _call_on(dev, stream, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
-             kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B, H,
-             Hkv, cap, D, Sp, S, scale, _cache_dtype(q.dtype, "q"), seg_m.data_ptr(),
+             kp.data_ptr(), vp.data_ptr(), _i32(prefix), k.data_ptr(), v.data_ptr(), _addr(lens),
+             *_c_ints(B, H, Hkv, cap, D, Sp, S), scale, _cache_dtype(q.dtype, "q"), seg_m.data_ptr(),
              seg_l.data_ptr(), seg_acc.data_ptr(), counters.data_ptr(), out.data_ptr(),
              _cache_dtype(out.dtype, "out"), _addr(lse))
 
@@ -605,8 +610,8 @@ def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight
     _on(dev, lens_out, torch.int32, (B,), "lens_out")
     _on(dev, kept, torch.int32, (B, Hkv, keep), "kept")
     _call_on(dev, stream, "rf_cache_evict", _lib.rf_cache_evict, k.data_ptr(), _addr(v),
-             weight.data_ptr(), _addr(lens), B, Hkv, cap, D, _cache_dtype(k.dtype, "k"), keep,
-             sinks, recent, k_out.shape[2], k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
+             weight.data_ptr(), _addr(lens), *_c_ints(B, Hkv, cap, D), _cache_dtype(k.dtype, "k"),
+             *_c_ints(keep, sinks, recent, k_out.shape[2]), k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
              lens_out.data_ptr(), kept.data_ptr())
 
 
@@ -799,8 +804,8 @@ def attn_decode_window(q, k, v, lens=None, window=0, sinks=0, scale=None, work=N
     work.check(dev, B, H, Hkv, D)
     out, lse = _outputs(q, out_dtype)
     _call_on(dev, None, "rf_attn_decode_window", _lib.rf_attn_decode_window, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, _i32(window),
-             _i32(sinks), work.S, D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
+             k.data_ptr(), v.data_ptr(), _addr(lens), *_c_ints(B, H, Hkv, cap, D, window, sinks, work.S),
+             D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
              out.data_ptr(), _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
 
@@ -846,8 +851,8 @@ def attn_decode_shared(q, kp, vp, k, v, lens=None, scale=None, work=None, out_dt
     work.check(dev, B, H, Hkv, D)
     out, lse = _outputs(q, out_dtype)
     _call_on(dev, None, "rf_attn_decode_shared", _lib.rf_attn_decode_shared, q.data_ptr(),
-             kp.data_ptr(), vp.data_ptr(), prefix, k.data_ptr(), v.data_ptr(), _addr(lens), B,
-             H, Hkv, cap, D, work.prefix_S, work.S, D ** -0.5 if scale is None else scale,
+             kp.data_ptr(), vp.data_ptr(), _i32(prefix), k.data_ptr(), v.data_ptr(), _addr(lens),
+             *_c_ints(B, H, Hkv, cap, D, work.prefix_S, work.S), D ** -0.5 if scale is None else scale,
              _cache_dtype(q.dtype, "q"), *work.addresses, out.data_ptr(),
              _cache_dtype(out.dtype, "out"), lse.data_ptr())
     return out, lse
@@ -882,7 +887,7 @@ def attn_decode_weights(q, k, v, lens=None, weight=None, scale=None, work=None, 
     else:
         _on(dev, weight_out, torch.float32, (B, Hkv, cap), "weight_out")
     _call_on(dev, None, "rf_attn_decode_weights", _lib.rf_attn_decode_weights, q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _addr(lens), B, H, Hkv, cap, D, work.S,
+             k.data_ptr(), v.data_ptr(), _addr(lens), *_c_ints(B, H, Hkv, cap, D, work.S),
              D ** -0.5 if scale is None else scale, _cache_dtype(q.dtype, "q"), *work.addresses,
              work.scores.data_ptr(), out.data_ptr(), _cache_dtype(out.dtype, "out"),
              lse.data_ptr(), _addr(weight), weight_out.data_ptr())
@@ -917,7 +922,7 @@ def cache_evict(k, v, weight, lens, keep, sinks=0, recent=0, cap_out=None, out=N
     new = dict(device=k.device, dtype=torch.int32)
     lens_out, kept = torch.empty(B, **new), torch.empty((B, Hkv, keep), **new)
     _call_on(dev, None, "rf_cache_evict", _lib.rf_cache_evict, k.data_ptr(), _addr(v),
-             weight.data_ptr(), _addr(lens), B, Hkv, cap, D, _cache_dtype(k.dtype, "k"), keep,
-             sinks, recent, k_out.shape[2], k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
+             weight.data_ptr(), _addr(lens), *_c_ints(B, Hkv, cap, D), _cache_dtype(k.dtype, "k"),
+             *_c_ints(keep, sinks, recent, k_out.shape[2]), k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
              lens_out.data_ptr(), kept.data_ptr())
     return k_out, v_out, weight_out, lens_out, kept
