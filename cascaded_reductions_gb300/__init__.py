@@ -226,7 +226,13 @@ def _c_ints(*counts):
 
 
 def _addr(t):
-    return None if t is None else t.data_ptr()
+    """The address of an optional tensor: null for None, and only then."""
+    if t is None:
+        return None
+    p = t.data_ptr()
+    if p == 0 and t.numel() > 0:
+        raise ValueError("a tensor without memory")
+    return p
 
 
 def version():

@@ -21,7 +21,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
-#include <exception>
+#include <stdexcept>
 
 #include "rf.h"
 
@@ -43,6 +43,15 @@ bool optional_tensor(PyObject* o, const at::Tensor** t) {
   if (o == Py_None) return true;
   *t = tensor(o);
   return *t != nullptr;
+}
+
+// The address of an optional tensor: null for none, and only then.
+template <typename T>
+const T* optional_address(const at::Tensor* t) {
+  if (!t) return nullptr;
+  const void* p = t->const_data_ptr();
+  if (!p && t->numel() > 0) throw std::runtime_error("a tensor without memory");
+  return static_cast<const T*>(p);
 }
 
 int type_code(at::ScalarType t) {
@@ -83,9 +92,7 @@ bool scale_of(PyObject* o, int D, float* scale) {
 struct Cache {
   const at::Tensor *q, *k, *v, *lens;
   int dev, B, H, Hkv, cap, D, type;
-  const int32_t* lens_ptr() const {
-    return lens ? static_cast<const int32_t*>(lens->const_data_ptr()) : nullptr;
-  }
+  const int32_t* lens_ptr() const { return optional_address<int32_t>(lens); }
 };
 
 // q [B, H, D], k and v [B, Hkv, cap, D], lens [B] int32 or None, on the current device.
@@ -154,13 +161,27 @@ PyObject* pack(T&&... t) {
   return r;
 }
 
+// Without the GIL while it lives.  An exception on its way out takes the GIL back
+// (a tensor without memory, or a wrapper of one, throws when asked for its address).
+class Released {
+ public:
+  Released() : state_(PyEval_SaveThread()) {}
+  ~Released() { PyEval_RestoreThread(state_); }
+  Released(const Released&) = delete;
+  Released& operator=(const Released&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // Runs `call` without the GIL; its status if that is not RF_OK, else null.
 template <typename F>
 PyObject* failed(F call) {
   int status;
-  Py_BEGIN_ALLOW_THREADS
-  status = call();
-  Py_END_ALLOW_THREADS
+  {
+    Released released;
+    status = call();
+  }
   return status == RF_OK ? nullptr : PyLong_FromLong(status);
 }
 
@@ -171,7 +192,7 @@ PyObject* guarded(F body) {
   try {
     at::AutoDispatchBelowADInplaceOrView below;
     return body();
-  } catch (const std::exception&) {
+  } catch (...) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
@@ -261,7 +282,7 @@ PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
               static_cast<float*>(w.l), static_cast<float*>(w.acc), static_cast<int*>(w.counters),
               static_cast<float*>(scores->mutable_data_ptr()), out.mutable_data_ptr(), c.type,
               static_cast<float*>(lse.mutable_data_ptr()),
-              weight ? static_cast<const float*>(weight->const_data_ptr()) : nullptr,
+              optional_address<float>(weight),
               static_cast<float*>(total.mutable_data_ptr()), stream_of(c.dev));
         }))
       return e;
@@ -334,9 +355,9 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor kept = like(*k, {B, Hkv, keep}, at::kInt);
     if (PyObject* e = failed([&] {
           return reinterpret_cast<decltype(&rf_cache_evict)>(fn)(
-              k->const_data_ptr(), v ? v->const_data_ptr() : nullptr,
+              k->const_data_ptr(), optional_address<void>(v),
               static_cast<const float*>(weight->const_data_ptr()),
-              lens ? static_cast<const int32_t*>(lens->const_data_ptr()) : nullptr, (int)B, (int)Hkv,
+              optional_address<int32_t>(lens), (int)B, (int)Hkv,
               (int)cap, (int)D, code, keep, sinks, recent, (int)cap_out, k_out->mutable_data_ptr(),
               v_out ? v_out->mutable_data_ptr() : nullptr,
               static_cast<float*>(weight_out->mutable_data_ptr()),
