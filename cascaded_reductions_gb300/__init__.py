@@ -23,6 +23,7 @@ instead, e.g. the bounds-checked debug variant that
 import ctypes
 import os
 import typing
+import warnings
 
 import torch
 
@@ -96,8 +97,8 @@ _lib = load_library()
 
 
 def _load_calls():
-    """The extension built from csrc/calls.cpp, or None: the wrappers below then marshal the
-    same calls in Python."""
+    """The extension built from csrc/calls.cpp, or None where it is not there or does not load (with
+    a warning): the wrappers below then marshal the same calls in Python."""
     from . import _build
     path, _ = _build.calls_path()
     if path is None or not os.path.exists(path):
@@ -105,8 +106,13 @@ def _load_calls():
     import importlib.machinery
     import importlib.util
     loader = importlib.machinery.ExtensionFileLoader("_rf_calls", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_rf_calls", loader))
-    loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_rf_calls", loader))
+        loader.exec_module(module)
+    except (ImportError, OSError) as e:
+        warnings.warn(f"{os.path.basename(path)} does not load, its calls are marshalled in Python: {e}",
+                      RuntimeWarning, stacklevel=2)
+        return None
     return module
 
 

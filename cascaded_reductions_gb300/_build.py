@@ -53,21 +53,23 @@ def build_calls(force=False):
     inc = [INCLUDE, os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", src, "-o", path + ".tmp"]
+    tmp = f"{path}.{os.getpid()}.tmp"       # of this process: builds may run side by side
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", src, "-o", tmp]
     cmd += [f"-I{i}" for i in inc]
     cmd += ["-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
-        err = r.stderr if r.returncode else ""
+        if r.returncode == 0:
+            os.replace(tmp, path)
+            return path
+        err = f"status {r.returncode} {r.stderr[-2000:]}"
     except OSError as e:
         err = str(e)
-    if err:
-        print(f"calls.cpp not built, the Python calls marshal in Python: {err[-2000:]}")
-        if os.path.exists(path):
-            os.remove(path)     # of an older rf.h
-        return None
-    os.replace(path + ".tmp", path)
-    return path
+    print(f"calls.cpp not built, the Python calls marshal in Python: {err}")
+    for p in (tmp, path):                   # what is there is of an older rf.h
+        if os.path.exists(p):
+            os.remove(p)
+    return None
 
 
 def _nvcc():
