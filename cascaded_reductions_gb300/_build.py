@@ -12,6 +12,7 @@ import glob
 import hashlib
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,7 +27,7 @@ LIB = os.path.join(HERE, "librf.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
-              "-Xptxas", "-warn-spills", "-I", INCLUDE, "-I", CSRC] + ARCH
+              "-Xptxas", "-v,-warn-spills", "-I", INCLUDE, "-I", CSRC] + ARCH
 
 
 def calls_path():
@@ -98,12 +99,46 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _log(obj):
+    """Where the compiler's report on an object's kernels is kept."""
+    return obj[:-2] + ".ptxas"
+
+
 def _compile(nvcc, src, obj, extra):
     cmd = [nvcc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stderr}")
+    with open(_log(obj), "w") as f:
+        f.write(r.stderr)
     return r.stderr
+
+
+def registers(log):
+    """Registers per thread of each kernel that a compiler's report names, by mangled name."""
+    used, name = {}, None
+    for line in log.splitlines():
+        m = re.search(r"Compiling entry function '(\w+)'", line)
+        name = m.group(1) if m else name
+        m = re.search(r"Used (\d+) registers", line)
+        if m and name:
+            used[name], name = int(m.group(1)), None
+    return used
+
+
+def pair_registers():
+    """What every attention kernel on CTA pairs has to be compiled to: they divide the registers of
+    exactly so many per thread between their warpgroups, and refuse to be launched with others."""
+    with open(os.path.join(CSRC, "attn_pair.cuh")) as f:
+        return int(re.search(r"constexpr int REGS = (\d+)", f.read()).group(1))
+
+
+def _report_pairs(log):
+    want = pair_registers()
+    for name, n in registers(log).items():
+        if "attn_pair_kernel" in name and n != want:
+            print(f"WARNING: {name} has {n} registers per thread instead of {want}: the calls that run on it "
+                  "will return RF_ERR_UNSUPPORTED", file=sys.stderr)
 
 
 def build(force=False, verbose=False, extra_flags=(), lib=None, objdir=None):
@@ -127,9 +162,11 @@ def build(force=False, verbose=False, extra_flags=(), lib=None, objdir=None):
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         calls = ex.submit(build_calls, force) if lib == LIB else None
         for s, o in zip(srcs, objs):
-            if force or _stale(o, [s] + hdrs):
+            if force or _stale(o, [s] + hdrs) or not os.path.exists(_log(o)):
                 jobs.append(ex.submit(_compile, nvcc, s, o, list(extra_flags)))
         logs = [j.result() for j in jobs]
+        for lg in logs:
+            _report_pairs(lg)
         if calls is not None:
             calls.result()
     if verbose:
