@@ -313,7 +313,7 @@ rf_status rf_attn_decode_weights(const void* q, const void* k, const void* v, co
   if (weight != weight_out && overlap(weight, bytes, weight_out, bytes)) return RF_ERR_INVALID_ARG;
   if ((long long)B * Hkv * ((cap + 255) / 256) > 0x7fffffffLL) return RF_ERR_UNSUPPORTED;
   if (!rf::aligned16(q) || !rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(out) ||
-      !rf::aligned16(seg_acc))
+      !rf::aligned16(seg_acc) || !rf::aligned16(scores))
     return RF_ERR_MISALIGNED;
   rf::CacheDecode a = {};
   a.q = static_cast<const uint8_t*>(q);

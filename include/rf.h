@@ -428,7 +428,7 @@ rf_status rf_attn_decode_shared(const void* q, const void* kp, const void* vp, i
  * Behind the end weight_out is a copy of weight.
  *   weight      [B, Hkv, cap] fp32, may be NULL (zeros) or equal to weight_out
  *               (in place; no other overlap)
- *   scores      [B, H, cap] fp32 scratch
+ *   scores      [B, H, cap] fp32 scratch, 16-byte aligned (else RF_ERR_MISALIGNED)
  *   weight_out  [B, Hkv, cap] fp32 out
  * Two launches or three (the weights need the finished normaliser of their row).
  */
