@@ -755,7 +755,8 @@ def decode_workspace(B, H, Hkv, cap, D=128, prefix=0, window=0, sinks=0, weights
                      device=None):
     """Scratch for attn_decode_window (window, sinks as in the call), attn_decode_shared (the
     prefix's length) or attn_decode_weights (weights=True).  S pieces per row (None: as many as
-    fill the device)."""
+    fill the device).  The counters are zeroed on the current stream: a call on another stream
+    has to come after that."""
     if H < 1 or Hkv < 1 or H % Hkv:
         raise ValueError("H must be a positive multiple of Hkv")
     with torch.cuda.device(torch.device("cuda" if device is None else device)):

@@ -635,8 +635,9 @@ cache_decode_kernel(const CacheDecode a) {
   const int k1 = (int)((long long)steps * (piece + 1) / pieces);
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * RING_BYTES;
 
-  // a large call's cache passes through L2 once; what it leaves there for the
-  // next kernel (states, scores) stays
+  // a large call's cache is loaded evict-first, so that what it leaves in L2 for the
+  // next kernel (states, scores) stays; with more than 16 query heads per key head
+  // each tile of them reads the same keys
   const uint64_t policy = l2_policy(!FUSED);
   int in = 0;                           // the stage that the next copies go to
   auto issue = [&](int k) {

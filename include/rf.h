@@ -343,7 +343,9 @@ rf_status rf_incremental_quant_fp8_gemm(const void* x, int M, int K, const uint8
  *     replays) that may overlap on the GPU need scratch and counters of their
  *     own.  S is the most pieces that a row's keys may be divided into, at most
  *     4096 (rf_decode_segments proposes one; 1 leaves every row whole): results
- *     do not depend on which CTA finishes first.
+ *     do not depend on which CTA finishes first;
+ *   - no output, scratch or counter overlaps an input or another of them, but
+ *     where a call says so.  Only what the calls' own sections name is checked.
  * Errors common to them: RF_ERR_INVALID_ARG for null pointers (but those that
  * may be NULL), sizes <= 0, H % Hkv != 0, window or sinks < 0, S < 1, a
  * non-finite scale or a bad dtype; RF_ERR_UNSUPPORTED for D != 128, RF_F32
@@ -361,7 +363,8 @@ int rf_decode_segments(int groups, int keys);
 
 /*
  * rf_attn_decode_window -- one token per sequence over the visible keys of a
- * ragged batch of caches, in one launch.
+ * ragged batch of caches.  One launch for a call whose pieces fit the device at once,
+ * two for a larger one with divided rows.
  *   q [B, H, D];  k, v [B, Hkv, cap, D];  out [B, H, D];  lse [B, H]
  */
 rf_status rf_attn_decode_window(const void* q, const void* k, const void* v, const int32_t* lens,
@@ -405,7 +408,8 @@ int rf_prefix_segments(int B, int H, int Hkv, int prefix);
  * (on the tensor cores, B * G rows against each key), the own keys as by
  * rf_attn_decode_window, and the states are merged.  Two launches or three; a
  * small call reads the prefix as the first keys of every sequence, in one
- * launch and at most Sp + S pieces.
+ * launch and at most Sp + S pieces.  Its weights are not rounded to 16 bits; in a
+ * larger call those over the prefix are, so last bits depend on the call's size.
  *   q [B, H, D];  kp, vp [Hkv, prefix, D], prefix >= 1;  k, v [B, Hkv, cap, D]
  *   with lens [B] own keys each (0 allowed; the query stands behind all of them)
  *   Sp   most pieces of the prefix, >= 2;  S  most pieces of the own keys, >= 1
