@@ -120,7 +120,9 @@ static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHER == THREADS * REGS,
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t S_COL = 0, P_COL = 256, O_COL = 384;
 constexpr float RESCALE_THRESHOLD = 8.0f;    // log2 units
-constexpr float P_SHIFT = 7.0f;              // log2 of the factor that an fp16 p is taken with
+constexpr float P_SHIFT = 7.0f;              // log2 of the factor that an fp16 p is taken with,
+constexpr float P_SHIFT_LIMIT = 1048576.0f;  // for references up to 2^20: there m - 7 is off by at most
+                                             // 2^-4, while from 2^24 on it may be m - 8 or less, and p 2^16
 
 struct Shared {
   uint64_t q_full[2];           // CTA 0: both Q tiles of a buffer
@@ -336,15 +338,17 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ++x;
         const float pm = fmaxf(red[r], red[BM + r]);
         const float mt = pm * scale_log2;
-        const bool move = mt > m_ref + RESCALE_THRESHOLD;
-        const float m_new = move ? mt : m_ref;
+        // an fp16 reference lies P_SHIFT below the maximum that it was taken from
+        const bool low = P::F16 && fabsf(m_ref) < P_SHIFT_LIMIT;
+        const bool move = mt > m_ref + (low ? RESCALE_THRESHOLD + P_SHIFT : RESCALE_THRESHOLD);
+        const float m_top = P::F16 && fabsf(mt) < P_SHIFT_LIMIT ? mt - P_SHIFT : mt;
+        const float m_new = move ? m_top : m_ref;
         const float alpha = ex2(m_ref - m_new);
         l *= alpha;
         m_ref = m_new;
         uint32_t w[NW > 0 ? 16 * NW : 1];
         if constexpr (NW > 0) {
-          const float nm = P::F16 ? P_SHIFT - m_new : -m_new;
-          const uint64_t nm2 = pack_f32x2(nm, nm);
+          const uint64_t nm2 = pack_f32x2(-m_new, -m_new);
           uint64_t sum2 = 0ull;
 #pragma unroll
           for (int c = 0; c < 16 * NW; ++c) {
@@ -407,7 +411,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // The output warps have read what was here two items ago: this block waited
       // for a P V that was issued after they had read that item's O.
       sh->part_l[t & 1][kh][r] = l;
-      if (kh == 0) sh->row_m[t & 1][r] = P::F16 ? m_ref - P_SHIFT : m_ref;
+      if (kh == 0) sh->row_m[t & 1][r] = m_ref;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh->l_ready[t & 1]);
     }

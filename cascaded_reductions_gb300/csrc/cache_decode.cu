@@ -238,8 +238,13 @@ __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, 
 // (index 1); acc[d] holds columns 8 d + 2 (lane % 4) and + 1 of both.
 template <bool F16, bool SCORES, bool POSITIONS>
 struct State {
-  // weights are exp2(score - (m - SHIFT)); the state given away has m - SHIFT for its m
-  static constexpr float SHIFT = F16 ? 15.f : 0.f;
+  // The weights' reference for the maximum m; the state given away has it for its m.
+  // From 2^24 on m - 15 may round to m - 16 or less, and a weight to 2^16: m itself then.
+  static __device__ __forceinline__ float below(float m) {
+    if constexpr (!F16) return m;
+    const float f = m - 15.f;
+    return m - f > 15.5f ? m : f;
+  }
   uint32_t qf[HD / 16][4];
   float acc[HD / 8][4];
   float m0, m1, l0, l1;
@@ -321,8 +326,7 @@ struct State {
   if (__any_sync(0xffffffffu, grew)) {
     const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
     // differences of the rounded references themselves
-    const float c0 = exp2f((m0 - SHIFT) - (ref_of(n0) - SHIFT));
-    const float c1 = exp2f((m1 - SHIFT) - (ref_of(n1) - SHIFT));
+    const float c0 = exp2f(below(m0) - below(ref_of(n0))), c1 = exp2f(below(m1) - below(ref_of(n1)));
     m0 = n0;
     m1 = n1;
     l0 *= c0;
@@ -335,7 +339,7 @@ struct State {
       acc[d][3] *= c1;
     }
   }
-  const float f0 = ref_of(m0) - SHIFT, f1 = ref_of(m1) - SHIFT;
+  const float f0 = below(ref_of(m0)), f1 = below(ref_of(m1));
   uint32_t hi[4], lw[4];
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {
@@ -379,7 +383,7 @@ struct State {
       for (int d = 0; d < HD / 8; ++d)
         *reinterpret_cast<float2*>(acc_buf + r * MERGE_PITCH + d * 8 + 2 * (lane & 3)) =
             make_float2(acc[d][2 * half], acc[d][2 * half + 1]);
-      if ((lane & 3) == 0) ml_buf[r] = half ? make_float2(m1 - SHIFT, l1) : make_float2(m0 - SHIFT, l0);
+      if ((lane & 3) == 0) ml_buf[r] = half ? make_float2(below(m1), l1) : make_float2(below(m0), l0);
     }
   }
 };
