@@ -419,7 +419,7 @@ struct Redo {
 };
 template <bool F16, bool PREFIX>
 __device__ __noinline__ float4 redo_columns(const Redo d, float4 A, int lane) {
-  constexpr int U = 4;                            // keys in flight
+  constexpr int U = 8;                            // keys in flight
   const float4 x = load_row4<F16>(d.q, lane);
   float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int t = d.t0; t < d.t1; t += U) {
@@ -438,11 +438,12 @@ __device__ __noinline__ float4 redo_columns(const Redo d, float4 A, int lane) {
       s[u] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, x.w * k.w)));
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = group_sum<32>(s[u]) * d.scale_log2;
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t + u >= d.t1) break;
-      const float w = exp2f(s[u] - d.ref);
+      const float w = t + u < d.t1 ? exp2f(__fmul_rn(s[u], d.scale_log2) - d.ref) : 0.f;
       R.x = fmaf(w, v[u].x, R.x);
       R.y = fmaf(w, v[u].y, R.y);
       R.z = fmaf(w, v[u].z, R.z);
