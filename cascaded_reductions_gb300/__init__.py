@@ -38,6 +38,7 @@ RF_FUSE_NONE, RF_FUSE_THREAD, RF_FUSE_WARP, RF_FUSE_BLOCK = range(4)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 
 _SIGNATURES = {
     "rf_status_string": (ctypes.c_char_p, [_I]),
@@ -76,6 +77,9 @@ _SIGNATURES = {
                                    _P, _P, _P, _P, _P, _I, _P, _P]),
     "rf_cache_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                             _P]),
+    "rf_page_tables": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "rf_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _I, _F, _P, _I, _P, _P,
+                             _I, _I, _I, _P, _I, _I, _P, _P, _P, _P]),
 }
 
 
@@ -627,6 +631,86 @@ def rf_cache_evict(k, v, weight, lens, keep, sinks, recent, k_out, v_out, weight
              lens_out.data_ptr(), kept.data_ptr())
 
 
+def rf_page_tables(lens, news, table, stack, n_free, page, starts, positions, slots, lens_out,
+                   n_free_out, stream=None):
+    """lens, news int32 [B], table int32 [B, width] and stack int32 [pages] (both updated), n_free
+    int32 [1] -> starts [B + 1], positions and slots [T], lens_out [B] (may be lens), n_free_out [1]
+    (may be n_free), all int32."""
+    dev = _device_of(lens, "lens")
+    if table.dim() != 2 or stack.dim() != 1 or slots.dim() != 1:
+        raise ValueError("table must be [B, width], stack [pages] and slots [T]")
+    B, width = table.shape
+    i32 = torch.int32
+    for name, t, shape in (("lens", lens, (B,)), ("news", news, (B,)), ("table", table, (B, width)),
+                           ("stack", stack, stack.shape), ("n_free", n_free, (1,)),
+                           ("starts", starts, (B + 1,)), ("positions", positions, slots.shape),
+                           ("slots", slots, slots.shape), ("lens_out", lens_out, (B,)),
+                           ("n_free_out", n_free_out, (1,))):
+        _on(dev, t, i32, shape, name)
+    _call_on(dev, stream, "rf_page_tables", _lib.rf_page_tables, lens.data_ptr(), news.data_ptr(),
+             _i32(B), table.data_ptr(), _i32(width), stack.data_ptr(), _i32(stack.shape[0]),
+             n_free.data_ptr(), *_c_ints(page, slots.shape[0]), starts.data_ptr(), positions.data_ptr(),
+             slots.data_ptr(), lens_out.data_ptr(), n_free_out.data_ptr())
+
+
+def _token_rows(dev, t, dtype, shape, name):
+    """``t`` [T, heads, D] with dense heads; returns the elements from a token's row to the next."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _on(dev, t.contiguous(), dtype, shape, name)
+    T, h, D = shape
+    if (D > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return t.stride(0) if T > 1 else h * D
+
+
+def rf_qk_norm_rope(q, k, v, q_weight, k_weight, eps, positions, freq, axis, interleaved, slots,
+                    q_out, k_out, v_out, stream=None):
+    """q [T, H, D], k/v [T, Hkv, D] (bf16 or fp16, tokens may lie apart), weights [D] or None,
+    positions int32 [axes, T], freq fp32 [R / 2], axis int32 [R / 2] or None -> q_out [T, H, D] and
+    k_out [T, Hkv, D] (slots, v and v_out None), or with slots int32 [T] the pages k_out, v_out
+    [pages, Hkv, page, D]."""
+    if q.dim() != 3 or k.dim() != 3 or positions.dim() != 2 or freq.dim() != 1:
+        raise ValueError("q and k must be [T, heads, D], positions [axes, T] and freq [R / 2]")
+    dev = _device_of(q, "q")
+    T, H, D = q.shape
+    Hkv, dt = k.shape[1], q.dtype
+    q_step = _token_rows(dev, q, dt, (T, H, D), "q")
+    k_step = _token_rows(dev, k, dt, (T, Hkv, D), "k")
+    v_step, pages, page = 0, 0, 0
+    _on(dev, positions, torch.int32, (positions.shape[0], T), "positions")
+    _on(dev, freq, torch.float32, freq.shape, "freq")
+    if axis is not None:
+        _on(dev, axis, torch.int32, freq.shape, "axis")
+    w_dtype = dt
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            w_dtype = w.dtype
+            if w.dtype not in (dt, torch.float32):
+                raise ValueError(f"{name} must be {dt} or torch.float32, got {w.dtype}")
+            _on(dev, w, w_dtype, (D,), name)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one type")
+    _on(dev, q_out, dt, (T, H, D), "q_out")
+    if (slots is None) != (v is None) or (v is None) != (v_out is None):
+        raise ValueError("slots, v and v_out come together")
+    if slots is None:
+        _on(dev, k_out, dt, (T, Hkv, D), "k_out")
+    else:
+        if k_out.dim() != 4:
+            raise ValueError("k_out must be pages [pages, Hkv, page, D]")
+        pages, _, page, _ = k_out.shape
+        v_step = _token_rows(dev, v, dt, (T, Hkv, D), "v")
+        _on(dev, slots, torch.int32, (T,), "slots")
+        _on(dev, k_out, dt, (pages, Hkv, page, D), "k_out")
+        _on(dev, v_out, dt, k_out.shape, "v_out")
+    _call_on(dev, stream, "rf_qk_norm_rope", _lib.rf_qk_norm_rope, q.data_ptr(), q_step, k.data_ptr(),
+             k_step, _addr(v), v_step, *_c_ints(T, H, Hkv, D), _addr(q_weight), _addr(k_weight),
+             _cache_dtype(w_dtype, "weights"), eps, positions.data_ptr(), _i32(positions.shape[0]),
+             freq.data_ptr(), _addr(axis), _i32(2 * freq.shape[0]), int(bool(interleaved)),
+             _cache_dtype(dt, "q"), _addr(slots), *_c_ints(pages, page), q_out.data_ptr(),
+             k_out.data_ptr(), _addr(v_out))
+
+
 def rf_stream_read(x, out_xor, stream=None):
     """XOR every 32-bit word of the CUDA tensor ``x`` into ``out_xor`` (one
     int32 element, device memory) with one streaming read of ``x``."""
@@ -939,3 +1023,44 @@ def cache_evict(k, v, weight, lens, keep, sinks=0, recent=0, cap_out=None, out=N
              *_c_ints(keep, sinks, recent, k_out.shape[2]), k_out.data_ptr(), _addr(v_out), weight_out.data_ptr(),
              lens_out.data_ptr(), kept.data_ptr())
     return k_out, v_out, weight_out, lens_out, kept
+
+
+def page_tables(lens, news, table, stack, n_free, page, tokens, lens_out=None, n_free_out=None,
+                stream=None):
+    """Pages for a step's new tokens, from a stack of free ones, and where each token goes.
+
+    lens, news int32 [B]: tokens held and new tokens of each request (new < 0: it has ended and gives
+    its pages back); table int32 [B, width] and stack int32 [pages] are updated in place; n_free int32
+    [1].  Returns starts [B + 1], positions [tokens], slots [tokens] (-1 where a token has no place),
+    lens_out [B] and n_free_out [1]; the last two may be given, as lens and n_free themselves for one."""
+    if stream is not None:
+        return _within(stream, lens, page_tables, lens, news, table, stack, n_free, page, tokens,
+                       lens_out, n_free_out)
+    new = dict(device=lens.device, dtype=torch.int32)
+    starts = torch.empty(lens.shape[0] + 1, **new)
+    positions, slots = torch.empty(tokens, **new), torch.empty(tokens, **new)
+    lens_out = torch.empty_like(lens) if lens_out is None else lens_out
+    n_free_out = torch.empty_like(n_free) if n_free_out is None else n_free_out
+    rf_page_tables(lens, news, table, stack, n_free, page, starts, positions, slots, lens_out, n_free_out)
+    return starts, positions, slots, lens_out, n_free_out
+
+
+def qk_norm_rope(q, k, positions, freq, q_weight=None, k_weight=None, axis=None, interleaved=False,
+                 eps=1e-6, v=None, slots=None, kp=None, vp=None, stream=None):
+    """RMS norm of each query and key head (where a weight is given) and rotation of its first
+    2 * len(freq) values by position * freq, on one or several axes.
+
+    q [T, H, D], k [T, Hkv, D] (bf16 or fp16; may be slices of one projection), positions int32
+    [axes, T], freq fp32 [R / 2], axis int32 [R / 2] (None: the first for all).  Returns q and k
+    rotated; with v [T, Hkv, D], slots int32 [T] and a cache kp, vp [pages, Hkv, page, D] the keys and
+    values go into the cache (not where a slot is negative) and only q comes back."""
+    if stream is not None:
+        return _within(stream, q, qk_norm_rope, q, k, positions, freq, q_weight, k_weight, axis,
+                       interleaved, eps, v, slots, kp, vp)
+    if (slots is None) != (kp is None):
+        raise ValueError("slots, kp and vp come together")
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if kp is None else kp
+    rf_qk_norm_rope(q, k, v, q_weight, k_weight, eps, positions, freq, axis, interleaved, slots, q_out,
+                    k_out, vp)
+    return (q_out, k_out) if kp is None else q_out

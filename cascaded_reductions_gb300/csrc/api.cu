@@ -452,6 +452,63 @@ rf_status rf_cache_evict(const void* k, const void* v, const float* weight, cons
                                 as_stream(stream));
 }
 
+rf_status rf_page_tables(const int32_t* lens, const int32_t* news, int B, int32_t* table, int width,
+                         int32_t* stack, int pages, const int32_t* n_free, int page, int T,
+                         int32_t* starts, int32_t* positions, int32_t* slots, int32_t* lens_out,
+                         int32_t* n_free_out, void* stream) {
+  if (!lens || !news || !table || !stack || !n_free || !starts || !positions || !slots || !lens_out ||
+      !n_free_out)
+    return RF_ERR_INVALID_ARG;
+  if (B <= 0 || width <= 0 || pages <= 0 || page <= 0 || T <= 0) return RF_ERR_INVALID_ARG;
+  if (B > rf::kMaxTableRequests || (long long)B * width > 0x7fffffffLL ||
+      (long long)pages * page > 0x7fffffffLL || (long long)width * page > 0x7fffffffLL)
+    return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(positions) || !rf::aligned16(slots)) return RF_ERR_MISALIGNED;
+  // lens_out may be lens and n_free_out n_free; nothing else may overlap
+  const struct { const void* p; size_t n; } buf[] = {
+      {lens, (size_t)B * 4}, {n_free, 4}, {news, (size_t)B * 4}, {table, (size_t)B * width * 4},
+      {stack, (size_t)pages * 4}, {starts, ((size_t)B + 1) * 4}, {positions, (size_t)T * 4},
+      {slots, (size_t)T * 4}, {lens_out, (size_t)B * 4}, {n_free_out, 4}};
+  for (int i = 3; i < 10; ++i)
+    for (int j = 0; j < i; ++j) {
+      if ((i == 8 && j == 0 && lens_out == lens) || (i == 9 && j == 1 && n_free_out == n_free)) continue;
+      if (overlap(buf[i].p, buf[i].n, buf[j].p, buf[j].n)) return RF_ERR_INVALID_ARG;
+    }
+  return rf::launch_page_tables(lens, news, B, table, width, stack, pages, n_free, page, T, starts,
+                                positions, slots, lens_out, n_free_out, as_stream(stream));
+}
+
+rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long long k_step,
+                          const void* v, long long v_step, int T, int H, int Hkv, int D,
+                          const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                          const int32_t* positions, int axes, const float* freq, const int32_t* axis,
+                          int R, int interleaved, int dtype, const int32_t* slots, int pages, int page,
+                          void* q_out, void* k_out, void* v_out, void* stream) {
+  if (!q || !k || !positions || !freq || !q_out || !k_out) return RF_ERR_INVALID_ARG;
+  if ((slots != nullptr) != (v != nullptr) || (v != nullptr) != (v_out != nullptr)) return RF_ERR_INVALID_ARG;
+  if (T <= 0 || H <= 0 || Hkv <= 0 || D <= 0 || axes <= 0 || R <= 0 || R > D) return RF_ERR_INVALID_ARG;
+  if (slots && (pages <= 0 || page <= 0)) return RF_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !isfinite(eps)) return RF_ERR_INVALID_ARG;
+  if (dtype != RF_F32 && dtype != RF_BF16 && dtype != RF_F16) return RF_ERR_INVALID_ARG;
+  if (weight_dtype != RF_F32 && weight_dtype != dtype) return RF_ERR_INVALID_ARG;
+  if (dtype == RF_F32 || (D != 64 && D != 128 && D != 256) || R % 16 != 0) return RF_ERR_UNSUPPORTED;
+  if ((long long)H * D > 0x7fffffffLL || (long long)Hkv * D > 0x7fffffffLL ||
+      (long long)H + 2ll * Hkv > 0x7fffffffLL || (long long)T * ((H + 2ll * Hkv + 7) / 8) > 0x7fffffffLL ||
+      (slots && (long long)pages * page > 0x7fffffffLL))
+    return RF_ERR_UNSUPPORTED;
+  if (q_step < (long long)H * D || k_step < (long long)Hkv * D || (v && v_step < (long long)Hkv * D))
+    return RF_ERR_INVALID_ARG;
+  if (q_step > (1ll << 40) || k_step > (1ll << 40) || (v && v_step > (1ll << 40))) return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(q) || !rf::aligned16(k) || !rf::aligned16(v) || !rf::aligned16(q_out) ||
+      !rf::aligned16(k_out) || !rf::aligned16(v_out) || q_step % 8 != 0 || k_step % 8 != 0 ||
+      (v && v_step % 8 != 0))
+    return RF_ERR_MISALIGNED;
+  return rf::launch_qk_norm_rope(q, q_step, k, k_step, v, v_step, T, H, Hkv, D, q_weight, k_weight,
+                                 weight_dtype == RF_F32, eps, positions, axes, freq, axis, R,
+                                 interleaved != 0, dtype, slots, pages, page, q_out, k_out, v_out,
+                                 as_stream(stream));
+}
+
 rf_status rf_device_error(int* status, void* stream) {
   if (!status) return RF_ERR_INVALID_ARG;
   return rf::read_device_error(status, as_stream(stream));

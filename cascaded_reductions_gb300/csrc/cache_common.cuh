@@ -159,4 +159,20 @@ rf_status launch_cache_evict(const void* k, const void* v, const float* weight,
                              float* weight_out, int32_t* lens_out, int32_t* kept,
                              cudaStream_t st);
 
+// The step of a loop over a paged cache.
+constexpr int kMaxTableRequests = 8192;    // of launch_page_tables
+rf_status launch_page_tables(const int32_t* lens, const int32_t* news, int B, int32_t* table, int width,
+                             int32_t* stack, int P, const int32_t* n_free, int page, int T,
+                             int32_t* starts, int32_t* positions, int32_t* slots, int32_t* lens_out,
+                             int32_t* n_free_out, cudaStream_t st);
+// steps: elements from a token's row to the next; slots null: k to k_out [T, Hkv, D] and no v,
+// else k and v to the pages k_out, v_out [P, Hkv, page, D].  w32: weights are fp32.
+rf_status launch_qk_norm_rope(const void* q, long long q_step, const void* k, long long k_step,
+                              const void* v, long long v_step, int T, int H, int Hkv, int D,
+                              const void* qw, const void* kw, bool w32, float eps,
+                              const int32_t* positions, int axes, const float* freq,
+                              const int32_t* axis, int R, bool interleaved, int dtype,
+                              const int32_t* slots, int P, int page, void* q_out, void* k_out,
+                              void* v_out, cudaStream_t st);
+
 }  // namespace rf

@@ -1,0 +1,247 @@
+// Pages for the new tokens of a ragged batch of requests, and where each token
+// goes: one launch per step of a serving loop, from lengths on the device.
+//
+// Mathematics: three prefix sums over the requests (new tokens, pages that ended
+// requests give back, pages that the others need).  Page x of those needed is the
+// x-th from the top of the stack of free pages, on which the pages given back lie
+// above the ones that were free before; a request gets its pages if those needed up
+// to it are there.  Token t belongs to the last request whose first token is at or
+// before t.
+//
+// What bounds it: latency.  A step moves kilobytes (256 requests, 25 prompt chunks:
+// 0.9 MB), and what it waits for are the launch, one read of the lengths, the sums and
+// one read of a page number.  So everything is one cluster: each of its CTAs makes the
+// prefix sums for itself in shared memory, and then pages and tokens are dealt out to
+// all threads, each of which finds its request by bisection.  Nothing that one thread
+// writes is read by another (a page just given back is read from the ended request's
+// table row), but for what the call may overwrite in place: the lengths and the number of
+// free pages, which are written after a barrier of the cluster behind every read.
+
+#include "cache_common.cuh"
+#include "tc_common.cuh"
+
+namespace rf {
+namespace {
+
+struct Tables {
+  const int32_t *lens, *news;
+  int32_t *table, *stack;
+  const int32_t* n_free;
+  int32_t *starts, *positions, *slots, *lens_out, *n_free_out;
+  int B, width, P, page, T;
+};
+
+constexpr int WARPS_MAX = 32;
+
+// inclusive prefix sums over the CTA of two values per thread, with their totals
+struct Sums {
+  long long a[WARPS_MAX + 1], b[WARPS_MAX + 1];
+};
+__device__ __forceinline__ long long scan_warp(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// last i of n ascending values with v[i] <= x (v[0] = 0 <= x)
+__device__ __forceinline__ int find(const int* v, int n, int x) {
+  int lo = 0;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (v[lo + half] <= x) lo += half;
+    n -= half;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
+  extern __shared__ int smem[];              // 16 bytes per request
+  __shared__ Sums sums;
+  __shared__ int took_all;
+  const int B = a.B, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  int* start = smem;                         // first new token, per request
+  int* need0 = smem + B;                     // pages needed before it
+  int* give0 = smem + 2 * B;                 // pages given back before it
+  int* len0 = smem + 3 * B;                  // its length, or -1 - length where it gets nothing
+  wait_prerequisite();
+  allow_dependents();
+  if (tid == 0) took_all = 0;
+  const int nfree = min(max(a.n_free[0], 0), a.P);
+  const int held_most = a.width;
+
+  long long tokens = 0, moved = 0;           // of the requests so far; moved: given << 32 | needed
+  for (int b0 = 0; b0 < B; b0 += (int)blockDim.x) {
+    const int b = b0 + tid;
+    int len = 0, now = 0;
+    if (b < B && RF_IDX_OK(b, a.B)) {
+      len = max(a.lens[b], 0);
+      now = a.news[b];
+    }
+    const int held = min((int)(((long long)len + a.page - 1) / a.page), held_most);
+    const long long total = ((long long)len + max(now, 0) + a.page - 1) / a.page;
+    const bool fits = total <= a.width && now >= 0;
+    const long long give = now < 0 ? held : 0, need = fits ? total - held : 0;
+    const long long x = max(now, 0), y = give << 32 | need;
+    const long long sx = scan_warp(x, lane), sy = scan_warp(y, lane);
+    if (lane == 31) {
+      sums.a[warp] = sx;
+      sums.b[warp] = sy;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const long long p = scan_warp(lane < warps ? sums.a[lane] : 0, lane);
+      const long long q = scan_warp(lane < warps ? sums.b[lane] : 0, lane);
+      __syncwarp();
+      sums.a[lane + 1] = p;                  // [w + 1]: of warps 0 .. w
+      sums.b[lane + 1] = q;
+      if (lane == 0) sums.a[0] = sums.b[0] = 0;
+    }
+    __syncthreads();
+    const long long ix = tokens + sums.a[warp] + sx - x, iy = moved + sums.b[warp] + sy - y;
+    if (b < B) {
+      start[b] = (int)min(ix, 0x7fffffffll);
+      need0[b] = (int)(iy & 0xffffffffll);
+      give0[b] = (int)(iy >> 32);
+      // the pool's top is known after the last chunk: see below
+      len0[b] = fits ? len : -1 - len;
+    }
+    tokens += sums.a[warps];
+    moved += sums.b[warps];
+    __syncthreads();
+  }
+  const int given = (int)(moved >> 32), needed = (int)(moved & 0xffffffffll);
+  const int top = min(nfree + given, a.P);
+  // requests whose pages are not all there get nothing; of those that get theirs the
+  // last one's pages end the ones taken
+  for (int b = tid; b < B; b += (int)blockDim.x) {
+    const int upto = b + 1 < B ? need0[b + 1] : needed;
+    if (upto > need0[b]) {
+      if (upto > top)
+        len0[b] = -1 - len0[b];
+      else
+        atomicMax(&took_all, upto);
+    }
+  }
+  const uint32_t ctas = gridDim.x;           // one cluster
+  if (ctas > 1)
+    tc::cluster_sync();                      // every CTA has read what may be overwritten
+  else
+    __syncthreads();
+  const int took = took_all;
+  const int first = (int)blockIdx.x * (int)blockDim.x + tid, step = (int)(ctas * blockDim.x);
+  const size_t entries = (size_t)B * a.width;
+  (void)entries;                             // read by the checked build only
+
+  auto given_page = [&](int y) -> int {      // the y-th page given back
+    const int b = find(give0, B, y);
+    const size_t at = (size_t)b * a.width + (y - give0[b]);
+    return RF_IDX_OK(at, entries) ? a.table[at] : -1;
+  };
+  auto page_of = [&](int x) -> int {         // the x-th page taken
+    const int i = top - 1 - x;
+    if (i >= nfree) return given_page(i - nfree);
+    return RF_IDX_OK(i, a.P) ? a.stack[i] : -1;
+  };
+  auto held_of = [&](int len) { return min((int)(((long long)len + a.page - 1) / a.page), held_most); };
+
+  for (int b = first; b < B; b += step) {
+    const int len = len0[b] < 0 ? -1 - len0[b] : len0[b];
+    const int end = b + 1 < B ? start[b + 1] : (int)min(tokens, 0x7fffffffll);
+    // an ended request gives pages where it has some; it has none of the tokens either way
+    const int gave = (b + 1 < B ? give0[b + 1] : given) - give0[b];
+    int out = len0[b] < 0 ? len : len + (end - start[b]);
+    if (gave > 0) out = 0;
+    if (RF_IDX_OK(b, a.B)) a.lens_out[b] = out;
+    if (RF_IDX_OK(b + 1, a.B + 1)) a.starts[b + 1] = end;
+    if (b == 0) {
+      a.starts[0] = 0;
+      a.n_free_out[0] = top - took;
+    }
+  }
+  for (int y = first; y < given && nfree + y < a.P; y += step)
+    if (RF_IDX_OK(nfree + y, a.P)) a.stack[nfree + y] = given_page(y);
+  for (int x = first; x < took; x += step) {
+    const int b = find(need0, B, x);
+    const size_t at = (size_t)b * a.width + held_of(len0[b]) + (x - need0[b]);
+    if (RF_IDX_OK(at, entries)) a.table[at] = page_of(x);
+  }
+  // four tokens per thread, in 16-byte stores
+  for (int t0 = 4 * first; t0 < a.T; t0 += 4 * step) {
+    int pos[4], slot[4];
+    int b = t0 < tokens ? find(start, B, t0) : 0;
+    int seen = -1, entry = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = t0 + e;
+      pos[e] = 0;
+      slot[e] = -1;
+      if (t >= tokens || t >= a.T) continue;
+      while (b + 1 < B && start[b + 1] <= t) {
+        ++b;
+        seen = -1;
+      }
+      const int len = len0[b];
+      pos[e] = (len < 0 ? -1 - len : len) + (t - start[b]);
+      if (len < 0) continue;
+      const int i = pos[e] / a.page;
+      if (i != seen) {
+        const int held = held_of(len);
+        const size_t at = (size_t)b * a.width + i;
+        seen = i;
+        entry = i >= held ? page_of(need0[b] + i - held) : RF_IDX_OK(at, entries) ? a.table[at] : -1;
+      }
+      slot[e] = entry * a.page + (pos[e] - i * a.page);
+    }
+    if (t0 + 4 <= a.T) {
+      if (!RF_SPAN_OK(t0, 4, a.T)) continue;
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (t0 + e >= a.T || !RF_IDX_OK(t0 + e, a.T)) continue;
+        a.positions[t0 + e] = pos[e];
+        a.slots[t0 + e] = slot[e];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+rf_status launch_page_tables(const int32_t* lens, const int32_t* news, int B, int32_t* table, int width,
+                             int32_t* stack, int P, const int32_t* n_free, int page, int T,
+                             int32_t* starts, int32_t* positions, int32_t* slots, int32_t* lens_out,
+                             int32_t* n_free_out, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const size_t smem = (size_t)B * 16;
+  if (smem_attr(page_tables_kernel, (size_t)kMaxTableRequests * 16, done) != RF_OK) return RF_ERR_CUDA;
+  Tables a = {lens, news, table, stack, n_free, starts, positions, slots, lens_out, n_free_out,
+              B, width, P, page, T};
+  const bool small = B <= 256 && T <= 1024;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = small ? 1 : 8;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(small ? 1 : 8);
+  cfg.blockDim = dim3(small ? 256 : 1024);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, page_tables_kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return RF_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+RF_BOUNDS_WORD_OF_THIS_FILE
+
+}  // namespace rf

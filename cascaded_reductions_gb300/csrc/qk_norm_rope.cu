@@ -1,0 +1,264 @@
+// Norm of each query and key head, rotation by position, and the write of keys and
+// values into a paged cache, from one read of a projection's rows.
+//
+// Mathematics, per head of D values:
+//   y = x w / sqrt(mean x^2 + eps);  a pair (y_a, y_b) of the first R values turns by
+//   t = pos f:  (y_a cos t - y_b sin t,  y_b cos t + y_a sin t);
+// pairs are (i, i + R/2), or (2i, 2i + 1) interleaved, and pos is the token's position
+// on the pair's axis (one for text; time, height and width for pictures).  All in
+// fp32, rounded once.
+//
+// The angle: an fp32 product pos f is off by up to pos 2^-24, 0.06 rad at a million.
+// A turn is taken as a 64-bit integer instead: f / 2 pi mod 1 in units of 2^-64 (from a
+// product in fp64), times the position, is the angle mod a whole turn exactly as the
+// integer wraps; its top 32 bits go through sincospi.  What is left of the error is
+// pos 2^-55 turns from f / 2 pi and half a step of fp32.
+//
+// What bounds it: HBM (a head is read once and written once).  Angles cost some 40
+// instructions a pair, so a CTA makes those of its tokens once, in shared memory, for
+// all heads.  A head takes D / 16 lanes, each with two 16-byte chunks that hold both
+// halves of its pairs, so that only the sum of squares crosses lanes.
+
+#include <cuda_fp16.h>
+
+#include "cache_common.cuh"
+#include "tc_common.cuh"
+
+namespace rf {
+namespace {
+
+constexpr int WARPS = 8;
+constexpr int MAX_PAIRS = 128;
+
+struct NormRope {
+  const uint16_t *q, *k, *v;
+  long long q_step, k_step, v_step;     // elements from a token's row to the next
+  const void *qw, *kw;                  // [D] or null
+  const int32_t* positions;             // [axes, T]
+  const float* freq;                    // [R / 2]
+  const int32_t* axis;                  // [R / 2] or null
+  const int32_t* slots;                 // [T] or null: k and v go to k_out, v is not taken
+  uint16_t *q_out, *k_out, *v_out;      // k_out, v_out: the pages where slots is given
+  long long n_slots;
+  float eps;
+  int T, H, Hkv, R, axes, page;
+  bool w32;                             // weights are fp32
+  int heads, tokens, slices;            // per token with v; of a CTA; CTAs that share a token
+};
+
+template <bool F16>
+__device__ __forceinline__ float2 widen(uint32_t w) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <bool F16>
+__device__ __forceinline__ void widen8(const uint4& u, float* f) {
+  const float2 a = widen<F16>(u.x), b = widen<F16>(u.y), c = widen<F16>(u.z), d = widen<F16>(u.w);
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
+}
+template <bool F16>
+__device__ __forceinline__ uint4 round8(const float* f) {
+  if constexpr (F16)
+    return make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                      pack_f16x2(f[6], f[7]));
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+template <bool F16>
+__device__ __forceinline__ float weight_of(const void* w, int i, bool w32) {
+  if (w32) return static_cast<const float*>(w)[i];
+  const uint32_t u = static_cast<const uint16_t*>(w)[i];
+  return widen<F16>(u).x;
+}
+
+__device__ __forceinline__ uint4 ld16(const uint16_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// One CTA: `tokens` adjacent tokens, or one slice of the heads of a single token.  Its
+// warps take groups of 32 / (D / 16) heads of a token at a time.
+template <bool F16, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(WARPS * 32)
+norm_rope_kernel(const NormRope a) {
+  constexpr int LANES = D / 16;                 // of a head
+  constexpr int HEADS = 32 / LANES;             // of a warp
+  extern __shared__ __align__(16) float smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int half = a.R / 2;
+  float* w_s = smem;                            // [2][D]: weights of q and k
+  float2* turn = reinterpret_cast<float2*>(smem + 2 * D);   // [tokens][R / 2]: cos, sin
+  const int t0 = (int)(blockIdx.x / a.slices) * a.tokens, slice = (int)(blockIdx.x % a.slices);
+  const int nt = min(a.tokens, a.T - t0);
+  const int groups = (a.heads + HEADS - 1) / HEADS;
+  const int items = nt * groups;
+  wait_prerequisite();
+  allow_dependents();
+
+  // a lane's part of one head
+  const int hl = lane / LANES, j = lane % LANES;
+  // its chunks of 8 values: both halves of its pairs, or what lies behind R
+  const int rc = a.R / 16;
+  const int c0 = INTERLEAVED ? 2 * j : j < rc ? j : 2 * rc + 2 * (j - rc);
+  const int c1 = INTERLEAVED ? 2 * j + 1 : j < rc ? j + rc : c0 + 1;
+  struct Item {
+    int t, h;                                   // token of the CTA, head (q, then k, then v)
+    uint4 x0, x1;
+  };
+  auto load = [&](int i, Item& it) {
+    it.t = i / groups;
+    it.h = (i - it.t * groups) * HEADS + hl;
+    it.x0 = it.x1 = make_uint4(0, 0, 0, 0);
+    if (i >= items || it.h >= a.heads) return;
+    const size_t t = t0 + it.t;
+    const bool is_q = it.h < a.H, is_k = !is_q && it.h < a.H + a.Hkv;
+    const int h = is_q ? it.h : is_k ? it.h - a.H : it.h - a.H - a.Hkv;
+    const uint16_t* row = is_q ? a.q + t * a.q_step : is_k ? a.k + t * a.k_step : a.v + t * a.v_step;
+    if (!RF_IDX_OK(t, a.T) || !RF_IDX_OK(h, is_q ? a.H : a.Hkv)) return;
+    it.x0 = ld16(row + (size_t)h * D + c0 * 8);
+    it.x1 = ld16(row + (size_t)h * D + c1 * 8);
+  };
+  const int stride = WARPS * a.slices;
+  int i = slice * WARPS + warp;
+  Item it;
+  load(i, it);                                  // under way while the angles are made
+
+  for (int e = tid; e < 2 * D; e += WARPS * 32) {
+    const void* w = e < D ? a.qw : a.kw;
+    w_s[e] = w ? weight_of<F16>(w, e < D ? e : e - D, a.w32) : 1.f;
+  }
+  for (int e = tid; e < nt * half; e += WARPS * 32) {
+    const int t = e / half, pair = e - t * half;
+    int ax = a.axis && RF_IDX_OK(pair, half) ? a.axis[pair] : 0;
+    ax = min(max(ax, 0), a.axes - 1);
+    const size_t at = (size_t)ax * a.T + t0 + t;
+    const long long pos = RF_IDX_OK(at, (size_t)a.axes * a.T) ? a.positions[at] : 0;
+    double f = (double)a.freq[pair] * 0.15915494309189533577;       // 1 / (2 pi)
+    f -= floor(f);
+    const unsigned long long unit = __double2ull_rn(f * 18446744073709551616.0);
+    const unsigned long long frac = unit * (unsigned long long)pos + 0x80000000ull;
+    float s, c;
+    // the top 32 bits as half turns in [-1, 1)
+    sincospif((float)(int)(unsigned)(frac >> 32) * 4.656612873077393e-10f, &s, &c);
+    turn[t * half + pair] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  for (; i < items; i += stride) {
+    Item next;
+    load(i + stride, next);
+    const bool is_q = it.h < a.H, is_k = !is_q && it.h < a.H + a.Hkv;
+    const bool in = it.h < a.heads;
+    const size_t t = t0 + it.t;
+    float x[16];
+    widen8<F16>(it.x0, x);
+    widen8<F16>(it.x1, x + 8);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (in && (is_q || is_k)) {
+      if (is_q ? a.qw != nullptr : a.kw != nullptr) {
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const float* w = w_s + (is_q ? 0 : D);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= r * w[(e < 8 ? c0 * 8 : c1 * 8 - 8) + e];
+      }
+      if (j < rc) {
+        const float2* cs = turn + it.t * half + 8 * j;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const float2 z = cs[p];
+          const int ia = INTERLEAVED ? 2 * p : p, ib = INTERLEAVED ? 2 * p + 1 : p + 8;
+          const float xa = x[ia], xb = x[ib];
+          x[ia] = fmaf(xa, z.x, -xb * z.y);
+          x[ib] = fmaf(xb, z.x, xa * z.y);
+        }
+      }
+      it.x0 = round8<F16>(x);
+      it.x1 = round8<F16>(x + 8);
+    }
+    if (in) {
+      uint16_t* dst = nullptr;
+      if (is_q) {
+        dst = a.q_out + (t * a.H + it.h) * D;
+      } else {
+        const int h = is_k ? it.h - a.H : it.h - a.H - a.Hkv;
+        if (a.slots == nullptr) {
+          dst = a.k_out + (t * a.Hkv + h) * D;
+        } else {
+          const int slot = RF_IDX_OK(t, a.T) ? a.slots[t] : -1;
+          if (slot >= 0 && slot < a.n_slots) {
+            const int p = slot / a.page;
+            dst = (is_k ? a.k_out : a.v_out) + (((size_t)p * a.Hkv + h) * a.page + (slot - p * a.page)) * D;
+          }
+        }
+      }
+      if (dst) {
+        *reinterpret_cast<uint4*>(dst + c0 * 8) = it.x0;
+        *reinterpret_cast<uint4*>(dst + c1 * 8) = it.x1;
+      }
+    }
+    it = next;
+  }
+}
+
+template <bool F16, int D>
+rf_status launch_d(NormRope a, bool interleaved, cudaStream_t st) {
+  const int sms = tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  const int heads_per_item = 32 / (D / 16);
+  const long long groups = (a.heads + heads_per_item - 1) / heads_per_item;
+  // A CTA's tokens: enough items to hide its angles behind, while every SM has its share of
+  // CTAs; where the tokens alone do not fill the device, several CTAs share one.
+  a.tokens = 1, a.slices = 1;
+  while (a.tokens < 8 && (long long)a.tokens * groups < 4 * WARPS && (long long)a.T / (2 * a.tokens) >= 8ll * sms)
+    a.tokens *= 2;
+  if (a.tokens == 1 && a.T < 4 * sms) {
+    const long long most = (groups + WARPS - 1) / WARPS, want = 4ll * sms / a.T;
+    a.slices = (int)(most < want ? most : want < 1 ? 1 : want);
+  }
+  const size_t smem = 2 * D * sizeof(float) + (size_t)a.tokens * (a.R / 2) * sizeof(float2);
+  const long long grid = ((long long)a.T + a.tokens - 1) / a.tokens * a.slices;
+  auto* kernel = interleaved ? norm_rope_kernel<F16, D, true> : norm_rope_kernel<F16, D, false>;
+  return launch_after(kernel, (unsigned)grid, WARPS * 32, smem, st, a);
+}
+
+}  // namespace
+
+rf_status launch_qk_norm_rope(const void* q, long long q_step, const void* k, long long k_step,
+                              const void* v, long long v_step, int T, int H, int Hkv, int D,
+                              const void* qw, const void* kw, bool w32, float eps,
+                              const int32_t* positions, int axes, const float* freq,
+                              const int32_t* axis, int R, bool interleaved, int dtype,
+                              const int32_t* slots, int P, int page, void* q_out, void* k_out,
+                              void* v_out, cudaStream_t st) {
+  NormRope a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_step = q_step, a.k_step = k_step, a.v_step = v_step;
+  a.qw = qw, a.kw = kw, a.w32 = w32, a.eps = eps;
+  a.positions = positions, a.axes = axes, a.freq = freq, a.axis = axis;
+  a.slots = slots, a.page = page, a.n_slots = (long long)P * page;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  a.T = T, a.H = H, a.Hkv = Hkv, a.R = R;
+  a.heads = H + (slots ? 2 : 1) * Hkv;
+  if (dtype == RF_F16)
+    return D == 64    ? launch_d<true, 64>(a, interleaved, st)
+           : D == 128 ? launch_d<true, 128>(a, interleaved, st)
+                      : launch_d<true, 256>(a, interleaved, st);
+  return D == 64    ? launch_d<false, 64>(a, interleaved, st)
+         : D == 128 ? launch_d<false, 128>(a, interleaved, st)
+                    : launch_d<false, 256>(a, interleaved, st);
+}
+
+RF_BOUNDS_WORD_OF_THIS_FILE
+
+}  // namespace rf

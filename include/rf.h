@@ -472,6 +472,77 @@ rf_status rf_cache_evict(const void* k, const void* v, const float* weight, cons
                          int recent, int cap_out, void* k_out, void* v_out, float* weight_out,
                          int32_t* lens_out, int32_t* kept, void* stream);
 
+/*
+ * A step over a paged cache
+ * -------------------------
+ * A server's requests come and go, and prompts arrive in chunks beside single
+ * tokens.  Their keys and values lie in pages of `page` rows that any request may
+ * hold, kp and vp [pages, Hkv, page, D]; table [B, width] (int32) lists each request's
+ * pages in order, entries behind the last one in use may hold anything.  The new
+ * tokens of all requests are packed one after the other: those of request b are
+ * rows starts[b] .. starts[b + 1] - 1.  All lengths, tables and slots are int32 in
+ * DEVICE memory.  The calls, in the order of a step: rf_page_tables, rf_paged_plan,
+ * then per layer rf_qk_norm_rope and rf_attn_paged.
+ */
+
+/*
+ * rf_page_tables -- pages for a step's new tokens, and where each token goes.
+ *   lens       [B]         tokens that each request holds (negative: taken as 0)
+ *   news       [B]         its new tokens (0 allowed); negative: it has ended, its
+ *                          pages go back and its length becomes 0
+ *   table      [B, width]  in/out: entries of new pages are filled in
+ *   stack      [pages]     in/out: the first n_free entries are free pages.  Pages given
+ *                          back are put on top, in order; then pages are taken from the
+ *                          top, request by request (so they may be ones just given back)
+ *   n_free     [1]
+ *   starts     [B + 1] out   sums of the new tokens before each request, and their total
+ *   positions  [T] out     position of each new token in its request; 0 past the total
+ *   slots      [T] out     page * `page` + row in the page, -1 past the total
+ *   lens_out   [B] out     the new lengths; may be lens itself
+ *   n_free_out [1] out     may be n_free itself
+ * Where the stack runs out, the first request whose new pages are not all there and
+ * all behind it that need pages get none, and so does a request that would need more
+ * than `width`: their tokens keep their rows with slot -1, their length and table stay.
+ * No other buffers overlap.  One launch.
+ * Errors: RF_ERR_INVALID_ARG for null pointers, sizes <= 0 or overlapping buffers;
+ * RF_ERR_UNSUPPORTED for B > 8192, or B * width, pages * page or width * page beyond
+ * 2^31 - 1; RF_ERR_MISALIGNED unless positions and slots are 16-byte aligned.
+ */
+rf_status rf_page_tables(const int32_t* lens, const int32_t* news, int B, int32_t* table, int width,
+                         int32_t* stack, int pages, const int32_t* n_free, int page, int T,
+                         int32_t* starts, int32_t* positions, int32_t* slots, int32_t* lens_out,
+                         int32_t* n_free_out, void* stream);
+
+/*
+ * rf_qk_norm_rope -- norm of each query and key head, rotation by position, and the
+ * write of keys and values into the cache, in one pass over a projection's rows.
+ * Per head x [D]:  y = x * weight / sqrt(mean(x^2) + eps)  (y = x without a weight);
+ * the pairs (i, i + R/2) of its first R values, or (2i, 2i + 1) if interleaved, turn by
+ * angle position * freq[i]:  (a, b) -> (a cos - b sin, b cos + a sin).  fp32, rounded
+ * once; the angle is exact to fp32 at any int32 position.
+ *   q [T, H, D], k, v [T, Hkv, D] of dtype RF_BF16 or RF_F16: heads dense, tokens
+ *               q_step, k_step, v_step elements apart (slices of one projection)
+ *   q_weight, k_weight [D] of weight_dtype (RF_F32 or dtype), each may be NULL
+ *   positions   [axes, T]; axis [R / 2] names the axis of each pair (NULL: the first;
+ *               numbers outside are taken as the nearer one)
+ *   freq        [R / 2] fp32, finite, radians per position
+ *   q_out       [T, H, D] out; may be q itself where q_step = H * D
+ *   slots NULL: k_out [T, Hkv, D] out (or k itself), v and v_out NULL
+ *   slots [T]:  k_out, v_out [pages, Hkv, page, D], the cache; a token with a slot
+ *               outside 0 .. pages * page - 1 is not written.  No slot may occur twice.
+ * Errors: RF_ERR_INVALID_ARG for null pointers (but those named), v or v_out without
+ * slots or the reverse, sizes <= 0, R > D, a bad dtype, a negative or non-finite eps, or
+ * steps shorter than a row; RF_ERR_UNSUPPORTED for RF_F32, D not 64, 128 or 256, R % 16
+ * != 0, or sizes beyond 2^31 (T * (H + 2 Hkv) / 8, pages * page); RF_ERR_MISALIGNED unless
+ * q, k, v and outputs are 16-byte aligned and steps multiples of 8.
+ */
+rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long long k_step,
+                          const void* v, long long v_step, int T, int H, int Hkv, int D,
+                          const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                          const int32_t* positions, int axes, const float* freq, const int32_t* axis,
+                          int R, int interleaved, int dtype, const int32_t* slots, int pages, int page,
+                          void* q_out, void* k_out, void* v_out, void* stream);
+
 /* Phase 1 of rf_absmax_quant_fp8_gemm alone (same arguments and rules;
  * any K % 8 == 0 is supported). */
 rf_status rf_absmax_quant_e4m3(const void* x, int M, int K, uint8_t* xq, float* sx,

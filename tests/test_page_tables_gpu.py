@@ -1,0 +1,107 @@
+"""Page tables against the definition, request by request: every output is a whole number and equal."""
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import cascaded_reductions_gb300 as rf
+from oracle import paged
+from paged_helpers import i32, tables
+
+pytestmark = pytest.mark.gpu
+
+
+def check(lens, news, page, width, free, tokens=None, seed=0, in_place=False):
+    B = len(lens)
+    held = [min(paged.pages(max(0, n), page), width) for n in lens]
+    table, stack, P = tables(B, page, held, width, free, seed)
+    total = sum(max(0, n) for n in news)
+    tokens = max(1, total) if tokens is None else tokens
+    ref = paged.page_tables(lens, news, table, stack, free, page, tokens)
+    dev = dict(lens=i32(lens), news=i32(news), table=i32(table), stack=i32(stack), n_free=i32([free]))
+    out = dict(lens_out=dev["lens"], n_free_out=dev["n_free"]) if in_place else {}
+    starts, positions, slots, lens_out, n_free_out = rf.page_tables(
+        dev["lens"], dev["news"], dev["table"], dev["stack"], dev["n_free"], page, tokens, **out)
+    got = (starts, positions, slots, lens_out, n_free_out[0], dev["table"], dev["stack"])
+    names = ("starts", "positions", "slots", "lens", "n_free", "table", "stack")
+    for name, g, r in zip(names, got, ref):
+        assert np.array_equal(g.cpu().numpy(), r), name
+    if not in_place:
+        assert dev["lens"].tolist() == list(lens) and dev["n_free"].tolist() == [free]
+    return got
+
+
+@pytest.mark.parametrize("page", [1, 16, 24, 256])
+@pytest.mark.parametrize("B", [1, 2, 31, 33, 300, 1025])
+def test_mixed_batches(B, page):
+    rng = random.Random(B * 1000 + page)
+    lens = [rng.choice([0, 1, page - 1, page, page + 1, rng.randint(0, 900)]) for _ in range(B)]
+    news = [rng.choice([-1, 0, 1, 1, 1, 2, page, rng.randint(1, 40)]) for _ in range(B)]
+    width = paged.pages(1000, page) + 1
+    need = sum(paged.pages(n + k, page) - paged.pages(n, page) for n, k in zip(lens, news) if k > 0)
+    for free in {need, need + 3, need // 2, 0}:
+        check(lens, news, page, width, free, seed=B)
+
+
+def test_first_that_does_not_fit_stops_those_behind_it():
+    # pages needed: 1, 3, 0 (inside its last page), 1; two are free
+    got = check([16, 16, 17, 32], [1, 40, 3, 1], 16, 8, 2)
+    assert got[3].tolist() == [17, 16, 20, 32] and got[4].item() == 1
+    assert (got[2].cpu() >= 0).tolist() == [True] + [False] * 40 + [True] * 3 + [False]
+
+
+def test_pages_given_back_are_taken_in_the_same_step():
+    got = check([48, 16, 5], [-1, 33, -1], 16, 4, 0)
+    assert got[4].item() == 1 and got[3].tolist() == [0, 49, 0]
+
+
+def test_more_than_the_table_holds():
+    got = check([64, 60, 0], [1, 4, 65], 16, 4, 50)
+    assert got[3].tolist() == [64, 64, 0]
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 1030, 5000])
+def test_rows_past_the_total_and_tokens_past_the_rows(tokens):
+    check([3, 900, 17], [2, 1023, 0], 16, 200, 100, tokens=tokens)
+
+
+def test_long_prompts_in_place():
+    lens, news = [0, 5000, 31, 0], [40000, 25001, 8192, 3]
+    check(lens, news, 64, 700, 1300, in_place=True)
+
+
+def test_negative_lengths_and_counts():
+    check([-5, 7, 0], [3, -9, -1], 16, 3, 4)
+
+
+def test_large_batch_and_refusal():
+    rng = random.Random(3)
+    check([rng.randint(0, 60) for _ in range(8192)], [rng.choice([-1, 0, 1, 5]) for _ in range(8192)],
+          16, 5, 6000)
+    z = i32(np.zeros(8193))
+    with pytest.raises(rf.RFError):
+        rf.page_tables(z, z, z.view(-1, 1), i32(np.zeros(4)), i32([4]), 16, 8)
+
+
+def test_captured_steps_in_place():
+    """One token per step, replayed: lengths and the stack go on from replay to replay."""
+    B, page, width = 5, 16, 20
+    lens, free = [0, 15, 16, 31, 7], 40
+    table, stack, _ = tables(B, page, [paged.pages(n, page) for n in lens], width, free, 1)
+    d = [i32(lens), i32([1] * B), i32(table), i32(stack), i32([free])]
+    step = lambda: rf.page_tables(*d, page, B, lens_out=d[0], n_free_out=d[4])      # noqa: E731
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = step()
+    for _ in range(40):
+        ref = paged.page_tables(lens, [1] * B, table, stack, free, page, B)
+        g.replay()
+        torch.cuda.synchronize()
+        lens, free, table, stack = ref[3], ref[4], ref[5], ref[6]
+        assert out[2].tolist() == ref[2].tolist()
+        assert d[0].tolist() == list(lens) and d[4].item() == free
+        assert np.array_equal(d[2].cpu().numpy(), table)
