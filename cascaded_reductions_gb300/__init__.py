@@ -78,6 +78,10 @@ _SIGNATURES = {
     "rf_cache_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                             _P]),
     "rf_page_tables": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "rf_paged_plan_bytes": (ctypes.c_size_t, [_I] * 8),
+    "rf_paged_plan": (_I, [_P, _P] + [_I] * 8 + [_P, ctypes.c_size_t, _P]),
+    "rf_attn_paged": (_I, [_P, _P, _P, _I, _I, _P, _I, _P, ctypes.c_size_t] + [_I] * 9
+                      + [_F, _I, _P, _P, _P]),
     "rf_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _I, _F, _P, _I, _P, _P,
                              _I, _I, _I, _P, _I, _I, _P, _P, _P, _P]),
 }
@@ -711,6 +715,48 @@ def rf_qk_norm_rope(q, k, v, q_weight, k_weight, eps, positions, freq, axis, int
              k_out.data_ptr(), _addr(v_out))
 
 
+def rf_paged_plan_bytes(B, T, H, Hkv, max_new, max_len, window=0, sinks=0):
+    """Bytes of a plan of these sizes on the current device (0: not valid, or no device)."""
+    return _lib.rf_paged_plan_bytes(*_c_ints(B, T, H, Hkv, max_new, max_len, window, sinks))
+
+
+def rf_paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window, sinks, plan, stream=None):
+    """starts int32 [B + 1], lens int32 [B] -> plan, a uint8 tensor of rf_paged_plan_bytes."""
+    dev = _device_of(lens, "lens")
+    if lens.dim() != 1 or plan.dim() != 1:
+        raise ValueError("lens must be [B] and plan [bytes]")
+    B = lens.shape[0]
+    _on(dev, lens, torch.int32, (B,), "lens")
+    _on(dev, starts, torch.int32, (B + 1,), "starts")
+    _on(dev, plan, torch.uint8, plan.shape, "plan")
+    _call_on(dev, stream, "rf_paged_plan", _lib.rf_paged_plan, starts.data_ptr(), lens.data_ptr(),
+             *_c_ints(B, T, H, Hkv, max_new, max_len, window, sinks), plan.data_ptr(), plan.shape[0])
+
+
+def rf_attn_paged(q, kp, vp, table, plan, max_new, max_len, window, sinks, scale, out, lse=None,
+                  stream=None):
+    """q/out [T, H, D], kp/vp [pages, Hkv, page, D] (bf16 or fp16, D = 128), table int32 [B, width],
+    plan from rf_paged_plan of the same sizes; lse [T, H] fp32 (optional)."""
+    if q.dim() != 3 or kp.dim() != 4 or table.dim() != 2:
+        raise ValueError("q must be [T, H, D], kp [pages, Hkv, page, D] and table [B, width]")
+    dev = _device_of(q, "q")
+    T, H, D = q.shape
+    pages, Hkv, page, _ = kp.shape
+    B, width = table.shape
+    _on(dev, q, q.dtype, q.shape, "q")
+    _on(dev, kp, q.dtype, (pages, Hkv, page, D), "kp")
+    _on(dev, vp, q.dtype, kp.shape, "vp")
+    _on(dev, table, torch.int32, table.shape, "table")
+    _on(dev, plan, torch.uint8, plan.shape, "plan")
+    _on(dev, out, q.dtype, q.shape, "out")
+    if lse is not None:
+        _on(dev, lse, torch.float32, (T, H), "lse")
+    _call_on(dev, stream, "rf_attn_paged", _lib.rf_attn_paged, q.data_ptr(), kp.data_ptr(), vp.data_ptr(),
+             *_c_ints(pages, page), table.data_ptr(), _i32(width), plan.data_ptr(), plan.shape[0],
+             *_c_ints(B, T, H, Hkv, D, max_new, max_len, window, sinks), scale,
+             _cache_dtype(q.dtype, "q"), out.data_ptr(), _addr(lse))
+
+
 def rf_stream_read(x, out_xor, stream=None):
     """XOR every 32-bit word of the CUDA tensor ``x`` into ``out_xor`` (one
     int32 element, device memory) with one streaming read of ``x``."""
@@ -1064,3 +1110,56 @@ def qk_norm_rope(q, k, positions, freq, q_weight=None, k_weight=None, axis=None,
     rf_qk_norm_rope(q, k, v, q_weight, k_weight, eps, positions, freq, axis, interleaved, slots, q_out,
                     k_out, vp)
     return (q_out, k_out) if kp is None else q_out
+
+
+class PagedPlan(typing.NamedTuple):
+    """A step's plan for attn_paged (paged_plan makes it), with the call's scratch.  Serves the calls of
+    one step, one at a time; a loop hands it back to paged_plan for the next step."""
+    plan: torch.Tensor
+    sizes: tuple        # (device index, B, T, H, Hkv)
+    max_new: int
+    max_len: int
+    window: int
+    sinks: int
+
+
+def paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window=0, sinks=0, plan=None, stream=None):
+    """The plan of a step over a paged cache, made on the device from its lengths.
+
+    starts int32 [B + 1], lens int32 [B] (as page_tables gives them), T rows of q, max_new and max_len:
+    the most new tokens and keys of a request.  ``plan``: an earlier one of the same sizes, whose memory
+    is used again."""
+    if stream is not None:
+        return _within(stream, lens, paged_plan, starts, lens, T, H, Hkv, max_new, max_len, window, sinks,
+                       plan)
+    dev = _device_of(lens, "lens")
+    sizes = (dev, lens.shape[0], T, H, Hkv)
+    if plan is None:
+        with torch.cuda.device(dev):
+            n = rf_paged_plan_bytes(lens.shape[0], T, H, Hkv, max_new, max_len, window, sinks)
+            buf = torch.empty(max(n, 1), dtype=torch.uint8, device=lens.device)
+        plan = PagedPlan(buf, sizes, max_new, max_len, window, sinks)
+    elif plan[1:] != (sizes, max_new, max_len, window, sinks):
+        raise ValueError(f"plan was made for (device, B, T, H, Hkv), max_new, max_len, window, sinks = "
+                         f"{plan[1:]}, the call has {(sizes, max_new, max_len, window, sinks)}")
+    rf_paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window, sinks, plan.plan)
+    return plan
+
+
+def attn_paged(q, kp, vp, table, plan, scale=None, stream=None):
+    """Attention of a batch's new tokens over a paged cache: single tokens, drafted ones, chunks and
+    whole prompts, mixed as they come.
+
+    q [T, H, D], kp/vp [pages, Hkv, page, D] (bf16 or fp16), table int32 [B, width], plan from
+    paged_plan.  Returns out [T, H, D] and lse [T, H]; rows of no request hold anything."""
+    if stream is not None:
+        return _within(stream, q, attn_paged, q, kp, vp, table, plan, scale)
+    if q.dim() != 3 or kp.dim() != 4 or table.dim() != 2:
+        raise ValueError("q must be [T, H, D], kp [pages, Hkv, page, D] and table [B, width]")
+    got = (q.get_device(), table.shape[0], q.shape[0], q.shape[1], kp.shape[1])
+    if got != plan.sizes:
+        raise ValueError(f"plan was made for (device, B, T, H, Hkv) = {plan.sizes}, the call has {got}")
+    out, lse = _outputs(q, None)
+    rf_attn_paged(q, kp, vp, table, plan.plan, plan.max_new, plan.max_len, plan.window, plan.sinks,
+                  q.shape[-1] ** -0.5 if scale is None else scale, out, lse)
+    return out, lse

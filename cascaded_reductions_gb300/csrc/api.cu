@@ -3,7 +3,7 @@
 
 #include <math.h>
 
-#include "cache_common.cuh"
+#include "paged.cuh"
 #include "tc_common.cuh"
 
 namespace {
@@ -34,6 +34,19 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   if (!a || !b) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+// The sizes of a step over a paged cache.
+rf_status check_paged(const rf::PagedShape& s) {
+  if (s.B <= 0 || s.T <= 0 || s.H <= 0 || s.Hkv <= 0 || s.max_new <= 0 || s.max_len <= 0 || s.window < 0 ||
+      s.sinks < 0)
+    return RF_ERR_INVALID_ARG;
+  if (s.H % s.Hkv != 0 || s.max_new > s.T) return RF_ERR_INVALID_ARG;
+  // row and unit numbers stay within an int
+  if (s.max_len > (1 << 30) || (long long)s.T * s.H > 0x7fffffffLL || s.B > (1 << 20) || s.H > (1 << 16) ||
+      (long long)s.B * s.Hkv * s.tiles() > 0x1fffffffLL)
+    return RF_ERR_UNSUPPORTED;
+  return RF_OK;
 }
 
 }  // namespace
@@ -507,6 +520,68 @@ rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long l
                                  weight_dtype == RF_F32, eps, positions, axes, freq, axis, R,
                                  interleaved != 0, dtype, slots, pages, page, q_out, k_out, v_out,
                                  as_stream(stream));
+}
+
+size_t rf_paged_plan_bytes(int B, int T, int H, int Hkv, int max_new, int max_len, int window, int sinks) {
+  const rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks};
+  rf::PagedLayout l;
+  return check_paged(s) == RF_OK && rf::paged_layout(s, &l) ? l.bytes : 0;
+}
+
+rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T, int H, int Hkv,
+                        int max_new, int max_len, int window, int sinks, void* plan, size_t bytes,
+                        void* stream) {
+  if (!starts || !lens || !plan) return RF_ERR_INVALID_ARG;
+  const rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks};
+  const rf_status st = check_paged(s);
+  if (st != RF_OK) return st;
+  if (reinterpret_cast<uintptr_t>(plan) % 256 != 0) return RF_ERR_MISALIGNED;
+  rf::PagedLayout l;
+  if (!rf::paged_layout(s, &l)) return RF_ERR_CUDA;
+  if (bytes < l.bytes) return RF_ERR_INVALID_ARG;
+  return rf::launch_paged_plan(starts, lens, s, plan, as_stream(stream));
+}
+
+rf_status rf_attn_paged(const void* q, const void* kp, const void* vp, int pages, int page,
+                        const int32_t* table, int width, void* plan, size_t bytes, int B, int T, int H,
+                        int Hkv, int D, int max_new, int max_len, int window, int sinks, float scale,
+                        int dtype, void* out, float* lse, void* stream) {
+  if (!q || !kp || !vp || !table || !plan || !out) return RF_ERR_INVALID_ARG;
+  if (pages <= 0 || page <= 0 || width <= 0 || D <= 0 || !isfinite(scale)) return RF_ERR_INVALID_ARG;
+  if (dtype != RF_F32 && dtype != RF_BF16 && dtype != RF_F16) return RF_ERR_INVALID_ARG;
+  const rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks};
+  rf_status st = check_paged(s);
+  if (st != RF_OK) return st;
+  if ((long long)width * page < max_len) return RF_ERR_INVALID_ARG;
+  if (D != 128 || dtype == RF_F32 || !(scale > 0.f)) return RF_ERR_UNSUPPORTED;
+  int log2 = 4;
+  while (log2 < 8 && (1 << log2) != page) ++log2;
+  if ((1 << log2) != page || (long long)pages * Hkv > 0x3fffffffLL || (long long)B * width > 0x7fffffffLL)
+    return RF_ERR_UNSUPPORTED;
+  if (!rf::aligned16(q) || !rf::aligned16(kp) || !rf::aligned16(vp) || !rf::aligned16(out) ||
+      reinterpret_cast<uintptr_t>(plan) % 256 != 0)
+    return RF_ERR_MISALIGNED;
+  rf::PagedLayout l;
+  if (!rf::paged_layout(s, &l)) return RF_ERR_CUDA;
+  if (bytes < l.bytes) return RF_ERR_INVALID_ARG;
+  rf::PagedAttn a = {};
+  a.v = rf::paged_view(s, l, plan);
+  a.q = static_cast<const uint8_t*>(q);
+  a.kp = static_cast<const uint8_t*>(kp);
+  a.vp = static_cast<const uint8_t*>(vp);
+  a.table = table;
+  a.pages = pages, a.page_log2 = log2, a.width = width;
+  a.scale_log2 = scale * rf::kLog2e;
+  a.out = static_cast<uint8_t*>(out);
+  a.lse = lse;
+  const bool pairs = s.some_pairs();
+  if (pairs) {
+    st = rf::launch_paged_prefill(a, dtype, as_stream(stream));
+    if (st != RF_OK) return st;
+  }
+  st = rf::launch_paged_decode(a, dtype, as_stream(stream));
+  if (st != RF_OK || !pairs) return st;
+  return rf::launch_paged_finish(a, dtype, as_stream(stream));
 }
 
 rf_status rf_device_error(int* status, void* stream) {

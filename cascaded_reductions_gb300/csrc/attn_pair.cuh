@@ -209,6 +209,34 @@ __device__ __forceinline__ void st_row32(void* dst, const uint32_t (&w)[16], boo
   }
 }
 
+// Whether a policy's keys lie in pages.  Such a one differs from the others so:
+//   item(t, c, it)             steps `it` on to the cluster's next item (t = 0: the first)
+//   Pages, pages_of(it, j, rank, lane)  what a lane copies of block j, and
+//   load_k / load_v(..., pages, rank, lane)  its copies; no tmW, v_bytes or narrow blocks
+//   partial(it), keep(it, rank, row, col, v, m, l)  whether the item is a part of a tile's
+//                              blocks, and then, instead of pack and send, its state
+//   boxed(pending)             whether the warp's 32 rows leave by send(); else pack has
+//                              stored the columns
+template <class P, class = void>
+struct Paged {
+  static constexpr bool value = false;
+};
+template <class P>
+struct Paged<P, decltype((void)sizeof(typename P::Pages))> {
+  static constexpr bool value = true;
+};
+template <class P>
+constexpr __host__ __device__ bool is_paged() {
+  return Paged<P>::value;
+}
+template <class P>
+__device__ __forceinline__ bool next_item(const P& p, int t, int cluster, int nclusters, typename P::Item& it) {
+  if constexpr (is_paged<P>())
+    return p.item(t, cluster, it);
+  else
+    return p.item(t, cluster, nclusters, it);
+}
+
 template <int N>
 struct Words {
   static constexpr int value = N;
@@ -234,11 +262,11 @@ __device__ __forceinline__ uint32_t pack_16x2(float lo, float hi) {
   return pack_bf16x2(lo, hi);
 }
 
+// The kernel's body, in line in each kernel that runs a policy.
 template <class P>
-__global__ void __launch_bounds__(THREADS, 1)
-attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmW,
-                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ P p) {
+__device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                               const CUtensorMap& tmV, const CUtensorMap& tmW,
+                                               const CUtensorMap& tmO, const P& p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -303,7 +331,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool ok = true;
     typename P::Item it;
     for (int t = 0; ok; ++t) {
-      if (!p.item(t, cluster, nclusters, it)) break;
+      if (!next_item(p, t, cluster, nclusters, it)) break;
       float m_ref = P::M_START, l = 0.f;
       // One block, of which this warp's rows see some of its 128 keys (NW = 4
       // 32-key words) or none (NW = 0); false if a wait gave up.
@@ -419,7 +447,32 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     if (warp == TMA_WARP) {
       // ------------------------------------------------------ TMA ----
-      if (lane == 0) {
+      if constexpr (is_paged<P>()) {
+        // every lane copies pages of its own
+        uint32_t g = 0;
+        bool ok = true;
+        typename P::Item it;
+        for (int t = 0; ok; ++t) {
+          if (!p.item(t, cluster, it)) break;
+          const int qb = t & 1;
+          if (!(ok = tc::mbar_wait(&sh->q_empty[qb], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort))) break;
+          if (lane == 0) {
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full[qb], 2 * p.q_bytes());
+            p.load_q(sQ + qb * TILE_BYTES, &tmQ, tc::mapa(tc::smem_u32(&sh->q_full[qb]), 0), it, rank);
+          }
+          for (int j = 0; j < it.n; ++j, ++g) {
+            const int s = (int)(g & 1u);
+            const uint32_t ph = (g >> 1) & 1u;
+            const typename P::Pages pages = p.pages_of(it, j, rank, lane);
+            if (!(ok = tc::mbar_wait(&sh->k_empty[s], ph ^ 1u, abort))) break;
+            if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh->k_full[s], 2 * TILE_BYTES);
+            p.load_k(sK + s * TILE_BYTES, &tmK, tc::mapa(tc::smem_u32(&sh->k_full[s]), 0), pages, rank, lane);
+            if (!(ok = tc::mbar_wait(&sh->v_empty[s], ph ^ 1u, abort))) break;
+            if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh->v_full[s], 2 * TILE_BYTES);
+            p.load_v(sV + s * TILE_BYTES, &tmV, tc::mapa(tc::smem_u32(&sh->v_full[s]), 0), pages, rank, lane);
+          }
+        }
+      } else if (lane == 0) {
         tc::prefetch_tmap(&tmQ);
         tc::prefetch_tmap(&tmK);
         tc::prefetch_tmap(&tmV);
@@ -504,11 +557,12 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // the first item's first S; then per block g: S(g + 1) (of this item or
         // the next) as soon as S(g) has been read, then P V(g) once P(g) is in
         typename P::Item it, next;
-        bool ok = p.item(0, cluster, nclusters, it);
+        bool ok = next_item(p, 0, cluster, nclusters, it);
         if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0), it.n == 1);
         uint32_t g = 0;
         for (int t = 0; ok; ++t) {
-          const bool has_next = p.item(t + 1, cluster, nclusters, next);
+          if constexpr (is_paged<P>()) next = it;
+          const bool has_next = next_item(p, t + 1, cluster, nclusters, next);
           for (int j = 0; ok && j < it.n; ++j, ++g) {
             if (j + 1 < it.n || has_next) {
               // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
@@ -541,7 +595,7 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       bool ok = true, repair = false;
       typename P::Item it;
       for (int t = 0; ok; ++t) {
-        if (!p.item(t, cluster, nclusters, it)) break;
+        if (!next_item(p, t, cluster, nclusters, it)) break;
         const int b = t & 1;
         // a whole item may pass meanwhile: 20 us more for each of its blocks (one takes 2)
         const unsigned long long limit = tc::kWaitLimitNs + (unsigned long long)it.n * 20000ull;
@@ -564,6 +618,12 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             __syncwarp();
             if (lane == 0) arrive_cluster_relaxed(o_free0);
           }
+          if constexpr (is_paged<P>()) {
+            if (p.partial(it)) {
+              p.keep(it, rank, r, 32 * c, v, m, lt);
+              continue;
+            }
+          }
           if constexpr (P::STAGED) {
             uint32_t w[16];
             repair |= p.pack(pending, 32 * c, v, m, lt, w);
@@ -580,9 +640,13 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           tc::fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) {
-            p.send(&tmO, box, pending);
-            tc::bulk_commit();
-            tc::bulk_wait_read();                     // the Q buffer may be filled again
+            bool boxed = true;
+            if constexpr (is_paged<P>()) boxed = !p.partial(it) && p.boxed(pending);
+            if (boxed) {
+              p.send(&tmO, box, pending);
+              tc::bulk_commit();
+              tc::bulk_wait_read();                   // the Q buffer may be filled again
+            }
             tc::mbar_arrive(&sh->q_empty[b]);
           }
           __syncwarp();
@@ -610,6 +674,14 @@ attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
+template <class P>
+__global__ void __launch_bounds__(THREADS, 1)
+attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ P p) {
+  attn_pair_body(tmQ, tmK, tmV, tmW, tmO, p);
+}
+
 inline cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, unsigned grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -627,8 +699,8 @@ inline cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, unsigned grid, 
 
 // clusters of two of these CTAs that are resident at once on the current
 // device (cached per device); 0 when none fits
-template <class P>
-int resident_pairs() {
+template <class P, class Kernel>
+int resident_pairs_of(Kernel kernel) {
   static std::atomic<int> count[64];
   static std::atomic<uint64_t> attr_done{0}, known{0};
   int dev = 0;
@@ -639,16 +711,21 @@ int resident_pairs() {
   // launched with fewer registers than the warpgroups' shares add up to, the
   // softmax warps would wait for them for ever
   cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, attn_pair_kernel<P>) == cudaSuccess && fa.numRegs == REGS &&
-      smem_attr(attn_pair_kernel<P>, SMEM_BYTES, attr_done) == RF_OK) {
+  if (cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == REGS &&
+      smem_attr(kernel, SMEM_BYTES, attr_done) == RF_OK) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pair_config(attr, 2u, 0);
-    if (cudaOccupancyMaxActiveClusters(&n, attn_pair_kernel<P>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   count[dev].store(n);
   known.fetch_or(bit, std::memory_order_release);
   return n;
+}
+
+template <class P>
+int resident_pairs() {
+  return resident_pairs_of<P>(attn_pair_kernel<P>);
 }
 
 template <class P>

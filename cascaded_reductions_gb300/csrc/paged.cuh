@@ -1,0 +1,196 @@
+// What the kernels of attention over a paged cache share: the plan of a step, and
+// which blocks of keys a tile of query rows visits.
+//
+// Requests with up to kPagedRows query rows per key head (new tokens times the heads
+// that share it) run on the streaming kernel (paged_decode.cu), 16 rows at a time; the
+// others on CTA pairs (paged_prefill.cu), 256 rows at a time.  Both take their work
+// from lists that paged_plan.cu makes once per step from the lengths on the device:
+//   units    of the streaming kernel: 16 rows and a piece of their keys;
+//   ranges   of the pair kernel: all 256-key blocks of all tiles, one after the other,
+//            cut into equal ranges wherever that falls, a range per cluster and round.
+#pragma once
+
+#include "cache_common.cuh"
+
+namespace rf {
+
+constexpr int kPagedRows = 64;          // query rows per key head of the streaming kernel
+constexpr int kPagedTileRows = 16;
+constexpr int kPagedBlock = 256;        // keys of the pair kernel's blocks
+constexpr int kPagedPairRows = 256;
+constexpr int kPagedSlotFloats = kPagedPairRows * (128 + 2);   // a partial state: O, m, l
+constexpr int kPagedRounds = 4;
+
+// The sizes that a plan and the calls over it share.
+struct PagedShape {
+  int B, T, H, Hkv, max_new, max_len, window, sinks;
+  __host__ __device__ int G() const { return H / Hkv; }
+  // query heads of a tile, and positions of it
+  __host__ __device__ int packed() const {
+    const int g = G();
+    return g % 8 == 0 ? 8 : g % 4 == 0 ? 4 : g % 2 == 0 ? 2 : 1;
+  }
+  __host__ __device__ int positions() const { return kPagedPairRows / packed(); }
+  __host__ __device__ bool some_pairs() const { return (long long)max_new * G() > kPagedRows; }
+  // of the streaming kernel: 16-row tiles per request at most, rows of one
+  __host__ __device__ int tiles() const {
+    const long long rows = (long long)max_new * G();
+    return (int)((rows < kPagedRows ? rows : kPagedRows) + kPagedTileRows - 1) / kPagedTileRows;
+  }
+  __host__ __device__ int unit_rows() const {
+    const long long rows = (long long)max_new * G();
+    return rows < kPagedTileRows ? (int)rows : kPagedTileRows;
+  }
+};
+
+// Words of a plan's head.
+enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
+
+// Where the parts of a plan lie, in bytes from its start.
+struct PagedLayout {
+  size_t seqs, before, ranges, units, counters, unit_ml, unit_acc, slots, bytes;
+  int unit_cap, range_cap;
+  uint32_t mark;                        // of the sizes: a plan of others is refused on the device
+};
+
+// One request as the plan found it.
+struct PagedSeq {
+  int start, n, len, pair;              // first row, rows, keys with the new ones, on the pair kernel
+};
+struct PagedUnit {
+  int b, tile, step0, step1;            // request, 16-row tile, steps of 64 keys
+  int first, pieces;                    // unit of the tile's first piece, pieces
+  int start, n, len;                    // the request, as in PagedSeq
+  int pad[3];
+};
+struct PagedRange {
+  int b, item, block, count;            // the first block's request, item and number in it; blocks
+};
+
+struct PagedView {
+  PagedShape s;
+  int* head;
+  const PagedSeq* seqs;
+  const PagedRange* ranges;
+  const PagedUnit* units;
+  int* counters;
+  float2* unit_ml;                      // [unit][Hkv][unit_rows]
+  float* unit_acc;                      // [unit][Hkv][unit_rows][128]
+  float* slots;
+  int unit_cap, range_cap;
+  uint32_t mark;
+};
+
+// The visible keys of a request's rows as tiles of 16: sinks' tiles first, then those
+// from the window's first key on.
+struct PagedTiles {
+  int sink_tiles, lo_tile, tiles;       // key tile of t: t < sink_tiles ? t : t - sink_tiles + lo_tile
+  __host__ __device__ PagedTiles(int n, int len, int window, int sinks) {
+    const int lo = window > 0 ? (len - n - window + 1 > 0 ? len - n - window + 1 : 0) : 0;
+    lo_tile = lo / kDecodeTile;
+    const int ns = sinks < lo_tile * kDecodeTile ? sinks : lo_tile * kDecodeTile;
+    sink_tiles = (ns + kDecodeTile - 1) / kDecodeTile;
+    tiles = sink_tiles + (len + kDecodeTile - 1) / kDecodeTile - lo_tile;
+  }
+  __host__ __device__ int steps() const { return (tiles + 3) / 4; }
+};
+
+// The tiles of one head group of a request on the pair kernel: tile i holds positions
+// p0 + i P .. , P = 256 / heads; it visits the window's blocks [lb, hb) and up to SB
+// blocks of sinks below them.
+struct PagedBlocks {
+  int n, p0, P, window, SB;
+  __host__ __device__ PagedBlocks(int n_, int len, int P_, int window_, int sinks)
+      : n(n_), p0(len - n_), P(P_), window(window_),
+        SB(window_ > 0 ? (int)(((long long)sinks + kPagedBlock - 1) / kPagedBlock) : 0) {}
+  __host__ __device__ int tiles() const { return (n + P - 1) / P; }
+  __host__ __device__ int end(int i) const { return (i + 1) * P < n ? (i + 1) * P : n; }
+  __host__ __device__ int hb(int i) const {
+    const int x = p0 + end(i);
+    return x <= kPagedBlock ? 1 : (x + kPagedBlock - 1) / kPagedBlock;
+  }
+  __host__ __device__ int lb(int i) const {
+    if (window == 0) return 0;
+    const int lo = p0 + i * P - window + 1;
+    return lo > 0 ? lo / kPagedBlock : 0;
+  }
+  __host__ __device__ int sink_blocks(int i) const {
+    const int l = lb(i);
+    return SB < l ? SB : l;
+  }
+  __host__ __device__ int blocks(int i) const { return hb(i) - lb(i) + sink_blocks(i); }
+
+  // blocks of tiles 0 .. m - 1
+  __host__ __device__ long long before(int m) const {
+    if (m <= 0) return 0;
+    long long sum = 0;
+    if (m == tiles()) {                 // the last one may hold fewer positions
+      --m;
+      sum = blocks(m);
+    }
+    const long long r = kPagedBlock / P;
+    // ends at or below 0 count one block; then ceil((p0 + (i + 1) P) / 256)
+    long long s = p0 < 0 ? (long long)(-(long long)p0) / P : 0;
+    if (s > m) s = m;
+    const long long first = p0 + s * P;                         // above -P
+    const long long u0 = first > 0 ? (first + P - 1) / P : 0;
+    sum += s + up(u0 + (m - s), r) - up(u0, r);
+    if (window > 0) {                   // less the blocks below the window that no sink keeps
+      long long c = (long long)p0 - window + 1 - (long long)kPagedBlock * SB;
+      long long k = c < 0 ? (-c + P - 1) / P : 0;
+      if (k < m) {
+        c += k * P;
+        sum -= down(c / P + (m - k), r) - down(c / P, r);
+      }
+    }
+    return sum;
+  }
+  // sum of ceil(k / r) for k = 1 .. x, of floor(k / r) for k = 0 .. x - 1
+  static __host__ __device__ long long up(long long x, long long r) {
+    const long long q = x / r;
+    return r * q * (q + 1) / 2 + (x - q * r) * (q + 1);
+  }
+  static __host__ __device__ long long down(long long x, long long r) {
+    const long long q = x / r;
+    return r * q * (q - 1) / 2 + (x - q * r) * q;
+  }
+};
+
+// false where the device cannot be queried
+bool paged_layout(const PagedShape& s, PagedLayout* l);
+inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* plan) {
+  uint8_t* p = static_cast<uint8_t*>(plan);
+  PagedView v;
+  v.s = s;
+  v.head = reinterpret_cast<int*>(p);
+  v.seqs = reinterpret_cast<const PagedSeq*>(p + l.seqs);
+  v.ranges = reinterpret_cast<const PagedRange*>(p + l.ranges);
+  v.units = reinterpret_cast<const PagedUnit*>(p + l.units);
+  v.counters = reinterpret_cast<int*>(p + l.counters);
+  v.unit_ml = reinterpret_cast<float2*>(p + l.unit_ml);
+  v.unit_acc = reinterpret_cast<float*>(p + l.unit_acc);
+  v.slots = reinterpret_cast<float*>(p + l.slots);
+  v.unit_cap = l.unit_cap, v.range_cap = l.range_cap;
+  v.mark = l.mark;
+  return v;
+}
+
+// The arguments of attention over a plan.
+struct PagedAttn {
+  PagedView v;
+  const uint8_t *q, *kp, *vp;           // [T, H, 128], [pages, Hkv, page, 128] of a 16-bit type
+  const int32_t* table;                 // [B, width]
+  int pages, page_log2, width;
+  float scale_log2;
+  uint8_t* out;                         // [T, H, 128]
+  float* lse;                           // [T, H] or null
+};
+
+rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const PagedShape& s, void* plan,
+                            cudaStream_t st);
+rf_status launch_paged_decode(const PagedAttn& a, int dtype, cudaStream_t st);
+rf_status launch_paged_prefill(const PagedAttn& a, int dtype, cudaStream_t st);
+rf_status launch_paged_finish(const PagedAttn& a, int dtype, cudaStream_t st);
+int paged_pairs();                      // clusters of the pair kernel on the current device; 0: none
+
+}  // namespace rf

@@ -1,0 +1,548 @@
+// Attention of few new tokens per request over a paged cache: single tokens, drafted
+// ones, short chunks.  The new tokens of a request times the query heads that share a
+// key head are its rows; 16 of them share every key that is read.
+//
+// Mathematics: per row the cascade of the split-KV decode (running m, l, acc, rescale by
+// exp2(m_old - m_new), states merged by the same rescale), over key <= position, in the
+// window or below the sinks.
+//
+// What bounds it: HBM.  As in the dense cache's decode, both products run on the
+// warp-level matrix instruction m16n8k16, four warps stream 16-key tiles of their own
+// through three stages of asynchronous copies, and weights enter in two 16-bit terms.
+// A tile of 16 keys lies in one page: a warp asks for the tile's page number one step
+// before its keys.
+//
+// Work comes from the plan's units (16 rows of a request, a piece of their keys) times
+// key heads, the first of a CTA by its number, the others from a queue.  A fifth warp
+// takes what would hold the stream up: it fetches the next unit, and behind a piece it
+// fences, counts it, and, where it was its tile's last, merges the pieces while the other
+// four are in the next unit.  In a small call, where there is no next unit, those four
+// merge, a row each.
+
+#include "paged.cuh"
+#include "tc_common.cuh"
+#include "warp_tile.cuh"
+
+namespace rf {
+namespace {
+
+constexpr int TK = kDecodeTile;
+constexpr int WARPS = 4;                // that stream; one more closes
+constexpr int THREADS = (WARPS + 1) * 32;
+constexpr int STAGES = 3;
+constexpr int STAGE_BYTES = 2 * TK * ROW_BYTES;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int MROWS = kPagedTileRows;
+constexpr size_t SMEM_BYTES = (size_t)WARPS * RING_BYTES;
+constexpr int MERGE_PITCH = HD + 8;
+static_assert((size_t)WARPS * MROWS * MERGE_PITCH * 4 <= SMEM_BYTES, "the warps' accumulators reuse the rings");
+
+template <int ID, int N>
+__device__ __forceinline__ void named_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+
+// A unit's rows and keys, for one key head.
+struct Work {
+  int b, hk, start, n, len, row0, rows;  // rows row0 .. row0 + rows - 1 of n * G
+  PagedTiles t;
+  __device__ __forceinline__ Work(const PagedAttn& a, const PagedUnit& u, int hk_)
+      : b(u.b), hk(hk_), start(u.start), n(u.n), len(u.len), row0(u.tile * MROWS),
+        rows(min(MROWS, u.n * a.v.s.G() - u.tile * MROWS)), t(u.n, u.len, a.v.s.window, a.v.s.sinks) {}
+  // row r's query row in [T * H], and its position
+  __device__ __forceinline__ size_t at(const PagedAttn& a, int r) const {
+    const int G = a.v.s.G(), i = (row0 + r) / G;
+    return (size_t)(start + i) * a.v.s.H + hk * G + (row0 + r - i * G);
+  }
+  __device__ __forceinline__ int pos(const PagedAttn& a, int r) const {
+    return len - n + (row0 + r) / a.v.s.G();
+  }
+  __device__ __forceinline__ int key_tile(int i) const {
+    return i < t.sink_tiles ? i : i - t.sink_tiles + t.lo_tile;
+  }
+};
+
+__device__ __forceinline__ int page_of(const PagedAttn& a, const Work& w, int tile) {
+  const int i = tile * TK >> a.page_log2;
+  const size_t at = (size_t)w.b * a.width + i;
+  return i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width) ? a.table[at] : -1;
+}
+
+// Keys 16 tile .. + 15 into a stage: K rows, then V rows, 16-byte chunks permuted by row
+// % 8.  Rows past the request's end, and those of a page outside the cache, are zeros.
+__device__ __forceinline__ void copy_tile(const PagedAttn& a, const Work& w, int tile, int page, uint32_t stage,
+                                          uint64_t policy, int lane) {
+  const bool has = (unsigned)page < (unsigned)a.pages;
+  const int key0 = tile * TK, mask = (1 << a.page_log2) - 1;
+  const size_t row0 = (((size_t)(has ? page : 0) * a.v.s.Hkv + w.hk) << a.page_log2) + (key0 & mask);
+#pragma unroll
+  for (int u = 0; u < TK / 2; ++u) {
+    const int r = 2 * u + (lane >> 4), c = lane & 15;
+    const bool in = has && key0 + r < w.len &&
+                    RF_IDX_OK(row0 + r, ((size_t)a.pages * a.v.s.Hkv) << a.page_log2);
+    const size_t off = (row0 + (in ? r : 0)) * ROW_BYTES + c * 16;
+    const uint32_t dst = stage + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
+    cp_async16(dst, a.kp + off, in ? 16u : 0u, policy);
+    cp_async16(dst + TK * ROW_BYTES, a.vp + off, in ? 16u : 0u, policy);
+  }
+}
+
+// One warp's running state: rows lane / 4 (index 0) and + 8 (index 1); acc[d] holds
+// columns 8 d + 2 (lane % 4) and + 1 of both.
+template <bool F16>
+struct State {
+  // The weights' reference for the maximum m: an fp16 weight is taken 2^15 times as large.
+  // From 2^24 on m - 15 may round to m - 16 or less, and a weight to 2^16: m itself then.
+  static __device__ __forceinline__ float below(float m) {
+    if constexpr (!F16) return m;
+    const float f = m - 15.f;
+    return m - f > 15.5f ? m : f;
+  }
+  uint32_t qf[HD / 16][4];
+  float acc[HD / 8][4];
+  float m0, m1, l0, l1;
+  int p0, p1, first, last;              // positions: the lane's rows', the tile's first and last
+
+  __device__ __forceinline__ void start(const PagedAttn& a, const Work& w, int lane) {
+    const int r = lane >> 2;
+    const size_t rows = (size_t)a.v.s.T * a.v.s.H;
+    (void)rows;                         // read by the checked build only
+    const size_t a0 = w.at(a, r < w.rows ? r : 0), a1 = w.at(a, r + 8 < w.rows ? r + 8 : 0);
+    const bool in0 = r < w.rows && RF_IDX_OK(a0, rows), in1 = r + 8 < w.rows && RF_IDX_OK(a1, rows);
+    const uint8_t* q0 = a.q + a0 * ROW_BYTES + (lane & 3) * 4;
+    const uint8_t* q1 = a.q + a1 * ROW_BYTES + (lane & 3) * 4;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      qf[kk][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32) : 0u;
+      qf[kk][1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + kk * 32) : 0u;
+      qf[kk][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16) : 0u;
+      qf[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + kk * 32 + 16) : 0u;
+    }
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+    first = w.pos(a, 0);
+    last = w.pos(a, w.rows - 1);
+    p0 = w.pos(a, min(r, w.rows - 1));
+    p1 = w.pos(a, min(r + 8, w.rows - 1));
+  }
+
+  // folds in keys key0 .. key0 + 15, whose copies are in `st`
+  __device__ __forceinline__ void tile(const PagedAttn& a, uint32_t st, int key0, int lane) {
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    {
+      const int r = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        const int c = 2 * kk + ((lane >> 3) & 1);
+        uint32_t kb[4];
+        ldmatrix_x4(st + r * ROW_BYTES + ((c ^ (r & 7)) << 4), kb);
+        mma16816<F16>(s[0], qf[kk], kb[0], kb[1]);
+        mma16816<F16>(s[1], qf[kk], kb[2], kb[3]);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] *= a.scale_log2;
+    const int window = a.v.s.window, sinks = a.v.s.sinks;
+    const bool whole = key0 + TK - 1 <= first && (window == 0 || key0 > last - window || key0 + TK <= sinks);
+    if (!whole) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = key0 + nt * 8 + 2 * (lane & 3) + e;
+          if (t > p0 || (window > 0 && t <= p0 - window && t >= sinks)) s[nt][e] = -INFINITY;
+          if (t > p1 || (window > 0 && t <= p1 - window && t >= sinks)) s[nt][2 + e] = -INFINITY;
+        }
+    }
+    float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+    float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+      // differences of the rounded references themselves
+      const float c0 = exp2f(below(m0) - below(ref_of(n0))), c1 = exp2f(below(m1) - below(ref_of(n1)));
+      m0 = n0;
+      m1 = n1;
+      l0 *= c0;
+      l1 *= c1;
+#pragma unroll
+      for (int d = 0; d < HD / 8; ++d) {
+        acc[d][0] *= c0;
+        acc[d][1] *= c0;
+        acc[d][2] *= c1;
+        acc[d][3] *= c1;
+      }
+    }
+    const float f0 = below(ref_of(m0)), f1 = below(ref_of(m1));
+    uint32_t hi[4], lw[4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const float p00 = exp2f(s[nt][0] - f0), p01 = exp2f(s[nt][1] - f0);
+      const float p10 = exp2f(s[nt][2] - f1), p11 = exp2f(s[nt][3] - f1);
+      l0 += p00 + p01;
+      l1 += p10 + p11;
+      split16<F16>(p00, p01, hi[2 * nt], lw[2 * nt]);
+      split16<F16>(p10, p11, hi[2 * nt + 1], lw[2 * nt + 1]);
+    }
+    {
+      const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d) {
+        const int c = 2 * d + (lane >> 4);
+        uint32_t vb[4];
+        ldmatrix_x4_trans(st + TK * ROW_BYTES + r * ROW_BYTES + ((c ^ (r & 7)) << 4), vb);
+        mma16816<F16>(acc[2 * d], hi, vb[0], vb[1]);
+        mma16816<F16>(acc[2 * d + 1], hi, vb[2], vb[3]);
+        mma16816<F16>(acc[2 * d], lw, vb[0], vb[1]);
+        mma16816<F16>(acc[2 * d + 1], lw, vb[2], vb[3]);
+      }
+    }
+  }
+
+  // the row sums over the four lanes that share a row; once, before the state is used
+  __device__ __forceinline__ void close() {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  }
+
+  // the warp's rows into its part of the merge buffer
+  __device__ __forceinline__ void give(float* acc_buf, float2* ml_buf, int rows, int lane) const {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = (lane >> 2) + 8 * half;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int d = 0; d < HD / 8; ++d)
+        *reinterpret_cast<float2*>(acc_buf + r * MERGE_PITCH + d * 8 + 2 * (lane & 3)) =
+            make_float2(acc[d][2 * half], acc[d][2 * half + 1]);
+      if ((lane & 3) == 0) ml_buf[r] = half ? make_float2(below(m1), l1) : make_float2(below(m0), l0);
+    }
+  }
+};
+
+// Row r's accumulator A over the keys of tiles t0 .. t1 - 1, weights relative to `ref`,
+// with the columns that are NaN computed again key by key from the row's visible keys:
+// an infinite value gives that infinity (its product with a weight's second term does
+// not), and a value that another row of the tile sees does not reach this one.  Ends once
+// the columns are all NaN again, which they stay.  A call, so that its code lies apart.
+template <bool F16>
+__device__ __noinline__ float4 redo_columns(const PagedAttn& a, const Work w, int r, int t0, int t1, float ref,
+                                            float4 A, int lane) {
+  const int window = a.v.s.window, sinks = a.v.s.sinks, p = w.pos(a, r);
+  const float4 x = load_row4<F16>(a.q + w.at(a, r) * ROW_BYTES, lane);
+  float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t = t0; t < t1; ++t) {
+    const int tile = w.key_tile(t), page = page_of(a, w, tile);
+    const bool has = (unsigned)page < (unsigned)a.pages;
+    const size_t row0 = (((size_t)(has ? page : 0) * a.v.s.Hkv + w.hk) << a.page_log2) +
+                        (tile * TK & ((1 << a.page_log2) - 1));
+    for (int u0 = 0; u0 < TK; u0 += 8) {
+      float s[8];
+      float4 v[8];
+      bool seen[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int key = tile * TK + u0 + u;
+        seen[u] = key <= p && (window == 0 || key > p - window || key < sinks);
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+        v[u] = k;
+        const size_t at = row0 + u0 + u;
+        if (seen[u] && has && RF_IDX_OK(at, ((size_t)a.pages * a.v.s.Hkv) << a.page_log2)) {
+          k = load_row4<F16>(a.kp + at * ROW_BYTES, lane);
+          v[u] = load_row4<F16>(a.vp + at * ROW_BYTES, lane);
+        }
+        s[u] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, x.w * k.w)));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (!seen[u]) continue;
+        const float e = exp2f(__fmul_rn(s[u], a.scale_log2) - ref);
+        R.x = fmaf(e, v[u].x, R.x);
+        R.y = fmaf(e, v[u].y, R.y);
+        R.z = fmaf(e, v[u].z, R.z);
+        R.w = fmaf(e, v[u].w, R.w);
+      }
+    }
+    const bool again = (A.x != A.x && R.x == R.x) || (A.y != A.y && R.y == R.y) ||
+                       (A.z != A.z && R.z == R.z) || (A.w != A.w && R.w == R.w);
+    if (!__any_sync(0xffffffffu, again)) break;
+  }
+  return make_float4(A.x != A.x ? R.x : A.x, A.y != A.y ? R.y : A.y, A.z != A.z ? R.z : A.z,
+                     A.w != A.w ? R.w : A.w);
+}
+
+// a finished row, four columns per lane
+__device__ __forceinline__ void write_row(const PagedAttn& a, size_t row, float4 A, float M, float L, int lane,
+                                          int dtype) {
+  if (!RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) return;
+  const size_t o = row * HD + lane * 4;
+  store_out2(a.out, o, normalised(A.x, L), normalised(A.y, L), dtype);
+  store_out2(a.out, o + 2, normalised(A.z, L), normalised(A.w, L), dtype);
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+// Row r of the CTA's warps merged by one warp, four columns per lane, into the output or
+// into the unit's state.
+template <bool F16>
+__device__ __forceinline__ void merge_warps(const PagedAttn& a, const Work& w, const float* acc_buf,
+                                            const float2 (*ml_buf)[MROWS], int r, bool direct, size_t state0,
+                                            int t0, int t1, int lane) {
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) M = fmaxf(M, ml_buf[i][r].x);
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    const float2 ml = ml_buf[i][r];
+    const float f = exp2f(ml.x - ref_of(M));
+    const float4 v = *reinterpret_cast<const float4*>(acc_buf + (i * MROWS + r) * MERGE_PITCH + lane * 4);
+    L = fmaf(f, ml.y, L);
+    A.x = fmaf(f, v.x, A.x);
+    A.y = fmaf(f, v.y, A.y);
+    A.z = fmaf(f, v.z, A.z);
+    A.w = fmaf(f, v.w, A.w);
+  }
+  if (__any_sync(0xffffffffu, L > 0.f && any_nan(A))) A = redo_columns<F16>(a, w, r, t0, t1, ref_of(M), A, lane);
+  if (direct) {
+    write_row(a, w.at(a, r), A, M, L, lane, F16 ? RF_F16 : RF_BF16);
+  } else {
+    const size_t s = state0 + r;
+    if (!RF_IDX_OK(s, (size_t)a.v.unit_cap * a.v.s.Hkv * a.v.s.unit_rows())) return;
+    *(reinterpret_cast<float4*>(a.v.unit_acc + s * HD) + lane) = A;
+    if (lane == 0) a.v.unit_ml[s] = make_float2(M, L);
+  }
+}
+
+// Rows r0 .. r0 + nr - 1 (at most RB) of a tile from the states of its pieces, in order;
+// one warp, four columns per lane, LOADS / RB states in flight.
+template <int RB, int LOADS = 16>
+__device__ __forceinline__ void merge_pieces(const PagedAttn& a, const Work& w, int first, int pieces, int r0,
+                                             int nr, int dtype, int lane) {
+  constexpr int SB = LOADS / RB;
+  const size_t step = (size_t)a.v.s.Hkv * a.v.s.unit_rows();
+  const size_t base = first * step + (size_t)w.hk * a.v.s.unit_rows() + r0;
+  const size_t states = (size_t)a.v.unit_cap * step;
+  (void)states;                         // read by the checked build only
+  float M[RB], L[RB];
+  float4 A[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    M[r] = -INFINITY;
+    L[r] = 0.f;
+    A[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int s0 = 0; s0 < pieces; s0 += 32) {
+    const int cnt = min(32, pieces - s0);
+    // lane j holds piece s0 + j's maximum and sum, then its weight; the accumulators are
+    // asked for before the weights are known
+    float2 ml[RB];
+    float f[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      ml[r] = make_float2(-INFINITY, 0.f);
+      const size_t at = base + (s0 + lane) * step + r;
+      if (r < nr && lane < cnt && RF_IDX_OK(at, states)) ml[r] = __ldcg(a.v.unit_ml + at);
+    }
+    for (int j0 = 0; j0 < cnt; j0 += SB) {
+      float4 v[RB][SB];
+#pragma unroll
+      for (int j = 0; j < SB; ++j)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const size_t at = base + (s0 + j0 + j) * step + r;
+          v[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < nr && j0 + j < cnt && RF_IDX_OK(at, states))
+            v[r][j] = __ldcg(reinterpret_cast<const float4*>(a.v.unit_acc + at * HD) + lane);
+        }
+      if (j0 == 0) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const float top = fmaxf(M[r], group_max<32>(ml[r].x)), c = exp2f(M[r] - ref_of(top));
+          M[r] = top;
+          L[r] *= c;
+          A[r].x *= c;
+          A[r].y *= c;
+          A[r].z *= c;
+          A[r].w *= c;
+          f[r] = -1.f;                            // a piece without keys: its accumulator is not read
+          if (ml[r].x != -INFINITY) {
+            f[r] = exp2f(ml[r].x - ref_of(top));
+            L[r] = fmaf(f[r], ml[r].y, L[r]);
+          } else {
+            L[r] += ml[r].y;                      // 0, or NaN where every score was NaN
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < SB; ++j)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const float fj = __shfl_sync(0xffffffffu, f[r], (j0 + j) & 31);
+          if (j0 + j >= cnt || fj == -1.f) continue;
+          A[r].x = fmaf(fj, v[r][j].x, A[r].x);
+          A[r].y = fmaf(fj, v[r][j].y, A[r].y);
+          A[r].z = fmaf(fj, v[r][j].z, A[r].z);
+          A[r].w = fmaf(fj, v[r][j].w, A[r].w);
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    L[r] = group_sum<32>(L[r]);
+    if (r < nr) write_row(a, w.at(a, r0 + r), A[r], M[r], L[r], lane, dtype);
+  }
+}
+
+__device__ __forceinline__ PagedUnit load_unit(const PagedUnit* p) {
+  PagedUnit u;
+  int4* d = reinterpret_cast<int4*>(&u);
+  const int4* s = reinterpret_cast<const int4*>(p);
+  static_assert(sizeof(PagedUnit) == 48, "three 16-byte loads");
+  d[0] = s[0], d[1] = s[1], d[2] = s[2];
+  return u;
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(THREADS, 2)
+paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 sm_ml[WARPS][MROWS];
+  __shared__ int sm_next[2], sm_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int Hkv = a.v.s.Hkv;
+  // behind the pair kernel of the same call, which has waited for what was before it
+  if (!behind_pairs) wait_prerequisite();
+  allow_dependents();
+  const bool planned = a.v.head[kPlanMark] == (int)a.v.mark;
+  const int total = planned ? min(a.v.head[kPlanUnits], a.v.unit_cap) * Hkv : 0;
+  const bool queued = total > (int)gridDim.x;
+  // a large call's cache is read once and goes first; a small one's may be read again
+  const uint64_t policy = l2_policy(queued);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + (warp & 3) * RING_BYTES;
+  float* acc_buf = reinterpret_cast<float*>(smem);
+  constexpr int dtype = F16 ? RF_F16 : RF_BF16;
+
+  int turn = 0;
+  for (int i = blockIdx.x; i < total; ++turn) {
+    const int unit = i / Hkv, hk = i - unit * Hkv;
+    if (!RF_IDX_OK(unit, a.v.unit_cap)) break;
+    const PagedUnit u = load_unit(a.v.units + unit);
+    const Work w(a, u, hk);
+    int next = total;
+    if (warp < WARPS) {
+      int in = 0;                       // the stage that the next copies go to
+      const int t_end = min(w.t.tiles, u.step1 * WARPS);
+      int t_in = u.step0 * WARPS + warp;
+      int page = t_in < t_end ? page_of(a, w, w.key_tile(t_in)) : -1;
+      auto issue = [&]() {
+        if (t_in < t_end) {
+          const int tile = w.key_tile(t_in), now = page;
+          if (t_in + WARPS < t_end) page = page_of(a, w, w.key_tile(t_in + WARPS));
+          copy_tile(a, w, tile, now, ring + (uint32_t)in * STAGE_BYTES, policy, lane);
+        }
+        cp_async_commit();
+        t_in += WARPS;
+        in = in + 1 == STAGES ? 0 : in + 1;
+      };
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k) issue();
+      State<F16> st;
+      st.start(a, w, lane);
+      int slot = 0;
+      for (int t = u.step0 * WARPS + warp; t < t_end; t += WARPS) {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();                   // every lane's copies of this tile landed, the last is read
+        issue();
+        st.tile(a, ring + (uint32_t)slot * STAGE_BYTES, w.key_tile(t) * TK, lane);
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+      }
+      cp_async_wait<0>();
+      st.close();
+      named_sync<1, WARPS * 32>();      // the rings are free
+      st.give(acc_buf + warp * MROWS * MERGE_PITCH, sm_ml[warp], w.rows, lane);
+      named_sync<1, WARPS * 32>();
+      const size_t state0 = ((size_t)unit * Hkv + hk) * a.v.s.unit_rows();
+      for (int r = warp; r < w.rows; r += WARPS)
+        merge_warps<F16>(a, w, acc_buf, sm_ml, r, u.pieces == 1, state0, u.step0 * WARPS, t_end, lane);
+    } else if (queued) {
+      if (lane == 0) {
+        const int got = atomicAdd(a.v.head + kPlanQueue, 1);
+        sm_next[turn & 1] = (int)gridDim.x + got;
+        // every unit fetches once, so this was the last fetch
+        if (got == total - 1) atomicExch(a.v.head + kPlanQueue, 0);
+      }
+      __syncwarp();
+    }
+    named_sync<2, THREADS>();           // states stored, next unit known
+    if (queued) next = sm_next[turn & 1];
+    if (u.pieces > 1) {
+      const size_t at = (size_t)u.first * Hkv + hk;
+      if (warp == WARPS) {
+        int last = 0;
+        if (lane == 0 && RF_IDX_OK(at, (size_t)a.v.unit_cap * Hkv)) {
+          __threadfence();              // stands for the CTA, which the barrier joined
+          last = atomicAdd(a.v.counters + at, 1) == u.pieces - 1;
+          __threadfence();
+          if (last) a.v.counters[at] = 0;
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (next >= total) {
+          if (lane == 0) sm_last = last;
+          named_sync<3, THREADS>();
+        } else if (last) {
+          for (int r = 0; r < w.rows; r += 4)
+            merge_pieces<4>(a, w, u.first, u.pieces, r, min(4, w.rows - r), dtype, lane);
+        }
+      } else if (next >= total) {
+        named_sync<3, THREADS>();
+        if (sm_last) {
+          const int share = (w.rows + WARPS - 1) / WARPS, r = warp * share, nr = min(share, w.rows - r);
+          if (nr > 0) {
+            if (share == 1)
+              merge_pieces<1>(a, w, u.first, u.pieces, r, nr, dtype, lane);
+            else if (share == 2)
+              merge_pieces<2>(a, w, u.first, u.pieces, r, nr, dtype, lane);
+            else
+              merge_pieces<4>(a, w, u.first, u.pieces, r, nr, dtype, lane);
+          }
+        }
+      }
+    }
+    i = next;
+  }
+  if (behind_pairs) wait_prerequisite();   // a kernel ends after the one before it
+}
+
+template <bool F16>
+rf_status launch_t(const PagedAttn& a, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (smem_attr(paged_decode_kernel<F16>, SMEM_BYTES, done) != RF_OK) return RF_ERR_CUDA;
+  const int sms = tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  const long long most = (long long)a.v.unit_cap * a.v.s.Hkv;
+  const unsigned grid = (unsigned)(most < 2ll * sms ? most : 2ll * sms);
+  return launch_after(paged_decode_kernel<F16>, grid, THREADS, SMEM_BYTES, st, a, a.v.s.some_pairs());
+}
+
+}  // namespace
+
+rf_status launch_paged_decode(const PagedAttn& a, int dtype, cudaStream_t st) {
+  return dtype == RF_F16 ? launch_t<true>(a, st) : launch_t<false>(a, st);
+}
+
+RF_BOUNDS_WORD_OF_THIS_FILE
+
+}  // namespace rf

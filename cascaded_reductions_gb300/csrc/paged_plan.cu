@@ -1,0 +1,304 @@
+// The plan of a step over a paged cache: which CTA reads which keys, made on the
+// device from the step's lengths, once for all layers.
+//
+// A table is made for the longest request that may come and the lengths are known to
+// the device alone, so a grid of CTAs by the largest sizes would mostly be idle (64
+// requests behind a table of 131072 keys: 87 000 CTAs).  One CTA sums up the work
+// instead and deals it out:
+//  * the streaming kernel's rows, in pieces of equal length that make one wave of two
+//    CTAs per SM where the call is small, and pieces of 768 keys or more, taken from a
+//    queue, where it is large (the rule of the dense cache's decode);
+//  * the pair kernel's blocks, counted in closed form per request, cut into ranges.
+//    Tiles of one key head read the same keys, so ranges that run at the same time
+//    should lie close together: with more keys than the L2 cache holds, the
+//    blocks are dealt out in up to four rounds.
+
+#include "paged.cuh"
+#include "tc_common.cuh"
+
+namespace rf {
+namespace {
+
+constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int FEW_STEPS = 16;           // per CTA of a small call
+constexpr int MANY_STEPS = 12;          // of a large call's piece at least
+constexpr int MANY_UNITS = 8;           // and per CTA at most, on average
+constexpr int ROUND_BLOCKS = 32;        // of a range at least, where there are several rounds
+constexpr long long ROUND_KEYS = 98304; // keys of all key heads (512 bytes each) of a round
+
+struct Plan {
+  PagedShape s;
+  const int32_t *starts, *lens;
+  int* head;
+  PagedSeq* seqs;
+  long long* before;                    // [B + 1]: pair blocks of the requests before
+  PagedRange* ranges;
+  PagedUnit* units;
+  int* counters;
+  int unit_cap, range_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
+  uint32_t mark;
+};
+
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// exclusive prefix sum over the CTA; *total gets the sum
+__device__ __forceinline__ long long block_scan(long long x, long long* sm, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long s = warp_scan(x, lane);
+  if (lane == 31) sm[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    const long long p = warp_scan(sm[lane], lane);
+    __syncwarp();
+    sm[lane] = p;
+  }
+  __syncthreads();
+  const long long r = s - x + (warp > 0 ? sm[warp - 1] : 0);
+  *total = sm[WARPS - 1];
+  __syncthreads();
+  return r;
+}
+
+__device__ __forceinline__ int tiles_of(const PagedShape& s, const PagedSeq& q) {
+  return q.pair ? 0 : (q.n * s.G() + kPagedTileRows - 1) / kPagedTileRows;
+}
+__device__ __forceinline__ int steps_of(const PagedShape& s, const PagedSeq& q) {
+  const int n = PagedTiles(q.n, q.len, s.window, s.sinks).steps();
+  return n > 0 ? n : 1;                 // rows without keys need a CTA all the same
+}
+__device__ __forceinline__ int pieces_of(int steps, int piece) { return (steps + piece - 1) / piece; }
+
+__global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
+  __shared__ long long sm[WARPS], fit[WARPS];
+  const PagedShape& s = a.s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int groups = s.Hkv * (s.G() / s.packed());
+  wait_prerequisite();
+  allow_dependents();
+  long long steps = 0, blocks = 0, keys = 0;
+  for (int b0 = 0; b0 < s.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    PagedSeq q = {0, 0, 0, 0};
+    if (b < s.B && RF_SPAN_OK(b, 2, s.B + 1)) {
+      const int first = min(max(a.starts[b], 0), s.T), last = min(max(a.starts[b + 1], first), s.T);
+      q.start = first;
+      q.n = min(last - first, s.max_new);
+      q.len = min(max(a.lens[b], 0), s.max_len);
+      q.pair = (long long)q.n * s.G() > kPagedRows;
+    }
+    long long mine = 0, total;
+    if (q.pair) {
+      const PagedBlocks k(q.n, q.len, s.positions(), s.window, s.sinks);
+      mine = k.before(k.tiles()) * groups;
+    }
+    const long long at = block_scan(mine, sm, &total);
+    if (b < s.B) {
+      if (RF_IDX_OK(b, s.B)) a.seqs[b] = q;
+      if (RF_IDX_OK(b, s.B + 1)) a.before[b] = blocks + at;
+    }
+    blocks += total;
+    const long long st = q.n > 0 && !q.pair ? (long long)tiles_of(s, q) * steps_of(s, q) : 0;
+    block_scan(st, sm, &total);
+    steps += total;
+    block_scan(q.pair ? (long long)s.Hkv * min(q.len, s.window > 0 ? s.window + q.n : q.len) : 0, sm, &total);
+    keys += total;
+  }
+  if (tid == 0) a.before[s.B] = blocks;
+  __syncthreads();
+
+  // the streaming kernel's pieces: of candidates a 16th apart the smallest that fits one wave
+  const long long ctas = steps * s.Hkv;
+  long long piece = max(1ll, (ctas + a.slots - 1) / a.slots);
+  const bool few = piece <= FEW_STEPS;
+  if (few) {
+    const long long p = piece + (piece * warp + 15) / 16;
+    long long units = 0;
+    for (int b = lane; b < s.B; b += 32) {
+      const PagedSeq q = a.seqs[b];
+      if (q.n > 0 && !q.pair) units += (long long)tiles_of(s, q) * pieces_of(steps_of(s, q), (int)p);
+    }
+    units = warp_sum(units);
+    if (lane == 0) fit[warp] = units * s.Hkv <= a.slots ? p : 0;
+    __syncthreads();
+    long long best = 0;
+    for (int w = WARPS - 1; w >= 0; --w)
+      if (fit[w] > 0) best = fit[w];
+    if (best > 0) piece = best;
+  } else {
+    const long long most = (long long)MANY_UNITS * a.slots;
+    piece = max((long long)MANY_STEPS, (ctas + most - 1) / most);
+  }
+  // rows of up to two pieces stay whole in a large call, to save the merge
+  auto pieces = [&](int n) { return !few && n <= 2 * MANY_STEPS ? 1 : pieces_of(n, (int)piece); };
+  long long units = 0;
+  for (int b0 = 0; b0 < s.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    PagedSeq q = {0, 0, 0, 1};
+    if (b < s.B && RF_IDX_OK(b, s.B)) q = a.seqs[b];
+    int nt = 0, ns = 0, np = 0;
+    if (q.n > 0 && !q.pair) nt = tiles_of(s, q), ns = steps_of(s, q), np = pieces(ns);
+    long long total;
+    const long long at = units + block_scan((long long)nt * np, sm, &total);
+    // a warp writes the units of its 32 requests, one request after the other
+    for (int w = 0; w < 32; ++w) {
+      const int count = __shfl_sync(0xffffffffu, nt * np, w);
+      if (count == 0) continue;
+      const int n_p = __shfl_sync(0xffffffffu, np, w), n_s = __shfl_sync(0xffffffffu, ns, w);
+      const long long u0 = __shfl_sync(0xffffffffu, at, w);
+      const int start = __shfl_sync(0xffffffffu, q.start, w), rows = __shfl_sync(0xffffffffu, q.n, w);
+      const int len = __shfl_sync(0xffffffffu, q.len, w);
+      for (int u = lane; u < count; u += 32) {
+        const int tile = u / n_p, i = u - tile * n_p;
+        if (u0 + u >= a.unit_cap || !RF_IDX_OK(u0 + u, a.unit_cap)) break;
+        PagedUnit x;
+        x.b = b0 + (warp << 5) + w;
+        x.tile = tile;
+        x.step0 = (int)((long long)n_s * i / n_p);
+        x.step1 = (int)((long long)n_s * (i + 1) / n_p);
+        x.first = (int)(u0 + tile * n_p);
+        x.pieces = n_p;
+        x.start = start, x.n = rows, x.len = len;
+        x.pad[0] = x.pad[1] = x.pad[2] = 0;
+        a.units[u0 + u] = x;
+      }
+    }
+    units += total;
+  }
+  const int n_units = (int)min(units, (long long)a.unit_cap);
+  for (long long i = tid; i < (long long)n_units * s.Hkv; i += THREADS) a.counters[i] = 0;
+
+  // the pair kernel's ranges
+  int n_ranges = 0, active = 0;
+  if (blocks > 0 && a.clusters > 0) {
+    active = (int)min((long long)a.clusters, blocks);
+    long long rounds = (keys + ROUND_KEYS - 1) / ROUND_KEYS;
+    rounds = max(1ll, min(min(rounds, blocks / ((long long)active * ROUND_BLOCKS)), (long long)(a.range_cap / active)));
+    n_ranges = (int)rounds * active;
+    for (int i = tid; i < n_ranges; i += THREADS) {
+      const long long w = blocks / n_ranges * i + blocks % n_ranges * i / n_ranges;
+      const long long end = blocks / n_ranges * (i + 1) + blocks % n_ranges * (i + 1) / n_ranges;
+      int lo = 0, n = s.B;              // last request with before[b] <= w
+      while (n > 1) {
+        const int half = n >> 1;
+        if (a.before[lo + half] <= w) lo += half;
+        n -= half;
+      }
+      PagedRange r;
+      r.b = lo;
+      const PagedSeq q = a.seqs[lo];
+      const PagedBlocks k(q.n, q.len, s.positions(), s.window, s.sinks);
+      const int tiles = k.tiles();
+      const long long all = k.before(tiles);
+      long long rel = w - a.before[lo];
+      const int group = (int)(rel / all);
+      rel -= group * all;               // blocks of the group's tiles before, the last tile first
+      int t0 = 0, tn = tiles;           // the last count t of tiles with all - before(tiles - t) <= rel
+      while (tn > 1) {
+        const int half = tn >> 1;
+        if (all - k.before(tiles - (t0 + half)) <= rel) t0 += half;
+        tn -= half;
+      }
+      r.item = group * tiles + t0;
+      r.block = (int)(rel - (all - k.before(tiles - t0)));
+      r.count = (int)(end - w);
+      if (RF_IDX_OK(i, a.range_cap)) a.ranges[i] = r;
+    }
+  }
+  if (tid < kPlanWords) {
+    int x = 0;
+    if (tid == kPlanMark) x = (int)a.mark;
+    if (tid == kPlanUnits) x = n_units;
+    if (tid == kPlanRanges) x = n_ranges;
+    if (tid == kPlanClusters) x = active;
+    a.head[tid] = x;
+  }
+}
+
+}  // namespace
+
+bool paged_layout(const PagedShape& s, PagedLayout* l) {
+  const int sms = tc::sm_count();
+  if (sms <= 0) return false;
+  const auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  // units: a piece per tile, and what cutting adds (fewer than the pieces that the total makes)
+  const long long tiles = (long long)s.B * s.tiles();
+  const long long steps = ((long long)s.max_len + 4 * kDecodeTile - 1) / (4 * kDecodeTile) + 2;
+  long long cut = (2ll * sms * MANY_UNITS + s.Hkv - 1) / s.Hkv;
+  if (cut > tiles * (steps - 1)) cut = tiles * (steps - 1);
+  l->unit_cap = (int)(tiles + cut);
+  l->range_cap = 0;
+  if (s.some_pairs()) {
+    // blocks at most, and the rounds that they make
+    const long long groups = (long long)s.Hkv * (s.G() / s.packed());
+    const long long pair_tiles = (long long)s.T / s.positions() + s.B;
+    const long long blocks = groups * pair_tiles * ((long long)s.max_len / kPagedBlock + 2);
+    const int pairs = sms / 2;
+    long long rounds = blocks / ((long long)pairs * ROUND_BLOCKS);
+    rounds = rounds < 1 ? 1 : rounds > kPagedRounds ? kPagedRounds : rounds;
+    l->range_cap = (int)(rounds * pairs);
+  }
+  size_t at = align(kPlanWords * sizeof(int));
+  const auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at = align(at + bytes);
+    return p;
+  };
+  const size_t rows = (size_t)l->unit_cap * s.Hkv * s.unit_rows();
+  l->seqs = take((size_t)s.B * sizeof(PagedSeq));
+  l->before = take(((size_t)s.B + 1) * sizeof(long long));
+  l->ranges = take((size_t)l->range_cap * sizeof(PagedRange));
+  l->units = take((size_t)l->unit_cap * sizeof(PagedUnit));
+  l->counters = take((size_t)l->unit_cap * s.Hkv * sizeof(int));
+  l->unit_ml = take(rows * sizeof(float2));
+  l->unit_acc = take(rows * 128 * sizeof(float));
+  l->slots = take((size_t)2 * l->range_cap * kPagedSlotFloats * sizeof(float));
+  l->bytes = at;
+  uint32_t h = 0x9e3779b9u;             // FNV-like mixing of the sizes
+  for (const int x : {s.B, s.T, s.H, s.Hkv, s.max_new, s.max_len, s.window, s.sinks, sms})
+    h = (h ^ (uint32_t)x) * 0x01000193u + 0x7f4a7c15u;
+  l->mark = h;
+  return true;
+}
+
+rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const PagedShape& s, void* plan,
+                            cudaStream_t st) {
+  PagedLayout l;
+  const int sms = tc::sm_count();
+  if (sms <= 0 || !paged_layout(s, &l)) return RF_ERR_CUDA;
+  uint8_t* p = static_cast<uint8_t*>(plan);
+  Plan a = {};
+  a.s = s;
+  a.starts = starts, a.lens = lens;
+  a.head = reinterpret_cast<int*>(p);
+  a.seqs = reinterpret_cast<PagedSeq*>(p + l.seqs);
+  a.before = reinterpret_cast<long long*>(p + l.before);
+  a.ranges = reinterpret_cast<PagedRange*>(p + l.ranges);
+  a.units = reinterpret_cast<PagedUnit*>(p + l.units);
+  a.counters = reinterpret_cast<int*>(p + l.counters);
+  a.unit_cap = l.unit_cap, a.range_cap = l.range_cap;
+  a.clusters = 0;
+  if (s.some_pairs()) {
+    a.clusters = paged_pairs();
+    if (a.clusters <= 0) return RF_ERR_UNSUPPORTED;
+    if (a.clusters > sms / 2) a.clusters = sms / 2;
+  }
+  a.slots = 2 * sms;
+  a.mark = l.mark;
+  return launch_after(plan_kernel, 1, THREADS, 0, st, a);
+}
+
+RF_BOUNDS_WORD_OF_THIS_FILE
+
+}  // namespace rf

@@ -1,0 +1,555 @@
+// Attention of many new tokens per request over a paged cache: chunks of prompts and
+// whole ones, on CTA pairs (the kernel's body is in attn_pair.cuh).
+//
+// Mathematics: the windowed prefill's cascade, for packed rows of requests that each have
+// a length and a number of new tokens of their own, over keys that lie in pages.
+//
+// What bounds it: the tensor pipe, 4 D flops per pair of row and key.  A tile is 256 query
+// rows on one key head: up to 8 of the query heads that share it and 256 / heads adjacent
+// positions.  It visits the 256-key blocks that its rows see, last block first.
+//
+// Pages: a block's pages are copied one by one, a lane of the copying warp each, from a
+// map of [pages * Hkv][page][128] whose boxes are one page of 64 columns.  Rows behind a
+// request's end must not be read, NaN among them would reach every row (0 * NaN); a
+// box has no shorter form, but one that starts above its page fills what lies outside
+// with zeros.  So the last page is copied from row m - page on for the m rows in use,
+// they end up at the end of the page's place in the block, and the mask counts from
+// there.  Pages behind the last, and numbers outside the cache, are copied from
+// outside the map: zeros.
+//
+// Balance: requests differ in length by orders, and a tile's work with its position.
+// All blocks of all tiles form one line, cut into equal ranges (paged_plan.cu).  A tile
+// that a cut divides leaves a state per part (O, m and l of 256 rows, 130 KiB), and
+// paged_finish_kernel joins them; the others are written as they are.
+//
+// Values that are not finite: as in the windowed prefill a weight of 0 times NaN reaches
+// rows that do not see the value.  Rows whose output is not finite are noted, and
+// paged_finish_kernel computes their NaN columns again from the visible keys alone.
+
+#include <cuda_fp16.h>
+
+#include "attn_pair.cuh"
+#include "paged.cuh"
+
+namespace rf {
+namespace {
+
+using pair::BM;
+using pair::BN;
+using pair::HALF_BYTES;
+using pair::HD;
+static_assert(2 * BM == kPagedPairRows && BN == kPagedBlock && HD == 128, "the plan's sizes");
+
+// The items of a range, one after the other: tiles, or what of a tile the range holds.
+struct RangeItem {
+  int rho, left;       // range, and its blocks behind this item
+  int b, m;            // request, tile (head group major, last positions first)
+  int j0, n, next;     // first block of the tile, blocks, the block after them (0: no more)
+  int slot;            // of the partial state, -1 for a whole tile
+  int start, rows, len;           // the request
+  int head, kvh, row0;            // first query head, key head, first new token of the tile
+  int hb, nw;          // window blocks hb - 1, hb - 2 .. (nw of them), then those of the sinks from 0 on
+};
+
+__device__ __forceinline__ void place_item(const PagedView& v, bool first, int j, RangeItem& it) {
+  const PagedShape& s = v.s;
+  const int G = s.G(), packed = s.packed();
+  const PagedBlocks k(it.rows, it.len, s.positions(), s.window, s.sinks);
+  const int tiles = k.tiles(), group = it.m / tiles, i = tiles - 1 - (it.m - group * tiles);
+  it.head = group * packed;
+  it.kvh = it.head / G;
+  it.row0 = i * s.positions();
+  it.hb = k.hb(i);
+  it.nw = it.hb - k.lb(i);
+  const int all = it.nw + k.sink_blocks(i);
+  it.j0 = j;
+  it.n = min(all - j, it.left);
+  it.left -= it.n;
+  it.next = j + it.n == all ? 0 : j + it.n;
+  it.slot = it.n == all ? -1 : 2 * it.rho + (first ? 0 : 1);
+}
+__device__ __forceinline__ PagedSeq load_seq(const PagedView& v, int b) {
+  PagedSeq q = {0, 0, 0, 1};
+  if (RF_IDX_OK(b, v.s.B)) *reinterpret_cast<int4*>(&q) = *reinterpret_cast<const int4*>(v.seqs + b);
+  return q;
+}
+__device__ __forceinline__ void first_item(const PagedView& v, int rho, RangeItem& it) {
+  PagedRange r = {0, 0, 0, 0};
+  if (RF_IDX_OK(rho, v.range_cap)) *reinterpret_cast<int4*>(&r) = *reinterpret_cast<const int4*>(v.ranges + rho);
+  const PagedSeq q = load_seq(v, r.b);
+  it.rho = rho, it.left = r.count, it.b = r.b, it.m = r.item;
+  it.start = q.start, it.rows = q.n, it.len = q.len;
+  place_item(v, true, r.block, it);
+}
+// the next item of the same range (left > 0)
+__device__ __forceinline__ void step_item(const PagedView& v, RangeItem& it) {
+  if (it.next == 0) {
+    const int P = v.s.positions();
+    if (++it.m == (it.rows + P - 1) / P * v.s.Hkv * (v.s.G() / v.s.packed())) {
+      PagedSeq q;
+      do {
+        q = load_seq(v, ++it.b);
+      } while (!q.pair);
+      it.m = 0;
+      it.start = q.start, it.rows = q.n, it.len = q.len;
+    }
+  }
+  place_item(v, false, it.next, it);
+}
+
+template <bool F16_>
+struct PagedPrefill {
+  static constexpr bool F16 = F16_;
+  static constexpr bool CHAINED = true, PARTIAL = true, STAGED = true;
+  static constexpr float M_START = -1e30f;
+  using Item = RangeItem;
+  struct Pages {
+    int kx, ky, kz, kat;          // coordinates and the place in the half; kat < 0: no copy
+    int vy, vz, vat;
+  };
+  struct Pending {
+    int row, head;
+    bool in, full;                // the row is one of the tile's, all 32 of the warp are
+  };
+
+  PagedAttn a;
+  float scale_log2;
+
+  __device__ __forceinline__ bool item(int t, int cluster, Item& it) const {
+    if (t > 0 && it.left > 0) {
+      step_item(a.v, it);
+      return true;
+    }
+    if (a.v.head[kPlanMark] != (int)a.v.mark) return false;
+    const int clusters = a.v.head[kPlanClusters], ranges = min(a.v.head[kPlanRanges], a.v.range_cap);
+    const int rho = t == 0 ? cluster : it.rho + clusters;
+    if (cluster >= clusters || rho >= ranges) return false;
+    first_item(a.v, rho, it);
+    return true;
+  }
+  // the block of keys that is the item's j-th
+  __device__ __forceinline__ int block_of(const Item& it, int j) const {
+    const int J = it.j0 + j;
+    return J < it.nw ? it.hb - 1 - J : J - it.nw;
+  }
+  __device__ __forceinline__ int page() const { return 1 << a.page_log2; }
+  // rows that the last page lacks, and whether the block holds that page
+  __device__ __forceinline__ int lacking(const Item& it) const { return -it.len & (page() - 1); }
+  __device__ __forceinline__ bool holds_last(const Item& it, int block) const {
+    return it.len > 0 && (it.len - 1) / BN == block;
+  }
+  __device__ __forceinline__ int head_of(int rank, int r) const { return (rank * BM + r) / a.v.s.positions(); }
+  __device__ __forceinline__ int row_of(int rank, int r) const {
+    return (rank * BM + r) & (a.v.s.positions() - 1);
+  }
+
+  __device__ __forceinline__ uint32_t q_bytes() const { return pair::TILE_BYTES; }
+  __device__ __forceinline__ void load_q(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Item& it,
+                                         int rank) const {
+    const int row = it.start + it.row0 + row_of(rank, 0), head = it.head + head_of(rank, 0);
+    tc::tma_load_3d_pair(dst, map, bar, 0, row, head);
+    tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, row, head);
+  }
+  // coordinates (y, z) of page i of the item's request; zeros come from behind the map
+  __device__ __forceinline__ void find_page(const Item& it, int i, int& y, int& z) const {
+    const int used = (it.len + page() - 1) >> a.page_log2;
+    const size_t at = (size_t)it.b * a.width + i;
+    int id = -1;
+    if (i < used && i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width)) id = a.table[at];
+    const bool in = (unsigned)id < (unsigned)a.pages;
+    z = in ? id * a.v.s.Hkv + it.kvh : a.pages * a.v.s.Hkv;
+    y = i == used - 1 ? -lacking(it) : 0;
+  }
+  // A half of K is 128 keys in two boxes of 64 columns per page (page <= 128), V all 256 in
+  // one; of a page of 256 a half of K is 128 rows.
+  __device__ __forceinline__ Pages pages_of(const Item& it, int j, int rank, int lane) const {
+    Pages p = {0, 0, 0, -1, 0, 0, -1};
+    const int first = block_of(it, j) * BN >> a.page_log2;
+    const int nk = max(1, BM >> a.page_log2), nv = BN >> a.page_log2;
+    if (lane < 2 * nk) {
+      const int col = lane >= nk, i = lane - col * nk;
+      find_page(it, first + (page() > BM ? 0 : rank * nk + i), p.ky, p.kz);
+      if (page() > BM) p.ky += rank * BM;
+      p.kx = 64 * col;
+      p.kat = col * HALF_BYTES + i * page() * 128;
+    }
+    if (lane < nv) {
+      find_page(it, first + lane, p.vy, p.vz);
+      p.vat = lane * page() * 128;
+    }
+    return p;
+  }
+  __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Pages& p,
+                                         int, int) const {
+    if (p.kat >= 0) tc::tma_load_3d_pair(dst + p.kat, map, bar, p.kx, p.ky, p.kz);
+  }
+  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Pages& p,
+                                         int rank, int) const {
+    if (p.vat >= 0) tc::tma_load_3d_pair(dst + p.vat, map, bar, rank * 64, p.vy, p.vz);
+  }
+  __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
+
+  static __device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  }
+  __device__ __forceinline__ bool sees(const Item& it, int j, int rank, int r, int kh) const {
+    const int block = block_of(it, j), base = block * BN + kh * BM;
+    const int first = it.len - it.rows + it.row0 + row_of(rank, r & ~31), last = first + 31;
+    const int window = a.v.s.window;
+    if (page() > BM && holds_last(it, block)) return true;       // its keys have moved between the halves
+    return last >= base && (window == 0 || first - window + 1 < base + BM || a.v.s.sinks > base);
+  }
+  __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh, float (&s)[128]) const {
+    const int block = block_of(it, j), base = block * BN + kh * BM;
+    const int p = it.len - it.rows + it.row0 + row_of(rank, r);   // this row's position
+    const int first = p - (r & 31), last = first + 31;
+    const int window = a.v.s.window;
+    const bool moved = holds_last(it, block) && lacking(it) != 0;
+    if (!moved && first - base >= BM - 1 && (window == 0 || last - window + 1 <= base)) return;
+    // visible are keys up to hi, from lo on or below cs, counted from base; where the last
+    // page moved by d, slots c0 + d .. of its place are keys c - d
+    const int hi = min(p, it.len - 1) - base, lo = window > 0 ? p - window + 1 - base : -2 * BN;
+    const int cs = a.v.s.sinks - base;
+    const int d = moved ? lacking(it) : 0;
+    const int c0 = moved ? ((it.len - 1) & ~(page() - 1)) - base : BN;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t vis = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));
+      if (moved) {
+        const uint32_t in = below(hi + d + 1 - 32 * q) & (~below(lo + d - 32 * q) | below(cs + d - 32 * q));
+        vis = (vis & below(c0 - 32 * q)) | (in & ~below(c0 + d - 32 * q));
+      }
+      if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!(vis & (1u << c))) s[32 * q + c] = -INFINITY;
+      }
+    }
+  }
+
+  __device__ __forceinline__ bool partial(const Item& it) const { return it.slot >= 0; }
+  __device__ __forceinline__ void keep(const Item& it, int rank, int r, int col, const uint32_t (&v)[32],
+                                       float m, float lt) const {
+    if (!RF_IDX_OK(it.slot, 2 * a.v.range_cap)) return;
+    float* slot = a.v.slots + (size_t)it.slot * kPagedSlotFloats;
+    const int row = rank * BM + r;
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) pair::st_global_v8(slot + row * HD + col + c, v + c);
+    if (col == 0) {
+      slot[kPagedPairRows * HD + row] = m;
+      slot[kPagedPairRows * (HD + 1) + row] = lt;
+    }
+  }
+  __device__ __forceinline__ Pending pending(const Item& it, int rank, int r) const {
+    const int i = it.row0 + row_of(rank, r);
+    return {it.start + i, it.head + head_of(rank, r), i < it.rows, (i | 31) < it.rows};
+  }
+  __device__ __forceinline__ bool boxed(const Pending& pend) const { return pend.full; }
+  __device__ __forceinline__ bool pack(const Pending& pend, int col, const uint32_t (&v)[32], float m, float lt,
+                                       uint32_t (&w)[16]) const {
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;       // 0: a row that sees nothing
+    const uint64_t inv2 = pair::pack_f32x2(inv, inv);
+    uint64_t probe = 0ull;                              // NaN if a value is not finite
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint64_t x = pair::mul_f32x2(
+          pair::pack_f32x2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), inv2);
+      probe = pair::fma_f32x2(x, 0ull, probe);
+      float x0, x1;
+      pair::unpack_f32x2(x, x0, x1);
+      w[c] = pair::pack_16x2<F16>(x0, x1);
+    }
+    const size_t row = (size_t)pend.row * a.v.s.H + pend.head;
+    if (pend.in && RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) {
+      if (a.lse != nullptr && col == 0) a.lse[row] = (m + log2f(lt)) * kLn2;
+      if (!pend.full) pair::st_row32(a.out + (row * HD + col) * 2, w, false);
+    }
+    float p0, p1;
+    pair::unpack_f32x2(probe, p0, p1);
+    return pend.in && !(p0 == 0.f && p1 == 0.f);
+  }
+  // called by the warp's first lane, whose row is the boxes' first
+  __device__ __forceinline__ void send(const CUtensorMap* map, const uint8_t* box, const Pending& pend) const {
+    tc::tma_store_3d(map, box, 0, pend.row, pend.head);
+    tc::tma_store_3d(map, box + HALF_BYTES, 64, pend.row, pend.head);
+  }
+  __device__ __forceinline__ void after(bool any, int, int, int, int) const {
+    if (any) atomicOr(a.v.head + kPlanFlag, 1);
+  }
+};
+
+template <class P>
+__global__ void __launch_bounds__(pair::THREADS, 1)
+paged_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                  const __grid_constant__ P p) {
+  pair::attn_pair_body(tmQ, tmK, tmV, tmV, tmO, p);
+}
+
+// ------------------------------------------------------------------ finish --
+
+constexpr int FIN_WARPS = 4, FIN_ROWS = 32, FIN_PARTS = kPagedPairRows / FIN_ROWS;
+
+template <bool F16>
+__device__ __forceinline__ float4 widen4(const uint8_t* row, int lane) {
+  const uint2 u = *reinterpret_cast<const uint2*>(row + lane * 8);
+  if constexpr (F16) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(x.x, x.y, y.x, y.y);
+  } else {
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  }
+}
+
+// Columns of a row that are NaN (bits of `todo`, four per lane), once more from the keys
+// that the row sees.  Ends once they are all NaN again.  Gives the row's sum and maximum too
+// (in log2 units), where it went through all of its keys.
+template <bool F16>
+__device__ __noinline__ float4 redo_row(const PagedAttn& a, const RangeItem it, int i, int head, uint32_t todo,
+                                        float4 y, float* lse2, int lane) {
+  constexpr int U = 8;                                // keys in flight
+  const int p = it.len - it.rows + i, window = a.v.s.window, page = 1 << a.page_log2;
+  const int last = min(p, it.len - 1);
+  const int lo = window > 0 ? max(0, p - window + 1) : 0, ns = min(a.v.s.sinks, lo);
+  const int n = last < 0 ? 0 : min(ns, last + 1) + max(0, last - lo + 1);
+  const size_t row = (size_t)(it.start + i) * a.v.s.H + head;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) x = widen4<F16>(a.q + row * HD * 2, lane);
+  float m = -INFINITY, l = 0.f;
+  float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool gone = false;
+  for (int t0 = 0; !gone && t0 < n; t0 += U) {
+    float s[U], mn = m;
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = min(t0 + u, n - 1), key = t < ns ? t : t - ns + lo, pi = key >> a.page_log2;
+      const size_t e = (size_t)it.b * a.width + pi;
+      const int id = pi < a.width && RF_IDX_OK(e, (size_t)a.v.s.B * a.width) ? a.table[e] : -1;
+      float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = k;
+      if ((unsigned)id < (unsigned)a.pages) {
+        const size_t at = (((size_t)id * a.v.s.Hkv + it.kvh) << a.page_log2) + (key & (page - 1));
+        if (RF_IDX_OK(at, ((size_t)a.pages * a.v.s.Hkv) << a.page_log2)) {
+          k = widen4<F16>(a.kp + at * HD * 2, lane);
+          v[u] = widen4<F16>(a.vp + at * HD * 2, lane);
+        }
+      }
+      s[u] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, x.w * k.w)));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] = t0 + u < n ? group_sum<32>(s[u]) * a.scale_log2 : -INFINITY;
+      mn = fmaxf(mn, s[u]);
+    }
+    const float ref = ref_of(mn), corr = exp2f(m - ref);
+    m = mn;
+    l *= corr;
+    R.x *= corr, R.y *= corr, R.z *= corr, R.w *= corr;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t0 + u >= n) break;
+      const float w = exp2f(s[u] - ref);
+      l += w;
+      R.x = fmaf(w, v[u].x, R.x);
+      R.y = fmaf(w, v[u].y, R.y);
+      R.z = fmaf(w, v[u].z, R.z);
+      R.w = fmaf(w, v[u].w, R.w);
+    }
+    const uint32_t now = (R.x != R.x) | (R.y != R.y) << 1 | (R.z != R.z) << 2 | (R.w != R.w) << 3;
+    gone = !__any_sync(0xffffffffu, (todo & ~now) != 0);
+  }
+  if (gone) return y;
+  *lse2 = m + log2f(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;         // 0: every visible score is -inf
+  if (l == 0.f) R = make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(todo & 1u ? R.x * inv : y.x, todo & 2u ? R.y * inv : y.y, todo & 4u ? R.z * inv : y.z,
+                     todo & 8u ? R.w * inv : y.w);
+}
+
+__device__ __forceinline__ uint32_t nan_of(const float4& y) {
+  return (y.x != y.x) | (y.y != y.y) << 1 | (y.z != y.z) << 2 | (y.w != y.w) << 3;
+}
+
+// A CTA per range and 32 of a tile's 256 rows.  First it joins the parts of the tile that the
+// range's start cut, if that was the tile's first cut; then, where the pair kernel noted
+// a value that is not finite, it looks at the whole tiles of the range.
+template <bool F16>
+__global__ void __launch_bounds__(FIN_WARPS * 32)
+paged_finish_kernel(const __grid_constant__ PagedAttn a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rho = (int)(blockIdx.x / FIN_PARTS), part = (int)(blockIdx.x % FIN_PARTS);
+  wait_prerequisite();
+  allow_dependents();
+  const PagedView& v = a.v;
+  if (v.head[kPlanMark] != (int)v.mark) return;
+  const int ranges = min(v.head[kPlanRanges], v.range_cap), flag = v.head[kPlanFlag];
+  const int P = v.s.positions();
+  const size_t all_rows = (size_t)v.s.T * v.s.H;
+  (void)all_rows;                                     // read by the checked build only
+  auto range = [&](int i) {
+    PagedRange r = {0, 0, 0, 0};
+    if (RF_IDX_OK(i, v.range_cap)) *reinterpret_cast<int4*>(&r) = *reinterpret_cast<const int4*>(v.ranges + i);
+    return r;
+  };
+  if (rho > 0 && rho < ranges) {
+    const PagedRange r = range(rho), before = range(rho - 1);
+    const bool same = before.b == r.b && before.item == r.item;
+    if (r.block > 0 && !(same && before.block > 0)) {
+      // the tile's parts: the last of the range before, then the first of each range that
+      // starts inside the tile
+      int parts = 2;
+      while (rho + parts - 1 < ranges) {
+        const PagedRange x = range(rho + parts - 1);
+        if (x.b != r.b || x.item != r.item || x.block == 0) break;
+        ++parts;
+      }
+      const int slot0 = 2 * (rho - 1) + (same ? 0 : 1);
+      RangeItem it;
+      first_item(v, rho, it);
+      constexpr int R = FIN_ROWS / FIN_WARPS;         // rows of a warp
+      const int row0 = part * FIN_ROWS + warp * R;    // of the tile
+      float M[R], L[R];
+      float4 A[R];
+#pragma unroll
+      for (int q = 0; q < R; ++q) M[q] = -INFINITY, L[q] = 0.f, A[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < parts; ++x) {
+        const int slot = x == 0 ? slot0 : 2 * (rho + x - 1);
+        if (!RF_IDX_OK(slot, 2 * v.range_cap)) break;
+        const float* at = v.slots + (size_t)slot * kPagedSlotFloats;
+        float4 o[R];
+        float m[R], l[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          o[q] = __ldcg(reinterpret_cast<const float4*>(at + (row0 + q) * HD) + lane);
+          m[q] = __ldcg(at + kPagedPairRows * HD + row0 + q);
+          l[q] = __ldcg(at + kPagedPairRows * (HD + 1) + row0 + q);
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          if (l[q] == 0.f) continue;                  // the part holds nothing that the row sees
+          const float top = fmaxf(M[q], m[q]), c = exp2f(M[q] - top), f = exp2f(m[q] - top);
+          M[q] = top;
+          L[q] = L[q] * c + l[q] * f;
+          A[q].x = A[q].x * c + o[q].x * f;
+          A[q].y = A[q].y * c + o[q].y * f;
+          A[q].z = A[q].z * c + o[q].z * f;
+          A[q].w = A[q].w * c + o[q].w * f;
+        }
+      }
+#pragma unroll 1
+      for (int q = 0; q < R; ++q) {
+        const int i = it.row0 + ((row0 + q) & (P - 1)), head = it.head + (row0 + q) / P;
+        if (i >= it.rows) continue;
+        // registers indexed by q: picked without an array in memory
+        float4 y = A[0];
+        float mq = M[0], lq = L[0];
+#pragma unroll
+        for (int e = 1; e < R; ++e)
+          if (e == q) y = A[e], mq = M[e], lq = L[e];
+        const float inv = lq == 0.f ? 0.f : 1.f / lq;
+        y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        float lse2 = mq + log2f(lq);
+        const uint32_t todo = nan_of(y);
+        if (__any_sync(0xffffffffu, todo != 0)) y = redo_row<F16>(a, it, i, head, todo, y, &lse2, lane);
+        const size_t row = (size_t)(it.start + i) * v.s.H + head;
+        if (!RF_IDX_OK(row, all_rows)) continue;
+        *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
+            make_uint2(pair::pack_16x2<F16>(y.x, y.y), pair::pack_16x2<F16>(y.z, y.w));
+        if (lane == 0 && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
+      }
+    }
+  }
+  if (flag == 0) return;
+  if (rho < ranges) {
+    RangeItem it;
+    first_item(v, rho, it);
+    for (;;) {
+      for (int q = warp; it.slot < 0 && q < FIN_ROWS; q += FIN_WARPS) {
+        const int t = part * FIN_ROWS + q, i = it.row0 + (t & (P - 1)), head = it.head + t / P;
+        const size_t row = (size_t)(it.start + i) * v.s.H + head;
+        if (i >= it.rows || !RF_IDX_OK(row, all_rows)) continue;
+        const float4 y = widen4<F16>(a.out + row * HD * 2, lane);
+        const uint32_t todo = nan_of(y);
+        if (!__any_sync(0xffffffffu, todo != 0)) continue;
+        float lse2 = NAN;
+        const float4 z = redo_row<F16>(a, it, i, head, todo, y, &lse2, lane);
+        *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
+            make_uint2(pair::pack_16x2<F16>(z.x, z.y), pair::pack_16x2<F16>(z.z, z.w));
+        // masked scores never entered the lse in place, but weights that all vanished
+        // against the reference that the row started from left it at -inf
+        if (lane == 0 && a.lse != nullptr && a.lse[row] == -INFINITY && lse2 == lse2) a.lse[row] = lse2 * kLn2;
+      }
+      if (it.left == 0) break;
+      step_item(v, it);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // the last CTA that has looked takes the note away
+    if (atomicInc(reinterpret_cast<unsigned*>(v.head) + kPlanDone, gridDim.x - 1) == gridDim.x - 1)
+      atomicExch(v.head + kPlanFlag, 0);
+  }
+}
+
+// a map of [outer][mid][128] 16-bit values with strides in bytes
+bool make_map(CUtensorMap* map, bool f16, const void* base, uint64_t mid, uint64_t outer, uint64_t mid_step,
+              uint64_t outer_step, uint32_t box_mid, uint32_t box_outer) {
+  return tc::make_tmap_3d_16_strided(map, f16, base, HD, mid, outer, mid_step, outer_step, 64, box_mid, box_outer,
+                                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool F16>
+rf_status launch_pairs(const PagedAttn& a, cudaStream_t st) {
+  using P = PagedPrefill<F16>;
+  auto* kernel = paged_pair_kernel<P>;
+  const int pairs = pair::resident_pairs_of<P>(kernel);
+  if (pairs <= 0) return RF_ERR_UNSUPPORTED;
+  const PagedShape& s = a.v.s;
+  const uint64_t row = (uint64_t)HD * 2, page = 1ull << a.page_log2;
+  const uint32_t box = s.positions() < BM ? s.positions() : BM;
+  CUtensorMap tq, tk, tv, to;
+  if (!make_map(&tq, F16, a.q, s.T, s.H, row * s.H, row, box, BM / box) ||
+      !make_map(&tk, F16, a.kp, page, (uint64_t)a.pages * s.Hkv, row, row * page,
+                (uint32_t)(page < BM ? page : BM), 1) ||
+      !make_map(&tv, F16, a.vp, page, (uint64_t)a.pages * s.Hkv, row, row * page, (uint32_t)page, 1) ||
+      !make_map(&to, F16, a.out, s.T, s.H, row * s.H, row, 32, 1))
+    return RF_ERR_CUDA;
+  P p = {};
+  p.a = a;
+  p.scale_log2 = a.scale_log2;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pair::pair_config(attr, 2u * (unsigned)pairs, st);
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, to, p) != cudaSuccess) {
+    cudaGetLastError();
+    return RF_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+}  // namespace
+
+int paged_pairs() {
+  // both types have the same registers and shared memory; each launch checks its own
+  return pair::resident_pairs_of<PagedPrefill<false>>(paged_pair_kernel<PagedPrefill<false>>);
+}
+
+rf_status launch_paged_prefill(const PagedAttn& a, int dtype, cudaStream_t st) {
+  return dtype == RF_F16 ? launch_pairs<true>(a, st) : launch_pairs<false>(a, st);
+}
+
+rf_status launch_paged_finish(const PagedAttn& a, int dtype, cudaStream_t st) {
+  const unsigned grid = (unsigned)a.v.range_cap * FIN_PARTS;
+  return launch_after(dtype == RF_F16 ? paged_finish_kernel<true> : paged_finish_kernel<false>, grid,
+                      FIN_WARPS * 32, 0, st, a);
+}
+
+RF_TIMEOUT_WORD_OF_THIS_FILE
+
+RF_BOUNDS_WORD_OF_THIS_FILE
+
+}  // namespace rf

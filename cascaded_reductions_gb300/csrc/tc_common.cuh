@@ -513,6 +513,11 @@ bool make_tmap_3d_16(CUtensorMap* map, bool f16, const void* base, uint64_t inne
                      uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
                      CUtensorMapSwizzle swizzle);
 
+// the same with rows of `mid` and slices of `outer` mid_step and outer_step bytes apart
+bool make_tmap_3d_16_strided(CUtensorMap* map, bool f16, const void* base, uint64_t inner, uint64_t mid,
+                             uint64_t outer, uint64_t mid_step, uint64_t outer_step, uint32_t box_inner,
+                             uint32_t box_mid, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
 int sm_count();
 
 }  // namespace tc

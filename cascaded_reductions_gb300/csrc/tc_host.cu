@@ -32,9 +32,16 @@ bool have_encode() {
 bool make_tmap_3d_16(CUtensorMap* map, bool f16, const void* base, uint64_t inner, uint64_t mid,
                      uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
                      CUtensorMapSwizzle swizzle) {
+  return make_tmap_3d_16_strided(map, f16, base, inner, mid, outer, inner * 2, inner * mid * 2, box_inner,
+                                 box_mid, box_outer, swizzle);
+}
+
+bool make_tmap_3d_16_strided(CUtensorMap* map, bool f16, const void* base, uint64_t inner, uint64_t mid,
+                             uint64_t outer, uint64_t mid_step, uint64_t outer_step, uint32_t box_inner,
+                             uint32_t box_mid, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
   if (!have_encode()) return false;
   const cuuint64_t dims[3] = {inner, mid, outer};
-  const cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
+  const cuuint64_t strides[2] = {mid_step, outer_step};
   const cuuint32_t box[3] = {box_inner, box_mid, box_outer};
   const cuuint32_t elem_strides[3] = {1, 1, 1};
   return g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,

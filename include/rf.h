@@ -543,6 +543,58 @@ rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long l
                           int R, int interleaved, int dtype, const int32_t* slots, int pages, int page,
                           void* q_out, void* k_out, void* v_out, void* stream);
 
+/*
+ * rf_paged_plan -- the plan of a step: which part of the device reads which keys in
+ * rf_attn_paged, from the lengths on the device.  Made once per step; the calls of all
+ * layers take it.
+ *   starts   [B + 1], lens [B]: rows of each request's new tokens, and its keys with
+ *            them, as rf_page_tables writes them.  The new tokens stand at its end:
+ *            row starts[b] + i is position lens[b] - new + i.
+ *   T        rows of q; max_new, max_len: the most new tokens and keys of a request
+ *            (larger ones are cut to them; sizes, not values: a plan's memory goes by them)
+ *   window, sinks  as in the calls over a dense cache
+ *   plan     DEVICE memory, 256-byte aligned, rf_paged_plan_bytes of the same sizes
+ *            long (0: the sizes are not valid or there is no device).  It holds the
+ *            call's scratch too: calls that may overlap on the GPU need plans of their
+ *            own, and a plan is made again only when the calls over it are done.
+ * The lengths are read here alone; what the calls do goes by the plan.
+ * Errors: RF_ERR_INVALID_ARG for null pointers, sizes <= 0, H % Hkv != 0, max_new > T,
+ * window or sinks < 0, or too few bytes; RF_ERR_UNSUPPORTED for max_len > 2^30, T * H
+ * beyond 2^31 - 1, B > 2^20, H > 2^16, more than 2^29 tiles of 16 rows, or a device that
+ * cannot hold a cluster of two CTAs with about 200 KiB of shared memory each (where
+ * max_new * H / Hkv > 64); RF_ERR_MISALIGNED for the plan.
+ */
+size_t rf_paged_plan_bytes(int B, int T, int H, int Hkv, int max_new, int max_len, int window, int sinks);
+rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T, int H, int Hkv,
+                        int max_new, int max_len, int window, int sinks, void* plan, size_t bytes,
+                        void* stream);
+
+/*
+ * rf_attn_paged -- attention of the new tokens of a batch of requests over their pages:
+ * single tokens, a few drafted ones, chunks of prompts and whole prompts, mixed as they
+ * come.  Row starts[b] + i sees the keys up to its position, with window and sinks as in
+ * the calls over a dense cache; a row without a visible key, or whose visible scores are
+ * all -inf, gets out = 0 and lse = -inf.
+ *   q [T, H, D];  kp, vp [pages, Hkv, page, D];  table [B, width] with width * page >= max_len
+ *   plan, bytes and the sizes as for rf_paged_plan.  A plan made for other sizes is not
+ *               used: the call then writes nothing
+ *   out [T, H, D] of q's type, lse [T, H] fp32 or NULL.  Rows of no request (behind
+ *               starts[B], or between a start and the rows before it) are left as they were
+ * Rows of a page behind a request's end are never read; a page number outside the cache
+ * reads as keys and values of zero.  A key or value that is not finite reaches only the rows
+ * that see it.  Requests with up to 64 rows per key head (new tokens * H / Hkv) run as
+ * rf_attn_decode_window does (weights not rounded to 16 bits), so a row's last bits
+ * may depend on how many tokens come with it.  One launch, three where max_new * H / Hkv > 64.
+ * Errors: as rf_paged_plan, RF_ERR_INVALID_ARG for width * page < max_len, a non-finite scale
+ * or a bad dtype; RF_ERR_UNSUPPORTED for D != 128, RF_F32, scale <= 0, a page that is not 16,
+ * 32, 64, 128 or 256, pages * Hkv >= 2^30 or B * width >= 2^31; RF_ERR_MISALIGNED unless q, kp,
+ * vp and out are 16-byte aligned.
+ */
+rf_status rf_attn_paged(const void* q, const void* kp, const void* vp, int pages, int page,
+                        const int32_t* table, int width, void* plan, size_t bytes, int B, int T, int H,
+                        int Hkv, int D, int max_new, int max_len, int window, int sinks, float scale,
+                        int dtype, void* out, float* lse, void* stream);
+
 /* Phase 1 of rf_absmax_quant_fp8_gemm alone (same arguments and rules;
  * any K % 8 == 0 is supported). */
 rf_status rf_absmax_quant_e4m3(const void* x, int M, int K, uint8_t* xq, float* sx,
