@@ -371,7 +371,7 @@ def run(state):
         if c["op"] == "tables":
             starts, positions, slots, lens, n_free = rf.page_tables(
                 st["lens"], st["news"], st["table"], st["stack"], st["n_free"], c["page"], st["tokens"])
-            return starts, positions, slots, lens, n_free[0], st["table"], st["stack"]
+            return starts, positions, slots, lens, n_free, st["table"], st["stack"]
         if c["op"] == "rope":
             if c["page"]:
                 q = rf.qk_norm_rope(st["q"], st["k"], st["positions"], st["freq"], st["qw"], st["kw"],
