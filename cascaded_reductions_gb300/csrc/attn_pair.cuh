@@ -143,6 +143,7 @@ struct Shared {
   float red[2][2][BM];          // [exchange & 1][key half][row]: partial row maxima
   float part_l[2][2][BM];       // [item & 1][key half][row]: partial row sums of an item
   float row_m[2][BM];           // [item & 1][row]: its reference maxima
+  int items[18][16];            // of a paged policy: an item per warp, and the MMA thread's next
   uint32_t tmem_base;
   int abort;
 };
@@ -212,9 +213,12 @@ __device__ __forceinline__ void st_row32(void* dst, const uint32_t (&w)[16], boo
 // Whether a policy's keys lie in pages.  Such a one differs from the others so:
 //   item(t, c, it)             steps `it` on to the cluster's next item (t = 0: the first)
 //   Pages, pages_of(it, j, rank, lane)  what a lane copies of block j, and
-//   load_k / load_v(..., pages, rank, lane)  its copies; no tmW, v_bytes or narrow blocks
+//   load_k / load_v(..., it, pages, rank, lane)  its copies; no tmW, v_bytes or narrow blocks
 //   partial(it), keep(it, rank, row, col, v, m, l)  whether the item is a part of a tile's
 //                              blocks, and then, instead of pack and send, its state
+//   Row, row_of_item(it, rank, row, kh)  of an item, for a softmax thread: which blocks hide
+//                              nothing from its warp (Row::all(j)); sees() and mask() take it
+//                              for the others
 //   boxed(pending)             whether the warp's 32 rows leave by send(); else pack has
 //                              stored the columns
 template <class P, class = void>
@@ -229,8 +233,46 @@ template <class P>
 constexpr __host__ __device__ bool is_paged() {
   return Paged<P>::value;
 }
+// Where a role keeps its item: `mine`, or, for a paged policy, whose items have more
+// fields than the roles have registers to spare, in shared memory, written by lane 0.
+template <class P, class = void>
+struct RowOfPolicy {
+  struct type {};
+};
 template <class P>
-__device__ __forceinline__ bool next_item(const P& p, int t, int cluster, int nclusters, typename P::Item& it) {
+struct RowOfPolicy<P, decltype((void)sizeof(typename P::Row))> {
+  using type = typename P::Row;
+};
+template <class P>
+using RowOf = typename RowOfPolicy<P>::type;
+
+template <class P>
+__device__ __forceinline__ typename P::Item& item_at(Shared* sh, int i, typename P::Item& mine) {
+  if constexpr (is_paged<P>()) {
+    static_assert(sizeof(mine) <= sizeof(sh->items[0]), "an item's place");
+    return *reinterpret_cast<typename P::Item*>(sh->items[i]);
+  } else {
+    return mine;
+  }
+}
+// all lanes of a warp
+template <class P>
+__device__ __forceinline__ bool next_item(const P& p, int t, int cluster, int nclusters, int lane,
+                                          typename P::Item& it) {
+  if constexpr (is_paged<P>()) {
+    int more = 0;
+    __syncwarp();                     // no lane reads the last item any more
+    if (lane == 0) more = p.item(t, cluster, it);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, more, 0) != 0;
+  } else {
+    return p.item(t, cluster, nclusters, it);
+  }
+}
+// one thread
+template <class P>
+__device__ __forceinline__ bool next_item_alone(const P& p, int t, int cluster, int nclusters,
+                                                typename P::Item& it) {
   if constexpr (is_paged<P>())
     return p.item(t, cluster, it);
   else
@@ -329,10 +371,13 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
     const uint64_t sl2 = pack_f32x2(scale_log2, scale_log2);
     uint32_t g = 0, x = 0;                          // blocks and red_bar exchanges so far
     bool ok = true;
-    typename P::Item it;
+    typename P::Item mine;
+    typename P::Item& it = item_at<P>(sh, warp, mine);
     for (int t = 0; ok; ++t) {
-      if (!next_item(p, t, cluster, nclusters, it)) break;
+      if (!next_item(p, t, cluster, nclusters, lane, it)) break;
       float m_ref = P::M_START, l = 0.f;
+      RowOf<P> row;
+      if constexpr (is_paged<P>()) row = p.row_of_item(it, rank, r, kh);
       // One block, of which this warp's rows see some of its 128 keys (NW = 4
       // 32-key words) or none (NW = 0); false if a wait gave up.
       auto block = [&](auto words, int j) -> bool {
@@ -353,7 +398,11 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         if (lane == 0) arrive_cluster_relaxed(s_free0);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if constexpr (NW > 0) {
-          p.mask(it, j, rank, r, kh, s);
+          if constexpr (is_paged<P>()) {
+            if (!row.all(j)) p.mask(it, row, j, r, kh, s);
+          } else {
+            p.mask(it, j, rank, r, kh, s);
+          }
 #pragma unroll
           for (int c = 0; c < 32 * NW; c += 2)
             mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], s[c], s[c + 1]);
@@ -427,9 +476,14 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         if (lane == 0) arrive_cluster_relaxed(p_ready0);
         return true;
       };
-      for (int j = 0; ok && j < it.n; ++j, ++g) {
+      const int blocks = it.n;
+      for (int j = 0; ok && j < blocks; ++j, ++g) {
         if constexpr (P::PARTIAL) {
-          const bool some = p.sees(it, j, rank, r, kh);
+          bool some;
+          if constexpr (is_paged<P>())
+            some = row.all(j) || p.sees(it, row, j, r, kh);
+          else
+            some = p.sees(it, j, rank, r, kh);
           ok = some ? block(Words<4>{}, j) : block(Words<0>{}, j);
         } else {
           ok = block(Words<4>{}, j);
@@ -451,25 +505,29 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         // every lane copies pages of its own
         uint32_t g = 0;
         bool ok = true;
-        typename P::Item it;
+        typename P::Item mine;
+        typename P::Item& it = item_at<P>(sh, warp, mine);
         for (int t = 0; ok; ++t) {
-          if (!p.item(t, cluster, it)) break;
+          if (!next_item(p, t, cluster, nclusters, lane, it)) break;
           const int qb = t & 1;
           if (!(ok = tc::mbar_wait(&sh->q_empty[qb], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort))) break;
           if (lane == 0) {
             if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full[qb], 2 * p.q_bytes());
             p.load_q(sQ + qb * TILE_BYTES, &tmQ, tc::mapa(tc::smem_u32(&sh->q_full[qb]), 0), it, rank);
           }
-          for (int j = 0; j < it.n; ++j, ++g) {
+          // page numbers are asked for a block ahead
+          const int blocks = it.n;
+          typename P::Pages pages = p.pages_of(it, 0, rank, lane), ahead;
+          for (int j = 0; j < blocks; ++j, ++g, pages = ahead) {
             const int s = (int)(g & 1u);
             const uint32_t ph = (g >> 1) & 1u;
-            const typename P::Pages pages = p.pages_of(it, j, rank, lane);
+            ahead = p.pages_of(it, min(j + 1, blocks - 1), rank, lane);
             if (!(ok = tc::mbar_wait(&sh->k_empty[s], ph ^ 1u, abort))) break;
             if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh->k_full[s], 2 * TILE_BYTES);
-            p.load_k(sK + s * TILE_BYTES, &tmK, tc::mapa(tc::smem_u32(&sh->k_full[s]), 0), pages, rank, lane);
+            p.load_k(sK + s * TILE_BYTES, &tmK, tc::mapa(tc::smem_u32(&sh->k_full[s]), 0), it, pages, rank, lane);
             if (!(ok = tc::mbar_wait(&sh->v_empty[s], ph ^ 1u, abort))) break;
             if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sh->v_full[s], 2 * TILE_BYTES);
-            p.load_v(sV + s * TILE_BYTES, &tmV, tc::mapa(tc::smem_u32(&sh->v_full[s]), 0), pages, rank, lane);
+            p.load_v(sV + s * TILE_BYTES, &tmV, tc::mapa(tc::smem_u32(&sh->v_full[s]), 0), it, pages, rank, lane);
           }
         }
       } else if (lane == 0) {
@@ -556,19 +614,21 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         };
         // the first item's first S; then per block g: S(g + 1) (of this item or
         // the next) as soon as S(g) has been read, then P V(g) once P(g) is in
-        typename P::Item it, next;
-        bool ok = next_item(p, 0, cluster, nclusters, it);
+        typename P::Item mine, mine2;
+        typename P::Item &it = item_at<P>(sh, MMA_WARP, mine), &next = item_at<P>(sh, THREADS / 32, mine2);
+        bool ok = next_item_alone(p, 0, cluster, nclusters, it);
         if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0), it.n == 1);
         uint32_t g = 0;
         for (int t = 0; ok; ++t) {
           if constexpr (is_paged<P>()) next = it;
-          const bool has_next = next_item(p, t + 1, cluster, nclusters, next);
-          for (int j = 0; ok && j < it.n; ++j, ++g) {
-            if (j + 1 < it.n || has_next) {
+          const bool has_next = next_item_alone(p, t + 1, cluster, nclusters, next);
+          const int blocks = it.n;
+          for (int j = 0; ok && j < blocks; ++j, ++g) {
+            if (j + 1 < blocks || has_next) {
               // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
               if (!(ok = tc::mbar_wait(&sh->s_free, g & 1u, abort))) break;
-              if (j + 1 < it.n) {
-                ok = issue_s(g + 1, t & 1, p.keys(it, j + 1), j + 2 == it.n);
+              if (j + 1 < blocks) {
+                ok = issue_s(g + 1, t & 1, p.keys(it, j + 1), j + 2 == blocks);
               } else {
                 const int qb = (t + 1) & 1;
                 ok = tc::mbar_wait(&sh->q_full[qb], ((uint32_t)(t + 1) >> 1) & 1u, abort) &&
@@ -580,7 +640,7 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
             // the item's first P V overwrites O: the last item's O has been read
             if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort)))
               break;
-            ok = issue_pv(g, p.keys(it, j), j > 0, j + 1 == it.n);
+            ok = issue_pv(g, p.keys(it, j), j > 0, j + 1 == blocks);
           }
           if (!has_next) break;
           it = next;
@@ -593,9 +653,10 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
       const uint32_t o_cols = tmem + ((uint32_t)(quarter * 32) << 16) + O_COL;
       const uint32_t o_free0 = tc::mapa(tc::smem_u32(&sh->o_free), 0);
       bool ok = true, repair = false;
-      typename P::Item it;
+      typename P::Item mine;
+      typename P::Item& it = item_at<P>(sh, warp, mine);
       for (int t = 0; ok; ++t) {
-        if (!next_item(p, t, cluster, nclusters, it)) break;
+        if (!next_item(p, t, cluster, nclusters, lane, it)) break;
         const int b = t & 1;
         // a whole item may pass meanwhile: 20 us more for each of its blocks (one takes 2)
         const unsigned long long limit = tc::kWaitLimitNs + (unsigned long long)it.n * 20000ull;

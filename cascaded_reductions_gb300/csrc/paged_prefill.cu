@@ -104,8 +104,8 @@ struct PagedPrefill {
   static constexpr float M_START = -1e30f;
   using Item = RangeItem;
   struct Pages {
-    int kx, ky, kz, kat;          // coordinates and the place in the half; kat < 0: no copy
-    int vy, vz, vat;
+    int kpage, vpage;             // the lane's pages of the block, by their places in the table's row
+    int kid, vid;                 // and the entries there, not looked at before the copies
   };
   struct Pending {
     int row, head;
@@ -150,62 +150,81 @@ struct PagedPrefill {
     tc::tma_load_3d_pair(dst, map, bar, 0, row, head);
     tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, row, head);
   }
-  // coordinates (y, z) of page i of the item's request; zeros come from behind the map
-  __device__ __forceinline__ void find_page(const Item& it, int i, int& y, int& z) const {
-    const int used = (it.len + page() - 1) >> a.page_log2;
-    const size_t at = (size_t)it.b * a.width + i;
-    int id = -1;
-    if (i < used && i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width)) id = a.table[at];
-    const bool in = (unsigned)id < (unsigned)a.pages;
-    z = in ? id * a.v.s.Hkv + it.kvh : a.pages * a.v.s.Hkv;
-    y = i == used - 1 ? -lacking(it) : 0;
-  }
   // A half of K is 128 keys in two boxes of 64 columns per page (page <= 128), V all 256 in
   // one; of a page of 256 a half of K is 128 rows.
+  __device__ __forceinline__ int k_pages() const { return max(1, BM >> a.page_log2); }
+  __device__ __forceinline__ int entry(const Item& it, int i) const {
+    const size_t at = (size_t)it.b * a.width + i;
+    return i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width) ? a.table[at] : -1;
+  }
   __device__ __forceinline__ Pages pages_of(const Item& it, int j, int rank, int lane) const {
-    Pages p = {0, 0, 0, -1, 0, 0, -1};
-    const int first = block_of(it, j) * BN >> a.page_log2;
-    const int nk = max(1, BM >> a.page_log2), nv = BN >> a.page_log2;
+    const int first = block_of(it, j) * BN >> a.page_log2, nk = k_pages();
+    Pages p = {0, 0, -1, -1};
     if (lane < 2 * nk) {
-      const int col = lane >= nk, i = lane - col * nk;
-      find_page(it, first + (page() > BM ? 0 : rank * nk + i), p.ky, p.kz);
-      if (page() > BM) p.ky += rank * BM;
-      p.kx = 64 * col;
-      p.kat = col * HALF_BYTES + i * page() * 128;
+      p.kpage = first + (page() > BM ? 0 : rank * nk + (lane >= nk ? lane - nk : lane));
+      p.kid = entry(it, p.kpage);
     }
-    if (lane < nv) {
-      find_page(it, first + lane, p.vy, p.vz);
-      p.vat = lane * page() * 128;
+    if (lane < BN >> a.page_log2) {
+      p.vpage = first + lane;
+      p.vid = entry(it, p.vpage);
     }
     return p;
   }
-  __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Pages& p,
-                                         int, int) const {
-    if (p.kat >= 0) tc::tma_load_3d_pair(dst + p.kat, map, bar, p.kx, p.ky, p.kz);
+  // coordinates (y, z) of page i with that entry; zeros come from behind the map
+  __device__ __forceinline__ void place(const Item& it, int i, int id, int& y, int& z) const {
+    const int used = (it.len + page() - 1) >> a.page_log2;
+    z = i < used && (unsigned)id < (unsigned)a.pages ? id * a.v.s.Hkv + it.kvh : a.pages * a.v.s.Hkv;
+    y = i == used - 1 ? -lacking(it) : 0;
   }
-  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Pages& p,
-                                         int rank, int) const {
-    if (p.vat >= 0) tc::tma_load_3d_pair(dst + p.vat, map, bar, rank * 64, p.vy, p.vz);
+  __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Item& it,
+                                         const Pages& p, int rank, int lane) const {
+    const int nk = k_pages(), col = lane >= nk, i = lane - col * nk;
+    if (lane >= 2 * nk) return;
+    int y, z;
+    place(it, p.kpage, p.kid, y, z);
+    if (page() > BM) y += rank * BM;
+    tc::tma_load_3d_pair(dst + col * HALF_BYTES + i * page() * 128, map, bar, 64 * col, y, z);
+  }
+  __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Item& it,
+                                         const Pages& p, int rank, int lane) const {
+    if (lane >= BN >> a.page_log2) return;
+    int y, z;
+    place(it, p.vpage, p.vid, y, z);
+    tc::tma_load_3d_pair(dst + lane * page() * 128, map, bar, rank * 64, y, z);
   }
   __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
 
   static __device__ __forceinline__ uint32_t below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   }
-  __device__ __forceinline__ bool sees(const Item& it, int j, int rank, int r, int kh) const {
+  // A softmax thread's position, and the item's blocks first .. end - 1 that hide nothing
+  // from its warp: all but those at the tile's own positions, at the window's edge, of the
+  // sinks, and one whose last page has moved.
+  struct Row {
+    int p, first, end;
+    __device__ __forceinline__ bool all(int j) const { return j >= first && j < end; }
+  };
+  __device__ __forceinline__ Row row_of_item(const Item& it, int rank, int r, int kh) const {
+    const int p = it.len - it.rows + it.row0 + row_of(rank, r), low = p - (r & 31), window = a.v.s.window;
+    const int top = (it.hb - 1) * BN + kh * BM;       // first key of the half in the tile's block 0
+    int first = max(0, (top + BM - 1 - low + BN - 1) >> 8), end = it.nw;
+    static_assert(BN == 256, "the shifts");
+    if (lacking(it) != 0 && holds_last(it, it.hb - 1)) first = max(first, 1);
+    if (window > 0) end = min(end, ((top - (low + 31 - window + 1)) >> 8) + 1);
+    return {p, first - it.j0, end - it.j0};
+  }
+  __device__ __forceinline__ bool sees(const Item& it, const Row& row, int j, int r, int kh) const {
     const int block = block_of(it, j), base = block * BN + kh * BM;
-    const int first = it.len - it.rows + it.row0 + row_of(rank, r & ~31), last = first + 31;
+    const int first = row.p - (r & 31), last = first + 31;
     const int window = a.v.s.window;
     if (page() > BM && holds_last(it, block)) return true;       // its keys have moved between the halves
     return last >= base && (window == 0 || first - window + 1 < base + BM || a.v.s.sinks > base);
   }
-  __device__ __forceinline__ void mask(const Item& it, int j, int rank, int r, int kh, float (&s)[128]) const {
+  __device__ __forceinline__ void mask(const Item& it, const Row& row, int j, int r, int kh,
+                                       float (&s)[128]) const {
     const int block = block_of(it, j), base = block * BN + kh * BM;
-    const int p = it.len - it.rows + it.row0 + row_of(rank, r);   // this row's position
-    const int first = p - (r & 31), last = first + 31;
-    const int window = a.v.s.window;
+    const int p = row.p, window = a.v.s.window;
     const bool moved = holds_last(it, block) && lacking(it) != 0;
-    if (!moved && first - base >= BM - 1 && (window == 0 || last - window + 1 <= base)) return;
     // visible are keys up to hi, from lo on or below cs, counted from base; where the last
     // page moved by d, slots c0 + d .. of its place are keys c - d
     const int hi = min(p, it.len - 1) - base, lo = window > 0 ? p - window + 1 - base : -2 * BN;
