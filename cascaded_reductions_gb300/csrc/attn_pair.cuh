@@ -110,9 +110,9 @@ constexpr int STAGES = 2;
 constexpr int TILE_BYTES = 32768;            // Q tile, K half or V half
 constexpr int HALF_BYTES = 16384;            // one 64-column swizzled box of a 128-row tile
 constexpr int SM_WARPS = 8;                // softmax warps: two per TMEM lane quarter
-constexpr int TMA_WARP = 8, MMA_WARP = 9;
+constexpr int TMA_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10;
 constexpr int OUT_WARP = 12, OUT_WARPS = 4;  // output warps, one per TMEM lane quarter
-constexpr int THREADS = 16 * 32;             // four warpgroups (10 and 11 only fill theirs)
+constexpr int THREADS = 16 * 32;             // four warpgroups (11, and 10 but of a paged policy, only fill theirs)
 // Registers per thread: at launch, then softmax warps and the others.
 constexpr int REGS = 128, REGS_SOFTMAX = 176, REGS_OTHER = 80;
 static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHER == THREADS * REGS,
@@ -143,7 +143,9 @@ struct Shared {
   float red[2][2][BM];          // [exchange & 1][key half][row]: partial row maxima
   float part_l[2][2][BM];       // [item & 1][key half][row]: partial row sums of an item
   float row_m[2][BM];           // [item & 1][row]: its reference maxima
-  int items[18][16];            // of a paged policy: an item per warp, and the MMA thread's next
+  uint64_t item_full[2];        // of a paged policy, each CTA: an item's record is written
+  int items[2][16];             // the records of two items
+  uint4 vis[32 * SM_WARPS];     // per softmax thread, a bit per key of its half block that it sees
   uint32_t tmem_base;
   int abort;
 };
@@ -211,14 +213,17 @@ __device__ __forceinline__ void st_row32(void* dst, const uint32_t (&w)[16], boo
 }
 
 // Whether a policy's keys lie in pages.  Such a one differs from the others so:
-//   item(t, c, it)             steps `it` on to the cluster's next item (t = 0: the first)
+//   item(t, c, it)             steps `it` on to the cluster's next item (t = 0: the first);
+//                              called by one thread
 //   Pages, pages_of(it, j, rank, lane)  what a lane copies of block j, and
 //   load_k / load_v(..., it, pages, rank, lane)  its copies; no tmW, v_bytes or narrow blocks
 //   partial(it), keep(it, rank, row, col, v, m, l)  whether the item is a part of a tile's
 //                              blocks, and then, instead of pack and send, its state
 //   Row, row_of_item(it, rank, row, kh)  of an item, for a softmax thread: which blocks hide
-//                              nothing from its warp (Row::all(j)); sees() and mask() take it
-//                              for the others
+//                              nothing from its warp (Row::all(j)); for the others, instead of
+//                              sees() and mask(),
+//   visible(it, j, rank, row, kh, vis)  sets a bit per key that the row sees; whether the warp
+//                              sees any
 //   boxed(pending)             whether the warp's 32 rows leave by send(); else pack has
 //                              stored the columns
 template <class P, class = void>
@@ -233,8 +238,6 @@ template <class P>
 constexpr __host__ __device__ bool is_paged() {
   return Paged<P>::value;
 }
-// Where a role keeps its item: `mine`, or, for a paged policy, whose items have more
-// fields than the roles have registers to spare, in shared memory, written by lane 0.
 template <class P, class = void>
 struct RowOfPolicy {
   struct type {};
@@ -246,37 +249,23 @@ struct RowOfPolicy<P, decltype((void)sizeof(typename P::Row))> {
 template <class P>
 using RowOf = typename RowOfPolicy<P>::type;
 
+// The t-th item of a role.  A paged policy's are stepped by a warp of their own, which runs
+// ahead of the others, writes them down and copies their Q tiles: their many fields would
+// cost the other roles registers, and the steps time at the start of every item.  The last
+// record has n = 0.
 template <class P>
-__device__ __forceinline__ typename P::Item& item_at(Shared* sh, int i, typename P::Item& mine) {
+__device__ __forceinline__ bool take_item(const P& p, Shared* sh, int t, int cluster, int nclusters,
+                                          typename P::Item& mine, const typename P::Item*& it,
+                                          volatile int* abort) {
   if constexpr (is_paged<P>()) {
     static_assert(sizeof(mine) <= sizeof(sh->items[0]), "an item's place");
-    return *reinterpret_cast<typename P::Item*>(sh->items[i]);
+    if (!tc::mbar_wait(&sh->item_full[t & 1], (uint32_t)(t >> 1) & 1u, abort)) return false;
+    it = reinterpret_cast<const typename P::Item*>(sh->items[t & 1]);
+    return it->n > 0;
   } else {
-    return mine;
+    it = &mine;
+    return p.item(t, cluster, nclusters, mine);
   }
-}
-// all lanes of a warp
-template <class P>
-__device__ __forceinline__ bool next_item(const P& p, int t, int cluster, int nclusters, int lane,
-                                          typename P::Item& it) {
-  if constexpr (is_paged<P>()) {
-    int more = 0;
-    __syncwarp();                     // no lane reads the last item any more
-    if (lane == 0) more = p.item(t, cluster, it);
-    __syncwarp();
-    return __shfl_sync(0xffffffffu, more, 0) != 0;
-  } else {
-    return p.item(t, cluster, nclusters, it);
-  }
-}
-// one thread
-template <class P>
-__device__ __forceinline__ bool next_item_alone(const P& p, int t, int cluster, int nclusters,
-                                                typename P::Item& it) {
-  if constexpr (is_paged<P>())
-    return p.item(t, cluster, it);
-  else
-    return p.item(t, cluster, nclusters, it);
 }
 
 template <int N>
@@ -341,6 +330,8 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
     tc::mbar_init(&sh->o_full, 1);
     tc::mbar_init(&sh->o_free, 2 * OUT_WARPS);
     for (int q = 0; q < 4; ++q) tc::mbar_init(&sh->red_bar[q], 2);
+    if constexpr (is_paged<P>())
+      for (int b = 0; b < 2; ++b) tc::mbar_init(&sh->item_full[b], 1);
     sh->abort = 0;
     tc::fence_barrier_init();
   }
@@ -372,15 +363,17 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
     uint32_t g = 0, x = 0;                          // blocks and red_bar exchanges so far
     bool ok = true;
     typename P::Item mine;
-    typename P::Item& it = item_at<P>(sh, warp, mine);
+    const typename P::Item* at;
     for (int t = 0; ok; ++t) {
-      if (!next_item(p, t, cluster, nclusters, lane, it)) break;
+      if (!take_item(p, sh, t, cluster, nclusters, mine, at, abort)) break;
+      const typename P::Item& it = *at;
       float m_ref = P::M_START, l = 0.f;
       RowOf<P> row;
       if constexpr (is_paged<P>()) row = p.row_of_item(it, rank, r, kh);
       // One block, of which this warp's rows see some of its 128 keys (NW = 4
       // 32-key words) or none (NW = 0); false if a wait gave up.
-      auto block = [&](auto words, int j) -> bool {
+      // `hides`: of a paged policy, that some keys are hidden (sh->vis).
+      auto block = [&](auto words, int j, bool hides) -> bool {
         constexpr int NW = decltype(words)::value;
         if (!tc::mbar_wait(&sh->s_full, g & 1u, abort)) return false;
         tc::fence_after_sync();
@@ -399,7 +392,15 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if constexpr (NW > 0) {
           if constexpr (is_paged<P>()) {
-            if (!row.all(j)) p.mask(it, row, j, r, kh, s);
+            if (hides) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t vis = reinterpret_cast<const uint32_t*>(&sh->vis[threadIdx.x])[q];
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(vis & (1u << c))) s[32 * q + c] = -INFINITY;
+              }
+            }
           } else {
             p.mask(it, j, rank, r, kh, s);
           }
@@ -476,17 +477,18 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         if (lane == 0) arrive_cluster_relaxed(p_ready0);
         return true;
       };
-      const int blocks = it.n;
-      for (int j = 0; ok && j < blocks; ++j, ++g) {
-        if constexpr (P::PARTIAL) {
-          bool some;
-          if constexpr (is_paged<P>())
-            some = row.all(j) || p.sees(it, row, j, r, kh);
-          else
-            some = p.sees(it, j, rank, r, kh);
-          ok = some ? block(Words<4>{}, j) : block(Words<0>{}, j);
+      for (int j = 0, blocks = it.n; ok && j < blocks; ++j, ++g) {
+        if constexpr (is_paged<P>()) {
+          // worked out while the products are under way, and kept out of the registers
+          const bool hides = !row.all(j);
+          bool some = true;
+          if (hides) some = p.visible(it, j, rank, r, kh, sh->vis[threadIdx.x]);
+          ok = some ? block(Words<4>{}, j, hides) : block(Words<0>{}, j, true);
+        } else if constexpr (P::PARTIAL) {
+          const bool some = p.sees(it, j, rank, r, kh);
+          ok = some ? block(Words<4>{}, j, true) : block(Words<0>{}, j, true);
         } else {
-          ok = block(Words<4>{}, j);
+          ok = block(Words<4>{}, j, true);
         }
       }
       if (!ok) break;
@@ -506,17 +508,12 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         uint32_t g = 0;
         bool ok = true;
         typename P::Item mine;
-        typename P::Item& it = item_at<P>(sh, warp, mine);
+        const typename P::Item* at;
         for (int t = 0; ok; ++t) {
-          if (!next_item(p, t, cluster, nclusters, lane, it)) break;
-          const int qb = t & 1;
-          if (!(ok = tc::mbar_wait(&sh->q_empty[qb], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort))) break;
-          if (lane == 0) {
-            if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full[qb], 2 * p.q_bytes());
-            p.load_q(sQ + qb * TILE_BYTES, &tmQ, tc::mapa(tc::smem_u32(&sh->q_full[qb]), 0), it, rank);
-          }
-          // page numbers are asked for a block ahead
+          if (!take_item(p, sh, t, cluster, nclusters, mine, at, abort)) break;
+          const typename P::Item& it = *at;
           const int blocks = it.n;
+          // page numbers are asked for a block ahead
           typename P::Pages pages = p.pages_of(it, 0, rank, lane), ahead;
           for (int j = 0; j < blocks; ++j, ++g, pages = ahead) {
             const int s = (int)(g & 1u);
@@ -556,6 +553,28 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
           }
         }
       }
+    } else if (is_paged<P>() && warp == ITEM_WARP) {
+      // ---------------------------------------------------- items ----
+      if constexpr (is_paged<P>()) {
+        if (lane == 0) {
+          typename P::Item step;
+          step.n = 0;
+          for (int t = 0, before = 0;; ++t) {
+            const int b = t & 1;
+            // 20 us more to wait for each block of the two items that may be under way
+            const unsigned long long limit = tc::kWaitLimitNs + (unsigned long long)(before + step.n) * 20000ull;
+            before = step.n;
+            if (!p.item(t, cluster, step)) step.n = 0;
+            // the item before the last has left its record and its Q buffer
+            if (!tc::mbar_wait(&sh->q_empty[b], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort, limit)) break;
+            *reinterpret_cast<typename P::Item*>(sh->items[b]) = step;
+            tc::mbar_arrive(&sh->item_full[b]);
+            if (step.n == 0) break;
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full[b], 2 * p.q_bytes());
+            p.load_q(sQ + b * TILE_BYTES, &tmQ, tc::mapa(tc::smem_u32(&sh->q_full[b]), 0), step, rank);
+          }
+        }
+      }
     } else if (warp == MMA_WARP) {
       // ------------------------------------------------------ MMA ----
       if (lane == 0 && rank == 0) {
@@ -581,8 +600,10 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
           const int s = (int)(g & 1u);
           if (!tc::mbar_wait(&sh->k_full[s], (g >> 1) & 1u, abort)) return false;
           tc::fence_after_sync();
-          const uint64_t kd = s ? k_desc1 : k_desc0;
-          const uint64_t qd = qb ? q_desc1 : q_desc0;
+          // (a paged policy's registers end at one descriptor of each: the stages are a tile apart)
+          constexpr uint64_t tile = TILE_BYTES >> 4;
+          const uint64_t kd = is_paged<P>() ? k_desc0 + s * tile : s ? k_desc1 : k_desc0;
+          const uint64_t qd = is_paged<P>() ? q_desc0 + qb * tile : qb ? q_desc1 : q_desc0;
           const uint32_t idesc = keys == BN ? idesc_s : keys == MIXED ? idesc_s_mixed : idesc_s_narrow;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
@@ -599,7 +620,7 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
           const int s = (int)(g & 1u);
           if (!tc::mbar_wait(&sh->v_full[s], (g >> 1) & 1u, abort)) return false;
           tc::fence_after_sync();
-          const uint64_t vd = s ? v_desc1 : v_desc0;
+          const uint64_t vd = is_paged<P>() ? v_desc0 + s * (uint64_t)(TILE_BYTES >> 4) : s ? v_desc1 : v_desc0;
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
             if ((kk == NARROW / 16 || kk == MIXED / 16) && kk * 16 >= keys) break;
@@ -614,36 +635,69 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         };
         // the first item's first S; then per block g: S(g + 1) (of this item or
         // the next) as soon as S(g) has been read, then P V(g) once P(g) is in
-        typename P::Item mine, mine2;
-        typename P::Item &it = item_at<P>(sh, MMA_WARP, mine), &next = item_at<P>(sh, THREADS / 32, mine2);
-        bool ok = next_item_alone(p, 0, cluster, nclusters, it);
-        if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0), it.n == 1);
-        uint32_t g = 0;
-        for (int t = 0; ok; ++t) {
-          if constexpr (is_paged<P>()) next = it;
-          const bool has_next = next_item_alone(p, t + 1, cluster, nclusters, next);
-          const int blocks = it.n;
-          for (int j = 0; ok && j < blocks; ++j, ++g) {
-            if (j + 1 < blocks || has_next) {
-              // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
-              if (!(ok = tc::mbar_wait(&sh->s_free, g & 1u, abort))) break;
-              if (j + 1 < blocks) {
-                ok = issue_s(g + 1, t & 1, p.keys(it, j + 1), j + 2 == blocks);
-              } else {
-                const int qb = (t + 1) & 1;
-                ok = tc::mbar_wait(&sh->q_full[qb], ((uint32_t)(t + 1) >> 1) & 1u, abort) &&
-                     issue_s(g + 1, qb, p.keys(next, 0), next.n == 1);
+        if constexpr (is_paged<P>()) {
+          // The same over the records, of which only the number of blocks is needed.  An item's
+          // first S is not waited for while the last item's last P V is still to be issued.
+          // (One place for either product: the roles' registers are few.)
+          uint32_t g = 0, sg = 0;             // blocks whose P V, whose S was issued
+          int t = 0, j = 0, n = 0;            // the item, block and number of blocks of P V g
+          int st = 0, sj = 0, sn = 0;         // and of S sg
+          bool ok = true;
+          for (;;) {
+            while (ok && sg <= g + 1) {
+              const int qb = st & 1;
+              const uint32_t ph = (uint32_t)(st >> 1) & 1u;
+              if (sj == 0) {
+                if (sg > g && !(tc::mbar_try_wait(&sh->item_full[qb], ph) && tc::mbar_try_wait(&sh->q_full[qb], ph)))
+                  break;
+                if (!(ok = tc::mbar_wait(&sh->item_full[qb], ph, abort))) break;
+                sn = reinterpret_cast<const typename P::Item*>(sh->items[qb])->n;
+                if (sn == 0 || !(ok = tc::mbar_wait(&sh->q_full[qb], ph, abort))) break;
               }
-              if (!ok) break;
+              // S(sg) overwrites S(sg - 1): both CTAs' softmax warps have read it
+              if (sg > 0 && !(ok = tc::mbar_wait(&sh->s_free, (sg - 1) & 1u, abort))) break;
+              if (!(ok = issue_s(sg, qb, BN, sj + 1 == sn))) break;
+              if (st == t) n = sn;
+              ++sg;
+              if (++sj == sn) ++st, sj = 0;
             }
+            if (!ok || sg <= g) break;        // no item is left
+            if (j == 0 && st > t) n = reinterpret_cast<const typename P::Item*>(sh->items[t & 1])->n;
             if (!(ok = tc::mbar_wait(&sh->p_ready, g & 1u, abort))) break;
-            // the item's first P V overwrites O: the last item's O has been read
-            if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort)))
-              break;
-            ok = issue_pv(g, p.keys(it, j), j > 0, j + 1 == blocks);
+            if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort))) break;
+            if (!(ok = issue_pv(g, BN, j > 0, j + 1 == n))) break;
+            ++g;
+            if (++j == n) ++t, j = 0;
           }
-          if (!has_next) break;
-          it = next;
+        } else {
+          typename P::Item it, next;
+          bool ok = p.item(0, cluster, nclusters, it);
+          if (ok) ok = tc::mbar_wait(&sh->q_full[0], 0, abort) && issue_s(0, 0, p.keys(it, 0), it.n == 1);
+          uint32_t g = 0;
+          for (int t = 0; ok; ++t) {
+            const bool has_next = p.item(t + 1, cluster, nclusters, next);
+            for (int j = 0; ok && j < it.n; ++j, ++g) {
+              if (j + 1 < it.n || has_next) {
+                // S(g + 1) overwrites S(g): both CTAs' softmax warps have read it
+                if (!(ok = tc::mbar_wait(&sh->s_free, g & 1u, abort))) break;
+                if (j + 1 < it.n) {
+                  ok = issue_s(g + 1, t & 1, p.keys(it, j + 1), j + 2 == it.n);
+                } else {
+                  const int qb = (t + 1) & 1;
+                  ok = tc::mbar_wait(&sh->q_full[qb], ((uint32_t)(t + 1) >> 1) & 1u, abort) &&
+                       issue_s(g + 1, qb, p.keys(next, 0), next.n == 1);
+                }
+                if (!ok) break;
+              }
+              if (!(ok = tc::mbar_wait(&sh->p_ready, g & 1u, abort))) break;
+              // the item's first P V overwrites O: the last item's O has been read
+              if (j == 0 && t > 0 && !(ok = tc::mbar_wait(&sh->o_free, (uint32_t)(t - 1) & 1u, abort)))
+                break;
+              ok = issue_pv(g, p.keys(it, j), j > 0, j + 1 == it.n);
+            }
+            if (!has_next) break;
+            it = next;
+          }
         }
       }
     } else if (warp >= OUT_WARP) {
@@ -654,9 +708,10 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
       const uint32_t o_free0 = tc::mapa(tc::smem_u32(&sh->o_free), 0);
       bool ok = true, repair = false;
       typename P::Item mine;
-      typename P::Item& it = item_at<P>(sh, warp, mine);
+      const typename P::Item* at;
       for (int t = 0; ok; ++t) {
-        if (!next_item(p, t, cluster, nclusters, lane, it)) break;
+        if (!take_item(p, sh, t, cluster, nclusters, mine, at, abort)) break;
+        const typename P::Item& it = *at;
         const int b = t & 1;
         // a whole item may pass meanwhile: 20 us more for each of its blocks (one takes 2)
         const unsigned long long limit = tc::kWaitLimitNs + (unsigned long long)it.n * 20000ull;

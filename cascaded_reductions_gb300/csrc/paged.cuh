@@ -44,11 +44,11 @@ struct PagedShape {
 };
 
 // Words of a plan's head.
-enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
+enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanJoins, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
 
 // Where the parts of a plan lie, in bytes from its start.
 struct PagedLayout {
-  size_t seqs, before, ranges, units, counters, unit_ml, unit_acc, slots, bytes;
+  size_t seqs, before, ranges, joins, units, counters, unit_ml, unit_acc, slots, bytes;
   int unit_cap, range_cap;
   uint32_t mark;                        // of the sizes: a plan of others is refused on the device
 };
@@ -66,12 +66,21 @@ struct PagedUnit {
 struct PagedRange {
   int b, item, block, count;            // the first block's request, item and number in it; blocks
 };
+// A tile that cuts divide: its first part is the state slot0, the others are slots
+// 2 rho, 2 rho + 2 ..
+struct PagedJoin {
+  int b, start, rows, len;              // the request
+  int head, kvh, row0;                  // first query head, key head, first new token of the tile
+  int parts, slot0, rho;
+  int pad[6];
+};
 
 struct PagedView {
   PagedShape s;
   int* head;
   const PagedSeq* seqs;
   const PagedRange* ranges;
+  const PagedJoin* joins;
   const PagedUnit* units;
   int* counters;
   float2* unit_ml;                      // [unit][Hkv][unit_rows]
@@ -79,6 +88,8 @@ struct PagedView {
   float* slots;
   int unit_cap, range_cap;
   uint32_t mark;
+  int G, packed, P_log2, groups, key_groups;   // heads per key head and per tile; positions of a
+                                        // tile; head groups in all and per key head
 };
 
 // The visible keys of a request's rows as tiles of 16: sinks' tiles first, then those
@@ -165,6 +176,7 @@ inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* pla
   v.head = reinterpret_cast<int*>(p);
   v.seqs = reinterpret_cast<const PagedSeq*>(p + l.seqs);
   v.ranges = reinterpret_cast<const PagedRange*>(p + l.ranges);
+  v.joins = reinterpret_cast<const PagedJoin*>(p + l.joins);
   v.units = reinterpret_cast<const PagedUnit*>(p + l.units);
   v.counters = reinterpret_cast<int*>(p + l.counters);
   v.unit_ml = reinterpret_cast<float2*>(p + l.unit_ml);
@@ -172,6 +184,9 @@ inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* pla
   v.slots = reinterpret_cast<float*>(p + l.slots);
   v.unit_cap = l.unit_cap, v.range_cap = l.range_cap;
   v.mark = l.mark;
+  v.G = s.G(), v.packed = s.packed(), v.P_log2 = 0;
+  while ((1 << v.P_log2) < s.positions()) ++v.P_log2;
+  v.key_groups = v.G / v.packed, v.groups = s.Hkv * v.key_groups;
   return v;
 }
 

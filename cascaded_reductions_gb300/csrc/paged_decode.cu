@@ -48,14 +48,14 @@ struct Work {
   PagedTiles t;
   __device__ __forceinline__ Work(const PagedAttn& a, const PagedUnit& u, int hk_)
       : b(u.b), hk(hk_), start(u.start), n(u.n), len(u.len), row0(u.tile * MROWS),
-        rows(min(MROWS, u.n * a.v.s.G() - u.tile * MROWS)), t(u.n, u.len, a.v.s.window, a.v.s.sinks) {}
+        rows(min(MROWS, u.n * a.v.G - u.tile * MROWS)), t(u.n, u.len, a.v.s.window, a.v.s.sinks) {}
   // row r's query row in [T * H], and its position
   __device__ __forceinline__ size_t at(const PagedAttn& a, int r) const {
-    const int G = a.v.s.G(), i = (row0 + r) / G;
+    const int G = a.v.G, i = (row0 + r) / G;
     return (size_t)(start + i) * a.v.s.H + hk * G + (row0 + r - i * G);
   }
   __device__ __forceinline__ int pos(const PagedAttn& a, int r) const {
-    return len - n + (row0 + r) / a.v.s.G();
+    return len - n + (row0 + r) / a.v.G;
   }
   __device__ __forceinline__ int key_tile(int i) const {
     return i < t.sink_tiles ? i : i - t.sink_tiles + t.lo_tile;

@@ -33,6 +33,7 @@ struct Plan {
   PagedSeq* seqs;
   long long* before;                    // [B + 1]: pair blocks of the requests before
   PagedRange* ranges;
+  PagedJoin* joins;
   PagedUnit* units;
   int* counters;
   int unit_cap, range_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
@@ -82,6 +83,7 @@ __device__ __forceinline__ int pieces_of(int steps, int piece) { return (steps +
 
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   __shared__ long long sm[WARPS], fit[WARPS];
+  __shared__ int n_joins;
   const PagedShape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = s.Hkv * (s.G() / s.packed());
@@ -216,8 +218,36 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       if (RF_IDX_OK(i, a.range_cap)) a.ranges[i] = r;
     }
   }
+  if (tid == 0) n_joins = 0;
+  __syncthreads();
+  // the tiles that a range's start cuts for the first time
+  for (int i = 1 + tid; i < n_ranges; i += THREADS) {
+    if (!RF_SPAN_OK(i - 1, 2, a.range_cap)) break;
+    const PagedRange r = a.ranges[i], before = a.ranges[i - 1];
+    const bool same = before.b == r.b && before.item == r.item;
+    if (r.block == 0 || (same && before.block > 0)) continue;
+    PagedJoin x = {};
+    x.parts = 2;
+    while (i + x.parts - 1 < n_ranges && RF_IDX_OK(i + x.parts - 1, a.range_cap)) {
+      const PagedRange y = a.ranges[i + x.parts - 1];
+      if (y.b != r.b || y.item != r.item || y.block == 0) break;
+      ++x.parts;
+    }
+    const PagedSeq q = a.seqs[r.b];
+    const int P = s.positions(), tiles = (q.n + P - 1) / P, group = r.item / tiles;
+    x.b = r.b, x.start = q.start, x.rows = q.n, x.len = q.len;
+    x.head = group * s.packed();
+    x.kvh = x.head / s.G();
+    x.row0 = (tiles - 1 - (r.item - group * tiles)) * P;
+    x.slot0 = 2 * (i - 1) + (same ? 0 : 1);
+    x.rho = i;
+    const int at = atomicAdd(&n_joins, 1);
+    if (RF_IDX_OK(at, a.range_cap)) a.joins[at] = x;
+  }
+  __syncthreads();
   if (tid < kPlanWords) {
     int x = 0;
+    if (tid == kPlanJoins) x = n_joins;
     if (tid == kPlanMark) x = (int)a.mark;
     if (tid == kPlanUnits) x = n_units;
     if (tid == kPlanRanges) x = n_ranges;
@@ -259,6 +289,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   l->seqs = take((size_t)s.B * sizeof(PagedSeq));
   l->before = take(((size_t)s.B + 1) * sizeof(long long));
   l->ranges = take((size_t)l->range_cap * sizeof(PagedRange));
+  l->joins = take((size_t)l->range_cap * sizeof(PagedJoin));
   l->units = take((size_t)l->unit_cap * sizeof(PagedUnit));
   l->counters = take((size_t)l->unit_cap * s.Hkv * sizeof(int));
   l->unit_ml = take(rows * sizeof(float2));
@@ -285,6 +316,7 @@ rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const Pa
   a.seqs = reinterpret_cast<PagedSeq*>(p + l.seqs);
   a.before = reinterpret_cast<long long*>(p + l.before);
   a.ranges = reinterpret_cast<PagedRange*>(p + l.ranges);
+  a.joins = reinterpret_cast<PagedJoin*>(p + l.joins);
   a.units = reinterpret_cast<PagedUnit*>(p + l.units);
   a.counters = reinterpret_cast<int*>(p + l.counters);
   a.unit_cap = l.unit_cap, a.range_cap = l.range_cap;

@@ -43,7 +43,7 @@ static_assert(2 * BM == kPagedPairRows && BN == kPagedBlock && HD == 128, "the p
 // The items of a range, one after the other: tiles, or what of a tile the range holds.
 struct RangeItem {
   int rho, left;       // range, and its blocks behind this item
-  int b, m;            // request, tile (head group major, last positions first)
+  int b, group;        // request, head group
   int j0, n, next;     // first block of the tile, blocks, the block after them (0: no more)
   int slot;            // of the partial state, -1 for a whole tile
   int start, rows, len;           // the request
@@ -51,14 +51,10 @@ struct RangeItem {
   int hb, nw;          // window blocks hb - 1, hb - 2 .. (nw of them), then those of the sinks from 0 on
 };
 
+// the item from block j on of the tile at row0
 __device__ __forceinline__ void place_item(const PagedView& v, bool first, int j, RangeItem& it) {
-  const PagedShape& s = v.s;
-  const int G = s.G(), packed = s.packed();
-  const PagedBlocks k(it.rows, it.len, s.positions(), s.window, s.sinks);
-  const int tiles = k.tiles(), group = it.m / tiles, i = tiles - 1 - (it.m - group * tiles);
-  it.head = group * packed;
-  it.kvh = it.head / G;
-  it.row0 = i * s.positions();
+  const PagedBlocks k(it.rows, it.len, 1 << v.P_log2, v.s.window, v.s.sinks);
+  const int i = it.row0 >> v.P_log2;
   it.hb = k.hb(i);
   it.nw = it.hb - k.lb(i);
   const int all = it.nw + k.sink_blocks(i);
@@ -67,6 +63,11 @@ __device__ __forceinline__ void place_item(const PagedView& v, bool first, int j
   it.left -= it.n;
   it.next = j + it.n == all ? 0 : j + it.n;
   it.slot = it.n == all ? -1 : 2 * it.rho + (first ? 0 : 1);
+}
+__device__ __forceinline__ void place_group(const PagedView& v, int group, RangeItem& it) {
+  it.group = group;
+  it.head = group * v.packed;
+  it.kvh = group / v.key_groups;
 }
 __device__ __forceinline__ PagedSeq load_seq(const PagedView& v, int b) {
   PagedSeq q = {0, 0, 0, 1};
@@ -77,21 +78,29 @@ __device__ __forceinline__ void first_item(const PagedView& v, int rho, RangeIte
   PagedRange r = {0, 0, 0, 0};
   if (RF_IDX_OK(rho, v.range_cap)) *reinterpret_cast<int4*>(&r) = *reinterpret_cast<const int4*>(v.ranges + rho);
   const PagedSeq q = load_seq(v, r.b);
-  it.rho = rho, it.left = r.count, it.b = r.b, it.m = r.item;
+  it.rho = rho, it.left = r.count, it.b = r.b;
   it.start = q.start, it.rows = q.n, it.len = q.len;
+  const int tiles = max(1, (q.n + (1 << v.P_log2) - 1) >> v.P_log2), group = r.item / tiles;
+  place_group(v, group, it);
+  it.row0 = (tiles - 1 - (r.item - group * tiles)) << v.P_log2;      // the last tile first
   place_item(v, true, r.block, it);
 }
 // the next item of the same range (left > 0)
 __device__ __forceinline__ void step_item(const PagedView& v, RangeItem& it) {
   if (it.next == 0) {
-    const int P = v.s.positions();
-    if (++it.m == (it.rows + P - 1) / P * v.s.Hkv * (v.s.G() / v.s.packed())) {
-      PagedSeq q;
-      do {
-        q = load_seq(v, ++it.b);
-      } while (!q.pair);
-      it.m = 0;
-      it.start = q.start, it.rows = q.n, it.len = q.len;
+    it.row0 -= 1 << v.P_log2;
+    if (it.row0 < 0) {
+      int group = it.group + 1;
+      if (group == v.groups) {
+        PagedSeq q;
+        do {
+          q = load_seq(v, ++it.b);
+        } while (!q.pair);
+        group = 0;
+        it.start = q.start, it.rows = q.n, it.len = q.len;
+      }
+      place_group(v, group, it);
+      it.row0 = (it.rows - 1) >> v.P_log2 << v.P_log2;
     }
   }
   place_item(v, false, it.next, it);
@@ -100,7 +109,7 @@ __device__ __forceinline__ void step_item(const PagedView& v, RangeItem& it) {
 template <bool F16_>
 struct PagedPrefill {
   static constexpr bool F16 = F16_;
-  static constexpr bool CHAINED = true, PARTIAL = true, STAGED = true;
+  static constexpr bool CHAINED = true, STAGED = true;
   static constexpr float M_START = -1e30f;
   using Item = RangeItem;
   struct Pages {
@@ -138,9 +147,9 @@ struct PagedPrefill {
   __device__ __forceinline__ bool holds_last(const Item& it, int block) const {
     return it.len > 0 && (it.len - 1) / BN == block;
   }
-  __device__ __forceinline__ int head_of(int rank, int r) const { return (rank * BM + r) / a.v.s.positions(); }
+  __device__ __forceinline__ int head_of(int rank, int r) const { return (rank * BM + r) >> a.v.P_log2; }
   __device__ __forceinline__ int row_of(int rank, int r) const {
-    return (rank * BM + r) & (a.v.s.positions() - 1);
+    return (rank * BM + r) & ((1 << a.v.P_log2) - 1);
   }
 
   __device__ __forceinline__ uint32_t q_bytes() const { return pair::TILE_BYTES; }
@@ -197,53 +206,44 @@ struct PagedPrefill {
   static __device__ __forceinline__ uint32_t below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   }
-  // A softmax thread's position, and the item's blocks first .. end - 1 that hide nothing
-  // from its warp: all but those at the tile's own positions, at the window's edge, of the
+  // Of a softmax thread: the item's blocks first .. end - 1 hide nothing from its warp: all but those at the tile's own positions, at the window's edge, of the
   // sinks, and one whose last page has moved.
   struct Row {
-    int p, first, end;
+    int first, end;
     __device__ __forceinline__ bool all(int j) const { return j >= first && j < end; }
   };
+  __device__ __forceinline__ int position(const Item& it, int rank, int r) const {
+    return it.len - it.rows + it.row0 + row_of(rank, r);
+  }
   __device__ __forceinline__ Row row_of_item(const Item& it, int rank, int r, int kh) const {
-    const int p = it.len - it.rows + it.row0 + row_of(rank, r), low = p - (r & 31), window = a.v.s.window;
+    const int low = position(it, rank, r & ~31), window = a.v.s.window;
     const int top = (it.hb - 1) * BN + kh * BM;       // first key of the half in the tile's block 0
     int first = max(0, (top + BM - 1 - low + BN - 1) >> 8), end = it.nw;
     static_assert(BN == 256, "the shifts");
     if (lacking(it) != 0 && holds_last(it, it.hb - 1)) first = max(first, 1);
     if (window > 0) end = min(end, ((top - (low + 31 - window + 1)) >> 8) + 1);
-    return {p, first - it.j0, end - it.j0};
+    return {first - it.j0, end - it.j0};
   }
-  __device__ __forceinline__ bool sees(const Item& it, const Row& row, int j, int r, int kh) const {
+  __device__ __forceinline__ bool visible(const Item& it, int j, int rank, int r, int kh,
+                                          uint4& bits) const {
     const int block = block_of(it, j), base = block * BN + kh * BM;
-    const int first = row.p - (r & 31), last = first + 31;
-    const int window = a.v.s.window;
-    if (page() > BM && holds_last(it, block)) return true;       // its keys have moved between the halves
-    return last >= base && (window == 0 || first - window + 1 < base + BM || a.v.s.sinks > base);
-  }
-  __device__ __forceinline__ void mask(const Item& it, const Row& row, int j, int r, int kh,
-                                       float (&s)[128]) const {
-    const int block = block_of(it, j), base = block * BN + kh * BM;
-    const int p = row.p, window = a.v.s.window;
+    const int p = position(it, rank, r), window = a.v.s.window;
     const bool moved = holds_last(it, block) && lacking(it) != 0;
-    // visible are keys up to hi, from lo on or below cs, counted from base; where the last
+    // seen are keys up to hi, from lo on or below cs, counted from base; where the last
     // page moved by d, slots c0 + d .. of its place are keys c - d
     const int hi = min(p, it.len - 1) - base, lo = window > 0 ? p - window + 1 - base : -2 * BN;
     const int cs = a.v.s.sinks - base;
     const int d = moved ? lacking(it) : 0;
     const int c0 = moved ? ((it.len - 1) & ~(page() - 1)) - base : BN;
+    uint32_t vis[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      uint32_t vis = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));
-      if (moved) {
-        const uint32_t in = below(hi + d + 1 - 32 * q) & (~below(lo + d - 32 * q) | below(cs + d - 32 * q));
-        vis = (vis & below(c0 - 32 * q)) | (in & ~below(c0 + d - 32 * q));
-      }
-      if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!(vis & (1u << c))) s[32 * q + c] = -INFINITY;
-      }
+      const uint32_t plain = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));
+      const uint32_t behind = below(hi + d + 1 - 32 * q) & (~below(lo + d - 32 * q) | below(cs + d - 32 * q));
+      vis[q] = (plain & below(c0 - 32 * q)) | (behind & ~below(c0 + d - 32 * q));
     }
+    bits = make_uint4(vis[0], vis[1], vis[2], vis[3]);
+    return __any_sync(0xffffffffu, (vis[0] | vis[1] | vis[2] | vis[3]) != 0);
   }
 
   __device__ __forceinline__ bool partial(const Item& it) const { return it.slot >= 0; }
@@ -307,7 +307,7 @@ paged_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
 // ------------------------------------------------------------------ finish --
 
-constexpr int FIN_WARPS = 4, FIN_ROWS = 32, FIN_PARTS = kPagedPairRows / FIN_ROWS;
+constexpr int FIN_WARPS = 8, FIN_ROWS = 32, FIN_PARTS = kPagedPairRows / FIN_ROWS;
 
 template <bool F16>
 __device__ __forceinline__ float4 widen4(const uint8_t* row, int lane) {
@@ -325,7 +325,7 @@ __device__ __forceinline__ float4 widen4(const uint8_t* row, int lane) {
 // that the row sees.  Ends once they are all NaN again.  Gives the row's sum and maximum too
 // (in log2 units), where it went through all of its keys.
 template <bool F16>
-__device__ __noinline__ float4 redo_row(const PagedAttn& a, const RangeItem it, int i, int head, uint32_t todo,
+__device__ __noinline__ float4 redo_row(const PagedAttn& a, const PagedJoin it, int i, int head, uint32_t todo,
                                         float4 y, float* lse2, int lane) {
   constexpr int U = 8;                                // keys in flight
   const int p = it.len - it.rows + i, window = a.v.s.window, page = 1 << a.page_log2;
@@ -391,9 +391,9 @@ __device__ __forceinline__ uint32_t nan_of(const float4& y) {
   return (y.x != y.x) | (y.y != y.y) << 1 | (y.z != y.z) << 2 | (y.w != y.w) << 3;
 }
 
-// A CTA per range and 32 of a tile's 256 rows.  First it joins the parts of the tile that the
-// range's start cut, if that was the tile's first cut; then, where the pair kernel noted
-// a value that is not finite, it looks at the whole tiles of the range.
+// A CTA per 32 of a tile's 256 rows, eight to a tile.  The first ones join the parts of a
+// tile that cuts divide; then, where the pair kernel noted a value that is not finite, a
+// range's eight look at its whole tiles.
 template <bool F16>
 __global__ void __launch_bounds__(FIN_WARPS * 32)
 paged_finish_kernel(const __grid_constant__ PagedAttn a) {
@@ -402,91 +402,78 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
   wait_prerequisite();
   allow_dependents();
   const PagedView& v = a.v;
-  if (v.head[kPlanMark] != (int)v.mark) return;
-  const int ranges = min(v.head[kPlanRanges], v.range_cap), flag = v.head[kPlanFlag];
-  const int P = v.s.positions();
   const size_t all_rows = (size_t)v.s.T * v.s.H;
   (void)all_rows;                                     // read by the checked build only
-  auto range = [&](int i) {
-    PagedRange r = {0, 0, 0, 0};
-    if (RF_IDX_OK(i, v.range_cap)) *reinterpret_cast<int4*>(&r) = *reinterpret_cast<const int4*>(v.ranges + i);
-    return r;
-  };
-  if (rho > 0 && rho < ranges) {
-    const PagedRange r = range(rho), before = range(rho - 1);
-    const bool same = before.b == r.b && before.item == r.item;
-    if (r.block > 0 && !(same && before.block > 0)) {
-      // the tile's parts: the last of the range before, then the first of each range that
-      // starts inside the tile
-      int parts = 2;
-      while (rho + parts - 1 < ranges) {
-        const PagedRange x = range(rho + parts - 1);
-        if (x.b != r.b || x.item != r.item || x.block == 0) break;
-        ++parts;
-      }
-      const int slot0 = 2 * (rho - 1) + (same ? 0 : 1);
-      RangeItem it;
-      first_item(v, rho, it);
-      constexpr int R = FIN_ROWS / FIN_WARPS;         // rows of a warp
-      const int row0 = part * FIN_ROWS + warp * R;    // of the tile
-      float M[R], L[R];
-      float4 A[R];
+  PagedJoin it = {};
+  if (RF_IDX_OK(rho, v.range_cap)) {                  // asked for before it is known whether it is one
+    const int4* at = reinterpret_cast<const int4*>(v.joins + rho);
+    int4* to = reinterpret_cast<int4*>(&it);
 #pragma unroll
-      for (int q = 0; q < R; ++q) M[q] = -INFINITY, L[q] = 0.f, A[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = 0; x < parts; ++x) {
-        const int slot = x == 0 ? slot0 : 2 * (rho + x - 1);
-        if (!RF_IDX_OK(slot, 2 * v.range_cap)) break;
-        const float* at = v.slots + (size_t)slot * kPagedSlotFloats;
-        float4 o[R];
-        float m[R], l[R];
+    for (int e = 0; e < 3; ++e) to[e] = at[e];
+  }
+  if (v.head[kPlanMark] != (int)v.mark) return;
+  const int ranges = min(v.head[kPlanRanges], v.range_cap), flag = v.head[kPlanFlag];
+  const int P = 1 << v.P_log2;
+  if (rho < min(v.head[kPlanJoins], v.range_cap)) {
+    constexpr int R = FIN_ROWS / FIN_WARPS;           // rows of a warp
+    const int row0 = part * FIN_ROWS + warp * R;      // of the tile
+    float M[R], L[R];
+    float4 A[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) M[q] = -INFINITY, L[q] = 0.f, A[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < it.parts; x0 += 2) {        // two parts in flight
+      float4 o[2][R];
+      float m[2][R], l[2][R];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int slot = x0 + x == 0 ? it.slot0 : 2 * (it.rho + x0 + x - 1);
+        const bool in = x0 + x < it.parts && RF_IDX_OK(slot, 2 * v.range_cap);
+        const float* at = v.slots + (size_t)(in ? slot : 0) * kPagedSlotFloats;
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-          o[q] = __ldcg(reinterpret_cast<const float4*>(at + (row0 + q) * HD) + lane);
-          m[q] = __ldcg(at + kPagedPairRows * HD + row0 + q);
-          l[q] = __ldcg(at + kPagedPairRows * (HD + 1) + row0 + q);
+          o[x][q] = __ldcg(reinterpret_cast<const float4*>(at + (row0 + q) * HD) + lane);
+          m[x][q] = __ldcg(at + kPagedPairRows * HD + row0 + q);
+          l[x][q] = in ? __ldcg(at + kPagedPairRows * (HD + 1) + row0 + q) : 0.f;
         }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-          if (l[q] == 0.f) continue;                  // the part holds nothing that the row sees
-          const float top = fmaxf(M[q], m[q]), c = exp2f(M[q] - top), f = exp2f(m[q] - top);
+          if (l[x][q] == 0.f) continue;               // the part holds nothing that the row sees
+          const float top = fmaxf(M[q], m[x][q]), c = exp2f(M[q] - top), f = exp2f(m[x][q] - top);
           M[q] = top;
-          L[q] = L[q] * c + l[q] * f;
-          A[q].x = A[q].x * c + o[q].x * f;
-          A[q].y = A[q].y * c + o[q].y * f;
-          A[q].z = A[q].z * c + o[q].z * f;
-          A[q].w = A[q].w * c + o[q].w * f;
+          L[q] = L[q] * c + l[x][q] * f;
+          A[q].x = A[q].x * c + o[x][q].x * f;
+          A[q].y = A[q].y * c + o[x][q].y * f;
+          A[q].z = A[q].z * c + o[x][q].z * f;
+          A[q].w = A[q].w * c + o[x][q].w * f;
         }
-      }
-#pragma unroll 1
-      for (int q = 0; q < R; ++q) {
-        const int i = it.row0 + ((row0 + q) & (P - 1)), head = it.head + (row0 + q) / P;
-        if (i >= it.rows) continue;
-        // registers indexed by q: picked without an array in memory
-        float4 y = A[0];
-        float mq = M[0], lq = L[0];
+    }
 #pragma unroll
-        for (int e = 1; e < R; ++e)
-          if (e == q) y = A[e], mq = M[e], lq = L[e];
-        const float inv = lq == 0.f ? 0.f : 1.f / lq;
-        y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-        float lse2 = mq + log2f(lq);
-        const uint32_t todo = nan_of(y);
-        if (__any_sync(0xffffffffu, todo != 0)) y = redo_row<F16>(a, it, i, head, todo, y, &lse2, lane);
-        const size_t row = (size_t)(it.start + i) * v.s.H + head;
-        if (!RF_IDX_OK(row, all_rows)) continue;
-        *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
-            make_uint2(pair::pack_16x2<F16>(y.x, y.y), pair::pack_16x2<F16>(y.z, y.w));
-        if (lane == 0 && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
-      }
+    for (int q = 0; q < R; ++q) {
+      const int i = it.row0 + ((row0 + q) & (P - 1)), head = it.head + ((row0 + q) >> v.P_log2);
+      const size_t row = (size_t)(it.start + i) * v.s.H + head;
+      if (i >= it.rows || !RF_IDX_OK(row, all_rows)) continue;
+      const float inv = L[q] == 0.f ? 0.f : 1.f / L[q];
+      float4 y = make_float4(A[q].x * inv, A[q].y * inv, A[q].z * inv, A[q].w * inv);
+      float lse2 = M[q] + log2f(L[q]);
+      const uint32_t todo = nan_of(y);
+      if (__any_sync(0xffffffffu, todo != 0)) y = redo_row<F16>(a, it, i, head, todo, y, &lse2, lane);
+      *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
+          make_uint2(pair::pack_16x2<F16>(y.x, y.y), pair::pack_16x2<F16>(y.z, y.w));
+      if (lane == 0 && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
     }
   }
   if (flag == 0) return;
   if (rho < ranges) {
-    RangeItem it;
-    first_item(v, rho, it);
+    RangeItem whole;
+    first_item(v, rho, whole);
     for (;;) {
-      for (int q = warp; it.slot < 0 && q < FIN_ROWS; q += FIN_WARPS) {
-        const int t = part * FIN_ROWS + q, i = it.row0 + (t & (P - 1)), head = it.head + t / P;
+      it.b = whole.b, it.start = whole.start, it.rows = whole.rows, it.len = whole.len;
+      it.head = whole.head, it.kvh = whole.kvh, it.row0 = whole.row0;
+      for (int q = warp; whole.slot < 0 && q < FIN_ROWS; q += FIN_WARPS) {
+        const int t = part * FIN_ROWS + q, i = it.row0 + (t & (P - 1)), head = it.head + (t >> v.P_log2);
         const size_t row = (size_t)(it.start + i) * v.s.H + head;
         if (i >= it.rows || !RF_IDX_OK(row, all_rows)) continue;
         const float4 y = widen4<F16>(a.out + row * HD * 2, lane);
@@ -500,8 +487,8 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
         // against the reference that the row started from left it at -inf
         if (lane == 0 && a.lse != nullptr && a.lse[row] == -INFINITY && lse2 == lse2) a.lse[row] = lse2 * kLn2;
       }
-      if (it.left == 0) break;
-      step_item(v, it);
+      if (whole.left == 0) break;
+      step_item(v, whole);
     }
   }
   __syncthreads();
