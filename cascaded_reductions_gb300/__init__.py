@@ -136,6 +136,10 @@ def _entry(name):
              "rf_attn_decode_weights", "rf_cache_evict"))
 
 
+_PAGE_TABLES, _QK_NORM_ROPE, _ATTN_PAGED = map(_entry, ("rf_page_tables", "rf_qk_norm_rope",
+                                                        "rf_attn_paged"))
+
+
 class RFError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -1082,6 +1086,10 @@ def page_tables(lens, news, table, stack, n_free, page, tokens, lens_out=None, n
     if stream is not None:
         return _within(stream, lens, page_tables, lens, news, table, stack, n_free, page, tokens,
                        lens_out, n_free_out)
+    if _calls is not None and lens_out is None and n_free_out is None:
+        r = _calls.page_tables(_PAGE_TABLES, lens, news, table, stack, n_free, page, tokens)
+        if r is not None:
+            return _done(r, "rf_page_tables")
     new = dict(device=lens.device, dtype=torch.int32)
     starts = torch.empty(lens.shape[0] + 1, **new)
     positions, slots = torch.empty(tokens, **new), torch.empty(tokens, **new)
@@ -1103,6 +1111,11 @@ def qk_norm_rope(q, k, positions, freq, q_weight=None, k_weight=None, axis=None,
     if stream is not None:
         return _within(stream, q, qk_norm_rope, q, k, positions, freq, q_weight, k_weight, axis,
                        interleaved, eps, v, slots, kp, vp)
+    if _calls is not None:
+        r = _calls.qk_norm_rope(_QK_NORM_ROPE, q, k, positions, freq, q_weight, k_weight, axis, interleaved,
+                                eps, v, slots, kp, vp)
+        if r is not None:
+            return _done(r, "rf_qk_norm_rope") if kp is None else _done(r, "rf_qk_norm_rope")[0]
     if (slots is None) != (kp is None):
         raise ValueError("slots, kp and vp come together")
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -1156,6 +1169,10 @@ def attn_paged(q, kp, vp, table, plan, scale=None, stream=None):
         return _within(stream, q, attn_paged, q, kp, vp, table, plan, scale)
     if q.dim() != 3 or kp.dim() != 4 or table.dim() != 2:
         raise ValueError("q must be [T, H, D], kp [pages, Hkv, page, D] and table [B, width]")
+    if _calls is not None:
+        r = _calls.attn_paged(_ATTN_PAGED, q, kp, vp, table, *plan, scale)
+        if r is not None:
+            return _done(r, "rf_attn_paged")
     got = (q.get_device(), table.shape[0], q.shape[0], q.shape[1], kp.shape[1])
     if got != plan.sizes:
         raise ValueError(f"plan was made for (device, B, T, H, Hkv) = {plan.sizes}, the call has {got}")

@@ -222,8 +222,7 @@ __device__ __forceinline__ void st_row32(void* dst, const uint32_t (&w)[16], boo
 //   Row, row_of_item(it, rank, row, kh)  of an item, for a softmax thread: which blocks hide
 //                              nothing from its warp (Row::all(j)); for the others, instead of
 //                              sees() and mask(),
-//   visible(it, j, rank, row, kh, vis)  sets a bit per key that the row sees; whether the warp
-//                              sees any
+//   visible(it, j, rank, row, kh, vis)  sets a bit per key that the row sees
 //   boxed(pending)             whether the warp's 32 rows leave by send(); else pack has
 //                              stored the columns
 template <class P, class = void>
@@ -481,9 +480,8 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         if constexpr (is_paged<P>()) {
           // worked out while the products are under way, and kept out of the registers
           const bool hides = !row.all(j);
-          bool some = true;
-          if (hides) some = p.visible(it, j, rank, r, kh, sh->vis[threadIdx.x]);
-          ok = some ? block(Words<4>{}, j, hides) : block(Words<0>{}, j, true);
+          if (hides) p.visible(it, j, rank, r, kh, sh->vis[threadIdx.x]);
+          ok = block(Words<4>{}, j, hides);
         } else if constexpr (P::PARTIAL) {
           const bool some = p.sees(it, j, rank, r, kh);
           ok = some ? block(Words<4>{}, j, true) : block(Words<0>{}, j, true);

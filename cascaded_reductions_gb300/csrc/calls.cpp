@@ -369,7 +369,155 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (function, lens, news, table, stack, n_free, page, tokens); gives starts, positions, slots,
+// lens_out and n_free_out
+PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    int page, tokens;
+    if (n != 8 || !pointer(a[0], &fn) || !count(a[6], &page) || !count(a[7], &tokens)) Py_RETURN_NONE;
+    const at::Tensor *lens = tensor(a[1]), *news = tensor(a[2]), *table = tensor(a[3]), *stack = tensor(a[4]),
+                     *n_free = tensor(a[5]);
+    if (!lens || !news || !table || !stack || !n_free || !lens->is_cuda() || table->dim() != 2 ||
+        stack->dim() != 1 || tokens < 1)
+      Py_RETURN_NONE;
+    const int64_t B = table->size(0), width = table->size(1), pages = stack->size(0);
+    const int dev = (int)lens->get_device();
+    if (B > 0x7fffffffLL || width > 0x7fffffffLL || pages > 0x7fffffffLL || !is(*lens, dev, at::kInt, {B}) ||
+        !is(*news, dev, at::kInt, {B}) || !is(*table, dev, at::kInt, {B, width}) ||
+        !is(*stack, dev, at::kInt, {pages}) || !is(*n_free, dev, at::kInt, {1}) ||
+        c10::cuda::current_device() != dev)
+      Py_RETURN_NONE;
+    at::Tensor starts = like(*lens, {B + 1}, at::kInt), positions = like(*lens, {tokens}, at::kInt);
+    at::Tensor slots = like(*lens, {tokens}, at::kInt);
+    at::Tensor lens_out = like(*lens, {B}, at::kInt), n_free_out = like(*lens, {1}, at::kInt);
+    const auto in = [](const at::Tensor& t) { return static_cast<const int32_t*>(t.const_data_ptr()); };
+    const auto out = [](const at::Tensor& t) { return static_cast<int32_t*>(t.mutable_data_ptr()); };
+    if (PyObject* e = failed([&] {
+          return reinterpret_cast<decltype(&rf_page_tables)>(fn)(
+              in(*lens), in(*news), (int)B, out(*table), (int)width, out(*stack), (int)pages, in(*n_free),
+              page, tokens, out(starts), out(positions), out(slots), out(lens_out), out(n_free_out),
+              stream_of(dev));
+        }))
+      return e;
+    return pack(std::move(starts), std::move(positions), std::move(slots), std::move(lens_out),
+                std::move(n_free_out));
+  });
+}
+
+// q, k or v [T, heads, D] with dense heads, and the elements from a token's row to the next.
+bool token_rows(const at::Tensor& t, int dev, at::ScalarType type, at::IntArrayRef sizes, long long* step) {
+  if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != type || t.sizes() != sizes ||
+      (sizes[2] > 1 && t.stride(2) != 1) || (sizes[1] > 1 && t.stride(1) != sizes[2]))
+    return false;
+  *step = sizes[0] > 1 ? t.stride(0) : sizes[1] * sizes[2];
+  return true;
+}
+
+// (function, q, k, positions, freq, q_weight, k_weight, axis, interleaved, eps, v, slots, kp, vp);
+// gives q, and k without a cache
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    if (n != 14 || !pointer(a[0], &fn) || !PyBool_Check(a[8]) || !PyFloat_CheckExact(a[9])) Py_RETURN_NONE;
+    const at::Tensor *q = tensor(a[1]), *k = tensor(a[2]), *positions = tensor(a[3]), *freq = tensor(a[4]);
+    const at::Tensor *qw, *kw, *axis, *v, *slots, *kp, *vp;
+    if (!q || !k || !positions || !freq || !optional_tensor(a[5], &qw) || !optional_tensor(a[6], &kw) ||
+        !optional_tensor(a[7], &axis) || !optional_tensor(a[10], &v) || !optional_tensor(a[11], &slots) ||
+        !optional_tensor(a[12], &kp) || !optional_tensor(a[13], &vp) || !q->is_cuda() || q->dim() != 3 ||
+        k->dim() != 3 || positions->dim() != 2 || freq->dim() != 1)
+      Py_RETURN_NONE;
+    if ((v != nullptr) != (slots != nullptr) || (v != nullptr) != (kp != nullptr) ||
+        (v != nullptr) != (vp != nullptr) || (kp && kp->dim() != 4))
+      Py_RETURN_NONE;
+    for (const at::Tensor* t : {q, k, positions, freq, kp})
+      if (t)
+        for (const int64_t s : t->sizes())
+          if (s > 0x3fffffffLL) Py_RETURN_NONE;
+    const at::ScalarType type = q->scalar_type();
+    const int dev = (int)q->get_device(), code = type_code(type);
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2), Hkv = k->size(1), half = freq->size(0);
+    const int64_t axes = positions->size(0), pages = kp ? kp->size(0) : 0, page = kp ? kp->size(2) : 0;
+    long long q_step, k_step, v_step = 0;
+    const at::Tensor* w = qw ? qw : kw;
+    const at::ScalarType w_type = w ? w->scalar_type() : type;
+    if (code < 0 || (w_type != type && w_type != at::kFloat) || !token_rows(*q, dev, type, {T, H, D}, &q_step) ||
+        !token_rows(*k, dev, type, {T, Hkv, D}, &k_step) || !is(*positions, dev, at::kInt, {axes, T}) ||
+        !is(*freq, dev, at::kFloat, {half}) || (qw && !is(*qw, dev, w_type, {D})) ||
+        (kw && !is(*kw, dev, w_type, {D})) || (axis && !is(*axis, dev, at::kInt, {half})) ||
+        (v && !token_rows(*v, dev, type, {T, Hkv, D}, &v_step)) || (slots && !is(*slots, dev, at::kInt, {T})) ||
+        (kp && !is(*kp, dev, type, {pages, Hkv, page, D})) || (vp && !is(*vp, dev, type, kp->sizes())) ||
+        c10::cuda::current_device() != dev)
+      Py_RETURN_NONE;
+    at::Tensor q_out = like(*q, {T, H, D}, type), k_out;
+    if (!kp) k_out = like(*k, {T, Hkv, D}, type);
+    if (PyObject* e = failed([&] {
+          return reinterpret_cast<decltype(&rf_qk_norm_rope)>(fn)(
+              q->const_data_ptr(), q_step, k->const_data_ptr(), k_step, optional_address<void>(v), v_step,
+              (int)T, (int)H, (int)Hkv, (int)D, optional_address<void>(qw), optional_address<void>(kw),
+              type_code(w_type), (float)PyFloat_AS_DOUBLE(a[9]),
+              static_cast<const int32_t*>(positions->const_data_ptr()), (int)axes,
+              static_cast<const float*>(freq->const_data_ptr()), optional_address<int32_t>(axis),
+              (int)(2 * half), a[8] == Py_True, code, optional_address<int32_t>(slots), (int)pages, (int)page,
+              q_out.mutable_data_ptr(), kp ? kp->mutable_data_ptr() : k_out.mutable_data_ptr(),
+              vp ? vp->mutable_data_ptr() : nullptr, stream_of(dev));
+        }))
+      return e;
+    return kp ? pack(std::move(q_out)) : pack(std::move(q_out), std::move(k_out));
+  });
+}
+
+// (function, q, kp, vp, table, plan, sizes, max_new, max_len, window, sinks, scale); sizes: (device,
+// B, T, H, Hkv)
+PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    int max_new, max_len, window, sinks;
+    float scale;
+    if (n != 12 || !pointer(a[0], &fn)) Py_RETURN_NONE;
+    const at::Tensor *q = tensor(a[1]), *kp = tensor(a[2]), *vp = tensor(a[3]), *table = tensor(a[4]),
+                     *plan = tensor(a[5]);
+    if (!q || !kp || !vp || !table || !plan || !q->is_cuda() || q->dim() != 3 || kp->dim() != 4 ||
+        table->dim() != 2 || plan->dim() != 1 || !PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 5 ||
+        !count(a[7], &max_new) || !count(a[8], &max_len) || !count(a[9], &window) || !count(a[10], &sinks))
+      Py_RETURN_NONE;
+    for (const at::Tensor* t : {q, kp, table})
+      for (const int64_t s : t->sizes())
+        if (s > 0x7fffffffLL) Py_RETURN_NONE;
+    const at::ScalarType type = q->scalar_type();
+    const int dev = (int)q->get_device(), code = type_code(type);
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2), pages = kp->size(0), Hkv = kp->size(1);
+    const int64_t page = kp->size(2), B = table->size(0), width = table->size(1);
+    const int64_t want[5] = {dev, B, T, H, Hkv};
+    for (int i = 0; i < 5; ++i) {
+      int x;
+      if (!count(PyTuple_GET_ITEM(a[6], i), &x) || x != want[i]) Py_RETURN_NONE;
+    }
+    if (code < 0 || !scale_of(a[11], (int)D, &scale) || !q->is_contiguous() ||
+        !is(*kp, dev, type, {pages, Hkv, page, D}) || !is(*vp, dev, type, kp->sizes()) ||
+        !is(*table, dev, at::kInt, {B, width}) || !is(*plan, dev, at::kByte, plan->sizes()) ||
+        c10::cuda::current_device() != dev)
+      Py_RETURN_NONE;
+    at::Tensor out = like(*q, q->sizes(), type), lse = like(*q, {T, H}, at::kFloat);
+    if (PyObject* e = failed([&] {
+          return reinterpret_cast<decltype(&rf_attn_paged)>(fn)(
+              q->const_data_ptr(), kp->const_data_ptr(), vp->const_data_ptr(), (int)pages, (int)page,
+              static_cast<const int32_t*>(table->const_data_ptr()), (int)width, plan->mutable_data_ptr(),
+              (size_t)plan->numel(), (int)B, (int)T, (int)H, (int)Hkv, (int)D, max_new, max_len, window, sinks,
+              scale, code, out.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()),
+              stream_of(dev));
+        }))
+      return e;
+    return pack(std::move(out), std::move(lse));
+  });
+}
+
 PyMethodDef methods[] = {
+    {"page_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_tables)), METH_FASTCALL,
+     nullptr},
+    {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope)), METH_FASTCALL,
+     nullptr},
+    {"attn_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attn_paged)), METH_FASTCALL, nullptr},
     {"decode_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_window)),
      METH_FASTCALL, nullptr},
     {"decode_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_shared)),

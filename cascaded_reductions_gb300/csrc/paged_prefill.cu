@@ -224,8 +224,7 @@ struct PagedPrefill {
     if (window > 0) end = min(end, ((top - (low + 31 - window + 1)) >> 8) + 1);
     return {first - it.j0, end - it.j0};
   }
-  __device__ __forceinline__ bool visible(const Item& it, int j, int rank, int r, int kh,
-                                          uint4& bits) const {
+  __device__ __forceinline__ void visible(const Item& it, int j, int rank, int r, int kh, uint4& bits) const {
     const int block = block_of(it, j), base = block * BN + kh * BM;
     const int p = position(it, rank, r), window = a.v.s.window;
     const bool moved = holds_last(it, block) && lacking(it) != 0;
@@ -243,7 +242,6 @@ struct PagedPrefill {
       vis[q] = (plain & below(c0 - 32 * q)) | (behind & ~below(c0 + d - 32 * q));
     }
     bits = make_uint4(vis[0], vis[1], vis[2], vis[3]);
-    return __any_sync(0xffffffffu, (vis[0] | vis[1] | vis[2] | vis[3]) != 0);
   }
 
   __device__ __forceinline__ bool partial(const Item& it) const { return it.slot >= 0; }
