@@ -35,6 +35,7 @@ constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int MROWS = kPagedTileRows;
 constexpr size_t SMEM_BYTES = (size_t)WARPS * RING_BYTES;
 constexpr int MERGE_PITCH = HD + 8;
+constexpr int FEW_ROWS = 4;
 static_assert((size_t)WARPS * MROWS * MERGE_PITCH * 4 <= SMEM_BYTES, "the warps' accumulators reuse the rings");
 
 template <int ID, int N>
@@ -62,30 +63,68 @@ struct Work {
   }
 };
 
-__device__ __forceinline__ int page_of(const PagedAttn& a, const Work& w, int tile) {
+__device__ __forceinline__ int page_of(const PagedAttn& a, int b, int tile) {
   const int i = tile * TK >> a.page_log2;
-  const size_t at = (size_t)w.b * a.width + i;
+  const size_t at = (size_t)b * a.width + i;
   return i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width) ? a.table[at] : -1;
 }
-
-// Keys 16 tile .. + 15 into a stage: K rows, then V rows, 16-byte chunks permuted by row
-// % 8.  Rows past the request's end, and those of a page outside the cache, are zeros.
-__device__ __forceinline__ void copy_tile(const PagedAttn& a, const Work& w, int tile, int page, uint32_t stage,
-                                          uint64_t policy, int lane) {
-  const bool has = (unsigned)page < (unsigned)a.pages;
-  const int key0 = tile * TK, mask = (1 << a.page_log2) - 1;
-  const size_t row0 = (((size_t)(has ? page : 0) * a.v.s.Hkv + w.hk) << a.page_log2) + (key0 & mask);
-#pragma unroll
-  for (int u = 0; u < TK / 2; ++u) {
-    const int r = 2 * u + (lane >> 4), c = lane & 15;
-    const bool in = has && key0 + r < w.len &&
-                    RF_IDX_OK(row0 + r, ((size_t)a.pages * a.v.s.Hkv) << a.page_log2);
-    const size_t off = (row0 + (in ? r : 0)) * ROW_BYTES + c * 16;
-    const uint32_t dst = stage + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
-    cp_async16(dst, a.kp + off, in ? 16u : 0u, policy);
-    cp_async16(dst + TK * ROW_BYTES, a.vp + off, in ? 16u : 0u, policy);
-  }
+// cache rows in front of the tile's keys, where the page is one
+__device__ __forceinline__ size_t row_of(const PagedAttn& a, int page, int hk, int tile) {
+  return (((size_t)page * a.v.s.Hkv + hk) << a.page_log2) + (tile * TK & ((1 << a.page_log2) - 1));
 }
+
+// What a warp copies of a unit: every fourth tile of 16 keys, into a ring of stages.  Its
+// lanes hold the page numbers of 32 tiles, and ask for the next 32 in time: behind a
+// stream that takes all of the memory's rate such a load may take longer than a tile.
+struct Stream {
+  int b, hk, len, sink_tiles, lo_tile;
+  int t, end, n;                        // next tile, the unit's last one, tiles so far
+  int ids, ahead;                       // the lane's page numbers
+  uint32_t ring;
+  int in;                               // stage of the next copies
+
+  __device__ __forceinline__ int key_tile(int i) const { return i < sink_tiles ? i : i - sink_tiles + lo_tile; }
+  __device__ __forceinline__ int id_of(const PagedAttn& a, int i) const {
+    return i < end ? page_of(a, b, key_tile(i)) : -1;
+  }
+  __device__ __forceinline__ void open(const PagedAttn& a, const PagedUnit& u, const int* first, int head, int warp,
+                                       int lane) {
+    const PagedTiles k(u.n, u.len, a.v.s.window, a.v.s.sinks);
+    b = u.b, hk = head, len = u.len;
+    sink_tiles = k.sink_tiles, lo_tile = k.lo_tile;
+    t = u.step0 * WARPS + warp;
+    end = min(k.tiles, u.step1 * WARPS);
+    n = 0;
+    ids = first[lane * WARPS + warp];
+  }
+  // Keys of the next tile into the next stage: K rows, then V rows, 16-byte chunks permuted
+  // by row % 8.  Rows past the request's end, and those of a page outside the cache, are zeros.
+  __device__ __forceinline__ void issue(const PagedAttn& a, uint64_t policy, int lane) {
+    if (t < end) {
+      const int tile = key_tile(t), now = __shfl_sync(0xffffffffu, ids, n & 31);
+      ++n;
+      if ((n & 31) == 8) ahead = id_of(a, t + (25 + lane) * WARPS);
+      if ((n & 31) == 0) ids = ahead;
+      const bool has = (unsigned)now < (unsigned)a.pages;
+      const int rows = has ? min(len - tile * TK, TK) : 0, r0 = lane >> 4, c = lane & 15;
+      const size_t first = row_of(a, has ? now : 0, hk, tile), at = first * ROW_BYTES + c * 16;
+      const uint8_t *k = a.kp + at, *v = a.vp + at;
+      const uint32_t stage = ring + (uint32_t)in * STAGE_BYTES;
+#pragma unroll
+      for (int u = 0; u < TK / 2; ++u) {
+        const int r = 2 * u + r0;
+        const bool on = r < rows && RF_IDX_OK(first + r, ((size_t)a.pages * a.v.s.Hkv) << a.page_log2);
+        const int off = on ? r * ROW_BYTES : 0;
+        const uint32_t dst = stage + r * ROW_BYTES + ((c ^ (r & 7)) << 4);
+        cp_async16(dst, k + off, on ? 16u : 0u, policy);
+        cp_async16(dst + TK * ROW_BYTES, v + off, on ? 16u : 0u, policy);
+      }
+    }
+    cp_async_commit();
+    t += WARPS;
+    in = in + 1 == STAGES ? 0 : in + 1;
+  }
+};
 
 // One warp's running state: rows lane / 4 (index 0) and + 8 (index 1); acc[d] holds
 // columns 8 d + 2 (lane % 4) and + 1 of both.
@@ -241,10 +280,9 @@ __device__ __noinline__ float4 redo_columns(const PagedAttn& a, const Work w, in
   const float4 x = load_row4<F16>(a.q + w.at(a, r) * ROW_BYTES, lane);
   float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int t = t0; t < t1; ++t) {
-    const int tile = w.key_tile(t), page = page_of(a, w, tile);
+    const int tile = w.key_tile(t), page = page_of(a, w.b, tile);
     const bool has = (unsigned)page < (unsigned)a.pages;
-    const size_t row0 = (((size_t)(has ? page : 0) * a.v.s.Hkv + w.hk) << a.page_log2) +
-                        (tile * TK & ((1 << a.page_log2) - 1));
+    const size_t row0 = row_of(a, has ? page : 0, w.hk, tile);
     for (int u0 = 0; u0 < TK; u0 += 8) {
       float s[8];
       float4 v[8];
@@ -296,7 +334,7 @@ __device__ __forceinline__ void write_row(const PagedAttn& a, size_t row, float4
 
 // Row r of the CTA's warps merged by one warp, four columns per lane, into the output or
 // into the unit's state.
-template <bool F16>
+template <bool F16, int PITCH_ROWS>
 __device__ __forceinline__ void merge_warps(const PagedAttn& a, const Work& w, const float* acc_buf,
                                             const float2 (*ml_buf)[MROWS], int r, bool direct, size_t state0,
                                             int t0, int t1, int lane) {
@@ -308,7 +346,7 @@ __device__ __forceinline__ void merge_warps(const PagedAttn& a, const Work& w, c
   for (int i = 0; i < WARPS; ++i) {
     const float2 ml = ml_buf[i][r];
     const float f = exp2f(ml.x - ref_of(M));
-    const float4 v = *reinterpret_cast<const float4*>(acc_buf + (i * MROWS + r) * MERGE_PITCH + lane * 4);
+    const float4 v = *reinterpret_cast<const float4*>(acc_buf + (i * PITCH_ROWS + r) * MERGE_PITCH + lane * 4);
     L = fmaf(f, ml.y, L);
     A.x = fmaf(f, v.x, A.x);
     A.y = fmaf(f, v.y, A.y);
@@ -406,89 +444,109 @@ __device__ __forceinline__ void merge_pieces(const PagedAttn& a, const Work& w, 
   }
 }
 
-__device__ __forceinline__ PagedUnit load_unit(const PagedUnit* p) {
-  PagedUnit u;
-  int4* d = reinterpret_cast<int4*>(&u);
-  const int4* s = reinterpret_cast<const int4*>(p);
-  static_assert(sizeof(PagedUnit) == 48, "three 16-byte loads");
-  d[0] = s[0], d[1] = s[1], d[2] = s[2];
-  return u;
-}
-
-template <bool F16>
+// FEW: units have up to FEW_ROWS rows, so that the warps' accumulators have a place beside
+// the rings, and a unit's first copies start before the last one's rows are merged.
+template <bool F16, bool FEW>
 __global__ void __launch_bounds__(THREADS, 2)
 paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 sm_ml[WARPS][MROWS];
+  __shared__ __align__(16) PagedUnit sm_unit[2];
+  __shared__ int sm_pages[2][32 * WARPS];         // page numbers of a unit's first tiles
   __shared__ int sm_next[2], sm_last;
+  static_assert(sizeof(PagedUnit) == 48, "three 16-byte loads");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hkv = a.v.s.Hkv;
   // behind the pair kernel of the same call, which has waited for what was before it
   if (!behind_pairs) wait_prerequisite();
   allow_dependents();
+  auto fetch_unit = [&](int i, int to) {          // by the closing warp
+    const int unit = i / Hkv;
+    if (lane < 3 && RF_IDX_OK(unit, a.v.unit_cap))
+      reinterpret_cast<int4*>(&sm_unit[to])[lane] = reinterpret_cast<const int4*>(a.v.units + unit)[lane];
+  };
+  auto fetch_pages = [&](int at) {
+    __syncwarp();
+    const PagedUnit& u = sm_unit[at];
+    const PagedTiles k(u.n, u.len, a.v.s.window, a.v.s.sinks);
+    const int t0 = u.step0 * WARPS, end = min(k.tiles, u.step1 * WARPS);
+#pragma unroll
+    for (int e = 0; e < WARPS; ++e) {
+      const int t = t0 + e * 32 + lane;
+      sm_pages[at][e * 32 + lane] =
+          t < end ? page_of(a, u.b, t < k.sink_tiles ? t : t - k.sink_tiles + k.lo_tile) : -1;
+    }
+  };
+  int i = blockIdx.x;                             // below the units that the plan has room for
+  if (warp == WARPS) fetch_unit(i, 0);            // asked for before it is known whether it is one
   const bool planned = a.v.head[kPlanMark] == (int)a.v.mark;
   const int total = planned ? min(a.v.head[kPlanUnits], a.v.unit_cap) * Hkv : 0;
   const bool queued = total > (int)gridDim.x;
   // a large call's cache is read once and goes first; a small one's may be read again
   const uint64_t policy = l2_policy(queued);
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + (warp & 3) * RING_BYTES;
-  float* acc_buf = reinterpret_cast<float*>(smem);
   constexpr int dtype = F16 ? RF_F16 : RF_BF16;
+  constexpr int PITCH_ROWS = FEW ? FEW_ROWS : MROWS;
+  float* acc_buf = reinterpret_cast<float*>(smem + (FEW ? WARPS * RING_BYTES : 0));
+  if (warp == WARPS && i < total) fetch_pages(0);
+  __syncthreads();
 
-  int turn = 0;
-  for (int i = blockIdx.x; i < total; ++turn) {
-    const int unit = i / Hkv, hk = i - unit * Hkv;
-    if (!RF_IDX_OK(unit, a.v.unit_cap)) break;
-    const PagedUnit u = load_unit(a.v.units + unit);
-    const Work w(a, u, hk);
-    int next = total;
-    if (warp < WARPS) {
-      int in = 0;                       // the stage that the next copies go to
-      const int t_end = min(w.t.tiles, u.step1 * WARPS);
-      int t_in = u.step0 * WARPS + warp;
-      int page = t_in < t_end ? page_of(a, w, w.key_tile(t_in)) : -1;
-      auto issue = [&]() {
-        if (t_in < t_end) {
-          const int tile = w.key_tile(t_in), now = page;
-          if (t_in + WARPS < t_end) page = page_of(a, w, w.key_tile(t_in + WARPS));
-          copy_tile(a, w, tile, now, ring + (uint32_t)in * STAGE_BYTES, policy, lane);
-        }
-        cp_async_commit();
-        t_in += WARPS;
-        in = in + 1 == STAGES ? 0 : in + 1;
-      };
+  Stream in;
+  in.ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + (warp & 3) * RING_BYTES;
+  in.in = 0;
+  int slot = 0;                                   // stage of the unit's next tile
+  auto begin = [&](int at, int head) {
+    in.open(a, sm_unit[at], sm_pages[at], head, warp, lane);
+    slot = in.in;
 #pragma unroll
-      for (int k = 0; k < STAGES - 1; ++k) issue();
+    for (int k = 0; k < STAGES - 1; ++k) in.issue(a, policy, lane);
+  };
+  if (warp < WARPS && i < total) begin(0, i - i / Hkv * Hkv);
+  for (int turn = 0; i < total; ++turn) {
+    const PagedUnit& u = sm_unit[turn & 1];
+    const int unit = i / Hkv, hk = i - unit * Hkv;
+    if (warp < WARPS) {
       State<F16> st;
-      st.start(a, w, lane);
-      int slot = 0;
-      for (int t = u.step0 * WARPS + warp; t < t_end; t += WARPS) {
+      st.start(a, Work(a, u, hk), lane);
+      for (int t = u.step0 * WARPS + warp, end = in.end; t < end; t += WARPS) {
         cp_async_wait<STAGES - 2>();
         __syncwarp();                   // every lane's copies of this tile landed, the last is read
-        issue();
-        st.tile(a, ring + (uint32_t)slot * STAGE_BYTES, w.key_tile(t) * TK, lane);
+        in.issue(a, policy, lane);
+        st.tile(a, in.ring + (uint32_t)slot * STAGE_BYTES, in.key_tile(t) * TK, lane);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
       }
       cp_async_wait<0>();
       st.close();
-      named_sync<1, WARPS * 32>();      // the rings are free
-      st.give(acc_buf + warp * MROWS * MERGE_PITCH, sm_ml[warp], w.rows, lane);
-      named_sync<1, WARPS * 32>();
-      const size_t state0 = ((size_t)unit * Hkv + hk) * a.v.s.unit_rows();
-      for (int r = warp; r < w.rows; r += WARPS)
-        merge_warps<F16>(a, w, acc_buf, sm_ml, r, u.pieces == 1, state0, u.step0 * WARPS, t_end, lane);
+      if (!FEW) named_sync<1, WARPS * 32>();      // the rings are free
+      st.give(acc_buf + warp * PITCH_ROWS * MERGE_PITCH, sm_ml[warp], min(MROWS, u.n * a.v.G - u.tile * MROWS),
+              lane);
     } else if (queued) {
+      int next = 0;
       if (lane == 0) {
         const int got = atomicAdd(a.v.head + kPlanQueue, 1);
-        sm_next[turn & 1] = (int)gridDim.x + got;
+        next = (int)gridDim.x + got;
+        sm_next[turn & 1] = next;
         // every unit fetches once, so this was the last fetch
         if (got == total - 1) atomicExch(a.v.head + kPlanQueue, 0);
       }
-      __syncwarp();
+      next = __shfl_sync(0xffffffffu, next, 0);
+      if (next < total) {
+        fetch_unit(next, (turn + 1) & 1);
+        fetch_pages((turn + 1) & 1);
+      }
     }
-    named_sync<2, THREADS>();           // states stored, next unit known
-    if (queued) next = sm_next[turn & 1];
+    named_sync<2, THREADS>();           // rows given, next unit known
+    const int next = queued ? sm_next[turn & 1] : total;
+    if (warp < WARPS) {
+      const int end = in.end;
+      if (FEW && next < total) begin((turn + 1) & 1, next - next / Hkv * Hkv);
+      const Work w(a, u, hk);
+      const size_t state0 = ((size_t)unit * Hkv + hk) * a.v.s.unit_rows();
+      for (int r = warp; r < w.rows; r += WARPS)
+        merge_warps<F16, PITCH_ROWS>(a, w, acc_buf, sm_ml, r, u.pieces == 1, state0, u.step0 * WARPS, end, lane);
+    }
+    named_sync<2, THREADS>();           // states stored
     if (u.pieces > 1) {
+      const Work w(a, u, hk);
       const size_t at = (size_t)u.first * Hkv + hk;
       if (warp == WARPS) {
         int last = 0;
@@ -521,20 +579,27 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
         }
       }
     }
+    if (!FEW && warp < WARPS && next < total) begin((turn + 1) & 1, next - next / Hkv * Hkv);
     i = next;
   }
   if (behind_pairs) wait_prerequisite();   // a kernel ends after the one before it
 }
 
-template <bool F16>
-rf_status launch_t(const PagedAttn& a, cudaStream_t st) {
+template <bool F16, bool FEW>
+rf_status launch_f(const PagedAttn& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  if (smem_attr(paged_decode_kernel<F16>, SMEM_BYTES, done) != RF_OK) return RF_ERR_CUDA;
+  constexpr size_t bytes = SMEM_BYTES + (FEW ? (size_t)WARPS * FEW_ROWS * MERGE_PITCH * 4 : 0);
+  if (smem_attr(paged_decode_kernel<F16, FEW>, bytes, done) != RF_OK) return RF_ERR_CUDA;
   const int sms = tc::sm_count();
   if (sms <= 0) return RF_ERR_CUDA;
   const long long most = (long long)a.v.unit_cap * a.v.s.Hkv;
   const unsigned grid = (unsigned)(most < 2ll * sms ? most : 2ll * sms);
-  return launch_after(paged_decode_kernel<F16>, grid, THREADS, SMEM_BYTES, st, a, a.v.s.some_pairs());
+  return launch_after(paged_decode_kernel<F16, FEW>, grid, THREADS, bytes, st, a, a.v.s.some_pairs());
+}
+
+template <bool F16>
+rf_status launch_t(const PagedAttn& a, cudaStream_t st) {
+  return a.v.s.unit_rows() <= FEW_ROWS ? launch_f<F16, true>(a, st) : launch_f<F16, false>(a, st);
 }
 
 }  // namespace
