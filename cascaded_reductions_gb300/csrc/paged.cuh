@@ -20,6 +20,7 @@ constexpr int kPagedBlock = 256;        // keys of the pair kernel's blocks
 constexpr int kPagedPairRows = 256;
 constexpr int kPagedSlotFloats = kPagedPairRows * (128 + 2);   // a partial state: O, m, l
 constexpr int kPagedRounds = 4;
+constexpr int kPagedFewSteps = 16;      // steps of 64 keys per CTA of a small call of the streaming kernel
 
 // The sizes that a plan and the calls over it share.
 struct PagedShape {

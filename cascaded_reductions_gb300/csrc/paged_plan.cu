@@ -20,7 +20,6 @@ namespace rf {
 namespace {
 
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int FEW_STEPS = 16;           // per CTA of a small call
 constexpr int MANY_STEPS = 12;          // of a large call's piece at least
 constexpr int MANY_UNITS = 8;           // and per CTA at most, on average
 constexpr int ROUND_BLOCKS = 32;        // of a range at least, where there are several rounds
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   // the streaming kernel's pieces: of candidates a 16th apart the smallest that fits one wave
   const long long ctas = steps * s.Hkv;
   long long piece = max(1ll, (ctas + a.slots - 1) / a.slots);
-  const bool few = piece <= FEW_STEPS;
+  const bool few = piece <= kPagedFewSteps;
   if (few) {
     const long long p = piece + (piece * warp + 15) / 16;
     long long units = 0;
