@@ -580,7 +580,7 @@ rf_status rf_attn_paged(const void* q, const void* kp, const void* vp, int pages
     if (st != RF_OK) return st;
   }
   st = rf::launch_paged_decode(a, dtype, as_stream(stream));
-  if (st != RF_OK || !pairs) return st;
+  if (st != RF_OK || s.few(rf::tc::sm_count())) return st;
   return rf::launch_paged_finish(a, dtype, as_stream(stream));
 }
 

@@ -38,6 +38,12 @@ struct PagedShape {
     const long long rows = (long long)max_new * G();
     return (int)((rows < kPagedRows ? rows : kPagedRows) + kPagedTileRows - 1) / kPagedTileRows;
   }
+  // whether the streaming kernel's call is small whatever the lengths: one launch, a CTA
+  // per unit; else the teams' kernel, and paged_finish_kernel
+  __host__ __device__ bool few(int sms) const {
+    const long long steps = (long long)B * tiles() * Hkv * ((max_len + 4 * kDecodeTile - 1) / (4 * kDecodeTile));
+    return !some_pairs() && steps <= kPagedFewSteps * 2ll * sms;
+  }
   __host__ __device__ int unit_rows() const {
     const long long rows = (long long)max_new * G();
     return rows < kPagedTileRows ? (int)rows : kPagedTileRows;
@@ -45,12 +51,12 @@ struct PagedShape {
 };
 
 // Words of a plan's head.
-enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanJoins, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
+enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanJoins, kPlanMerges, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
 
 // Where the parts of a plan lie, in bytes from its start.
 struct PagedLayout {
-  size_t seqs, before, ranges, joins, units, counters, unit_ml, unit_acc, slots, bytes;
-  int unit_cap, range_cap;
+  size_t seqs, before, ranges, joins, units, merges, counters, unit_ml, unit_acc, slots, bytes;
+  int unit_cap, range_cap, merge_cap;
   uint32_t mark;                        // of the sizes: a plan of others is refused on the device
 };
 
@@ -83,11 +89,12 @@ struct PagedView {
   const PagedRange* ranges;
   const PagedJoin* joins;
   const PagedUnit* units;
-  int* counters;
+  const int* merges;                    // first units of the 16-row tiles in several pieces
+  int* counters;                        // pieces of a small call's tiles that are done
   float2* unit_ml;                      // [unit][Hkv][unit_rows]
   float* unit_acc;                      // [unit][Hkv][unit_rows][128]
   float* slots;
-  int unit_cap, range_cap;
+  int unit_cap, range_cap, merge_cap;
   uint32_t mark;
   int G, packed, P_log2, groups, key_groups;   // heads per key head and per tile; positions of a
                                         // tile; head groups in all and per key head
@@ -183,7 +190,8 @@ inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* pla
   v.unit_ml = reinterpret_cast<float2*>(p + l.unit_ml);
   v.unit_acc = reinterpret_cast<float*>(p + l.unit_acc);
   v.slots = reinterpret_cast<float*>(p + l.slots);
-  v.unit_cap = l.unit_cap, v.range_cap = l.range_cap;
+  v.merges = reinterpret_cast<const int*>(p + l.merges);
+  v.unit_cap = l.unit_cap, v.range_cap = l.range_cap, v.merge_cap = l.merge_cap;
   v.mark = l.mark;
   v.G = s.G(), v.packed = s.packed(), v.P_log2 = 0;
   while ((1 << v.P_log2) < s.positions()) ++v.P_log2;

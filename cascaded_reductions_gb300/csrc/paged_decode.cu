@@ -49,9 +49,9 @@ constexpr int TEAM_BYTES = WARPS * RING_BYTES + MERGE_BYTES + MROWS * ROW_BYTES;
 constexpr size_t SMEM_BYTES = (size_t)TEAMS * TEAM_BYTES;
 static_assert(SMEM_BYTES + 4096 <= 232448, "exceeds the 227 KiB of shared memory a CTA may use");
 
-// A team's barriers: its streaming warps; all five at a unit's end; all five behind the
-// last one's count; its query rows have been read
-enum { kBarStream = 1, kBarEnd, kBarLast, kBarRows, kBars = 4 };
+// A team's barriers: its streaming warps; all five at a unit's end; its query rows have
+// been read
+enum { kBarStream = 1, kBarEnd, kBarRows, kBars = 3 };
 template <int N>
 __device__ __forceinline__ void named_sync(int id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
@@ -500,13 +500,13 @@ __device__ __forceinline__ void merge_pieces(const PagedAttn& a, const Work& w, 
 // shortest way from launch to output.
 template <bool F16>
 __global__ void __launch_bounds__(WARPS * 32, 2)
-paged_few_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs) {
+paged_few_kernel(const __grid_constant__ PagedAttn a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 sm_ml[WARPS][MERGE_ROWS], sm_redo[MROWS];
   __shared__ int sm_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hkv = a.v.s.Hkv;
   float* acc_buf = reinterpret_cast<float*>(smem + WARPS * RING_BYTES);
-  if (!behind_pairs) wait_prerequisite();
+  wait_prerequisite();
   allow_dependents();
   int total = 0x7fffffff;               // known with the first unit
   for (int i = blockIdx.x, turn = 0; i < total; i += (int)gridDim.x, ++turn) {
@@ -591,7 +591,6 @@ paged_few_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs) {
     }
     __syncthreads();                    // sm_last may be written again
   }
-  if (behind_pairs) wait_prerequisite();   // a kernel ends after the one before it
 }
 
 // What a team's warps hand one another; units are copied 16 bytes at a time.
@@ -600,7 +599,7 @@ struct alignas(16) Team {
   int pages[2][32 * WARPS];             // page numbers of a unit's first tiles
   float2 ml[WARPS][MERGE_ROWS], redo[MROWS];
   uint64_t ready;                       // a phase per unit: what comes behind it is known
-  int next[2], last;
+  int next[2];
 };
 
 template <bool F16>
@@ -664,7 +663,6 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
   const int total = planned ? min(a.v.head[kPlanUnits], a.v.unit_cap) * Hkv : 0;
   const int at_once = (int)gridDim.x * TEAMS;
   const bool queued = total > at_once;
-  constexpr int dtype = F16 ? RF_F16 : RF_BF16;
   if (warp < CLOSE_WARP + TEAMS && closes && i < total) fetch_pages(0);
   __syncthreads();
 
@@ -757,20 +755,6 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
         known = true;
         move_on();
       }
-      if (next >= total && u.pieces > 1) {
-        named_sync<TEAM>(bars + kBarLast);
-        if (tm.last) {
-          const int share = (w.rows + WARPS - 1) / WARPS, r = wt * share, nr = min(share, w.rows - r);
-          if (nr > 0) {
-            if (share == 1)
-              merge_pieces<1, 16>(a, w, u.first, u.pieces, r, nr, dtype, lane);
-            else if (share == 2)
-              merge_pieces<2, 8>(a, w, u.first, u.pieces, r, nr, dtype, lane);
-            else
-              merge_pieces<4, 8>(a, w, u.first, u.pieces, r, nr, dtype, lane);
-          }
-        }
-      }
       i = next;
       ++turn;
       ahead = 0;
@@ -789,8 +773,6 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
       named_sync<TEAM>(bars + kBarEnd);
     }
     for (int turn = 0; i < total; ++turn) {
-      const PagedUnit& u = tm.unit[turn & 1];
-      const int hk = i % Hkv;
       int next = total;
       if (queued) {
         if (lane == 0) {
@@ -823,25 +805,6 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
         }
       }
       named_sync<TEAM>(bars + kBarEnd);
-      if (u.pieces > 1) {
-        const Work w(a, u, hk);
-        const size_t at = (size_t)u.first * Hkv + hk;
-        int last = 0;
-        if (lane == 0 && RF_IDX_OK(at, (size_t)a.v.unit_cap * Hkv)) {
-          __threadfence();              // stands for the team, which the barrier joined
-          last = atomicAdd(a.v.counters + at, 1) == u.pieces - 1;
-          __threadfence();
-          if (last) a.v.counters[at] = 0;
-        }
-        last = __shfl_sync(0xffffffffu, last, 0);
-        if (next >= total) {
-          if (lane == 0) tm.last = last;
-          named_sync<TEAM>(bars + kBarLast);
-        } else if (last) {
-          for (int r = 0; r < w.rows; r += 4)
-            merge_pieces<4, 16>(a, w, u.first, u.pieces, r, min(4, w.rows - r), dtype, lane);
-        }
-      }
       i = next;
     }
   }
@@ -855,7 +818,7 @@ rf_status launch_few(const PagedAttn& a, int sms, cudaStream_t st) {
   if (smem_attr(paged_few_kernel<F16>, bytes, done) != RF_OK) return RF_ERR_CUDA;
   const long long most = (long long)a.v.unit_cap * a.v.s.Hkv;
   const unsigned grid = (unsigned)(most < 2ll * sms ? most : 2ll * sms);
-  return launch_after(paged_few_kernel<F16>, grid, WARPS * 32, bytes, st, a, a.v.s.some_pairs());
+  return launch_after(paged_few_kernel<F16>, grid, WARPS * 32, bytes, st, a);
 }
 
 template <bool F16>
@@ -863,10 +826,7 @@ rf_status launch_t(const PagedAttn& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const int sms = tc::sm_count();
   if (sms <= 0) return RF_ERR_CUDA;
-  // by the largest sizes, as the lengths are the device's
-  const PagedShape& s = a.v.s;
-  const long long steps = (long long)s.B * s.tiles() * s.Hkv * ((s.max_len + 4 * TK - 1) / (4 * TK));
-  if (!s.some_pairs() && steps <= kPagedFewSteps * 2ll * sms) return launch_few<F16>(a, sms, st);
+  if (a.v.s.few(sms)) return launch_few<F16>(a, sms, st);
   auto* kernel = paged_decode_kernel<F16>;
   // launched with fewer registers than the warpgroups' shares add up to, the streaming
   // warps would wait for them for ever

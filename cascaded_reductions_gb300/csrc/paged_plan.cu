@@ -34,8 +34,8 @@ struct Plan {
   PagedRange* ranges;
   PagedJoin* joins;
   PagedUnit* units;
-  int* counters;
-  int unit_cap, range_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
+  int *merges, *counters;
+  int unit_cap, range_cap, merge_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
   uint32_t mark;
 };
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ int pieces_of(int steps, int piece) { return (steps +
 
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   __shared__ long long sm[WARPS], fit[WARPS];
-  __shared__ int n_joins;
+  __shared__ int n_joins, n_merges;
   const PagedShape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = s.Hkv * (s.G() / s.packed());
@@ -143,6 +143,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   }
   // rows of up to two pieces stay whole in a large call, to save the merge
   auto pieces = [&](int n) { return !few && n <= 2 * MANY_STEPS ? 1 : pieces_of(n, (int)piece); };
+  if (tid == 0) n_joins = n_merges = 0;
+  __syncthreads();
   long long units = 0;
   for (int b0 = 0; b0 < s.B; b0 += THREADS) {
     const int b = b0 + tid;
@@ -173,6 +175,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
         x.start = start, x.n = rows, x.len = len;
         x.pad[0] = x.pad[1] = x.pad[2] = 0;
         a.units[u0 + u] = x;
+        if (i == 0 && n_p > 1) {
+          const int m = atomicAdd(&n_merges, 1);
+          if (m < a.merge_cap && RF_IDX_OK(m, a.merge_cap)) a.merges[m] = (int)(u0 + u);
+        }
       }
     }
     units += total;
@@ -217,7 +223,6 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       if (RF_IDX_OK(i, a.range_cap)) a.ranges[i] = r;
     }
   }
-  if (tid == 0) n_joins = 0;
   __syncthreads();
   // the tiles that a range's start cuts for the first time
   for (int i = 1 + tid; i < n_ranges; i += THREADS) {
@@ -247,6 +252,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   if (tid < kPlanWords) {
     int x = 0;
     if (tid == kPlanJoins) x = n_joins;
+    if (tid == kPlanMerges) x = min(n_merges, a.merge_cap);
     if (tid == kPlanMark) x = (int)a.mark;
     if (tid == kPlanUnits) x = n_units;
     if (tid == kPlanRanges) x = n_ranges;
@@ -267,6 +273,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   long long cut = (2ll * sms * MANY_UNITS + s.Hkv - 1) / s.Hkv;
   if (cut > tiles * (steps - 1)) cut = tiles * (steps - 1);
   l->unit_cap = (int)(tiles + cut);
+  l->merge_cap = (int)tiles;
   l->range_cap = 0;
   if (s.some_pairs()) {
     // blocks at most, and the rounds that they make
@@ -290,6 +297,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   l->ranges = take((size_t)l->range_cap * sizeof(PagedRange));
   l->joins = take((size_t)l->range_cap * sizeof(PagedJoin));
   l->units = take((size_t)l->unit_cap * sizeof(PagedUnit));
+  l->merges = take((size_t)l->merge_cap * sizeof(int));
   l->counters = take((size_t)l->unit_cap * s.Hkv * sizeof(int));
   l->unit_ml = take(rows * sizeof(float2));
   l->unit_acc = take(rows * 128 * sizeof(float));
@@ -317,8 +325,9 @@ rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const Pa
   a.ranges = reinterpret_cast<PagedRange*>(p + l.ranges);
   a.joins = reinterpret_cast<PagedJoin*>(p + l.joins);
   a.units = reinterpret_cast<PagedUnit*>(p + l.units);
+  a.merges = reinterpret_cast<int*>(p + l.merges);
   a.counters = reinterpret_cast<int*>(p + l.counters);
-  a.unit_cap = l.unit_cap, a.range_cap = l.range_cap;
+  a.unit_cap = l.unit_cap, a.range_cap = l.range_cap, a.merge_cap = l.merge_cap;
   a.clusters = 0;
   if (s.some_pairs()) {
     a.clusters = paged_pairs();

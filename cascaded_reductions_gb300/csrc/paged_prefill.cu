@@ -389,9 +389,65 @@ __device__ __forceinline__ uint32_t nan_of(const float4& y) {
   return (y.x != y.x) | (y.y != y.y) << 1 | (y.z != y.z) << 2 | (y.w != y.w) << 3;
 }
 
-// A CTA per 32 of a tile's 256 rows, eight to a tile.  The first ones join the parts of a
-// tile that cuts divide; then, where the pair kernel noted a value that is not finite, a
-// range's eight look at its whole tiles.
+// A row of the streaming kernel's tile from the states of its pieces, in order; one warp,
+// four columns per lane.
+template <bool F16>
+__device__ __forceinline__ void merge_row(const PagedAttn& a, const PagedUnit& u, int first, int hk, int r, int lane) {
+  constexpr int U = 16;                               // states in flight
+  const PagedView& v = a.v;
+  const size_t step = (size_t)v.s.Hkv * v.s.unit_rows(), base = first * step + (size_t)hk * v.s.unit_rows() + r;
+  const size_t states = (size_t)v.unit_cap * step;
+  (void)states;                                       // read by the checked build only
+  float M = -INFINITY, L = 0.f;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < u.pieces; s0 += U) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < U && s0 + lane < u.pieces && RF_IDX_OK(base + (s0 + lane) * step, states))
+      ml = __ldcg(v.unit_ml + base + (s0 + lane) * step);
+    float4 o[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const size_t at = base + (s0 + j) * step;
+      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + j < u.pieces && RF_IDX_OK(at, states))
+        o[j] = __ldcg(reinterpret_cast<const float4*>(v.unit_acc + at * HD) + lane);
+    }
+    const float top = fmaxf(M, group_max<32>(ml.x)), c = exp2f(M - ref_of(top));
+    M = top;
+    L *= c;
+    A.x *= c, A.y *= c, A.z *= c, A.w *= c;
+    float f = -1.f;                                   // a piece without keys: its accumulator is not read
+    if (ml.x != -INFINITY) {
+      f = exp2f(ml.x - ref_of(top));
+      L = fmaf(f, ml.y, L);
+    } else {
+      L += ml.y;                                      // 0, or NaN where every score was NaN
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      if (fj == -1.f) continue;
+      A.x = fmaf(fj, o[j].x, A.x);
+      A.y = fmaf(fj, o[j].y, A.y);
+      A.z = fmaf(fj, o[j].z, A.z);
+      A.w = fmaf(fj, o[j].w, A.w);
+    }
+    // every lane's share of L was rescaled alike; they are added up at the end
+  }
+  L = group_sum<32>(L);
+  const int i = (u.tile * kPagedTileRows + r) / v.G, head = hk * v.G + u.tile * kPagedTileRows + r - i * v.G;
+  const size_t row = (size_t)(u.start + i) * v.s.H + head;
+  if (!RF_IDX_OK(row, (size_t)v.s.T * v.s.H)) return;
+  const float4 y = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x / L, A.y / L, A.z / L, A.w / L);
+  *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
+      make_uint2(pair::pack_16x2<F16>(y.x, y.y), pair::pack_16x2<F16>(y.z, y.w));
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+// What the kernels before it left in parts.  Rows of the streaming kernel in several pieces,
+// a warp each; then the pair kernel's tiles, a CTA per 32 of a tile's 256 rows, eight to a
+// tile: the first ones join the parts of a tile that cuts divide, and where that kernel
+// noted a value that is not finite, a range's eight look at its whole tiles.
 template <bool F16>
 __global__ void __launch_bounds__(FIN_WARPS * 32)
 paged_finish_kernel(const __grid_constant__ PagedAttn a) {
@@ -403,7 +459,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
   const size_t all_rows = (size_t)v.s.T * v.s.H;
   (void)all_rows;                                     // read by the checked build only
   PagedJoin it = {};
-  if (RF_IDX_OK(rho, v.range_cap)) {                  // asked for before it is known whether it is one
+  if (rho < v.range_cap) {                            // asked for before it is known whether it is one
     const int4* at = reinterpret_cast<const int4*>(v.joins + rho);
     int4* to = reinterpret_cast<int4*>(&it);
 #pragma unroll
@@ -412,6 +468,18 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
   if (v.head[kPlanMark] != (int)v.mark) return;
   const int ranges = min(v.head[kPlanRanges], v.range_cap), flag = v.head[kPlanFlag];
   const int P = 1 << v.P_log2;
+  {
+    const int per = v.s.Hkv * v.s.unit_rows();        // rows of a tile, over the key heads
+    const long long rows = (long long)min(v.head[kPlanMerges], v.merge_cap) * per;
+    for (long long i = (long long)blockIdx.x * FIN_WARPS + warp; i < rows; i += (long long)gridDim.x * FIN_WARPS) {
+      const int m = (int)(i / per), hk = (int)(i - (long long)m * per) / v.s.unit_rows();
+      const int r = (int)(i - (long long)m * per) - hk * v.s.unit_rows();
+      const int first = RF_IDX_OK(m, v.merge_cap) ? v.merges[m] : 0;
+      if (!RF_IDX_OK(first, v.unit_cap)) continue;
+      const PagedUnit u = v.units[first];
+      if (r < u.n * v.G - u.tile * kPagedTileRows) merge_row<F16>(a, u, first, hk, r, lane);
+    }
+  }
   if (rho < min(v.head[kPlanJoins], v.range_cap)) {
     constexpr int R = FIN_ROWS / FIN_WARPS;           // rows of a warp
     const int row0 = part * FIN_ROWS + warp * R;      // of the tile
@@ -547,7 +615,13 @@ rf_status launch_paged_prefill(const PagedAttn& a, int dtype, cudaStream_t st) {
 }
 
 rf_status launch_paged_finish(const PagedAttn& a, int dtype, cudaStream_t st) {
-  const unsigned grid = (unsigned)a.v.range_cap * FIN_PARTS;
+  const int sms = tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  // eight CTAs per tile that may be cut, enough for all rows in pieces up to four CTAs per SM
+  const PagedShape& s = a.v.s;
+  const long long rows = ((long long)a.v.merge_cap * s.Hkv * s.unit_rows() + FIN_WARPS - 1) / FIN_WARPS;
+  const long long pairs = (long long)a.v.range_cap * FIN_PARTS, most = rows < 4ll * sms ? rows : 4ll * sms;
+  const unsigned grid = (unsigned)(pairs > most ? pairs : most);
   return launch_after(dtype == RF_F16 ? paged_finish_kernel<true> : paged_finish_kernel<false>, grid,
                       FIN_WARPS * 32, 0, st, a);
 }

@@ -584,7 +584,8 @@ rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T
  * reads as keys and values of zero.  A key or value that is not finite reaches only the rows
  * that see it.  Requests with up to 64 rows per key head (new tokens * H / Hkv) run as
  * rf_attn_decode_window does (weights not rounded to 16 bits), so a row's last bits
- * may depend on how many tokens come with it.  One launch, three where max_new * H / Hkv > 64.
+ * may depend on how many tokens come with it.  One launch for a small batch of
+ * single or few tokens, two for a larger one, three where max_new * H / Hkv > 64.
  * Errors: as rf_paged_plan, RF_ERR_INVALID_ARG for width * page < max_len, a non-finite scale
  * or a bad dtype; RF_ERR_UNSUPPORTED for D != 128, RF_F32, scale <= 0, a page that is not 16,
  * 32, 64, 128 or 256, pages * Hkv >= 2^30 or B * width >= 2^31; RF_ERR_MISALIGNED unless q, kp,
