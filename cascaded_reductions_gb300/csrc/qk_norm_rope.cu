@@ -14,21 +14,29 @@
 // integer wraps; its top 32 bits go through sincospi.  What is left of the error is
 // pos 2^-55 turns from f / 2 pi and half a step of fp32.
 //
-// What bounds it: HBM (a head is read once and written once).  Angles cost some 40
-// instructions a pair, so a CTA makes those of its tokens once, in shared memory, for
-// all heads.  A head takes D / 16 lanes, each with two 16-byte chunks that hold both
-// halves of its pairs, so that only the sum of squares crosses lanes.
+// What bounds it: HBM (a head is read once and written once), if little goes through
+// shared memory.  A head takes D / 16 lanes, each with two 16-byte chunks that hold both
+// halves of its pairs, so that only the sum of squares crosses lanes.  Angles cost some 40
+// instructions a pair and are made once per token, for all heads.
+//   Many tokens (norm_rope_kernel): a warp takes a share of all heads of all tokens, makes
+// a token's angles, keeps them in registers and goes through its heads, with the rows of
+// two more items in flight.
+//   Few (norm_rope_few_kernel): the heads of a token are spread over the warps of one CTA or
+// of several, each of which makes the token's angles for its own.
+// [8192 tokens, 32 + 8 + 8 heads of 128]: FIGURE; by the second kernel 45 us, whose every
+// item reads weights and angles from shared memory (85 % of its rate).
 
 #include <cuda_fp16.h>
 
 #include "cache_common.cuh"
+#include "f32x2.cuh"
 #include "tc_common.cuh"
 
 namespace rf {
 namespace {
 
 constexpr int WARPS = 8;
-constexpr int MAX_PAIRS = 128;
+constexpr int MANY = 8;                 // tokens per SM from which on a warp takes a whole one
 
 struct NormRope {
   const uint16_t *q, *k, *v;
@@ -65,6 +73,18 @@ __device__ __forceinline__ uint4 round8(const float* f) {
                     pack_bf16x2(f[6], f[7]));
 }
 template <bool F16>
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+  const float2 f = widen<F16>(w);
+  return pair::pack_f32x2(f.x, f.y);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t round2(uint64_t x) {
+  float a, b;
+  pair::unpack_f32x2(x, a, b);
+  if constexpr (F16) return pack_f16x2(a, b);
+  return pack_bf16x2(a, b);
+}
+template <bool F16>
 __device__ __forceinline__ float weight_of(const void* w, int i, bool w32) {
   if (w32) return static_cast<const float*>(w)[i];
   const uint32_t u = static_cast<const uint16_t*>(w)[i];
@@ -79,11 +99,175 @@ __device__ __forceinline__ uint4 ld16(const uint16_t* p) {
   return r;
 }
 
+// a turn's 2^-64 th parts that position times makes of frequency f
+__device__ __forceinline__ unsigned long long turn_unit(float freq) {
+  double f = (double)freq * 0.15915494309189533577;           // 1 / (2 pi)
+  f -= floor(f);
+  return __double2ull_rn(f * 18446744073709551616.0);
+}
+__device__ __forceinline__ void turn_of(const NormRope& a, unsigned long long unit, int pair, size_t t, float* s,
+                                        float* c) {
+  int ax = a.axis && RF_IDX_OK(pair, a.R / 2) ? a.axis[pair] : 0;
+  ax = min(max(ax, 0), a.axes - 1);
+  const size_t at = (size_t)ax * a.T + t;
+  const long long pos = RF_IDX_OK(at, (size_t)a.axes * a.T) ? a.positions[at] : 0;
+  const unsigned long long frac = unit * (unsigned long long)pos + 0x80000000ull;
+  // the top 32 bits as half turns in [-1, 1)
+  sincospif((float)(int)(unsigned)(frac >> 32) * 4.656612873077393e-10f, s, c);
+}
+
+template <bool F16, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(WARPS * 32, 3)
+norm_rope_kernel(const NormRope a) {
+  constexpr int LANES = D / 16;                 // of a head
+  constexpr int HEADS = 32 / LANES;             // of a warp
+  extern __shared__ __align__(16) float smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int half = a.R / 2;
+  // weights of q and k as the lanes take them, four floats each: [2][4][LANES][4]
+  float* w_s = smem;
+  unsigned long long* unit = reinterpret_cast<unsigned long long*>(smem + 2 * D);   // [R / 2]
+  float* turn = reinterpret_cast<float*>(unit + half) + warp * a.R;                 // the warp's cos, sin
+  wait_prerequisite();
+  allow_dependents();
+  const int hl = lane / LANES, j = lane % LANES;
+  const int rc = a.R / 16;
+  const int c0 = INTERLEAVED ? 2 * j : j < rc ? j : 2 * rc + 2 * (j - rc);
+  const int c1 = INTERLEAVED ? 2 * j + 1 : j < rc ? j + rc : c0 + 1;
+  // items of a token: groups of heads of q, then of k, then of v
+  const int nq = (a.H + HEADS - 1) / HEADS, nk = (a.Hkv + HEADS - 1) / HEADS;
+  const int items = nq + (a.slots ? 2 : 1) * nk;
+  // the warp's share of all items, to the item: 8192 tokens for 3648 warps are 2.2 each
+  const long long all = (long long)a.T * items, w0 = (long long)blockIdx.x * WARPS + warp;
+  const long long ws = (long long)gridDim.x * WARPS;
+  const long long first = all / ws * w0 + all % ws * w0 / ws, last = all / ws * (w0 + 1) + all % ws * (w0 + 1) / ws;
+  const int t_end = (int)(last / items), i_end = (int)(last - (long long)t_end * items);
+
+  struct Item {
+    int t, i;
+    uint4 x0, x1;
+  };
+  auto within = [&](const Item& it) { return it.t < t_end || (it.t == t_end && it.i < i_end); };
+  auto load = [&](Item& it) {
+    it.x0 = it.x1 = make_uint4(0, 0, 0, 0);
+    if (!within(it) || !RF_IDX_OK(it.t, a.T)) return;
+    const bool q = it.i < nq, k = !q && it.i < nq + nk;
+    const int h = (q ? it.i : k ? it.i - nq : it.i - nq - nk) * HEADS + hl;
+    if (h >= (q ? a.H : a.Hkv)) return;
+    const uint16_t* row = (q ? a.q + it.t * a.q_step : k ? a.k + it.t * a.k_step : a.v + it.t * a.v_step) + h * D;
+    it.x0 = ld16(row + c0 * 8);
+    it.x1 = ld16(row + c1 * 8);
+  };
+  auto follow = [&](const Item& it, Item& to) {
+    to.i = it.i + 1, to.t = it.t;
+    if (to.i == items) to.i = 0, ++to.t;
+  };
+  Item it, one, two;
+  it.t = (int)(first / items), it.i = (int)(first - (long long)it.t * items);
+  load(it);                                     // under way while the tables are made
+  follow(it, one);
+  load(one);
+  for (int e = tid; e < 2 * D; e += WARPS * 32) {
+    const void* w = e < D ? a.qw : a.kw;
+    const int f = e % D, k = f / (4 * LANES), l = f / 4 % LANES;          // part k of lane l
+    const int lc0 = INTERLEAVED ? 2 * l : l < rc ? l : 2 * rc + 2 * (l - rc);
+    const int lc1 = INTERLEAVED ? 2 * l + 1 : l < rc ? l + rc : lc0 + 1;
+    w_s[e] = w ? weight_of<F16>(w, (k < 2 ? lc0 : lc1) * 8 + k % 2 * 4 + f % 4, a.w32) : 1.f;
+  }
+  for (int e = tid; e < half; e += WARPS * 32) unit[e] = turn_unit(RF_IDX_OK(e, half) ? a.freq[e] : 0.f);
+  __syncthreads();
+
+  while (within(it)) {
+    const int t = it.t;
+    __syncwarp();                               // the last token's angles have been read
+    for (int e = lane; e < half; e += 32) turn_of(a, unit[e], e, t, &turn[half + e], &turn[e]);
+    const int slot = a.slots && RF_IDX_OK(t, a.T) ? a.slots[t] : -1;
+    const bool placed = slot >= 0 && slot < a.n_slots;
+    const int page = placed ? slot / a.page : 0;
+    // row of head 0 in a pair of pages' places, or of the dense outputs
+    const size_t kv_row = a.slots ? (size_t)page * a.Hkv * a.page + (slot - page * a.page) : (size_t)t * a.Hkv;
+    const size_t kv_head = a.slots ? a.page : 1;
+    __syncwarp();
+    uint64_t c[4], s[4];
+    if (j < rc) {
+      const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(turn + 8 * j);
+      const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(turn + half + 8 * j);
+      c[0] = c2[0].x, c[1] = c2[0].y, c[2] = c2[1].x, c[3] = c2[1].y;
+      s[0] = s2[0].x, s[1] = s2[0].y, s[2] = s2[1].x, s[3] = s2[1].y;
+    }
+    while (it.t == t && within(it)) {
+      follow(one, two);
+      load(two);
+      const bool q = it.i < nq, k = !q && it.i < nq + nk;
+      const int h = (q ? it.i : k ? it.i - nq : it.i - nq - nk) * HEADS + hl;
+      const bool in = h < (q ? a.H : a.Hkv);
+      if (q || k) {
+        uint64_t x[8] = {widen2<F16>(it.x0.x), widen2<F16>(it.x0.y), widen2<F16>(it.x0.z), widen2<F16>(it.x0.w),
+                         widen2<F16>(it.x1.x), widen2<F16>(it.x1.y), widen2<F16>(it.x1.z), widen2<F16>(it.x1.w)};
+        if (q ? a.qw != nullptr : a.kw != nullptr) {
+          uint64_t s2 = 0ull;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s2 = pair::fma_f32x2(x[e], x[e], s2);
+          float s0, s1;
+          pair::unpack_f32x2(s2, s0, s1);
+          const float r = rsqrtf(group_sum<LANES>(s0 + s1) * (1.f / D) + a.eps);
+          const uint64_t r2 = pair::pack_f32x2(r, r);
+          const ulonglong2* w = reinterpret_cast<const ulonglong2*>(w_s + (q ? 0 : D)) + j;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const ulonglong2 w2 = w[e * LANES];
+            x[2 * e] = pair::mul_f32x2(x[2 * e], pair::mul_f32x2(r2, w2.x));
+            x[2 * e + 1] = pair::mul_f32x2(x[2 * e + 1], pair::mul_f32x2(r2, w2.y));
+          }
+        }
+        if (j < rc) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // two pairs: their first values, their second ones
+            uint64_t u = x[e], v = x[e + 4];
+            if constexpr (INTERLEAVED) {
+              float p0, p1, q0, q1;
+              pair::unpack_f32x2(x[2 * e], p0, p1);
+              pair::unpack_f32x2(x[2 * e + 1], q0, q1);
+              u = pair::pack_f32x2(p0, q0);
+              v = pair::pack_f32x2(p1, q1);
+            }
+            float s0, s1;
+            pair::unpack_f32x2(s[e], s0, s1);
+            const uint64_t y = pair::fma_f32x2(u, c[e], pair::mul_f32x2(v, pair::pack_f32x2(-s0, -s1)));
+            const uint64_t z = pair::fma_f32x2(v, c[e], pair::mul_f32x2(u, s[e]));
+            if constexpr (INTERLEAVED) {
+              float p0, p1, q0, q1;
+              pair::unpack_f32x2(y, p0, q0);
+              pair::unpack_f32x2(z, p1, q1);
+              x[2 * e] = pair::pack_f32x2(p0, p1);
+              x[2 * e + 1] = pair::pack_f32x2(q0, q1);
+            } else {
+              x[e] = y;
+              x[e + 4] = z;
+            }
+          }
+        }
+        it.x0 = make_uint4(round2<F16>(x[0]), round2<F16>(x[1]), round2<F16>(x[2]), round2<F16>(x[3]));
+        it.x1 = make_uint4(round2<F16>(x[4]), round2<F16>(x[5]), round2<F16>(x[6]), round2<F16>(x[7]));
+      }
+      if (in && (q || !a.slots || placed)) {
+        uint16_t* dst = q ? a.q_out + ((size_t)t * a.H + h) * D
+                          : (k ? a.k_out : a.v_out) + (kv_row + h * kv_head) * D;
+        *reinterpret_cast<uint4*>(dst + c0 * 8) = it.x0;
+        *reinterpret_cast<uint4*>(dst + c1 * 8) = it.x1;
+      }
+      it = one;
+      one = two;
+    }
+  }
+}
+
 // One CTA: `tokens` adjacent tokens, or one slice of the heads of a single token.  Its
 // warps take groups of 32 / (D / 16) heads of a token at a time.
 template <bool F16, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(WARPS * 32)
-norm_rope_kernel(const NormRope a) {
+norm_rope_few_kernel(const NormRope a) {
   constexpr int LANES = D / 16;                 // of a head
   constexpr int HEADS = 32 / LANES;             // of a warp
   extern __shared__ __align__(16) float smem[];
@@ -131,19 +315,10 @@ norm_rope_kernel(const NormRope a) {
     w_s[e] = w ? weight_of<F16>(w, e < D ? e : e - D, a.w32) : 1.f;
   }
   for (int e = tid; e < nt * half; e += WARPS * 32) {
-    const int t = e / half, pair = e - t * half;
-    int ax = a.axis && RF_IDX_OK(pair, half) ? a.axis[pair] : 0;
-    ax = min(max(ax, 0), a.axes - 1);
-    const size_t at = (size_t)ax * a.T + t0 + t;
-    const long long pos = RF_IDX_OK(at, (size_t)a.axes * a.T) ? a.positions[at] : 0;
-    double f = (double)a.freq[pair] * 0.15915494309189533577;       // 1 / (2 pi)
-    f -= floor(f);
-    const unsigned long long unit = __double2ull_rn(f * 18446744073709551616.0);
-    const unsigned long long frac = unit * (unsigned long long)pos + 0x80000000ull;
+    const int t = e / half, p = e - t * half;
     float s, c;
-    // the top 32 bits as half turns in [-1, 1)
-    sincospif((float)(int)(unsigned)(frac >> 32) * 4.656612873077393e-10f, &s, &c);
-    turn[t * half + pair] = make_float2(c, s);
+    turn_of(a, turn_unit(RF_IDX_OK(p, half) ? a.freq[p] : 0.f), p, (size_t)t0 + t, &s, &c);
+    turn[t * half + p] = make_float2(c, s);
   }
   __syncthreads();
 
@@ -211,6 +386,12 @@ template <bool F16, int D>
 rf_status launch_d(NormRope a, bool interleaved, cudaStream_t st) {
   const int sms = tc::sm_count();
   if (sms <= 0) return RF_ERR_CUDA;
+  if (a.T >= MANY * sms) {
+    const size_t smem = 2 * D * sizeof(float) + (a.R / 2) * sizeof(unsigned long long) + WARPS * a.R * sizeof(float);
+    const long long ctas = ((long long)a.T + WARPS - 1) / WARPS, most = 3ll * sms;
+    return launch_after(interleaved ? norm_rope_kernel<F16, D, true> : norm_rope_kernel<F16, D, false>,
+                        (unsigned)(ctas < most ? ctas : most), WARPS * 32, smem, st, a);
+  }
   const int heads_per_item = 32 / (D / 16);
   const long long groups = (a.heads + heads_per_item - 1) / heads_per_item;
   // A CTA's tokens: enough items to hide its angles behind, while every SM has its share of
@@ -224,7 +405,7 @@ rf_status launch_d(NormRope a, bool interleaved, cudaStream_t st) {
   }
   const size_t smem = 2 * D * sizeof(float) + (size_t)a.tokens * (a.R / 2) * sizeof(float2);
   const long long grid = ((long long)a.T + a.tokens - 1) / a.tokens * a.slices;
-  auto* kernel = interleaved ? norm_rope_kernel<F16, D, true> : norm_rope_kernel<F16, D, false>;
+  auto* kernel = interleaved ? norm_rope_few_kernel<F16, D, true> : norm_rope_few_kernel<F16, D, false>;
   return launch_after(kernel, (unsigned)grid, WARPS * 32, smem, st, a);
 }
 
