@@ -10,12 +10,14 @@
 //
 // What bounds it: latency.  A step moves kilobytes (256 requests, 25 prompt chunks:
 // 0.9 MB), and what it waits for are the launch, one read of the lengths, the sums and
-// one read of a page number.  So everything is one cluster: each of its CTAs makes the
-// prefix sums for itself in shared memory, and then pages and tokens are dealt out to
-// all threads, each of which finds its request by bisection.  Nothing that one thread
-// writes is read by another (a page just given back is read from the ended request's
-// table row), but for what the call may overwrite in place: the lengths and the number of
-// free pages, which are written after a barrier of the cluster behind every read.
+// one read of a page number.  So it is one cluster: each of its CTAs makes the prefix sums
+// for itself in shared memory, and then pages and tokens are dealt out to all threads,
+// each of which finds its request by bisection.  Nothing that one thread writes is read
+// by another (a page just given back is read from the ended request's table row), but for
+// what the call may overwrite in place: the lengths and the number of free pages, which are
+// written after a barrier of the cluster behind every read.  Eight SMs are few for a hundred
+// thousand tokens: from MANY_TOKENS on the cluster places each request's first token only,
+// and a kernel on all SMs that begins beside its end the others.
 
 #include "cache_common.cuh"
 #include "tc_common.cuh"
@@ -29,7 +31,16 @@ struct Tables {
   const int32_t* n_free;
   int32_t *starts, *positions, *slots, *lens_out, *n_free_out;
   int B, width, P, page, T;
+  int page_log2;                             // -1: the page is no power of two
+  bool firsts;                               // only each request's first token is placed
 };
+
+constexpr int MANY_TOKENS = 16384;
+
+// pos / page
+__device__ __forceinline__ int page_index(const Tables& a, int pos) {
+  return a.page_log2 >= 0 ? pos >> a.page_log2 : pos / a.page;
+}
 
 constexpr int WARPS_MAX = 32;
 
@@ -168,6 +179,23 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
     const size_t at = (size_t)b * a.width + held_of(len0[b]) + (x - need0[b]);
     if (RF_IDX_OK(at, entries)) a.table[at] = page_of(x);
   }
+  if (a.firsts) {
+    for (int b = first; b < B; b += step) {
+      const int t = start[b], end = b + 1 < B ? start[b + 1] : (int)min(tokens, 0x7fffffffll);
+      if (t == end || t >= a.T || !RF_IDX_OK(t, a.T)) continue;
+      const int len = len0[b], pos = len < 0 ? -1 - len : len;
+      int slot = -1;
+      if (len >= 0) {
+        const int i = page_index(a, pos), held = held_of(len);
+        const size_t at = (size_t)b * a.width + i;
+        slot = (i >= held ? page_of(need0[b] + i - held) : RF_IDX_OK(at, entries) ? a.table[at] : -1) * a.page +
+               (pos - i * a.page);
+      }
+      a.positions[t] = pos;
+      a.slots[t] = slot;
+    }
+    return;
+  }
   // four tokens per thread, in 16-byte stores
   for (int t0 = 4 * first; t0 < a.T; t0 += 4 * step) {
     int pos[4], slot[4];
@@ -186,7 +214,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
       const int len = len0[b];
       pos[e] = (len < 0 ? -1 - len : len) + (t - start[b]);
       if (len < 0) continue;
-      const int i = pos[e] / a.page;
+      const int i = page_index(a, pos[e]);
       if (i != seen) {
         const int held = held_of(len);
         const size_t at = (size_t)b * a.width + i;
@@ -210,6 +238,45 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
   }
 }
 
+// All tokens but the requests' first ones, which are in place and say where the others go;
+// behind the last one positions are 0 and slots -1.
+__global__ void __launch_bounds__(256) page_slots_kernel(const Tables a) {
+  extern __shared__ int start[];             // [B + 1]
+  wait_prerequisite();
+  allow_dependents();
+  for (int b = threadIdx.x; b <= a.B; b += 256) start[b] = RF_IDX_OK(b, a.B + 1) ? a.starts[b] : 0;
+  __syncthreads();
+  const int tokens = start[a.B];
+  for (int t0 = 4 * (blockIdx.x * 256 + threadIdx.x); t0 < a.T; t0 += 4 * 256 * (int)gridDim.x) {
+    int b = t0 < tokens ? find(start, a.B, t0) : 0, of = -1, first_pos = 0, seen = -1, entry = 0;
+    bool fits = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = t0 + e;
+      if (t >= a.T || !RF_IDX_OK(t, a.T)) break;
+      int pos = 0, slot = -1;
+      if (t < tokens) {
+        while (start[b + 1] <= t) ++b;
+        if (start[b] == t) continue;
+        if (of != b) {
+          of = b, seen = -1;
+          first_pos = __ldcg(a.positions + start[b]);
+          fits = __ldcg(a.slots + start[b]) >= 0;
+        }
+        pos = first_pos + (t - start[b]);
+        if (fits) {
+          const int i = page_index(a, pos);
+          const size_t at = (size_t)b * a.width + i;
+          if (i != seen) seen = i, entry = RF_IDX_OK(at, (size_t)a.B * a.width) ? a.table[at] : 0;
+          slot = entry * a.page + (pos - i * a.page);
+        }
+      }
+      a.positions[t] = pos;
+      a.slots[t] = slot;
+    }
+  }
+}
+
 }  // namespace
 
 rf_status launch_page_tables(const int32_t* lens, const int32_t* news, int B, int32_t* table, int width,
@@ -220,7 +287,9 @@ rf_status launch_page_tables(const int32_t* lens, const int32_t* news, int B, in
   const size_t smem = (size_t)B * 16;
   if (smem_attr(page_tables_kernel, (size_t)kMaxTableRequests * 16, done) != RF_OK) return RF_ERR_CUDA;
   Tables a = {lens, news, table, stack, n_free, starts, positions, slots, lens_out, n_free_out,
-              B, width, P, page, T};
+              B, width, P, page, T, -1, T >= MANY_TOKENS};
+  for (int e = 0; e < 31; ++e)
+    if ((1 << e) == page) a.page_log2 = e;
   const bool small = B <= 256 && T <= 1024;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -239,7 +308,12 @@ rf_status launch_page_tables(const int32_t* lens, const int32_t* news, int B, in
     cudaGetLastError();
     return RF_ERR_CUDA;
   }
-  return launch_status();
+  if (!a.firsts) return launch_status();
+  const int sms = tc::sm_count();
+  if (sms <= 0) return RF_ERR_CUDA;
+  const long long ctas = ((long long)T + 1023) / 1024;
+  return launch_after(page_slots_kernel, (unsigned)(ctas < 4ll * sms ? ctas : 4ll * sms), 256,
+                      ((size_t)B + 1) * sizeof(int), st, a);
 }
 
 RF_BOUNDS_WORD_OF_THIS_FILE

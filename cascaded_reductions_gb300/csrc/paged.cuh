@@ -32,6 +32,10 @@ struct PagedShape {
     return g % 8 == 0 ? 8 : g % 4 == 0 ? 4 : g % 2 == 0 ? 2 : 1;
   }
   __host__ __device__ int positions() const { return kPagedPairRows / packed(); }
+  __host__ __device__ int positions_log2() const {
+    const int p = packed();
+    return p == 8 ? 5 : p == 4 ? 6 : p == 2 ? 7 : 8;
+  }
   __host__ __device__ bool some_pairs() const { return (long long)max_new * G() > kPagedRows; }
   // of the streaming kernel: 16-row tiles per request at most, rows of one
   __host__ __device__ int tiles() const {
@@ -118,19 +122,19 @@ struct PagedTiles {
 // p0 + i P .. , P = 256 / heads; it visits the window's blocks [lb, hb) and up to SB
 // blocks of sinks below them.
 struct PagedBlocks {
-  int n, p0, P, window, SB;
-  __host__ __device__ PagedBlocks(int n_, int len, int P_, int window_, int sinks)
-      : n(n_), p0(len - n_), P(P_), window(window_),
+  int n, p0, log2, window, SB;          // P = 2^log2
+  __host__ __device__ PagedBlocks(int n_, int len, int log2_, int window_, int sinks)
+      : n(n_), p0(len - n_), log2(log2_), window(window_),
         SB(window_ > 0 ? (int)(((long long)sinks + kPagedBlock - 1) / kPagedBlock) : 0) {}
-  __host__ __device__ int tiles() const { return (n + P - 1) / P; }
-  __host__ __device__ int end(int i) const { return (i + 1) * P < n ? (i + 1) * P : n; }
+  __host__ __device__ int tiles() const { return (n + (1 << log2) - 1) >> log2; }
+  __host__ __device__ int end(int i) const { return (i + 1) << log2 < n ? (i + 1) << log2 : n; }
   __host__ __device__ int hb(int i) const {
     const int x = p0 + end(i);
     return x <= kPagedBlock ? 1 : (x + kPagedBlock - 1) / kPagedBlock;
   }
   __host__ __device__ int lb(int i) const {
     if (window == 0) return 0;
-    const int lo = p0 + i * P - window + 1;
+    const int lo = p0 + (i << log2) - window + 1;
     return lo > 0 ? lo / kPagedBlock : 0;
   }
   __host__ __device__ int sink_blocks(int i) const {
@@ -147,31 +151,33 @@ struct PagedBlocks {
       --m;
       sum = blocks(m);
     }
-    const long long r = kPagedBlock / P;
+    const long long P = 1ll << log2;
+    const int r = 8 - log2;             // 256 / P = 2^r tiles to a block
+    static_assert(kPagedBlock == 256, "as in r");
     // ends at or below 0 count one block; then ceil((p0 + (i + 1) P) / 256)
-    long long s = p0 < 0 ? (long long)(-(long long)p0) / P : 0;
+    long long s = p0 < 0 ? -(long long)p0 >> log2 : 0;
     if (s > m) s = m;
-    const long long first = p0 + s * P;                         // above -P
-    const long long u0 = first > 0 ? (first + P - 1) / P : 0;
+    const long long first = p0 + (s << log2);                   // above -P
+    const long long u0 = first > 0 ? (first + P - 1) >> log2 : 0;
     sum += s + up(u0 + (m - s), r) - up(u0, r);
     if (window > 0) {                   // less the blocks below the window that no sink keeps
       long long c = (long long)p0 - window + 1 - (long long)kPagedBlock * SB;
-      long long k = c < 0 ? (-c + P - 1) / P : 0;
+      const long long k = c < 0 ? (-c + P - 1) >> log2 : 0;
       if (k < m) {
-        c += k * P;
-        sum -= down(c / P + (m - k), r) - down(c / P, r);
+        c = (c + (k << log2)) >> log2;
+        sum -= down(c + (m - k), r) - down(c, r);
       }
     }
     return sum;
   }
-  // sum of ceil(k / r) for k = 1 .. x, of floor(k / r) for k = 0 .. x - 1
-  static __host__ __device__ long long up(long long x, long long r) {
-    const long long q = x / r;
-    return r * q * (q + 1) / 2 + (x - q * r) * (q + 1);
+  // sum of ceil(k / 2^r) for k = 1 .. x, of floor(k / 2^r) for k = 0 .. x - 1
+  static __host__ __device__ long long up(long long x, int r) {
+    const long long q = x >> r;
+    return (q * (q + 1) << r) / 2 + (x - (q << r)) * (q + 1);
   }
-  static __host__ __device__ long long down(long long x, long long r) {
-    const long long q = x / r;
-    return r * q * (q - 1) / 2 + (x - q * r) * q;
+  static __host__ __device__ long long down(long long x, int r) {
+    const long long q = x >> r;
+    return (q * (q - 1) << r) / 2 + (x - (q << r)) * q;
   }
 };
 
@@ -193,8 +199,7 @@ inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* pla
   v.merges = reinterpret_cast<const int*>(p + l.merges);
   v.unit_cap = l.unit_cap, v.range_cap = l.range_cap, v.merge_cap = l.merge_cap;
   v.mark = l.mark;
-  v.G = s.G(), v.packed = s.packed(), v.P_log2 = 0;
-  while ((1 << v.P_log2) < s.positions()) ++v.P_log2;
+  v.G = s.G(), v.packed = s.packed(), v.P_log2 = s.positions_log2();
   v.key_groups = v.G / v.packed, v.groups = s.Hkv * v.key_groups;
   return v;
 }

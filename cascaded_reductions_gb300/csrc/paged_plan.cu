@@ -37,6 +37,7 @@ struct Plan {
   int *merges, *counters;
   int unit_cap, range_cap, merge_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
   uint32_t mark;
+  int G, P_log2, groups;                // heads per key head; positions of a tile, head groups of the pair kernel
 };
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
@@ -71,8 +72,8 @@ __device__ __forceinline__ long long block_scan(long long x, long long* sm, long
   return r;
 }
 
-__device__ __forceinline__ int tiles_of(const PagedShape& s, const PagedSeq& q) {
-  return q.pair ? 0 : (q.n * s.G() + kPagedTileRows - 1) / kPagedTileRows;
+__device__ __forceinline__ int tiles_of(const Plan& a, const PagedSeq& q) {
+  return q.pair ? 0 : (q.n * a.G + kPagedTileRows - 1) / kPagedTileRows;
 }
 __device__ __forceinline__ int steps_of(const PagedShape& s, const PagedSeq& q) {
   const int n = PagedTiles(q.n, q.len, s.window, s.sinks).steps();
@@ -83,9 +84,11 @@ __device__ __forceinline__ int pieces_of(int steps, int piece) { return (steps +
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   __shared__ long long sm[WARPS], fit[WARPS];
   __shared__ int n_joins, n_merges;
+  __shared__ int2 cuts[THREADS];
+  __shared__ long long firsts[THREADS];
   const PagedShape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int groups = s.Hkv * (s.G() / s.packed());
+  const int groups = a.groups;
   wait_prerequisite();
   allow_dependents();
   long long steps = 0, blocks = 0, keys = 0;
@@ -97,26 +100,28 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       q.start = first;
       q.n = min(last - first, s.max_new);
       q.len = min(max(a.lens[b], 0), s.max_len);
-      q.pair = (long long)q.n * s.G() > kPagedRows;
+      q.pair = (long long)q.n * a.G > kPagedRows;
     }
     long long mine = 0, total;
     if (q.pair) {
-      const PagedBlocks k(q.n, q.len, s.positions(), s.window, s.sinks);
+      const PagedBlocks k(q.n, q.len, a.P_log2, s.window, s.sinks);
       mine = k.before(k.tiles()) * groups;
     }
-    const long long at = block_scan(mine, sm, &total);
-    if (b < s.B) {
-      if (RF_IDX_OK(b, s.B)) a.seqs[b] = q;
-      if (RF_IDX_OK(b, s.B + 1)) a.before[b] = blocks + at;
+    long long at = 0;
+    if (a.clusters > 0) {
+      at = block_scan(mine, sm, &total);
+      if (b < s.B && RF_IDX_OK(b, s.B + 1)) a.before[b] = blocks + at;
+      blocks += total;
     }
-    blocks += total;
-    const long long st = q.n > 0 && !q.pair ? (long long)tiles_of(s, q) * steps_of(s, q) : 0;
+    if (b < s.B && RF_IDX_OK(b, s.B)) a.seqs[b] = q;
+    const long long st = q.n > 0 && !q.pair ? (long long)tiles_of(a, q) * steps_of(s, q) : 0;
     block_scan(st, sm, &total);
     steps += total;
-    block_scan(q.pair ? (long long)s.Hkv * min(q.len, s.window > 0 ? s.window + q.n : q.len) : 0, sm, &total);
-    keys += total;
+    if (a.clusters > 0) {
+      block_scan(q.pair ? (long long)s.Hkv * min(q.len, s.window > 0 ? s.window + q.n : q.len) : 0, sm, &total);
+      keys += total;
+    }
   }
-  if (tid == 0) a.before[s.B] = blocks;
   __syncthreads();
 
   // the streaming kernel's pieces: of candidates a 16th apart the smallest that fits one wave
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     long long units = 0;
     for (int b = lane; b < s.B; b += 32) {
       const PagedSeq q = a.seqs[b];
-      if (q.n > 0 && !q.pair) units += (long long)tiles_of(s, q) * pieces_of(steps_of(s, q), (int)p);
+      if (q.n > 0 && !q.pair) units += (long long)tiles_of(a, q) * pieces_of(steps_of(s, q), (int)p);
     }
     units = warp_sum(units);
     if (lane == 0) fit[warp] = units * s.Hkv <= a.slots ? p : 0;
@@ -151,28 +156,30 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     PagedSeq q = {0, 0, 0, 1};
     if (b < s.B && RF_IDX_OK(b, s.B)) q = a.seqs[b];
     int nt = 0, ns = 0, np = 0;
-    if (q.n > 0 && !q.pair) nt = tiles_of(s, q), ns = steps_of(s, q), np = pieces(ns);
+    if (q.n > 0 && !q.pair) nt = tiles_of(a, q), ns = steps_of(s, q), np = pieces(ns);
     long long total;
     const long long at = units + block_scan((long long)nt * np, sm, &total);
-    // a warp writes the units of its 32 requests, one request after the other
-    for (int w = 0; w < 32; ++w) {
-      const int count = __shfl_sync(0xffffffffu, nt * np, w);
+    // a warp per request writes its units
+    cuts[tid] = make_int2(nt * np, np);
+    if (nt * np > 0) firsts[tid] = at;
+    __syncthreads();
+    for (int w = warp; w < THREADS && b0 + w < s.B; w += WARPS) {
+      const int count = cuts[w].x, n_p = cuts[w].y;
       if (count == 0) continue;
-      const int n_p = __shfl_sync(0xffffffffu, np, w), n_s = __shfl_sync(0xffffffffu, ns, w);
-      const long long u0 = __shfl_sync(0xffffffffu, at, w);
-      const int start = __shfl_sync(0xffffffffu, q.start, w), rows = __shfl_sync(0xffffffffu, q.n, w);
-      const int len = __shfl_sync(0xffffffffu, q.len, w);
+      const long long u0 = firsts[w];
+      const PagedSeq r = a.seqs[b0 + w];
+      const int n_s = steps_of(s, r);
       for (int u = lane; u < count; u += 32) {
         const int tile = u / n_p, i = u - tile * n_p;
         if (u0 + u >= a.unit_cap || !RF_IDX_OK(u0 + u, a.unit_cap)) break;
         PagedUnit x;
-        x.b = b0 + (warp << 5) + w;
+        x.b = b0 + w;
         x.tile = tile;
         x.step0 = (int)((long long)n_s * i / n_p);
         x.step1 = (int)((long long)n_s * (i + 1) / n_p);
         x.first = (int)(u0 + tile * n_p);
         x.pieces = n_p;
-        x.start = start, x.n = rows, x.len = len;
+        x.start = r.start, x.n = r.n, x.len = r.len;
         x.pad[0] = x.pad[1] = x.pad[2] = 0;
         a.units[u0 + u] = x;
         if (i == 0 && n_p > 1) {
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
         }
       }
     }
+    __syncthreads();
     units += total;
   }
   const int n_units = (int)min(units, (long long)a.unit_cap);
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       PagedRange r;
       r.b = lo;
       const PagedSeq q = a.seqs[lo];
-      const PagedBlocks k(q.n, q.len, s.positions(), s.window, s.sinks);
+      const PagedBlocks k(q.n, q.len, a.P_log2, s.window, s.sinks);
       const int tiles = k.tiles();
       const long long all = k.before(tiles);
       long long rel = w - a.before[lo];
@@ -238,11 +246,11 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       ++x.parts;
     }
     const PagedSeq q = a.seqs[r.b];
-    const int P = s.positions(), tiles = (q.n + P - 1) / P, group = r.item / tiles;
+    const int tiles = (q.n + (1 << a.P_log2) - 1) >> a.P_log2, group = r.item / tiles;
     x.b = r.b, x.start = q.start, x.rows = q.n, x.len = q.len;
     x.head = group * s.packed();
-    x.kvh = x.head / s.G();
-    x.row0 = (tiles - 1 - (r.item - group * tiles)) * P;
+    x.kvh = x.head / a.G;
+    x.row0 = (tiles - 1 - (r.item - group * tiles)) << a.P_log2;
     x.slot0 = 2 * (i - 1) + (same ? 0 : 1);
     x.rho = i;
     const int at = atomicAdd(&n_joins, 1);
@@ -335,6 +343,7 @@ rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const Pa
     if (a.clusters > sms / 2) a.clusters = sms / 2;
   }
   a.slots = 2 * sms;
+  a.G = s.G(), a.P_log2 = s.positions_log2(), a.groups = s.Hkv * (s.G() / s.packed());
   a.mark = l.mark;
   return launch_after(plan_kernel, 1, THREADS, 0, st, a);
 }

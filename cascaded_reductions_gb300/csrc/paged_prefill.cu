@@ -53,7 +53,7 @@ struct RangeItem {
 
 // the item from block j on of the tile at row0
 __device__ __forceinline__ void place_item(const PagedView& v, bool first, int j, RangeItem& it) {
-  const PagedBlocks k(it.rows, it.len, 1 << v.P_log2, v.s.window, v.s.sinks);
+  const PagedBlocks k(it.rows, it.len, v.P_log2, v.s.window, v.s.sinks);
   const int i = it.row0 >> v.P_log2;
   it.hb = k.hb(i);
   it.nw = it.hb - k.lb(i);

@@ -19,12 +19,14 @@
 // halves of its pairs, so that only the sum of squares crosses lanes.  Angles cost some 40
 // instructions a pair and are made once per token, for all heads.
 //   Many tokens (norm_rope_kernel): a warp takes a share of all heads of all tokens, makes
-// a token's angles, keeps them in registers and goes through its heads, with the rows of
-// two more items in flight.
+// a token's angles, keeps them in registers and goes through its heads, the next group's rows
+// in flight.
 //   Few (norm_rope_few_kernel): the heads of a token are spread over the warps of one CTA or
 // of several, each of which makes the token's angles for its own.
-// [8192 tokens, 32 + 8 + 8 heads of 128]: FIGURE; by the second kernel 45 us, whose every
-// item reads weights and angles from shared memory (85 % of its rate).
+// [8192 tokens, 32 + 8 + 8 heads of 128, 201 MB]: 40 us, 5.0 TB/s, and 45 us by the second
+// kernel, whose every item reads weights and angles from shared memory (85 % of its rate).
+// The first issues an instruction in 61 % of the cycles; shares of whole tokens take 44 us (2.2
+// per warp), two or more groups in flight 42, four CTAs per SM 45, two 44.
 
 #include <cuda_fp16.h>
 
@@ -141,32 +143,53 @@ norm_rope_kernel(const NormRope a) {
   const long long all = (long long)a.T * items, w0 = (long long)blockIdx.x * WARPS + warp;
   const long long ws = (long long)gridDim.x * WARPS;
   const long long first = all / ws * w0 + all % ws * w0 / ws, last = all / ws * (w0 + 1) + all % ws * (w0 + 1) / ws;
-  const int t_end = (int)(last / items), i_end = (int)(last - (long long)t_end * items);
-
-  struct Item {
-    int t, i;
+  // Walks over the items from item i of token t on: where the group's rows are, and the heads
+  // from it to the end of its part.
+  struct Walk {
+    int t, part, heads;
+  };
+  auto open = [&](long long n) {
+    Walk w;
+    w.t = (int)(n / items);
+    const int i = (int)(n - (long long)w.t * items);
+    w.part = i < nq ? 0 : i < nq + nk ? 1 : 2;
+    w.heads = (w.part ? a.Hkv : a.H) - HEADS * (i - (w.part == 0 ? 0 : w.part == 1 ? nq : nq + nk));
+    return w;
+  };
+  // on to the next group; true in a new part
+  auto step = [&](Walk& w) {
+    w.heads -= HEADS;
+    if (w.heads > 0) return false;
+    if (++w.part == (a.slots ? 3 : 2)) w.part = 0, ++w.t;
+    w.heads = w.part ? a.Hkv : a.H;
+    return true;
+  };
+  const int o0 = hl * D + c0 * 8, o1 = hl * D + c1 * 8;
+  auto from_of = [&](const Walk& w) {
+    return w.part == 0   ? a.q + w.t * a.q_step + (a.H - w.heads) * D
+           : w.part == 1 ? a.k + w.t * a.k_step + (a.Hkv - w.heads) * D
+                         : a.v + w.t * a.v_step + (a.Hkv - w.heads) * D;
+  };
+  Walk in = open(first);
+  const uint16_t* from = from_of(in);
+  int to_load = (int)(last - first), to_do = to_load;
+  struct Rows {
     uint4 x0, x1;
   };
-  auto within = [&](const Item& it) { return it.t < t_end || (it.t == t_end && it.i < i_end); };
-  auto load = [&](Item& it) {
-    it.x0 = it.x1 = make_uint4(0, 0, 0, 0);
-    if (!within(it) || !RF_IDX_OK(it.t, a.T)) return;
-    const bool q = it.i < nq, k = !q && it.i < nq + nk;
-    const int h = (q ? it.i : k ? it.i - nq : it.i - nq - nk) * HEADS + hl;
-    if (h >= (q ? a.H : a.Hkv)) return;
-    const uint16_t* row = (q ? a.q + it.t * a.q_step : k ? a.k + it.t * a.k_step : a.v + it.t * a.v_step) + h * D;
-    it.x0 = ld16(row + c0 * 8);
-    it.x1 = ld16(row + c1 * 8);
+  auto load = [&](Rows& r) {
+    r.x0 = r.x1 = make_uint4(0, 0, 0, 0);
+    if (to_load <= 0) return;
+    if (hl < in.heads && RF_IDX_OK(in.t, a.T)) {
+      r.x0 = ld16(from + o0);
+      r.x1 = ld16(from + o1);
+    }
+    --to_load;
+    from += HEADS * D;
+    if (step(in)) from = from_of(in);
   };
-  auto follow = [&](const Item& it, Item& to) {
-    to.i = it.i + 1, to.t = it.t;
-    if (to.i == items) to.i = 0, ++to.t;
-  };
-  Item it, one, two;
-  it.t = (int)(first / items), it.i = (int)(first - (long long)it.t * items);
+  Walk at = in;
+  Rows it, next;
   load(it);                                     // under way while the tables are made
-  follow(it, one);
-  load(one);
   for (int e = tid; e < 2 * D; e += WARPS * 32) {
     const void* w = e < D ? a.qw : a.kw;
     const int f = e % D, k = f / (4 * LANES), l = f / 4 % LANES;          // part k of lane l
@@ -177,88 +200,92 @@ norm_rope_kernel(const NormRope a) {
   for (int e = tid; e < half; e += WARPS * 32) unit[e] = turn_unit(RF_IDX_OK(e, half) ? a.freq[e] : 0.f);
   __syncthreads();
 
-  while (within(it)) {
-    const int t = it.t;
+  while (to_do > 0) {
+    const int t = at.t;
     __syncwarp();                               // the last token's angles have been read
     for (int e = lane; e < half; e += 32) turn_of(a, unit[e], e, t, &turn[half + e], &turn[e]);
     const int slot = a.slots && RF_IDX_OK(t, a.T) ? a.slots[t] : -1;
     const bool placed = slot >= 0 && slot < a.n_slots;
     const int page = placed ? slot / a.page : 0;
-    // row of head 0 in a pair of pages' places, or of the dense outputs
+    // a key head's row of the token, and the distance to the next head's
     const size_t kv_row = a.slots ? (size_t)page * a.Hkv * a.page + (slot - page * a.page) : (size_t)t * a.Hkv;
-    const size_t kv_head = a.slots ? a.page : 1;
+    const size_t kv_step = a.slots ? a.page : 1;
     __syncwarp();
-    uint64_t c[4], s[4];
+    uint64_t c[4], s[4], ns[4];
     if (j < rc) {
       const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(turn + 8 * j);
       const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(turn + half + 8 * j);
       c[0] = c2[0].x, c[1] = c2[0].y, c[2] = c2[1].x, c[3] = c2[1].y;
       s[0] = s2[0].x, s[1] = s2[0].y, s[2] = s2[1].x, s[3] = s2[1].y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ns[e] = pair::mul_f32x2(s[e], pair::pack_f32x2(-1.f, -1.f));
     }
-    while (it.t == t && within(it)) {
-      follow(one, two);
-      load(two);
-      const bool q = it.i < nq, k = !q && it.i < nq + nk;
-      const int h = (q ? it.i : k ? it.i - nq : it.i - nq - nk) * HEADS + hl;
-      const bool in = h < (q ? a.H : a.Hkv);
-      if (q || k) {
-        uint64_t x[8] = {widen2<F16>(it.x0.x), widen2<F16>(it.x0.y), widen2<F16>(it.x0.z), widen2<F16>(it.x0.w),
-                         widen2<F16>(it.x1.x), widen2<F16>(it.x1.y), widen2<F16>(it.x1.z), widen2<F16>(it.x1.w)};
-        if (q ? a.qw != nullptr : a.kw != nullptr) {
-          uint64_t s2 = 0ull;
+    while (to_do > 0 && at.t == t) {
+      // the groups of one part
+      const int part = at.part, all = part ? a.Hkv : a.H;
+      const bool stored = part == 0 || a.slots == nullptr || placed, norms = part == 0 ? a.qw != nullptr : a.kw != nullptr;
+      const size_t to_step = part == 0 ? D : kv_step * D;
+      uint16_t* to = part == 0 ? a.q_out + ((size_t)t * a.H + all - at.heads) * D
+                               : (part == 1 ? a.k_out : a.v_out) + (kv_row + (all - at.heads) * kv_step) * D;
+      to += hl * to_step;
+      const ulonglong2* w = reinterpret_cast<const ulonglong2*>(w_s + (part == 0 ? 0 : D)) + j;
+      bool more = true;
+      while (more && to_do > 0) {
+        load(next);
+        if (part < 2) {
+          uint64_t x[8] = {widen2<F16>(it.x0.x), widen2<F16>(it.x0.y), widen2<F16>(it.x0.z), widen2<F16>(it.x0.w),
+                           widen2<F16>(it.x1.x), widen2<F16>(it.x1.y), widen2<F16>(it.x1.z), widen2<F16>(it.x1.w)};
+          if (norms) {
+            uint64_t s2 = 0ull;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s2 = pair::fma_f32x2(x[e], x[e], s2);
-          float s0, s1;
-          pair::unpack_f32x2(s2, s0, s1);
-          const float r = rsqrtf(group_sum<LANES>(s0 + s1) * (1.f / D) + a.eps);
-          const uint64_t r2 = pair::pack_f32x2(r, r);
-          const ulonglong2* w = reinterpret_cast<const ulonglong2*>(w_s + (q ? 0 : D)) + j;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const ulonglong2 w2 = w[e * LANES];
-            x[2 * e] = pair::mul_f32x2(x[2 * e], pair::mul_f32x2(r2, w2.x));
-            x[2 * e + 1] = pair::mul_f32x2(x[2 * e + 1], pair::mul_f32x2(r2, w2.y));
-          }
-        }
-        if (j < rc) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // two pairs: their first values, their second ones
-            uint64_t u = x[e], v = x[e + 4];
-            if constexpr (INTERLEAVED) {
-              float p0, p1, q0, q1;
-              pair::unpack_f32x2(x[2 * e], p0, p1);
-              pair::unpack_f32x2(x[2 * e + 1], q0, q1);
-              u = pair::pack_f32x2(p0, q0);
-              v = pair::pack_f32x2(p1, q1);
-            }
+            for (int e = 0; e < 8; ++e) s2 = pair::fma_f32x2(x[e], x[e], s2);
             float s0, s1;
-            pair::unpack_f32x2(s[e], s0, s1);
-            const uint64_t y = pair::fma_f32x2(u, c[e], pair::mul_f32x2(v, pair::pack_f32x2(-s0, -s1)));
-            const uint64_t z = pair::fma_f32x2(v, c[e], pair::mul_f32x2(u, s[e]));
-            if constexpr (INTERLEAVED) {
-              float p0, p1, q0, q1;
-              pair::unpack_f32x2(y, p0, q0);
-              pair::unpack_f32x2(z, p1, q1);
-              x[2 * e] = pair::pack_f32x2(p0, p1);
-              x[2 * e + 1] = pair::pack_f32x2(q0, q1);
-            } else {
-              x[e] = y;
-              x[e + 4] = z;
+            pair::unpack_f32x2(s2, s0, s1);
+            const float r = rsqrtf(group_sum<LANES>(s0 + s1) * (1.f / D) + a.eps);
+            const uint64_t r2 = pair::pack_f32x2(r, r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const ulonglong2 w2 = w[e * LANES];
+              x[2 * e] = pair::mul_f32x2(x[2 * e], pair::mul_f32x2(r2, w2.x));
+              x[2 * e + 1] = pair::mul_f32x2(x[2 * e + 1], pair::mul_f32x2(r2, w2.y));
             }
           }
+          if (j < rc) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // two pairs: their first values, their second ones
+              uint64_t u = x[INTERLEAVED ? 2 * e : e], v = x[INTERLEAVED ? 2 * e + 1 : e + 4];
+              float p0, p1, q0, q1;
+              if constexpr (INTERLEAVED) {
+                pair::unpack_f32x2(u, p0, p1);
+                pair::unpack_f32x2(v, q0, q1);
+                u = pair::pack_f32x2(p0, q0);
+                v = pair::pack_f32x2(p1, q1);
+              }
+              uint64_t y = pair::fma_f32x2(u, c[e], pair::mul_f32x2(v, ns[e]));
+              uint64_t z = pair::fma_f32x2(v, c[e], pair::mul_f32x2(u, s[e]));
+              if constexpr (INTERLEAVED) {
+                pair::unpack_f32x2(y, p0, q0);
+                pair::unpack_f32x2(z, p1, q1);
+                y = pair::pack_f32x2(p0, p1);
+                z = pair::pack_f32x2(q0, q1);
+              }
+              x[INTERLEAVED ? 2 * e : e] = y;
+              x[INTERLEAVED ? 2 * e + 1 : e + 4] = z;
+            }
+          }
+          it.x0 = make_uint4(round2<F16>(x[0]), round2<F16>(x[1]), round2<F16>(x[2]), round2<F16>(x[3]));
+          it.x1 = make_uint4(round2<F16>(x[4]), round2<F16>(x[5]), round2<F16>(x[6]), round2<F16>(x[7]));
         }
-        it.x0 = make_uint4(round2<F16>(x[0]), round2<F16>(x[1]), round2<F16>(x[2]), round2<F16>(x[3]));
-        it.x1 = make_uint4(round2<F16>(x[4]), round2<F16>(x[5]), round2<F16>(x[6]), round2<F16>(x[7]));
+        if (stored && hl < at.heads) {
+          *reinterpret_cast<uint4*>(to + c0 * 8) = it.x0;
+          *reinterpret_cast<uint4*>(to + c1 * 8) = it.x1;
+        }
+        to += HEADS * to_step;
+        --to_do;
+        more = !step(at);
+        it = next;
       }
-      if (in && (q || !a.slots || placed)) {
-        uint16_t* dst = q ? a.q_out + ((size_t)t * a.H + h) * D
-                          : (k ? a.k_out : a.v_out) + (kv_row + h * kv_head) * D;
-        *reinterpret_cast<uint4*>(dst + c0 * 8) = it.x0;
-        *reinterpret_cast<uint4*>(dst + c1 * 8) = it.x1;
-      }
-      it = one;
-      one = two;
     }
   }
 }

@@ -503,7 +503,7 @@ rf_status rf_cache_evict(const void* k, const void* v, const float* weight, cons
  * Where the stack runs out, the first request whose new pages are not all there and
  * all behind it that need pages get none, and so does a request that would need more
  * than `width`: their tokens keep their rows with slot -1, their length and table stay.
- * No other buffers overlap.  One launch.
+ * No other buffers overlap.  One launch, two from 16384 tokens on.
  * Errors: RF_ERR_INVALID_ARG for null pointers, sizes <= 0 or overlapping buffers;
  * RF_ERR_UNSUPPORTED for B > 8192, or B * width, pages * page or width * page beyond
  * 2^31 - 1; RF_ERR_MISALIGNED unless positions and slots are 16-byte aligned.
