@@ -133,12 +133,20 @@ def pair_registers():
         return int(re.search(r"constexpr int REGS = (\d+)", f.read()).group(1))
 
 
+def divided_registers():
+    """The same of all kernels that divide their registers, by a part of their names."""
+    pair = pair_registers()
+    with open(os.path.join(CSRC, "paged_decode.cu")) as f:
+        teams = int(re.search(r"constexpr int REGS = (\d+)", f.read()).group(1))
+    return {"attn_pair_kernel": pair, "paged_pair_kernel": pair, "paged_decode_kernel": teams}
+
+
 def _report_pairs(log):
-    want = pair_registers()
     for name, n in registers(log).items():
-        if "attn_pair_kernel" in name and n != want:
-            print(f"WARNING: {name} has {n} registers per thread instead of {want}: the calls that run on it "
-                  "will return RF_ERR_UNSUPPORTED", file=sys.stderr)
+        for part, want in divided_registers().items():
+            if part in name and n != want:
+                print(f"WARNING: {name} has {n} registers per thread instead of {want}: the calls that run on "
+                      "it will return RF_ERR_UNSUPPORTED", file=sys.stderr)
 
 
 def build(force=False, verbose=False, extra_flags=(), lib=None, objdir=None):

@@ -36,7 +36,13 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-// The sizes of a step over a paged cache.
+// The sizes of a step over a paged cache.  A window that no request outgrows hides nothing.
+rf::PagedShape paged_shape(int B, int T, int H, int Hkv, int max_new, int max_len, int window, int sinks) {
+  if (window >= max_len) window = 0;
+  if (window == 0 && sinks > 0) sinks = 0;
+  return {B, T, H, Hkv, max_new, max_len, window, sinks > max_len && max_len > 0 ? max_len : sinks};
+}
+
 rf_status check_paged(const rf::PagedShape& s) {
   if (s.B <= 0 || s.T <= 0 || s.H <= 0 || s.Hkv <= 0 || s.max_new <= 0 || s.max_len <= 0 || s.window < 0 ||
       s.sinks < 0)
@@ -523,7 +529,7 @@ rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long l
 }
 
 size_t rf_paged_plan_bytes(int B, int T, int H, int Hkv, int max_new, int max_len, int window, int sinks) {
-  const rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks};
+  const rf::PagedShape s = paged_shape(B, T, H, Hkv, max_new, max_len, window, sinks);
   rf::PagedLayout l;
   return check_paged(s) == RF_OK && rf::paged_layout(s, &l) ? l.bytes : 0;
 }
@@ -532,7 +538,7 @@ rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T
                         int max_new, int max_len, int window, int sinks, void* plan, size_t bytes,
                         void* stream) {
   if (!starts || !lens || !plan) return RF_ERR_INVALID_ARG;
-  const rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks};
+  const rf::PagedShape s = paged_shape(B, T, H, Hkv, max_new, max_len, window, sinks);
   const rf_status st = check_paged(s);
   if (st != RF_OK) return st;
   if (reinterpret_cast<uintptr_t>(plan) % 256 != 0) return RF_ERR_MISALIGNED;
@@ -549,7 +555,7 @@ rf_status rf_attn_paged(const void* q, const void* kp, const void* vp, int pages
   if (!q || !kp || !vp || !table || !plan || !out) return RF_ERR_INVALID_ARG;
   if (pages <= 0 || page <= 0 || width <= 0 || D <= 0 || !isfinite(scale)) return RF_ERR_INVALID_ARG;
   if (dtype != RF_F32 && dtype != RF_BF16 && dtype != RF_F16) return RF_ERR_INVALID_ARG;
-  const rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks};
+  const rf::PagedShape s = paged_shape(B, T, H, Hkv, max_new, max_len, window, sinks);
   rf_status st = check_paged(s);
   if (st != RF_OK) return st;
   if ((long long)width * page < max_len) return RF_ERR_INVALID_ARG;

@@ -99,3 +99,126 @@ def test_python_layer_refuses_cpu_tensors_and_bad_shapes():
                  lambda: rf.qk_norm_rope(q, k, i(1, 4), f, v=k)):
         with pytest.raises(ValueError):
             call()
+
+
+def plan_args(**o):
+    return [o.get("starts", at(0)), o.get("lens", at(1)), o.get("B", 4), o.get("T", 100), o.get("H", 8),
+            o.get("Hkv", 2), o.get("max_new", 20), o.get("max_len", 1000), o.get("window", 0), o.get("sinks", 0),
+            o.get("plan", at(2)), ctypes.c_size_t(o.get("bytes", 1 << 40)), NULL]
+
+
+def attn_args(**o):
+    return [o.get("q", at(0)), o.get("kp", at(1)), o.get("vp", at(2)), o.get("pages", 300), o.get("page", 16),
+            o.get("table", at(3)), o.get("width", 64), o.get("plan", at(4)), ctypes.c_size_t(o.get("bytes", 1 << 40)),
+            o.get("B", 4), o.get("T", 100), o.get("H", 8), o.get("Hkv", 2), o.get("D", 128), o.get("max_new", 20),
+            o.get("max_len", 1000), o.get("window", 0), o.get("sinks", 0), F(o.get("scale", 0.1)), o.get("dtype", 1),
+            o.get("out", at(5)), NULL, NULL]
+
+
+@pytest.mark.parametrize("call,args", [("rf_paged_plan", plan_args), ("rf_attn_paged", attn_args)])
+def test_paged_size_refusals(lib, call, args):
+    f = getattr(lib, call)
+    for name in ("B", "T", "H", "Hkv", "max_new", "max_len"):
+        assert f(*args(**{name: 0})) == 1, name
+        assert f(*args(**{name: -1})) == 1, name
+    assert f(*args(H=7)) == 1                       # not a multiple of Hkv
+    assert f(*args(max_new=101)) == 1               # more than there are rows
+    assert f(*args(window=-1)) == 1
+    assert f(*args(sinks=-1)) == 1
+    assert f(*args(plan=NULL)) == 1
+    big = (1 << 30) + 1
+    assert f(*args(max_len=big, width=1 << 27)) == 2
+    assert f(*args(T=1 << 28, H=8)) == 2
+    assert f(*args(B=(1 << 20) + 1, width=64)) == 2
+    assert f(*args(H=(1 << 16) + 2)) == 2
+    assert f(*args(plan=at(4, 128))) == 3
+
+
+def test_plan_refusals(lib):
+    for name in ("starts", "lens"):
+        assert lib.rf_paged_plan(*plan_args(**{name: NULL})) == 1, name
+    lib.rf_paged_plan_bytes.restype = ctypes.c_size_t
+    for bad in ((0, 1, 1, 1, 1, 1, 0, 0), (1, 1, 3, 2, 1, 1, 0, 0), (1, 1, 1, 1, 2, 1, 0, 0), (1, 1, 1, 1, 1, 1, -1, 0)):
+        assert lib.rf_paged_plan_bytes(*bad) == 0
+
+
+def test_attn_refusals(lib):
+    f = lib.rf_attn_paged
+    for name in ("q", "kp", "vp", "table", "out"):
+        assert f(*attn_args(**{name: NULL})) == 1, name
+    for name in ("pages", "page", "width", "D"):
+        assert f(*attn_args(**{name: 0})) == 1, name
+    assert f(*attn_args(width=62)) == 1             # 992 keys
+    for scale in (float("nan"), float("inf")):
+        assert f(*attn_args(scale=scale)) == 1
+    assert f(*attn_args(dtype=3)) == 1
+    assert f(*attn_args(dtype=0)) == 2              # fp32
+    assert f(*attn_args(D=64)) == 2
+    assert f(*attn_args(scale=0.0)) == 2
+    assert f(*attn_args(scale=-0.1)) == 2
+    for page in (1, 8, 24, 48, 512):
+        assert f(*attn_args(page=page, width=2000)) == 2, page
+    assert f(*attn_args(pages=1 << 30)) == 2
+    assert f(*attn_args(width=1 << 30)) == 2
+    for name in ("q", "kp", "vp", "out"):
+        assert f(*attn_args(**{name: at(20, 8)})) == 3, name
+
+
+def test_python_layer_of_the_paged_attention():
+    import cascaded_reductions_gb300 as rf
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)                                   # noqa: E731
+    q, kp = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(9, 2, 16, 128, dtype=torch.bfloat16)
+    plan = rf.PagedPlan(torch.zeros(100, dtype=torch.uint8), (0, 2, 4, 8, 2), 2, 48, 0, 0)
+    for call in (lambda: rf.paged_plan(i(3), i(2), 4, 8, 2, 2, 48),
+                 lambda: rf.attn_paged(q, kp, kp, i(2, 3), plan),
+                 lambda: rf.attn_paged(q[0], kp, kp, i(2, 3), plan),
+                 lambda: rf.attn_paged(q, kp, kp, i(6), plan)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_quick_calls_leave_what_they_cannot_take_to_python():
+    import cascaded_reductions_gb300 as rf
+    if rf._calls is None:
+        pytest.skip("the extension is not built here")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)                                   # noqa: E731
+    q, k = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    c = rf._calls
+    assert c.page_tables(1, i(4), i(4), i(4, 3), i(9), i(1), 16, 8) is None             # not on a GPU
+    assert c.page_tables(1, i(4), i(4), i(4, 3), i(9), i(1), 16) is None                # too few
+    assert c.qk_norm_rope(1, q, k, i(1, 4), torch.ones(64), None, None, None, False, 1e-6, None, None, None,
+                          None) is None
+    assert c.qk_norm_rope(1, q, k, i(1, 4), torch.ones(64), None, None, None, 0, 1e-6, None, None, None,
+                          None) is None                                                 # interleaved is no bool
+    kp = torch.zeros(9, 2, 16, 128, dtype=torch.bfloat16)
+    sizes = (0, 2, 4, 8, 2)
+    assert c.attn_paged(1, q, kp, kp, i(2, 3), torch.zeros(9, dtype=torch.uint8), sizes, 2, 48, 0, 0, None) is None
+    assert c.attn_paged("x", q, kp, kp, i(2, 3), None, sizes, 2, 48, 0, 0, None) is None
+
+
+def test_kernels_that_divide_their_registers_have_them():
+    """Read from the compiler's report of the library in place."""
+    import glob
+    import os
+
+    from conftest import load_builder
+    b = load_builder()
+    b.build()
+    want, seen = b.divided_registers(), {}
+    for path in glob.glob(os.path.join(b.OBJDIR, "paged_*.ptxas")):
+        with open(path) as f:
+            seen.update(b.registers(f.read()))
+    for part in ("paged_pair_kernel", "paged_decode_kernel"):
+        mine = {n: r for n, r in seen.items() if part in n}
+        assert len(mine) == 2 and set(mine.values()) == {want[part]}, (part, mine)
+
+
+def test_other_registers_of_the_teams_kernel_are_told(capfd):
+    from conftest import load_builder
+    b = load_builder()
+    report = ("ptxas info    : Compiling entry function '_Z19paged_decode_kernelI1P' for 'sm_103a'\n"
+              "ptxas info    : Used {} registers, used 16 barriers\n")
+    b._report_pairs(report.format(160))
+    assert "RF_ERR_UNSUPPORTED" in capfd.readouterr().err
+    b._report_pairs(report.format(b.divided_registers()["paged_decode_kernel"]))
+    assert capfd.readouterr().err == ""
