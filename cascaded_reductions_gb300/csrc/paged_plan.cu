@@ -22,6 +22,8 @@ namespace {
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr int MANY_STEPS = 12;          // of a large call's piece at least
 constexpr int MANY_UNITS = 8;           // and per CTA at most, on average
+constexpr int MAX_RANGES = 1024;
+constexpr int WHOLE_BLOCKS = 3;         // of a tile that is never cut
 constexpr int ROUND_BLOCKS = 32;        // of a range at least, where there are several rounds
 constexpr long long ROUND_KEYS = 98304; // keys of all key heads (512 bytes each) of a round
 
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   __shared__ long long sm[WARPS], fit[WARPS];
   __shared__ int n_joins, n_merges;
   __shared__ int2 cuts[THREADS];
-  __shared__ long long firsts[THREADS];
+  __shared__ long long firsts[THREADS], starts[MAX_RANGES + 1];
   const PagedShape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = a.groups;
@@ -203,7 +205,6 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     n_ranges = (int)rounds * active;
     for (int i = tid; i < n_ranges; i += THREADS) {
       const long long w = blocks / n_ranges * i + blocks % n_ranges * i / n_ranges;
-      const long long end = blocks / n_ranges * (i + 1) + blocks % n_ranges * (i + 1) / n_ranges;
       int lo = 0, n = s.B;              // last request with before[b] <= w
       while (n > 1) {
         const int half = n >> 1;
@@ -227,9 +228,29 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       }
       r.item = group * tiles + t0;
       r.block = (int)(rel - (all - k.before(tiles - t0)));
-      r.count = (int)(end - w);
+      // A tile of few blocks is not worth its parts' way through memory: it goes whole to the
+      // range that has more of it.
+      const int mine = k.blocks(tiles - 1 - t0);
+      long long start = w;
+      if (mine <= WHOLE_BLOCKS && r.block > 0) {
+        const bool up = 2 * r.block >= mine;
+        start += up ? mine - r.block : -r.block;
+        r.block = 0;
+        if (up && ++r.item == tiles * a.groups) {
+          r.item = 0;
+          while (++r.b < s.B && !a.seqs[r.b].pair) {
+          }
+          if (r.b == s.B) r.b = lo;     // behind the last block: the range has none
+        }
+      }
+      r.count = 0;
+      starts[i] = start;
       if (RF_IDX_OK(i, a.range_cap)) a.ranges[i] = r;
     }
+    if (tid == 0) starts[n_ranges] = blocks;
+    __syncthreads();
+    for (int i = tid; i < n_ranges; i += THREADS)
+      if (RF_IDX_OK(i, a.range_cap)) a.ranges[i].count = (int)(starts[i + 1] - starts[i]);
   }
   __syncthreads();
   // the tiles that a range's start cuts for the first time
@@ -291,7 +312,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
     const int pairs = sms / 2;
     long long rounds = blocks / ((long long)pairs * ROUND_BLOCKS);
     rounds = rounds < 1 ? 1 : rounds > kPagedRounds ? kPagedRounds : rounds;
-    l->range_cap = (int)(rounds * pairs);
+    l->range_cap = (int)(rounds * pairs < MAX_RANGES ? rounds * pairs : MAX_RANGES);
   }
   size_t at = align(kPlanWords * sizeof(int));
   const auto take = [&](size_t bytes) {

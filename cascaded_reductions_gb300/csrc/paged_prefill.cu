@@ -131,10 +131,12 @@ struct PagedPrefill {
     }
     if (a.v.head[kPlanMark] != (int)a.v.mark) return false;
     const int clusters = a.v.head[kPlanClusters], ranges = min(a.v.head[kPlanRanges], a.v.range_cap);
-    const int rho = t == 0 ? cluster : it.rho + clusters;
-    if (cluster >= clusters || rho >= ranges) return false;
-    first_item(a.v, rho, it);
-    return true;
+    if (cluster >= clusters) return false;
+    for (int rho = t == 0 ? cluster : it.rho + clusters; rho < ranges; rho += clusters) {
+      first_item(a.v, rho, it);
+      if (it.n > 0) return true;                        // a range may have lost its few blocks
+    }
+    return false;
   }
   // the block of keys that is the item's j-th
   __device__ __forceinline__ int block_of(const Item& it, int j) const {
