@@ -20,6 +20,7 @@ constexpr int kPagedBlock = 256;        // keys of the pair kernel's blocks
 constexpr int kPagedPairRows = 256;
 constexpr int kPagedSlotFloats = kPagedPairRows * (128 + 2);   // a partial state: O, m, l
 constexpr int kPagedRounds = 4;
+constexpr int kPagedSinks = 64;         // keys of the pair kernel's copies at most
 constexpr int kPagedFewSteps = 16;      // steps of 64 keys per CTA of a small call of the streaming kernel
 
 // The sizes that a plan and the calls over it share.
@@ -120,26 +121,29 @@ struct PagedTiles {
 
 // The tiles of one head group of a request on the pair kernel: tile i holds positions
 // p0 + i P .. , P = 256 / heads; it visits the window's blocks [lb, hb) and up to SB
-// blocks of sinks below them.
+// blocks of sinks below them.  Where the lowest window block begins with as many keys that
+// no row of the tile sees as the sinks take (in 64s), the sinks go in their place: 4 sinks
+// would else cost a block of their own.
 struct PagedBlocks {
-  int n, p0, log2, window, SB;          // P = 2^log2
+  int n, p0, log2, window, SB, S64;     // P = 2^log2
   __host__ __device__ PagedBlocks(int n_, int len, int log2_, int window_, int sinks)
       : n(n_), p0(len - n_), log2(log2_), window(window_),
-        SB(window_ > 0 ? (int)(((long long)sinks + kPagedBlock - 1) / kPagedBlock) : 0) {}
+        SB(window_ > 0 ? (int)(((long long)sinks + kPagedBlock - 1) / kPagedBlock) : 0),
+        S64(window_ > 0 ? (sinks + kPagedSinks - 1) / kPagedSinks * kPagedSinks : 0) {}
   __host__ __device__ int tiles() const { return (n + (1 << log2) - 1) >> log2; }
   __host__ __device__ int end(int i) const { return (i + 1) << log2 < n ? (i + 1) << log2 : n; }
   __host__ __device__ int hb(int i) const {
     const int x = p0 + end(i);
     return x <= kPagedBlock ? 1 : (x + kPagedBlock - 1) / kPagedBlock;
   }
-  __host__ __device__ int lb(int i) const {
-    if (window == 0) return 0;
-    const int lo = p0 + (i << log2) - window + 1;
-    return lo > 0 ? lo / kPagedBlock : 0;
+  __host__ __device__ int lo(int i) const { return p0 + (i << log2) - window + 1; }
+  __host__ __device__ int lb(int i) const { return window > 0 && lo(i) > 0 ? lo(i) / kPagedBlock : 0; }
+  __host__ __device__ bool folds(int i) const {
+    return S64 > 0 && lo(i) >= kPagedBlock && lo(i) % kPagedBlock >= S64;
   }
   __host__ __device__ int sink_blocks(int i) const {
     const int l = lb(i);
-    return SB < l ? SB : l;
+    return folds(i) ? 0 : SB < l ? SB : l;
   }
   __host__ __device__ int blocks(int i) const { return hb(i) - lb(i) + sink_blocks(i); }
 
@@ -166,6 +170,20 @@ struct PagedBlocks {
       if (k < m) {
         c = (c + (k << log2)) >> log2;
         sum -= down(c + (m - k), r) - down(c, r);
+      }
+      if (S64 > 0 && S64 < kPagedBlock) {   // and a block for each tile that folds its sinks in
+        const long long c1 = (long long)p0 - window + 1;
+        const long long k1 = c1 < kPagedBlock ? (kPagedBlock - c1 + P - 1) >> log2 : 0;
+        if (k1 < m) {
+          const long long turns = (m - k1) >> r, rest = (m - k1) & ((1 << r) - 1);
+          int all = 0, some = 0;
+          for (int j = 0; j < 1 << r; ++j) {
+            const bool is = ((c1 + ((k1 + j) << log2)) & (kPagedBlock - 1)) >= S64;
+            all += is;
+            some += is && j < rest;
+          }
+          sum -= turns * all + some;
+        }
       }
     }
     return sum;

@@ -9,7 +9,7 @@
 // positions.  It visits the 256-key blocks that its rows see, last block first.
 //
 // Pages: a block's pages are copied one by one, a lane of the copying warp each, from a
-// map of [pages * Hkv][page][128] whose boxes are one page of 64 columns.  Rows behind a
+// map of [pages * Hkv][page][128] whose boxes are a page, or 64 rows of one, by 64 columns.  Rows behind a
 // request's end must not be read, NaN among them would reach every row (0 * NaN); a
 // box has no shorter form, but one that starts above its page fills what lies outside
 // with zeros.  So the last page is copied from row m - page on for the m rows in use,
@@ -48,7 +48,10 @@ struct RangeItem {
   int slot;            // of the partial state, -1 for a whole tile
   int start, rows, len;           // the request
   int head, kvh, row0;            // first query head, key head, first new token of the tile
-  int hb, nw;          // window blocks hb - 1, hb - 2 .. (nw of them), then those of the sinks from 0 on
+  int hb, nw;          // window blocks hb - 1, hb - 2 .. (nw of them), then those of the sinks from 0 on;
+                       // with FOLDS the sinks are in the last window block's first places
+  static constexpr int FOLDS = 1 << 30;
+  __device__ __forceinline__ int windows() const { return nw & ~FOLDS; }
 };
 
 // the item from block j on of the tile at row0
@@ -58,6 +61,7 @@ __device__ __forceinline__ void place_item(const PagedView& v, bool first, int j
   it.hb = k.hb(i);
   it.nw = it.hb - k.lb(i);
   const int all = it.nw + k.sink_blocks(i);
+  if (k.folds(i)) it.nw |= RangeItem::FOLDS;
   it.j0 = j;
   it.n = min(all - j, it.left);
   it.left -= it.n;
@@ -113,8 +117,8 @@ struct PagedPrefill {
   static constexpr float M_START = -1e30f;
   using Item = RangeItem;
   struct Pages {
-    int kpage, vpage;             // the lane's pages of the block, by their places in the table's row
-    int kid, vid;                 // and the entries there, not looked at before the copies
+    int kkey, vkey;               // first keys of the lane's copies
+    int kid, vid;                 // and their pages' entries, not looked at before the copies
   };
   struct Pending {
     int row, head;
@@ -140,8 +144,14 @@ struct PagedPrefill {
   }
   // the block of keys that is the item's j-th
   __device__ __forceinline__ int block_of(const Item& it, int j) const {
-    const int J = it.j0 + j;
-    return J < it.nw ? it.hb - 1 - J : J - it.nw;
+    const int J = it.j0 + j, nw = it.windows();
+    return J < nw ? it.hb - 1 - J : J - nw;
+  }
+  // keys of the block's first places that are sinks instead
+  __device__ __forceinline__ int folded(const Item& it, int j) const {
+    return it.nw & Item::FOLDS && it.j0 + j == it.windows() - 1
+               ? (a.v.s.sinks + kPagedSinks - 1) / kPagedSinks * kPagedSinks
+               : 0;
   }
   __device__ __forceinline__ int page() const { return 1 << a.page_log2; }
   // rows that the last page lacks, and whether the block holds that page
@@ -161,47 +171,49 @@ struct PagedPrefill {
     tc::tma_load_3d_pair(dst, map, bar, 0, row, head);
     tc::tma_load_3d_pair(dst + HALF_BYTES, map, bar, 64, row, head);
   }
-  // A half of K is 128 keys in two boxes of 64 columns per page (page <= 128), V all 256 in
-  // one; of a page of 256 a half of K is 128 rows.
-  __device__ __forceinline__ int k_pages() const { return max(1, BM >> a.page_log2); }
-  __device__ __forceinline__ int entry(const Item& it, int i) const {
+  // Keys are copied a page at a time, or 64 of a larger page: a half of K is 128 keys in
+  // boxes of 64 columns, two of them each, V all 256 in one.
+  __device__ __forceinline__ int box_log2() const { return min(a.page_log2, 6); }
+  __device__ __forceinline__ int entry(const Item& it, int key) const {
+    const int i = key >> a.page_log2;
     const size_t at = (size_t)it.b * a.width + i;
     return i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width) ? a.table[at] : -1;
   }
   __device__ __forceinline__ Pages pages_of(const Item& it, int j, int rank, int lane) const {
-    const int first = block_of(it, j) * BN >> a.page_log2, nk = k_pages();
+    const int base = block_of(it, j) * BN, fold = folded(it, j), nk = BM >> box_log2();
     Pages p = {0, 0, -1, -1};
     if (lane < 2 * nk) {
-      p.kpage = first + (page() > BM ? 0 : rank * nk + (lane >= nk ? lane - nk : lane));
-      p.kid = entry(it, p.kpage);
+      const int at = (rank * nk + (lane >= nk ? lane - nk : lane)) << box_log2();
+      p.kkey = at < fold ? at : base + at;
+      p.kid = entry(it, p.kkey);
     }
-    if (lane < BN >> a.page_log2) {
-      p.vpage = first + lane;
-      p.vid = entry(it, p.vpage);
+    if (lane < 2 * nk) {
+      const int at = lane << box_log2();
+      p.vkey = at < fold ? at : base + at;
+      p.vid = entry(it, p.vkey);
     }
     return p;
   }
-  // coordinates (y, z) of page i with that entry; zeros come from behind the map
-  __device__ __forceinline__ void place(const Item& it, int i, int id, int& y, int& z) const {
-    const int used = (it.len + page() - 1) >> a.page_log2;
+  // coordinates (y, z) of a key with that entry; zeros come from behind the map
+  __device__ __forceinline__ void place(const Item& it, int key, int id, int& y, int& z) const {
+    const int i = key >> a.page_log2, used = (it.len + page() - 1) >> a.page_log2;
     z = i < used && (unsigned)id < (unsigned)a.pages ? id * a.v.s.Hkv + it.kvh : a.pages * a.v.s.Hkv;
-    y = i == used - 1 ? -lacking(it) : 0;
+    y = (key & (page() - 1)) - (i == used - 1 ? lacking(it) : 0);
   }
   __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Item& it,
-                                         const Pages& p, int rank, int lane) const {
-    const int nk = k_pages(), col = lane >= nk, i = lane - col * nk;
+                                         const Pages& p, int, int lane) const {
+    const int nk = BM >> box_log2(), col = lane >= nk, i = lane - col * nk;
     if (lane >= 2 * nk) return;
     int y, z;
-    place(it, p.kpage, p.kid, y, z);
-    if (page() > BM) y += rank * BM;
-    tc::tma_load_3d_pair(dst + col * HALF_BYTES + i * page() * 128, map, bar, 64 * col, y, z);
+    place(it, p.kkey, p.kid, y, z);
+    tc::tma_load_3d_pair(dst + col * HALF_BYTES + (i << box_log2()) * 128, map, bar, 64 * col, y, z);
   }
   __device__ __forceinline__ void load_v(uint8_t* dst, const CUtensorMap* map, uint32_t bar, const Item& it,
                                          const Pages& p, int rank, int lane) const {
-    if (lane >= BN >> a.page_log2) return;
+    if (lane >= BN >> box_log2()) return;
     int y, z;
-    place(it, p.vpage, p.vid, y, z);
-    tc::tma_load_3d_pair(dst + lane * page() * 128, map, bar, rank * 64, y, z);
+    place(it, p.vkey, p.vid, y, z);
+    tc::tma_load_3d_pair(dst + (lane << box_log2()) * 128, map, bar, rank * 64, y, z);
   }
   __device__ __forceinline__ int keys(const Item&, int) const { return BN; }
 
@@ -220,7 +232,7 @@ struct PagedPrefill {
   __device__ __forceinline__ Row row_of_item(const Item& it, int rank, int r, int kh) const {
     const int low = position(it, rank, r & ~31), window = a.v.s.window;
     const int top = (it.hb - 1) * BN + kh * BM;       // first key of the half in the tile's block 0
-    int first = max(0, (top + BM - 1 - low + BN - 1) >> 8), end = it.nw;
+    int first = max(0, (top + BM - 1 - low + BN - 1) >> 8), end = it.windows();
     static_assert(BN == 256, "the shifts");
     if (lacking(it) != 0 && holds_last(it, it.hb - 1)) first = max(first, 1);
     if (window > 0) end = min(end, ((top - (low + 31 - window + 1)) >> 8) + 1);
@@ -236,12 +248,15 @@ struct PagedPrefill {
     const int cs = a.v.s.sinks - base;
     const int d = moved ? lacking(it) : 0;
     const int c0 = moved ? ((it.len - 1) & ~(page() - 1)) - base : BN;
+    // the sinks' places and those of them that hold sinks
+    const int fold = folded(it, j) - kh * BM, sunk = a.v.s.sinks - kh * BM;
     uint32_t vis[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t plain = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(cs - 32 * q));
       const uint32_t behind = below(hi + d + 1 - 32 * q) & (~below(lo + d - 32 * q) | below(cs + d - 32 * q));
       vis[q] = (plain & below(c0 - 32 * q)) | (behind & ~below(c0 + d - 32 * q));
+      vis[q] = (vis[q] & ~below(fold - 32 * q)) | (below(sunk - 32 * q) & below(fold - 32 * q));
     }
     bits = make_uint4(vis[0], vis[1], vis[2], vis[3]);
   }
@@ -583,11 +598,12 @@ rf_status launch_pairs(const PagedAttn& a, cudaStream_t st) {
   const PagedShape& s = a.v.s;
   const uint64_t row = (uint64_t)HD * 2, page = 1ull << a.page_log2;
   const uint32_t box = s.positions() < BM ? s.positions() : BM;
+  const uint32_t rows = (uint32_t)(page < 64 ? page : 64);
   CUtensorMap tq, tk, tv, to;
   if (!make_map(&tq, F16, a.q, s.T, s.H, row * s.H, row, box, BM / box) ||
       !make_map(&tk, F16, a.kp, page, (uint64_t)a.pages * s.Hkv, row, row * page,
-                (uint32_t)(page < BM ? page : BM), 1) ||
-      !make_map(&tv, F16, a.vp, page, (uint64_t)a.pages * s.Hkv, row, row * page, (uint32_t)page, 1) ||
+                rows, 1) ||
+      !make_map(&tv, F16, a.vp, page, (uint64_t)a.pages * s.Hkv, row, row * page, rows, 1) ||
       !make_map(&to, F16, a.out, s.T, s.H, row * s.H, row, 32, 1))
     return RF_ERR_CUDA;
   P p = {};

@@ -142,6 +142,13 @@ def test_windowed_chunks(window, sinks):
     run(lens, news, 4, 1, 32, window, sinks, seed=window, rows=[0, 1, 63, 64, 100, 255, 256, -2, -1])
 
 
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(300, 1), (257, 64), (700, 65), (200, 128), (640, 190), (129, 200)])
+def test_sinks_in_the_window_s_lowest_block(window, sinks, page):
+    """Tiles whose lowest block begins with room for the sinks, and tiles beside them without."""
+    run([1500, 900, 777], [400, 130, 777], 8, 1, page, window, sinks, seed=window + page, rows=list(range(0, 400, 13)))
+
+
 def test_mixed_batch():
     news = [1, 200, 0, 5, 1, 77, 0, 1, 16, 300]
     lens = [900, 500, 40, 5, 1, 1300, 0, 256, 16, 300]
