@@ -7,7 +7,8 @@
 // from lists that paged_plan.cu makes once per step from the lengths on the device:
 //   units    of the streaming kernel: 16 rows and a piece of their keys;
 //   ranges   of the pair kernel: all 256-key blocks of all tiles, one after the other,
-//            cut into equal ranges wherever that falls, a range per cluster and round.
+//            in a range per cluster and round; those of the last round are cut wherever an
+//            equal share for all clusters falls, inside a tile too.
 #pragma once
 
 #include "cache_common.cuh"
@@ -19,7 +20,7 @@ constexpr int kPagedTileRows = 16;
 constexpr int kPagedBlock = 256;        // keys of the pair kernel's blocks
 constexpr int kPagedPairRows = 256;
 constexpr int kPagedSlotFloats = kPagedPairRows * (128 + 2);   // a partial state: O, m, l
-constexpr int kPagedRounds = 4;
+constexpr int kPagedRounds = 16;
 constexpr int kPagedSinks = 64;         // keys of the pair kernel's copies at most
 constexpr int kPagedFewSteps = 16;      // steps of 64 keys per CTA of a small call of the streaming kernel
 
@@ -56,12 +57,12 @@ struct PagedShape {
 };
 
 // Words of a plan's head.
-enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanJoins, kPlanMerges, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
+enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanLast, kPlanJoins, kPlanMerges, kPlanQueue, kPlanFlag, kPlanDone, kPlanWords = 64 };
 
 // Where the parts of a plan lie, in bytes from its start.
 struct PagedLayout {
   size_t seqs, before, ranges, joins, units, merges, counters, unit_ml, unit_acc, slots, bytes;
-  int unit_cap, range_cap, merge_cap;
+  int unit_cap, range_cap, merge_cap, slot_cap;
   uint32_t mark;                        // of the sizes: a plan of others is refused on the device
 };
 
@@ -79,7 +80,7 @@ struct PagedRange {
   int b, item, block, count;            // the first block's request, item and number in it; blocks
 };
 // A tile that cuts divide: its first part is the state slot0, the others are slots
-// 2 rho, 2 rho + 2 ..
+// 2 rho, 2 rho + 2 .. (rho: the range of the second part, of the last round's)
 struct PagedJoin {
   int b, start, rows, len;              // the request
   int head, kvh, row0;                  // first query head, key head, first new token of the tile
@@ -99,7 +100,7 @@ struct PagedView {
   float2* unit_ml;                      // [unit][Hkv][unit_rows]
   float* unit_acc;                      // [unit][Hkv][unit_rows][128]
   float* slots;
-  int unit_cap, range_cap, merge_cap;
+  int unit_cap, range_cap, merge_cap, slot_cap;
   uint32_t mark;
   int G, packed, P_log2, groups, key_groups;   // heads per key head and per tile; positions of a
                                         // tile; head groups in all and per key head
@@ -215,7 +216,7 @@ inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* pla
   v.unit_acc = reinterpret_cast<float*>(p + l.unit_acc);
   v.slots = reinterpret_cast<float*>(p + l.slots);
   v.merges = reinterpret_cast<const int*>(p + l.merges);
-  v.unit_cap = l.unit_cap, v.range_cap = l.range_cap, v.merge_cap = l.merge_cap;
+  v.unit_cap = l.unit_cap, v.range_cap = l.range_cap, v.merge_cap = l.merge_cap, v.slot_cap = l.slot_cap;
   v.mark = l.mark;
   v.G = s.G(), v.packed = s.packed(), v.P_log2 = s.positions_log2();
   v.key_groups = v.G / v.packed, v.groups = s.Hkv * v.key_groups;

@@ -11,7 +11,9 @@
 //  * the pair kernel's blocks, counted in closed form per request, cut into ranges.
 //    Tiles of one key head read the same keys, so ranges that run at the same time
 //    should lie close together: with more keys than the L2 cache holds, the
-//    blocks are dealt out in up to four rounds.
+//    blocks are dealt out in rounds (4 x 32 heads of 8192 keys of their own: FIG).  Ranges of
+//    the rounds before the last end with a tile; in the last one every cluster gets what
+//    it lacks to an equal share.
 
 #include "paged.cuh"
 #include "tc_common.cuh"
@@ -22,7 +24,7 @@ namespace {
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr int MANY_STEPS = 12;          // of a large call's piece at least
 constexpr int MANY_UNITS = 8;           // and per CTA at most, on average
-constexpr int MAX_RANGES = 1024;
+constexpr int MAX_RANGES = 2048;
 constexpr int WHOLE_BLOCKS = 3;         // of a tile that is never cut
 constexpr int ROUND_BLOCKS = 32;        // of a range at least, where there are several rounds
 constexpr long long ROUND_KEYS = 98304; // keys of all key heads (512 bytes each) of a round
@@ -85,12 +87,14 @@ __device__ __forceinline__ int pieces_of(int steps, int piece) { return (steps +
 
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   __shared__ long long sm[WARPS], fit[WARPS];
-  __shared__ int n_joins, n_merges;
+  __shared__ int n_joins, n_merges, top_blocks;
   __shared__ int2 cuts[THREADS];
   __shared__ long long firsts[THREADS], starts[MAX_RANGES + 1];
   const PagedShape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = a.groups;
+  if (tid == 0) top_blocks = 0;
+  __syncthreads();
   wait_prerequisite();
   allow_dependents();
   long long steps = 0, blocks = 0, keys = 0;
@@ -108,6 +112,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     if (q.pair) {
       const PagedBlocks k(q.n, q.len, a.P_log2, s.window, s.sinks);
       mine = k.before(k.tiles()) * groups;
+      atomicMax(&top_blocks, k.blocks(k.tiles() - 1));
     }
     long long at = 0;
     if (a.clusters > 0) {
@@ -197,22 +202,17 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   for (long long i = tid; i < (long long)n_units * s.Hkv; i += THREADS) a.counters[i] = 0;
 
   // the pair kernel's ranges
-  int n_ranges = 0, active = 0;
+  int n_ranges = 0, active = 0, last0 = 0;
   if (blocks > 0 && a.clusters > 0) {
     active = (int)min((long long)a.clusters, blocks);
-    long long rounds = (keys + ROUND_KEYS - 1) / ROUND_KEYS;
-    rounds = max(1ll, min(min(rounds, blocks / ((long long)active * ROUND_BLOCKS)), (long long)(a.range_cap / active)));
-    n_ranges = (int)rounds * active;
-    for (int i = tid; i < n_ranges; i += THREADS) {
-      const long long w = blocks / n_ranges * i + blocks % n_ranges * i / n_ranges;
+    // where block w of all lies: its tile's request, item, blocks, and its number in the tile
+    auto locate = [&](long long w, PagedRange& r, int& mine) {
       int lo = 0, n = s.B;              // last request with before[b] <= w
       while (n > 1) {
         const int half = n >> 1;
         if (a.before[lo + half] <= w) lo += half;
         n -= half;
       }
-      PagedRange r;
-      r.b = lo;
       const PagedSeq q = a.seqs[lo];
       const PagedBlocks k(q.n, q.len, a.P_log2, s.window, s.sinks);
       const int tiles = k.tiles();
@@ -226,27 +226,55 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
         if (all - k.before(tiles - (t0 + half)) <= rel) t0 += half;
         tn -= half;
       }
+      r.b = lo;
       r.item = group * tiles + t0;
       r.block = (int)(rel - (all - k.before(tiles - t0)));
-      // A tile of few blocks is not worth its parts' way through memory: it goes whole to the
-      // range that has more of it.
-      const int mine = k.blocks(tiles - 1 - t0);
-      long long start = w;
-      if (mine <= WHOLE_BLOCKS && r.block > 0) {
+      r.count = 0;
+      mine = k.blocks(tiles - 1 - t0);
+      return tiles * a.groups;          // the request's items
+    };
+    // Range i starts at block w; or, where its tile has at most `whole` blocks, at the end of
+    // that tile that is nearer.
+    auto start_range = [&](int i, long long w, int whole) {
+      PagedRange r;
+      int mine;
+      const int items = locate(min(w, blocks - 1), r, mine);
+      if (w >= blocks) {
+        r.block = 0;                    // the range has no block
+      } else if (mine <= whole && r.block > 0) {
         const bool up = 2 * r.block >= mine;
-        start += up ? mine - r.block : -r.block;
+        w += up ? mine - r.block : -r.block;
         r.block = 0;
-        if (up && ++r.item == tiles * a.groups) {
+        if (up && ++r.item == items) {
+          const int b = r.b;
           r.item = 0;
           while (++r.b < s.B && !a.seqs[r.b].pair) {
           }
-          if (r.b == s.B) r.b = lo;     // behind the last block: the range has none
+          if (r.b == s.B) r.b = b;      // behind the last block
         }
       }
-      r.count = 0;
-      starts[i] = start;
+      starts[i] = w;
       if (RF_IDX_OK(i, a.range_cap)) a.ranges[i] = r;
+    };
+    // rounds of ranges that are long beside the longest tile, as they end with one
+    const long long least = max(ROUND_BLOCKS, 2 * top_blocks);
+    const long long rounds = max(1ll, min(min((keys + ROUND_KEYS - 1) / ROUND_KEYS, blocks / (active * least)),
+                                          (long long)(a.range_cap / active)));
+    n_ranges = (int)rounds * active;
+    last0 = n_ranges - active;
+    for (int i = tid; i <= last0; i += THREADS)
+      start_range(i, blocks / n_ranges * i + blocks % n_ranges * i / n_ranges, 0x7fffffff);
+    __syncthreads();
+    // what each cluster lacks to its share of all, and from that its part of the last round
+    long long lacks = 0, total;
+    if (tid < active) {
+      lacks = (blocks + active - 1) / active;
+      for (int i = tid; i < last0; i += active) lacks -= starts[i + 1] - starts[i];
+      lacks = max(0ll, lacks);
     }
+    const long long at = block_scan(lacks, sm, &total), first = starts[last0];
+    if (tid > 0 && tid < active)
+      start_range(last0 + tid, first + (total > 0 ? (blocks - first) * at / total : 0), WHOLE_BLOCKS);
     if (tid == 0) starts[n_ranges] = blocks;
     __syncthreads();
     for (int i = tid; i < n_ranges; i += THREADS)
@@ -254,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   }
   __syncthreads();
   // the tiles that a range's start cuts for the first time
-  for (int i = 1 + tid; i < n_ranges; i += THREADS) {
+  for (int i = last0 + 1 + tid; i < n_ranges; i += THREADS) {
     if (!RF_SPAN_OK(i - 1, 2, a.range_cap)) break;
     const PagedRange r = a.ranges[i], before = a.ranges[i - 1];
     const bool same = before.b == r.b && before.item == r.item;
@@ -272,8 +300,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     x.head = group * s.packed();
     x.kvh = x.head / a.G;
     x.row0 = (tiles - 1 - (r.item - group * tiles)) << a.P_log2;
-    x.slot0 = 2 * (i - 1) + (same ? 0 : 1);
-    x.rho = i;
+    x.slot0 = 2 * (i - 1 - last0) + (same ? 0 : 1);
+    x.rho = i - last0;
     const int at = atomicAdd(&n_joins, 1);
     if (RF_IDX_OK(at, a.range_cap)) a.joins[at] = x;
   }
@@ -286,6 +314,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     if (tid == kPlanUnits) x = n_units;
     if (tid == kPlanRanges) x = n_ranges;
     if (tid == kPlanClusters) x = active;
+    if (tid == kPlanLast) x = last0;
     a.head[tid] = x;
   }
 }
@@ -303,7 +332,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   if (cut > tiles * (steps - 1)) cut = tiles * (steps - 1);
   l->unit_cap = (int)(tiles + cut);
   l->merge_cap = (int)tiles;
-  l->range_cap = 0;
+  l->range_cap = l->slot_cap = 0;
   if (s.some_pairs()) {
     // blocks at most, and the rounds that they make
     const long long groups = (long long)s.Hkv * (s.G() / s.packed());
@@ -313,6 +342,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
     long long rounds = blocks / ((long long)pairs * ROUND_BLOCKS);
     rounds = rounds < 1 ? 1 : rounds > kPagedRounds ? kPagedRounds : rounds;
     l->range_cap = (int)(rounds * pairs < MAX_RANGES ? rounds * pairs : MAX_RANGES);
+    l->slot_cap = 2 * pairs;            // two parts of tiles per range of the last round
   }
   size_t at = align(kPlanWords * sizeof(int));
   const auto take = [&](size_t bytes) {
@@ -330,7 +360,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   l->counters = take((size_t)l->unit_cap * s.Hkv * sizeof(int));
   l->unit_ml = take(rows * sizeof(float2));
   l->unit_acc = take(rows * 128 * sizeof(float));
-  l->slots = take((size_t)2 * l->range_cap * kPagedSlotFloats * sizeof(float));
+  l->slots = take((size_t)l->slot_cap * kPagedSlotFloats * sizeof(float));
   l->bytes = at;
   uint32_t h = 0x9e3779b9u;             // FNV-like mixing of the sizes
   for (const int x : {s.B, s.T, s.H, s.Hkv, s.max_new, s.max_len, s.window, s.sinks, sms})

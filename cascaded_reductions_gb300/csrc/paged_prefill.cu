@@ -66,7 +66,7 @@ __device__ __forceinline__ void place_item(const PagedView& v, bool first, int j
   it.n = min(all - j, it.left);
   it.left -= it.n;
   it.next = j + it.n == all ? 0 : j + it.n;
-  it.slot = it.n == all ? -1 : 2 * it.rho + (first ? 0 : 1);
+  it.slot = it.n == all ? -1 : 2 * (it.rho - v.head[kPlanLast]) + (first ? 0 : 1);
 }
 __device__ __forceinline__ void place_group(const PagedView& v, int group, RangeItem& it) {
   it.group = group;
@@ -264,7 +264,7 @@ struct PagedPrefill {
   __device__ __forceinline__ bool partial(const Item& it) const { return it.slot >= 0; }
   __device__ __forceinline__ void keep(const Item& it, int rank, int r, int col, const uint32_t (&v)[32],
                                        float m, float lt) const {
-    if (!RF_IDX_OK(it.slot, 2 * a.v.range_cap)) return;
+    if (!RF_IDX_OK(it.slot, a.v.slot_cap)) return;
     float* slot = a.v.slots + (size_t)it.slot * kPagedSlotFloats;
     const int row = rank * BM + r;
 #pragma unroll
@@ -469,15 +469,15 @@ template <bool F16>
 __global__ void __launch_bounds__(FIN_WARPS * 32)
 paged_finish_kernel(const __grid_constant__ PagedAttn a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rho = (int)(blockIdx.x / FIN_PARTS), part = (int)(blockIdx.x % FIN_PARTS);
+  const int join = (int)(blockIdx.x / FIN_PARTS), part = (int)(blockIdx.x % FIN_PARTS);
   wait_prerequisite();
   allow_dependents();
   const PagedView& v = a.v;
   const size_t all_rows = (size_t)v.s.T * v.s.H;
   (void)all_rows;                                     // read by the checked build only
   PagedJoin it = {};
-  if (rho < v.range_cap) {                            // asked for before it is known whether it is one
-    const int4* at = reinterpret_cast<const int4*>(v.joins + rho);
+  if (join < v.range_cap) {                           // asked for before it is known whether it is one
+    const int4* at = reinterpret_cast<const int4*>(v.joins + join);
     int4* to = reinterpret_cast<int4*>(&it);
 #pragma unroll
     for (int e = 0; e < 3; ++e) to[e] = at[e];
@@ -497,7 +497,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
       if (r < u.n * v.G - u.tile * kPagedTileRows) merge_row<F16>(a, u, first, hk, r, lane);
     }
   }
-  if (rho < min(v.head[kPlanJoins], v.range_cap)) {
+  if (join < min(v.head[kPlanJoins], v.range_cap)) {
     constexpr int R = FIN_ROWS / FIN_WARPS;           // rows of a warp
     const int row0 = part * FIN_ROWS + warp * R;      // of the tile
     float M[R], L[R];
@@ -510,7 +510,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int slot = x0 + x == 0 ? it.slot0 : 2 * (it.rho + x0 + x - 1);
-        const bool in = x0 + x < it.parts && RF_IDX_OK(slot, 2 * v.range_cap);
+        const bool in = x0 + x < it.parts && RF_IDX_OK(slot, v.slot_cap);
         const float* at = v.slots + (size_t)(in ? slot : 0) * kPagedSlotFloats;
 #pragma unroll
         for (int q = 0; q < R; ++q) {
@@ -549,13 +549,13 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
     }
   }
   if (flag == 0) return;
-  if (rho < ranges) {
+  for (int rho = join; rho < ranges; rho += (int)(gridDim.x / FIN_PARTS)) {
     RangeItem whole;
     first_item(v, rho, whole);
     for (;;) {
       it.b = whole.b, it.start = whole.start, it.rows = whole.rows, it.len = whole.len;
       it.head = whole.head, it.kvh = whole.kvh, it.row0 = whole.row0;
-      for (int q = warp; whole.slot < 0 && q < FIN_ROWS; q += FIN_WARPS) {
+      for (int q = warp; whole.slot < 0 && whole.n > 0 && q < FIN_ROWS; q += FIN_WARPS) {
         const int t = part * FIN_ROWS + q, i = it.row0 + (t & (P - 1)), head = it.head + (t >> v.P_log2);
         const size_t row = (size_t)(it.start + i) * v.s.H + head;
         if (i >= it.rows || !RF_IDX_OK(row, all_rows)) continue;
@@ -638,8 +638,8 @@ rf_status launch_paged_finish(const PagedAttn& a, int dtype, cudaStream_t st) {
   // eight CTAs per tile that may be cut, enough for all rows in pieces up to four CTAs per SM
   const PagedShape& s = a.v.s;
   const long long rows = ((long long)a.v.merge_cap * s.Hkv * s.unit_rows() + FIN_WARPS - 1) / FIN_WARPS;
-  const long long pairs = (long long)a.v.range_cap * FIN_PARTS, most = rows < 4ll * sms ? rows : 4ll * sms;
-  const unsigned grid = (unsigned)(pairs > most ? pairs : most);
+  const long long pairs = (long long)a.v.slot_cap / 2 * FIN_PARTS, most = rows < 4ll * sms ? rows : 4ll * sms;
+  const unsigned grid = (unsigned)((pairs > most ? pairs : most) + FIN_PARTS - 1) / FIN_PARTS * FIN_PARTS;
   return launch_after(dtype == RF_F16 ? paged_finish_kernel<true> : paged_finish_kernel<false>, grid,
                       FIN_WARPS * 32, 0, st, a);
 }

@@ -111,6 +111,24 @@ def test_many_requests():
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+def test_small_call_of_more_units_than_ctas():
+    lens = [200 - b for b in range(60)]
+    x, out, lse = run(lens, [1] * 60, 16, 8, 16, rows=[0], seed=5)
+    again = call(x)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("news", [1, 5, 100])
+def test_window_that_hides_nothing_and_sinks_without_one(news):
+    """The same bits as without: no row is as far from its first key."""
+    x = make([300, 150], [news, news], 8, 2, 32, seed=news)
+    want = call(x)
+    for window, sinks in ((320, 4), (2 ** 31 - 1, 2 ** 31 - 1), (0, 7)):
+        got = call(x, window, sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(x, *call(x, 299, 2 ** 31 - 1), 299, 400, rows=[0, -1])
+
+
 # -------------------------------------------------------------- few and many --
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
