@@ -11,9 +11,9 @@
 //  * the pair kernel's blocks, counted in closed form per request, cut into ranges.
 //    Tiles of one key head read the same keys, so ranges that run at the same time
 //    should lie close together: with more keys than the L2 cache holds, the
-//    blocks are dealt out in rounds (4 x 32 heads of 8192 keys of their own: FIG).  Ranges of
-//    the rounds before the last end with a tile; in the last one every cluster gets what
-//    it lacks to an equal share.
+//    blocks are dealt out in rounds (4 x 32 key heads of 8192 keys, 1705 -> 1605 us).  Ranges
+//    of the rounds before the last end with a tile; each round gives a cluster what it
+//    lacks to an equal share so far.
 
 #include "paged.cuh"
 #include "tc_common.cuh"
@@ -262,19 +262,26 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
                                           (long long)(a.range_cap / active)));
     n_ranges = (int)rounds * active;
     last0 = n_ranges - active;
-    for (int i = tid; i <= last0; i += THREADS)
-      start_range(i, blocks / n_ranges * i + blocks % n_ranges * i / n_ranges, 0x7fffffff);
-    __syncthreads();
-    // what each cluster lacks to its share of all, and from that its part of the last round
-    long long lacks = 0, total;
-    if (tid < active) {
-      lacks = (blocks + active - 1) / active;
-      for (int i = tid; i < last0; i += active) lacks -= starts[i + 1] - starts[i];
-      lacks = max(0ll, lacks);
+    // A round gives a cluster what it lacks to its share of all rounds so far, so that what
+    // one range has too many or too few by its tiles' ends the next one takes back.  The
+    // share of a round is twice the longest tile, so no range lacks all of it.
+    long long given = 0, first = 0, total;
+    for (int k = 0; k < (int)rounds; ++k) {
+      const long long goal = blocks / rounds * (k + 1) + blocks % rounds * (k + 1) / rounds;
+      const long long lacks =
+          tid < active ? max(0ll, goal * (tid + 1) / active - goal * tid / active - given) : 0;
+      const long long at = block_scan(lacks, sm, &total);
+      const bool last = k + 1 == (int)rounds;
+      if (tid > 0 && tid < active)
+        start_range(k * active + tid, first + (total > 0 ? (goal - first) * at / total : 0),
+                    last ? WHOLE_BLOCKS : 0x7fffffff);
+      if (tid == 0 && k == 0) start_range(0, 0, 0);
+      if (tid == active && !last) start_range((k + 1) * active, goal, 0x7fffffff);
+      __syncthreads();
+      if (last) break;
+      if (tid < active) given += starts[k * active + tid + 1] - starts[k * active + tid];
+      first = starts[(k + 1) * active];
     }
-    const long long at = block_scan(lacks, sm, &total), first = starts[last0];
-    if (tid > 0 && tid < active)
-      start_range(last0 + tid, first + (total > 0 ? (blocks - first) * at / total : 0), WHOLE_BLOCKS);
     if (tid == 0) starts[n_ranges] = blocks;
     __syncthreads();
     for (int i = tid; i < n_ranges; i += THREADS)

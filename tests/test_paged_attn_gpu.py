@@ -189,6 +189,32 @@ def test_long_prompts_in_rounds():
 
 # ------------------------------------------------------------------- masks --
 
+@pytest.mark.parametrize("B,L,N,H,Hkv", [(16, 3165, 340, 64, 32), (11, 5276, 1181, 32, 16)])
+def test_equal_prompts_in_rounds(B, L, N, H, Hkv):
+    """Requests that are all the same, over the same pages: tiles of equal length, whose ends all
+    ranges of a cluster miss in the same direction.  Each request against the first, which is against
+    the definition; the plan's memory holds 3e9 before, so that a part which nobody wrote shows (NaN columns are
+    computed again)."""
+    x = make([L], [N], H, Hkv, 64, seed=B)
+    x = dict(x, q=x["q"].repeat(B, 1, 1), table=x["table"].repeat(B, 1), starts=i32(np.arange(B + 1) * N),
+             lens=i32([L] * B))
+    plan = rf.paged_plan(x["starts"], x["lens"], B * N, H, Hkv, N, x["table"].shape[1] * 64)
+    plan.plan.view(torch.uint8).fill_(0x4f)
+    out, lse = call(x, plan=plan)
+    one = dict(x, q=x["q"][:N], table=x["table"][:1], starts=i32([0, N]), lens=i32([L]))
+    check(one, out[:N], lse[:N], rows=[0, 100, 255, -1])
+    q, k = f64(one["q"]), paged.gather(f64(x["kp"]), x["table"][0].cpu().numpy(), L)
+    delta = max(C.score_error(q[:, h], k[h // (H // Hkv)], SCALE) for h in range(H))
+    vmax = float(np.abs(np.nan_to_num(f64(x["vp"]))).max())
+    out, lse = out.view(B, N, H, 128).float(), lse.view(B, N, H)
+    # both are off by their bounds at most, and so is the value that a bound is taken of
+    off = torch.from_numpy(np.float32(1.01 * out_bound(f64(out[0]), delta, vmax, torch.bfloat16, HALF_STEP[torch.bfloat16])))
+    off, off_lse = off.cuda(), delta + 2.0 ** -19 + 2.0 ** -22 * lse[0].abs()
+    for b in range(1, B):
+        assert ((out[b] - out[0]).abs() <= 2 * off).all(), b
+        assert ((lse[b] - lse[0]).abs() <= 2 * off_lse).all(), b
+
+
 @pytest.mark.parametrize("news", [1, 3, 70])
 def test_rows_without_keys_and_empty_requests(news):
     """New tokens that are not in the cache (lens < new) stand at negative positions."""
