@@ -13,11 +13,19 @@
 // before its keys.
 //
 // Work comes from the plan's units (16 rows of a request, a piece of their keys) times
-// key heads, the first of a CTA by its number, the others from a queue.  A fifth warp
-// takes what would hold the stream up: it fetches the next unit, and behind a piece it
-// fences, counts it, and, where it was its tile's last, merges the pieces while the other
-// four are in the next unit.  In a small call, where there is no next unit, those four
-// merge, a row each.
+// key heads.  Two kernels take it:
+//  * paged_few_kernel where the call is small whatever the lengths: a CTA of four warps
+//    per unit, the shortest way from launch to output; the CTA that ends a tile's last
+//    piece merges them (1 request of 1028 keys, 32/8 heads: 7.0 us, by the other kernel
+//    7.9; 16 000 keys 14.3 and 16.9).
+//  * paged_decode_kernel otherwise: one CTA per SM, two teams of four streaming warps, a
+//    unit each, the first by its number, the others from a queue.  A team's fifth warp
+//    fetches the next unit, its page numbers and its query rows meanwhile, so that the
+//    copies run on from unit to unit (64 requests of 4100 keys 160 us, 6.7 TB/s; without
+//    169).  Pieces are left as states: paged_finish_kernel merges them, a warp per row
+//    (17 requests with 4 drafted tokens 75 us; merged by the fifth warps 90).
+// 16 rows of 17 x 5 drafted tokens keep the matrix pipe busier than single tokens do, at
+// 62 % of the memory's rate; 64 requests of up to 16 384 keys run at the plain copy's rate.
 
 #include <stddef.h>
 
