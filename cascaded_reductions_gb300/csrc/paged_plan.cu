@@ -5,15 +5,18 @@
 // the device alone, so a grid of CTAs by the largest sizes would mostly be idle (64
 // requests behind a table of 131072 keys: 87 000 CTAs).  One CTA sums up the work
 // instead and deals it out:
-//  * the streaming kernel's rows, in pieces of equal length that make one wave of two
-//    CTAs per SM where the call is small, and pieces of 768 keys or more, taken from a
-//    queue, where it is large (the rule of the dense cache's decode);
+//  * the streaming kernel's rows, in pieces of equal length: one wave of two CTAs per SM
+//    where the call is small, of 6 to 24 steps of 64 keys, or longer ones, from a queue
+//    where it is large (17 requests with 4 drafted tokens 67 us, 40 requests of 500 to
+//    3930 keys 64; with pieces of 12 steps whatever the lengths 73 and 74);
 //  * the pair kernel's blocks, counted in closed form per request, cut into ranges.
 //    Tiles of one key head read the same keys, so ranges that run at the same time
 //    should lie close together: with more keys than the L2 cache holds, the
 //    blocks are dealt out in rounds (4 x 32 key heads of 8192 keys, 1705 -> 1605 us).  Ranges
 //    of the rounds before the last end with a tile; each round gives a cluster what it
 //    lacks to an equal share so far.
+
+#include <limits.h>
 
 #include "paged.cuh"
 #include "tc_common.cuh"
@@ -22,8 +25,8 @@ namespace rf {
 namespace {
 
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int MANY_STEPS = 12;          // of a large call's piece at least
-constexpr int MANY_UNITS = 8;           // and per CTA at most, on average
+constexpr int MANY_LOW = 6, MANY_HIGH = 24;   // steps of a large call's pieces, as long as
+constexpr int MANY_UNITS = 8;           // they are no more than these per CTA on average
 constexpr int MAX_RANGES = 2048;
 constexpr int WHOLE_BLOCKS = 3;         // of a tile that is never cut
 constexpr int ROUND_BLOCKS = 32;        // of a range at least, where there are several rounds
@@ -57,7 +60,6 @@ __device__ __forceinline__ long long warp_sum(long long x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-
 // exclusive prefix sum over the CTA; *total gets the sum
 __device__ __forceinline__ long long block_scan(long long x, long long* sm, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -83,10 +85,13 @@ __device__ __forceinline__ int steps_of(const PagedShape& s, const PagedSeq& q) 
   const int n = PagedTiles(q.n, q.len, s.window, s.sinks).steps();
   return n > 0 ? n : 1;                 // rows without keys need a CTA all the same
 }
-__device__ __forceinline__ int pieces_of(int steps, int piece) { return (steps + piece - 1) / piece; }
+__device__ __forceinline__ int pieces_of(int steps, int piece) {
+  return (int)(((unsigned)steps + piece - 1) / (unsigned)piece);
+}
 
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   __shared__ long long sm[WARPS], fit[WARPS];
+  __shared__ int lengths[WARPS];
   __shared__ int n_joins, n_merges, top_blocks;
   __shared__ int2 cuts[THREADS];
   __shared__ long long firsts[THREADS], starts[MAX_RANGES + 1];
@@ -121,8 +126,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       blocks += total;
     }
     if (b < s.B && RF_IDX_OK(b, s.B)) a.seqs[b] = q;
-    const long long st = q.n > 0 && !q.pair ? (long long)tiles_of(a, q) * steps_of(s, q) : 0;
-    block_scan(st, sm, &total);
+    int2 rows = make_int2(0, 0);        // 16-row tiles, steps
+    if (q.n > 0 && !q.pair) rows = make_int2(tiles_of(a, q), steps_of(s, q));
+    if (b0 == 0) cuts[tid] = rows;
+    block_scan((long long)rows.x * rows.y, sm, &total);
     steps += total;
     if (a.clusters > 0) {
       block_scan(q.pair ? (long long)s.Hkv * min(q.len, s.window > 0 ? s.window + q.n : q.len) : 0, sm, &total);
@@ -131,30 +138,46 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   }
   __syncthreads();
 
-  // the streaming kernel's pieces: of candidates a 16th apart the smallest that fits one wave
+  // The streaming kernel's pieces, of one candidate length per warp.  A small call takes
+  // the shortest that fits one wave.  A large one takes its pieces from a queue, that of
+  // fewest steps by waves times the longest piece; a step's time for each piece's ends.
   const long long ctas = steps * s.Hkv;
   long long piece = max(1ll, (ctas + a.slots - 1) / a.slots);
   const bool few = piece <= kPagedFewSteps;
-  if (few) {
-    const long long p = piece + (piece * warp + 15) / 16;
-    long long units = 0;
-    for (int b = lane; b < s.B; b += 32) {
-      const PagedSeq q = a.seqs[b];
-      if (q.n > 0 && !q.pair) units += (long long)tiles_of(a, q) * pieces_of(steps_of(s, q), (int)p);
-    }
-    units = warp_sum(units);
-    if (lane == 0) fit[warp] = units * s.Hkv <= a.slots ? p : 0;
-    __syncthreads();
-    long long best = 0;
-    for (int w = WARPS - 1; w >= 0; --w)
-      if (fit[w] > 0) best = fit[w];
-    if (best > 0) piece = best;
-  } else {
+  {
     const long long most = (long long)MANY_UNITS * a.slots;
-    piece = max((long long)MANY_STEPS, (ctas + most - 1) / most);
+    const int low = (int)(few ? piece : max((long long)MANY_LOW, (ctas + most - 1) / most));
+    const int p = low + (few ? (low * warp + 15) / 16 : max(0, MANY_HIGH - low) * warp / (WARPS - 1));
+    long long units = 0;
+    int longest = 0;
+    for (int b = lane; b < s.B; b += 32) {
+      int2 rows = make_int2(0, 0);
+      if (b < THREADS) {
+        rows = cuts[b];
+      } else {
+        const PagedSeq q = a.seqs[b];
+        if (q.n > 0 && !q.pair) rows = make_int2(tiles_of(a, q), steps_of(s, q));
+      }
+      if (rows.x == 0) continue;
+      const int np = pieces_of(rows.y, p);
+      units += (long long)rows.x * np;
+      longest = max(longest, pieces_of(rows.y, np));
+    }
+    units = warp_sum(units) * s.Hkv;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      long long cost = few ? p : (units + a.slots - 1) / a.slots * (longest + 1);
+      if (few && units > a.slots) cost = LLONG_MAX >> 8;
+      fit[warp] = cost << 5 | (WARPS - 1 - warp);     // equal ones: the longer
+      lengths[warp] = p;
+    }
+    __syncthreads();
+    long long best = fit[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+    piece = few && best >> 5 == LLONG_MAX >> 8 ? low : lengths[WARPS - 1 - (int)(best & 31)];
   }
-  // rows of up to two pieces stay whole in a large call, to save the merge
-  auto pieces = [&](int n) { return !few && n <= 2 * MANY_STEPS ? 1 : pieces_of(n, (int)piece); };
+  auto pieces = [&](int n) { return pieces_of(n, (int)piece); };
   if (tid == 0) n_joins = n_merges = 0;
   __syncthreads();
   long long units = 0;
