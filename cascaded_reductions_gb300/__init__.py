@@ -1082,7 +1082,8 @@ def page_tables(lens, news, table, stack, n_free, page, tokens, lens_out=None, n
     lens, news int32 [B]: tokens held and new tokens of each request (new < 0: it has ended and gives
     its pages back); table int32 [B, width] and stack int32 [pages] are updated in place; n_free int32
     [1].  Returns starts [B + 1], positions [tokens], slots [tokens] (-1 where a token has no place),
-    lens_out [B] and n_free_out [1]; the last two may be given, as lens and n_free themselves for one."""
+    lens_out [B] and n_free_out [1]; the last two may be given, as lens and n_free themselves for one.
+    Outputs may lie in one allocation, which lives as long as any of them."""
     if stream is not None:
         return _within(stream, lens, page_tables, lens, news, table, stack, n_free, page, tokens,
                        lens_out, n_free_out)

@@ -145,6 +145,14 @@ at::Tensor like(const at::Tensor& t, at::IntArrayRef sizes, at::ScalarType type)
   return at::empty(sizes, t.options().dtype(type));
 }
 
+// Elements at .. at + n - 1 of a 1-D tensor as one of their own, over the same memory.
+at::Tensor part(const at::Tensor& all, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 template <typename... T>
 PyObject* pack(T&&... t) {
   PyObject* items[] = {THPVariable_Wrap(std::forward<T>(t))...};
@@ -388,9 +396,12 @@ PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !is(*stack, dev, at::kInt, {pages}) || !is(*n_free, dev, at::kInt, {1}) ||
         c10::cuda::current_device() != dev)
       Py_RETURN_NONE;
-    at::Tensor starts = like(*lens, {B + 1}, at::kInt), positions = like(*lens, {tokens}, at::kInt);
-    at::Tensor slots = like(*lens, {tokens}, at::kInt);
-    at::Tensor lens_out = like(*lens, {B}, at::kInt), n_free_out = like(*lens, {1}, at::kInt);
+    // one allocation, each output from 256 bytes on (a call takes the host 5.2 us; of five, 9.4)
+    const auto up = [](int64_t x) { return (x + 63) / 64 * 64; };
+    const int64_t at1 = up(tokens), at2 = at1 + up(tokens), at3 = at2 + up(B + 1), at4 = at3 + up(B);
+    const at::Tensor all = like(*lens, {at4 + 1}, at::kInt);
+    at::Tensor positions = part(all, 0, tokens), slots = part(all, at1, tokens), starts = part(all, at2, B + 1);
+    at::Tensor lens_out = part(all, at3, B), n_free_out = part(all, at4, 1);
     const auto in = [](const at::Tensor& t) { return static_cast<const int32_t*>(t.const_data_ptr()); };
     const auto out = [](const at::Tensor& t) { return static_cast<int32_t*>(t.mutable_data_ptr()); };
     if (PyObject* e = failed([&] {

@@ -105,3 +105,20 @@ def test_captured_steps_in_place():
         assert out[2].tolist() == ref[2].tolist()
         assert d[0].tolist() == list(lens) and d[4].item() == free
         assert np.array_equal(d[2].cpu().numpy(), table)
+
+
+def test_outputs_are_tensors_of_their_own():
+    """They may share memory behind them, but no element, and each can be sliced, viewed and written."""
+    lens, news, stack = i32([3, 0, 17]), i32([2, 1, 0]), i32(list(range(8)))
+    table = i32(np.full((3, 4), -1))
+    table[0, 0], table[2, :2] = 6, i32([5, 7])
+    outs = rf.page_tables(lens, news, table, stack, i32([5]), 16, 5)
+    want = [t.clone() for t in outs]
+    assert [tuple(t.shape) for t in outs] == [(4,), (5,), (5,), (3,), (1,)]
+    for i, t in enumerate(outs):
+        assert t.is_contiguous() and t.dtype == torch.int32 and t.data_ptr() % 16 == 0
+        t.view(-1, 1).fill_(-7)
+        for j, other in enumerate(outs):
+            if j > i:
+                assert torch.equal(other, want[j])
+    assert outs[1][1:3].tolist() == [-7, -7]
