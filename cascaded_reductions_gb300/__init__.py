@@ -11,7 +11,9 @@ The convenience wrappers (``attn_decode``, ``softmax_topk``,
 with torch and call the entry points; so do ``attn_prefill_window``,
 ``attn_decode_window``, ``attn_decode_shared``, ``attn_decode_weights`` and
 ``cache_evict``, which work over a serving cache of grouped heads, with scratch
-from ``decode_workspace`` where a loop keeps it.
+from ``decode_workspace`` where a loop keeps it.  A step over a cache in pages is
+``page_tables`` and ``paged_plan`` once, then per layer ``qk_norm_rope`` (which writes
+the new keys and values into their pages) and ``attn_paged``.
 
 There is no fallback: importing this package fails if librf.so has not been
 built (``cascaded_reductions_gb300._build.build()``).  The environment
