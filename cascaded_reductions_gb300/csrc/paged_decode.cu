@@ -689,7 +689,7 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
     // are those of the first tile of the unit and the next: a tile has landed when all but
     // the last group of copies have, two issues after its own.
     int turn = 0, ahead = 0, calls = 0, call0 = 0, call1 = 0, slot = 0, next = total;
-    bool known = !queued;               // whether next is
+    bool known = true;                  // whether next is; the first unit's query rows come before it
     auto open = [&](int at, int head) {
       in.open(a, tm.unit[at], head, wt);
       in.ids = tm.pages[at][lane * WARPS + wt];
@@ -698,7 +698,9 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
     auto move_on = [&]() {              // the stream into the next unit, if there is one
       if (!known) {
         known = true;
-        if (tc::mbar_wait(&tm.ready, (uint32_t)turn & 1u, &sm_abort)) next = tm.next[turn & 1];
+        const bool there = tc::mbar_wait(&tm.ready, (uint32_t)turn & 1u, &sm_abort);
+        __syncwarp();
+        if (there) next = tm.next[turn & 1];
       }
       if (ahead == 0 && next < total) {
         ahead = 1;
@@ -728,7 +730,10 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
       }
       State<F16> st;
       st.start(a, Work(a, u, hk), lane);
-      if (turn == 0) named_sync<TEAM>(bars + kBarEnd);   // the first unit's query rows are in place
+      if (turn == 0) {                  // the first unit's query rows are in place
+        named_sync<TEAM>(bars + kBarEnd);
+        known = !queued;
+      }
       st.load_rows(sq, lane);
       if (queued) named_arrive<TEAM>(bars + kBarRows);
       for (int t = t0 + wt; t < t1; t += WARPS) {

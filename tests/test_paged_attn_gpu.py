@@ -118,6 +118,18 @@ def test_small_call_of_more_units_than_ctas():
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("top,news", [(16, 1), (40, 1), (70, 3), (300, 2)])
+def test_many_short_requests_where_long_ones_may_come(top, news):
+    """A large call by its sizes (a queue of units) of units with fewer keys than are kept in flight."""
+    lens = [max(news, 1 + (37 * b) % top) for b in range(90)]
+    x = make(lens, [news] * 90, 16, 8, 16, seed=top)
+    out, lse = call(x, max_len=x["table"].shape[1] * 16)
+    x["table"] = torch.cat([x["table"], torch.full((90, 512), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    for _ in range(2):
+        out, lse = call(x)
+        check(x, out, lse, rows=[0, -1])
+
+
 @pytest.mark.parametrize("news", [1, 5, 100])
 def test_window_that_hides_nothing_and_sinks_without_one(news):
     """The same bits as without: no row is as far from its first key."""
