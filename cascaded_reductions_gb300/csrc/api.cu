@@ -40,7 +40,10 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 rf::PagedShape paged_shape(int B, int T, int H, int Hkv, int max_new, int max_len, int window, int sinks) {
   if (window >= max_len) window = 0;
   if (window == 0 && sinks > 0) sinks = 0;
-  return {B, T, H, Hkv, max_new, max_len, window, sinks > max_len && max_len > 0 ? max_len : sinks};
+  rf::PagedShape s = {B, T, H, Hkv, max_new, max_len, window, sinks > max_len && max_len > 0 ? max_len : sinks,
+                      rf::kPagedRows, 0};
+  if (B > 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && max_new > 0 && max_len > 0) s.divide(rf::tc::sm_count());
+  return s;
 }
 
 rf_status check_paged(const rf::PagedShape& s) {
@@ -586,7 +589,7 @@ rf_status rf_attn_paged(const void* q, const void* kp, const void* vp, int pages
     if (st != RF_OK) return st;
   }
   st = rf::launch_paged_decode(a, dtype, as_stream(stream));
-  if (st != RF_OK || s.few(rf::tc::sm_count())) return st;
+  if (st != RF_OK || s.few) return st;
   return rf::launch_paged_finish(a, dtype, as_stream(stream));
 }
 

@@ -1,9 +1,9 @@
 // What the kernels of attention over a paged cache share: the plan of a step, and
 // which blocks of keys a tile of query rows visits.
 //
-// Requests with up to kPagedRows query rows per key head (new tokens times the heads
-// that share it) run on the streaming kernel (paged_decode.cu), 16 rows at a time; the
-// others on CTA pairs (paged_prefill.cu), 256 rows at a time.  Both take their work
+// Requests of few query rows per key head (new tokens times the heads that share it;
+// PagedShape::limit) run on the streaming kernel (paged_decode.cu), 16 rows at a time;
+// the others on CTA pairs (paged_prefill.cu), 256 rows at a time.  Both take their work
 // from lists that paged_plan.cu makes once per step from the lengths on the device:
 //   units    of the streaming kernel: 16 rows and a piece of their keys;
 //   ranges   of the pair kernel: all 256-key blocks of all tiles, one after the other,
@@ -15,7 +15,8 @@
 
 namespace rf {
 
-constexpr int kPagedRows = 64;          // query rows per key head of the streaming kernel
+constexpr int kPagedRows = 64;          // query rows per key head of the streaming kernel at most
+constexpr int kPagedManyRows = 32;      // and in a large call, for each tile of the pair kernel
 constexpr int kPagedTileRows = 16;
 constexpr int kPagedBlock = 256;        // keys of the pair kernel's blocks
 constexpr int kPagedPairRows = 256;
@@ -27,6 +28,7 @@ constexpr int kPagedFewSteps = 16;      // steps of 64 keys per CTA of a small c
 // The sizes that a plan and the calls over it share.
 struct PagedShape {
   int B, T, H, Hkv, max_new, max_len, window, sinks;
+  int limit, few;                       // set by divide()
   __host__ __device__ int G() const { return H / Hkv; }
   // query heads of a tile, and positions of it
   __host__ __device__ int packed() const {
@@ -38,17 +40,25 @@ struct PagedShape {
     const int p = packed();
     return p == 8 ? 5 : p == 4 ? 6 : p == 2 ? 7 : 8;
   }
-  __host__ __device__ bool some_pairs() const { return (long long)max_new * G() > kPagedRows; }
-  // of the streaming kernel: 16-row tiles per request at most, rows of one
+  // Which kernels a call takes, by its sizes alone.  It is small (few) if its requests are
+  // all of up to kPagedRows rows and the streaming kernel's units make about one wave, whatever
+  // the lengths: that kernel alone then, a CTA per unit, in one launch.  A large call's
+  // requests go to the pair kernel where that reads the keys less than half as often: 16 rows
+  // a time here, there packed() heads and any of so few positions (24 requests of 8000 keys,
+  // 32/8 heads, 40 rows: 155 us instead of 270; 32 rows: 155 instead of 192, but 29 instead
+  // of 15 us where the requests are short).
+  __host__ __device__ void divide(int sms) {
+    limit = kPagedRows;
+    const long long units = (long long)B * tiles() * Hkv;
+    const long long steps = units * (((long long)max_len + 4 * kDecodeTile - 1) / (4 * kDecodeTile));
+    few = !some_pairs() && steps <= kPagedFewSteps * 2ll * sms;
+    if (!few && kPagedManyRows * (G() / packed()) < kPagedRows) limit = kPagedManyRows * (G() / packed());
+  }
+  __host__ __device__ bool some_pairs() const { return (long long)max_new * G() > limit; }
+  // of the streaming kernel: 16-row tiles per request at most
   __host__ __device__ int tiles() const {
     const long long rows = (long long)max_new * G();
-    return (int)((rows < kPagedRows ? rows : kPagedRows) + kPagedTileRows - 1) / kPagedTileRows;
-  }
-  // whether the streaming kernel's call is small whatever the lengths: one launch, a CTA
-  // per unit; else the teams' kernel, and paged_finish_kernel
-  __host__ __device__ bool few(int sms) const {
-    const long long steps = (long long)B * tiles() * Hkv * ((max_len + 4 * kDecodeTile - 1) / (4 * kDecodeTile));
-    return !some_pairs() && steps <= kPagedFewSteps * 2ll * sms;
+    return (int)((rows < limit ? rows : limit) + kPagedTileRows - 1) / kPagedTileRows;
   }
   __host__ __device__ int unit_rows() const {
     const long long rows = (long long)max_new * G();

@@ -839,7 +839,7 @@ rf_status launch_t(const PagedAttn& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const int sms = tc::sm_count();
   if (sms <= 0) return RF_ERR_CUDA;
-  if (a.v.s.few(sms)) return launch_few<F16>(a, sms, st);
+  if (a.v.s.few) return launch_few<F16>(a, sms, st);
   auto* kernel = paged_decode_kernel<F16>;
   // launched with fewer registers than the warpgroups' shares add up to, the streaming
   // warps would wait for them for ever

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       q.start = first;
       q.n = min(last - first, s.max_new);
       q.len = min(max(a.lens[b], 0), s.max_len);
-      q.pair = (long long)q.n * a.G > kPagedRows;
+      q.pair = (long long)q.n * a.G > s.limit;
     }
     long long mine = 0, total;
     if (q.pair) {
@@ -393,7 +393,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   l->slots = take((size_t)l->slot_cap * kPagedSlotFloats * sizeof(float));
   l->bytes = at;
   uint32_t h = 0x9e3779b9u;             // FNV-like mixing of the sizes
-  for (const int x : {s.B, s.T, s.H, s.Hkv, s.max_new, s.max_len, s.window, s.sinks, sms})
+  for (const int x : {s.B, s.T, s.H, s.Hkv, s.max_new, s.max_len, s.window, s.sinks, s.limit, sms})
     h = (h ^ (uint32_t)x) * 0x01000193u + 0x7f4a7c15u;
   l->mark = h;
   return true;

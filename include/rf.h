@@ -562,7 +562,8 @@ rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long l
  * window or sinks < 0, or too few bytes; RF_ERR_UNSUPPORTED for max_len > 2^30, T * H
  * beyond 2^31 - 1, B > 2^20, H > 2^16, more than 2^29 tiles of 16 rows, or a device that
  * cannot hold a cluster of two CTAs with about 200 KiB of shared memory each (where
- * max_new * H / Hkv > 64); RF_ERR_MISALIGNED for the plan.
+ * requests of that many rows may run on the tensor-bound kernel, see rf_attn_paged);
+ * RF_ERR_MISALIGNED for the plan.
  */
 size_t rf_paged_plan_bytes(int B, int T, int H, int Hkv, int max_new, int max_len, int window, int sinks);
 rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T, int H, int Hkv,
@@ -582,10 +583,13 @@ rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T
  *               starts[B], or between a start and the rows before it) are left as they were
  * Rows of a page behind a request's end are never read; a page number outside the cache
  * reads as keys and values of zero.  A key or value that is not finite reaches only the rows
- * that see it.  Requests with up to 64 rows per key head (new tokens * H / Hkv) run as
- * rf_attn_decode_window does (weights not rounded to 16 bits), so a row's last bits
- * may depend on how many tokens come with it.  One launch for a small batch of
- * single or few tokens, two for a larger one, three where max_new * H / Hkv > 64.
+ * that see it.  With G = H / Hkv, requests of few rows per key head (new tokens * G) run as
+ * rf_attn_decode_window does (weights not rounded to 16 bits), the others on the tensor-bound
+ * kernel of rf_attn_prefill_window (weights rounded once), so a row's last bits may depend on
+ * how many tokens come with it.  Few are up to 64 where the call is small by its sizes: max_new *
+ * G <= 64 and B * Hkv * ceil(max_new * G / 16) * ceil(max_len / 64) at most 32 per SM; else up
+ * to the smaller of 64 and 32 * G / g, g the largest of 8, 4, 2 and 1 that divides G.  One launch
+ * for a small call, two for a large one, three where a request may have more rows than few.
  * Errors: as rf_paged_plan, RF_ERR_INVALID_ARG for width * page < max_len, a non-finite scale
  * or a bad dtype; RF_ERR_UNSUPPORTED for D != 128, RF_F32, scale <= 0, a page that is not 16,
  * 32, 64, 128 or 256, pages * Hkv >= 2^30 or B * width >= 2^31; RF_ERR_MISALIGNED unless q, kp,

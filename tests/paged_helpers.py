@@ -41,3 +41,13 @@ def paged_cache(lens, Hkv, page, seed, dtype=torch.bfloat16, D=128, width=None, 
                 x[table[b, i], :, :m] = rows[:, i * page:i * page + m]
         pages.append(x)
     return pages[0], pages[1], table
+
+
+def few_rows(B, H, Hkv, max_new, max_len, sms=None):
+    """Rows per key head (new tokens * H / Hkv) up to which a request of a call of these sizes has its
+    weights in two 16-bit terms, as the header file documents it."""
+    sms = sms or torch.cuda.get_device_properties(0).multi_processor_count
+    G = H // Hkv
+    if max_new * G <= 64 and B * Hkv * -(-max_new * G // 16) * -(-max_len // 64) <= 32 * sms:
+        return 64
+    return min(64, 32 * G // max(g for g in (8, 4, 2, 1) if G % g == 0))

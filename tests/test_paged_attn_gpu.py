@@ -1,8 +1,8 @@
 """Attention over a paged cache against the definition in float64, row by row.
 
 Bounds as for the calls over a dense cache: the score's fp32 rounding, the weights' rounding for the
-second product (requests of up to 64 rows per key head: two 16-bit terms, 2^-16; larger ones: half a
-step of the 16-bit type) and one rounding of the output.  Rows of the pages that no request uses hold
+second product (requests of few rows per key head: two 16-bit terms, 2^-16; larger ones, where each
+weight is rounded once to the 16-bit type: half a step of it) and one rounding of the output.  Rows of the pages that no request uses hold
 NaN."""
 
 import numpy as np
@@ -14,7 +14,7 @@ from cache_helpers import DT, HALF_STEP, assert_within, normal, out_bound
 from helpers import f64
 from oracle import cache as C
 from oracle import paged
-from paged_helpers import i32, paged_cache
+from paged_helpers import few_rows, i32, paged_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -31,9 +31,10 @@ def make(lens, news, H, Hkv, page, dtype=torch.bfloat16, seed=0, gain=1.0, extra
 def call(x, window=0, sinks=0, scale=SCALE, max_new=None, max_len=None, plan=None):
     kp, st = x["kp"], x["starts"].tolist()
     news = [b - a for a, b in zip(st, st[1:])]
-    plan = rf.paged_plan(x["starts"], x["lens"], x["q"].shape[0], x["q"].shape[1], kp.shape[1],
-                         max_new or max(max(news), 1), max_len or x["table"].shape[1] * kp.shape[2], window, sinks,
-                         plan=plan)
+    max_new, max_len = max_new or max(max(news), 1), max_len or x["table"].shape[1] * kp.shape[2]
+    x["few"] = few_rows(len(news), x["q"].shape[1], kp.shape[1], max_new, max_len)
+    plan = rf.paged_plan(x["starts"], x["lens"], x["q"].shape[0], x["q"].shape[1], kp.shape[1], max_new, max_len,
+                         window, sinks, plan=plan)
     out, lse = rf.attn_paged(x["q"], kp, x["vp"], x["table"], plan, scale=scale)
     torch.cuda.synchronize()
     assert rf.rf_device_error() == 0
@@ -51,7 +52,7 @@ def check(x, out, lse, window=0, sinks=0, scale=SCALE, rows=None, finite=True):
             continue
         k, v = paged.gather(kp, table[b], L), paged.gather(vp, table[b], L)
         fk, fv = (np.nan_to_num(t, posinf=0, neginf=0) for t in (k, v))
-        p_step = 2.0 ** -16 if N * G <= 64 else HALF_STEP[out.dtype]
+        p_step = 2.0 ** -16 if N * G <= x["few"] else HALF_STEP[out.dtype]
         vmax = float(np.abs(fv).max()) if L else 0.0
         mine = range(N) if rows is None else sorted({r % N for r in rows})
         for h in range(H):
@@ -142,6 +143,15 @@ def test_window_that_hides_nothing_and_sinks_without_one(news):
 
 
 # -------------------------------------------------------------- few and many --
+
+@pytest.mark.parametrize("H,Hkv,news", [(32, 8, 8), (32, 8, 9), (16, 16, 33), (12, 4, 11), (12, 4, 22), (64, 2, 2)])
+def test_rows_on_either_side_of_few_in_a_large_call(H, Hkv, news):
+    """Requests of 32 to 96 rows per key head, one to four times what one reading of the keys serves."""
+    lens = [2000, 700, 1300, news, 64, 900, 1111, 257, 300, 800, 1500, 600, 999, 1024]
+    x, out, lse = run(lens, [news] * 14, H, Hkv, 64, rows=[0, -1], seed=news)
+    assert x["few"] < 64 or news * H // Hkv > 64 or H == 64 or H == 12
+    assert torch.equal(out, call(x)[0])
+
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("H,Hkv,news", [(4, 1, 2), (8, 2, 4), (8, 8, 9), (5, 1, 7), (64, 4, 3), (4, 1, 16), (7, 7, 64)])
@@ -309,6 +319,7 @@ def test_dominant_key():
 
 def test_rows_of_no_request_are_left():
     x = make([50, 200, 70], [1, 100, 2], 8, 2, 16, extra=9, seed=6)
+    x["few"] = few_rows(len(x["lens"]), 8, 2, 100, 208)
     plan = rf.paged_plan(x["starts"], x["lens"], x["q"].shape[0], 8, 2, 100, 208)
     out, lse = torch.full_like(x["q"], 7.0), torch.full((112, 8), 7.0, device="cuda")
     rf.rf_attn_paged(x["q"], x["kp"], x["vp"], x["table"], plan.plan, 100, 208, 0, 0, SCALE, out, lse)
@@ -343,7 +354,7 @@ def test_sizes_above_the_lengths_and_lengths_above_them():
 
 def test_on_another_stream():
     x = make([3000, 700], [130, 1], 8, 2, 64, seed=8)
-    want = call(x)
+    want = call(dict(x))
     s = torch.cuda.Stream()
     for _ in range(5):
         y = {k: torch.zeros_like(v) for k, v in x.items()}
@@ -368,6 +379,7 @@ def test_captured_and_replayed_with_other_lengths():
         with torch.cuda.graph(g, stream=s):
             plan = rf.paged_plan(x["starts"], x["lens"], 270, 8, 2, 90, 320)
             out, lse = rf.attn_paged(x["q"], x["kp"], x["vp"], x["table"], plan)
+    x["few"] = few_rows(3, 8, 2, 90, 320)
     for lens, starts in (([300, 300, 300], [0, 90, 180, 270]), ([1, 77, 256], [0, 1, 1, 30]), ([300, 16, 9], [0, 80, 90, 99])):
         x["lens"].copy_(i32(lens))
         x["starts"].copy_(i32(starts))

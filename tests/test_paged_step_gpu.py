@@ -12,7 +12,7 @@ import cascaded_reductions_gb300 as rf
 from cache_helpers import assert_within, normal
 from helpers import f64
 from oracle import paged
-from paged_helpers import i32
+from paged_helpers import few_rows, i32
 from test_paged_attn_gpu import check as check_attn
 from test_qk_norm_rope_gpu import bound as rope_bound
 
@@ -91,7 +91,8 @@ def check(s, history, starts, outs, news):
             assert_within(paged.gather(kp, table[b], L).transpose(1, 0, 2), ref,
                           rope_bound(ref, size, torch.bfloat16), f"keys of request {b}")
             assert np.array_equal(paged.gather(vp, table[b], L).transpose(1, 0, 2), raw[:, 1])
-        x = dict(q=q, kp=s.kp[layer], vp=s.vp[layer], table=s.table, starts=starts, lens=s.lens)
+        x = dict(q=q, kp=s.kp[layer], vp=s.vp[layer], table=s.table, starts=starts, lens=s.lens,
+                 few=few_rows(len(lens), H, HKV, s.max_new, WIDTH * PAGE))
         check_attn(x, out, lse, s.window, s.sinks, rows=[0, 1, 40, 63, 64, -2, -1])
 
 
