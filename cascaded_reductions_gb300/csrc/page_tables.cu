@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
     __syncthreads();
   }
   const int given = (int)(moved >> 32), needed = (int)(moved & 0xffffffffll);
-  const int top = min(nfree + given, a.P);
+  const int top = (int)min((long long)nfree + given, (long long)a.P);
   // requests whose pages are not all there get nothing; of those that get theirs the
   // last one's pages end the ones taken
   for (int b = tid; b < B; b += (int)blockDim.x) {
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
   else
     __syncthreads();
   const int took = took_all;
-  const int first = (int)blockIdx.x * (int)blockDim.x + tid, step = (int)(ctas * blockDim.x);
+  // counts reach the largest int, past which a step may go: unsigned
+  const unsigned first = blockIdx.x * blockDim.x + threadIdx.x, step = ctas * blockDim.x;
   const size_t entries = (size_t)B * a.width;
   (void)entries;                             // read by the checked build only
 
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
   };
   auto held_of = [&](int len) { return min((int)(((long long)len + a.page - 1) / a.page), held_most); };
 
-  for (int b = first; b < B; b += step) {
+  for (int b = (int)first; b < B; b += (int)step) {
     const int len = len0[b] < 0 ? -1 - len0[b] : len0[b];
     const int end = b + 1 < B ? start[b + 1] : (int)min(tokens, 0x7fffffffll);
     // an ended request gives pages where it has some; it has none of the tokens either way
@@ -173,15 +174,15 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
       a.n_free_out[0] = top - took;
     }
   }
-  for (int y = first; y < given && nfree + y < a.P; y += step)
-    if (RF_IDX_OK(nfree + y, a.P)) a.stack[nfree + y] = given_page(y);
-  for (int x = first; x < took; x += step) {
-    const int b = find(need0, B, x);
+  for (unsigned y = first; y < (unsigned)given && y < (unsigned)(a.P - nfree); y += step)
+    if (RF_IDX_OK(nfree + y, a.P)) a.stack[nfree + y] = given_page((int)y);
+  for (unsigned i = first; i < (unsigned)took; i += step) {
+    const int x = (int)i, b = find(need0, B, x);
     const size_t at = (size_t)b * a.width + held_of(len0[b]) + (x - need0[b]);
     if (RF_IDX_OK(at, entries)) a.table[at] = page_of(x);
   }
   if (a.firsts) {
-    for (int b = first; b < B; b += step) {
+    for (int b = (int)first; b < B; b += (int)step) {
       const int t = start[b], end = b + 1 < B ? start[b + 1] : (int)min(tokens, 0x7fffffffll);
       if (t == end || t >= a.T || !RF_IDX_OK(t, a.T)) continue;
       const int len = len0[b], pos = len < 0 ? -1 - len : len;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(1024) page_tables_kernel(const Tables a) {
     return;
   }
   // four tokens per thread, in 16-byte stores
-  for (int t0 = 4 * first; t0 < a.T; t0 += 4 * step) {
+  for (int t0 = 4 * (int)first; t0 < a.T; t0 += 4 * (int)step) {   // below MANY_TOKENS
     int pos[4], slot[4];
     int b = t0 < tokens ? find(start, B, t0) : 0;
     int seen = -1, entry = -1;
@@ -247,16 +248,17 @@ __global__ void __launch_bounds__(256) page_slots_kernel(const Tables a) {
   allow_dependents();
   for (int b = threadIdx.x; b <= a.B; b += 256) start[b] = RF_IDX_OK(b, a.B + 1) ? a.starts[b] : 0;
   __syncthreads();
-  const int tokens = start[a.B];
-  for (int t0 = 4 * (blockIdx.x * 256 + threadIdx.x); t0 < a.T; t0 += 4 * 256 * (int)gridDim.x) {
-    int b = t0 < tokens ? find(start, a.B, t0) : 0, of = -1, first_pos = 0, seen = -1, entry = 0;
+  const unsigned tokens = (unsigned)start[a.B], T = (unsigned)a.T;
+  // unsigned: T reaches the largest int, past which a step may go
+  for (unsigned t0 = 4 * (blockIdx.x * 256 + threadIdx.x); t0 < T; t0 += 4 * 256 * gridDim.x) {
+    int b = t0 < tokens ? find(start, a.B, (int)t0) : 0, of = -1, first_pos = 0, seen = -1, entry = 0;
     bool fits = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int t = t0 + e;
-      if (t >= a.T || !RF_IDX_OK(t, a.T)) break;
+      if (t0 + e >= T || !RF_IDX_OK(t0 + e, a.T)) break;
+      const int t = (int)(t0 + e);
       int pos = 0, slot = -1;
-      if (t < tokens) {
+      if (t0 + e < tokens) {
         while (start[b + 1] <= t) ++b;
         if (start[b] == t) continue;
         if (of != b) {

@@ -122,3 +122,38 @@ def test_outputs_are_tensors_of_their_own():
             if j > i:
                 assert torch.equal(other, want[j])
     assert outs[1][1:3].tolist() == [-7, -7]
+
+
+def filled(n, x=7):
+    return torch.full((n,), x, dtype=torch.int32, device="cuda")
+
+
+def test_as_many_rows_as_an_int_counts():
+    """T = 2^31 - 1, near which a thread's next row passes the largest int."""
+    lens, news, page, width, free, T = [0, 33], [20000, 5], 16, 1260, 1260, 2 ** 31 - 1
+    table, stack, _ = tables(2, page, [0, 3], width, free, 4)
+    total = sum(news)
+    ref = paged.page_tables(lens, news, table, stack, free, page, total)
+    positions, slots = filled(T), filled(T)
+    starts, lens_out, n_free_out, dev_table = filled(3), filled(2), filled(1), i32(table)
+    rf.rf_page_tables(i32(lens), i32(news), dev_table, i32(stack), i32([free]), page, starts, positions, slots, lens_out,
+                      n_free_out)
+    for got, want in zip((starts, positions[:total], slots[:total], lens_out, n_free_out[0], dev_table), ref):
+        assert np.array_equal(got.cpu().numpy(), want)
+    for at in range(total, T, 1 << 28):
+        assert (positions[at:at + (1 << 28)] == 0).all() and (slots[at:at + (1 << 28)] == -1).all(), at
+
+
+def test_as_many_pages_as_an_int_counts():
+    """A stack of 2^31 - 1 pages, whose top the pages given back reach and are taken from."""
+    P, given, taken = 2 ** 31 - 1, 20000, 9000
+    table = filled(2 * given).view(2, given)
+    table[0] = torch.arange(given, dtype=torch.int32, device="cuda") + 5
+    stack = filled(P, -3)
+    starts, positions, slots, lens_out, n_free_out = rf.page_tables(
+        i32([given, 0]), i32([-1, taken]), table, stack, i32([P - given]), 1, taken)
+    assert n_free_out.item() == P - taken and lens_out.tolist() == [0, taken]
+    assert torch.equal(stack[P - given:], table[0])
+    assert torch.equal(table[1, :taken], table[0].flip(0)[:taken]) and (table[1, taken:] == 7).all()
+    assert torch.equal(slots, table[1, :taken]) and torch.equal(positions, torch.arange(taken, device="cuda").int())
+    assert (stack[:P - given][-(1 << 20):] == -3).all() and (stack[:1 << 20] == -3).all()
