@@ -33,7 +33,16 @@ rf_status check_segments(int B, int H, int Hkv, int S, int dtype, int out_dtype)
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   if (!a || !b) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
+  return x < y ? y - x < na : x - y < nb;
+}
+// The same with `rows` rows of nb bytes, `step` bytes from one to the next: what lies
+// between them is no part of them.
+bool overlap_rows(const void* a, size_t na, const void* b, size_t rows, size_t nb, size_t step) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (x < y) return y - x < na;
+  const uintptr_t d = x - y, i = d < nb ? 0 : (d - nb) / step + 1;   // the first row that ends behind x
+  return i < rows && (i * step <= d || i * step - d < na);
 }
 
 // The sizes of a step over a paged cache.  A window that no request outgrows hides nothing.
@@ -525,6 +534,26 @@ rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long l
       !rf::aligned16(k_out) || !rf::aligned16(v_out) || q_step % 8 != 0 || k_step % 8 != 0 ||
       (v && v_step % 8 != 0))
     return RF_ERR_MISALIGNED;
+  // q_out may be q and k_out k, row for row; nothing else may overlap
+  const size_t rows = (size_t)T, q_row = (size_t)H * D * 2, k_row = (size_t)Hkv * D * 2;
+  const size_t kv = slots ? (size_t)pages * page * k_row : rows * k_row, w = weight_dtype == RF_F32 ? 4 : 2;
+  const struct { const void* p; size_t n; } out[] = {{q_out, rows * q_row}, {k_out, kv}, {v_out, kv}};
+  const struct { const void* p; size_t row, step; } tokens[] = {
+      {q, q_row, (size_t)q_step * 2}, {k, k_row, (size_t)k_step * 2}, {v, k_row, (size_t)v_step * 2}};
+  const struct { const void* p; size_t n; } in[] = {
+      {q_weight, D * w}, {k_weight, D * w}, {positions, (size_t)axes * T * 4}, {freq, (size_t)R * 2},
+      {axis, (size_t)R * 2}, {slots, rows * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      const auto& t = tokens[j];
+      const bool in_place = i == j && out[i].p == t.p && (i == 0 || slots == nullptr) && (T == 1 || t.step == t.row);
+      if (!in_place && overlap_rows(out[i].p, out[i].n, t.p, rows, t.row, t.step)) return RF_ERR_INVALID_ARG;
+    }
+    for (const auto& x : in)
+      if (overlap(out[i].p, out[i].n, x.p, x.n)) return RF_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return RF_ERR_INVALID_ARG;
+  }
   return rf::launch_qk_norm_rope(q, q_step, k, k_step, v, v_step, T, H, Hkv, D, q_weight, k_weight,
                                  weight_dtype == RF_F32, eps, positions, axes, freq, axis, R,
                                  interleaved != 0, dtype, slots, pages, page, q_out, k_out, v_out,

@@ -526,13 +526,15 @@ rf_status rf_page_tables(const int32_t* lens, const int32_t* news, int B, int32_
  *   positions   [axes, T]; axis [R / 2] names the axis of each pair (NULL: the first;
  *               numbers outside are taken as the nearer one)
  *   freq        [R / 2] fp32, finite, radians per position
- *   q_out       [T, H, D] out; may be q itself where q_step = H * D
- *   slots NULL: k_out [T, Hkv, D] out (or k itself), v and v_out NULL
+ *   q_out       [T, H, D] out; may be q itself where q_step = H * D or T = 1
+ *   slots NULL: k_out [T, Hkv, D] out, v and v_out NULL; may be k itself where
+ *               k_step = Hkv * D or T = 1
  *   slots [T]:  k_out, v_out [pages, Hkv, page, D], the cache; a token with a slot
  *               outside 0 .. pages * page - 1 is not written.  No slot may occur twice.
+ * No other buffer overlaps an output (what lies between the rows of q, k and v may).
  * Errors: RF_ERR_INVALID_ARG for null pointers (but those named), v or v_out without
- * slots or the reverse, sizes <= 0, R > D, a bad dtype, a negative or non-finite eps, or
- * steps shorter than a row; RF_ERR_UNSUPPORTED for RF_F32, D not 64, 128 or 256, R % 16
+ * slots or the reverse, sizes <= 0, R > D, a bad dtype, a negative or non-finite eps,
+ * steps shorter than a row, or overlapping buffers; RF_ERR_UNSUPPORTED for RF_F32, D not 64, 128 or 256, R % 16
  * != 0, or sizes beyond 2^31 (T * (H + 2 Hkv) / 8, pages * page); RF_ERR_MISALIGNED unless
  * q, k, v and outputs are 16-byte aligned and steps multiples of 8.
  */

@@ -86,6 +86,31 @@ def test_norm_rope_refusals(lib):
     assert f(*rope_args(pages=1 << 27)) == 2
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would be launched")
+def test_norm_rope_refuses_overlapping_buffers(lib):
+    """Outputs over rows that other warps have still to read, over the small inputs, over one another."""
+    f = lib.rf_qk_norm_rope
+    pages = dict(q_out=5 * 2048, k_out=160 * 512, v_out=160 * 512)        # bytes of each output
+    for out in pages:
+        for name in ("q", "k", "v", "positions", "freq", "slots", "qw"):
+            assert f(*rope_args(**{name: at(20), out: at(20)})) == 1 or (out, name) == ("q_out", "q"), (out, name)
+            assert f(*rope_args(**{name: at(20, pages[out] - 16), out: at(20)})) == 1, (out, name)
+    assert f(*rope_args(q_out=at(7))) == 1                      # on k_out
+    assert f(*rope_args(v_out=at(7, 160 * 512 - 16))) == 1
+    assert f(*rope_args(v_out=at(7, 160 * 512))) == 4           # side by side: no device here, but not refused
+    # without a cache; in place only where the rows lie one behind the other
+    dense = dict(slots=NULL, v=NULL, v_out=NULL)
+    assert f(*rope_args(**dense, q_out=at(0), q_step=1032)) == 1
+    assert f(*rope_args(**dense, k_out=at(1), k_step=264)) == 1
+    assert f(*rope_args(**dense, k_out=at(1, 16))) == 1
+    assert f(*rope_args(**dense, q_out=at(0, 2048))) == 1       # a token on
+    assert f(*rope_args(**dense, k_out=at(0), q_step=1280)) == 1
+    # q, k and v beside one another in rows of 1536 values, an output over the last row's end
+    assert f(*rope_args(**dense, k=at(0, 2048), q_step=1536, k_step=1536, k_out=at(0, 4 * 3072 + 2048 + 496))) == 1
+    # the cache is not k's place
+    assert f(*rope_args(k_out=at(1))) == 1
+
+
 def test_python_layer_refuses_cpu_tensors_and_bad_shapes():
     import cascaded_reductions_gb300 as rf
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)                                   # noqa: E731

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import cascaded_reductions_gb300 as rf
-from cache_helpers import DT, HALF_STEP, assert_within
+from cache_helpers import DT, HALF_STEP, assert_within, normal
 from helpers import f64
 from oracle import paged
 from paged_helpers import i32
@@ -153,3 +153,26 @@ def test_far_rows():
     a = rf.qk_norm_rope(q, k, pos, freqs(64))
     b = rf.qk_norm_rope(q.contiguous(), k.contiguous(), pos, freqs(64))
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_in_place_of_one_token_and_outputs_between_the_rows():
+    """What the check of overlapping buffers lets through."""
+    q, k, _, qw, kw = inputs(1, 4, 2, 128, torch.bfloat16, 16)          # steps of a longer row, T = 1
+    pos = i32([[77]])
+    want = rf.qk_norm_rope(q, k, pos, freqs(128), qw, kw)
+    q, k = q.clone(), k.clone()
+    rf.rf_qk_norm_rope(q, k, None, qw, kw, 1e-6, pos, freqs(128), None, False, None, q, k, None)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    # two tokens 64 KiB apart, both outputs in the gap
+    wide = torch.zeros(2, 32768, dtype=torch.bfloat16, device="cuda")
+    rows = normal(17, 2, 6, 128).cuda()
+    wide[:, :768] = rows.view(2, 768)
+    q, k = wide[:, :512].view(2, 4, 128), wide[:, 512:768].view(2, 2, 128)
+    q_out, k_out = wide[0, 4096:5120].view(2, 4, 128), wide[0, 768:1280].view(2, 2, 128)
+    pos = i32([[5, 6]])
+    want = rf.qk_norm_rope(q, k, pos, freqs(128), qw, kw)
+    rf.rf_qk_norm_rope(q, k, None, qw, kw, 1e-6, pos, freqs(128), None, False, None, q_out, k_out, None)
+    assert torch.equal(q_out, want[0]) and torch.equal(k_out, want[1])
+    with pytest.raises(rf.RFError):                                     # half a row over the second token's key
+        rf.rf_qk_norm_rope(q, k, None, qw, kw, 1e-6, pos, freqs(128), None, False, None, q_out,
+                           wide.view(-1)[32768 + 704:32768 + 1216].view(2, 2, 128), None)
