@@ -82,6 +82,7 @@ _SIGNATURES = {
     "rf_page_tables": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
     "rf_paged_plan_bytes": (ctypes.c_size_t, [_I] * 8),
     "rf_paged_plan": (_I, [_P, _P] + [_I] * 8 + [_P, ctypes.c_size_t, _P]),
+    "rf_paged_plan_slots": (_I, [_P, _P, _P] + [_I] * 8 + [_P, ctypes.c_size_t, _P]),
     "rf_attn_paged": (_I, [_P, _P, _P, _I, _I, _P, _I, _P, ctypes.c_size_t] + [_I] * 9
                       + [_F, _I, _P, _P, _P]),
     "rf_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _I, _F, _P, _I, _P, _P,
@@ -739,6 +740,21 @@ def rf_paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window, sinks, plan
              *_c_ints(B, T, H, Hkv, max_new, max_len, window, sinks), plan.data_ptr(), plan.shape[0])
 
 
+def rf_paged_plan_slots(starts, lens, slots, T, H, Hkv, max_new, max_len, window, sinks, plan, stream=None):
+    """rf_paged_plan with the rows' slots, int32 [T]: a request whose first one is negative has no keys."""
+    dev = _device_of(lens, "lens")
+    if lens.dim() != 1 or plan.dim() != 1:
+        raise ValueError("lens must be [B] and plan [bytes]")
+    B = lens.shape[0]
+    _on(dev, lens, torch.int32, (B,), "lens")
+    _on(dev, starts, torch.int32, (B + 1,), "starts")
+    _on(dev, slots, torch.int32, (T,), "slots")
+    _on(dev, plan, torch.uint8, plan.shape, "plan")
+    _call_on(dev, stream, "rf_paged_plan_slots", _lib.rf_paged_plan_slots, starts.data_ptr(), lens.data_ptr(),
+             slots.data_ptr(), *_c_ints(B, T, H, Hkv, max_new, max_len, window, sinks), plan.data_ptr(),
+             plan.shape[0])
+
+
 def rf_attn_paged(q, kp, vp, table, plan, max_new, max_len, window, sinks, scale, out, lse=None,
                   stream=None):
     """q/out [T, H, D], kp/vp [pages, Hkv, page, D] (bf16 or fp16, D = 128), table int32 [B, width],
@@ -1085,6 +1101,8 @@ def page_tables(lens, news, table, stack, n_free, page, tokens, lens_out=None, n
     its pages back); table int32 [B, width] and stack int32 [pages] are updated in place; n_free int32
     [1].  Returns starts [B + 1], positions [tokens], slots [tokens] (-1 where a token has no place),
     lens_out [B] and n_free_out [1]; the last two may be given, as lens and n_free themselves for one.
+    A request whose pages are not all there gets none: its length stays, its slots are -1 (paged_plan
+    takes the slots, so that its rows attend to nothing).
     Outputs may lie in one allocation, which lives as long as any of them."""
     if stream is not None:
         return _within(stream, lens, page_tables, lens, news, table, stack, n_free, page, tokens,
@@ -1139,15 +1157,17 @@ class PagedPlan(typing.NamedTuple):
     sinks: int
 
 
-def paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window=0, sinks=0, plan=None, stream=None):
+def paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window=0, sinks=0, plan=None, stream=None, slots=None):
     """The plan of a step over a paged cache, made on the device from its lengths.
 
     starts int32 [B + 1], lens int32 [B] (as page_tables gives them), T rows of q, max_new and max_len:
     the most new tokens and keys of a request.  ``plan``: an earlier one of the same sizes, whose memory
-    is used again."""
+    is used again.  ``slots`` int32 [T] (as page_tables gives them): where the stack of free pages may run
+    out, so that requests without pages get out = 0 and lse = -inf; without them their rows would see
+    their last keys as if they were the new ones."""
     if stream is not None:
         return _within(stream, lens, paged_plan, starts, lens, T, H, Hkv, max_new, max_len, window, sinks,
-                       plan)
+                       plan, slots=slots)
     dev = _device_of(lens, "lens")
     sizes = (dev, lens.shape[0], T, H, Hkv)
     if plan is None:
@@ -1158,7 +1178,10 @@ def paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window=0, sinks=0, pla
     elif plan[1:] != (sizes, max_new, max_len, window, sinks):
         raise ValueError(f"plan was made for (device, B, T, H, Hkv), max_new, max_len, window, sinks = "
                          f"{plan[1:]}, the call has {(sizes, max_new, max_len, window, sinks)}")
-    rf_paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window, sinks, plan.plan)
+    if slots is None:
+        rf_paged_plan(starts, lens, T, H, Hkv, max_new, max_len, window, sinks, plan.plan)
+    else:
+        rf_paged_plan_slots(starts, lens, slots, T, H, Hkv, max_new, max_len, window, sinks, plan.plan)
     return plan
 
 

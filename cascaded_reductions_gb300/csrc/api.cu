@@ -67,6 +67,18 @@ rf_status check_paged(const rf::PagedShape& s) {
   return RF_OK;
 }
 
+rf_status make_plan(const int32_t* starts, const int32_t* lens, const int32_t* slots, const rf::PagedShape& s,
+                    void* plan, size_t bytes, void* stream) {
+  if (!starts || !lens || !plan) return RF_ERR_INVALID_ARG;
+  const rf_status st = check_paged(s);
+  if (st != RF_OK) return st;
+  if (reinterpret_cast<uintptr_t>(plan) % 256 != 0) return RF_ERR_MISALIGNED;
+  rf::PagedLayout l;
+  if (!rf::paged_layout(s, &l)) return RF_ERR_CUDA;
+  if (bytes < l.bytes) return RF_ERR_INVALID_ARG;
+  return rf::launch_paged_plan(starts, lens, slots, s, plan, as_stream(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -569,15 +581,16 @@ size_t rf_paged_plan_bytes(int B, int T, int H, int Hkv, int max_new, int max_le
 rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T, int H, int Hkv,
                         int max_new, int max_len, int window, int sinks, void* plan, size_t bytes,
                         void* stream) {
-  if (!starts || !lens || !plan) return RF_ERR_INVALID_ARG;
-  const rf::PagedShape s = paged_shape(B, T, H, Hkv, max_new, max_len, window, sinks);
-  const rf_status st = check_paged(s);
-  if (st != RF_OK) return st;
-  if (reinterpret_cast<uintptr_t>(plan) % 256 != 0) return RF_ERR_MISALIGNED;
-  rf::PagedLayout l;
-  if (!rf::paged_layout(s, &l)) return RF_ERR_CUDA;
-  if (bytes < l.bytes) return RF_ERR_INVALID_ARG;
-  return rf::launch_paged_plan(starts, lens, s, plan, as_stream(stream));
+  return make_plan(starts, lens, nullptr, paged_shape(B, T, H, Hkv, max_new, max_len, window, sinks), plan, bytes,
+                   stream);
+}
+
+rf_status rf_paged_plan_slots(const int32_t* starts, const int32_t* lens, const int32_t* slots, int B, int T,
+                              int H, int Hkv, int max_new, int max_len, int window, int sinks, void* plan,
+                              size_t bytes, void* stream) {
+  if (!slots) return RF_ERR_INVALID_ARG;
+  return make_plan(starts, lens, slots, paged_shape(B, T, H, Hkv, max_new, max_len, window, sinks), plan, bytes,
+                   stream);
 }
 
 rf_status rf_attn_paged(const void* q, const void* kp, const void* vp, int pages, int page,

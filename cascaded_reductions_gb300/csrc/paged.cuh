@@ -244,8 +244,9 @@ struct PagedAttn {
   float* lse;                           // [T, H] or null
 };
 
-rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const PagedShape& s, void* plan,
-                            cudaStream_t st);
+// slots: of the new tokens, or null where every request has its place
+rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const int32_t* slots, const PagedShape& s,
+                            void* plan, cudaStream_t st);
 rf_status launch_paged_decode(const PagedAttn& a, int dtype, cudaStream_t st);
 rf_status launch_paged_prefill(const PagedAttn& a, int dtype, cudaStream_t st);
 rf_status launch_paged_finish(const PagedAttn& a, int dtype, cudaStream_t st);

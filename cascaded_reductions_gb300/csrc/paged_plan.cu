@@ -34,7 +34,7 @@ constexpr long long ROUND_KEYS = 98304; // keys of all key heads (512 bytes each
 
 struct Plan {
   PagedShape s;
-  const int32_t *starts, *lens;
+  const int32_t *starts, *lens, *places;   // places: the rows' slots, null where every request has its own
   int* head;
   PagedSeq* seqs;
   long long* before;                    // [B + 1]: pair blocks of the requests before
@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       q.start = first;
       q.n = min(last - first, s.max_new);
       q.len = min(max(a.lens[b], 0), s.max_len);
+      // a request that got no pages has its old length: none of its keys is for these rows
+      if (a.places != nullptr && q.n > 0 && RF_IDX_OK(first, s.T) && a.places[first] < 0) q.len = 0;
       q.pair = (long long)q.n * a.G > s.limit;
     }
     long long mine = 0, total;
@@ -399,15 +401,15 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   return true;
 }
 
-rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const PagedShape& s, void* plan,
-                            cudaStream_t st) {
+rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const int32_t* slots, const PagedShape& s,
+                            void* plan, cudaStream_t st) {
   PagedLayout l;
   const int sms = tc::sm_count();
   if (sms <= 0 || !paged_layout(s, &l)) return RF_ERR_CUDA;
   uint8_t* p = static_cast<uint8_t*>(plan);
   Plan a = {};
   a.s = s;
-  a.starts = starts, a.lens = lens;
+  a.starts = starts, a.lens = lens, a.places = slots;
   a.head = reinterpret_cast<int*>(p);
   a.seqs = reinterpret_cast<PagedSeq*>(p + l.seqs);
   a.before = reinterpret_cast<long long*>(p + l.before);

@@ -502,7 +502,9 @@ rf_status rf_cache_evict(const void* k, const void* v, const float* weight, cons
  *   n_free_out [1] out     may be n_free itself
  * Where the stack runs out, the first request whose new pages are not all there and
  * all behind it that need pages get none, and so does a request that would need more
- * than `width`: their tokens keep their rows with slot -1, their length and table stay.
+ * than `width`: their tokens keep their rows with slot -1, their length and table stay (a
+ * step where that may happen plans with rf_paged_plan_slots; the tokens can come again in
+ * a later step).
  * No other buffers overlap.  One launch, two from 16384 tokens on.
  * Errors: RF_ERR_INVALID_ARG for null pointers, sizes <= 0 or overlapping buffers;
  * RF_ERR_UNSUPPORTED for B > 8192, or B * width, pages * page or width * page beyond
@@ -559,7 +561,13 @@ rf_status rf_qk_norm_rope(const void* q, long long q_step, const void* k, long l
  *            long (0: the sizes are not valid or there is no device).  It holds the
  *            call's scratch too: calls that may overlap on the GPU need plans of their
  *            own, and a plan is made again only when the calls over it are done.
- * The lengths are read here alone; what the calls do goes by the plan.
+ * The lengths are read here alone; what the calls do goes by the plan.  Every request's new
+ * tokens have to be among its keys: one that rf_page_tables gave no pages keeps its old
+ * length, and its rows would see its last keys as if they were the new ones.
+ *
+ * rf_paged_plan_slots -- the same where requests may have got no pages.  slots [T] are the
+ * rows' as rf_page_tables writes them; a request whose first row's is negative has no keys
+ * in this plan, so that its rows get out = 0 and lse = -inf.
  * Errors: RF_ERR_INVALID_ARG for null pointers, sizes <= 0, H % Hkv != 0, max_new > T,
  * window or sinks < 0, or too few bytes; RF_ERR_UNSUPPORTED for max_len > 2^30, T * H
  * beyond 2^31 - 1, B > 2^20, H > 2^16, more than 2^29 tiles of 16 rows, or a device that
@@ -571,6 +579,9 @@ size_t rf_paged_plan_bytes(int B, int T, int H, int Hkv, int max_new, int max_le
 rf_status rf_paged_plan(const int32_t* starts, const int32_t* lens, int B, int T, int H, int Hkv,
                         int max_new, int max_len, int window, int sinks, void* plan, size_t bytes,
                         void* stream);
+rf_status rf_paged_plan_slots(const int32_t* starts, const int32_t* lens, const int32_t* slots, int B, int T,
+                              int H, int Hkv, int max_new, int max_len, int window, int sinks, void* plan,
+                              size_t bytes, void* stream);
 
 /*
  * rf_attn_paged -- attention of the new tokens of a batch of requests over their pages:

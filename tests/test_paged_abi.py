@@ -167,6 +167,21 @@ def test_plan_refusals(lib):
         assert lib.rf_paged_plan_bytes(*bad) == 0
 
 
+def test_plan_with_slots_refusals(lib):
+    """As the plan without: the slots stand behind the lengths."""
+    def f(slots=at(9), **o):
+        a = plan_args(**o)
+        return lib.rf_paged_plan_slots(*a[:2], slots, *a[2:])
+    assert f(slots=NULL) == 1
+    for name in ("starts", "lens", "plan"):
+        assert f(**{name: NULL}) == 1, name
+    for name in ("B", "T", "H", "Hkv", "max_new", "max_len"):
+        assert f(**{name: 0}) == 1, name
+    assert f(window=-1) == 1 and f(sinks=-1) == 1 and f(max_new=101) == 1
+    assert f(max_len=(1 << 30) + 1) == 2
+    assert f(plan=at(4, 128)) == 3
+
+
 def test_attn_refusals(lib):
     f = lib.rf_attn_paged
     for name in ("q", "kp", "vp", "table", "out"):

@@ -386,3 +386,40 @@ def test_captured_and_replayed_with_other_lengths():
         g.replay()
         torch.cuda.synchronize()
         check(x, out, lse, rows=[0, 5, 33, -1])
+
+
+# --------------------------------------------------------- requests without pages --
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 3)])
+@pytest.mark.parametrize("B,news,keys", [(5, 1, 64), (5, 3, 64), (90, 2, 9000), (5, 70, 64), (5, 300, 64)])
+def test_requests_without_pages(B, news, keys, window, sinks):
+    """Small calls, a queue of units, the pair kernel: rows of a request whose first slot is negative get
+    0 and -inf, those beside it what they get without it."""
+    lens = [news + (37 * b) % 400 for b in range(B)]
+    x = make(lens, [news] * B, 8, 2, 16, seed=news + B)
+    width = max(x["table"].shape[1], keys // 16)
+    x["table"] = torch.nn.functional.pad(x["table"], (0, width - x["table"].shape[1]), value=-1)
+    T = B * news
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    refused = [0, 2, B - 1]
+    for b in refused:
+        slots[b * news:(b + 1) * news] = -1
+    want = call(x, window, sinks)
+    plan = rf.paged_plan(x["starts"], x["lens"], T, 8, 2, news, width * 16, window, sinks, slots=slots)
+    out, lse = rf.attn_paged(x["q"], x["kp"], x["vp"], x["table"], plan)
+    off = torch.zeros(B, dtype=torch.bool, device="cuda")
+    off[refused] = True
+    off = off.repeat_interleave(news)
+    assert (out[off] == 0).all() and torch.isneginf(lse[off]).all()
+    x["lens"] = torch.where(torch.isin(torch.arange(B, device="cuda"), torch.tensor(refused, device="cuda")), 0, x["lens"])
+    check(x, out, lse, window, sinks, rows=[0, -1])
+    # the same plan's memory again, for a step in which all have their places
+    rf.paged_plan(x["starts"], i32(lens), T, 8, 2, news, width * 16, window, sinks, plan=plan, slots=torch.arange(
+        T, dtype=torch.int32, device="cuda"))
+    out, lse = rf.attn_paged(x["q"], x["kp"], x["vp"], x["table"], plan)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_slots_of_another_size_are_refused():
+    with pytest.raises(ValueError):
+        rf.paged_plan(i32([0, 4]), i32([9]), 4, 8, 2, 4, 16, slots=i32([1, 2, 3]))

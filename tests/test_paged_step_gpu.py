@@ -234,3 +234,57 @@ def test_pages_whose_offsets_pass_32_bits():
     rf.qk_norm_rope(q, k, i32([[0] * 7]), FREQ.cuda(), v=k, slots=slots, kp=kp, vp=vp)
     assert torch.equal(vp[-1, :, -7:].transpose(0, 1).flip(0), k) and torch.equal(kp[-1, :, -7:], vp[-1, :, -7:])
     torch.cuda.empty_cache()
+
+
+class Tight(Server):
+    """A loop whose pool may run out: its plan takes the slots."""
+
+    def step(self):
+        starts, pos, slots, _, _ = rf.page_tables(self.lens, self.news, self.table, self.stack, self.n_free, PAGE,
+                                                  self.tokens, lens_out=self.lens, n_free_out=self.n_free)
+        self.plan = rf.paged_plan(starts, self.lens, self.tokens, H, HKV, self.max_new, WIDTH * PAGE, self.window,
+                                  self.sinks, plan=self.plan, slots=slots)
+        outs = []
+        for layer in range(LAYERS):
+            q, k, v = self.rows[layer].split([H * D, HKV * D, HKV * D], 1)
+            q = rf.qk_norm_rope(q.view(-1, H, D), k.view(-1, HKV, D), pos[None], self.freq, *self.weights,
+                                v=v.view(-1, HKV, D), slots=slots, kp=self.kp[layer], vp=self.vp[layer])
+            outs.append((q, *rf.attn_paged(q, self.kp[layer], self.vp[layer], self.table, self.plan)))
+        return starts, pos, slots, outs
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3)])
+def test_steps_without_enough_pages(window, sinks):
+    """Twelve pages: chunks and single tokens that get none, and come again once a request has ended."""
+    s = Tight(4, 12, 240, 200, window, sinks, seed=5)
+    history = [torch.zeros(LAYERS, 0, 2 * HKV * D, dtype=torch.bfloat16)] * 4
+    script = [([100, 5, 30, 1], []), ([70, 1, 40, 1], [0, 2]), ([0, 1, 40, 14], [2]), ([-1, 1, 40, 70], []),
+              ([200, 1, 9, 1], [0]), ([0, 190, 0, 1], [1]), ([0, 7, 1, 1], []), ([1, -1, 0, 1], [])]
+    for step, (news, refused) in enumerate(script):
+        old = list(history)
+        feed(s, history, news, 200 + step)
+        for b in refused:
+            history[b] = old[b]
+        starts, _, slots, outs = s.step()
+        at, lens = starts.tolist(), [h.shape[1] for h in history]
+        assert s.lens.tolist() == lens
+        for b, n in enumerate(news):
+            assert ((slots[at[b]:at[b + 1]] < 0) == (b in refused)).all(), (step, b)
+        # the oracle's request without pages has no keys
+        seen = i32([0 if b in refused else n for b, n in enumerate(lens)])
+        table, kw, freq = s.table.cpu().numpy(), f64(s.weights[1]), f64(s.freq)
+        for layer, (q, out, lse) in enumerate(outs):
+            for b, L in enumerate(lens):
+                if L == 0:
+                    continue
+                raw = f64(history[b][layer]).reshape(L, 2, HKV, D)
+                ref, size = paged.norm_rope(raw[:, 0], kw, 1e-6, np.arange(L)[None], freq)
+                assert_within(paged.gather(f64(s.kp[layer]), table[b], L).transpose(1, 0, 2), ref,
+                              rope_bound(ref, size, torch.bfloat16), f"step {step}: keys of request {b}")
+                assert np.array_equal(paged.gather(f64(s.vp[layer]), table[b], L).transpose(1, 0, 2), raw[:, 1])
+            x = dict(q=q, kp=s.kp[layer], vp=s.vp[layer], table=s.table, starts=starts, lens=seen,
+                     few=few_rows(4, H, HKV, s.max_new, WIDTH * PAGE))
+            check_attn(x, out, lse, window, sinks, rows=[0, 1, 40, 63, -2, -1])
+            for b in refused:
+                assert (out[at[b]:at[b + 1]] == 0).all() and torch.isneginf(lse[at[b]:at[b + 1]]).all()
+    assert rf.rf_device_error() == 0
