@@ -67,8 +67,11 @@
 //   F16                        operands are fp16 (else bf16)
 //   M_START                    a row's reference before its first block: -inf
 //                              where the first block always holds a visible
-//                              key, else a finite value below every score, for
+//                              key, else a finite value below every score (LOWEST,
+//                              or where huge ones are computed again -1e30), for
 //                              which a block without visible keys gives p = 0
+//   ROUNDS                     scores of any size: those of a block with huge ones are
+//                              rounded in log2 units before the reference is taken off
 //   CHAINED                    the kernel is set up beside the end of the one before
 //                              it on the stream, and lets the next one begin so
 //   Item, Pending              a work item; what its output still needs
@@ -124,6 +127,19 @@ constexpr float RESCALE_THRESHOLD = 8.0f;    // log2 units
 constexpr float P_SHIFT = 7.0f;              // log2 of the factor that an fp16 p is taken with,
 constexpr float P_SHIFT_LIMIT = 1048576.0f;  // for references up to 2^20: there m - 7 is off by at most
                                              // 2^-4, while from 2^24 on it may be m - 8 or less, and p 2^16
+
+// Whether a row's weights may have passed what their type holds.  A weight is exp2(s c - m)
+// with one rounding, but m is s c rounded: what that left out, up to 2^-25 m, is in all of a
+// row's exponents.  It cancels in out and lse, but from 2^31 on (fp16: 2^27) the
+// weights, which may already be 2^8, get too large or too small.  Rounding s c before m is
+// taken off for such blocks (ROUNDS) costs the prefix's states 0.4 %, but the prefills 4 to
+// 13 % of every call (windowed, 4 x 32 heads of 8192 rows, 491 -> 537 us; causal 386 -> 402):
+// the windowed and the paged one compute such rows again, the causal one ends there.
+constexpr float LOWEST = -3.402823466e38f;   // a reference below every score
+template <bool F16>
+__device__ __forceinline__ bool huge(float m) {
+  return fabsf(m) >= (F16 ? 134217728.f : 2147483648.f) && fabsf(m) < -LOWEST;
+}
 
 struct Shared {
   uint64_t q_full[2];           // CTA 0: both Q tiles of a buffer
@@ -401,11 +417,19 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
         uint32_t w[NW > 0 ? 16 * NW : 1];
         if constexpr (NW > 0) {
           const uint64_t nm2 = pack_f32x2(-m_new, -m_new);
-          uint64_t sum2 = 0ull;
+          uint64_t sum2 = 0ull, by2 = sl2;
+          if constexpr (P::ROUNDS) {
+            if (__any_sync(0xffffffffu, huge<P::F16>(mt))) {
+#pragma unroll
+              for (int c = 0; c < 16 * NW; ++c)
+                unpack_f32x2(mul_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), sl2), s[2 * c], s[2 * c + 1]);
+              by2 = pack_f32x2(1.f, 1.f);
+            }
+          }
 #pragma unroll
           for (int c = 0; c < 16 * NW; ++c) {
             float a0, a1;
-            unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), sl2, nm2), a0, a1);
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), by2, nm2), a0, a1);
             const float p0 = ex2(a0), p1 = ex2(a1);
             sum2 = add_f32x2(sum2, pack_f32x2(p0, p1));
             w[c] = pack_16x2<P::F16>(p0, p1);

@@ -33,6 +33,7 @@
 // Values that are not finite: as in the windowed prefill a weight of 0 times NaN reaches
 // rows that do not see the value.  Rows whose output is not finite are noted, and
 // paged_finish_kernel computes their NaN columns again from the visible keys alone.
+// Rows of huge scores (pair::huge) are written as NaN and computed again in the same way.
 
 #include <cuda_fp16.h>
 
@@ -46,6 +47,7 @@ using pair::BM;
 using pair::BN;
 using pair::HALF_BYTES;
 using pair::HD;
+using pair::huge;
 static_assert(2 * BM == kPagedPairRows && BN == kPagedBlock && HD == 128, "the plan's sizes");
 
 // The items of a range, one after the other: tiles, or what of a tile the range holds.
@@ -121,8 +123,8 @@ __device__ __forceinline__ void step_item(const PagedView& v, RangeItem& it) {
 template <bool F16_>
 struct PagedPrefill {
   static constexpr bool F16 = F16_;
-  static constexpr bool CHAINED = true, STAGED = true;
-  static constexpr float M_START = -1e30f;
+  static constexpr bool CHAINED = true, STAGED = true, ROUNDS = false;
+  static constexpr float M_START = pair::LOWEST;
   using Item = RangeItem;
   struct Pages {
     int kkey, vkey;               // first keys of the lane's copies
@@ -290,7 +292,8 @@ struct PagedPrefill {
   __device__ __forceinline__ bool boxed(const Pending& pend) const { return pend.full; }
   __device__ __forceinline__ bool pack(const Pending& pend, int col, const uint32_t (&v)[32], float m, float lt,
                                        uint32_t (&w)[16]) const {
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;       // 0: a row that sees nothing
+    // 0: a row that sees nothing
+    const float inv = huge<F16>(m) ? NAN : lt == 0.f ? 0.f : 1.f / lt;
     const uint64_t inv2 = pair::pack_f32x2(inv, inv);
     uint64_t probe = 0ull;                              // NaN if a value is not finite
 #pragma unroll
@@ -304,7 +307,9 @@ struct PagedPrefill {
     }
     const size_t row = (size_t)pend.row * a.v.s.H + pend.head;
     if (pend.in && RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) {
-      if (a.lse != nullptr && col == 0) a.lse[row] = (m + log2f(lt)) * kLn2;
+      // -inf too where the sum says nothing: the row has NaN columns then, and gets its lse with them
+      if (a.lse != nullptr && col == 0)
+        a.lse[row] = lt > 0.f && lt < INFINITY ? (m + log2f(lt)) * kLn2 : -INFINITY;
       if (!pend.full) pair::st_row32(a.out + (row * HD + col) * 2, w, false);
     }
     float p0, p1;
@@ -346,11 +351,11 @@ __device__ __forceinline__ float4 widen4(const uint8_t* row, int lane) {
 }
 
 // Columns of a row that are NaN (bits of `todo`, four per lane), once more from the keys
-// that the row sees.  Ends once they are all NaN again.  Gives the row's sum and maximum too
-// (in log2 units), where it went through all of its keys.
+// that the row sees.  Ends once they are all NaN again; with `whole` only if the sum is NaN too, so
+// that *lse2 gets the row's sum and maximum (in log2 units).
 template <bool F16>
 __device__ __noinline__ float4 redo_row(const PagedAttn& a, const PagedJoin it, int i, int head, uint32_t todo,
-                                        float4 y, float* lse2, int lane) {
+                                        bool whole, float4 y, float* lse2, int lane) {
   constexpr int U = 8;                                // keys in flight
   const int p = it.len - it.rows + i, window = a.v.s.window, page = 1 << a.page_log2;
   const int last = min(p, it.len - 1);
@@ -401,10 +406,10 @@ __device__ __noinline__ float4 redo_row(const PagedAttn& a, const PagedJoin it, 
       R.w = fmaf(w, v[u].w, R.w);
     }
     const uint32_t now = (R.x != R.x) | (R.y != R.y) << 1 | (R.z != R.z) << 2 | (R.w != R.w) << 3;
-    gone = !__any_sync(0xffffffffu, (todo & ~now) != 0);
+    gone = !__any_sync(0xffffffffu, (todo & ~now) != 0 || (whole && l == l));
   }
+  if (whole) *lse2 = m + log2f(l);
   if (gone) return y;
-  *lse2 = m + log2f(l);
   const float inv = l == 0.f ? 0.f : 1.f / l;         // 0: every visible score is -inf
   if (l == 0.f) R = make_float4(0.f, 0.f, 0.f, 0.f);
   return make_float4(todo & 1u ? R.x * inv : y.x, todo & 2u ? R.y * inv : y.y, todo & 4u ? R.z * inv : y.z,
@@ -511,6 +516,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
     const int row0 = part * FIN_ROWS + warp * R;      // of the tile
     float M[R], L[R];
     float4 A[R];
+    uint32_t again = 0;                               // a bit per row of huge scores
 #pragma unroll
     for (int q = 0; q < R; ++q) M[q] = -INFINITY, L[q] = 0.f, A[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x0 = 0; x0 < it.parts; x0 += 2) {        // two parts in flight
@@ -532,6 +538,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int q = 0; q < R; ++q) {
+          if (x0 + x < it.parts && huge<F16>(m[x][q])) again |= 1u << q;
           if (l[x][q] == 0.f) continue;               // the part holds nothing that the row sees
           const float top = fmaxf(M[q], m[x][q]), c = exp2f(M[q] - top), f = exp2f(m[x][q] - top);
           M[q] = top;
@@ -550,8 +557,11 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
       const float inv = L[q] == 0.f ? 0.f : 1.f / L[q];
       float4 y = make_float4(A[q].x * inv, A[q].y * inv, A[q].z * inv, A[q].w * inv);
       float lse2 = M[q] + log2f(L[q]);
-      const uint32_t todo = nan_of(y);
-      if (__any_sync(0xffffffffu, todo != 0)) y = redo_row<F16>(a, it, i, head, todo, y, &lse2, lane);
+      const uint32_t todo = again >> q & 1u ? 15u : nan_of(y);
+      if (__any_sync(0xffffffffu, todo != 0)) {
+        const bool whole = (again >> q & 1u) != 0 || !(L[q] > 0.f && L[q] < INFINITY);
+        y = redo_row<F16>(a, it, i, head, todo, whole, y, &lse2, lane);
+      }
       *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
           make_uint2(pair::pack_16x2<F16>(y.x, y.y), pair::pack_16x2<F16>(y.z, y.w));
       if (lane == 0 && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
@@ -571,13 +581,13 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
         const float4 y = widen4<F16>(a.out + row * HD * 2, lane);
         const uint32_t todo = nan_of(y);
         if (!__any_sync(0xffffffffu, todo != 0)) continue;
+        // masked scores never entered the lse in place; -inf where the sum said nothing
         float lse2 = NAN;
-        const float4 z = redo_row<F16>(a, it, i, head, todo, y, &lse2, lane);
+        const bool whole = a.lse != nullptr && a.lse[row] == -INFINITY;
+        const float4 z = redo_row<F16>(a, it, i, head, todo, whole, y, &lse2, lane);
         *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
             make_uint2(pair::pack_16x2<F16>(z.x, z.y), pair::pack_16x2<F16>(z.z, z.w));
-        // masked scores never entered the lse in place, but weights that all vanished
-        // against the reference that the row started from left it at -inf
-        if (lane == 0 && a.lse != nullptr && a.lse[row] == -INFINITY && lse2 == lse2) a.lse[row] = lse2 * kLn2;
+        if (lane == 0 && whole) a.lse[row] = lse2 * kLn2;
       }
       if (whole.left == 0) break;
       step_item(v, whole);

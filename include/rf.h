@@ -174,7 +174,8 @@ rf_status rf_mla_decode_split(const void* q, const void* c, int B, int H, int L,
  *
  *   q, k, v   [B, H, N, D]  bf16        D = 128
  *   causal    1: query i sees keys 0..i (top-left aligned); 0: all keys
- *   scale     score scale (1/sqrt(D))
+ *   scale     score scale (1/sqrt(D)).  Scores (q . k * scale * log2 e) lie below 2^31 in
+ *             magnitude; a row that has one beyond may come out as NaN or 0
  *   out       [B, H, N, D]  bf16 out
  *   lse       [B, H, N]     fp32 out (m + ln l, natural log), may be NULL
  * Any N >= 1: the last query and key tiles of a head are partial (keys past
