@@ -22,7 +22,16 @@ constexpr int kDecodeTile = 16;        // keys of one tile of the decode kernels
 //    dependents, whatever ran before it on the stream;
 //  * a kernel ends only after its prerequisite has (at least one CTA waits);
 //  * what an earlier kernel may have written is not read through the read-only path,
-//    which may load ahead of the wait.
+//    which may load ahead of the wait;
+//  * a call's later kernel may read what was there before the call's first one without
+//    a wait of its own (a decode beside the pair kernel that it follows: with the wait a
+//    mixed batch takes 327 us instead of 315).  It begins after every CTA of the kernel
+//    before it has waited and said so, when those writes have been performed; but it is a
+//    wait that makes them visible past a kernel's own caches.  So paged_decode reads them
+//    by L2 alone (__ldcg, cp.async.cg), at no cost.  cache_decode behind a prefix does so
+//    with keys and values only: lengths and queries, 4 bytes at a time, it reads through
+//    L1, and relies on L1 to hold no line from before its kernel began (by L2 alone a
+//    step of 128 sequences takes 64.7 us instead of 64.2, of 38 sequences 19.4 and 18.4).
 // Back to back, a single-token decode takes 6.0 us so and 8.2 us when its kernel is
 // set up only after the one before has ended.
 __device__ __forceinline__ void allow_dependents() {

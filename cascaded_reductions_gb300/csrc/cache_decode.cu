@@ -522,7 +522,9 @@ cache_decode_kernel(const CacheDecode a) {
   __shared__ int last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = (int)(blockIdx.x / a.S), piece = (int)(blockIdx.x - (unsigned)g * a.S);
-  if (a.seg0 == 0) wait_prerequisite();   // the prefix kernel has done so for its successor
+  // behind the prefix kernel, which has waited, what was there before is read without a wait
+  // (see launch_after for what that relies on)
+  if (a.seg0 == 0) wait_prerequisite();
   allow_dependents();
   const Group q = group_of<POSITIONS>(a, g);
   const int pieces = pieces_of(a, q.n);

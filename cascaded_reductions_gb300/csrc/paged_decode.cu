@@ -93,7 +93,7 @@ struct Work {
 __device__ __forceinline__ int page_of(const PagedAttn& a, int b, int tile) {
   const int i = tile * TK >> a.page_log2;
   const size_t at = (size_t)b * a.width + i;
-  return i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width) ? a.table[at] : -1;
+  return i < a.width && RF_IDX_OK(at, (size_t)a.v.s.B * a.width) ? __ldcg(a.table + at) : -1;
 }
 // cache rows in front of the tile's keys, where the page is one
 __device__ __forceinline__ size_t row_of(const PagedAttn& a, int page, int hk, int tile) {
@@ -629,14 +629,14 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
   const int Hkv = a.v.s.Hkv;
   if (threadIdx.x < TEAMS) tc::mbar_init(&teams[threadIdx.x].ready, 1);
   if (threadIdx.x == 0) sm_abort = 0;
-  // behind the pair kernel of the same call, which has waited for what was before it
+  // behind the pair kernel of the same call, which has waited: what was before that is read by L2 alone
   if (!behind_pairs) wait_prerequisite();
   allow_dependents();
   // by the closing warp
   auto fetch_unit = [&](int i, int to) {
     const int unit = i / Hkv;
     if (lane < 3 && RF_IDX_OK(unit, a.v.unit_cap))
-      reinterpret_cast<int4*>(&tm.unit[to])[lane] = reinterpret_cast<const int4*>(a.v.units + unit)[lane];
+      reinterpret_cast<int4*>(&tm.unit[to])[lane] = __ldcg(reinterpret_cast<const int4*>(a.v.units + unit) + lane);
     __syncwarp();
   };
   auto fetch_pages = [&](int at) {
@@ -656,7 +656,7 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
     const size_t row = r < w.rows ? w.at(a, r) : 0;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < w.rows && RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H))
-      x = reinterpret_cast<const uint4*>(a.q + row * ROW_BYTES)[lane & 15];
+      x = __ldcg(reinterpret_cast<const uint4*>(a.q + row * ROW_BYTES) + (lane & 15));
     return x;
   };
   auto keep_row = [&](int e, const uint4& x) {
@@ -667,8 +667,8 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
   int i = (int)(blockIdx.x + team * gridDim.x);
   const bool fits = i < a.v.unit_cap * Hkv;
   if (warp < CLOSE_WARP + TEAMS && closes && fits) fetch_unit(i, 0);   // before it is known whether it is one
-  const bool planned = a.v.head[kPlanMark] == (int)a.v.mark;
-  const int total = planned ? min(a.v.head[kPlanUnits], a.v.unit_cap) * Hkv : 0;
+  const bool planned = __ldcg(a.v.head + kPlanMark) == (int)a.v.mark;
+  const int total = planned ? min(__ldcg(a.v.head + kPlanUnits), a.v.unit_cap) * Hkv : 0;
   const int at_once = (int)gridDim.x * TEAMS;
   const bool queued = total > at_once;
   if (warp < CLOSE_WARP + TEAMS && closes && i < total) fetch_pages(0);

@@ -97,10 +97,10 @@ __device__ __forceinline__ bool any_nan(const float4& x) {
   return x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w;
 }
 
-// Columns 4 lane .. + 3 of a 16-bit row, widened
+// Columns 4 lane .. + 3 of a 16-bit row, widened (by L2 alone: the kernel may not have waited)
 template <bool F16>
 __device__ __forceinline__ float4 load_row4(const uint8_t* row, int lane) {
-  const uint2 u = *reinterpret_cast<const uint2*>(row + lane * 8);
+  const uint2 u = __ldcg(reinterpret_cast<const uint2*>(row + lane * 8));
   if constexpr (F16) {
     const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
     const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
