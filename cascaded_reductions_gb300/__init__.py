@@ -1102,7 +1102,8 @@ def page_tables(lens, news, table, stack, n_free, page, tokens, lens_out=None, n
     [1].  Returns starts [B + 1], positions [tokens], slots [tokens] (-1 where a token has no place),
     lens_out [B] and n_free_out [1]; the last two may be given, as lens and n_free themselves for one.
     A request whose pages are not all there gets none: its length stays, its slots are -1 (paged_plan
-    takes the slots, so that its rows attend to nothing).
+    takes the slots, so that its rows attend to nothing).  ``tokens``: at least all new tokens together;
+    0 where requests only end (the step's other calls have nothing to do then).
     Outputs may lie in one allocation, which lives as long as any of them."""
     if stream is not None:
         return _within(stream, lens, page_tables, lens, news, table, stack, n_free, page, tokens,
@@ -1113,10 +1114,13 @@ def page_tables(lens, news, table, stack, n_free, page, tokens, lens_out=None, n
             return _done(r, "rf_page_tables")
     new = dict(device=lens.device, dtype=torch.int32)
     starts = torch.empty(lens.shape[0] + 1, **new)
-    positions, slots = torch.empty(tokens, **new), torch.empty(tokens, **new)
+    rows = 1 if tokens == 0 else tokens     # the call has a row at least
+    positions, slots = torch.empty(rows, **new), torch.empty(rows, **new)
     lens_out = torch.empty_like(lens) if lens_out is None else lens_out
     n_free_out = torch.empty_like(n_free) if n_free_out is None else n_free_out
     rf_page_tables(lens, news, table, stack, n_free, page, starts, positions, slots, lens_out, n_free_out)
+    if tokens == 0:
+        positions, slots = positions[:0], slots[:0]
     return starts, positions, slots, lens_out, n_free_out
 
 

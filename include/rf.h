@@ -498,7 +498,9 @@ rf_status rf_cache_evict(const void* k, const void* v, const float* weight, cons
  *   n_free     [1]
  *   starts     [B + 1] out   sums of the new tokens before each request, and their total
  *   positions  [T] out     position of each new token in its request; 0 past the total
- *   slots      [T] out     page * `page` + row in the page, -1 past the total
+ *   slots      [T] out     page * `page` + row in the page, -1 past the total.  T is the
+ *                          total at least (tokens behind row T - 1 count in starts and
+ *                          lens_out, but have no row), 1 in a step where requests only end
  *   lens_out   [B] out     the new lengths; may be lens itself
  *   n_free_out [1] out     may be n_free itself
  * Where the stack runs out, the first request whose new pages are not all there and

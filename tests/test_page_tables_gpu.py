@@ -157,3 +157,15 @@ def test_as_many_pages_as_an_int_counts():
     assert torch.equal(table[1, :taken], table[0].flip(0)[:taken]) and (table[1, taken:] == 7).all()
     assert torch.equal(slots, table[1, :taken]) and torch.equal(positions, torch.arange(taken, device="cuda").int())
     assert (stack[:P - given][-(1 << 20):] == -3).all() and (stack[:1 << 20] == -3).all()
+
+
+def test_requests_that_only_end():
+    """A step without new tokens."""
+    table, stack, _ = tables(3, 16, [2, 0, 3], 4, 5, 6)
+    ref = paged.page_tables([20, 0, 48], [-1, 0, -1], table, stack, 5, 16, 0)
+    dev_table, dev_stack = i32(table), i32(stack)
+    got = rf.page_tables(i32([20, 0, 48]), i32([-1, 0, -1]), dev_table, dev_stack, i32([5]), 16, 0)
+    for g, r in zip((*got[:4], got[4][0], dev_table, dev_stack), ref):
+        assert tuple(g.shape) == np.shape(r) and np.array_equal(g.cpu().numpy(), r)
+    with pytest.raises((ValueError, RuntimeError)):
+        rf.page_tables(i32([20]), i32([1]), i32([[0, 1]]), i32([3, 2]), i32([2]), 16, -1)
