@@ -22,7 +22,7 @@
 // a token's angles, keeps them in registers and goes through its heads, the next group's rows
 // in flight.
 //   Few (norm_rope_few_kernel): the heads of a token are spread over the warps of one CTA or
-// of several, each of which makes the token's angles for its own.
+// of several, each of which makes the token's angles for itself.
 // [8192 tokens, 32 + 8 + 8 heads of 128, 201 MB]: 40 us, 5.0 TB/s, and 45 us by the second
 // kernel, whose every item reads weights and angles from shared memory (85 % of its rate).
 // The first issues an instruction in 61 % of the cycles; shares of whole tokens take 44 us (2.2
@@ -38,7 +38,7 @@ namespace rf {
 namespace {
 
 constexpr int WARPS = 8;
-constexpr int MANY = 8;                 // tokens per SM from which on a warp takes a whole one
+constexpr int MANY = 8;                 // tokens per SM from which on a warp takes a share of all heads
 
 struct NormRope {
   const uint16_t *q, *k, *v;
@@ -53,7 +53,7 @@ struct NormRope {
   float eps;
   int T, H, Hkv, R, axes, page;
   bool w32;                             // weights are fp32
-  int heads, tokens, slices;            // per token with v; of a CTA; CTAs that share a token
+  int heads, slices;                    // per token with v; CTAs that share a token
 };
 
 template <bool F16>
@@ -290,8 +290,8 @@ norm_rope_kernel(const NormRope a) {
   }
 }
 
-// One CTA: `tokens` adjacent tokens, or one slice of the heads of a single token.  Its
-// warps take groups of 32 / (D / 16) heads of a token at a time.
+// One CTA: a token's heads, or a slice of them.  Its warps take groups of 32 / (D / 16) heads
+// at a time.
 template <bool F16, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(WARPS * 32)
 norm_rope_few_kernel(const NormRope a) {
@@ -301,11 +301,10 @@ norm_rope_few_kernel(const NormRope a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int half = a.R / 2;
   float* w_s = smem;                            // [2][D]: weights of q and k
-  float2* turn = reinterpret_cast<float2*>(smem + 2 * D);   // [tokens][R / 2]: cos, sin
-  const int t0 = (int)(blockIdx.x / a.slices) * a.tokens, slice = (int)(blockIdx.x % a.slices);
-  const int nt = min(a.tokens, a.T - t0);
+  float2* turn = reinterpret_cast<float2*>(smem + 2 * D);   // [R / 2]: cos, sin
+  const size_t t = blockIdx.x / a.slices;
+  const int slice = (int)(blockIdx.x % a.slices);
   const int groups = (a.heads + HEADS - 1) / HEADS;
-  const int items = nt * groups;
   wait_prerequisite();
   allow_dependents();
 
@@ -316,15 +315,13 @@ norm_rope_few_kernel(const NormRope a) {
   const int c0 = INTERLEAVED ? 2 * j : j < rc ? j : 2 * rc + 2 * (j - rc);
   const int c1 = INTERLEAVED ? 2 * j + 1 : j < rc ? j + rc : c0 + 1;
   struct Item {
-    int t, h;                                   // token of the CTA, head (q, then k, then v)
+    int h;                                      // head (q, then k, then v)
     uint4 x0, x1;
   };
   auto load = [&](int i, Item& it) {
-    it.t = i / groups;
-    it.h = (i - it.t * groups) * HEADS + hl;
+    it.h = i * HEADS + hl;
     it.x0 = it.x1 = make_uint4(0, 0, 0, 0);
-    if (i >= items || it.h >= a.heads) return;
-    const size_t t = t0 + it.t;
+    if (i >= groups || it.h >= a.heads) return;
     const bool is_q = it.h < a.H, is_k = !is_q && it.h < a.H + a.Hkv;
     const int h = is_q ? it.h : is_k ? it.h - a.H : it.h - a.H - a.Hkv;
     const uint16_t* row = is_q ? a.q + t * a.q_step : is_k ? a.k + t * a.k_step : a.v + t * a.v_step;
@@ -341,20 +338,18 @@ norm_rope_few_kernel(const NormRope a) {
     const void* w = e < D ? a.qw : a.kw;
     w_s[e] = w ? weight_of<F16>(w, e < D ? e : e - D, a.w32) : 1.f;
   }
-  for (int e = tid; e < nt * half; e += WARPS * 32) {
-    const int t = e / half, p = e - t * half;
+  for (int p = tid; p < half; p += WARPS * 32) {
     float s, c;
-    turn_of(a, turn_unit(RF_IDX_OK(p, half) ? a.freq[p] : 0.f), p, (size_t)t0 + t, &s, &c);
-    turn[t * half + p] = make_float2(c, s);
+    turn_of(a, turn_unit(RF_IDX_OK(p, half) ? a.freq[p] : 0.f), p, t, &s, &c);
+    turn[p] = make_float2(c, s);
   }
   __syncthreads();
 
-  for (; i < items; i += stride) {
+  for (; i < groups; i += stride) {
     Item next;
     load(i + stride, next);
     const bool is_q = it.h < a.H, is_k = !is_q && it.h < a.H + a.Hkv;
     const bool in = it.h < a.heads;
-    const size_t t = t0 + it.t;
     float x[16];
     widen8<F16>(it.x0, x);
     widen8<F16>(it.x1, x + 8);
@@ -371,7 +366,7 @@ norm_rope_few_kernel(const NormRope a) {
         for (int e = 0; e < 16; ++e) x[e] *= r * w[(e < 8 ? c0 * 8 : c1 * 8 - 8) + e];
       }
       if (j < rc) {
-        const float2* cs = turn + it.t * half + 8 * j;
+        const float2* cs = turn + 8 * j;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
           const float2 z = cs[p];
@@ -421,17 +416,14 @@ rf_status launch_d(NormRope a, bool interleaved, cudaStream_t st) {
   }
   const int heads_per_item = 32 / (D / 16);
   const long long groups = (a.heads + heads_per_item - 1) / heads_per_item;
-  // A CTA's tokens: enough items to hide its angles behind, while every SM has its share of
-  // CTAs; where the tokens alone do not fill the device, several CTAs share one.
-  a.tokens = 1, a.slices = 1;
-  while (a.tokens < 8 && (long long)a.tokens * groups < 4 * WARPS && (long long)a.T / (2 * a.tokens) >= 8ll * sms)
-    a.tokens *= 2;
-  if (a.tokens == 1 && a.T < 4 * sms) {
+  // where the tokens alone do not fill the device, several CTAs share one
+  a.slices = 1;
+  if (a.T < 4 * sms) {
     const long long most = (groups + WARPS - 1) / WARPS, want = 4ll * sms / a.T;
     a.slices = (int)(most < want ? most : want < 1 ? 1 : want);
   }
-  const size_t smem = 2 * D * sizeof(float) + (size_t)a.tokens * (a.R / 2) * sizeof(float2);
-  const long long grid = ((long long)a.T + a.tokens - 1) / a.tokens * a.slices;
+  const size_t smem = 2 * D * sizeof(float) + (size_t)(a.R / 2) * sizeof(float2);
+  const long long grid = (long long)a.T * a.slices;
   auto* kernel = interleaved ? norm_rope_few_kernel<F16, D, true> : norm_rope_few_kernel<F16, D, false>;
   return launch_after(kernel, (unsigned)grid, WARPS * 32, smem, st, a);
 }
