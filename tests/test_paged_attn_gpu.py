@@ -423,3 +423,27 @@ def test_requests_without_pages(B, news, keys, window, sinks):
 def test_slots_of_another_size_are_refused():
     with pytest.raises(ValueError):
         rf.paged_plan(i32([0, 4]), i32([9]), 4, 8, 2, 4, 16, slots=i32([1, 2, 3]))
+
+
+@pytest.mark.parametrize("H,Hkv,news,kernel", [(32, 8, 8, "streaming"), (32, 8, 9, "pairs"), (16, 16, 32, "streaming"),
+                                               (16, 16, 33, "pairs"), (12, 4, 21, "streaming"), (12, 4, 22, "pairs"),
+                                               (64, 2, 2, "streaming"), (64, 2, 3, "pairs")])
+def test_rows_at_the_limit_of_a_large_call(H, Hkv, news, kernel):
+    """On either side of the rows per key head up to which a large call streams, 32 times G over the heads
+    that the other kernel packs (32 at G = 4 and 1; 64 at most, 63 and 66 rows at G = 3; 64 and 96 at G = 32):
+    weights in two 16-bit terms up to it."""
+    G, sms = H // Hkv, torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [2000, 700, 1300, news, 64, 900, 1111, 257, 300, 800, 1500, 600, 999, 1024]
+    x = make(lens, [news] * 14, H, Hkv, 64, seed=news + H)
+    max_len = 64 * x["table"].shape[1]
+    while 14 * Hkv * -(-news * G // 16) * -(-max_len // 64) <= 32 * sms:      # small: room for longer requests
+        max_len += 6400
+    width = max_len // 64
+    x["table"] = torch.nn.functional.pad(x["table"], (0, width - x["table"].shape[1]), value=-1)
+    out, lse = call(x)
+    # the documented rule: a large call, and the request on the side of it that the case is for
+    few = few_rows(14, H, Hkv, news, max_len)
+    assert few == x["few"] == min(64, 32 * G // max(g for g in (8, 4, 2, 1) if G % g == 0))
+    assert not (news * G <= 64 and 14 * Hkv * -(-news * G // 16) * -(-max_len // 64) <= 32 * sms)
+    assert kernel == ("streaming" if news * G <= few else "pairs")
+    check(x, out, lse, rows=[0, -1])
