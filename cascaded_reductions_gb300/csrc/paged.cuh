@@ -72,7 +72,7 @@ enum { kPlanMark, kPlanUnits, kPlanRanges, kPlanClusters, kPlanLast, kPlanJoins,
 // Where the parts of a plan lie, in bytes from its start.
 struct PagedLayout {
   size_t seqs, before, ranges, joins, units, merges, counters, unit_ml, unit_acc, slots, bytes;
-  int unit_cap, range_cap, merge_cap, slot_cap;
+  int unit_cap, state_cap, range_cap, merge_cap, slot_cap;
   uint32_t mark;                        // of the sizes: a plan of others is refused on the device
 };
 
@@ -84,7 +84,8 @@ struct PagedUnit {
   int b, tile, step0, step1;            // request, 16-row tile, steps of 64 keys
   int first, pieces;                    // unit of the tile's first piece, pieces
   int start, n, len;                    // the request, as in PagedSeq
-  int pad[3];
+  int state;                            // place of its state, with several pieces
+  int pad[2];
 };
 struct PagedRange {
   int b, item, block, count;            // the first block's request, item and number in it; blocks
@@ -107,10 +108,10 @@ struct PagedView {
   const PagedUnit* units;
   const int* merges;                    // first units of the 16-row tiles in several pieces
   int* counters;                        // pieces of a small call's tiles that are done
-  float2* unit_ml;                      // [unit][Hkv][unit_rows]
-  float* unit_acc;                      // [unit][Hkv][unit_rows][128]
+  float2* unit_ml;                      // [state][Hkv][unit_rows]
+  float* unit_acc;                      // [state][Hkv][unit_rows][128]
   float* slots;
-  int unit_cap, range_cap, merge_cap, slot_cap;
+  int unit_cap, state_cap, range_cap, merge_cap, slot_cap;
   uint32_t mark;
   int G, packed, P_log2, groups, key_groups;   // heads per key head and per tile; positions of a
                                         // tile; head groups in all and per key head
@@ -226,7 +227,7 @@ inline PagedView paged_view(const PagedShape& s, const PagedLayout& l, void* pla
   v.unit_acc = reinterpret_cast<float*>(p + l.unit_acc);
   v.slots = reinterpret_cast<float*>(p + l.slots);
   v.merges = reinterpret_cast<const int*>(p + l.merges);
-  v.unit_cap = l.unit_cap, v.range_cap = l.range_cap, v.merge_cap = l.merge_cap, v.slot_cap = l.slot_cap;
+  v.unit_cap = l.unit_cap, v.state_cap = l.state_cap, v.range_cap = l.range_cap, v.merge_cap = l.merge_cap, v.slot_cap = l.slot_cap;
   v.mark = l.mark;
   v.G = s.G(), v.packed = s.packed(), v.P_log2 = s.positions_log2();
   v.key_groups = v.G / v.packed, v.groups = s.Hkv * v.key_groups;

@@ -392,7 +392,7 @@ __device__ __forceinline__ bool merge_warps(const PagedAttn& a, const Work& w, c
     write_row(a, w.at(a, r), A, M, L, lane, F16 ? RF_F16 : RF_BF16);
   } else {
     const size_t s = state0 + r;
-    if (!RF_IDX_OK(s, (size_t)a.v.unit_cap * a.v.s.Hkv * a.v.s.unit_rows())) return false;
+    if (!RF_IDX_OK(s, (size_t)a.v.state_cap * a.v.s.Hkv * a.v.s.unit_rows())) return false;
     *(reinterpret_cast<float4*>(a.v.unit_acc + s * HD) + lane) = A;
     if (lane == 0) a.v.unit_ml[s] = make_float2(M, L);
   }
@@ -408,7 +408,7 @@ __device__ __noinline__ void redo_row(const PagedAttn& a, const Work w, int r, b
                                       float2 ml, int t0, int t1, int lane) {
   const size_t row = w.at(a, r), s = state0 + r;
   if (direct ? !RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)
-             : !RF_IDX_OK(s, (size_t)a.v.unit_cap * a.v.s.Hkv * a.v.s.unit_rows()))
+             : !RF_IDX_OK(s, (size_t)a.v.state_cap * a.v.s.Hkv * a.v.s.unit_rows()))
     return;
   float4* state = reinterpret_cast<float4*>(a.v.unit_acc + s * HD) + lane;
   const float4 A = direct ? load_row4<F16>(a.out + row * ROW_BYTES, lane) : *state;
@@ -432,7 +432,7 @@ __device__ __forceinline__ void merge_pieces(const PagedAttn& a, const Work& w, 
   constexpr int SB = LOADS / RB;
   const size_t step = (size_t)a.v.s.Hkv * a.v.s.unit_rows();
   const size_t base = first * step + (size_t)w.hk * a.v.s.unit_rows() + r0;
-  const size_t states = (size_t)a.v.unit_cap * step;
+  const size_t states = (size_t)a.v.state_cap * step;
   (void)states;                         // read by the checked build only
   float M[RB], L[RB];
   float4 A[RB];
@@ -556,7 +556,7 @@ paged_few_kernel(const __grid_constant__ PagedAttn a) {
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
     st.close();
-    const size_t state0 = ((size_t)unit * Hkv + hk) * a.v.s.unit_rows();
+    const size_t state0 = ((size_t)u.state * Hkv + hk) * a.v.s.unit_rows();
     uint32_t bad = 0;
     for (int r = 0; r < w.rows; r += MERGE_ROWS) {
       if (r > 0) __syncthreads();       // the last rows have been read
@@ -587,14 +587,15 @@ paged_few_kernel(const __grid_constant__ PagedAttn a) {
     __syncthreads();
     if (sm_last) {
       const int share = (w.rows + WARPS - 1) / WARPS, r = warp * share, nr = min(share, w.rows - r);
+      const int first = u.state - (unit - u.first);          // the first piece's state
       constexpr int dtype = F16 ? RF_F16 : RF_BF16;
       if (nr > 0) {
         if (share == 1)
-          merge_pieces<1, 32>(a, w, u.first, u.pieces, r, nr, dtype, lane);
+          merge_pieces<1, 32>(a, w, first, u.pieces, r, nr, dtype, lane);
         else if (share == 2)
-          merge_pieces<2, 32>(a, w, u.first, u.pieces, r, nr, dtype, lane);
+          merge_pieces<2, 32>(a, w, first, u.pieces, r, nr, dtype, lane);
         else
-          merge_pieces<4, 32>(a, w, u.first, u.pieces, r, nr, dtype, lane);
+          merge_pieces<4, 32>(a, w, first, u.pieces, r, nr, dtype, lane);
       }
     }
     __syncthreads();                    // sm_last may be written again
@@ -746,7 +747,7 @@ paged_decode_kernel(const __grid_constant__ PagedAttn a, const bool behind_pairs
       }
       st.close();
       const Work w(a, u, hk);
-      const size_t state0 = ((size_t)unit * Hkv + hk) * a.v.s.unit_rows();
+      const size_t state0 = ((size_t)u.state * Hkv + hk) * a.v.s.unit_rows();
       uint32_t bad = 0;
       for (int r = 0; r < w.rows; r += MERGE_ROWS) {
         if (r > 0) named_sync<WARPS * 32>(bars + kBarStream);   // the last rows have been read

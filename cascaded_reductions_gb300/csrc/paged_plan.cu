@@ -42,7 +42,7 @@ struct Plan {
   PagedJoin* joins;
   PagedUnit* units;
   int *merges, *counters;
-  int unit_cap, range_cap, merge_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
+  int unit_cap, state_cap, range_cap, merge_cap, clusters, slots;   // slots: CTAs of the streaming kernel at once
   uint32_t mark;
   int G, P_log2, groups;                // heads per key head; positions of a tile, head groups of the pair kernel
 };
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
   auto pieces = [&](int n) { return pieces_of(n, (int)piece); };
   if (tid == 0) n_joins = n_merges = 0;
   __syncthreads();
-  long long units = 0;
+  long long counts = 0;                 // units so far << 32 | those with a state
   for (int b0 = 0; b0 < s.B; b0 += THREADS) {
     const int b = b0 + tid;
     PagedSeq q = {0, 0, 0, 1};
@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     int nt = 0, ns = 0, np = 0;
     if (q.n > 0 && !q.pair) nt = tiles_of(a, q), ns = steps_of(s, q), np = pieces(ns);
     long long total;
-    const long long at = units + block_scan((long long)nt * np, sm, &total);
+    const long long mine = (long long)nt * np;
+    const long long at = counts + block_scan(mine << 32 | (np > 1 ? mine : 0ll), sm, &total);
     // a warp per request writes its units
     cuts[tid] = make_int2(nt * np, np);
     if (nt * np > 0) firsts[tid] = at;
@@ -198,7 +199,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
     for (int w = warp; w < THREADS && b0 + w < s.B; w += WARPS) {
       const int count = cuts[w].x, n_p = cuts[w].y;
       if (count == 0) continue;
-      const long long u0 = firsts[w];
+      const long long u0 = firsts[w] >> 32;
+      const int s0 = (int)(firsts[w] & 0xffffffffll);
       const PagedSeq r = a.seqs[b0 + w];
       const int n_s = steps_of(s, r);
       for (int u = lane; u < count; u += 32) {
@@ -212,7 +214,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
         x.first = (int)(u0 + tile * n_p);
         x.pieces = n_p;
         x.start = r.start, x.n = r.n, x.len = r.len;
-        x.pad[0] = x.pad[1] = x.pad[2] = 0;
+        x.state = n_p > 1 ? min(s0 + u, a.state_cap - 1) : 0;
+        x.pad[0] = x.pad[1] = 0;
         a.units[u0 + u] = x;
         if (i == 0 && n_p > 1) {
           const int m = atomicAdd(&n_merges, 1);
@@ -221,9 +224,9 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Plan a) {
       }
     }
     __syncthreads();
-    units += total;
+    counts += total;
   }
-  const int n_units = (int)min(units, (long long)a.unit_cap);
+  const int n_units = (int)min(counts >> 32, (long long)a.unit_cap);
   for (long long i = tid; i < (long long)n_units * s.Hkv; i += THREADS) a.counters[i] = 0;
 
   // the pair kernel's ranges
@@ -363,6 +366,8 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
   long long cut = (2ll * sms * MANY_UNITS + s.Hkv - 1) / s.Hkv;
   if (cut > tiles * (steps - 1)) cut = tiles * (steps - 1);
   l->unit_cap = (int)(tiles + cut);
+  // states of the units of divided tiles alone: each of those tiles has one of the cuts at least
+  l->state_cap = (int)(tiles < cut ? tiles + cut : 2 * cut);
   l->merge_cap = (int)tiles;
   l->range_cap = l->slot_cap = 0;
   if (s.some_pairs()) {
@@ -382,7 +387,7 @@ bool paged_layout(const PagedShape& s, PagedLayout* l) {
     at = align(at + bytes);
     return p;
   };
-  const size_t rows = (size_t)l->unit_cap * s.Hkv * s.unit_rows();
+  const size_t rows = (size_t)l->state_cap * s.Hkv * s.unit_rows();
   l->seqs = take((size_t)s.B * sizeof(PagedSeq));
   l->before = take(((size_t)s.B + 1) * sizeof(long long));
   l->ranges = take((size_t)l->range_cap * sizeof(PagedRange));
@@ -418,7 +423,7 @@ rf_status launch_paged_plan(const int32_t* starts, const int32_t* lens, const in
   a.units = reinterpret_cast<PagedUnit*>(p + l.units);
   a.merges = reinterpret_cast<int*>(p + l.merges);
   a.counters = reinterpret_cast<int*>(p + l.counters);
-  a.unit_cap = l.unit_cap, a.range_cap = l.range_cap, a.merge_cap = l.merge_cap;
+  a.unit_cap = l.unit_cap, a.state_cap = l.state_cap, a.range_cap = l.range_cap, a.merge_cap = l.merge_cap;
   a.clusters = 0;
   if (s.some_pairs()) {
     a.clusters = paged_pairs();

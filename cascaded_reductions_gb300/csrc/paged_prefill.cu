@@ -420,14 +420,14 @@ __device__ __forceinline__ uint32_t nan_of(const float4& y) {
   return (y.x != y.x) | (y.y != y.y) << 1 | (y.z != y.z) << 2 | (y.w != y.w) << 3;
 }
 
-// A row of the streaming kernel's tile from the states of its pieces, in order; one warp,
-// four columns per lane.
+// A row of the streaming kernel's tile, whose first piece is u, from the states of its pieces,
+// in order; one warp, four columns per lane.
 template <bool F16>
-__device__ __forceinline__ void merge_row(const PagedAttn& a, const PagedUnit& u, int first, int hk, int r, int lane) {
+__device__ __forceinline__ void merge_row(const PagedAttn& a, const PagedUnit& u, int hk, int r, int lane) {
   constexpr int U = 16;                               // states in flight
   const PagedView& v = a.v;
-  const size_t step = (size_t)v.s.Hkv * v.s.unit_rows(), base = first * step + (size_t)hk * v.s.unit_rows() + r;
-  const size_t states = (size_t)v.unit_cap * step;
+  const size_t step = (size_t)v.s.Hkv * v.s.unit_rows(), base = u.state * step + (size_t)hk * v.s.unit_rows() + r;
+  const size_t states = (size_t)v.state_cap * step;
   (void)states;                                       // read by the checked build only
   float M = -INFINITY, L = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -508,7 +508,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
       const int first = RF_IDX_OK(m, v.merge_cap) ? v.merges[m] : 0;
       if (!RF_IDX_OK(first, v.unit_cap)) continue;
       const PagedUnit u = v.units[first];
-      if (r < u.n * v.G - u.tile * kPagedTileRows) merge_row<F16>(a, u, first, hk, r, lane);
+      if (r < u.n * v.G - u.tile * kPagedTileRows) merge_row<F16>(a, u, hk, r, lane);
     }
   }
   if (join < min(v.head[kPlanJoins], v.range_cap)) {

@@ -447,3 +447,21 @@ def test_rows_at_the_limit_of_a_large_call(H, Hkv, news, kernel):
     assert not (news * G <= 64 and 14 * Hkv * -(-news * G // 16) * -(-max_len // 64) <= 32 * sms)
     assert kernel == ("streaming" if news * G <= few else "pairs")
     check(x, out, lse, rows=[0, -1])
+
+
+def test_scratch_goes_by_what_is_divided():
+    """States are kept of divided tiles alone, however many requests there are."""
+    for B, Hkv in ((1024, 8), (1024, 32), (8192, 8)):
+        size = rf.rf_paged_plan_bytes(B, B + 4096, 32, Hkv, 4096, 32768)
+        assert 0 < size < 80 << 20, size
+    # whole tiles between divided ones, behind memory that holds 3e9
+    lens = [9000 if b % 97 == 5 else 1 + b % 60 for b in range(700)]
+    x = make(lens, [1] * 700, 16, 8, 16, seed=700)
+    plan = rf.paged_plan(x["starts"], x["lens"], 700, 16, 8, 1, x["table"].shape[1] * 16)
+    plan.plan.fill_(0x4f)
+    out, lse = call(x, plan=plan)
+    some = [0, 4, 5, 6, 101, 102, 103, 296, 399, 493, 684, 699]
+    starts = np.arange(len(some) + 1)
+    at = torch.tensor(some, device="cuda")
+    check(dict(q=x["q"][at], kp=x["kp"], vp=x["vp"], table=x["table"][at], starts=i32(starts), lens=x["lens"][at],
+               few=x["few"]), out[at], lse[at])
