@@ -1,6 +1,8 @@
 // What the kernels over a serving cache of grouped heads share.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace rf {
@@ -10,6 +12,29 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Columns 4 lane .. + 3 of a 16-bit row, widened (by L2 alone: the kernel may not have waited)
+template <bool F16>
+__device__ __forceinline__ float4 load_row4(const uint8_t* row, int lane) {
+  const uint2 u = __ldcg(reinterpret_cast<const uint2*>(row + lane * 8));
+  if constexpr (F16) {
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+  } else {
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  }
+}
+
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ long long scan_warp(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
 }
 
 constexpr int kDecodeTile = 16;        // keys of one tile of the decode kernels

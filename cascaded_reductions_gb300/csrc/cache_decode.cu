@@ -151,20 +151,16 @@ __device__ __forceinline__ void copy_tile(const CacheDecode& a, const Group& q, 
   }
 }
 
-// One warp's running state of a row group: rows lane / 4 (index 0) and + 8
-// (index 1); acc[d] holds columns 8 d + 2 (lane % 4) and + 1 of both.
+// One warp's running state of a row group.
 template <bool F16, bool SCORES, bool POSITIONS>
-struct State {
-  // The weights' reference for the maximum m; the state given away has it for its m.
-  // From 2^24 on m - 15 may round to m - 16 or less, and a weight to 2^16: m itself then.
-  static __device__ __forceinline__ float below(float m) {
-    if constexpr (!F16) return m;
-    const float f = m - 15.f;
-    return m - f > 15.5f ? m : f;
-  }
-  uint32_t qf[HD / 16][4];
-  float acc[HD / 8][4];
-  float m0, m1, l0, l1;
+struct State : RowState<F16> {
+  using RowState<F16>::qf;
+  using RowState<F16>::acc;
+  using RowState<F16>::m0;
+  using RowState<F16>::m1;
+  using RowState<F16>::l0;
+  using RowState<F16>::l1;
+  using RowState<F16>::below;
 
   __device__ __forceinline__ void start(const CacheDecode& a, const Rows& w, int lane) {
     // Q fragments: columns 16 kk + 2 (lane % 4) (+ 8) of the two rows
@@ -181,113 +177,45 @@ struct State {
       qf[kk][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + kk * 32 + 16) : 0u;
       qf[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + kk * 32 + 16) : 0u;
     }
-#pragma unroll
-    for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
-    m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
+    this->clear();
   }
 
   // folds in keys t0 .. min(t0 + 15, n - 1), whose copies are in `st`
   __device__ __forceinline__ void tile(const CacheDecode& a, const Rows& w, uint32_t st, int t0, int n,
                                        int lane) {
-  float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-  {
-    const int r = (lane & 7) + ((lane >> 4) << 3);
+    float s[2][4];
+    this->products(st, s, lane);
 #pragma unroll
-    for (int kk = 0; kk < HD / 16; ++kk) {
-      const int c = 2 * kk + ((lane >> 3) & 1);
-      uint32_t kb[4];
-      ldmatrix_x4(st + r * ROW_BYTES + ((c ^ (r & 7)) << 4), kb);
-      mma16816<F16>(s[0], qf[kk], kb[0], kb[1]);
-      mma16816<F16>(s[1], qf[kk], kb[2], kb[3]);
-    }
-  }
-  float mx0 = -INFINITY, mx1 = -INFINITY;
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        const int t = t0 + nt * 8 + 2 * (lane & 3) + e;
+        const bool in = t < n;
+        s[nt][e] = in ? s[nt][e] * a.scale_log2 : -INFINITY;
+        s[nt][2 + e] = in ? s[nt][2 + e] * a.scale_log2 : -INFINITY;
+      }
+    if constexpr (SCORES) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int t = t0 + nt * 8 + 2 * (lane & 3) + e;
-      const bool in = t < n;
-      s[nt][e] = in ? s[nt][e] * a.scale_log2 : -INFINITY;
-      s[nt][2 + e] = in ? s[nt][2 + e] * a.scale_log2 : -INFINITY;
-      mx0 = fmaxf(mx0, s[nt][e]);
-      mx1 = fmaxf(mx1, s[nt][2 + e]);
-    }
-  if constexpr (SCORES) {
+      for (int nt = 0; nt < 2; ++nt) {
+        const int t = t0 + nt * 8 + 2 * (lane & 3);
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int t = t0 + nt * 8 + 2 * (lane & 3);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = (lane >> 2) + 8 * half;
-        if (r >= w.n || t >= n) continue;
-        float* at = a.scores + (w.row0 + r) * a.cap + t;
-        const size_t i = (w.row0 + r) * a.cap + t, all = (size_t)a.B * a.H * a.cap;
-        (void)i, (void)all;                       // read by the checked build only
-        if (t + 1 < n && a.cap % 2 == 0) {        // t is even, and so the pair is aligned
-          if (RF_SPAN_OK(i, 2, all))
-            *reinterpret_cast<float2*>(at) = make_float2(s[nt][2 * half], s[nt][2 * half + 1]);
-        } else {
-          if (RF_IDX_OK(i, all)) at[0] = s[nt][2 * half];
-          if (t + 1 < n && RF_IDX_OK(i + 1, all)) at[1] = s[nt][2 * half + 1];
+        for (int half = 0; half < 2; ++half) {
+          const int r = (lane >> 2) + 8 * half;
+          if (r >= w.n || t >= n) continue;
+          float* at = a.scores + (w.row0 + r) * a.cap + t;
+          const size_t i = (w.row0 + r) * a.cap + t, all = (size_t)a.B * a.H * a.cap;
+          (void)i, (void)all;                       // read by the checked build only
+          if (t + 1 < n && a.cap % 2 == 0) {        // t is even, and so the pair is aligned
+            if (RF_SPAN_OK(i, 2, all))
+              *reinterpret_cast<float2*>(at) = make_float2(s[nt][2 * half], s[nt][2 * half + 1]);
+          } else {
+            if (RF_IDX_OK(i, all)) at[0] = s[nt][2 * half];
+            if (t + 1 < n && RF_IDX_OK(i + 1, all)) at[1] = s[nt][2 * half + 1];
+          }
         }
       }
     }
-  }
-  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-  const bool grew = mx0 > m0 || mx1 > m1;
-  if (__any_sync(0xffffffffu, grew)) {
-    const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-    // differences of the rounded references themselves
-    const float c0 = exp2f(below(m0) - below(ref_of(n0))), c1 = exp2f(below(m1) - below(ref_of(n1)));
-    m0 = n0;
-    m1 = n1;
-    l0 *= c0;
-    l1 *= c1;
-#pragma unroll
-    for (int d = 0; d < HD / 8; ++d) {
-      acc[d][0] *= c0;
-      acc[d][1] *= c0;
-      acc[d][2] *= c1;
-      acc[d][3] *= c1;
-    }
-  }
-  const float f0 = below(ref_of(m0)), f1 = below(ref_of(m1));
-  uint32_t hi[4], lw[4];
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    const float p00 = exp2f(s[nt][0] - f0), p01 = exp2f(s[nt][1] - f0);
-    const float p10 = exp2f(s[nt][2] - f1), p11 = exp2f(s[nt][3] - f1);
-    l0 += p00 + p01;
-    l1 += p10 + p11;
-    split16<F16>(p00, p01, hi[2 * nt], lw[2 * nt]);
-    split16<F16>(p10, p11, hi[2 * nt + 1], lw[2 * nt + 1]);
-  }
-  {
-    const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
-#pragma unroll
-    for (int d = 0; d < HD / 16; ++d) {
-      const int c = 2 * d + (lane >> 4);
-      uint32_t vb[4];
-      ldmatrix_x4_trans(st + TK * ROW_BYTES + r * ROW_BYTES + ((c ^ (r & 7)) << 4), vb);
-      mma16816<F16>(acc[2 * d], hi, vb[0], vb[1]);
-      mma16816<F16>(acc[2 * d + 1], hi, vb[2], vb[3]);
-      mma16816<F16>(acc[2 * d], lw, vb[0], vb[1]);
-      mma16816<F16>(acc[2 * d + 1], lw, vb[2], vb[3]);
-    }
-  }
-  }
-
-  // the row sums over the four lanes that share a row; once, before the state is used
-  __device__ __forceinline__ void close() {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    this->fold(s, st, lane);
   }
 
   // the warp's rows into its part of the merge buffer

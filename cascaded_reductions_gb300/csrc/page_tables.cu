@@ -49,14 +49,6 @@ constexpr int WARPS_MAX = 32;
 struct Sums {
   long long a[WARPS_MAX + 1], b[WARPS_MAX + 1];
 };
-__device__ __forceinline__ long long scan_warp(long long x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
 
 // last i of n ascending values with v[i] <= x (v[0] = 0 <= x)
 __device__ __forceinline__ int find(const int* v, int n, int x) {

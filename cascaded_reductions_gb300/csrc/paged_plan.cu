@@ -47,14 +47,6 @@ struct Plan {
   int G, P_log2, groups;                // heads per key head; positions of a tile, head groups of the pair kernel
 };
 
-__device__ __forceinline__ long long warp_scan(long long x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
 __device__ __forceinline__ long long warp_sum(long long x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -63,11 +55,11 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // exclusive prefix sum over the CTA; *total gets the sum
 __device__ __forceinline__ long long block_scan(long long x, long long* sm, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long s = warp_scan(x, lane);
+  const long long s = scan_warp(x, lane);
   if (lane == 31) sm[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    const long long p = warp_scan(sm[lane], lane);
+    const long long p = scan_warp(sm[lane], lane);
     __syncwarp();
     sm[lane] = p;
   }

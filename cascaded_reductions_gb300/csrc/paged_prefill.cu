@@ -338,18 +338,6 @@ paged_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
 constexpr int FIN_WARPS = 8, FIN_ROWS = 32, FIN_PARTS = kPagedPairRows / FIN_ROWS;
 
-template <bool F16>
-__device__ __forceinline__ float4 widen4(const uint8_t* row, int lane) {
-  const uint2 u = *reinterpret_cast<const uint2*>(row + lane * 8);
-  if constexpr (F16) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(x.x, x.y, y.x, y.y);
-  } else {
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-  }
-}
-
 // Columns of a row that are NaN (bits of `todo`, four per lane), once more from the keys
 // that the row sees.  Ends once they are all NaN again; with `whole` only if the sum is NaN too, so
 // that *lse2 gets the row's sum and maximum (in log2 units).
@@ -363,7 +351,7 @@ __device__ __noinline__ float4 redo_row(const PagedAttn& a, const PagedJoin it, 
   const int n = last < 0 ? 0 : min(ns, last + 1) + max(0, last - lo + 1);
   const size_t row = (size_t)(it.start + i) * a.v.s.H + head;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) x = widen4<F16>(a.q + row * HD * 2, lane);
+  if (RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) x = load_row4<F16>(a.q + row * HD * 2, lane);
   float m = -INFINITY, l = 0.f;
   float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
   bool gone = false;
@@ -380,8 +368,8 @@ __device__ __noinline__ float4 redo_row(const PagedAttn& a, const PagedJoin it, 
       if ((unsigned)id < (unsigned)a.pages) {
         const size_t at = (((size_t)id * a.v.s.Hkv + it.kvh) << a.page_log2) + (key & (page - 1));
         if (RF_IDX_OK(at, ((size_t)a.pages * a.v.s.Hkv) << a.page_log2)) {
-          k = widen4<F16>(a.kp + at * HD * 2, lane);
-          v[u] = widen4<F16>(a.vp + at * HD * 2, lane);
+          k = load_row4<F16>(a.kp + at * HD * 2, lane);
+          v[u] = load_row4<F16>(a.vp + at * HD * 2, lane);
         }
       }
       s[u] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, x.w * k.w)));
@@ -578,7 +566,7 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
         const int t = part * FIN_ROWS + q, i = it.row0 + (t & (P - 1)), head = it.head + (t >> v.P_log2);
         const size_t row = (size_t)(it.start + i) * v.s.H + head;
         if (i >= it.rows || !RF_IDX_OK(row, all_rows)) continue;
-        const float4 y = widen4<F16>(a.out + row * HD * 2, lane);
+        const float4 y = load_row4<F16>(a.out + row * HD * 2, lane);
         const uint32_t todo = nan_of(y);
         if (!__any_sync(0xffffffffu, todo != 0)) continue;
         // masked scores never entered the lse in place; -inf where the sum said nothing

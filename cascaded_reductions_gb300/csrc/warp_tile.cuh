@@ -80,6 +80,101 @@ __device__ __forceinline__ void split16(float p0, float p1, uint32_t& hi, uint32
   }
 }
 
+// One warp's running state of 16 rows: rows lane / 4 (index 0) and + 8 (index 1); acc[d]
+// holds columns 8 d + 2 (lane % 4) and + 1 of both.
+template <bool F16>
+struct RowState {
+  // The weights' reference for the maximum m: an fp16 weight is taken 2^15 times as large;
+  // the state given away has it for its m.  From 2^24 on m - 15 may round to m - 16 or less,
+  // and a weight to 2^16: m itself then.
+  static __device__ __forceinline__ float below(float m) {
+    if constexpr (!F16) return m;
+    const float f = m - 15.f;
+    return m - f > 15.5f ? m : f;
+  }
+  uint32_t qf[HD / 16][4];
+  float acc[HD / 8][4];
+  float m0, m1, l0, l1;
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  }
+
+  // products of the rows with the 16 keys in `st`: s[n][e], key 8 n + 2 (lane % 4) + e % 2 of row e / 2
+  __device__ __forceinline__ void products(uint32_t st, float (&s)[2][4], int lane) const {
+    const int r = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const int c = 2 * kk + ((lane >> 3) & 1);
+      uint32_t kb[4];
+      ldmatrix_x4(st + r * ROW_BYTES + ((c ^ (r & 7)) << 4), kb);
+      mma16816<F16>(s[0], qf[kk], kb[0], kb[1]);
+      mma16816<F16>(s[1], qf[kk], kb[2], kb[3]);
+    }
+  }
+
+  // folds in those keys, whose values follow them in `st`, by their scores in log2 units (-inf: hidden)
+  __device__ __forceinline__ void fold(const float (&s)[2][4], uint32_t st, int lane) {
+    float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+    float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+      // differences of the rounded references themselves
+      const float c0 = exp2f(below(m0) - below(ref_of(n0))), c1 = exp2f(below(m1) - below(ref_of(n1)));
+      m0 = n0;
+      m1 = n1;
+      l0 *= c0;
+      l1 *= c1;
+#pragma unroll
+      for (int d = 0; d < HD / 8; ++d) {
+        acc[d][0] *= c0;
+        acc[d][1] *= c0;
+        acc[d][2] *= c1;
+        acc[d][3] *= c1;
+      }
+    }
+    const float f0 = below(ref_of(m0)), f1 = below(ref_of(m1));
+    uint32_t hi[4], lw[4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const float p00 = exp2f(s[nt][0] - f0), p01 = exp2f(s[nt][1] - f0);
+      const float p10 = exp2f(s[nt][2] - f1), p11 = exp2f(s[nt][3] - f1);
+      l0 += p00 + p01;
+      l1 += p10 + p11;
+      split16<F16>(p00, p01, hi[2 * nt], lw[2 * nt]);
+      split16<F16>(p10, p11, hi[2 * nt + 1], lw[2 * nt + 1]);
+    }
+    const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) {
+      const int c = 2 * d + (lane >> 4);
+      uint32_t vb[4];
+      ldmatrix_x4_trans(st + kDecodeTile * ROW_BYTES + r * ROW_BYTES + ((c ^ (r & 7)) << 4), vb);
+      mma16816<F16>(acc[2 * d], hi, vb[0], vb[1]);
+      mma16816<F16>(acc[2 * d + 1], hi, vb[2], vb[3]);
+      mma16816<F16>(acc[2 * d], lw, vb[0], vb[1]);
+      mma16816<F16>(acc[2 * d + 1], lw, vb[2], vb[3]);
+    }
+  }
+
+  // the row sums over the four lanes that share a row; once, before the state is used
+  __device__ __forceinline__ void close() {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  }
+};
+
 // elements i and i + 1 (i even) of the output
 __device__ __forceinline__ void store_out2(void* out, size_t i, float x, float y, int dtype) {
   if (dtype == RF_F32)
@@ -95,19 +190,6 @@ __device__ __forceinline__ float normalised(float acc, float l) { return l == 0.
 
 __device__ __forceinline__ bool any_nan(const float4& x) {
   return x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w;
-}
-
-// Columns 4 lane .. + 3 of a 16-bit row, widened (by L2 alone: the kernel may not have waited)
-template <bool F16>
-__device__ __forceinline__ float4 load_row4(const uint8_t* row, int lane) {
-  const uint2 u = __ldcg(reinterpret_cast<const uint2*>(row + lane * 8));
-  if constexpr (F16) {
-    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-  } else {
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-  }
 }
 
 }  // namespace
