@@ -12,7 +12,7 @@
 // A turn is taken as a 64-bit integer instead: f / 2 pi mod 1 in units of 2^-64 (from a
 // product in fp64), times the position, is the angle mod a whole turn exactly as the
 // integer wraps; its top 32 bits go through sincospi.  What is left of the error is
-// pos 2^-55 turns from f / 2 pi and half a step of fp32.
+// pos max(1, |f|) 2^-52 rad from the rounding of f / 2 pi and half a step of fp32.
 //
 // What bounds it: HBM (a head is read once and written once), if little goes through
 // shared memory.  A head takes D / 16 lanes, each with two 16-byte chunks that hold both

@@ -524,7 +524,8 @@ rf_status rf_page_tables(const int32_t* lens, const int32_t* news, int B, int32_
  * Per head x [D]:  y = x * weight / sqrt(mean(x^2) + eps)  (y = x without a weight);
  * the pairs (i, i + R/2) of its first R values, or (2i, 2i + 1) if interleaved, turn by
  * angle position * freq[i]:  (a, b) -> (a cos - b sin, b cos + a sin).  fp32, rounded
- * once; the angle is exact to fp32 at any int32 position.
+ * once; the angle, taken mod a turn, is off by at most |position| * max(1, |freq|) * 2^-52
+ * rad beside its rounding to fp32 (5e-7 rad at any int32 position and freq up to 1).
  *   q [T, H, D], k, v [T, Hkv, D] of dtype RF_BF16 or RF_F16: heads dense, tokens
  *               q_step, k_step, v_step elements apart (slices of one projection)
  *   q_weight, k_weight [D] of weight_dtype (RF_F32 or dtype), each may be NULL

@@ -5,6 +5,8 @@ each a rounding of 2^-24, halved by the root; the mean, eps, rsqrt's 2 ulp and t
 cosine by less than 2^-21 (2 ulp, and half a step of the fp32 angle), the rotation's two terms by a
 rounding each: in all less than 2^-18 of |a| + |b|.  Rounding the result adds half a step of it."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -176,3 +178,27 @@ def test_in_place_of_one_token_and_outputs_between_the_rows():
     with pytest.raises(rf.RFError):                                     # half a row over the second token's key
         rf.rf_qk_norm_rope(q, k, None, qw, kw, 1e-6, pos, freqs(128), None, False, None, q_out,
                            wide.view(-1)[32768 + 704:32768 + 1216].view(2, 2, 128), None)
+
+
+TURN = Fraction("6.28318530717958647692528676655900576839433879875021164194988918461563281257242")    # 2 pi
+
+
+@pytest.mark.parametrize("top", [1.0, 6.2831855, 100.0, 30000.0])
+def test_angles_at_the_farthest_positions(top):
+    """Against the exact product, taken mod a turn: off by |pos| max(1, |f|) 2^-52 rad and what the other
+    tests allow the rest (sine and cosine 2^-18 of 1, half a step of the result)."""
+    T, R = 40, 32
+    rng = np.random.default_rng(int(top))
+    pos = rng.integers(-2 ** 31, 2 ** 31 - 1, T)
+    freq = np.float32(top * rng.random(R // 2))
+    freq[0] = -top
+    x = torch.zeros(T, 1, 64, dtype=torch.float16, device="cuda")
+    x[..., :R // 2] = 1                                                     # (1, 0) turns to (cos, sin)
+    out = f64(rf.qk_norm_rope(x, x, i32(pos[None]), torch.from_numpy(freq).cuda())[0])[:, 0]
+    for t in range(T):
+        for i in range(R // 2):
+            f = float(freq[i])
+            angle = float(Fraction(f) * int(pos[t]) % TURN)
+            far = abs(int(pos[t])) * max(1.0, abs(f)) * 2.0 ** -52 + 2.0 ** -18
+            got, want = out[t, [i, i + R // 2]], np.array([np.cos(angle), np.sin(angle)])
+            assert_within(got, want, far + 2.0 ** -11 * (np.abs(want) + far) + 2.0 ** -25, f"token {t}, pair {i}")
