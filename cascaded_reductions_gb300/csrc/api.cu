@@ -41,8 +41,10 @@ bool overlap_rows(const void* a, size_t na, const void* b, size_t rows, size_t n
   if (!a || !b) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   if (x < y) return y - x < na;
-  const uintptr_t d = x - y, i = d < nb ? 0 : (d - nb) / step + 1;   // the first row that ends behind x
-  return i < rows && (i * step <= d || i * step - d < na);
+  const uintptr_t d = x - y;
+  if ((unsigned __int128)(rows - 1) * step + nb <= d) return false;   // behind the last row
+  const uintptr_t i = d < nb ? 0 : (d - nb) / step + 1;               // the first row that ends behind x
+  return i * step <= d || i * step - d < na;
 }
 
 // The sizes of a step over a paged cache.  A window that no request outgrows hides nothing.
