@@ -45,8 +45,8 @@ struct PagedShape {
   // the lengths: that kernel alone then, a CTA per unit, in one launch.  A large call's
   // requests go to the pair kernel where that reads the keys less than half as often: 16 rows
   // a time here, there packed() heads and any of so few positions (24 requests of 8000 keys,
-  // 32/8 heads, 40 rows: 155 us instead of 270; 32 rows: 155 instead of 192, but 29 instead
-  // of 15 us where the requests are short).
+  // 32/8 heads, 40 rows: 162 us instead of 283, of 40 keys 20 instead of 18; 32 rows: 162
+  // instead of 203 and 20 instead of 18, but 38 instead of 33 where 64 requests have 100 keys).
   __host__ __device__ void divide(int sms) {
     limit = kPagedRows;
     const long long units = (long long)B * tiles() * Hkv;

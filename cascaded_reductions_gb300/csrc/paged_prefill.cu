@@ -25,9 +25,9 @@
 // visible keys of a tile are worked out ahead as bits, and only blocks at an edge look at
 // them (4 prompts of up to 8192 tokens 1226 -> 939 us).
 //
-// Measured: 4 x 32/8 heads of 8192 tokens 1590 us, 1.38 PFLOP/s (the dense cache's
-// windowed kernel 1551); 512 tokens behind 32 256 keys 205 us (that kernel 228), 4864
-// behind 27 904 1690 us (1627); tensor pipe 54 % on two prompts of up to 4096 tokens,
+// Measured: 4 x 32/8 heads of 8192 tokens 1580 us, 1.39 PFLOP/s (the dense cache's
+// windowed kernel 1551); 512 tokens behind 32 256 keys 202 us (that kernel 228), 4864
+// behind 27 904 1600 us (1627); tensor pipe 55 % on two prompts of up to 4096 tokens,
 // the softmax between the two products is what it waits for.
 //
 // Values that are not finite: as in the windowed prefill a weight of 0 times NaN reaches

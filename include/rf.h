@@ -482,8 +482,10 @@ rf_status rf_cache_evict(const void* k, const void* v, const float* weight, cons
  * pages in order, entries behind the last one in use may hold anything.  The new
  * tokens of all requests are packed one after the other: those of request b are
  * rows starts[b] .. starts[b + 1] - 1.  All lengths, tables and slots are int32 in
- * DEVICE memory.  The calls, in the order of a step: rf_page_tables, rf_paged_plan,
- * then per layer rf_qk_norm_rope and rf_attn_paged.
+ * DEVICE memory.  The calls, in the order of a step: rf_page_tables, rf_paged_plan (or
+ * rf_paged_plan_slots), then per layer rf_qk_norm_rope and rf_attn_paged.  No output or
+ * plan overlaps an input or another of them, but where a call says so; rf_page_tables and
+ * rf_qk_norm_rope check that.
  */
 
 /*
