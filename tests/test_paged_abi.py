@@ -105,8 +105,8 @@ def test_norm_rope_refuses_overlapping_buffers(lib):
     assert f(*rope_args(**dense, k_out=at(1, 16))) == 1
     assert f(*rope_args(**dense, q_out=at(0, 2048))) == 1       # a token on
     assert f(*rope_args(**dense, k_out=at(0), q_step=1280)) == 1
-    # q, k and v beside one another in rows of 1536 values, an output over the last row's end
-    assert f(*rope_args(**dense, k=at(0, 2048), q_step=1536, k_step=1536, k_out=at(0, 4 * 3072 + 2048 + 496))) == 1
+    # q, k and v beside one another in rows of 1544 values, an output over the last row's end
+    assert f(*rope_args(**dense, k=at(0, 2048), q_step=1544, k_step=1544, k_out=at(0, 4 * 3088 + 2048 + 496))) == 1
     # the cache is not k's place
     assert f(*rope_args(k_out=at(1))) == 1
 
