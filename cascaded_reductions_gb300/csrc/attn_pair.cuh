@@ -72,6 +72,8 @@
 //                              which a block without visible keys gives p = 0
 //   ROUNDS                     scores of any size: those of a block with huge ones are
 //                              rounded in log2 units before the reference is taken off
+//   REDOES                     instead, a row of huge scores gets a sum of NaN, and
+//                              the policy computes it again
 //   CHAINED                    the kernel is set up beside the end of the one before
 //                              it on the stream, and lets the next one begin so
 //   Item, Pending              a work item; what its output still needs
@@ -491,6 +493,7 @@ __device__ __forceinline__ void attn_pair_body(const CUtensorMap& tmQ, const CUt
       if (!ok) break;
       // The output warps have read what was here two items ago: this block waited
       // for a P V that was issued after they had read that item's O.
+      if constexpr (P::REDOES) l = huge<P::F16>(m_ref) ? NAN : l;
       sh->part_l[t & 1][kh][r] = l;
       if (kh == 0) sh->row_m[t & 1][r] = m_ref;
       __syncwarp();

@@ -33,7 +33,7 @@
 // Values that are not finite: as in the windowed prefill a weight of 0 times NaN reaches
 // rows that do not see the value.  Rows whose output is not finite are noted, and
 // paged_finish_kernel computes their NaN columns again from the visible keys alone.
-// Rows of huge scores (pair::huge) are written as NaN and computed again in the same way.
+// Rows of huge scores (pair::huge) come out as NaN and are computed again in the same way.
 
 #include <cuda_fp16.h>
 
@@ -123,7 +123,7 @@ __device__ __forceinline__ void step_item(const PagedView& v, RangeItem& it) {
 template <bool F16_>
 struct PagedPrefill {
   static constexpr bool F16 = F16_;
-  static constexpr bool CHAINED = true, STAGED = true, ROUNDS = false;
+  static constexpr bool CHAINED = true, STAGED = true, ROUNDS = false, REDOES = true;
   static constexpr float M_START = pair::LOWEST;
   using Item = RangeItem;
   struct Pages {
@@ -292,8 +292,7 @@ struct PagedPrefill {
   __device__ __forceinline__ bool boxed(const Pending& pend) const { return pend.full; }
   __device__ __forceinline__ bool pack(const Pending& pend, int col, const uint32_t (&v)[32], float m, float lt,
                                        uint32_t (&w)[16]) const {
-    // 0: a row that sees nothing
-    const float inv = huge<F16>(m) ? NAN : lt == 0.f ? 0.f : 1.f / lt;
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;       // 0: a row that sees nothing
     const uint64_t inv2 = pair::pack_f32x2(inv, inv);
     uint64_t probe = 0ull;                              // NaN if a value is not finite
 #pragma unroll
@@ -307,9 +306,7 @@ struct PagedPrefill {
     }
     const size_t row = (size_t)pend.row * a.v.s.H + pend.head;
     if (pend.in && RF_IDX_OK(row, (size_t)a.v.s.T * a.v.s.H)) {
-      // -inf too where the sum says nothing: the row has NaN columns then, and gets its lse with them
-      if (a.lse != nullptr && col == 0)
-        a.lse[row] = lt > 0.f && lt < INFINITY ? (m + log2f(lt)) * kLn2 : -INFINITY;
+      if (a.lse != nullptr && col == 0) a.lse[row] = (m + log2f(lt)) * kLn2;
       if (!pend.full) pair::st_row32(a.out + (row * HD + col) * 2, w, false);
     }
     float p0, p1;
@@ -569,9 +566,9 @@ paged_finish_kernel(const __grid_constant__ PagedAttn a) {
         const float4 y = load_row4<F16>(a.out + row * HD * 2, lane);
         const uint32_t todo = nan_of(y);
         if (!__any_sync(0xffffffffu, todo != 0)) continue;
-        // masked scores never entered the lse in place; -inf where the sum said nothing
+        // masked scores never entered the lse in place; it is not finite where the sum said nothing
         float lse2 = NAN;
-        const bool whole = a.lse != nullptr && a.lse[row] == -INFINITY;
+        const bool whole = a.lse != nullptr && !(fabsf(a.lse[row]) < INFINITY);
         const float4 z = redo_row<F16>(a, it, i, head, todo, whole, y, &lse2, lane);
         *reinterpret_cast<uint2*>(a.out + row * HD * 2 + lane * 8) =
             make_uint2(pair::pack_16x2<F16>(z.x, z.y), pair::pack_16x2<F16>(z.z, z.w));

@@ -21,7 +21,8 @@ using pair::HD;
 
 struct CausalPrefill {
   static constexpr bool F16 = false;
-  static constexpr bool CHAINED = false, PARTIAL = false, STAGED = false, ROUNDS = false;
+  static constexpr bool CHAINED = false, PARTIAL = false, STAGED = false;
+  static constexpr bool ROUNDS = false, REDOES = false;
   static constexpr float M_START = -INFINITY;
   // A work item: 256 query rows (two 128-row tiles) of one head.
   struct Item {

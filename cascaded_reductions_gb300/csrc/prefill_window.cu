@@ -24,7 +24,7 @@
 // see it.  A row with NaN in its output is therefore looked at again after the
 // last item: columns that are NaN by right (a value that the warp's 32 rows all see,
 // found in one pass over their keys) stay, the others are computed from the
-// row's visible keys alone.  So are rows of huge scores (pair::huge), written as NaN.
+// row's visible keys alone.  So are rows of huge scores (pair::huge), which come out as NaN.
 
 #include <cuda_fp16.h>
 
@@ -41,7 +41,8 @@ using pair::HD;
 template <bool F16_>
 struct WindowPrefill {
   static constexpr bool F16 = F16_;
-  static constexpr bool CHAINED = true, PARTIAL = true, STAGED = true, ROUNDS = false;
+  static constexpr bool CHAINED = true, PARTIAL = true, STAGED = true;
+  static constexpr bool ROUNDS = false, REDOES = true;
   static constexpr float M_START = -1e30f;
   struct Item {
     int bh, kvh;     // first query head and key head, of the batch
@@ -190,7 +191,7 @@ struct WindowPrefill {
   }
   __device__ __forceinline__ bool pack(const Pending& pend, int col, const uint32_t (&v)[32], float m,
                                        float lt, uint32_t (&w)[16]) const {
-    const float inv = pair::huge<F16>(m) ? NAN : 1.f / lt;
+    const float inv = 1.f / lt;
     const uint64_t inv2 = pair::pack_f32x2(inv, inv);
     uint64_t probe = 0ull;                              // NaN if a value is not finite
 #pragma unroll
@@ -204,7 +205,7 @@ struct WindowPrefill {
     }
     const size_t row = (size_t)pend.bh * N + pend.row;
     if (lse != nullptr && col == 0 && pend.in && RF_IDX_OK(row, (size_t)heads * N))
-      lse[row] = lt > 0.f && lt < INFINITY ? (m + log2f(lt)) * kLn2 : -INFINITY;
+      lse[row] = (m + log2f(lt)) * kLn2;
     float p0, p1;
     pair::unpack_f32x2(probe, p0, p1);
     return pend.in && !(p0 == 0.f && p1 == 0.f);
@@ -273,8 +274,8 @@ struct WindowPrefill {
 
   // The NaN columns of one output row, but for those that are NaN by `right`, once
   // more from the keys that the row sees; four columns per lane.  Ends once they are
-  // all NaN again.  The lse in place stands (no masked score entered it), unless it
-  // is -inf: the row's sum was 0, infinite or NaN.
+  // all NaN again.  The lse in place stands (no masked score entered it) where it is
+  // finite: else the row's sum was 0, infinite or NaN.
   // A row costs about 0.2 us per key.  The form of the loops here was chosen by the time
   // of calls that never reach them, whose code lies beside it: other widths and
   // orders cost the long windowed prefill 501 to 538 us instead of 499.
@@ -282,13 +283,7 @@ struct WindowPrefill {
     const size_t q0 = ((size_t)bh * N + row) * HD, o = q0 + lane * 4;
     uint2 word = RF_SPAN_OK(o, 4, q_elems()) ? *reinterpret_cast<const uint2*>(out + o) : make_uint2(0, 0);
     const uint32_t todo = nan_bits(word) & ~right;
-    const size_t i = (size_t)bh * N + row;
-    // whether the lse is to be found too: the sum said nothing, and is NaN where the columns stay so
-    const bool ask = lse != nullptr && RF_IDX_OK(i, (size_t)heads * N) && lse[i] == -INFINITY;
-    if (!__any_sync(0xffffffffu, todo != 0)) {
-      if (ask && lane == 0) lse[i] = NAN;
-      return;
-    }
+    if (!__any_sync(0xffffffffu, todo != 0)) return;
     const int p = L - N + row;
     const int lo = max(0, p - window + 1), ns = min(sinks, lo), n = ns + p - lo + 1;
     const size_t kv0 = (size_t)(bh / G) * L;
@@ -338,7 +333,6 @@ struct WindowPrefill {
       for (int e = 0; e < 4; ++e) now |= (uint32_t)(acc[e] != acc[e]) << e;
       gone = !__any_sync(0xffffffffu, (todo & ~now) != 0);
     }
-    if (ask && lane == 0) lse[i] = gone ? NAN : (m + log2f(l)) * kLn2;
     if (gone) return;
     float y[4];                                         // l = 0: every visible score is -inf
 #pragma unroll
@@ -349,6 +343,9 @@ struct WindowPrefill {
     word.x = (word.x & ~m01) | (y01 & m01);
     word.y = (word.y & ~m23) | (y23 & m23);
     if (RF_SPAN_OK(o, 4, q_elems())) *reinterpret_cast<uint2*>(out + o) = word;
+    const size_t i = (size_t)bh * N + row;
+    if (lse != nullptr && lane == 0 && RF_IDX_OK(i, (size_t)heads * N) && !(fabsf(lse[i]) < INFINITY))
+      lse[i] = (m + log2f(l)) * kLn2;
   }
 
   // Rows of this thread whose stored values hold a NaN are looked at again, a

@@ -54,7 +54,8 @@ struct Split {
 template <bool F16_>
 struct PrefixStates {
   static constexpr bool F16 = F16_;
-  static constexpr bool CHAINED = true, PARTIAL = false, STAGED = false, ROUNDS = true;
+  static constexpr bool CHAINED = true, PARTIAL = false, STAGED = false;
+  static constexpr bool ROUNDS = true, REDOES = false;
   static constexpr float M_START = pair::LOWEST;
   struct Item {
     int hk, seq0;            // key head; first sequence of the pair of tiles
